@@ -30,5 +30,10 @@ from ._binding import (  # noqa: F401
     decode_step,
     decode_step_workspace,
     moe_ffn,
+    KVPages,
+    kv_read,
+    kv_write,
+    paged_attn,
+    paged_attn_workspace,
 )
 from .decoder import BlockDecoder  # noqa: F401

@@ -469,3 +469,193 @@ def moe_ffn(h, w_router, w13, w2, topk, out_fp32=True, out=None, ids=None, weigh
                           _ptr(ws, None, "ws"), ws.numel(), _stream(stream))
     _ck(rc, "dllm_moe_ffn")
     return out, ids, weights
+
+
+# ---------------------------------------------------------------------------
+# paged K/V cache (dllm_kv_write, dllm_kv_read, dllm_paged_attn)
+# ---------------------------------------------------------------------------
+class KvPagesDesc(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p), ("type", c_int),
+                ("num_pages", c_int), ("page_size", c_int), ("heads", c_int), ("dh", c_int)]
+
+
+class PagedAttnArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("q_stride", ctypes.c_longlong), ("out", c_void_p), ("out_fp32", c_int),
+                ("lse", c_void_p), ("q_off", c_void_p), ("kv_len", c_void_p), ("q_pos", c_void_p),
+                ("page_table", c_void_p), ("max_pages", c_int), ("B", c_int), ("Hq", c_int), ("max_q", c_int),
+                ("max_kv", c_int), ("q_rows", c_int), ("scale", c_float), ("left", c_int), ("right", c_int),
+                ("sinks", c_int)]
+
+
+_PAGES_P = ctypes.POINTER(KvPagesDesc)
+SIGNATURES.update({
+    "dllm_kv_write": (c_int, [_PAGES_P, c_void_p, c_void_p, ctypes.c_longlong, ctypes.c_longlong, c_int, c_void_p,
+                              c_void_p, c_void_p, c_int, c_int, c_void_p]),
+    "dllm_kv_read": (c_int, [_PAGES_P, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p]),
+    "dllm_paged_attn_workspace": (c_size_t, [_PAGES_P, ctypes.POINTER(PagedAttnArgs)]),
+    "dllm_paged_attn": (c_int, [_PAGES_P, ctypes.POINTER(PagedAttnArgs), c_void_p, c_size_t, c_void_p]),
+})
+for _name in ("dllm_kv_write", "dllm_kv_read", "dllm_paged_attn_workspace", "dllm_paged_attn"):
+    _fn = getattr(LIB, _name)
+    _fn.restype, _fn.argtypes = SIGNATURES[_name]
+
+
+class KVPages:
+    """Page pools of a K/V cache: k, v [num_pages][heads][page_size][dh], bf16
+    or float8_e4m3fn; the 8-bit rows with uint8 k_scale, v_scale
+    [num_pages][heads][page_size] (a row stands for code * 2^(byte - 127))."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must be [num_pages][heads][page_size][dh]")
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise TypeError(f"pages must be bfloat16 or float8_e4m3fn, got {k.dtype}")
+        fp8 = k.dtype == torch.float8_e4m3fn
+        if fp8 != (k_scale is not None) or fp8 != (v_scale is not None):
+            raise ValueError("e4m3 pages need k_scale and v_scale, bf16 pages have none")
+        if fp8 and not (k_scale.shape == k.shape[:3] and v_scale.shape == k.shape[:3]):
+            raise ValueError("scales must be [num_pages][heads][page_size]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        self.num_pages, self.heads, self.page_size, self.dh = k.shape
+        self.desc = KvPagesDesc(
+            _ptr_on(k, self.device, k.dtype, "k"), _ptr_on(v, self.device, k.dtype, "v"),
+            _ptr_on(k_scale, self.device, torch.uint8, "k_scale"), _ptr_on(v_scale, self.device, torch.uint8, "v_scale"),
+            1 if fp8 else 0, self.num_pages, self.page_size, self.heads, self.dh)
+
+    @classmethod
+    def empty(cls, num_pages, page_size, heads, dh, dtype=torch.bfloat16, device="cuda"):
+        """Pools of uninitialised pages."""
+        shape = (int(num_pages), int(heads), int(page_size), int(dh))
+        k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        if dtype != torch.float8_e4m3fn:
+            return cls(k, v)
+        return cls(k, v, *(torch.empty(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)))
+
+
+def _ptr_on(t, device, dtype, name):
+    """_ptr of a tensor that has to be on `device` (None stays None)."""
+    p = _ptr(t, dtype, name)
+    if t is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the pages are on {device}")
+    return p
+
+
+def _rows_ptr(t, device, heads, dh, name):
+    """(pointer, row stride) of bf16 rows [rows][heads][dh], dense within a row."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the pages are on {device}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dh:
+        raise ValueError(f"{name} must be [rows][{heads}][{dh}], got {tuple(t.shape)}")
+    n, s = t.shape[0], t.stride()
+    if n and (s[2] != 1 or (heads > 1 and s[1] != dh)):
+        raise ValueError(f"{name} must be dense within a row")
+    return t.data_ptr(), s[0] if n > 1 else heads * dh
+
+
+def _ragged(device, off, page_table, **per_request):
+    """(B, max_pages) after checking the ragged batch's metadata."""
+    _ptr_on(off, device, torch.int32, "offsets")
+    _ptr_on(page_table, device, torch.int32, "page_table")
+    B = off.numel() - 1
+    if B < 0 or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B][max_pages] with B = offsets - 1")
+    for name, t in per_request.items():
+        if t is not None:
+            _ptr_on(t, device, torch.int32, name)
+            if t.numel() != B:
+                raise ValueError(f"{name} must have one entry per request")
+    return B, page_table.shape[1]
+
+
+def _launch(device, stream, fn, *args):
+    """fn(*args, stream) with `device` current (its current stream by default)."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
+    with torch.cuda.device(device):
+        return fn(*args, (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
+
+
+def _alloc(shape, dtype, device, stream):
+    """torch.empty that stays allocated until `stream`'s work on it is done."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def kv_write(pages: KVPages, k, v, off, pos0, page_table, stream=None):
+    """Store rows k, v [rows][heads][dh] bf16 (any row stride) in the pages:
+    row off[i] + t at position pos0[i] + t of request i. off int32 [B+1], pos0
+    int32 [B], page_table int32 [B][max_pages]."""
+    dev = pages.device
+    kp, ks = _rows_ptr(k, dev, pages.heads, pages.dh, "k")
+    vp, vs = _rows_ptr(v, dev, pages.heads, pages.dh, "v")
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have the same rows")
+    B, n = _ragged(dev, off, page_table, pos0=pos0)
+    _ck(_launch(dev, stream, LIB.dllm_kv_write, ctypes.byref(pages.desc), kp, vp, ks, vs, k.shape[0], off.data_ptr(),
+                pos0.data_ptr(), page_table.data_ptr(), n, B), "dllm_kv_write")
+
+
+def kv_read(pages: KVPages, off, pos0, page_table, rows, k=None, v=None, stream=None):
+    """The cached rows of positions pos0[i] + t as bf16 rows off[i] + t of (k, v)
+    [rows][heads][dh] (allocated unless given)."""
+    dev = pages.device
+    shape = (int(rows), pages.heads, pages.dh)
+    k = k if k is not None else _alloc(shape, torch.bfloat16, dev, stream)
+    v = v if v is not None else _alloc(shape, torch.bfloat16, dev, stream)
+    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+        raise ValueError(f"k and v must be {list(shape)}")
+    B, n = _ragged(dev, off, page_table, pos0=pos0)
+    _ck(_launch(dev, stream, LIB.dllm_kv_read, ctypes.byref(pages.desc), _ptr_on(k, dev, torch.bfloat16, "k"),
+                _ptr_on(v, dev, torch.bfloat16, "v"), shape[0], off.data_ptr(), pos0.data_ptr(), page_table.data_ptr(),
+                n, B), "dllm_kv_read")
+    return k, v
+
+
+def paged_attn_workspace(pages: KVPages, B, Hq, max_q, max_kv) -> int:
+    """Workspace bytes of paged_attn for no larger B, max_q and max_kv."""
+    a = PagedAttnArgs(B=int(B), Hq=int(Hq), max_q=int(max_q), max_kv=int(max_kv))
+    return int(LIB.dllm_paged_attn_workspace(ctypes.byref(pages.desc), ctypes.byref(a)))
+
+
+def paged_attn(q, pages: KVPages, q_off, kv_len, page_table, max_q, max_kv, q_pos=None, scale=None, left=-1, right=-1,
+               sinks=0, out=None, out_fp32=False, return_lse=False, lse=None, ws=None, stream=None):
+    """Attention of q [rows][Hq][dh] bf16 (any row stride) over the pages.
+
+    Row t of request i has position q_pos[i] + t (default: the last rows of
+    the cache) and sees keys u < kv_len[i] with u <= position + right and
+    (u >= position - left or u < sinks); negative left / right: no limit.
+    Returns out [rows][Hq][dh], or (out, lse [rows][Hq]) with return_lse.
+    """
+    dev = pages.device
+    Hq = q.shape[1] if q.dim() == 3 else -1
+    qp, qs = _rows_ptr(q, dev, Hq, pages.dh, "q")
+    B, n = _ragged(dev, q_off, page_table, kv_len=kv_len, q_pos=q_pos)
+    rows = q.shape[0]
+    if out is None:
+        out = _alloc((rows, Hq, pages.dh), torch.float32 if out_fp32 else torch.bfloat16, dev, stream)
+    elif tuple(out.shape) != (rows, Hq, pages.dh) or out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out must be bf16 or fp32 [{rows}][{Hq}][{pages.dh}]")
+    if lse is None and return_lse:
+        lse = _alloc((rows, Hq), torch.float32, dev, stream)
+    elif lse is not None and tuple(lse.shape) != (rows, Hq):
+        raise ValueError(f"lse must be [{rows}][{Hq}]")
+    a = PagedAttnArgs(qp, qs, _ptr_on(out, dev, out.dtype, "out"), 1 if out.dtype == torch.float32 else 0,
+                      _ptr_on(lse, dev, torch.float32, "lse"), q_off.data_ptr(), kv_len.data_ptr(),
+                      q_pos.data_ptr() if q_pos is not None else None, page_table.data_ptr(), n, B, Hq, int(max_q),
+                      int(max_kv), rows, float(scale if scale is not None else 1.0 / math.sqrt(pages.dh)), int(left),
+                      int(right), int(sinks))
+    if ws is None:
+        need = int(LIB.dllm_paged_attn_workspace(ctypes.byref(pages.desc), ctypes.byref(a)))
+        if need:
+            ws = _alloc(need, torch.uint8, dev, stream)
+    _ck(_launch(dev, stream, LIB.dllm_paged_attn, ctypes.byref(pages.desc), ctypes.byref(a),
+                _ptr_on(ws, dev, None, "ws"), ws.numel() * ws.element_size() if ws is not None else 0),
+        "dllm_paged_attn")
+    return (out, lse) if return_lse else out

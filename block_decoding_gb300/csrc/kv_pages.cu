@@ -1,0 +1,271 @@
+// Writing new K/V rows into the pages of the cache (in bf16 as they are, or
+// in 8 bits with one power-of-two scale per row and head) and reading rows
+// back as contiguous bf16. Both move each byte once: memory bound.
+//
+// One row of one head is handled by dh / 16 neighbouring lanes, 16 elements
+// of K and 16 of V each: two 16-byte chunks half a row apart, so that the
+// lanes of a row read and write contiguous runs and a thread has four
+// 16-byte loads in flight before it needs the first.
+#include "pages.cuh"
+
+namespace dllm {
+
+DLLM_DEFINE_STATUS(kv)
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct MoveArgs {
+  KvPages c;
+  uint16_t *k, *v;             // the contiguous side
+  long long k_stride, v_stride;
+  int rows, B;
+  const int32_t *off, *pos0;
+  unsigned int *status;
+};
+
+// Request that holds row r (the last i with off[i] <= r), or -1.
+__device__ __forceinline__ int request_of(const int32_t *off, int B, int r) {
+  int lo = 0, hi = B;   // off[lo] <= r < off[hi]
+  if (r < off[0] || r >= off[B]) return -1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= r) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Exponent byte of a row with the largest magnitude bits `a` (finite bf16):
+// the least e >= -117 with |x| <= 448 * 2^e, + 127. 448 = 1.75 * 2^8, and
+// |x| = (1 + m / 128) * 2^(a >> 7 - 127).
+__device__ __forceinline__ int scale_byte(uint32_t a) {
+  const int b = static_cast<int>(a >> 7) - 8 + ((a & 127) > 96 ? 1 : 0);
+  return min(max(b, 10), 247);
+}
+
+// Eight bf16 -> eight e4m3 codes of x * f. `odd`: the row holds an infinity
+// or NaN, or magnitudes whose code would stand for 2^128.
+__device__ __forceinline__ uint2 quantise8(const uint4 &u, float f, bool odd, float top) {
+  float x[8];
+  unpack8(u, x);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = x[2 * i] * f, b = x[2 * i + 1] * f;
+    if (odd) {   // an infinity becomes NaN; NaN passes through both comparisons
+      a = isinf(a) ? NAN : (a > top ? top : a < -top ? -top : a);
+      b = isinf(b) ? NAN : (b > top ? top : b < -top ? -top : b);
+    }
+    uint16_t p;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(b), "f"(a));
+    w[i] = p;
+  }
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+__device__ __forceinline__ uint32_t max_mag(const uint4 &u, uint32_t m) {
+  m = __vmaxu2(m, u.x & 0x7fff7fffu);
+  m = __vmaxu2(m, u.y & 0x7fff7fffu);
+  m = __vmaxu2(m, u.z & 0x7fff7fffu);
+  return __vmaxu2(m, u.w & 0x7fff7fffu);
+}
+
+// Largest finite magnitude among the halves of u (slow path).
+__device__ __forceinline__ uint32_t max_finite(const uint4 &u, uint32_t m) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = w[i] & 0x7fffu, b = (w[i] >> 16) & 0x7fffu;
+    if (a < 0x7f80u) m = max(m, a);
+    if (b < 0x7f80u) m = max(m, b);
+  }
+  return m;
+}
+
+// Quantise one row held by LPR lanes (chunks a, b of this lane); returns the
+// exponent byte.
+template <int LPR>
+__device__ __forceinline__ int quantise_row(const uint4 &a, const uint4 &b, uint2 &qa, uint2 &qb) {
+  uint32_t m2 = max_mag(b, max_mag(a, 0));
+  uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const bool nonfinite = m >= 0x7f80u;
+  if (__any_sync(0xffffffffu, nonfinite)) {
+    uint32_t f = max_finite(b, max_finite(a, 0));
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) f = max(f, __shfl_xor_sync(0xffffffffu, f, o));
+    m = f;
+  }
+  const int byte = scale_byte(m);
+  const float f = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
+  const bool odd = nonfinite || byte == 247;
+  const float top = byte == 247 ? 240.f : 448.f;
+  qa = quantise8(a, f, odd, top);
+  qb = quantise8(b, f, odd, top);
+  return byte;
+}
+
+// Unit = one row of one head; a warp holds 32 / LPR of them.
+template <int DH, bool FP8>
+__global__ void __launch_bounds__(kThreads) kv_write_kernel(const MoveArgs g) {
+  constexpr int LPR = DH / 16;
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (g.off[0] < 0 || g.off[g.B] > g.rows)) atomicOr(g.status, DLLM_DEV_OFFSETS);
+  const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
+  const int l = threadIdx.x % LPR;
+  const int r = static_cast<int>(min(unit / g.c.heads, 0x7fffffffll)), h = static_cast<int>(unit % g.c.heads);
+  int row = -1;
+  if (r < g.rows) {
+    const int i = request_of(g.off, g.B, r);
+    if (i >= 0) {
+      const long long u = static_cast<long long>(g.pos0[i]) + (r - g.off[i]);
+      row = u < 0 || u > 0x7fffffffll ? -1 : page_row(g.c, i, static_cast<int>(u));
+      if (row < 0) {
+        if (l == 0 && h == 0) atomicOr(g.status, DLLM_DEV_PAGE);
+      } else {
+        row += h << g.c.page_shift;
+      }
+    }
+  }
+  uint4 ka = make_uint4(0, 0, 0, 0), kb = ka, va = ka, vb = ka;
+  if (row >= 0) {
+    const uint4 *ks = reinterpret_cast<const uint4 *>(g.k + r * g.k_stride + h * DH);
+    const uint4 *vs = reinterpret_cast<const uint4 *>(g.v + r * g.v_stride + h * DH);
+    ka = __ldg(ks + l); kb = __ldg(ks + l + LPR);
+    va = __ldg(vs + l); vb = __ldg(vs + l + LPR);
+  }
+  if constexpr (FP8) {
+    uint2 qa, qb;
+    const int kbyte = quantise_row<LPR>(ka, kb, qa, qb);
+    if (row >= 0) {
+      uint2 *d = reinterpret_cast<uint2 *>(g.c.k + static_cast<size_t>(row) * DH);
+      d[l] = qa; d[l + LPR] = qb;
+    }
+    const int vbyte = quantise_row<LPR>(va, vb, qa, qb);
+    if (row >= 0) {
+      uint2 *d = reinterpret_cast<uint2 *>(g.c.v + static_cast<size_t>(row) * DH);
+      d[l] = qa; d[l + LPR] = qb;
+      if (l == 0) {
+        g.c.k_scale[row] = static_cast<uint8_t>(kbyte);
+        g.c.v_scale[row] = static_cast<uint8_t>(vbyte);
+      }
+    }
+  } else if (row >= 0) {
+    uint4 *d = reinterpret_cast<uint4 *>(g.c.k + static_cast<size_t>(row) * (DH * 2));
+    d[l] = ka; d[l + LPR] = kb;
+    d = reinterpret_cast<uint4 *>(g.c.v + static_cast<size_t>(row) * (DH * 2));
+    d[l] = va; d[l + LPR] = vb;
+  }
+}
+
+// Eight codes -> eight bf16 of code * 2^(byte - 127): exact (a code has four
+// significant bits, and the scales keep every value normal).
+__device__ __forceinline__ uint4 restore8(uint2 q, float f) {
+  float x[8];
+  const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 a = e4m3x2_to_f32(static_cast<uint16_t>(w[i])), b = e4m3x2_to_f32(static_cast<uint16_t>(w[i] >> 16));
+    x[4 * i] = a.x * f; x[4 * i + 1] = a.y * f; x[4 * i + 2] = b.x * f; x[4 * i + 3] = b.y * f;
+  }
+  return pack8(x);
+}
+
+template <int DH, bool FP8>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const MoveArgs g) {
+  constexpr int LPR = DH / 16;
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (g.off[0] < 0 || g.off[g.B] > g.rows)) atomicOr(g.status, DLLM_DEV_OFFSETS);
+  const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
+  const int l = threadIdx.x % LPR;
+  const int r = static_cast<int>(min(unit / g.c.heads, 0x7fffffffll)), h = static_cast<int>(unit % g.c.heads);
+  if (r >= g.rows) return;
+  const int i = request_of(g.off, g.B, r);
+  if (i < 0) return;
+  const long long u = static_cast<long long>(g.pos0[i]) + (r - g.off[i]);
+  int row = u < 0 || u > 0x7fffffffll ? -1 : page_row(g.c, i, static_cast<int>(u));
+  uint4 ka = make_uint4(0, 0, 0, 0), kb = ka, va = ka, vb = ka;
+  if (row < 0) {
+    if (l == 0 && h == 0) atomicOr(g.status, DLLM_DEV_PAGE);
+  } else {
+    row += h << g.c.page_shift;
+    if constexpr (FP8) {
+      const uint2 *ks = reinterpret_cast<const uint2 *>(g.c.k + static_cast<size_t>(row) * DH);
+      const uint2 *vs = reinterpret_cast<const uint2 *>(g.c.v + static_cast<size_t>(row) * DH);
+      const uint2 qa = __ldg(ks + l), qb = __ldg(ks + l + LPR), pa = __ldg(vs + l), pb = __ldg(vs + l + LPR);
+      const float kf = __uint_as_float(static_cast<uint32_t>(g.c.k_scale[row]) << 23);
+      const float vf = __uint_as_float(static_cast<uint32_t>(g.c.v_scale[row]) << 23);
+      ka = restore8(qa, kf); kb = restore8(qb, kf);
+      va = restore8(pa, vf); vb = restore8(pb, vf);
+    } else {
+      const uint4 *ks = reinterpret_cast<const uint4 *>(g.c.k + static_cast<size_t>(row) * (DH * 2));
+      const uint4 *vs = reinterpret_cast<const uint4 *>(g.c.v + static_cast<size_t>(row) * (DH * 2));
+      ka = __ldg(ks + l); kb = __ldg(ks + l + LPR);
+      va = __ldg(vs + l); vb = __ldg(vs + l + LPR);
+    }
+  }
+  uint4 *d = reinterpret_cast<uint4 *>(g.k + r * g.k_stride + h * DH);
+  d[l] = ka; d[l + LPR] = kb;
+  d = reinterpret_cast<uint4 *>(g.v + r * g.v_stride + h * DH);
+  d[l] = va; d[l + LPR] = vb;
+}
+
+dllm_status move(bool write, const dllm_kv_pages *pages, uint16_t *k, uint16_t *v, long long k_stride,
+                 long long v_stride, int rows, const int32_t *off, const int32_t *pos0, const int32_t *page_table,
+                 int max_pages, int B, cudaStream_t s) {
+  const dllm_status st = check_pages(pages);
+  if (st != DLLM_OK) return st;
+  if (rows < 0 || B < 0 || max_pages < 0) return DLLM_ERR_INVALID_ARG;
+  if (B > 4096) return DLLM_ERR_UNSUPPORTED;
+  if (rows == 0 || B == 0) return DLLM_OK;
+  const dllm_status sp = check_page_pointers(pages);
+  if (sp != DLLM_OK) return sp;
+  const long long d = static_cast<long long>(pages->heads) * pages->dh;
+  if (!k || !v || !off || !pos0 || !page_table) return DLLM_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || k_stride < d || v_stride < d || k_stride % 8 || v_stride % 8)
+    return DLLM_ERR_INVALID_ARG;
+  MoveArgs g{};
+  g.c = device_pages(pages, page_table, max_pages);
+  g.k = k; g.v = v; g.k_stride = k_stride; g.v_stride = v_stride;
+  g.rows = rows; g.B = B; g.off = off; g.pos0 = pos0;
+  cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&g.status), g_status_kv);
+  if (e != cudaSuccess) return cuda_error(e);
+  const int per_block = kThreads / (pages->dh / 16);
+  const long long units = static_cast<long long>(rows) * pages->heads;
+  const long long blocks = (units + per_block - 1) / per_block;
+  if (blocks > 0x7fffffffll) return DLLM_ERR_UNSUPPORTED;
+  const bool fp8 = pages->type == DLLM_KV_E4M3;
+  void (*kern)(MoveArgs);
+  if (write)
+    kern = pages->dh == 64 ? (fp8 ? kv_write_kernel<64, true> : kv_write_kernel<64, false>)
+                           : (fp8 ? kv_write_kernel<128, true> : kv_write_kernel<128, false>);
+  else
+    kern = pages->dh == 64 ? (fp8 ? kv_read_kernel<64, true> : kv_read_kernel<64, false>)
+                           : (fp8 ? kv_read_kernel<128, true> : kv_read_kernel<128, false>);
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, g);
+  if (e != cudaSuccess) return cuda_error(e);
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace dllm
+
+using namespace dllm;
+
+extern "C" dllm_status dllm_kv_write(const dllm_kv_pages *pages, const dllm_bf16 *k, const dllm_bf16 *v,
+                                     long long k_stride, long long v_stride, int rows, const int32_t *off,
+                                     const int32_t *pos0, const int32_t *page_table, int max_pages, int B,
+                                     dllm_stream stream) {
+  return move(true, pages, const_cast<dllm_bf16 *>(k), const_cast<dllm_bf16 *>(v), k_stride, v_stride, rows, off, pos0,
+              page_table, max_pages, B, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" dllm_status dllm_kv_read(const dllm_kv_pages *pages, dllm_bf16 *k, dllm_bf16 *v, int rows,
+                                    const int32_t *off, const int32_t *pos0, const int32_t *page_table, int max_pages,
+                                    int B, dllm_stream stream) {
+  const long long d = pages ? static_cast<long long>(pages->heads) * pages->dh : 0;
+  return move(false, pages, k, v, d, d, rows, off, pos0, page_table, max_pages, B, static_cast<cudaStream_t>(stream));
+}

@@ -1,0 +1,72 @@
+// The paged K/V cache as the kernels see it: page and slot of a position,
+// argument checks shared by the entry points, and the 8-bit row format.
+#pragma once
+
+#include "common.cuh"
+
+namespace dllm {
+
+struct KvPages {
+  uint8_t *k, *v;                  // [num_pages][heads][page_size][dh], bf16 or e4m3
+  uint8_t *k_scale, *v_scale;      // [num_pages][heads][page_size], or null (bf16)
+  int num_pages, heads, dh, page_shift;
+  const int32_t *table;            // [B][max_pages]
+  int max_pages;
+};
+
+// Cache row of head 0 at position u of request i, as an index over
+// [num_pages][heads][page_size] (the row of head h: + h << page_shift);
+// -1 when the table or the pool does not hold it.
+__device__ __forceinline__ int page_row(const KvPages &c, int i, int u) {
+  const int n = u >> c.page_shift;
+  if (u < 0 || n >= c.max_pages) return -1;
+  const int page = c.table[static_cast<size_t>(i) * c.max_pages + n];
+  if (page < 0 || page >= c.num_pages) return -1;
+  return ((page * c.heads) << c.page_shift) + (u & ((1 << c.page_shift) - 1));
+}
+
+inline dllm_status check_pages(const dllm_kv_pages *p) {
+  if (!p) return DLLM_ERR_INVALID_ARG;
+  if (p->type != DLLM_KV_BF16 && p->type != DLLM_KV_E4M3) return DLLM_ERR_UNSUPPORTED;
+  if (p->dh != 64 && p->dh != 128) return DLLM_ERR_UNSUPPORTED;
+  if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128)
+    return DLLM_ERR_UNSUPPORTED;
+  if (p->num_pages < 1 || p->heads < 1) return DLLM_ERR_INVALID_ARG;
+  if (p->heads > 256) return DLLM_ERR_UNSUPPORTED;
+  if (static_cast<long long>(p->num_pages) * p->heads * p->page_size >= (1ll << 31)) return DLLM_ERR_UNSUPPORTED;
+  return DLLM_OK;
+}
+
+inline dllm_status check_page_pointers(const dllm_kv_pages *p) {
+  if (!p->k || !p->v || !aligned16(p->k) || !aligned16(p->v)) return DLLM_ERR_INVALID_ARG;
+  if (p->type == DLLM_KV_E4M3 && (!p->k_scale || !p->v_scale)) return DLLM_ERR_INVALID_ARG;
+  return DLLM_OK;
+}
+
+inline KvPages device_pages(const dllm_kv_pages *p, const int32_t *table, int max_pages) {
+  KvPages c{};
+  c.k = static_cast<uint8_t *>(p->k);
+  c.v = static_cast<uint8_t *>(p->v);
+  c.k_scale = p->type == DLLM_KV_E4M3 ? p->k_scale : nullptr;
+  c.v_scale = p->type == DLLM_KV_E4M3 ? p->v_scale : nullptr;
+  c.num_pages = p->num_pages;
+  c.heads = p->heads;
+  c.dh = p->dh;
+  c.page_shift = p->page_size == 16 ? 4 : p->page_size == 32 ? 5 : p->page_size == 64 ? 6 : 7;
+  c.table = table;
+  c.max_pages = max_pages;
+  return c;
+}
+
+// Two e4m3 codes (low byte first) -> two floats, exactly.
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t v) {
+  uint32_t h;   // f16x2 holds every e4m3 value
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
+  float2 f;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+
+}  // namespace dllm

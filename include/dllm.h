@@ -62,6 +62,7 @@ typedef enum {
 #define DLLM_DEV_WAIT_TIMEOUT  0x8   /* a bounded device wait gave up           */
 #define DLLM_DEV_ROW_RANGE     0x10  /* a row map entry outside [0,B) x [0,blk) */
 #define DLLM_DEV_OFFSETS       0x20  /* q_off / kv_off beyond the given buffers  */
+#define DLLM_DEV_PAGE          0x40  /* a page id or position outside the pages  */
 
 /* Decoding-strategy parameters (host struct, passed by pointer).
  *  tau          confidence threshold: commit when p >= tau
@@ -428,6 +429,125 @@ dllm_status dllm_moe_ffn(const dllm_bf16 *h, const dllm_bf16 *w_router,
                          int d, int E, int F, int topk, void *out,
                          int out_fp32, int32_t *topk_ids, float *topk_w,
                          void *ws, size_t ws_bytes, dllm_stream stream);
+
+/* ---------------------------------------------------------------------
+ * Paged K/V cache. The rows of many requests live in a pool of fixed-size
+ * pages; page_table names each request's pages in order, so the cache row
+ * of request i at position u is slot u % page_size of page
+ * page_table[i][u / page_size].
+ *
+ *   k, v     [num_pages][heads][page_size][dh]: one head's rows of a page
+ *            are one contiguous piece
+ *   type     DLLM_KV_BF16: bf16 rows. DLLM_KV_E4M3: 8-bit codes, with one
+ *            power-of-two scale per row and head: the row stands for
+ *            code * 2^(byte - 127), byte from
+ *   k_scale, v_scale  uint8 [num_pages][heads][page_size] (NULL with bf16)
+ *
+ * A row x is stored in 8 bits with the least exponent e >= -117 for which
+ * max|x| <= 448 * 2^e, code = x * 2^-e rounded to the nearest e4m3 value,
+ * ties to even. Scaling by a power of two is exact and costs a
+ * floating-point code no precision, so a code is within half an e4m3 step
+ * of its element (2^-4 relative; below 2^-6 * 2^e, 2^-10 * 2^e absolute).
+ * An infinity or NaN is stored as NaN and does not enter the scale.
+ * Magnitudes above 1.875 * 2^127 are stored as that value.
+ *
+ *   Supported: dh in {64, 128}; page_size in {16, 32, 64, 128};
+ *   1 <= heads <= 256; num_pages * heads * page_size < 2^31; k and v
+ *   16-byte aligned.
+ *   A page id outside [0, num_pages) and a position outside the table set
+ *   DLLM_DEV_PAGE: such a row is not written, and reads as zeros.
+ * ------------------------------------------------------------------- */
+enum { DLLM_KV_BF16 = 0, DLLM_KV_E4M3 = 1 };
+typedef struct {
+  void *k, *v;
+  uint8_t *k_scale, *v_scale;
+  int type;
+  int num_pages, page_size, heads, dh;
+} dllm_kv_pages;
+
+/* dllm_kv_write -- store new K/V rows in the pages, quantising them with
+ * DLLM_KV_E4M3. Row off[i] + t of k and v goes to position pos0[i] + t of
+ * request i, for t < off[i+1] - off[i].
+ *   k, v  bf16 [rows][heads][dh], k_stride / v_stride elements from one row
+ *         to the next (>= heads*dh, a multiple of 8), 16-byte aligned: the
+ *         K and V columns of one projection's output serve as they are
+ *   off   int32 [B+1], as q_off of dllm_block_attn (rows it names beyond
+ *         `rows` are skipped, DLLM_DEV_OFFSETS; rows it names in no request
+ *         are not read); pos0 int32 [B]; page_table int32 [B][max_pages]
+ * Slots that no row is stored in keep their bytes. Two rows for one slot
+ * leave it unspecified. B <= 4096. No workspace. */
+dllm_status dllm_kv_write(const dllm_kv_pages *pages /* host */,
+                          const dllm_bf16 *k, const dllm_bf16 *v,
+                          long long k_stride, long long v_stride, int rows,
+                          const int32_t *off, const int32_t *pos0,
+                          const int32_t *page_table, int max_pages, int B,
+                          dllm_stream stream);
+
+/* dllm_kv_read -- the cache rows of given positions as contiguous bf16:
+ * position pos0[i] + t of request i to row off[i] + t of k and v
+ * [rows][heads][dh], in the layout that dllm_block_attn reads. e4m3 rows are
+ * read back exactly (every value they stand for is a bf16 value). Rows of k
+ * and v in no request keep their values. Other arguments as above. */
+dllm_status dllm_kv_read(const dllm_kv_pages *pages /* host */, dllm_bf16 *k,
+                         dllm_bf16 *v, int rows, const int32_t *off,
+                         const int32_t *pos0, const int32_t *page_table,
+                         int max_pages, int B, dllm_stream stream);
+
+/* ---------------------------------------------------------------------
+ * dllm_paged_attn -- attention of new tokens over the paged cache: single
+ * tokens, blocks and pieces of prompts, in any mix.
+ *
+ *   Query row t of request i (row q_off[i] + t of q, t < W_i) has position
+ *   p = q_pos[i] + t. It sees the cached positions u with
+ *     0 <= u < kv_len[i],
+ *     u <= p + right             (right >= 0; right < 0: no limit), and
+ *     u >= p - left or u < sinks (left >= 0; left < 0: no limit),
+ *   so right = 0 is causal order, left = right = -1 the bidirectional
+ *   attention of a denoising step, and left = w - 1 with sinks = s a sliding
+ *   window of w tokens beside the first s. Query head h reads cached head
+ *   h / (Hq / heads):
+ *     out[t,h,:] = sum_u softmax_u(scale * <q[t,h,:], k[u,:]>) v[u,:]
+ *     lse[t,h]   = log sum_u exp(scale * <q[t,h,:], k[u,:]>)
+ *   A row that sees no key gets zeros, and lse = -infinity.
+ *
+ *   q        bf16 [q_rows][Hq][dh], q_stride elements from row to row
+ *            (>= Hq*dh, a multiple of 8), 16-byte aligned
+ *   out      [q_rows][Hq][dh] bf16 (out_fp32 = 0) or float; lse float
+ *            [q_rows][Hq] or NULL. Rows in no request keep their values.
+ *   q_off    int32 [B+1], kv_len int32 [B], q_pos int32 [B] or NULL (then
+ *            kv_len[i] - W_i: the rows are the last ones of the cache),
+ *            page_table int32 [B][max_pages], all on the device
+ *   max_q, max_kv  host upper bounds of W_i and kv_len[i]; what is beyond
+ *            them, q_rows or the table is not processed (DLLM_DEV_OFFSETS)
+ * The cache must hold the rows' own K/V already (dllm_kv_write before, on
+ * the same stream). Cached rows that no query row of the request sees may
+ * hold anything, infinities and NaN included.
+ *   Scores, maxima, sums and outputs are accumulated in fp32; the weights
+ *   that multiply V are rounded to bf16 (e4m3 pages: to 9 bits or more).
+ *   The same call on the same GPU gives the same bits.
+ *   Supported: Hq a multiple of heads, Hq / heads <= 64; B <= 4096;
+ *   left, right, sinks < 2^30.
+ * dllm_paged_attn_workspace: bytes that serve this call and every call with
+ * the same pages and Hq and no larger B, max_q or max_kv; 0 for an
+ * unsupported shape. The contents need not be kept between calls. Calls
+ * that may run at the same time need a workspace each.
+ * ------------------------------------------------------------------- */
+typedef struct {
+  const dllm_bf16 *q;
+  long long q_stride;
+  void *out;
+  int out_fp32;
+  float *lse;
+  const int32_t *q_off, *kv_len, *q_pos, *page_table;
+  int max_pages, B, Hq, max_q, max_kv, q_rows;
+  float scale;
+  int left, right, sinks;
+} dllm_paged_attn_args;
+size_t dllm_paged_attn_workspace(const dllm_kv_pages *pages /* host */,
+                                 const dllm_paged_attn_args *args /* host */);
+dllm_status dllm_paged_attn(const dllm_kv_pages *pages /* host */,
+                            const dllm_paged_attn_args *args /* host */,
+                            void *ws, size_t ws_bytes, dllm_stream stream);
 
 /* ---------------------------------------------------------------------
  * Status helpers.
