@@ -36,14 +36,6 @@ __device__ __forceinline__ int request_of(const int32_t *off, int B, int r) {
   return lo;
 }
 
-// Exponent byte of a row with the largest magnitude bits `a` (finite bf16):
-// the least e >= -117 with |x| <= 448 * 2^e, + 127. 448 = 1.75 * 2^8, and
-// |x| = (1 + m / 128) * 2^(a >> 7 - 127).
-__device__ __forceinline__ int scale_byte(uint32_t a) {
-  const int b = static_cast<int>(a >> 7) - 8 + ((a & 127) > 96 ? 1 : 0);
-  return min(max(b, 10), 247);
-}
-
 // Eight bf16 -> eight e4m3 codes of x * f. `odd`: the row holds an infinity
 // or NaN, or magnitudes whose code would stand for 2^128.
 __device__ __forceinline__ uint2 quantise8(const uint4 &u, float f, bool odd, float top) {
@@ -57,9 +49,7 @@ __device__ __forceinline__ uint2 quantise8(const uint4 &u, float f, bool odd, fl
       a = isinf(a) ? NAN : (a > top ? top : a < -top ? -top : a);
       b = isinf(b) ? NAN : (b > top ? top : b < -top ? -top : b);
     }
-    uint16_t p;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(b), "f"(a));
-    w[i] = p;
+    w[i] = f32_to_e4m3x2(a, b);
   }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
@@ -69,17 +59,6 @@ __device__ __forceinline__ uint32_t max_mag(const uint4 &u, uint32_t m) {
   m = __vmaxu2(m, u.y & 0x7fff7fffu);
   m = __vmaxu2(m, u.z & 0x7fff7fffu);
   return __vmaxu2(m, u.w & 0x7fff7fffu);
-}
-
-// Largest finite magnitude among the halves of u (slow path).
-__device__ __forceinline__ uint32_t max_finite(const uint4 &u, uint32_t m) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = w[i] & 0x7fffu, b = (w[i] >> 16) & 0x7fffu;
-    if (a < 0x7f80u) m = max(m, a);
-    if (b < 0x7f80u) m = max(m, b);
-  }
-  return m;
 }
 
 // Quantise one row held by LPR lanes (chunks a, b of this lane); returns the
@@ -92,7 +71,7 @@ __device__ __forceinline__ int quantise_row(const uint4 &a, const uint4 &b, uint
   for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   const bool nonfinite = m >= 0x7f80u;
   if (__any_sync(0xffffffffu, nonfinite)) {
-    uint32_t f = max_finite(b, max_finite(a, 0));
+    uint32_t f = max(row_top_bits(a), row_top_bits(b));
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) f = max(f, __shfl_xor_sync(0xffffffffu, f, o));
     m = f;

@@ -2,10 +2,38 @@
 // grouped query heads, causal or bidirectional, sliding window with the
 // first tokens visible.
 //
-// One warp per (query row, query head): the lanes split dh, each key's score
-// is a warp sum, and the softmax runs with a running maximum and sum in
-// registers, one pass over the visible keys.
-#include "pages.cuh"
+// The work of one (request, cached head) is S^T = K Q^T over the head's
+// cached rows, with the query rows that share the head (W rows x group heads)
+// as N. Keys are the M = 128 rows of the tensor-core tile, so N is as small
+// as the rows are (16, 32 or 64): a single token costs a tile of 16, not of
+// 128, the exponentials of one key tile spread over 128 threads (one key
+// each, whatever N is), and a key's scales and visibility are one thread's
+// scalars. O^T = V^T P^T accumulates in TMEM.
+//
+// The key tiles of all (request, head, row tile) items form one line that is
+// cut into equal pieces, one per CTA: long and short requests balance, and a
+// single long one spreads over the whole GPU. An item that a cut divides
+// leaves partial (m, l, O) of its pieces in the workspace, and a second
+// kernel joins them.
+//
+// Warp roles:
+//   warp 0      TMA: one box per page and tile; K and V tiles alternate in one ring
+//   warp 1      S^T MMAs: K tile (A) x query rows (B) into S buffer n mod 3
+//   warp 2      O^T MMAs: V tile (A, transposed by its descriptor) x P (B)
+//   warps 4..   softmax warpgroups of 128 threads, one key each; a group
+//               takes up to 32 columns (query rows)
+//   last four   (e4m3 pages) V codes -> bf16 tiles
+// A reference maximum per row moves only when a score passes it by more than
+// 2^8 (P is bf16: no precision is lost), so most tiles need no maximum at
+// all, only the vote that nobody passed it.
+//
+// e4m3 pages: K codes go to the tensor cores as they are, against the query
+// rows split into two e4m3 parts (high + low: exact for elements within 2^-10
+// of the row's largest, else 2^-19 of that off), and the key's scale is a
+// factor of its thread's scores. V codes become bf16, which holds them
+// exactly, and the scale enters P before its one rounding to bf16, so tail
+// weights keep their relative precision however small they are.
+#include "paged.cuh"
 
 namespace dllm {
 
@@ -13,122 +41,726 @@ DLLM_DEFINE_STATUS(paged)
 
 namespace {
 
-struct PagedArgs {
-  KvPages c;
-  const uint16_t *q;
-  long long q_stride;
-  void *out;
-  int out_fp32;
-  float *lse;
-  const int32_t *q_off, *kv_len, *q_pos;
-  int B, Hq, group, max_q, max_kv, q_rows;
-  float scale;
-  int left, right, sinks;
-  unsigned int *status;
+constexpr int kSBuf = 3, kPBuf = 2, kCBuf = 2;
+constexpr int kMinTiles = 2;     // fewest tiles a CTA is given: each piece costs a prologue and a join
+constexpr int kMaxCtas = 192;    // bound of the workspace, above any GB300's SM count
+
+template <int DH, bool FP8, int N>
+struct Cfg {
+  static constexpr int kGroups = N > 32 ? N / 32 : 1;           // softmax warpgroups
+  static constexpr int kCols = N / kGroups;                     // columns of one group: 16 or 32
+  static constexpr int kConvWarps = FP8 ? 4 : 0;
+  static constexpr int kThreads = 32 * (4 + 4 * kGroups + kConvWarps);
+  static constexpr int kConvWarp0 = 4 + 4 * kGroups;
+  static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);       // one K or V tile as it is cached
+  static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);        // eight cached rows
+  static constexpr int kVGroup8 = 8 * DH * 2;                   // eight bf16 rows of V
+  static constexpr int kP = kTile * N * 2;
+  static constexpr int kQ = N * DH * 2;                         // bf16, or two e4m3 parts
+  static constexpr int kConv = FP8 ? kCBuf * kTile * DH * 2 : 0;
+  static constexpr int kFixed = kConv + kPBuf * kP + kQ + 8192;  // 8192: row tables, barriers, alignment
+  static constexpr int kMaxStages = (232448 - kFixed) / kRaw;
+  // even, so that K tiles have the even stages; 192 KB in flight are enough
+  static constexpr int kStages = (kMaxStages * kRaw > 196608 ? 196608 / kRaw : kMaxStages) & ~1;
+  static constexpr int kOffConv = kStages * kRaw;
+  static constexpr int kOffP = kOffConv + kConv;
+  static constexpr int kOffQ = kOffP + kPBuf * kP;
+  static constexpr int kOffMisc = kOffQ + kQ;
+  static constexpr int kBytes = kOffMisc + 8192;
+  static constexpr uint32_t kTmemCols = N * 4;                  // three S buffers and O
+  static_assert(kStages >= 4 && kBytes <= 232448, "shared memory");
 };
 
-// Request i clipped to the buffers and host bounds: query rows [q0, q0 + W),
-// L keys, position of the first row.
-struct Extent {
-  int q0, W, L, pos;
+// What the softmax needs to know of the row tile's rows.
+template <int N>
+struct RowInfo {
+  int lo[N], hi[N];   // the keys the row sees, apart from the sinks
+  int out[N];         // row of out [q_rows * Hq], or -1: not a query row
+  float scale[N];     // e4m3 parts: what the query row was divided by
 };
 
-__device__ __forceinline__ Extent paged_extent(const PagedArgs &a, int i, bool report) {
+// The pieces of work of one CTA, walked alike by every warp.
+struct Walk {
+  const PagedArgs &a;
+  int n_rows;
+  int i, item, j;          // request, item of the request, tile of the item
+  long long left;          // tiles of this CTA still to come
   Extent x;
-  bool bad = false;
-  x.q0 = a.q_off[i];
-  x.W = a.q_off[i + 1] - x.q0;
-  x.L = a.kv_len[i];
-  if (x.q0 < 0 || x.W < 0 || x.q0 > a.q_rows) { bad = true; x.q0 = 0; x.W = 0; }
-  if (x.W > a.q_rows - x.q0) { bad = true; x.W = a.q_rows - x.q0; }
-  if (x.W > a.max_q) { bad = true; x.W = a.max_q; }
-  if (x.L < 0) { bad = true; x.L = 0; }
-  if (x.L > a.max_kv) { bad = true; x.L = a.max_kv; }
-  // positions beyond +-2^30 see nothing or everything alike
-  x.pos = a.q_pos ? min(max(a.q_pos[i], -(1 << 30)), 1 << 30) : x.L - x.W;
-  if (bad && report) atomicOr(a.status, DLLM_DEV_OFFSETS);
-  return x;
-}
-
-// Keys [lo, hi) that a row at position p sees apart from the sinks.
-__device__ __forceinline__ void visible(const PagedArgs &a, int p, int L, int &lo, int &hi) {
-  hi = a.right < 0 ? L : min(L, max(p + a.right + 1, 0));
-  lo = a.left < 0 ? 0 : max(p - a.left, 0);
-}
-
-template <int DH, bool FP8>
-__device__ __forceinline__ void load_row(const KvPages &c, const uint8_t *pool, const uint8_t *scale, int row, int lane,
-                                         float (&x)[DH / 32]) {
-  constexpr int N = DH / 32;
-  if (row < 0) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) x[e] = 0.f;
-    return;
+  int n, items, row_tiles;
+  // the current piece
+  int h, rt, j0, j1;       // head, row tile, tiles [j0, j1) of it
+  TileList t;
+  __device__ __forceinline__ Walk(const PagedArgs &args, int rows) : a(args), n_rows(rows) {}
+  __device__ __forceinline__ void load() {
+    x = paged_extent(a, i, false);
+    row_tiles = (x.W * a.group + n_rows - 1) / n_rows;
+    items = row_tiles * a.c.heads;
+    n = items ? tiles_per_item(a, x, n_rows) : 0;
   }
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    while (item >= items) {
+      if (++i >= a.B) return false;
+      item = 0;
+      load();
+    }
+    h = item / row_tiles;
+    rt = item - h * row_tiles;
+    j0 = j;
+    j1 = static_cast<int>(min(static_cast<long long>(n), j + left));
+    left -= j1 - j0;
+    if (j1 == n) { j = 0; ++item; } else { j = j1; }
+    t = tile_list(a, x, rt, n_rows);
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == n; }
+  __device__ __forceinline__ int tiles() const { return max(min(j1, t.count) - j0, 0); }   // that hold visible keys
+};
+
+// Where this CTA starts: the total of all items' tiles, cut into gridDim.x
+// pieces. Every thread of the CTA takes part; s_scan holds 32 values.
+struct Start {
+  long long residual;   // tiles of request i before this CTA's first
+  long long left;       // tiles of this CTA
+  long long per;        // tiles of every CTA
+  int i;
+};
+
+__device__ __forceinline__ long long request_tiles(const PagedArgs &a, int i, int n_rows, bool report) {
+  const Extent x = paged_extent(a, i, report);
+  const long long items = static_cast<long long>((static_cast<long long>(x.W) * a.group + n_rows - 1) / n_rows) * a.c.heads;
+  return items ? items * tiles_per_item(a, x, n_rows) : 0;
+}
+
+__device__ void find_start(const PagedArgs &a, int n_rows, int min_tiles, long long *s_scan, Start *s_start) {
+  const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int chunk = (a.B + nt - 1) / nt;
+  const int i0 = tid * chunk, i1 = min(a.B, i0 + chunk);
+  long long mine = 0;
+  for (int i = i0; i < i1; ++i) mine += request_tiles(a, i, n_rows, blockIdx.x == 0);
+  long long incl = mine;
 #pragma unroll
-  for (int e = 0; e < N; e += 2) {
-    const size_t at = static_cast<size_t>(row) * DH + lane * N + e;
-    if constexpr (FP8) {
-      const float2 v = e4m3x2_to_f32(*reinterpret_cast<const uint16_t *>(pool + at));
-      const float s = __uint_as_float(static_cast<uint32_t>(scale[row]) << 23);
-      x[e] = v.x * s; x[e + 1] = v.y * s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  if (tid == 0) s_start->left = 0;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < nt / 32; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(min_tiles));
+  if (a.uniform) per = (per + a.uniform - 1) / a.uniform * a.uniform;
+  const long long begin = per * blockIdx.x;
+  const long long excl = before + incl - mine;
+  if (begin >= excl && begin < excl + mine) {
+    long long at = excl;
+    for (int i = i0; i < i1; ++i) {
+      const long long m = request_tiles(a, i, n_rows, false);
+      if (begin < at + m) {
+        s_start->i = i;
+        s_start->residual = begin - at;
+        s_start->left = min(per, total - begin);
+        s_start->per = per;
+        break;
+      }
+      at += m;
+    }
+  }
+  __syncthreads();
+}
+
+// v[k] of every lane reduced over the warp's lanes, for CNT values: lane c
+// (mod CNT) ends with the result of value c. CNT - 1 shuffles (+ 1 for 16).
+template <int CNT, typename Op>
+__device__ __forceinline__ float reduce_columns(float (&v)[CNT], int lane, Op op) {
+#pragma unroll
+  for (int o = CNT / 2; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int k = 0; k < o; ++k) {
+      const float send = up ? v[k] : v[k + o], keep = up ? v[k + o] : v[k];
+      v[k] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+  float r = v[0];
+#pragma unroll
+  for (int o = CNT; o < 32; o <<= 1) r = op(r, __shfl_xor_sync(0xffffffffu, r, o));
+  return r;
+}
+
+template <int CNT>
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[CNT]) {
+  if constexpr (CNT == 32) tmem_ld32(addr, r); else tmem_ld16(addr, r);
+}
+template <int CNT>
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[CNT]) {
+  if constexpr (CNT == 32) tmem_st32(addr, r); else tmem_st16(addr, r);
+}
+
+// Query rows [c0, c0 + COLS) of the row tile into shared memory as the B
+// operand of S^T (core matrices along K, row groups of 8), by 128 threads,
+// with what the softmax needs to know of each row.
+template <int DH, bool FP8, int N, int COLS>
+__device__ __forceinline__ void stage_queries(const PagedArgs &a, const Walk &w, uint8_t *sq, RowInfo<N> &info, int c0, int tid) {
+  const int rows = w.x.W * a.group;
+  constexpr int kChunks = DH / 8;                  // 16-byte chunks of a bf16 row
+  constexpr int kRounds = COLS * kChunks / 128;
+#pragma unroll
+  for (int it = 0; it < kRounds; ++it) {
+    const int idx = it * 128 + tid, n = c0 + idx / kChunks, c = idx % kChunks;
+    const int r = w.rt * N + n, t = r / a.group, g = r - t * a.group;
+    const bool live = r < rows;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (live)
+      u = *reinterpret_cast<const uint4 *>(a.q + (w.x.q0 + t) * a.q_stride + (w.h * a.group + g) * DH + c * 8);
+    if constexpr (!FP8) {
+      *reinterpret_cast<uint4 *>(sq + (n / 8) * (kChunks * 128) + c * 128 + (n % 8) * 16) = u;
     } else {
-      const uint32_t v = *reinterpret_cast<const uint32_t *>(pool + at * 2);
-      x[e] = __uint_as_float(v << 16); x[e + 1] = __uint_as_float(v & 0xffff0000u);
+      // scaled by a power of two into (224, 448], then hi = rn(x), lo = rn(x - hi)
+      uint32_t m = row_top_bits(u);
+#pragma unroll
+      for (int o = kChunks / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const int byte = scale_byte(m);
+      float x[8];
+      unpack8(u, x);
+      const float f = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // an infinity times the factor minus itself is NaN: it reaches every score of the row
+        const float p = x[2 * e] * f, q = x[2 * e + 1] * f;
+        const uint16_t hh = f32_to_e4m3x2(p, q);
+        const float2 b = e4m3x2_to_f32(hh);
+        hi[e] = hh;
+        lo[e] = f32_to_e4m3x2(p - b.x, q - b.y);
+      }
+      uint8_t *d = sq + (n / 8) * (DH / 16 * 128) + (c / 2) * 128 + (n % 8) * 16 + (c & 1) * 8;
+      *reinterpret_cast<uint2 *>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+      *reinterpret_cast<uint2 *>(d + N * DH) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+      if (c == 0) info.scale[n] = __uint_as_float(static_cast<uint32_t>(byte) << 23);
+    }
+    if (c == 0) {
+      int lo = 0, hi = 0x7fffffff;   // a column that is no row masks nothing; its results go nowhere
+      if (live) visible(a, static_cast<long long>(w.x.pos) + t, w.x.L, lo, hi);
+      info.lo[n] = lo;
+      info.hi[n] = hi;
+      info.out[n] = live ? (w.x.q0 + t) * a.Hq + w.h * a.group + g : -1;
     }
   }
 }
 
-template <int DH, bool FP8>
-__global__ void __launch_bounds__(128) paged_attn_rows_kernel(const PagedArgs a) {
-  constexpr int N = DH / 32;
+template <int DH, bool FP8, int N>
+__global__ void __launch_bounds__(Cfg<DH, FP8, N>::kThreads, 1)
+paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a,
+                  const int min_tiles) {
+  using C = Cfg<DH, FP8, N>;
+  constexpr int kSt = C::kStages, kCols = C::kCols;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *misc = smem + C::kOffMisc;
+  RowInfo<N> *info = reinterpret_cast<RowInfo<N> *>(misc);                // [2]: this piece's and the next one's
+  float *m_s = reinterpret_cast<float *>(info + 2);                       // [N] reference maxima
+  float *corr_s = m_s + N;                                                // [N]
+  float *red_s = corr_s + N;                                              // [4][N]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(red_s + 4 * N);
+  uint64_t *full = bars;                    // [kSt] stage loaded
+  uint64_t *empty = full + kSt;             // [kSt] stage read by its MMAs (or converted)
+  uint64_t *s_full = empty + kSt;           // [kSBuf]
+  uint64_t *s_free = s_full + kSBuf;        // [kSBuf]
+  uint64_t *p_full = s_free + kSBuf;        // [kPBuf]
+  uint64_t *p_free = p_full + kPBuf;        // [kPBuf] O^T MMAs of the tile done
+  uint64_t *c_full = p_free + kPBuf;        // [kCBuf] V tile converted
+  uint64_t *q_full = c_full + kCBuf;
+  uint64_t *o_full = q_full + 1;
+  uint64_t *o_free = o_full + 1;
+  long long *s_scan = reinterpret_cast<long long *>(o_free + 1);          // [32]
+  Start *start = reinterpret_cast<Start *>(s_scan + 32);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  static_assert(2 * sizeof(RowInfo<N>) + 6 * N * 4 + (2 * kSt + 2 * kSBuf + 2 * kPBuf + kCBuf + 3) * 8 + 256 + 64 <= 8192 - 1024,
+                "row tables and barriers");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, h = blockIdx.y * 4 + (threadIdx.x >> 5), i = blockIdx.z, t = blockIdx.x;
-  const Extent x = paged_extent(a, i, t == 0 && blockIdx.y == 0 && threadIdx.x == 0);
-  if (t >= x.W || h >= a.Hq) return;
-  const int kh = h / a.group;
-  const size_t r = static_cast<size_t>(x.q0) + t;
-  float q[N], o[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) {
-    q[e] = bf16_to_f32(a.q[r * a.q_stride + h * DH + lane * N + e]) * a.scale;
-    o[e] = 0.f;
+  if (threadIdx.x == 0) {
+    constexpr int kSoftWarps = 4 * C::kGroups;
+    for (int s = 0; s < kSt; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], FP8 && (s & 1) ? 4 : 1);
+    }
+    for (int b = 0; b < kSBuf; ++b) { mbar_init(&s_full[b], 1); mbar_init(&s_free[b], kSoftWarps); }
+    for (int b = 0; b < kPBuf; ++b) { mbar_init(&p_full[b], kSoftWarps); mbar_init(&p_free[b], 1); }
+    for (int b = 0; b < kCBuf; ++b) mbar_init(&c_full[b], 4);
+    mbar_init(q_full, kSoftWarps);
+    mbar_init(o_full, 1);
+    mbar_init(o_free, kSoftWarps);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
-  int lo, hi;
-  visible(a, x.pos + t, x.L, lo, hi);
-  float m = -INFINITY, l = 0.f;
-  bool bad = false;
-  const int first = a.left >= 0 ? min(a.sinks, min(lo, hi)) : 0;   // sinks before the window
-  for (int n = 0; n < first + max(hi - lo, 0); ++n) {
-    const int u = n < first ? n : lo + n - first;
-    int row = page_row(a.c, i, u);
-    if (row < 0) bad = true; else row += kh << a.c.page_shift;
-    float k[N], v[N];
-    load_row<DH, FP8>(a.c, a.c.k, a.c.k_scale, row, lane, k);
-    load_row<DH, FP8>(a.c, a.c.v, a.c.v_scale, row, lane, v);
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < N; ++e) s = fmaf(q[e], k[e], s);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s);
-    const float corr = m == mn ? 1.f : expf(m - mn), p = expf(s - mn);
-    l = l * corr + p;
-#pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = fmaf(p, v[e], o[e] * corr);
-    m = mn;
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
   }
-  if (bad && lane == 0) atomicOr(a.status, DLLM_DEV_PAGE);
-  const float inv = l != 0.f ? 1.f / l : 0.f;   // a row that sees nothing: zeros
-#pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const size_t at = (r * a.Hq + h) * DH + lane * N + e;
-    if (a.out_fp32) static_cast<float *>(a.out)[at] = o[e] * inv;
-    else static_cast<uint16_t *>(a.out)[at] = f32_to_bf16(o[e] * inv);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t t_o = tmem + kSBuf * N;
+
+  pdl_wait();   // the batch's metadata, the pages and the queries may come from the previous kernel
+  find_start(a, N, min_tiles, s_scan, start);
+  Walk w(a, N);
+  w.left = start->left;
+  if (w.left > 0) {
+    w.i = start->i;
+    w.load();
+    w.item = static_cast<int>(start->residual / w.n);
+    w.j = static_cast<int>(start->residual - static_cast<long long>(w.item) * w.n);
   }
-  if (a.lse && lane == 0) a.lse[r * a.Hq + h] = l != 0.f ? m + logf(l) : -INFINITY;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- producer
+    const int per_tile = kTile >> a.c.page_shift;
+    const int page_rows = 1 << a.c.page_shift;
+    const int none = static_cast<int>((static_cast<long long>(a.c.num_pages) * a.c.heads << a.c.page_shift) / 8);
+    bool bad = false, ok = true;
+    uint32_t n = 0, issued = 0;
+    while (ok && w.next()) {
+      const int nT = w.tiles();
+      const int32_t *row = a.c.table + static_cast<size_t>(w.i) * a.c.max_pages;
+      // 8-row group of lane's page of tile j; pages without cached rows read as zeros
+      auto group_of = [&](int j) {
+        if (lane >= per_tile || j >= w.j0 + nT) return none;
+        const long long u = static_cast<long long>(w.t.tile(j)) * kTile + lane * page_rows;
+        if (u >= w.x.L) return none;
+        const int page = __ldg(row + (u >> a.c.page_shift));
+        if (page < 0 || page >= a.c.num_pages) { bad = true; return none; }
+        return ((page * a.c.heads + w.h) << a.c.page_shift) / 8;
+      };
+      int g = group_of(w.j0);
+      for (int j = w.j0; j < w.j0 + nT; ++j, ++n) {
+        const int g_next = group_of(j + 1);     // its latency passes behind this tile's waits
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t pos = 2 * n + kv, st = pos % kSt, round = pos / kSt;
+          if (round > 0) ok = mbar_wait(&empty[st], (round - 1) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kRaw);
+          __syncwarp();
+          if (lane < per_tile)
+            tma_load_4d(smem + st * C::kRaw + lane * page_rows * (C::kGroup8 / 8), kv ? &tm_v : &tm_k, &full[st], g);
+          issued = pos + 1;
+        }
+        if (!ok) break;
+        g = g_next;
+      }
+    }
+    if (bad) atomicOr(a.status, DLLM_DEV_PAGE);
+    // after an abort: the loads in flight land before the CTA's memory is given up
+    if (!ok && lane < kSt && lane < issued) mbar_drain(&full[lane], ((issued - 1 - lane) / kSt) & 1);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- S^T MMAs
+    if (lane == 0) {
+      uint32_t n = 0, seg = 0;
+      bool ok = true;
+      const uint32_t sq = smem_u32(smem + C::kOffQ);
+      while (ok && w.next()) {
+        const int nT = w.tiles();
+        if (nT == 0) continue;
+        ok = mbar_wait(q_full, seg++ & 1, abort_flag);
+        for (int j = 0; ok && j < nT; ++j, ++n) {
+          const uint32_t pos = 2 * n, st = pos % kSt, b = n % kSBuf;
+          ok = mbar_wait(&full[st], (pos / kSt) & 1, abort_flag) &&
+               (n < kSBuf || mbar_wait(&s_free[b], (n / kSBuf - 1) & 1, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sk = smem_u32(smem + st * C::kRaw);
+          if constexpr (!FP8) {
+            const uint64_t dk = sw128_desc(sk, 16, C::kGroup8), dq = plain_desc(sq, 128, DH / 8 * 128);
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk)
+              umma_bf16(tmem + b * N, dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), dq + ((kk * 256) >> 4),
+                        idesc_bf16(128, N, 0, 0), kk > 0);
+          } else {
+            const uint64_t dk = DH == 128 ? sw128_desc(sk, 16, C::kGroup8) : sw64_desc(sk, 16, C::kGroup8);
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              const uint64_t dq = plain_desc(sq + part * N * DH, 128, DH / 16 * 128);
+#pragma unroll
+              for (int kk = 0; kk < DH / 32; ++kk)
+                umma_f8(tmem + b * N, dk + ((kk * 32) >> 4), dq + ((kk * 256) >> 4), idesc_e4m3(128, N), part + kk > 0);
+            }
+          }
+          umma_commit(&s_full[b]);
+          umma_commit(&empty[st]);
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------- O^T MMAs
+    if (lane == 0) {
+      uint32_t n = 0, seg = 0;
+      bool ok = true;
+      while (ok && w.next()) {
+        const int nT = w.tiles();
+        if (nT == 0) continue;
+        for (int j = 0; ok && j < nT; ++j, ++n) {
+          const uint32_t pos = 2 * n + 1, st = pos % kSt, b = n % kPBuf;
+          ok = mbar_wait(&p_full[b], (n / kPBuf) & 1, abort_flag);
+          if (ok && j == 0 && seg > 0) ok = mbar_wait(o_free, (seg - 1) & 1, abort_flag);
+          uint32_t sv;
+          if constexpr (FP8) {
+            ok = ok && mbar_wait(&c_full[n % kCBuf], (n / kCBuf) & 1, abort_flag);
+            sv = smem_u32(smem + C::kOffConv + (n % kCBuf) * (kTile * DH * 2));
+          } else {
+            ok = ok && mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+            sv = smem_u32(smem + st * C::kRaw);
+          }
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dv = sw128_desc(sv, 1024, C::kVGroup8);
+          const uint64_t dp = plain_desc(smem_u32(smem + C::kOffP + b * C::kP), 128, 2048);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16(t_o, dv + ((kk * 2 * C::kVGroup8) >> 4), dp + ((kk * 256) >> 4), idesc_bf16(DH, N, 1, 1),
+                      j > 0 || kk > 0);
+          umma_commit(&p_free[b]);
+          if constexpr (!FP8) umma_commit(&empty[st]);
+          if (j + 1 == nT) umma_commit(o_full);
+        }
+        ++seg;
+      }
+    }
+  } else if (FP8 && warp >= C::kConvWarp0) {
+    // ------------------------------------------------------------- V codes -> bf16
+    if constexpr (FP8) {
+      const int key = (warp - C::kConvWarp0) * 32 + lane;
+      uint32_t n = 0;
+      while (w.next()) {
+        const int nT = w.tiles();
+        for (int j = 0; j < nT; ++j, ++n) {
+          const uint32_t pos = 2 * n + 1, st = pos % kSt, cb = n % kCBuf;
+          mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+          if (n >= kCBuf) mbar_wait(&p_free[n % kPBuf], (n / kPBuf - 1) & 1, abort_flag);
+          const int u = w.t.tile(w.j0 + j) * kTile + key;
+          const bool seen = u < w.t.hi && (u >= w.t.lo || u < a.sinks);
+          const uint8_t *src = smem + st * C::kRaw + key * DH;
+          uint8_t *dst = smem + C::kOffConv + cb * (kTile * DH * 2) + (key / 8) * C::kVGroup8 + (key % 8) * 128;
+#pragma unroll
+          for (int c = 0; c < DH / 16; ++c) {
+            // chunk c of the row under the load's swizzle (rows of 128 or 64 bytes)
+            const int sc = DH == 128 ? (c ^ (key & 7)) : (c ^ ((key >> 1) & 3));
+            uint4 q = *reinterpret_cast<const uint4 *>(src + sc * 16);
+            if (!seen) q = make_uint4(0, 0, 0, 0);   // 0 * NaN would not be 0
+            uint4 lo, hi;
+            e4m3x8_to_bf16(q.x, q.y, lo);
+            e4m3x8_to_bf16(q.z, q.w, hi);
+            uint8_t *d = dst + (c / 4) * 1024;
+            *reinterpret_cast<uint4 *>(d + (((2 * c) & 7) ^ (key & 7)) * 16) = lo;
+            *reinterpret_cast<uint4 *>(d + (((2 * c + 1) & 7) ^ (key & 7)) * 16) = hi;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&c_full[cb]);
+            mbar_arrive(&empty[st]);
+          }
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------- softmax
+    const int wg = (warp - 4) >> 2, quarter = warp & 3, tid = threadIdx.x & 127;
+    const int key = quarter * 32 + lane, c0 = wg * kCols;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    constexpr float kLazy = 8.f;
+    const auto maxop = [](float p, float q) { return fmaxf(p, q); };
+    const auto addop = [](float p, float q) { return p + q; };
+    uint32_t n = 0, seg = 0, o_seg = 0;
+    bool more = w.next();
+    bool joined = false;       // this CTA's last piece began an item that others finish
+    if (more) {
+      stage_queries<DH, FP8, N, kCols>(a, w, smem + C::kOffQ, info[0], c0, tid);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && w.tiles() > 0) mbar_arrive(q_full);
+    }
+    while (more) {
+      const RowInfo<N> &ri = info[seg & 1];
+      const int nT = w.tiles();
+      float l[kCols];
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) l[e] = 0.f;
+      named_bar_sync(1 + wg, 128);          // the rows' info is written, the last piece's maxima are read
+      if (tid < kCols) m_s[c0 + tid] = -INFINITY;
+      named_bar_sync(1 + wg, 128);
+      const int32_t *pages = a.c.table + static_cast<size_t>(w.i) * a.c.max_pages;
+      // scales of this thread's key in tile j (1 where no row sees it)
+      auto scales_of = [&](int j, float &ks, float &vs) {
+        ks = vs = 1.f;
+        if constexpr (FP8) {
+          if (j >= w.j0 + nT) return;
+          const int u = w.t.tile(j) * kTile + key;
+          if (u >= w.t.hi || !(u >= w.t.lo || u < a.sinks)) return;
+          const int page = __ldg(pages + (u >> a.c.page_shift));
+          if (page < 0 || page >= a.c.num_pages) return;
+          const size_t row = (static_cast<size_t>(page) * a.c.heads + w.h << a.c.page_shift) + (u & ((1 << a.c.page_shift) - 1));
+          ks = __uint_as_float(static_cast<uint32_t>(__ldg(a.c.k_scale + row)) << 23);
+          vs = __uint_as_float(static_cast<uint32_t>(__ldg(a.c.v_scale + row)) << 23);
+        }
+      };
+      float ks, vs;
+      scales_of(w.j0, ks, vs);
+      for (int j = 0; j < nT; ++j, ++n) {
+        const uint32_t b = n % kSBuf, pb = n % kPBuf;
+        float ks_next, vs_next;
+        scales_of(w.j0 + j + 1, ks_next, vs_next);
+        const int key0 = w.t.tile(w.j0 + j) * kTile, u = key0 + key;
+        // every row of the tile sees every key of it?
+        const bool all_seen = key0 + kTile <= w.t.hi_first && (key0 >= w.t.lo_last || key0 + kTile <= a.sinks);
+        const float c = a.scale_log2 * ks;
+        mbar_wait(&s_full[b], (n / kSBuf) & 1, abort_flag);
+        tc_fence_after();
+        uint32_t s[kCols];
+        const uint32_t t_s = tmem + lane_base + b * N + c0;
+        tmem_load<kCols>(t_s, s);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[b]);
+        // scores in log2 units
+        float d[kCols];
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) {
+          d[e] = __uint_as_float(s[e]) * (FP8 ? c * ri.scale[c0 + e] : c);
+          if (!all_seen) {
+            const int lo = ri.lo[c0 + e], hi = ri.hi[c0 + e];
+            if (!(u < hi && (u >= lo || u < a.sinks))) d[e] = -INFINITY;
+          }
+        }
+        bool pass = false;
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) pass |= d[e] > m_s[c0 + e] + kLazy;
+        // anyone's score past the reference: new maxima for the columns
+        if (bar_any(1 + wg, 128, pass)) {
+          float v[kCols];
+#pragma unroll
+          for (int e = 0; e < kCols; ++e) v[e] = d[e];
+          const float top = reduce_columns<kCols>(v, lane, maxop);
+          if (lane < kCols) red_s[quarter * N + c0 + lane] = top;
+          named_bar_sync(1 + wg, 128);
+          if (tid < kCols) {
+            const int e = c0 + tid;
+            const float mx = fmaxf(fmaxf(red_s[e], red_s[N + e]), fmaxf(red_s[2 * N + e], red_s[3 * N + e]));
+            const float old = m_s[e], now = mx > old + kLazy ? mx : old;
+            corr_s[e] = now == old ? 1.f : ex2_approx(old - now);
+            m_s[e] = now;
+          }
+          named_bar_sync(1 + wg, 128);
+#pragma unroll
+          for (int e = 0; e < kCols; ++e) l[e] *= corr_s[c0 + e];
+          if (j > 0) {
+            // O holds exactly the tiles before this one once the last one's MMAs are done
+            mbar_wait(&p_free[(n - 1) % kPBuf], ((n - 1) / kPBuf) & 1, abort_flag);
+            tc_fence_after();
+            uint32_t o[kCols];
+            tmem_load<kCols>(t_o + lane_base + c0, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr_s[c0 + e]);
+            tmem_store<kCols>(t_o + lane_base + c0, o);
+            tmem_st_wait();
+            tc_fence_before();
+          }
+        }
+        // P = 2^(score - reference), its column sums per key, and P * v scale as bf16
+        uint32_t pk[kCols / 2];
+#pragma unroll
+        for (int e = 0; e < kCols; e += 2) {
+          const float ma = m_s[c0 + e], mb = m_s[c0 + e + 1];
+          float p = ex2_approx(d[e] - (ma == -INFINITY ? 0.f : ma));
+          float q = ex2_approx(d[e + 1] - (mb == -INFINITY ? 0.f : mb));
+          l[e] += p;
+          l[e + 1] += q;
+          if constexpr (FP8) { p *= vs; q *= vs; }
+          pk[e / 2] = pack_bf16x2(p, q);
+        }
+        if (n >= kPBuf) mbar_wait(&p_free[pb], (n / kPBuf - 1) & 1, abort_flag);
+        uint8_t *sp = smem + C::kOffP + pb * C::kP + (c0 / 8) * 2048 + (key / 8) * 128 + (key % 8) * 16;
+#pragma unroll
+        for (int e = 0; e < kCols / 8; ++e)
+          *reinterpret_cast<uint4 *>(sp + e * 2048) = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+        if constexpr (!FP8) {
+          // rows of V that no query row sees may hold anything, and 0 * NaN is not 0
+          if (wg == 0 && !(u < w.t.hi && (u >= w.t.lo || u < a.sinks))) {
+            const uint32_t pos = 2 * n + 1, st = pos % kSt;
+            mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+            uint8_t *sv = smem + st * C::kRaw + (key / 8) * C::kGroup8 + (key % 8) * 128;
+#pragma unroll
+            for (int e = 0; e < DH / 8; ++e)
+              *reinterpret_cast<uint4 *>(sv + (e / 8) * 1024 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[pb]);
+        ks = ks_next;
+        vs = vs_next;
+      }
+      // the next piece's queries are staged before this one's results are
+      // written: its scores run meanwhile (every S^T of this piece is done)
+      const Walk done = w;
+      more = w.next();
+      ++seg;
+      if (more) {
+        stage_queries<DH, FP8, N, kCols>(a, w, smem + C::kOffQ, info[seg & 1], c0, tid);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && w.tiles() > 0) mbar_arrive(q_full);
+      }
+      const float part = reduce_columns<kCols>(l, lane, addop);
+      if (lane < kCols) red_s[quarter * N + c0 + lane] = part;
+      named_bar_sync(1 + wg, 128);
+      if (tid < kCols) {
+        const int e = c0 + tid;
+        const float sum = (red_s[e] + red_s[N + e]) + (red_s[2 * N + e] + red_s[3 * N + e]);
+        corr_s[e] = sum;
+      }
+      if (nT > 0) {
+        mbar_wait(o_full, o_seg & 1, abort_flag);
+        ++o_seg;
+        tc_fence_after();
+      }
+      named_bar_sync(1 + wg, 128);
+      uint32_t o[kCols];
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) o[e] = 0;
+      if (nT > 0) {
+        tmem_load<kCols>(t_o + lane_base + c0, o);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
+      }
+      // M = 64: rows 16 q .. 16 q + 15 lie in the first 16 lanes of quarter q
+      const int dc = DH == 128 ? key : quarter * 16 + lane;
+      const bool dlive = DH == 128 || lane < 16;
+      if (done.whole()) {
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) {
+          const int row = ri.out[c0 + e];
+          if (row < 0) break;
+          const float sum = corr_s[c0 + e];
+          const float y = sum != 0.f ? __uint_as_float(o[e]) / sum : 0.f;
+          if (dlive) {
+            if (a.out_fp32) static_cast<float *>(a.out)[static_cast<size_t>(row) * DH + dc] = y;
+            else static_cast<uint16_t *>(a.out)[static_cast<size_t>(row) * DH + dc] = f32_to_bf16(y);
+          }
+        }
+        if (a.lse && tid < kCols && ri.out[c0 + tid] >= 0) {
+          const float sum = corr_s[c0 + tid];
+          a.lse[ri.out[c0 + tid]] = sum != 0.f ? (m_s[c0 + tid] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        }
+      } else {
+        // the first piece of a CTA goes to its first slot, a later one (its last) to the second
+        const size_t slot = static_cast<size_t>(blockIdx.x) * 2 + (seg > 1 ? 1 : 0);
+        float *po = a.part_o + (slot * N + c0) * DH + dc;
+        if (dlive)
+#pragma unroll
+          for (int e = 0; e < kCols; ++e) po[e * DH] = __uint_as_float(o[e]);
+        if (tid < kCols) a.part_ml[slot * N + c0 + tid] = make_float2(m_s[c0 + tid], corr_s[c0 + tid]);
+        if (done.j0 == 0) {
+          joined = true;
+          if (tid == 0 && wg == 0) {
+            // the item's other pieces are the first slots of the next CTAs
+            const int parts = 1 + static_cast<int>((done.n - done.j1 + start->per - 1) / start->per);
+            a.join[blockIdx.x] = make_int4(done.i, done.h * done.row_tiles + done.rt, static_cast<int>(slot), parts);
+          }
+        }
+      }
+    }
+    if (a.join && !joined && tid == 0 && wg == 0) a.join[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(a.status, DLLM_DEV_WAIT_TIMEOUT);
 }
 
+// Joins the partial results of the item that CTA blockIdx.x began and others
+// finished: block y takes the item's rows y, y + gridDim.y, ...
+constexpr int kJoinThreads = 256;
+
+template <int DH>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArgs a, const int n_rows) {
+  constexpr int kGroups = kJoinThreads / DH;      // threads of one column: each takes every kGroups-th piece
+  __shared__ float weight[2 * kMaxCtas];
+  __shared__ float acc[kJoinThreads];
+  __shared__ float sum_s;
+  pdl_trigger();
+  pdl_wait();
+  const int4 job = a.join[blockIdx.x];
+  const int parts = job.w;
+  if (parts == 0) return;
+  const Extent x = paged_extent(a, job.x, false);
+  const int row_tiles = (x.W * a.group + n_rows - 1) / n_rows;
+  const int h = job.y / row_tiles, rt = job.y - h * row_tiles;
+  const int tid = threadIdx.x, c = tid % DH, grp = tid / DH;
+  auto slot_of = [&](int p) { return static_cast<size_t>(p == 0 ? job.z : 2 * (blockIdx.x + p)); };
+  for (int n = blockIdx.y; n < n_rows; n += gridDim.y) {
+    const int r = rt * n_rows + n, t = r / a.group;
+    if (t >= x.W) break;
+    const int row = (x.q0 + t) * a.Hq + h * a.group + (r - t * a.group);
+    if (tid < 32) {
+      float m = -INFINITY, l = 0.f;
+      for (int p = tid; p < parts; p += 32) m = fmaxf(m, a.part_ml[slot_of(p) * n_rows + n].x);
+      m = warp_max(m);
+      for (int p = tid; p < parts; p += 32) {
+        const float2 ml = a.part_ml[slot_of(p) * n_rows + n];
+        const float wgt = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+        weight[p] = wgt;
+        l += wgt * ml.y;
+      }
+      l = warp_sum(l);
+      if (tid == 0) {
+        sum_s = l;
+        if (a.lse) a.lse[row] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      }
+    }
+    __syncthreads();
+    float y = 0.f;
+#pragma unroll 4
+    for (int p = grp; p < parts; p += kGroups) {
+      const float wgt = weight[p];
+      if (wgt != 0.f) y += wgt * a.part_o[(slot_of(p) * n_rows + n) * DH + c];
+    }
+    acc[tid] = y;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g) y += acc[g * DH + c];
+      y = sum_s != 0.f ? y / sum_s : 0.f;
+      if (a.out_fp32) static_cast<float *>(a.out)[static_cast<size_t>(row) * DH + c] = y;
+      else static_cast<uint16_t *>(a.out)[static_cast<size_t>(row) * DH + c] = f32_to_bf16(y);
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
 dllm_status check_shape(const dllm_kv_pages *pages, const dllm_paged_attn_args *a) {
   const dllm_status st = check_pages(pages);
   if (st != DLLM_OK) return st;
@@ -137,7 +769,73 @@ dllm_status check_shape(const dllm_kv_pages *pages, const dllm_paged_attn_args *
   if (a->Hq % pages->heads || a->Hq / pages->heads > 64 || a->B > 4096) return DLLM_ERR_UNSUPPORTED;
   if (a->left >= (1 << 30) || a->right >= (1 << 30) || a->sinks >= (1 << 30)) return DLLM_ERR_UNSUPPORTED;
   if (a->max_kv >= (1 << 30)) return DLLM_ERR_UNSUPPORTED;
+  if (static_cast<long long>(a->q_rows) * a->Hq >= (1ll << 31) || static_cast<long long>(a->max_q) * a->Hq >= (1ll << 31))
+    return DLLM_ERR_UNSUPPORTED;
   return DLLM_OK;
+}
+
+// Columns of a row tile: the least of 16, 32 and 64 that holds a request's
+// rows of one cached head, 64 where none does.
+int row_tile(const dllm_kv_pages *pages, const dllm_paged_attn_args *a) {
+  const long long rows = static_cast<long long>(a->max_q) * (a->Hq / pages->heads);
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+// A CTA's piece is at least kMinTiles tiles: items of no more are never cut.
+bool may_split(const dllm_paged_attn_args *a) { return a->max_kv > kMinTiles * kTile; }
+
+struct Ws {
+  size_t part_ml, join, total;   // part_o at 0
+};
+
+Ws ws_layout(const dllm_kv_pages *pages, const dllm_paged_attn_args *a) {
+  Ws w{};
+  if (a->B == 0 || a->max_q == 0 || !may_split(a)) return w;
+  const size_t rows = static_cast<size_t>(2 * kMaxCtas) * row_tile(pages, a);
+  w.part_ml = align256(rows * pages->dh * 4);
+  w.join = w.part_ml + align256(rows * 8);
+  w.total = w.join + align256(kMaxCtas * 16);
+  return w;
+}
+
+template <int DH, bool FP8, int N>
+dllm_status launch(const dllm_kv_pages *pages, const dllm_paged_attn_args *a, PagedArgs &g, cudaStream_t s) {
+  using C = Cfg<DH, FP8, N>;
+  CUtensorMap tk, tv;
+  const uint64_t rows = static_cast<uint64_t>(pages->num_pages) * pages->heads * pages->page_size;
+  if (!make_tmap_page_rows(&tk, pages->k, rows, DH, FP8 ? 1 : 2, pages->page_size) ||
+      !make_tmap_page_rows(&tv, pages->v, rows, DH, FP8 ? 1 : 2, pages->page_size))
+    return DLLM_ERR_CUDA;
+  auto kern = paged_attn_kernel<DH, FP8, N>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  if (e != cudaSuccess) return cuda_error(e);
+  // most tiles that the bounds allow, and so most CTAs with work
+  const long long row_tiles = (static_cast<long long>(a->max_q) * g.group + N - 1) / N;
+  const long long per_item = g.max_kv > 0 ? (g.max_kv + kTile - 1) / kTile : 1;
+  const bool split = may_split(a);
+  const int min_tiles = split ? kMinTiles : static_cast<int>(per_item);
+  g.uniform = split ? 0 : min_tiles;
+  const double most = static_cast<double>(a->B) * pages->heads * row_tiles * per_item;
+  int ctas = sm_budget() < kMaxCtas ? sm_budget() : kMaxCtas;
+  if (most / min_tiles < ctas) ctas = static_cast<int>(most / min_tiles) + 1;
+  e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kBytes, s, tk, tv, g, min_tiles);
+  if (e != cudaSuccess) return cuda_error(e);
+  unsigned launches = 1;
+  if (split) {
+    e = launch_pdl(paged_join_kernel<DH>, dim3(ctas, N < 16 ? N : 16), dim3(kJoinThreads), 0, s, g, N);
+    if (e != cudaSuccess) return cuda_error(e);
+    launches = 2;
+  }
+  return launch_status(launches);
+}
+
+template <int DH, bool FP8>
+dllm_status launch_n(const dllm_kv_pages *pages, const dllm_paged_attn_args *a, PagedArgs &g, cudaStream_t s) {
+  switch (row_tile(pages, a)) {
+    case 16: return launch<DH, FP8, 16>(pages, a, g, s);
+    case 32: return launch<DH, FP8, 32>(pages, a, g, s);
+    default: return launch<DH, FP8, 64>(pages, a, g, s);
+  }
 }
 
 }  // namespace
@@ -147,7 +845,7 @@ using namespace dllm;
 
 extern "C" size_t dllm_paged_attn_workspace(const dllm_kv_pages *pages, const dllm_paged_attn_args *a) {
   if (check_shape(pages, a) != DLLM_OK) return 0;
-  return 0;
+  return ws_layout(pages, a).total;
 }
 
 extern "C" dllm_status dllm_paged_attn(const dllm_kv_pages *pages, const dllm_paged_attn_args *a, void *ws,
@@ -161,6 +859,9 @@ extern "C" dllm_status dllm_paged_attn(const dllm_kv_pages *pages, const dllm_pa
   if (!aligned16(a->q) || !aligned16(a->out) || a->q_stride < static_cast<long long>(a->Hq) * pages->dh ||
       a->q_stride % 8)
     return DLLM_ERR_INVALID_ARG;
+  const Ws layout = ws_layout(pages, a);
+  if (layout.total > 0 && (!ws || ws_bytes < layout.total || (reinterpret_cast<uintptr_t>(ws) & 255)))
+    return DLLM_ERR_WORKSPACE;
   PagedArgs g{};
   g.c = device_pages(pages, a->page_table, a->max_pages);
   g.q = a->q; g.q_stride = a->q_stride; g.out = a->out; g.out_fp32 = a->out_fp32; g.lse = a->lse;
@@ -169,14 +870,18 @@ extern "C" dllm_status dllm_paged_attn(const dllm_kv_pages *pages, const dllm_pa
   // keys beyond the table are not there
   const long long table = static_cast<long long>(a->max_pages) * pages->page_size;
   g.max_kv = static_cast<int>(table < a->max_kv ? table : a->max_kv);
-  g.scale = a->scale;
+  g.scale_log2 = a->scale * 1.4426950408889634f;
   g.left = a->left; g.right = a->right; g.sinks = a->left >= 0 ? a->sinks : 0;
   cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&g.status), g_status_paged);
   if (e != cudaSuccess) return cuda_error(e);
+  if (layout.total > 0) {
+    char *base = static_cast<char *>(ws);
+    g.part_o = reinterpret_cast<float *>(base);
+    g.part_ml = reinterpret_cast<float2 *>(base + layout.part_ml);
+    g.join = reinterpret_cast<int4 *>(base + layout.join);
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool fp8 = pages->type == DLLM_KV_E4M3;
-  auto kern = pages->dh == 64 ? (fp8 ? paged_attn_rows_kernel<64, true> : paged_attn_rows_kernel<64, false>)
-                              : (fp8 ? paged_attn_rows_kernel<128, true> : paged_attn_rows_kernel<128, false>);
-  e = launch_pdl(kern, dim3(a->max_q, (a->Hq + 3) / 4, a->B), dim3(128), 0, static_cast<cudaStream_t>(stream), g);
-  if (e != cudaSuccess) return cuda_error(e);
-  return launch_status();
+  if (pages->dh == 64) return fp8 ? launch_n<64, true>(pages, a, g, s) : launch_n<64, false>(pages, a, g, s);
+  return fp8 ? launch_n<128, true>(pages, a, g, s) : launch_n<128, false>(pages, a, g, s);
 }

@@ -69,4 +69,44 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint16_t v) {
   return f;
 }
 
+// Two floats -> two e4m3 codes (nearest even, clamped to +-448; NaN stays NaN).
+__device__ __forceinline__ uint16_t f32_to_e4m3x2(float a, float b) {
+  uint16_t p;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(b), "f"(a));
+  return p;
+}
+
+// Eight codes -> eight bf16, exactly.
+__device__ __forceinline__ void e4m3x8_to_bf16(uint32_t a, uint32_t b, uint4 &out) {
+  float x[8];
+  const uint32_t w[2] = {a, b};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 p = e4m3x2_to_f32(static_cast<uint16_t>(w[i])), q = e4m3x2_to_f32(static_cast<uint16_t>(w[i] >> 16));
+    x[4 * i] = p.x; x[4 * i + 1] = p.y; x[4 * i + 2] = q.x; x[4 * i + 3] = q.y;
+  }
+  out = pack8(x);
+}
+
+// Exponent byte of a row with the largest magnitude bits `a` (finite bf16):
+// the least e >= -117 with |x| <= 448 * 2^e, + 127. 448 = 1.75 * 2^8, and
+// |x| = (1 + m / 128) * 2^(a >> 7 - 127).
+__device__ __forceinline__ int scale_byte(uint32_t a) {
+  const int b = static_cast<int>(a >> 7) - 8 + ((a & 127) > 96 ? 1 : 0);
+  return min(max(b, 10), 247);
+}
+
+// Largest finite magnitude bits among eight bf16.
+__device__ __forceinline__ uint32_t row_top_bits(const uint4 &u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = w[i] & 0x7fffu, b = (w[i] >> 16) & 0x7fffu;
+    if (a < 0x7f80u) m = max(m, a);
+    if (b < 0x7f80u) m = max(m, b);
+  }
+  return m;
+}
+
 }  // namespace dllm

@@ -45,6 +45,22 @@ bool make_tmap_bf16_sw128(CUtensorMap *map, const void *base, uint64_t rows, uin
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_page_rows(CUtensorMap *map, const void *base, uint64_t rows, int dh, int elem_bytes,
+                         uint32_t box_rows) {
+  EncodeTiledFn fn = encoder();
+  if (!fn || !base || rows == 0 || rows % 8 || box_rows % 8 || reinterpret_cast<uintptr_t>(base) % 16) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(dh) * elem_bytes;      // 64, 128 or 256 bytes
+  const cuuint32_t piece = row < 128 ? static_cast<cuuint32_t>(row) : 128u, pieces = static_cast<cuuint32_t>(row / piece);
+  cuuint64_t dims[4] = {piece / elem_bytes, 8, pieces, rows / 8};
+  cuuint64_t strides[3] = {row, piece, row * 8};
+  cuuint32_t box[4] = {piece / elem_bytes, 8, pieces, box_rows / 8};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+            const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            piece == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int num_sms() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
