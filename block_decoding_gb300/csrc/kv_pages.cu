@@ -36,53 +36,32 @@ __device__ __forceinline__ int request_of(const int32_t *off, int B, int r) {
   return lo;
 }
 
-// Eight bf16 -> eight e4m3 codes of x * f. `odd`: the row holds an infinity
-// or NaN, or magnitudes whose code would stand for 2^128.
-__device__ __forceinline__ uint2 quantise8(const uint4 &u, float f, bool odd, float top) {
+// Eight bf16 -> eight e4m3 codes of x * f, |x * f| limited to top.
+__device__ __forceinline__ uint2 quantise8(const uint4 &u, float f, float top) {
   float x[8];
   unpack8(u, x);
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a = x[2 * i] * f, b = x[2 * i + 1] * f;
-    if (odd) {   // an infinity becomes NaN; NaN passes through both comparisons
-      a = isinf(a) ? NAN : (a > top ? top : a < -top ? -top : a);
-      b = isinf(b) ? NAN : (b > top ? top : b < -top ? -top : b);
-    }
-    w[i] = f32_to_e4m3x2(a, b);
-  }
+  for (int i = 0; i < 4; ++i)
+    w[i] = f32_to_e4m3x2(fminf(fmaxf(x[2 * i] * f, -top), top), fminf(fmaxf(x[2 * i + 1] * f, -top), top));
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-__device__ __forceinline__ uint32_t max_mag(const uint4 &u, uint32_t m) {
-  m = __vmaxu2(m, u.x & 0x7fff7fffu);
-  m = __vmaxu2(m, u.y & 0x7fff7fffu);
-  m = __vmaxu2(m, u.z & 0x7fff7fffu);
-  return __vmaxu2(m, u.w & 0x7fff7fffu);
-}
-
 // Quantise one row held by LPR lanes (chunks a, b of this lane); returns the
-// exponent byte.
+// scale byte.
 template <int LPR>
 __device__ __forceinline__ int quantise_row(const uint4 &a, const uint4 &b, uint2 &qa, uint2 &qb) {
-  uint32_t m2 = max_mag(b, max_mag(a, 0));
+  const uint32_t m2 = max_mag(b, max_mag(a, 0));
   uint32_t m = max(m2 & 0xffffu, m2 >> 16);
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const bool nonfinite = m >= 0x7f80u;
-  if (__any_sync(0xffffffffu, nonfinite)) {
-    uint32_t f = max(row_top_bits(a), row_top_bits(b));
-#pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) f = max(f, __shfl_xor_sync(0xffffffffu, f, o));
-    m = f;
-  }
   const int byte = scale_byte(m);
   const float f = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
-  const bool odd = nonfinite || byte == 247;
+  // the code of a magnitude above 1.875 * 2^127 would stand for 2^128
   const float top = byte == 247 ? 240.f : 448.f;
-  qa = quantise8(a, f, odd, top);
-  qb = quantise8(b, f, odd, top);
-  return byte;
+  qa = quantise8(a, f, top);
+  qb = quantise8(b, f, top);
+  return m >= 0x7f80u ? 255 : byte;
 }
 
 // Unit = one row of one head; a warp holds 32 / LPR of them.
@@ -175,8 +154,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const MoveArgs g) {
       const uint2 *ks = reinterpret_cast<const uint2 *>(g.c.k + static_cast<size_t>(row) * DH);
       const uint2 *vs = reinterpret_cast<const uint2 *>(g.c.v + static_cast<size_t>(row) * DH);
       const uint2 qa = __ldg(ks + l), qb = __ldg(ks + l + LPR), pa = __ldg(vs + l), pb = __ldg(vs + l + LPR);
-      const float kf = __uint_as_float(static_cast<uint32_t>(g.c.k_scale[row]) << 23);
-      const float vf = __uint_as_float(static_cast<uint32_t>(g.c.v_scale[row]) << 23);
+      const float kf = scale_of(g.c.k_scale[row]);
+      const float vf = scale_of(g.c.v_scale[row]);
       ka = restore8(qa, kf); kb = restore8(qb, kf);
       va = restore8(pa, vf); vb = restore8(pb, vf);
     } else {

@@ -58,7 +58,8 @@ struct Cfg {
   static constexpr int kP = kTile * N * 2;
   static constexpr int kQ = N * DH * 2;                         // bf16, or two e4m3 parts
   static constexpr int kConv = FP8 ? kCBuf * kTile * DH * 2 : 0;
-  static constexpr int kFixed = kConv + kPBuf * kP + kQ + 8192;  // 8192: row tables, barriers, alignment
+  static constexpr int kMisc = FP8 ? 12288 : 8192;              // row tables, scales, barriers, alignment
+  static constexpr int kFixed = kConv + kPBuf * kP + kQ + kMisc;
   static constexpr int kMaxStages = (232448 - kFixed) / kRaw;
   // even, so that K tiles have the even stages; 192 KB in flight are enough
   static constexpr int kStages = (kMaxStages * kRaw > 196608 ? 196608 / kRaw : kMaxStages) & ~1;
@@ -66,7 +67,12 @@ struct Cfg {
   static constexpr int kOffP = kOffConv + kConv;
   static constexpr int kOffQ = kOffP + kPBuf * kP;
   static constexpr int kOffMisc = kOffQ + kQ;
-  static constexpr int kBytes = kOffMisc + 8192;
+  static constexpr int kBytes = kOffMisc + kMisc;
+  // Scales of a tile's keys. A slot is written again once the K stage of the
+  // tile kStages / 2 before it is free: that tile's S^T is done, so every
+  // softmax warp has read the scores of the tile three before, and has
+  // finished the one before that.
+  static constexpr int kScaleSlots = FP8 ? kStages / 2 + kSBuf + 1 : 0;
   static constexpr uint32_t kTmemCols = N * 4;                  // three S buffers and O
   static_assert(kStages >= 4 && kBytes <= 232448, "shared memory");
 };
@@ -221,7 +227,8 @@ __device__ __forceinline__ void stage_queries(const PagedArgs &a, const Walk &w,
       *reinterpret_cast<uint4 *>(sq + (n / 8) * (kChunks * 128) + c * 128 + (n % 8) * 16) = u;
     } else {
       // scaled by a power of two into (224, 448], then hi = rn(x), lo = rn(x - hi)
-      uint32_t m = row_top_bits(u);
+      const uint32_t m2 = max_mag(u, 0);
+      uint32_t m = max(m2 & 0xffffu, m2 >> 16);
 #pragma unroll
       for (int o = kChunks / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       const int byte = scale_byte(m);
@@ -231,7 +238,6 @@ __device__ __forceinline__ void stage_queries(const PagedArgs &a, const Walk &w,
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        // an infinity times the factor minus itself is NaN: it reaches every score of the row
         const float p = x[2 * e] * f, q = x[2 * e + 1] * f;
         const uint16_t hh = f32_to_e4m3x2(p, q);
         const float2 b = e4m3x2_to_f32(hh);
@@ -241,7 +247,7 @@ __device__ __forceinline__ void stage_queries(const PagedArgs &a, const Walk &w,
       uint8_t *d = sq + (n / 8) * (DH / 16 * 128) + (c / 2) * 128 + (n % 8) * 16 + (c & 1) * 8;
       *reinterpret_cast<uint2 *>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
       *reinterpret_cast<uint2 *>(d + N * DH) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-      if (c == 0) info.scale[n] = __uint_as_float(static_cast<uint32_t>(byte) << 23);
+      if (c == 0) info.scale[n] = scale_of(m < 0x7f80u ? byte : 255);   // a row with an infinity or NaN scores NaN
     }
     if (c == 0) {
       int lo = 0, hi = 0x7fffffff;   // a column that is no row masks nothing; its results go nowhere
@@ -266,7 +272,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   float *m_s = reinterpret_cast<float *>(info + 2);                       // [N] reference maxima
   float *corr_s = m_s + N;                                                // [N]
   float *red_s = corr_s + N;                                              // [4][N]
-  uint64_t *bars = reinterpret_cast<uint64_t *>(red_s + 4 * N);
+  uint8_t *scales = reinterpret_cast<uint8_t *>(red_s + 4 * N);           // [kScaleSlots][K, V][kTile]
+  uint32_t *pages_of = reinterpret_cast<uint32_t *>(scales + C::kScaleSlots * 2 * kTile);   // [kScaleSlots]: pages the tile has
+  uint64_t *bars = reinterpret_cast<uint64_t *>(pages_of + ((C::kScaleSlots + 1) & ~1));
   uint64_t *full = bars;                    // [kSt] stage loaded
   uint64_t *empty = full + kSt;             // [kSt] stage read by its MMAs (or converted)
   uint64_t *s_full = empty + kSt;           // [kSBuf]
@@ -274,14 +282,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   uint64_t *p_full = s_free + kSBuf;        // [kPBuf]
   uint64_t *p_free = p_full + kPBuf;        // [kPBuf] O^T MMAs of the tile done
   uint64_t *c_full = p_free + kPBuf;        // [kCBuf] V tile converted
-  uint64_t *q_full = c_full + kCBuf;
+  uint64_t *sc_full = c_full + kCBuf;       // [kScaleSlots]
+  uint64_t *q_full = sc_full + C::kScaleSlots;
   uint64_t *o_full = q_full + 1;
   uint64_t *o_free = o_full + 1;
   long long *s_scan = reinterpret_cast<long long *>(o_free + 1);          // [32]
   Start *start = reinterpret_cast<Start *>(s_scan + 32);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert(2 * sizeof(RowInfo<N>) + 6 * N * 4 + (2 * kSt + 2 * kSBuf + 2 * kPBuf + kCBuf + 3) * 8 + 256 + 64 <= 8192 - 1024,
+  static_assert(2 * sizeof(RowInfo<N>) + 6 * N * 4 + (2 * kSt + 2 * kSBuf + 2 * kPBuf + kCBuf + 3) * 8 + 256 + 64 +
+                        C::kScaleSlots * (2 * kTile + 8 + 4) + 4 <= C::kMisc - 1024,
                 "row tables and barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -295,6 +305,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     for (int b = 0; b < kSBuf; ++b) { mbar_init(&s_full[b], 1); mbar_init(&s_free[b], kSoftWarps); }
     for (int b = 0; b < kPBuf; ++b) { mbar_init(&p_full[b], kSoftWarps); mbar_init(&p_free[b], 1); }
     for (int b = 0; b < kCBuf; ++b) mbar_init(&c_full[b], 4);
+    for (int b = 0; b < C::kScaleSlots; ++b) mbar_init(&sc_full[b], 1);
     mbar_init(q_full, kSoftWarps);
     mbar_init(o_full, 1);
     mbar_init(o_free, kSoftWarps);
@@ -356,6 +367,22 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           if (lane < per_tile)
             tma_load_4d(smem + st * C::kRaw + lane * page_rows * (C::kGroup8 / 8), kv ? &tm_v : &tm_k, &full[st], g);
           issued = pos + 1;
+          if constexpr (FP8) {
+            if (kv == 0) {   // the tile's scales, page_rows bytes of each page
+              const bool live = g < none;
+              const uint32_t slot = n % C::kScaleSlots, pages = __ballot_sync(0xffffffffu, live);
+              if (lane == 0) {
+                pages_of[slot] = pages;
+                mbar_arrive_expect_tx(&sc_full[slot], __popc(pages) * page_rows * 2);
+              }
+              __syncwarp();
+              if (live) {
+                uint8_t *dst = scales + slot * (2 * kTile) + lane * page_rows;
+                bulk_load(dst, a.c.k_scale + static_cast<size_t>(g) * 8, page_rows, &sc_full[slot]);
+                bulk_load(dst + kTile, a.c.v_scale + static_cast<size_t>(g) * 8, page_rows, &sc_full[slot]);
+              }
+            }
+          }
         }
         if (!ok) break;
         g = g_next;
@@ -364,6 +391,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (bad) atomicOr(a.status, DLLM_DEV_PAGE);
     // after an abort: the loads in flight land before the CTA's memory is given up
     if (!ok && lane < kSt && lane < issued) mbar_drain(&full[lane], ((issued - 1 - lane) / kSt) & 1);
+    if constexpr (FP8) {
+      const uint32_t tiles = (issued + 1) / 2;
+      if (!ok && lane < C::kScaleSlots && lane < tiles)
+        mbar_drain(&sc_full[lane], ((tiles - 1 - lane) / C::kScaleSlots) & 1);
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------- S^T MMAs
     if (lane == 0) {
@@ -458,12 +490,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const int sc = DH == 128 ? (c ^ (key & 7)) : (c ^ ((key >> 1) & 3));
             uint4 q = *reinterpret_cast<const uint4 *>(src + sc * 16);
             if (!seen) q = make_uint4(0, 0, 0, 0);   // 0 * NaN would not be 0
-            uint4 lo, hi;
-            e4m3x8_to_bf16(q.x, q.y, lo);
-            e4m3x8_to_bf16(q.z, q.w, hi);
+            const uint2 a0 = e4m3x4_to_bf16_0213(q.x), a1 = e4m3x4_to_bf16_0213(q.y);
+            const uint2 b0 = e4m3x4_to_bf16_0213(q.z), b1 = e4m3x4_to_bf16_0213(q.w);
             uint8_t *d = dst + (c / 4) * 1024;
-            *reinterpret_cast<uint4 *>(d + (((2 * c) & 7) ^ (key & 7)) * 16) = lo;
-            *reinterpret_cast<uint4 *>(d + (((2 * c + 1) & 7) ^ (key & 7)) * 16) = hi;
+            *reinterpret_cast<uint4 *>(d + (((2 * c) & 7) ^ (key & 7)) * 16) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+            *reinterpret_cast<uint4 *>(d + (((2 * c + 1) & 7) ^ (key & 7)) * 16) = make_uint4(b0.x, b0.y, b1.x, b1.y);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -500,31 +531,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       named_bar_sync(1 + wg, 128);          // the rows' info is written, the last piece's maxima are read
       if (tid < kCols) m_s[c0 + tid] = -INFINITY;
       named_bar_sync(1 + wg, 128);
-      const int32_t *pages = a.c.table + static_cast<size_t>(w.i) * a.c.max_pages;
-      // scales of this thread's key in tile j (1 where no row sees it)
-      auto scales_of = [&](int j, float &ks, float &vs) {
-        ks = vs = 1.f;
-        if constexpr (FP8) {
-          if (j >= w.j0 + nT) return;
-          const int u = w.t.tile(j) * kTile + key;
-          if (u >= w.t.hi || !(u >= w.t.lo || u < a.sinks)) return;
-          const int page = __ldg(pages + (u >> a.c.page_shift));
-          if (page < 0 || page >= a.c.num_pages) return;
-          const size_t row = (static_cast<size_t>(page) * a.c.heads + w.h << a.c.page_shift) + (u & ((1 << a.c.page_shift) - 1));
-          ks = __uint_as_float(static_cast<uint32_t>(__ldg(a.c.k_scale + row)) << 23);
-          vs = __uint_as_float(static_cast<uint32_t>(__ldg(a.c.v_scale + row)) << 23);
-        }
-      };
-      float ks, vs;
-      scales_of(w.j0, ks, vs);
       for (int j = 0; j < nT; ++j, ++n) {
         const uint32_t b = n % kSBuf, pb = n % kPBuf;
-        float ks_next, vs_next;
-        scales_of(w.j0 + j + 1, ks_next, vs_next);
         const int key0 = w.t.tile(w.j0 + j) * kTile, u = key0 + key;
         // every row of the tile sees every key of it?
         const bool all_seen = key0 + kTile <= w.t.hi_first && (key0 >= w.t.lo_last || key0 + kTile <= a.sinks);
-        const float c = a.scale_log2 * ks;
+        const bool seen = u < w.t.hi && (u >= w.t.lo || u < a.sinks);   // this key, by any row
+        float c = a.scale_log2, vs = 1.f;
+        if constexpr (FP8) {
+          const uint32_t slot = n % C::kScaleSlots;
+          mbar_wait(&sc_full[slot], (n / C::kScaleSlots) & 1, abort_flag);
+          // a key without a page is a row of zeros, one that no row sees may have any scale
+          if ((pages_of[slot] >> (key >> a.c.page_shift) & 1) && seen) {
+            const uint8_t *sc = scales + slot * (2 * kTile) + key;
+            c *= scale_of(sc[0]);
+            vs = scale_of(sc[kTile]);
+          }
+        }
         mbar_wait(&s_full[b], (n / kSBuf) & 1, abort_flag);
         tc_fence_after();
         uint32_t s[kCols];
@@ -588,7 +611,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           float q = ex2_approx(d[e + 1] - (mb == -INFINITY ? 0.f : mb));
           l[e] += p;
           l[e + 1] += q;
-          if constexpr (FP8) { p *= vs; q *= vs; }
+          if constexpr (FP8) { p *= vs; q *= vs; }   // NaN scales: a row that holds NaN
           pk[e / 2] = pack_bf16x2(p, q);
         }
         if (n >= kPBuf) mbar_wait(&p_free[pb], (n / kPBuf - 1) & 1, abort_flag);
@@ -598,7 +621,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           *reinterpret_cast<uint4 *>(sp + e * 2048) = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
         if constexpr (!FP8) {
           // rows of V that no query row sees may hold anything, and 0 * NaN is not 0
-          if (wg == 0 && !(u < w.t.hi && (u >= w.t.lo || u < a.sinks))) {
+          if (wg == 0 && !seen) {
             const uint32_t pos = 2 * n + 1, st = pos % kSt;
             mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
             uint8_t *sv = smem + st * C::kRaw + (key / 8) * C::kGroup8 + (key % 8) * 128;
@@ -611,8 +634,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[pb]);
-        ks = ks_next;
-        vs = vs_next;
       }
       // the next piece's queries are staged before this one's results are
       // written: its scores run meanwhile (every S^T of this piece is done)
@@ -650,7 +671,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (lane == 0) mbar_arrive(o_free);
       }
       // M = 64: rows 16 q .. 16 q + 15 lie in the first 16 lanes of quarter q
-      const int dc = DH == 128 ? key : quarter * 16 + lane;
+      // converted V rows hold every four elements in the order 0, 2, 1, 3
+      const int dm = DH == 128 ? key : quarter * 16 + lane;
+      const int dc = FP8 ? (dm & ~3) | ((dm & 1) << 1) | ((dm >> 1) & 1) : dm;
       const bool dlive = DH == 128 || lane < 16;
       if (done.whole()) {
 #pragma unroll

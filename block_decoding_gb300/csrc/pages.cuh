@@ -39,7 +39,8 @@ inline dllm_status check_pages(const dllm_kv_pages *p) {
 
 inline dllm_status check_page_pointers(const dllm_kv_pages *p) {
   if (!p->k || !p->v || !aligned16(p->k) || !aligned16(p->v)) return DLLM_ERR_INVALID_ARG;
-  if (p->type == DLLM_KV_E4M3 && (!p->k_scale || !p->v_scale)) return DLLM_ERR_INVALID_ARG;
+  if (p->type == DLLM_KV_E4M3 && (!p->k_scale || !p->v_scale || !aligned16(p->k_scale) || !aligned16(p->v_scale)))
+    return DLLM_ERR_INVALID_ARG;
   return DLLM_OK;
 }
 
@@ -76,37 +77,37 @@ __device__ __forceinline__ uint16_t f32_to_e4m3x2(float a, float b) {
   return p;
 }
 
-// Eight codes -> eight bf16, exactly.
-__device__ __forceinline__ void e4m3x8_to_bf16(uint32_t a, uint32_t b, uint4 &out) {
-  float x[8];
-  const uint32_t w[2] = {a, b};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 p = e4m3x2_to_f32(static_cast<uint16_t>(w[i])), q = e4m3x2_to_f32(static_cast<uint16_t>(w[i] >> 16));
-    x[4 * i] = p.x; x[4 * i + 1] = p.y; x[4 * i + 2] = q.x; x[4 * i + 3] = q.y;
-  }
-  out = pack8(x);
+// The scale that a byte stands for: 2^(byte - 127), and NaN for 255.
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float((byte << 23) | (byte == 255 ? 0x400000u : 0u)); }
+
+// Four codes (lowest byte first) -> four bf16 in the order 0, 2, 1, 3, exactly
+// (NaN codes, which no row holds, become +-480). A code's exponent and
+// mantissa bits are put where bf16 has its lowest exponent and highest
+// mantissa bits; the product with 2^120 makes up for the exponent bias and
+// turns subnormal codes into normal numbers. Nine integer and packed-half
+// operations: conversions through half and float cost twice the time.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16_0213(uint32_t w) {
+  uint32_t even = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
+  uint32_t odd = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(even) : "r"(0x7b807b80u));
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(odd) : "r"(0x7b807b80u));
+  return make_uint2(even, odd);
 }
 
 // Exponent byte of a row with the largest magnitude bits `a` (finite bf16):
 // the least e >= -117 with |x| <= 448 * 2^e, + 127. 448 = 1.75 * 2^8, and
-// |x| = (1 + m / 128) * 2^(a >> 7 - 127).
+// |x| = (1 + m / 128) * 2^((a >> 7) - 127).
 __device__ __forceinline__ int scale_byte(uint32_t a) {
   const int b = static_cast<int>(a >> 7) - 8 + ((a & 127) > 96 ? 1 : 0);
   return min(max(b, 10), 247);
 }
 
-// Largest finite magnitude bits among eight bf16.
-__device__ __forceinline__ uint32_t row_top_bits(const uint4 &u) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = w[i] & 0x7fffu, b = (w[i] >> 16) & 0x7fffu;
-    if (a < 0x7f80u) m = max(m, a);
-    if (b < 0x7f80u) m = max(m, b);
-  }
-  return m;
+// Largest magnitude bits among eight bf16 and the halves of m.
+__device__ __forceinline__ uint32_t max_mag(const uint4 &u, uint32_t m) {
+  m = __vmaxu2(m, u.x & 0x7fff7fffu);
+  m = __vmaxu2(m, u.y & 0x7fff7fffu);
+  m = __vmaxu2(m, u.z & 0x7fff7fffu);
+  return __vmaxu2(m, u.w & 0x7fff7fffu);
 }
 
 }  // namespace dllm

@@ -448,12 +448,13 @@ dllm_status dllm_moe_ffn(const dllm_bf16 *h, const dllm_bf16 *w_router,
  * ties to even. Scaling by a power of two is exact and costs a
  * floating-point code no precision, so a code is within half an e4m3 step
  * of its element (2^-4 relative; below 2^-6 * 2^e, 2^-10 * 2^e absolute).
- * An infinity or NaN is stored as NaN and does not enter the scale.
- * Magnitudes above 1.875 * 2^127 are stored as that value.
+ * Magnitudes above 1.875 * 2^127 are stored as that value. A row that holds
+ * an infinity or NaN has the byte 255: all of it stands for NaN. (No row has
+ * NaN codes; pages filled by other means must not have any either.)
  *
  *   Supported: dh in {64, 128}; page_size in {16, 32, 64, 128};
- *   1 <= heads <= 256; num_pages * heads * page_size < 2^31; k and v
- *   16-byte aligned.
+ *   1 <= heads <= 256; num_pages * heads * page_size < 2^31; k, v,
+ *   k_scale and v_scale 16-byte aligned.
  *   A page id outside [0, num_pages) and a position outside the table set
  *   DLLM_DEV_PAGE: such a row is not written, and reads as zeros.
  * ------------------------------------------------------------------- */

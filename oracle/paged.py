@@ -2,7 +2,8 @@
 
 A cached row of one head holds its elements as bf16 or, in 8 bits, as e4m3
 codes with one power-of-two scale: the row stands for code * 2^e with the
-least e >= -117 for which max|x| <= 448 * 2^e. Attention over the cache: a
+least e >= -117 for which max|x| <= 448 * 2^e; a row with an infinity or NaN
+stands for NaN. Attention over the cache: a
 query row at position p sees the cached positions u < kv_len with
 u <= p + right, and with u >= p - left or u < sinks.
 """
@@ -38,22 +39,25 @@ def nearest_code(x):
 
 
 def quantise(x):
-    """(codes uint8, scale bytes uint8) of rows x [..., dh] of bf16 values."""
+    """(codes uint8, scale bytes uint8) of rows x [..., dh] of bf16 values. A
+    row with an infinity or NaN has the byte 255 (its codes mean nothing: 0
+    here)."""
     x = np.asarray(x, np.float64)
-    fine = np.isfinite(x)
-    top = np.where(fine, np.abs(x), 0.0).max(axis=-1)
+    fine = np.isfinite(x).all(axis=-1)
+    x = np.where(fine[..., None], x, 0.0)
+    top = np.abs(x).max(axis=-1)
     e = np.full(top.shape, E_MIN)
     for k in range(E_MIN, 121):
         e = np.where(top > 448 * 2.0 ** e, k + 1, e)
-    y = np.where(fine, x, 0.0) / (2.0 ** e)[..., None]
     lim = np.where(e == 120, 240.0, 448.0)[..., None]     # a code may not stand for 2^128
-    codes = nearest_code(np.clip(y, -lim, lim))
-    return np.where(fine, codes, 0x7F).astype(np.uint8), (e + 127).astype(np.uint8)
+    codes = nearest_code(np.clip(x / (2.0 ** e)[..., None], -lim, lim))
+    return codes, np.where(fine, e + 127, 255).astype(np.uint8)
 
 
 def restore(codes, scale):
     """The values that codes [..., dh] with scale bytes [...] stand for."""
-    return E4M3[codes] * (2.0 ** (scale.astype(np.float64) - 127))[..., None]
+    f = np.where(scale == 255, np.nan, 2.0 ** (np.minimum(scale, 254).astype(np.float64) - 127))
+    return E4M3[codes] * f[..., None]
 
 
 def visible(pos, kv_len, left, right, sinks):

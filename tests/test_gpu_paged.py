@@ -172,9 +172,8 @@ def test_write_of_uncommon_values(dh):
     for pool, scale, rows in ((pages.k, pages.k_scale, x), (pages.v, pages.v_scale, x.flip(0))):
         codes, b = paged.quantise(f64(rows))
         got = pool.view(torch.uint8).cpu().numpy()[0, :, 2:11].swapaxes(0, 1)
-        nan = (codes & 0x7F) == 0x7F
         assert np.array_equal(scale.cpu().numpy()[0, :, 2:11].T, b)
-        assert np.array_equal(got[~nan], codes[~nan]) and ((got[nan] & 0x7F) == 0x7F).all()
+        assert np.array_equal(got[b < 255], codes[b < 255]) and (b == 255).sum() == 2
     k, _ = bd.kv_read(pages, i32([0, 9]), i32([2]), i32([[0]]), 9)
     codes, b = paged.quantise(f64(x))
     assert np.array_equal(f64(k), paged.restore(codes, b), equal_nan=True)
@@ -370,6 +369,28 @@ def test_out_of_bounds_metadata_is_clipped_and_reported():
     bd.paged_attn(b.q, b.pages, i32([8, 4, 2]), i32([100, 60]), b.table, 6, 100)
     torch.cuda.synchronize()
     assert bd.device_status() == DEV_OFFSETS | DEV_PAGE
+
+
+@pytest.mark.parametrize("w", [1, 20])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_that_hold_nan_reach_what_sees_them(w, fp8):
+    b = Batch(29, [700], 2, 64, 16, fp8)
+    b.queries([w], 2)
+    k, v = b.k_in.clone(), b.v_in.clone()
+    k[600, 0, 3] = float("nan")
+    v[300, 1, 5] = float("inf")
+    bd.kv_write(b.pages, k, v, b.off, i32([0]), b.table)
+    b.k[0][600] = b.v[0][300] = 0
+    p = np.arange(700 - w, 700)
+    for left in (-1, 250):
+        out, lse = b.run(left=left, right=0)
+        out = f64(out)
+        see = paged.visible(p, 700, left, 0, 0)
+        assert np.array_equal(np.isnan(out[:, :2]).any(-1).all(-1), see[:, 600])      # heads of cached head 0
+        assert np.array_equal(np.isnan(f64(lse)[:, 0]), see[:, 600])
+        assert np.array_equal(~np.isfinite(out[:, 2:]).all(-1).all(-1), see[:, 300])
+        if not fp8:
+            assert np.array_equal(np.isposinf(out[:, 2, 5]), see[:, 300])
 
 
 @pytest.mark.parametrize("w", [1, 32, 300])

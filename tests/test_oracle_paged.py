@@ -34,7 +34,7 @@ def test_scale_is_the_least_that_fits():
     assert paged.restore(codes, b)[0, 0] == 448 and paged.restore(codes, b)[2, 0] == 1.75
     x = np.array([[np.inf, 1.0, np.nan, -2.0]])
     codes, b = paged.quantise(x)
-    assert np.isnan(paged.restore(codes, b)[0, [0, 2]]).all() and paged.restore(codes, b)[0, 3] == -2.0
+    assert b[0] == 255 and np.isnan(paged.restore(codes, b)).all()
     top = float(torch.finfo(torch.bfloat16).max)
     codes, b = paged.quantise(np.array([[top, -top, 0.0, 1.0]]))
     assert paged.restore(codes, b)[0, :2].tolist() == [1.875 * 2.0 ** 127, -1.875 * 2.0 ** 127]
