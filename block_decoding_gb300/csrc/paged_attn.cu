@@ -198,6 +198,14 @@ __device__ __forceinline__ float reduce_columns(float (&v)[CNT], int lane, Op op
   return r;
 }
 
+// Scores of a key at position u in the columns whose rows do not see it.
+template <int CNT>
+__device__ __forceinline__ void mask_columns(float (&x)[CNT], const int *lo, const int *hi, int u, int sinks) {
+#pragma unroll
+  for (int e = 0; e < CNT; ++e)
+    if (!(u < hi[e] && (u >= lo[e] || u < sinks))) x[e] = -INFINITY;
+}
+
 template <int CNT>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[CNT]) {
   if constexpr (CNT == 32) tmem_ld32(addr, r); else tmem_ld16(addr, r);
@@ -484,17 +492,22 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           const bool seen = u < w.t.hi && (u >= w.t.lo || u < a.sinks);
           const uint8_t *src = smem + st * C::kRaw + key * DH;
           uint8_t *dst = smem + C::kOffConv + cb * (kTile * DH * 2) + (key / 8) * C::kVGroup8 + (key % 8) * 128;
+          if (seen) {
 #pragma unroll
-          for (int c = 0; c < DH / 16; ++c) {
-            // chunk c of the row under the load's swizzle (rows of 128 or 64 bytes)
-            const int sc = DH == 128 ? (c ^ (key & 7)) : (c ^ ((key >> 1) & 3));
-            uint4 q = *reinterpret_cast<const uint4 *>(src + sc * 16);
-            if (!seen) q = make_uint4(0, 0, 0, 0);   // 0 * NaN would not be 0
-            const uint2 a0 = e4m3x4_to_bf16_0213(q.x), a1 = e4m3x4_to_bf16_0213(q.y);
-            const uint2 b0 = e4m3x4_to_bf16_0213(q.z), b1 = e4m3x4_to_bf16_0213(q.w);
-            uint8_t *d = dst + (c / 4) * 1024;
-            *reinterpret_cast<uint4 *>(d + (((2 * c) & 7) ^ (key & 7)) * 16) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-            *reinterpret_cast<uint4 *>(d + (((2 * c + 1) & 7) ^ (key & 7)) * 16) = make_uint4(b0.x, b0.y, b1.x, b1.y);
+            for (int c = 0; c < DH / 16; ++c) {
+              // chunk c of the row under the load's swizzle (rows of 128 or 64 bytes)
+              const int sc = DH == 128 ? (c ^ (key & 7)) : (c ^ ((key >> 1) & 3));
+              const uint4 q = *reinterpret_cast<const uint4 *>(src + sc * 16);
+              const uint2 a0 = e4m3x4_to_bf16_0213(q.x), a1 = e4m3x4_to_bf16_0213(q.y);
+              const uint2 b0 = e4m3x4_to_bf16_0213(q.z), b1 = e4m3x4_to_bf16_0213(q.w);
+              uint8_t *d = dst + (c / 4) * 1024;
+              *reinterpret_cast<uint4 *>(d + (((2 * c) & 7) ^ (key & 7)) * 16) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+              *reinterpret_cast<uint4 *>(d + (((2 * c + 1) & 7) ^ (key & 7)) * 16) = make_uint4(b0.x, b0.y, b1.x, b1.y);
+            }
+          } else {   // whatever lies there: 0 * NaN would not be 0
+#pragma unroll
+            for (int c = 0; c < DH / 8; ++c)
+              *reinterpret_cast<uint4 *>(dst + (c / 8) * 1024 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -511,6 +524,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int key = quarter * 32 + lane, c0 = wg * kCols;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     constexpr float kLazy = 8.f;
+    constexpr float kNone = -3.0e38f;   // reference of a row that has seen no key: finite, so that x is not NaN
     const auto maxop = [](float p, float q) { return fmaxf(p, q); };
     const auto addop = [](float p, float q) { return p + q; };
     uint32_t n = 0, seg = 0, o_seg = 0;
@@ -529,7 +543,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
       for (int e = 0; e < kCols; ++e) l[e] = 0.f;
       named_bar_sync(1 + wg, 128);          // the rows' info is written, the last piece's maxima are read
-      if (tid < kCols) m_s[c0 + tid] = -INFINITY;
+      if (tid < kCols) m_s[c0 + tid] = kNone;
       named_bar_sync(1 + wg, 128);
       for (int j = 0; j < nT; ++j, ++n) {
         const uint32_t b = n % kSBuf, pb = n % kPBuf;
@@ -557,26 +571,40 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[b]);
-        // scores in log2 units
-        float d[kCols];
+        // x = score - reference in log2 units, two columns at a time; nobody
+        // past the reference by more than 2^8 is the common case
+        float x[kCols];
+        auto score2 = [&](int e) {
+          float2 f = make_float2(c, c);
+          if constexpr (FP8) f = __fmul2_rn(f, *reinterpret_cast<const float2 *>(&ri.scale[c0 + e]));
+          return f;
+        };
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) {
-          d[e] = __uint_as_float(s[e]) * (FP8 ? c * ri.scale[c0 + e] : c);
-          if (!all_seen) {
-            const int lo = ri.lo[c0 + e], hi = ri.hi[c0 + e];
-            if (!(u < hi && (u >= lo || u < a.sinks))) d[e] = -INFINITY;
-          }
+        for (int e = 0; e < kCols; e += 2) {
+          const float2 m2 = *reinterpret_cast<const float2 *>(&m_s[c0 + e]);
+          const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), score2(e),
+                                      make_float2(-m2.x, -m2.y));
+          x[e] = y.x;
+          x[e + 1] = y.y;
         }
-        bool pass = false;
+        if (!all_seen) mask_columns<kCols>(x, ri.lo + c0, ri.hi + c0, u, a.sinks);
+        float top = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) pass |= d[e] > m_s[c0 + e] + kLazy;
-        // anyone's score past the reference: new maxima for the columns
-        if (bar_any(1 + wg, 128, pass)) {
+        for (int e = 0; e < kCols; e += 2) top = fmaxf(top, fmaxf(x[e], x[e + 1]));
+        if (bar_any(1 + wg, 128, top > kLazy)) {
+          // new references: the columns' maxima over the tile
           float v[kCols];
 #pragma unroll
-          for (int e = 0; e < kCols; ++e) v[e] = d[e];
-          const float top = reduce_columns<kCols>(v, lane, maxop);
-          if (lane < kCols) red_s[quarter * N + c0 + lane] = top;
+          for (int e = 0; e < kCols; e += 2) {
+            const float2 y = __fmul2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), score2(e));
+            v[e] = y.x;
+            v[e + 1] = y.y;
+          }
+          if (!all_seen) mask_columns<kCols>(v, ri.lo + c0, ri.hi + c0, u, a.sinks);
+#pragma unroll
+          for (int e = 0; e < kCols; ++e) x[e] = v[e];
+          const float most = reduce_columns<kCols>(v, lane, maxop);
+          if (lane < kCols) red_s[quarter * N + c0 + lane] = most;
           named_bar_sync(1 + wg, 128);
           if (tid < kCols) {
             const int e = c0 + tid;
@@ -587,7 +615,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           }
           named_bar_sync(1 + wg, 128);
 #pragma unroll
-          for (int e = 0; e < kCols; ++e) l[e] *= corr_s[c0 + e];
+          for (int e = 0; e < kCols; ++e) {
+            l[e] *= corr_s[c0 + e];
+            x[e] -= m_s[c0 + e];
+          }
           if (j > 0) {
             // O holds exactly the tiles before this one once the last one's MMAs are done
             mbar_wait(&p_free[(n - 1) % kPBuf], ((n - 1) / kPBuf) & 1, abort_flag);
@@ -602,17 +633,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             tc_fence_before();
           }
         }
-        // P = 2^(score - reference), its column sums per key, and P * v scale as bf16
+        // P = 2^x, its column sums per key, and P * v scale as bf16
         uint32_t pk[kCols / 2];
 #pragma unroll
         for (int e = 0; e < kCols; e += 2) {
-          const float ma = m_s[c0 + e], mb = m_s[c0 + e + 1];
-          float p = ex2_approx(d[e] - (ma == -INFINITY ? 0.f : ma));
-          float q = ex2_approx(d[e + 1] - (mb == -INFINITY ? 0.f : mb));
-          l[e] += p;
-          l[e + 1] += q;
-          if constexpr (FP8) { p *= vs; q *= vs; }   // NaN scales: a row that holds NaN
-          pk[e / 2] = pack_bf16x2(p, q);
+          float2 p = make_float2(ex2_approx(x[e]), ex2_approx(x[e + 1]));
+          const float2 sum = __fadd2_rn(make_float2(l[e], l[e + 1]), p);
+          l[e] = sum.x;
+          l[e + 1] = sum.y;
+          if constexpr (FP8) p = __fmul2_rn(p, make_float2(vs, vs));
+          pk[e / 2] = pack_bf16x2(p.x, p.y);
         }
         if (n >= kPBuf) mbar_wait(&p_free[pb], (n / kPBuf - 1) & 1, abort_flag);
         uint8_t *sp = smem + C::kOffP + pb * C::kP + (c0 / 8) * 2048 + (key / 8) * 128 + (key % 8) * 16;
@@ -746,12 +776,12 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
     if (t >= x.W) break;
     const int row = (x.q0 + t) * a.Hq + h * a.group + (r - t * a.group);
     if (tid < 32) {
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f;   // a piece without keys: m = -3e38, l = 0
       for (int p = tid; p < parts; p += 32) m = fmaxf(m, a.part_ml[slot_of(p) * n_rows + n].x);
       m = warp_max(m);
       for (int p = tid; p < parts; p += 32) {
         const float2 ml = a.part_ml[slot_of(p) * n_rows + n];
-        const float wgt = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+        const float wgt = ex2_approx(ml.x - m);
         weight[p] = wgt;
         l += wgt * ml.y;
       }
