@@ -18,11 +18,10 @@
 //
 // Warp roles:
 //   warp 0      TMA: one box per page and tile; K and V tiles alternate in one ring
-//   warp 1      S^T MMAs: K tile (A) x query rows (B) into S buffer n mod 3
+//   warp 1      S^T MMAs: K tile (A) x query rows (B) into an S buffer
 //   warp 2      O^T MMAs: V tile (A, transposed by its descriptor) x P (B)
-//   warps 4..   softmax warpgroups of 128 threads, one key each; a group
-//               takes up to 32 columns (query rows)
-//   last four   (e4m3 pages) V codes -> bf16 tiles
+//   warps 4..11 two softmax warpgroups, one key per thread
+//   last four   (e4m3 pages) V codes -> bf16, 64 keys at a time
 // A reference maximum per row moves only when a score passes it by more than
 // 2^8 (P is bf16: no precision is lost), so most tiles need no maximum at
 // all, only the vote that nobody passed it.
@@ -41,23 +40,32 @@ DLLM_DEFINE_STATUS(paged)
 
 namespace {
 
-constexpr int kSBuf = 3, kPBuf = 2, kCBuf = 2;
+constexpr int kPBuf = 2, kCBuf = 2;
+constexpr int kConvKeys = 64;    // keys of one converted V piece
 constexpr int kMinTiles = 2;     // fewest tiles a CTA is given: each piece costs a prologue and a join
 constexpr int kMaxCtas = 192;    // bound of the workspace, above any GB300's SM count
 
 template <int DH, bool FP8, int N>
 struct Cfg {
-  static constexpr int kGroups = N > 32 ? N / 32 : 1;           // softmax warpgroups
-  static constexpr int kCols = N / kGroups;                     // columns of one group: 16 or 32
-  static constexpr int kConvWarps = FP8 ? 4 : 0;
-  static constexpr int kThreads = 32 * (4 + 4 * kGroups + kConvWarps);
-  static constexpr int kConvWarp0 = 4 + 4 * kGroups;
+  // Two softmax warpgroups. With up to 32 columns they take every other key
+  // tile (each with its own references, sums and O, merged at the end): the
+  // steps of one tile depend on each other, and two tiles under way hide
+  // that. With 64 columns each takes 32 of them, of every tile.
+  static constexpr bool kByTile = N <= 32;
+  static constexpr int kCols = kByTile ? N : N / 2;             // columns of one group
+  static constexpr int kSBuf = kByTile ? 4 : 3;
+  static constexpr int kConvWarp0 = 12;
+  static constexpr int kThreads = 32 * (kConvWarp0 + (FP8 ? 4 : 0));
+  // registers a thread: what the TMA and MMA warps and the converters do not
+  // need goes to the softmax groups (the sum is the launch's)
+  static constexpr int kRegsIssue = FP8 ? 64 : 72, kRegsSoft = FP8 ? 176 : 216, kRegsConv = 96;
+  static_assert(FP8 ? kRegsIssue + 2 * kRegsSoft + kRegsConv <= 4 * 128 : kRegsIssue + 2 * kRegsSoft <= 3 * 168, "registers");
   static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);       // one K or V tile as it is cached
   static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);        // eight cached rows
   static constexpr int kVGroup8 = 8 * DH * 2;                   // eight bf16 rows of V
   static constexpr int kP = kTile * N * 2;
   static constexpr int kQ = N * DH * 2;                         // bf16, or two e4m3 parts
-  static constexpr int kConv = FP8 ? kCBuf * kTile * DH * 2 : 0;
+  static constexpr int kConv = FP8 ? kCBuf * kConvKeys * DH * 2 : 0;
   static constexpr int kMisc = FP8 ? 12288 : 8192;              // row tables, scales, barriers, alignment
   static constexpr int kFixed = kConv + kPBuf * kP + kQ + kMisc;
   static constexpr int kMaxStages = (232448 - kFixed) / kRaw;
@@ -69,11 +77,10 @@ struct Cfg {
   static constexpr int kOffMisc = kOffQ + kQ;
   static constexpr int kBytes = kOffMisc + kMisc;
   // Scales of a tile's keys. A slot is written again once the K stage of the
-  // tile kStages / 2 before it is free: that tile's S^T is done, so every
-  // softmax warp has read the scores of the tile three before, and has
-  // finished the one before that.
+  // tile kStages / 2 before it is free: that tile's S^T is done, so the
+  // scores and scales of every tile up to kSBuf before that one are read.
   static constexpr int kScaleSlots = FP8 ? kStages / 2 + kSBuf + 1 : 0;
-  static constexpr uint32_t kTmemCols = N * 4;                  // three S buffers and O
+  static constexpr uint32_t kTmemCols = N * (kByTile ? 8 : 4);  // S buffers and O (kSBuf + 1 or 2, a power of two)
   static_assert(kStages >= 4 && kBytes <= 232448, "shared memory");
 };
 
@@ -208,7 +215,9 @@ __device__ __forceinline__ void mask_columns(float (&x)[CNT], const int *lo, con
 
 template <int CNT>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[CNT]) {
-  if constexpr (CNT == 32) tmem_ld32(addr, r); else tmem_ld16(addr, r);
+  if constexpr (CNT == 32) tmem_ld32(addr, r);
+  else if constexpr (CNT == 16) tmem_ld16(addr, r);
+  else tmem_ld8(addr, r);
 }
 template <int CNT>
 __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[CNT]) {
@@ -222,10 +231,12 @@ template <int DH, bool FP8, int N, int COLS>
 __device__ __forceinline__ void stage_queries(const PagedArgs &a, const Walk &w, uint8_t *sq, RowInfo<N> &info, int c0, int tid) {
   const int rows = w.x.W * a.group;
   constexpr int kChunks = DH / 8;                  // 16-byte chunks of a bf16 row
-  constexpr int kRounds = COLS * kChunks / 128;
+  constexpr int kPieces = COLS * kChunks;
 #pragma unroll
-  for (int it = 0; it < kRounds; ++it) {
-    const int idx = it * 128 + tid, n = c0 + idx / kChunks, c = idx % kChunks;
+  for (int it = 0; it < (kPieces + 127) / 128; ++it) {
+    const int idx = it * 128 + tid;
+    if (kPieces % 128 && idx >= kPieces) break;    // whole warps
+    const int n = c0 + idx / kChunks, c = idx % kChunks;
     const int r = w.rt * N + n, t = r / a.group, g = r - t * a.group;
     const bool live = r < rows;
     uint4 u = make_uint4(0, 0, 0, 0);
@@ -272,15 +283,16 @@ __global__ void __launch_bounds__(Cfg<DH, FP8, N>::kThreads, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a,
                   const int min_tiles) {
   using C = Cfg<DH, FP8, N>;
-  constexpr int kSt = C::kStages, kCols = C::kCols;
+  constexpr int kSt = C::kStages, kCols = C::kCols, kSBuf = C::kSBuf;
+  constexpr bool kByTile = C::kByTile;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *misc = smem + C::kOffMisc;
   RowInfo<N> *info = reinterpret_cast<RowInfo<N> *>(misc);                // [2]: this piece's and the next one's
-  float *m_s = reinterpret_cast<float *>(info + 2);                       // [N] reference maxima
-  float *corr_s = m_s + N;                                                // [N]
-  float *red_s = corr_s + N;                                              // [4][N]
-  uint8_t *scales = reinterpret_cast<uint8_t *>(red_s + 4 * N);           // [kScaleSlots][K, V][kTile]
+  float *m_s = reinterpret_cast<float *>(info + 2);                       // [group][kCols] reference maxima
+  float *corr_s = m_s + 2 * kCols;                                        // [group][kCols]
+  float *red_s = corr_s + 2 * kCols;                                      // [quarter][group][kCols]
+  uint8_t *scales = reinterpret_cast<uint8_t *>(red_s + 8 * kCols);           // [kScaleSlots][K, V][kTile]
   uint32_t *pages_of = reinterpret_cast<uint32_t *>(scales + C::kScaleSlots * 2 * kTile);   // [kScaleSlots]: pages the tile has
   uint64_t *bars = reinterpret_cast<uint64_t *>(pages_of + ((C::kScaleSlots + 1) & ~1));
   uint64_t *full = bars;                    // [kSt] stage loaded
@@ -289,8 +301,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   uint64_t *s_free = s_full + kSBuf;        // [kSBuf]
   uint64_t *p_full = s_free + kSBuf;        // [kPBuf]
   uint64_t *p_free = p_full + kPBuf;        // [kPBuf] O^T MMAs of the tile done
-  uint64_t *c_full = p_free + kPBuf;        // [kCBuf] V tile converted
-  uint64_t *sc_full = c_full + kCBuf;       // [kScaleSlots]
+  uint64_t *c_full = p_free + kPBuf;        // [kCBuf] V piece converted
+  uint64_t *c_free = c_full + kCBuf;        // [kCBuf] its O^T MMAs done
+  uint64_t *sc_full = c_free + kCBuf;       // [kScaleSlots]
   uint64_t *q_full = sc_full + C::kScaleSlots;
   uint64_t *o_full = q_full + 1;
   uint64_t *o_free = o_full + 1;
@@ -298,25 +311,25 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   Start *start = reinterpret_cast<Start *>(s_scan + 32);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert(2 * sizeof(RowInfo<N>) + 6 * N * 4 + (2 * kSt + 2 * kSBuf + 2 * kPBuf + kCBuf + 3) * 8 + 256 + 64 +
+  static_assert(2 * sizeof(RowInfo<N>) + 12 * kCols * 4 + (2 * kSt + 2 * kSBuf + 2 * kPBuf + 2 * kCBuf + 3) * 8 + 256 + 64 +
                         C::kScaleSlots * (2 * kTile + 8 + 4) + 4 <= C::kMisc - 1024,
                 "row tables and barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   if (threadIdx.x == 0) {
-    constexpr int kSoftWarps = 4 * C::kGroups;
+    constexpr int kTileWarps = C::kByTile ? 4 : 8;   // softmax warps of one tile
     for (int s = 0; s < kSt; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], FP8 && (s & 1) ? 4 : 1);
     }
-    for (int b = 0; b < kSBuf; ++b) { mbar_init(&s_full[b], 1); mbar_init(&s_free[b], kSoftWarps); }
-    for (int b = 0; b < kPBuf; ++b) { mbar_init(&p_full[b], kSoftWarps); mbar_init(&p_free[b], 1); }
-    for (int b = 0; b < kCBuf; ++b) mbar_init(&c_full[b], 4);
+    for (int b = 0; b < kSBuf; ++b) { mbar_init(&s_full[b], 1); mbar_init(&s_free[b], kTileWarps); }
+    for (int b = 0; b < kPBuf; ++b) { mbar_init(&p_full[b], kTileWarps); mbar_init(&p_free[b], 1); }
+    for (int b = 0; b < kCBuf; ++b) { mbar_init(&c_full[b], 4); mbar_init(&c_free[b], 1); }
     for (int b = 0; b < C::kScaleSlots; ++b) mbar_init(&sc_full[b], 1);
-    mbar_init(q_full, kSoftWarps);
+    mbar_init(q_full, 8);
     mbar_init(o_full, 1);
-    mbar_init(o_free, kSoftWarps);
+    mbar_init(o_free, 8);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm_k);
@@ -343,6 +356,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     w.j = static_cast<int>(start->residual - static_cast<long long>(w.item) * w.n);
   }
 
+  if (warp < 4) {
+  reg_dealloc<C::kRegsIssue>();
   if (warp == 0) {
     // ------------------------------------------------------------- producer
     const int per_tile = kTile >> a.c.page_shift;
@@ -406,21 +421,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- S^T MMAs
-    if (lane == 0) {
-      uint32_t n = 0, seg = 0;
-      bool ok = true;
-      const uint32_t sq = smem_u32(smem + C::kOffQ);
-      while (ok && w.next()) {
-        const int nT = w.tiles();
-        if (nT == 0) continue;
-        ok = mbar_wait(q_full, seg++ & 1, abort_flag);
-        for (int j = 0; ok && j < nT; ++j, ++n) {
-          const uint32_t pos = 2 * n, st = pos % kSt, b = n % kSBuf;
-          ok = mbar_wait(&full[st], (pos / kSt) & 1, abort_flag) &&
-               (n < kSBuf || mbar_wait(&s_free[b], (n / kSBuf - 1) & 1, abort_flag));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sk = smem_u32(smem + st * C::kRaw);
+    uint32_t n = 0, seg = 0;
+    bool ok = true;
+    const uint32_t sq = smem_u32(smem + C::kOffQ);
+    while (ok && w.next()) {
+      const int nT = w.tiles();
+      if (nT == 0) continue;
+      ok = warp_wait(q_full, seg++ & 1, abort_flag);
+      for (int j = 0; ok && j < nT; ++j, ++n) {
+        const uint32_t pos = 2 * n, st = pos % kSt, b = n % kSBuf;
+        ok = warp_wait(&full[st], (pos / kSt) & 1, abort_flag);
+        if (ok && n >= kSBuf) ok = warp_wait(&s_free[b], (n / kSBuf - 1) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sk = smem_u32(smem + st * C::kRaw);
+        if (elect_one()) {
           if constexpr (!FP8) {
             const uint64_t dk = sw128_desc(sk, 16, C::kGroup8), dq = plain_desc(sq, 128, DH / 8 * 128);
 #pragma unroll
@@ -440,88 +455,106 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           umma_commit(&s_full[b]);
           umma_commit(&empty[st]);
         }
+        __syncwarp();
       }
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------- O^T MMAs
-    if (lane == 0) {
-      uint32_t n = 0, seg = 0;
-      bool ok = true;
-      while (ok && w.next()) {
-        const int nT = w.tiles();
-        if (nT == 0) continue;
-        for (int j = 0; ok && j < nT; ++j, ++n) {
-          const uint32_t pos = 2 * n + 1, st = pos % kSt, b = n % kPBuf;
-          ok = mbar_wait(&p_full[b], (n / kPBuf) & 1, abort_flag);
-          if (ok && j == 0 && seg > 0) ok = mbar_wait(o_free, (seg - 1) & 1, abort_flag);
-          uint32_t sv;
-          if constexpr (FP8) {
-            ok = ok && mbar_wait(&c_full[n % kCBuf], (n / kCBuf) & 1, abort_flag);
-            sv = smem_u32(smem + C::kOffConv + (n % kCBuf) * (kTile * DH * 2));
-          } else {
-            ok = ok && mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
-            sv = smem_u32(smem + st * C::kRaw);
-          }
+    uint32_t n = 0, seg = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      const int nT = w.tiles();
+      if (nT == 0) continue;
+      for (int j = 0; ok && j < nT; ++j, ++n) {
+        const uint32_t pos = 2 * n + 1, st = pos % kSt, b = n % kPBuf;
+        ok = warp_wait(&p_full[b], (n / kPBuf) & 1, abort_flag);
+        if (ok && j == 0 && seg > 0) ok = warp_wait(o_free, (seg - 1) & 1, abort_flag);
+        if (ok && !FP8) ok = warp_wait(&full[st], (pos / kSt) & 1, abort_flag);
+        const uint32_t t_d = kByTile ? t_o + (n & 1) * N : t_o;
+        const bool first = j == 0 || (kByTile && j == 1);   // of its accumulator
+        const uint64_t dp = plain_desc(smem_u32(smem + C::kOffP + b * C::kP), 128, 2048);
+        // bf16: the tile as one piece; e4m3: its converted pieces
+        constexpr int kPieces = FP8 ? kTile / kConvKeys : 1, kSteps = 8 / kPieces;
+#pragma unroll
+        for (int piece = 0; piece < kPieces; ++piece) {
+          const uint32_t cn = n * kPieces + piece, cb = cn % kCBuf;
+          if (FP8 && ok) ok = warp_wait(&c_full[cb], (cn / kCBuf) & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t dv = sw128_desc(sv, 1024, C::kVGroup8);
-          const uint64_t dp = plain_desc(smem_u32(smem + C::kOffP + b * C::kP), 128, 2048);
+          const uint32_t sv = smem_u32(FP8 ? smem + C::kOffConv + cb * (kConvKeys * DH * 2) : smem + st * C::kRaw);
+          if (elect_one()) {
+            const uint64_t dv = sw128_desc(sv, 1024, C::kVGroup8);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_bf16(t_o, dv + ((kk * 2 * C::kVGroup8) >> 4), dp + ((kk * 256) >> 4), idesc_bf16(DH, N, 1, 1),
-                      j > 0 || kk > 0);
-          umma_commit(&p_free[b]);
-          if constexpr (!FP8) umma_commit(&empty[st]);
-          if (j + 1 == nT) umma_commit(o_full);
+            for (int kk = 0; kk < kSteps; ++kk)
+              umma_bf16(t_d, dv + ((kk * 2 * C::kVGroup8) >> 4), dp + (((piece * kSteps + kk) * 256) >> 4),
+                        idesc_bf16(DH, N, 1, 1), !first || piece + kk > 0);
+            umma_commit(FP8 ? &c_free[cb] : &empty[st]);
+            if (piece + 1 == kPieces) {
+              umma_commit(&p_free[b]);
+              if (j + 1 == nT) umma_commit(o_full);
+            }
+          }
+          __syncwarp();
         }
-        ++seg;
       }
+      ++seg;
     }
+  }
   } else if (FP8 && warp >= C::kConvWarp0) {
     // ------------------------------------------------------------- V codes -> bf16
     if constexpr (FP8) {
-      const int key = (warp - C::kConvWarp0) * 32 + lane;
+      reg_dealloc<C::kRegsConv>();
+      // a thread takes half of a key's row
+      constexpr int kChunks = DH / 32;   // 16-byte pieces of codes
+      const int t = (warp - C::kConvWarp0) * 32 + lane, k64 = t % kConvKeys, ch = t / kConvKeys * kChunks;
       uint32_t n = 0;
       while (w.next()) {
         const int nT = w.tiles();
         for (int j = 0; j < nT; ++j, ++n) {
-          const uint32_t pos = 2 * n + 1, st = pos % kSt, cb = n % kCBuf;
+          const uint32_t pos = 2 * n + 1, st = pos % kSt;
           mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
-          if (n >= kCBuf) mbar_wait(&p_free[n % kPBuf], (n / kPBuf - 1) & 1, abort_flag);
-          const int u = w.t.tile(w.j0 + j) * kTile + key;
-          const bool seen = u < w.t.hi && (u >= w.t.lo || u < a.sinks);
-          const uint8_t *src = smem + st * C::kRaw + key * DH;
-          uint8_t *dst = smem + C::kOffConv + cb * (kTile * DH * 2) + (key / 8) * C::kVGroup8 + (key % 8) * 128;
-          if (seen) {
+#pragma unroll 1
+          for (int half = 0; half < kTile / kConvKeys; ++half) {
+            const uint32_t cn = n * (kTile / kConvKeys) + half, cb = cn % kCBuf;
+            const int key = half * kConvKeys + k64, u = w.t.tile(w.j0 + j) * kTile + key;
+            const bool seen = u < w.t.hi && (u >= w.t.lo || u < a.sinks);
+            const uint8_t *src = smem + st * C::kRaw + key * DH;
+            uint8_t *dst = smem + C::kOffConv + cb * (kConvKeys * DH * 2) + (k64 / 8) * C::kVGroup8 + (k64 % 8) * 128;
+            uint4 q[kChunks];
 #pragma unroll
-            for (int c = 0; c < DH / 16; ++c) {
-              // chunk c of the row under the load's swizzle (rows of 128 or 64 bytes)
-              const int sc = DH == 128 ? (c ^ (key & 7)) : (c ^ ((key >> 1) & 3));
-              const uint4 q = *reinterpret_cast<const uint4 *>(src + sc * 16);
-              const uint2 a0 = e4m3x4_to_bf16_0213(q.x), a1 = e4m3x4_to_bf16_0213(q.y);
-              const uint2 b0 = e4m3x4_to_bf16_0213(q.z), b1 = e4m3x4_to_bf16_0213(q.w);
-              uint8_t *d = dst + (c / 4) * 1024;
-              *reinterpret_cast<uint4 *>(d + (((2 * c) & 7) ^ (key & 7)) * 16) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-              *reinterpret_cast<uint4 *>(d + (((2 * c + 1) & 7) ^ (key & 7)) * 16) = make_uint4(b0.x, b0.y, b1.x, b1.y);
+            for (int c = 0; c < kChunks; ++c)   // under the load's swizzle (rows of 128 or 64 bytes)
+              q[c] = *reinterpret_cast<const uint4 *>(src + (DH == 128 ? (ch + c) ^ (key & 7) : (ch + c) ^ ((key >> 1) & 3)) * 16);
+            if (cn >= kCBuf) mbar_wait(&c_free[cb], (cn / kCBuf - 1) & 1, abort_flag);
+            if (!seen) {   // whatever lies there: 0 * NaN would not be 0
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c) q[c] = make_uint4(0, 0, 0, 0);
             }
-          } else {   // whatever lies there: 0 * NaN would not be 0
 #pragma unroll
-            for (int c = 0; c < DH / 8; ++c)
-              *reinterpret_cast<uint4 *>(dst + (c / 8) * 1024 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < kChunks; ++c) {
+              const uint2 a0 = e4m3x4_to_bf16_0213(q[c].x), a1 = e4m3x4_to_bf16_0213(q[c].y);
+              const uint2 b0 = e4m3x4_to_bf16_0213(q[c].z), b1 = e4m3x4_to_bf16_0213(q[c].w);
+              const int o = 2 * (ch + c);       // bf16 pieces o and o + 1 of the row, eight to a 128-byte column piece
+              uint8_t *d = dst + (o / 8) * 1024;
+              *reinterpret_cast<uint4 *>(d + ((o & 7) ^ (key & 7)) * 16) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+              *reinterpret_cast<uint4 *>(d + (((o + 1) & 7) ^ (key & 7)) * 16) = make_uint4(b0.x, b0.y, b1.x, b1.y);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c_full[cb]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&c_full[cb]);
-            mbar_arrive(&empty[st]);
-          }
+          if (lane == 0) mbar_arrive(&empty[st]);
         }
       }
     }
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------- softmax
+    reg_alloc<C::kRegsSoft>();
     const int wg = (warp - 4) >> 2, quarter = warp & 3, tid = threadIdx.x & 127;
-    const int key = quarter * 32 + lane, c0 = wg * kCols;
+    const int key = quarter * 32 + lane;
+    const int c0 = kByTile ? 0 : wg * kCols;   // first column of the group's tiles
+    const int g0 = wg * kCols;                 // its part of the groups' arrays
+    constexpr int kOut = N / 2;                // rows that a group stages and writes
+    const int out0 = wg * kOut;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     constexpr float kLazy = 8.f;
     constexpr float kNone = -3.0e38f;   // reference of a row that has seen no key: finite, so that x is not NaN
@@ -531,7 +564,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     bool more = w.next();
     bool joined = false;       // this CTA's last piece began an item that others finish
     if (more) {
-      stage_queries<DH, FP8, N, kCols>(a, w, smem + C::kOffQ, info[0], c0, tid);
+      stage_queries<DH, FP8, N, kOut>(a, w, smem + C::kOffQ, info[0], out0, tid);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && w.tiles() > 0) mbar_arrive(q_full);
@@ -542,10 +575,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       float l[kCols];
 #pragma unroll
       for (int e = 0; e < kCols; ++e) l[e] = 0.f;
-      named_bar_sync(1 + wg, 128);          // the rows' info is written, the last piece's maxima are read
-      if (tid < kCols) m_s[c0 + tid] = kNone;
+      named_bar_sync(3, 256);               // the rows' info is written, the last piece's maxima are read
+      if (tid < kCols) m_s[g0 + tid] = kNone;
       named_bar_sync(1 + wg, 128);
+      bool first = true;                    // of the group's tiles
       for (int j = 0; j < nT; ++j, ++n) {
+        if (kByTile && (n & 1) != wg) continue;
         const uint32_t b = n % kSBuf, pb = n % kPBuf;
         const int key0 = w.t.tile(w.j0 + j) * kTile, u = key0 + key;
         // every row of the tile sees every key of it?
@@ -581,7 +616,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         };
 #pragma unroll
         for (int e = 0; e < kCols; e += 2) {
-          const float2 m2 = *reinterpret_cast<const float2 *>(&m_s[c0 + e]);
+          const float2 m2 = *reinterpret_cast<const float2 *>(&m_s[g0 + e]);
           const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), score2(e),
                                       make_float2(-m2.x, -m2.y));
           x[e] = y.x;
@@ -604,11 +639,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
           for (int e = 0; e < kCols; ++e) x[e] = v[e];
           const float most = reduce_columns<kCols>(v, lane, maxop);
-          if (lane < kCols) red_s[quarter * N + c0 + lane] = most;
+          if (lane < kCols) red_s[quarter * (2 * kCols) + g0 + lane] = most;
           named_bar_sync(1 + wg, 128);
           if (tid < kCols) {
-            const int e = c0 + tid;
-            const float mx = fmaxf(fmaxf(red_s[e], red_s[N + e]), fmaxf(red_s[2 * N + e], red_s[3 * N + e]));
+            const int e = g0 + tid;
+            const float mx = fmaxf(fmaxf(red_s[e], red_s[2 * kCols + e]), fmaxf(red_s[4 * kCols + e], red_s[6 * kCols + e]));
             const float old = m_s[e], now = mx > old + kLazy ? mx : old;
             corr_s[e] = now == old ? 1.f : ex2_approx(old - now);
             m_s[e] = now;
@@ -616,19 +651,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           named_bar_sync(1 + wg, 128);
 #pragma unroll
           for (int e = 0; e < kCols; ++e) {
-            l[e] *= corr_s[c0 + e];
-            x[e] -= m_s[c0 + e];
+            l[e] *= corr_s[g0 + e];
+            x[e] -= m_s[g0 + e];
           }
-          if (j > 0) {
-            // O holds exactly the tiles before this one once the last one's MMAs are done
-            mbar_wait(&p_free[(n - 1) % kPBuf], ((n - 1) / kPBuf) & 1, abort_flag);
+          if (!first) {
+            // O holds exactly the group's tiles before this one once the MMAs of the last are done
+            const uint32_t last = n - (kByTile ? 2 : 1), t_d = t_o + lane_base + (kByTile ? wg * N : c0);
+            mbar_wait(&p_free[last % kPBuf], (last / kPBuf) & 1, abort_flag);
             tc_fence_after();
             uint32_t o[kCols];
-            tmem_load<kCols>(t_o + lane_base + c0, o);
+            tmem_load<kCols>(t_d, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr_s[c0 + e]);
-            tmem_store<kCols>(t_o + lane_base + c0, o);
+            for (int e = 0; e < kCols; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr_s[g0 + e]);
+            tmem_store<kCols>(t_d, o);
             tmem_st_wait();
             tc_fence_before();
           }
@@ -651,7 +687,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           *reinterpret_cast<uint4 *>(sp + e * 2048) = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
         if constexpr (!FP8) {
           // rows of V that no query row sees may hold anything, and 0 * NaN is not 0
-          if (wg == 0 && !seen) {
+          if ((kByTile || wg == 0) && !seen) {
             const uint32_t pos = 2 * n + 1, st = pos % kSt;
             mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
             uint8_t *sv = smem + st * C::kRaw + (key / 8) * C::kGroup8 + (key % 8) * 128;
@@ -664,42 +700,71 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[pb]);
+        first = false;
       }
       // the next piece's queries are staged before this one's results are
-      // written: its scores run meanwhile (every S^T of this piece is done)
+      // written, so that its scores run meanwhile: once every S^T of this
+      // piece is done, the last of which may be the other group's
+      if (kByTile && nT > 0 && ((n - 1) & 1) != wg) mbar_wait(&s_full[(n - 1) % kSBuf], ((n - 1) / kSBuf) & 1, abort_flag);
       const Walk done = w;
       more = w.next();
       ++seg;
       if (more) {
-        stage_queries<DH, FP8, N, kCols>(a, w, smem + C::kOffQ, info[seg & 1], c0, tid);
+        stage_queries<DH, FP8, N, kOut>(a, w, smem + C::kOffQ, info[seg & 1], out0, tid);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && w.tiles() > 0) mbar_arrive(q_full);
       }
       const float part = reduce_columns<kCols>(l, lane, addop);
-      if (lane < kCols) red_s[quarter * N + c0 + lane] = part;
+      if (lane < kCols) red_s[quarter * (2 * kCols) + g0 + lane] = part;
       named_bar_sync(1 + wg, 128);
       if (tid < kCols) {
-        const int e = c0 + tid;
-        const float sum = (red_s[e] + red_s[N + e]) + (red_s[2 * N + e] + red_s[3 * N + e]);
-        corr_s[e] = sum;
+        const int e = g0 + tid;
+        corr_s[e] = (red_s[e] + red_s[2 * kCols + e]) + (red_s[4 * kCols + e] + red_s[6 * kCols + e]);
       }
       if (nT > 0) {
         mbar_wait(o_full, o_seg & 1, abort_flag);
         ++o_seg;
         tc_fence_after();
       }
-      named_bar_sync(1 + wg, 128);
-      uint32_t o[kCols];
+      named_bar_sync(3, 256);
+      // rows [out0, out0 + kOut): maximum, sum, and what the groups' O count for
+      uint32_t o[kOut];
+      if constexpr (kByTile) {
+        uint32_t o1[kOut];
+        // a single tile leaves the other group without an O
+        const bool has0 = nT > 1 || (nT == 1 && ((n - 1) & 1) == 0), has1 = nT > 1 || (nT == 1 && ((n - 1) & 1) == 1);
+        if (nT > 0) {
+          tmem_load<kOut>(t_o + lane_base + out0, o);
+          tmem_load<kOut>(t_o + lane_base + N + out0, o1);
+          tmem_ld_wait();
+        }
 #pragma unroll
-      for (int e = 0; e < kCols; ++e) o[e] = 0;
+        for (int e = 0; e < kOut; ++e) {
+          const float m0 = m_s[out0 + e], m1 = m_s[kCols + out0 + e], m = fmaxf(m0, m1);
+          const float y0 = has0 ? __uint_as_float(o[e]) * ex2_approx(m0 - m) : 0.f;
+          const float y1 = has1 ? __uint_as_float(o1[e]) * ex2_approx(m1 - m) : 0.f;
+          o[e] = __float_as_uint(y0 + y1);
+        }
+      } else {
+        if (nT > 0) {
+          tmem_load<kOut>(t_o + lane_base + out0, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < kOut; ++e) o[e] = 0;
+        }
+      }
       if (nT > 0) {
-        tmem_load<kCols>(t_o + lane_base + c0, o);
-        tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free);
       }
+      auto merged = [&](int e) {   // {maximum, sum} of row e
+        if constexpr (!kByTile) return make_float2(m_s[e], corr_s[e]);
+        const float m = fmaxf(m_s[e], m_s[kCols + e]);
+        return make_float2(m, corr_s[e] * ex2_approx(m_s[e] - m) + corr_s[kCols + e] * ex2_approx(m_s[kCols + e] - m));
+      };
       // M = 64: rows 16 q .. 16 q + 15 lie in the first 16 lanes of quarter q
       // converted V rows hold every four elements in the order 0, 2, 1, 3
       const int dm = DH == 128 ? key : quarter * 16 + lane;
@@ -707,28 +772,28 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const bool dlive = DH == 128 || lane < 16;
       if (done.whole()) {
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) {
-          const int row = ri.out[c0 + e];
+        for (int e = 0; e < kOut; ++e) {
+          const int row = ri.out[out0 + e];
           if (row < 0) break;
-          const float sum = corr_s[c0 + e];
+          const float sum = merged(out0 + e).y;
           const float y = sum != 0.f ? __uint_as_float(o[e]) / sum : 0.f;
           if (dlive) {
             if (a.out_fp32) static_cast<float *>(a.out)[static_cast<size_t>(row) * DH + dc] = y;
             else static_cast<uint16_t *>(a.out)[static_cast<size_t>(row) * DH + dc] = f32_to_bf16(y);
           }
         }
-        if (a.lse && tid < kCols && ri.out[c0 + tid] >= 0) {
-          const float sum = corr_s[c0 + tid];
-          a.lse[ri.out[c0 + tid]] = sum != 0.f ? (m_s[c0 + tid] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        if (a.lse && tid < kOut && ri.out[out0 + tid] >= 0) {
+          const float2 ml = merged(out0 + tid);
+          a.lse[ri.out[out0 + tid]] = ml.y != 0.f ? (ml.x + log2f(ml.y)) * 0.69314718055994531f : -INFINITY;
         }
       } else {
         // the first piece of a CTA goes to its first slot, a later one (its last) to the second
         const size_t slot = static_cast<size_t>(blockIdx.x) * 2 + (seg > 1 ? 1 : 0);
-        float *po = a.part_o + (slot * N + c0) * DH + dc;
+        float *po = a.part_o + (slot * N + out0) * DH + dc;
         if (dlive)
 #pragma unroll
-          for (int e = 0; e < kCols; ++e) po[e * DH] = __uint_as_float(o[e]);
-        if (tid < kCols) a.part_ml[slot * N + c0 + tid] = make_float2(m_s[c0 + tid], corr_s[c0 + tid]);
+          for (int e = 0; e < kOut; ++e) po[e * DH] = __uint_as_float(o[e]);
+        if (tid < kOut) a.part_ml[slot * N + out0 + tid] = merged(out0 + tid);
         if (done.j0 == 0) {
           joined = true;
           if (tid == 0 && wg == 0) {
