@@ -23,7 +23,13 @@ struct PagedArgs {
   // partial results of items whose keys several CTAs share
   float *part_o;
   float2 *part_ml;
-  int4 *join;
+  struct JoinJob *join;
+};
+
+// An item that several CTAs shared: its first piece, the number of pieces,
+// its first flat row, the request's flat rows, first query row and the head.
+struct JoinJob {
+  int slot, parts, r0, rows, q0, h, pad0, pad1;
 };
 
 // Request i clipped to the buffers and host bounds: query rows [q0, q0 + W),
@@ -49,10 +55,11 @@ __device__ __forceinline__ Extent paged_extent(const PagedArgs &a, int i, bool r
   return x;
 }
 
-// Keys [lo, hi) that a row at position p sees apart from the sinks.
-__device__ __forceinline__ void visible(const PagedArgs &a, long long p, int L, int &lo, int &hi) {
-  hi = a.right < 0 ? L : static_cast<int>(min(static_cast<long long>(L), max(p + a.right + 1, 0ll)));
-  lo = a.left < 0 ? 0 : static_cast<int>(min(max(p - a.left, 0ll), 1ll << 30));
+// Keys [lo, hi) that a row at position p (|p| < 2^31) sees apart from the
+// sinks. Sums that pass 2^31 are clamped: right and left are below 2^30.
+__device__ __forceinline__ void visible(const PagedArgs &a, int p, int L, int &lo, int &hi) {
+  hi = a.right < 0 ? L : min(L, max(min(p, (1 << 30) - 1) + a.right + 1, 0));
+  lo = a.left < 0 ? 0 : max(max(p, -(1 << 30)) - a.left, 0);
 }
 
 constexpr int kTile = 128;   // keys per tile
@@ -70,8 +77,7 @@ struct TileList {
 // Flat rows r = t * group + g of one cached head, tiles of `n` of them.
 __device__ __forceinline__ TileList tile_list(const PagedArgs &a, const Extent &x, int rt, int n) {
   TileList t;
-  const long long t0 = (static_cast<long long>(rt) * n) / a.group;
-  const long long t1 = min((static_cast<long long>(rt + 1) * n - 1) / a.group, static_cast<long long>(x.W) - 1);
+  const int t0 = rt * n / a.group, t1 = min(((rt + 1) * n - 1) / a.group, x.W - 1);   // W * group <= 2^30
   visible(a, x.pos + t0, x.L, t.lo, t.hi_first);
   visible(a, x.pos + t1, x.L, t.lo_last, t.hi);
   const int s = min(a.sinks, t.hi);
@@ -94,15 +100,239 @@ __device__ __forceinline__ TileList tile_list(const PagedArgs &a, const Extent &
 __device__ __forceinline__ int tiles_per_item(const PagedArgs &a, const Extent &x, int n) {
   if (a.uniform) return a.uniform;
   int lo, hi;
-  visible(a, static_cast<long long>(x.pos) + x.W - 1, x.L, lo, hi);
+  visible(a, x.pos + x.W - 1, x.L, lo, hi);
   int most = (hi + kTile - 1) / kTile;
   if (a.left >= 0 && a.right >= 0) {
     // window keys of one row tile: left + right + 1 of a row, and the rows' spread
-    const long long keys = static_cast<long long>(a.left) + a.right + 1 + (n - 1) / a.group + 1;
-    const long long win = (keys - 1) / kTile + 2 + (min(a.sinks, hi) + kTile - 1) / kTile;
-    most = static_cast<int>(min(static_cast<long long>(most), win));
+    const unsigned keys = static_cast<unsigned>(a.left) + a.right + 1 + (n - 1) / a.group + 1;
+    const unsigned win = (keys - 1) / kTile + 2 + (min(a.sinks, hi) + kTile - 1) / kTile;
+    most = static_cast<int>(min(static_cast<unsigned>(most), win));
   }
   return max(most, 1);
 }
+
+// Where this CTA starts: the total of all items' tiles, cut into gridDim.x
+// equal pieces (whole items with `uniform`).
+struct Start {
+  long long residual;   // tiles of request i before this CTA's first
+  long long left;       // tiles of this CTA
+  long long per;        // tiles of every CTA
+  int i;
+};
+
+__device__ __forceinline__ long long request_tiles(const PagedArgs &a, int i, int n_rows, bool report) {
+  const Extent x = paged_extent(a, i, report);
+  const long long items = static_cast<long long>((x.W * a.group + n_rows - 1) / n_rows) * a.c.heads;
+  return items ? items * tiles_per_item(a, x, n_rows) : 0;
+}
+
+// Every thread of the CTA takes part; s_scan holds 32 values.
+__device__ __forceinline__ void find_start(const PagedArgs &a, int n_rows, int min_tiles, long long *s_scan,
+                                           Start *s_start) {
+  const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int chunk = (a.B + nt - 1) / nt;
+  const int i0 = tid * chunk, i1 = min(a.B, i0 + chunk);
+  long long mine = 0;
+  for (int i = i0; i < i1; ++i) mine += request_tiles(a, i, n_rows, blockIdx.x == 0);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  if (tid == 0) s_start->left = 0;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < nt / 32; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(min_tiles));
+  if (a.uniform) per = (per + a.uniform - 1) / a.uniform * a.uniform;
+  const long long begin = per * blockIdx.x;
+  const long long excl = before + incl - mine;
+  if (begin >= excl && begin < excl + mine) {
+    long long at = excl;
+    for (int i = i0; i < i1; ++i) {
+      const long long m = request_tiles(a, i, n_rows, false);
+      if (begin < at + m) {
+        s_start->i = i;
+        s_start->residual = begin - at;
+        s_start->left = min(per, total - begin);
+        s_start->per = per;
+        break;
+      }
+      at += m;
+    }
+  }
+  __syncthreads();
+}
+
+// The pieces of work of one CTA, walked by the warps that prepare them.
+struct Walk {
+  const PagedArgs &a;
+  int n_rows;
+  int i, item, j;          // request, item of the request, tile of the item
+  long long left;          // tiles of this CTA still to come
+  Extent x;
+  int n, items, row_tiles;
+  // the current piece
+  int h, rt, j0, j1;       // head, row tile, tiles [j0, j1) of it
+  TileList t;
+  __device__ __forceinline__ Walk(const PagedArgs &args, int rows, const Start &s) : a(args), n_rows(rows), left(s.left) {
+    if (left <= 0) return;
+    i = s.i;
+    load();
+    item = static_cast<int>(s.residual / n);
+    j = static_cast<int>(s.residual - static_cast<long long>(item) * n);
+  }
+  __device__ __forceinline__ void load() {
+    x = paged_extent(a, i, false);
+    row_tiles = (x.W * a.group + n_rows - 1) / n_rows;
+    items = row_tiles * a.c.heads;
+    n = items ? tiles_per_item(a, x, n_rows) : 0;
+  }
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    while (item >= items) {
+      if (++i >= a.B) return false;
+      item = 0;
+      load();
+    }
+    h = item / row_tiles;
+    rt = item - h * row_tiles;
+    j0 = j;
+    j1 = static_cast<int>(min(static_cast<long long>(n), j + left));
+    left -= j1 - j0;
+    if (j1 == n) { j = 0; ++item; } else { j = j1; }
+    t = tile_list(a, x, rt, n_rows);
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == n; }
+  __device__ __forceinline__ int tiles() const { return max(min(j1, t.count) - j0, 0); }   // that hold visible keys
+};
+
+// What is to join for the item that the CTA's piece `w` begins (its partial
+// results in `slot`): the item's other pieces are the first slots of the next
+// CTAs. Returns whether the item is divided there.
+__device__ __forceinline__ bool begin_join(const PagedArgs &a, const Walk &w, const Start &s, int slot) {
+  if (w.j0 != 0 || w.whole()) return false;
+  const int parts = 1 + static_cast<int>((w.n - w.j1 + s.per - 1) / s.per);
+  a.join[blockIdx.x] = JoinJob{slot, parts, w.rt * w.n_rows, w.x.W * a.group, w.x.q0, w.h, 0, 0};
+  return true;
+}
+
+// The warp that loads the K and V tiles of a CTA's pieces into one ring of
+// SLOTS stages, K tiles in the even ones: one box per page and tile. With
+// e4m3 pages (SCALES > 0) a tile's scale bytes, K's then V's, go to a ring of
+// SCALES slots with the truth of which pages the tile has.
+template <int DH, int ELEM, int SLOTS, int SCALES>
+__device__ __forceinline__ void load_tiles(const PagedArgs &a, const Start &start, int n_rows, const CUtensorMap *tm_k,
+                                           const CUtensorMap *tm_v, uint8_t *ring, uint64_t *full, uint64_t *empty,
+                                           uint8_t *scales, uint32_t *pages_of, uint64_t *sc_full, volatile int *abort,
+                                           int lane) {
+  constexpr int kRow = DH * ELEM, kRaw = kTile * kRow;
+  const int per_tile = kTile >> a.c.page_shift, page_rows = 1 << a.c.page_shift;
+  const int none = static_cast<int>((static_cast<long long>(a.c.num_pages) * a.c.heads << a.c.page_shift) / 8);
+  Walk w(a, n_rows, start);
+  bool bad = false, ok = true;
+  uint32_t n = 0, issued = 0;
+  while (ok && w.next()) {
+    const int nT = w.tiles();
+    const int32_t *row = a.c.table + static_cast<size_t>(w.i) * a.c.max_pages;
+    // 8-row group of this lane's page of tile j; pages without cached rows read as zeros
+    auto group_of = [&](int j) {
+      if (lane >= per_tile || j >= w.j0 + nT) return none;
+      const int u = w.t.tile(j) * kTile + lane * page_rows;
+      if (u >= w.x.L) return none;
+      const int page = __ldg(row + (u >> a.c.page_shift));
+      if (page < 0 || page >= a.c.num_pages) { bad = true; return none; }
+      return ((page * a.c.heads + w.h) << a.c.page_shift) / 8;
+    };
+    int g = group_of(w.j0);
+    for (int j = w.j0; ok && j < w.j0 + nT; ++j, ++n) {
+      const int g_next = group_of(j + 1);     // its latency passes behind this tile's waits
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t pos = 2 * n + kv, st = pos % SLOTS, round = pos / SLOTS;
+        if (round > 0) ok = warp_wait(&empty[st], (round - 1) & 1, abort);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], kRaw);
+        __syncwarp();
+        if (lane < per_tile) tma_load_4d(ring + st * kRaw + lane * page_rows * kRow, kv ? tm_v : tm_k, &full[st], g);
+        issued = pos + 1;
+        if constexpr (SCALES > 0) {
+          if (kv == 0) {
+            const bool live = g < none;
+            const uint32_t slot = n % SCALES, pages = __ballot_sync(0xffffffffu, live);
+            if (lane == 0) {
+              pages_of[slot] = pages;
+              mbar_arrive_expect_tx(&sc_full[slot], __popc(pages) * page_rows * 2);
+            }
+            __syncwarp();
+            if (live) {
+              uint8_t *dst = scales + slot * (2 * kTile) + lane * page_rows;
+              bulk_load(dst, a.c.k_scale + static_cast<size_t>(g) * 8, page_rows, &sc_full[slot]);
+              bulk_load(dst + kTile, a.c.v_scale + static_cast<size_t>(g) * 8, page_rows, &sc_full[slot]);
+            }
+          }
+        }
+      }
+      g = g_next;
+    }
+  }
+  if (bad) atomicOr(a.status, DLLM_DEV_PAGE);
+  // after an abort: the loads in flight land before the CTA's memory is given up
+  if (!ok && lane < SLOTS && lane < issued) mbar_drain(&full[lane], ((issued - 1 - lane) / SLOTS) & 1);
+  if constexpr (SCALES > 0) {
+    const uint32_t tiles = (issued + 1) / 2;
+    if (!ok && lane < SCALES && lane < tiles) mbar_drain(&sc_full[lane], ((tiles - 1 - lane) / SCALES) & 1);
+  }
+}
+
+// 64 keys of a V tile of e4m3 codes (rows of DH bytes as the load lays them
+// out, the first of them key 64 * piece of the tile) to bf16 rows in the
+// layout of a bf16 tile, every four elements in the order 0, 2, 1, 3, by 128
+// threads (t): half a row each, of key 64 * piece + t % 64. `ready` waits
+// until dst may be written; factor(key) is the rows' scale, or 1.
+template <int DH, typename Ready, typename Extra>
+__device__ __forceinline__ void convert_v(const uint8_t *raw, uint8_t *dst, int piece, int t, bool seen, Ready ready,
+                                          Extra extra) {
+  constexpr int kChunks = DH / 32;   // 16-byte pieces of codes
+  const int k64 = t % 64, ch = t / 64 * kChunks, key = piece * 64 + k64;
+  const uint8_t *src = raw + key * DH;
+  uint8_t *out = dst + (k64 / 8) * (8 * DH * 2) + (k64 % 8) * 128;
+  uint4 q[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c)   // under the load's swizzle (rows of 128 or 64 bytes)
+    q[c] = *reinterpret_cast<const uint4 *>(src + (DH == 128 ? (ch + c) ^ (key & 7) : (ch + c) ^ ((key >> 1) & 3)) * 16);
+  ready();
+  if (!seen) {   // whatever lies there: 0 * NaN would not be 0
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) q[c] = make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const uint2 a0 = extra(e4m3x4_to_bf16_0213(q[c].x)), a1 = extra(e4m3x4_to_bf16_0213(q[c].y));
+    const uint2 b0 = extra(e4m3x4_to_bf16_0213(q[c].z)), b1 = extra(e4m3x4_to_bf16_0213(q[c].w));
+    const int o = 2 * (ch + c);       // bf16 pieces o and o + 1 of the row, eight to a 128-byte column piece
+    uint8_t *d = out + (o / 8) * 1024;
+    *reinterpret_cast<uint4 *>(d + ((o & 7) ^ (key & 7)) * 16) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+    *reinterpret_cast<uint4 *>(d + (((o + 1) & 7) ^ (key & 7)) * 16) = make_uint4(b0.x, b0.y, b1.x, b1.y);
+  }
+}
+
+constexpr int kMinTiles = 2;     // fewest tiles a CTA is given: each piece costs a prologue and a join
+constexpr int kMaxCtas = 192;    // bound of the workspace, above any GB300's SM count
+constexpr int kConvKeys = 64;    // keys of one converted V piece
+constexpr float kLazy = 8.f;     // a reference maximum moves when a score passes it by more than 2^8
+constexpr float kNone = -3.0e38f;   // reference of a row that has seen no key: finite, so that differences are not NaN
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Launches the kernel for many rows per cached head (paged_rows.cu) with row
+// tiles of n_rows = 128 or 256 on `ctas` CTAs.
+dllm_status launch_paged_rows(int dh, bool fp8, int n_rows, const CUtensorMap &tk, const CUtensorMap &tv,
+                              const PagedArgs &a, int min_tiles, int ctas, cudaStream_t s);
 
 }  // namespace dllm

@@ -32,6 +32,8 @@
 // factor of its thread's scores. V codes become bf16, which holds them
 // exactly, and the scale enters P before its one rounding to bf16, so tail
 // weights keep their relative precision however small they are.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace dllm {
@@ -41,9 +43,6 @@ DLLM_DEFINE_STATUS(paged)
 namespace {
 
 constexpr int kPBuf = 2, kCBuf = 2;
-constexpr int kConvKeys = 64;    // keys of one converted V piece
-constexpr int kMinTiles = 2;     // fewest tiles a CTA is given: each piece costs a prologue and a join
-constexpr int kMaxCtas = 192;    // bound of the workspace, above any GB300's SM count
 
 template <int DH, bool FP8, int N>
 struct Cfg {
@@ -67,14 +66,14 @@ struct Cfg {
   static constexpr int kQ = N * DH * 2;                         // bf16, or two e4m3 parts
   static constexpr int kConv = FP8 ? kCBuf * kConvKeys * DH * 2 : 0;
   static constexpr int kMisc = FP8 ? 12288 : 8192;              // row tables, scales, barriers, alignment
-  static constexpr int kFixed = kConv + kPBuf * kP + kQ + kMisc;
+  static constexpr int kFixed = kConv + kPBuf * kP + 2 * kQ + kMisc;
   static constexpr int kMaxStages = (232448 - kFixed) / kRaw;
   // even, so that K tiles have the even stages; 192 KB in flight are enough
   static constexpr int kStages = (kMaxStages * kRaw > 196608 ? 196608 / kRaw : kMaxStages) & ~1;
   static constexpr int kOffConv = kStages * kRaw;
   static constexpr int kOffP = kOffConv + kConv;
   static constexpr int kOffQ = kOffP + kPBuf * kP;
-  static constexpr int kOffMisc = kOffQ + kQ;
+  static constexpr int kOffMisc = kOffQ + 2 * kQ;               // this piece's query rows and the next one's
   static constexpr int kBytes = kOffMisc + kMisc;
   // Scales of a tile's keys. A slot is written again once the K stage of the
   // tile kStages / 2 before it is free: that tile's S^T is done, so the
@@ -92,99 +91,16 @@ struct RowInfo {
   float scale[N];     // e4m3 parts: what the query row was divided by
 };
 
-// The pieces of work of one CTA, walked alike by every warp.
-struct Walk {
-  const PagedArgs &a;
-  int n_rows;
-  int i, item, j;          // request, item of the request, tile of the item
-  long long left;          // tiles of this CTA still to come
-  Extent x;
-  int n, items, row_tiles;
-  // the current piece
-  int h, rt, j0, j1;       // head, row tile, tiles [j0, j1) of it
+// A piece of an item as the warps that work on it need it.
+template <int N>
+struct alignas(16) Piece {
+  RowInfo<N> rows;
   TileList t;
-  __device__ __forceinline__ Walk(const PagedArgs &args, int rows) : a(args), n_rows(rows) {}
-  __device__ __forceinline__ void load() {
-    x = paged_extent(a, i, false);
-    row_tiles = (x.W * a.group + n_rows - 1) / n_rows;
-    items = row_tiles * a.c.heads;
-    n = items ? tiles_per_item(a, x, n_rows) : 0;
-  }
-  __device__ __forceinline__ bool next() {
-    if (left <= 0) return false;
-    while (item >= items) {
-      if (++i >= a.B) return false;
-      item = 0;
-      load();
-    }
-    h = item / row_tiles;
-    rt = item - h * row_tiles;
-    j0 = j;
-    j1 = static_cast<int>(min(static_cast<long long>(n), j + left));
-    left -= j1 - j0;
-    if (j1 == n) { j = 0; ++item; } else { j = j1; }
-    t = tile_list(a, x, rt, n_rows);
-    return true;
-  }
-  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == n; }
-  __device__ __forceinline__ int tiles() const { return max(min(j1, t.count) - j0, 0); }   // that hold visible keys
+  int j0, tiles;           // first tile of the piece, tiles of it that hold visible keys
+  int more;                // 0: there is no such piece, the CTA is done
+  int whole;               // the whole item: its results are final
+  int slot;                // else where its partial results go
 };
-
-// Where this CTA starts: the total of all items' tiles, cut into gridDim.x
-// pieces. Every thread of the CTA takes part; s_scan holds 32 values.
-struct Start {
-  long long residual;   // tiles of request i before this CTA's first
-  long long left;       // tiles of this CTA
-  long long per;        // tiles of every CTA
-  int i;
-};
-
-__device__ __forceinline__ long long request_tiles(const PagedArgs &a, int i, int n_rows, bool report) {
-  const Extent x = paged_extent(a, i, report);
-  const long long items = static_cast<long long>((static_cast<long long>(x.W) * a.group + n_rows - 1) / n_rows) * a.c.heads;
-  return items ? items * tiles_per_item(a, x, n_rows) : 0;
-}
-
-__device__ void find_start(const PagedArgs &a, int n_rows, int min_tiles, long long *s_scan, Start *s_start) {
-  const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int chunk = (a.B + nt - 1) / nt;
-  const int i0 = tid * chunk, i1 = min(a.B, i0 + chunk);
-  long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += request_tiles(a, i, n_rows, blockIdx.x == 0);
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  if (tid == 0) s_start->left = 0;
-  __syncthreads();
-  long long before = 0, total = 0;
-  for (int w = 0; w < nt / 32; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
-  }
-  long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(min_tiles));
-  if (a.uniform) per = (per + a.uniform - 1) / a.uniform * a.uniform;
-  const long long begin = per * blockIdx.x;
-  const long long excl = before + incl - mine;
-  if (begin >= excl && begin < excl + mine) {
-    long long at = excl;
-    for (int i = i0; i < i1; ++i) {
-      const long long m = request_tiles(a, i, n_rows, false);
-      if (begin < at + m) {
-        s_start->i = i;
-        s_start->residual = begin - at;
-        s_start->left = min(per, total - begin);
-        s_start->per = per;
-        break;
-      }
-      at += m;
-    }
-  }
-  __syncthreads();
-}
 
 // v[k] of every lane reduced over the warp's lanes, for CNT values: lane c
 // (mod CNT) ends with the result of value c. CNT - 1 shuffles (+ 1 for 16).
@@ -224,56 +140,43 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[CN
   if constexpr (CNT == 32) tmem_st32(addr, r); else tmem_st16(addr, r);
 }
 
-// Query rows [c0, c0 + COLS) of the row tile into shared memory as the B
-// operand of S^T (core matrices along K, row groups of 8), by 128 threads,
-// with what the softmax needs to know of each row.
-template <int DH, bool FP8, int N, int COLS>
-__device__ __forceinline__ void stage_queries(const PagedArgs &a, const Walk &w, uint8_t *sq, RowInfo<N> &info, int c0, int tid) {
-  const int rows = w.x.W * a.group;
-  constexpr int kChunks = DH / 8;                  // 16-byte chunks of a bf16 row
-  constexpr int kPieces = COLS * kChunks;
+// The query rows of a row tile into shared memory as the B operand of S^T
+// (core matrices along K, row groups of 8), by one warp, with what the
+// softmax needs to know of each row.
+template <int DH, bool FP8, int N>
+__device__ __forceinline__ void stage_queries(const PagedArgs &a, const Walk &w, uint8_t *sq, RowInfo<N> &info, int lane) {
+  const int rows = w.x.W * a.group, r0 = w.rt * N;
 #pragma unroll
-  for (int it = 0; it < (kPieces + 127) / 128; ++it) {
-    const int idx = it * 128 + tid;
-    if (kPieces % 128 && idx >= kPieces) break;    // whole warps
-    const int n = c0 + idx / kChunks, c = idx % kChunks;
-    const int r = w.rt * N + n, t = r / a.group, g = r - t * a.group;
-    const bool live = r < rows;
+  for (int n = lane; n < N; n += 32) {
+    const int r = r0 + n, t = r / a.group;
+    int lo = 0, hi = 0x7fffffff;   // a column that is no row masks nothing; its results go nowhere
+    if (r < rows) visible(a, w.x.pos + t, w.x.L, lo, hi);
+    info.lo[n] = lo;
+    info.hi[n] = hi;
+    info.out[n] = r < rows ? (w.x.q0 + t) * a.Hq + w.h * a.group + (r - t * a.group) : -1;
+  }
+  constexpr int kChunks = DH / 8;                  // 16-byte chunks of a bf16 row
+  constexpr int kRows = 32 / kChunks;              // rows of one round of the warp
+  const int c = lane % kChunks;
+#pragma unroll 8
+  for (int n = lane / kChunks; n < N; n += kRows) {
+    const int r = r0 + n, t = r / a.group, g = r - t * a.group;
     uint4 u = make_uint4(0, 0, 0, 0);
-    if (live)
+    if (r < rows)
       u = *reinterpret_cast<const uint4 *>(a.q + (w.x.q0 + t) * a.q_stride + (w.h * a.group + g) * DH + c * 8);
     if constexpr (!FP8) {
       *reinterpret_cast<uint4 *>(sq + (n / 8) * (kChunks * 128) + c * 128 + (n % 8) * 16) = u;
     } else {
-      // scaled by a power of two into (224, 448], then hi = rn(x), lo = rn(x - hi)
       const uint32_t m2 = max_mag(u, 0);
       uint32_t m = max(m2 & 0xffffu, m2 >> 16);
 #pragma unroll
       for (int o = kChunks / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const int byte = scale_byte(m);
-      float x[8];
-      unpack8(u, x);
-      const float f = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float p = x[2 * e] * f, q = x[2 * e + 1] * f;
-        const uint16_t hh = f32_to_e4m3x2(p, q);
-        const float2 b = e4m3x2_to_f32(hh);
-        hi[e] = hh;
-        lo[e] = f32_to_e4m3x2(p - b.x, q - b.y);
-      }
+      uint2 hi, lo;
+      const int byte = split_e4m3(u, m, hi, lo);
       uint8_t *d = sq + (n / 8) * (DH / 16 * 128) + (c / 2) * 128 + (n % 8) * 16 + (c & 1) * 8;
-      *reinterpret_cast<uint2 *>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-      *reinterpret_cast<uint2 *>(d + N * DH) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+      *reinterpret_cast<uint2 *>(d) = hi;
+      *reinterpret_cast<uint2 *>(d + N * DH) = lo;
       if (c == 0) info.scale[n] = scale_of(m < 0x7f80u ? byte : 255);   // a row with an infinity or NaN scores NaN
-    }
-    if (c == 0) {
-      int lo = 0, hi = 0x7fffffff;   // a column that is no row masks nothing; its results go nowhere
-      if (live) visible(a, static_cast<long long>(w.x.pos) + t, w.x.L, lo, hi);
-      info.lo[n] = lo;
-      info.hi[n] = hi;
-      info.out[n] = live ? (w.x.q0 + t) * a.Hq + w.h * a.group + g : -1;
     }
   }
 }
@@ -288,8 +191,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *misc = smem + C::kOffMisc;
-  RowInfo<N> *info = reinterpret_cast<RowInfo<N> *>(misc);                // [2]: this piece's and the next one's
-  float *m_s = reinterpret_cast<float *>(info + 2);                       // [group][kCols] reference maxima
+  Piece<N> *pieces = reinterpret_cast<Piece<N> *>(misc);                  // [2]: this one and the next one
+  float *m_s = reinterpret_cast<float *>(pieces + 2);                       // [group][kCols] reference maxima
   float *corr_s = m_s + 2 * kCols;                                        // [group][kCols]
   float *red_s = corr_s + 2 * kCols;                                      // [quarter][group][kCols]
   uint8_t *scales = reinterpret_cast<uint8_t *>(red_s + 8 * kCols);           // [kScaleSlots][K, V][kTile]
@@ -304,16 +207,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   uint64_t *c_full = p_free + kPBuf;        // [kCBuf] V piece converted
   uint64_t *c_free = c_full + kCBuf;        // [kCBuf] its O^T MMAs done
   uint64_t *sc_full = c_free + kCBuf;       // [kScaleSlots]
-  uint64_t *q_full = sc_full + C::kScaleSlots;
-  uint64_t *o_full = q_full + 1;
+  uint64_t *q_full = sc_full + C::kScaleSlots;   // [2] piece prepared
+  uint64_t *q_free = q_full + 2;            // [2] its last use over
+  uint64_t *o_full = q_free + 2;
   uint64_t *o_free = o_full + 1;
   long long *s_scan = reinterpret_cast<long long *>(o_free + 1);          // [32]
   Start *start = reinterpret_cast<Start *>(s_scan + 32);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert(2 * sizeof(RowInfo<N>) + 12 * kCols * 4 + (2 * kSt + 2 * kSBuf + 2 * kPBuf + 2 * kCBuf + 3) * 8 + 256 + 64 +
+  static_assert(2 * sizeof(Piece<N>) + 12 * kCols * 4 + (2 * kSt + 2 * kSBuf + 2 * kPBuf + 2 * kCBuf + 6) * 8 + 256 + 64 +
                         C::kScaleSlots * (2 * kTile + 8 + 4) + 4 <= C::kMisc - 1024,
                 "row tables and barriers");
+  static_assert(sizeof(Piece<N>) % 16 == 0 && kCols % 16 == 0, "scales, 16-byte aligned for the bulk loads");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
@@ -327,7 +232,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     for (int b = 0; b < kPBuf; ++b) { mbar_init(&p_full[b], kTileWarps); mbar_init(&p_free[b], 1); }
     for (int b = 0; b < kCBuf; ++b) { mbar_init(&c_full[b], 4); mbar_init(&c_free[b], 1); }
     for (int b = 0; b < C::kScaleSlots; ++b) mbar_init(&sc_full[b], 1);
-    mbar_init(q_full, 8);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&q_full[b], 1);
+      mbar_init(&q_free[b], 8 + 2 + (FP8 ? 4 : 0));   // the warps that read the piece
+    }
     mbar_init(o_full, 1);
     mbar_init(o_free, 8);
     *abort_flag = 0;
@@ -347,88 +255,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 
   pdl_wait();   // the batch's metadata, the pages and the queries may come from the previous kernel
   find_start(a, N, min_tiles, s_scan, start);
-  Walk w(a, N);
-  w.left = start->left;
-  if (w.left > 0) {
-    w.i = start->i;
-    w.load();
-    w.item = static_cast<int>(start->residual / w.n);
-    w.j = static_cast<int>(start->residual - static_cast<long long>(w.item) * w.n);
-  }
-
   if (warp < 4) {
   reg_dealloc<C::kRegsIssue>();
   if (warp == 0) {
     // ------------------------------------------------------------- producer
-    const int per_tile = kTile >> a.c.page_shift;
-    const int page_rows = 1 << a.c.page_shift;
-    const int none = static_cast<int>((static_cast<long long>(a.c.num_pages) * a.c.heads << a.c.page_shift) / 8);
-    bool bad = false, ok = true;
-    uint32_t n = 0, issued = 0;
-    while (ok && w.next()) {
-      const int nT = w.tiles();
-      const int32_t *row = a.c.table + static_cast<size_t>(w.i) * a.c.max_pages;
-      // 8-row group of lane's page of tile j; pages without cached rows read as zeros
-      auto group_of = [&](int j) {
-        if (lane >= per_tile || j >= w.j0 + nT) return none;
-        const long long u = static_cast<long long>(w.t.tile(j)) * kTile + lane * page_rows;
-        if (u >= w.x.L) return none;
-        const int page = __ldg(row + (u >> a.c.page_shift));
-        if (page < 0 || page >= a.c.num_pages) { bad = true; return none; }
-        return ((page * a.c.heads + w.h) << a.c.page_shift) / 8;
-      };
-      int g = group_of(w.j0);
-      for (int j = w.j0; j < w.j0 + nT; ++j, ++n) {
-        const int g_next = group_of(j + 1);     // its latency passes behind this tile's waits
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t pos = 2 * n + kv, st = pos % kSt, round = pos / kSt;
-          if (round > 0) ok = mbar_wait(&empty[st], (round - 1) & 1, abort_flag);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kRaw);
-          __syncwarp();
-          if (lane < per_tile)
-            tma_load_4d(smem + st * C::kRaw + lane * page_rows * (C::kGroup8 / 8), kv ? &tm_v : &tm_k, &full[st], g);
-          issued = pos + 1;
-          if constexpr (FP8) {
-            if (kv == 0) {   // the tile's scales, page_rows bytes of each page
-              const bool live = g < none;
-              const uint32_t slot = n % C::kScaleSlots, pages = __ballot_sync(0xffffffffu, live);
-              if (lane == 0) {
-                pages_of[slot] = pages;
-                mbar_arrive_expect_tx(&sc_full[slot], __popc(pages) * page_rows * 2);
-              }
-              __syncwarp();
-              if (live) {
-                uint8_t *dst = scales + slot * (2 * kTile) + lane * page_rows;
-                bulk_load(dst, a.c.k_scale + static_cast<size_t>(g) * 8, page_rows, &sc_full[slot]);
-                bulk_load(dst + kTile, a.c.v_scale + static_cast<size_t>(g) * 8, page_rows, &sc_full[slot]);
-              }
-            }
-          }
-        }
-        if (!ok) break;
-        g = g_next;
-      }
-    }
-    if (bad) atomicOr(a.status, DLLM_DEV_PAGE);
-    // after an abort: the loads in flight land before the CTA's memory is given up
-    if (!ok && lane < kSt && lane < issued) mbar_drain(&full[lane], ((issued - 1 - lane) / kSt) & 1);
-    if constexpr (FP8) {
-      const uint32_t tiles = (issued + 1) / 2;
-      if (!ok && lane < C::kScaleSlots && lane < tiles)
-        mbar_drain(&sc_full[lane], ((tiles - 1 - lane) / C::kScaleSlots) & 1);
-    }
+    load_tiles<DH, FP8 ? 1 : 2, kSt, C::kScaleSlots>(a, *start, N, &tm_k, &tm_v, smem, full, empty, scales, pages_of, sc_full,
+                                                     abort_flag, lane);
   } else if (warp == 1) {
     // ------------------------------------------------------------- S^T MMAs
-    uint32_t n = 0, seg = 0;
+    uint32_t n = 0;
     bool ok = true;
-    const uint32_t sq = smem_u32(smem + C::kOffQ);
-    while (ok && w.next()) {
-      const int nT = w.tiles();
-      if (nT == 0) continue;
-      ok = warp_wait(q_full, seg++ & 1, abort_flag);
-      for (int j = 0; ok && j < nT; ++j, ++n) {
+    for (uint32_t seg = 0; ok; ++seg) {
+      const uint32_t pi = seg & 1;
+      ok = warp_wait(&q_full[pi], (seg >> 1) & 1, abort_flag);
+      if (!ok || !pieces[pi].more) break;
+      const int nT = pieces[pi].tiles;
+      const uint32_t sq = smem_u32(smem + C::kOffQ + pi * C::kQ);
+      for (int j = 0; j < nT; ++j, ++n) {
         const uint32_t pos = 2 * n, st = pos % kSt, b = n % kSBuf;
         ok = warp_wait(&full[st], (pos / kSt) & 1, abort_flag);
         if (ok && n >= kSBuf) ok = warp_wait(&s_free[b], (n / kSBuf - 1) & 1, abort_flag);
@@ -457,18 +300,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         __syncwarp();
       }
+      if (lane == 0) mbar_arrive(&q_free[pi]);
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------- O^T MMAs
-    uint32_t n = 0, seg = 0;
+    uint32_t n = 0, o_seg = 0;
     bool ok = true;
-    while (ok && w.next()) {
-      const int nT = w.tiles();
-      if (nT == 0) continue;
+    for (uint32_t seg = 0; ok; ++seg) {
+      const uint32_t pi = seg & 1;
+      ok = warp_wait(&q_full[pi], (seg >> 1) & 1, abort_flag);
+      if (!ok || !pieces[pi].more) break;
+      const int nT = pieces[pi].tiles;
       for (int j = 0; ok && j < nT; ++j, ++n) {
         const uint32_t pos = 2 * n + 1, st = pos % kSt, b = n % kPBuf;
         ok = warp_wait(&p_full[b], (n / kPBuf) & 1, abort_flag);
-        if (ok && j == 0 && seg > 0) ok = warp_wait(o_free, (seg - 1) & 1, abort_flag);
+        if (ok && j == 0 && o_seg > 0) ok = warp_wait(o_free, (o_seg - 1) & 1, abort_flag);
         if (ok && !FP8) ok = warp_wait(&full[st], (pos / kSt) & 1, abort_flag);
         const uint32_t t_d = kByTile ? t_o + (n & 1) * N : t_o;
         const bool first = j == 0 || (kByTile && j == 1);   // of its accumulator
@@ -497,53 +343,69 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           __syncwarp();
         }
       }
-      ++seg;
+      o_seg += nT > 0;
+      if (lane == 0) mbar_arrive(&q_free[pi]);
     }
+  } else {
+    // ------------------------------------------------------------- pieces and their query rows
+    // One piece ahead of the others, so that its metadata and its rows are
+    // there when the scores of the last one are.
+    Walk w(a, N, *start);
+    bool more = true, began = false;
+    for (uint32_t seg = 0; more; ++seg) {
+      const uint32_t pi = seg & 1;
+      if (seg >= 2 && !warp_wait(&q_free[pi], ((seg >> 1) - 1) & 1, abort_flag)) break;
+      Piece<N> &pc = pieces[pi];
+      more = w.next();
+      if (lane == 0) {
+        pc.more = more;
+        if (more) {
+          pc.t = w.t;
+          pc.j0 = w.j0;
+          pc.tiles = w.tiles();
+          pc.whole = w.whole();
+          // a CTA's first piece has its first slot, its last one the second
+          pc.slot = 2 * blockIdx.x + (seg > 0);
+          began |= begin_join(a, w, *start, pc.slot);
+        }
+      }
+      if (more) stage_queries<DH, FP8, N>(a, w, smem + C::kOffQ + pi * C::kQ, pc.rows, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[pi]);
+    }
+    if (a.join && lane == 0 && !began) a.join[blockIdx.x].parts = 0;
   }
   } else if (FP8 && warp >= C::kConvWarp0) {
     // ------------------------------------------------------------- V codes -> bf16
     if constexpr (FP8) {
       reg_dealloc<C::kRegsConv>();
-      // a thread takes half of a key's row
-      constexpr int kChunks = DH / 32;   // 16-byte pieces of codes
-      const int t = (warp - C::kConvWarp0) * 32 + lane, k64 = t % kConvKeys, ch = t / kConvKeys * kChunks;
+      const int t = (warp - C::kConvWarp0) * 32 + lane;
       uint32_t n = 0;
-      while (w.next()) {
-        const int nT = w.tiles();
+      for (uint32_t seg = 0;; ++seg) {
+        const uint32_t pi = seg & 1;
+        if (!warp_wait(&q_full[pi], (seg >> 1) & 1, abort_flag) || !pieces[pi].more) break;
+        const TileList tl = pieces[pi].t;
+        const int j0 = pieces[pi].j0, nT = pieces[pi].tiles;
         for (int j = 0; j < nT; ++j, ++n) {
           const uint32_t pos = 2 * n + 1, st = pos % kSt;
           mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
 #pragma unroll 1
           for (int half = 0; half < kTile / kConvKeys; ++half) {
             const uint32_t cn = n * (kTile / kConvKeys) + half, cb = cn % kCBuf;
-            const int key = half * kConvKeys + k64, u = w.t.tile(w.j0 + j) * kTile + key;
-            const bool seen = u < w.t.hi && (u >= w.t.lo || u < a.sinks);
-            const uint8_t *src = smem + st * C::kRaw + key * DH;
-            uint8_t *dst = smem + C::kOffConv + cb * (kConvKeys * DH * 2) + (k64 / 8) * C::kVGroup8 + (k64 % 8) * 128;
-            uint4 q[kChunks];
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c)   // under the load's swizzle (rows of 128 or 64 bytes)
-              q[c] = *reinterpret_cast<const uint4 *>(src + (DH == 128 ? (ch + c) ^ (key & 7) : (ch + c) ^ ((key >> 1) & 3)) * 16);
-            if (cn >= kCBuf) mbar_wait(&c_free[cb], (cn / kCBuf - 1) & 1, abort_flag);
-            if (!seen) {   // whatever lies there: 0 * NaN would not be 0
-#pragma unroll
-              for (int c = 0; c < kChunks; ++c) q[c] = make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-              const uint2 a0 = e4m3x4_to_bf16_0213(q[c].x), a1 = e4m3x4_to_bf16_0213(q[c].y);
-              const uint2 b0 = e4m3x4_to_bf16_0213(q[c].z), b1 = e4m3x4_to_bf16_0213(q[c].w);
-              const int o = 2 * (ch + c);       // bf16 pieces o and o + 1 of the row, eight to a 128-byte column piece
-              uint8_t *d = dst + (o / 8) * 1024;
-              *reinterpret_cast<uint4 *>(d + ((o & 7) ^ (key & 7)) * 16) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-              *reinterpret_cast<uint4 *>(d + (((o + 1) & 7) ^ (key & 7)) * 16) = make_uint4(b0.x, b0.y, b1.x, b1.y);
-            }
+            const int u = tl.tile(j0 + j) * kTile + half * kConvKeys + t % kConvKeys;
+            convert_v<DH>(smem + st * C::kRaw, smem + C::kOffConv + cb * (kConvKeys * DH * 2), half, t,
+                          u < tl.hi && (u >= tl.lo || u < a.sinks),
+                          [&] { if (cn >= kCBuf) mbar_wait(&c_free[cb], (cn / kCBuf - 1) & 1, abort_flag); },
+                          [](uint2 v) { return v; });
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&c_full[cb]);
           }
           if (lane == 0) mbar_arrive(&empty[st]);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_free[pi]);
       }
     }
   } else {
@@ -556,36 +418,31 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     constexpr int kOut = N / 2;                // rows that a group stages and writes
     const int out0 = wg * kOut;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    constexpr float kLazy = 8.f;
-    constexpr float kNone = -3.0e38f;   // reference of a row that has seen no key: finite, so that x is not NaN
     const auto maxop = [](float p, float q) { return fmaxf(p, q); };
     const auto addop = [](float p, float q) { return p + q; };
-    uint32_t n = 0, seg = 0, o_seg = 0;
-    bool more = w.next();
-    bool joined = false;       // this CTA's last piece began an item that others finish
-    if (more) {
-      stage_queries<DH, FP8, N, kOut>(a, w, smem + C::kOffQ, info[0], out0, tid);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0 && w.tiles() > 0) mbar_arrive(q_full);
-    }
-    while (more) {
-      const RowInfo<N> &ri = info[seg & 1];
-      const int nT = w.tiles();
+    uint32_t n = 0, o_seg = 0;
+    for (uint32_t seg = 0;; ++seg) {
+      const uint32_t pi = seg & 1;
+      // all of both groups go on or none does (the last piece's maxima are read, too)
+      if (bar_any(3, 256, !mbar_wait(&q_full[pi], (seg >> 1) & 1, abort_flag))) break;
+      const Piece<N> &pc = pieces[pi];
+      if (!pc.more) break;
+      const RowInfo<N> &ri = pc.rows;
+      const TileList tl = pc.t;
+      const int nT = pc.tiles, j0 = pc.j0;
       float l[kCols];
 #pragma unroll
       for (int e = 0; e < kCols; ++e) l[e] = 0.f;
-      named_bar_sync(3, 256);               // the rows' info is written, the last piece's maxima are read
       if (tid < kCols) m_s[g0 + tid] = kNone;
       named_bar_sync(1 + wg, 128);
       bool first = true;                    // of the group's tiles
       for (int j = 0; j < nT; ++j, ++n) {
         if (kByTile && (n & 1) != wg) continue;
         const uint32_t b = n % kSBuf, pb = n % kPBuf;
-        const int key0 = w.t.tile(w.j0 + j) * kTile, u = key0 + key;
+        const int key0 = tl.tile(j0 + j) * kTile, u = key0 + key;
         // every row of the tile sees every key of it?
-        const bool all_seen = key0 + kTile <= w.t.hi_first && (key0 >= w.t.lo_last || key0 + kTile <= a.sinks);
-        const bool seen = u < w.t.hi && (u >= w.t.lo || u < a.sinks);   // this key, by any row
+        const bool all_seen = key0 + kTile <= tl.hi_first && (key0 >= tl.lo_last || key0 + kTile <= a.sinks);
+        const bool seen = u < tl.hi && (u >= tl.lo || u < a.sinks);   // this key, by any row
         float c = a.scale_log2, vs = 1.f;
         if constexpr (FP8) {
           const uint32_t slot = n % C::kScaleSlots;
@@ -702,19 +559,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (lane == 0) mbar_arrive(&p_full[pb]);
         first = false;
       }
-      // the next piece's queries are staged before this one's results are
-      // written, so that its scores run meanwhile: once every S^T of this
-      // piece is done, the last of which may be the other group's
-      if (kByTile && nT > 0 && ((n - 1) & 1) != wg) mbar_wait(&s_full[(n - 1) % kSBuf], ((n - 1) / kSBuf) & 1, abort_flag);
-      const Walk done = w;
-      more = w.next();
-      ++seg;
-      if (more) {
-        stage_queries<DH, FP8, N, kOut>(a, w, smem + C::kOffQ, info[seg & 1], out0, tid);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && w.tiles() > 0) mbar_arrive(q_full);
-      }
       const float part = reduce_columns<kCols>(l, lane, addop);
       if (lane < kCols) red_s[quarter * (2 * kCols) + g0 + lane] = part;
       named_bar_sync(1 + wg, 128);
@@ -770,7 +614,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const int dm = DH == 128 ? key : quarter * 16 + lane;
       const int dc = FP8 ? (dm & ~3) | ((dm & 1) << 1) | ((dm >> 1) & 1) : dm;
       const bool dlive = DH == 128 || lane < 16;
-      if (done.whole()) {
+      if (pc.whole) {
 #pragma unroll
         for (int e = 0; e < kOut; ++e) {
           const int row = ri.out[out0 + e];
@@ -784,27 +628,19 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         if (a.lse && tid < kOut && ri.out[out0 + tid] >= 0) {
           const float2 ml = merged(out0 + tid);
-          a.lse[ri.out[out0 + tid]] = ml.y != 0.f ? (ml.x + log2f(ml.y)) * 0.69314718055994531f : -INFINITY;
+          a.lse[ri.out[out0 + tid]] = ml.y != 0.f ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
         }
       } else {
-        // the first piece of a CTA goes to its first slot, a later one (its last) to the second
-        const size_t slot = static_cast<size_t>(blockIdx.x) * 2 + (seg > 1 ? 1 : 0);
+        const size_t slot = pc.slot;
         float *po = a.part_o + (slot * N + out0) * DH + dc;
         if (dlive)
 #pragma unroll
           for (int e = 0; e < kOut; ++e) po[e * DH] = __uint_as_float(o[e]);
         if (tid < kOut) a.part_ml[slot * N + out0 + tid] = merged(out0 + tid);
-        if (done.j0 == 0) {
-          joined = true;
-          if (tid == 0 && wg == 0) {
-            // the item's other pieces are the first slots of the next CTAs
-            const int parts = 1 + static_cast<int>((done.n - done.j1 + start->per - 1) / start->per);
-            a.join[blockIdx.x] = make_int4(done.i, done.h * done.row_tiles + done.rt, static_cast<int>(slot), parts);
-          }
-        }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_free[pi]);
     }
-    if (a.join && !joined && tid == 0 && wg == 0) a.join[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
 
   tc_fence_before();
@@ -817,63 +653,57 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 }
 
 // Joins the partial results of the item that CTA blockIdx.x began and others
-// finished: block y takes the item's rows y, y + gridDim.y, ...
+// finished: one warp per row, the pieces in their order with a running
+// maximum, four of them on the way at a time.
 constexpr int kJoinThreads = 256;
 
 template <int DH>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArgs a, const int n_rows) {
-  constexpr int kGroups = kJoinThreads / DH;      // threads of one column: each takes every kGroups-th piece
-  __shared__ float weight[2 * kMaxCtas];
-  __shared__ float acc[kJoinThreads];
-  __shared__ float sum_s;
+  using Vec = typename std::conditional<DH == 128, float4, float2>::type;   // a lane's columns
+  constexpr int kVec = DH / 32, kAhead = 4;
   pdl_trigger();
   pdl_wait();
-  const int4 job = a.join[blockIdx.x];
-  const int parts = job.w;
-  if (parts == 0) return;
-  const Extent x = paged_extent(a, job.x, false);
-  const int row_tiles = (x.W * a.group + n_rows - 1) / n_rows;
-  const int h = job.y / row_tiles, rt = job.y - h * row_tiles;
-  const int tid = threadIdx.x, c = tid % DH, grp = tid / DH;
-  auto slot_of = [&](int p) { return static_cast<size_t>(p == 0 ? job.z : 2 * (blockIdx.x + p)); };
-  for (int n = blockIdx.y; n < n_rows; n += gridDim.y) {
-    const int r = rt * n_rows + n, t = r / a.group;
-    if (t >= x.W) break;
-    const int row = (x.q0 + t) * a.Hq + h * a.group + (r - t * a.group);
-    if (tid < 32) {
-      float m = -INFINITY, l = 0.f;   // a piece without keys: m = -3e38, l = 0
-      for (int p = tid; p < parts; p += 32) m = fmaxf(m, a.part_ml[slot_of(p) * n_rows + n].x);
-      m = warp_max(m);
-      for (int p = tid; p < parts; p += 32) {
-        const float2 ml = a.part_ml[slot_of(p) * n_rows + n];
-        const float wgt = ex2_approx(ml.x - m);
-        weight[p] = wgt;
-        l += wgt * ml.y;
-      }
-      l = warp_sum(l);
-      if (tid == 0) {
-        sum_s = l;
-        if (a.lse) a.lse[row] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-      }
-    }
-    __syncthreads();
-    float y = 0.f;
-#pragma unroll 4
-    for (int p = grp; p < parts; p += kGroups) {
-      const float wgt = weight[p];
-      if (wgt != 0.f) y += wgt * a.part_o[(slot_of(p) * n_rows + n) * DH + c];
-    }
-    acc[tid] = y;
-    __syncthreads();
-    if (grp == 0) {
+  const JoinJob job = a.join[blockIdx.x];
+  const int n = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (job.parts == 0 || n >= n_rows || job.r0 + n >= job.rows) return;
+  float m = -INFINITY, l = 0.f, o[kVec] = {};
+  for (int p0 = 0; p0 < job.parts; p0 += kAhead) {
+    float2 ml[kAhead];
+    Vec y[kAhead];
 #pragma unroll
-      for (int g = 1; g < kGroups; ++g) y += acc[g * DH + c];
-      y = sum_s != 0.f ? y / sum_s : 0.f;
-      if (a.out_fp32) static_cast<float *>(a.out)[static_cast<size_t>(row) * DH + c] = y;
-      else static_cast<uint16_t *>(a.out)[static_cast<size_t>(row) * DH + c] = f32_to_bf16(y);
+    for (int k = 0; k < kAhead; ++k) {
+      const int p = p0 + k;
+      const size_t at = static_cast<size_t>(p == 0 ? job.slot : 2 * (blockIdx.x + p)) * n_rows + n;
+      if (p < job.parts) {
+        ml[k] = a.part_ml[at];
+        y[k] = reinterpret_cast<const Vec *>(a.part_o + at * DH)[lane];
+      }
     }
-    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (p0 + k >= job.parts) break;
+      const float mn = fmaxf(m, ml[k].x), f = ex2_approx(m - mn), g = ex2_approx(ml[k].x - mn);
+      l = l * f + ml[k].y * g;
+      const float *v = reinterpret_cast<const float *>(&y[k]);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) o[e] = o[e] * f + v[e] * g;
+      m = mn;
+    }
   }
+  const int r = job.r0 + n, t = r / a.group;
+  const size_t row = static_cast<size_t>(job.q0 + t) * a.Hq + job.h * a.group + (r - t * a.group);
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) o[e] = l != 0.f ? o[e] / l : 0.f;
+  if (a.out_fp32) {
+    float *d = static_cast<float *>(a.out) + row * DH + lane * kVec;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) d[e] = o[e];
+  } else {
+    uint32_t *d = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + row * DH + lane * kVec);
+#pragma unroll
+    for (int e = 0; e < kVec; e += 2) d[e / 2] = pack_bf16x2(o[e], o[e + 1]);
+  }
+  if (a.lse && lane == 0) a.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -887,16 +717,17 @@ dllm_status check_shape(const dllm_kv_pages *pages, const dllm_paged_attn_args *
   if (a->Hq % pages->heads || a->Hq / pages->heads > 64 || a->B > 4096) return DLLM_ERR_UNSUPPORTED;
   if (a->left >= (1 << 30) || a->right >= (1 << 30) || a->sinks >= (1 << 30)) return DLLM_ERR_UNSUPPORTED;
   if (a->max_kv >= (1 << 30)) return DLLM_ERR_UNSUPPORTED;
-  if (static_cast<long long>(a->q_rows) * a->Hq >= (1ll << 31) || static_cast<long long>(a->max_q) * a->Hq >= (1ll << 31))
+  if (static_cast<long long>(a->q_rows) * a->Hq >= (1ll << 30) || static_cast<long long>(a->max_q) * a->Hq >= (1ll << 30))
     return DLLM_ERR_UNSUPPORTED;
   return DLLM_OK;
 }
 
-// Columns of a row tile: the least of 16, 32 and 64 that holds a request's
-// rows of one cached head, 64 where none does.
+// Rows of a row tile: the least of 16, 32 and 128 that holds a request's rows
+// of one cached head, 256 where none does. Up to 32 they are the N of the
+// MMAs here, from there on the M of those in paged_rows.cu.
 int row_tile(const dllm_kv_pages *pages, const dllm_paged_attn_args *a) {
   const long long rows = static_cast<long long>(a->max_q) * (a->Hq / pages->heads);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
 }
 
 // A CTA's piece is at least kMinTiles tiles: items of no more are never cut.
@@ -912,23 +743,29 @@ Ws ws_layout(const dllm_kv_pages *pages, const dllm_paged_attn_args *a) {
   const size_t rows = static_cast<size_t>(2 * kMaxCtas) * row_tile(pages, a);
   w.part_ml = align256(rows * pages->dh * 4);
   w.join = w.part_ml + align256(rows * 8);
-  w.total = w.join + align256(kMaxCtas * 16);
+  w.total = w.join + align256(kMaxCtas * sizeof(JoinJob));
   return w;
 }
 
 template <int DH, bool FP8, int N>
-dllm_status launch(const dllm_kv_pages *pages, const dllm_paged_attn_args *a, PagedArgs &g, cudaStream_t s) {
+dllm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &g, int min_tiles, int ctas, cudaStream_t s) {
   using C = Cfg<DH, FP8, N>;
+  auto kern = paged_attn_kernel<DH, FP8, N>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kBytes, s, tk, tv, g, min_tiles);
+  return e == cudaSuccess ? DLLM_OK : cuda_error(e);
+}
+
+template <int DH, bool FP8>
+dllm_status launch_attn(const dllm_kv_pages *pages, const dllm_paged_attn_args *a, PagedArgs &g, cudaStream_t s) {
   CUtensorMap tk, tv;
   const uint64_t rows = static_cast<uint64_t>(pages->num_pages) * pages->heads * pages->page_size;
   if (!make_tmap_page_rows(&tk, pages->k, rows, DH, FP8 ? 1 : 2, pages->page_size) ||
       !make_tmap_page_rows(&tv, pages->v, rows, DH, FP8 ? 1 : 2, pages->page_size))
     return DLLM_ERR_CUDA;
-  auto kern = paged_attn_kernel<DH, FP8, N>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
-  if (e != cudaSuccess) return cuda_error(e);
   // most tiles that the bounds allow, and so most CTAs with work
-  const long long row_tiles = (static_cast<long long>(a->max_q) * g.group + N - 1) / N;
+  const int n = row_tile(pages, a);
+  const long long row_tiles = (static_cast<long long>(a->max_q) * g.group + n - 1) / n;
   const long long per_item = g.max_kv > 0 ? (g.max_kv + kTile - 1) / kTile : 1;
   const bool split = may_split(a);
   const int min_tiles = split ? kMinTiles : static_cast<int>(per_item);
@@ -936,24 +773,18 @@ dllm_status launch(const dllm_kv_pages *pages, const dllm_paged_attn_args *a, Pa
   const double most = static_cast<double>(a->B) * pages->heads * row_tiles * per_item;
   int ctas = sm_budget() < kMaxCtas ? sm_budget() : kMaxCtas;
   if (most / min_tiles < ctas) ctas = static_cast<int>(most / min_tiles) + 1;
-  e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kBytes, s, tk, tv, g, min_tiles);
-  if (e != cudaSuccess) return cuda_error(e);
+  const dllm_status st = n == 16   ? launch<DH, FP8, 16>(tk, tv, g, min_tiles, ctas, s)
+                         : n == 32 ? launch<DH, FP8, 32>(tk, tv, g, min_tiles, ctas, s)
+                                   : launch_paged_rows(DH, FP8, n, tk, tv, g, min_tiles, ctas, s);
+  if (st != DLLM_OK) return st;
   unsigned launches = 1;
   if (split) {
-    e = launch_pdl(paged_join_kernel<DH>, dim3(ctas, N < 16 ? N : 16), dim3(kJoinThreads), 0, s, g, N);
+    const cudaError_t e = launch_pdl(paged_join_kernel<DH>, dim3(ctas, (n * 32 + kJoinThreads - 1) / kJoinThreads),
+                                     dim3(kJoinThreads), 0, s, g, n);
     if (e != cudaSuccess) return cuda_error(e);
     launches = 2;
   }
   return launch_status(launches);
-}
-
-template <int DH, bool FP8>
-dllm_status launch_n(const dllm_kv_pages *pages, const dllm_paged_attn_args *a, PagedArgs &g, cudaStream_t s) {
-  switch (row_tile(pages, a)) {
-    case 16: return launch<DH, FP8, 16>(pages, a, g, s);
-    case 32: return launch<DH, FP8, 32>(pages, a, g, s);
-    default: return launch<DH, FP8, 64>(pages, a, g, s);
-  }
 }
 
 }  // namespace
@@ -996,10 +827,10 @@ extern "C" dllm_status dllm_paged_attn(const dllm_kv_pages *pages, const dllm_pa
     char *base = static_cast<char *>(ws);
     g.part_o = reinterpret_cast<float *>(base);
     g.part_ml = reinterpret_cast<float2 *>(base + layout.part_ml);
-    g.join = reinterpret_cast<int4 *>(base + layout.join);
+    g.join = reinterpret_cast<JoinJob *>(base + layout.join);
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool fp8 = pages->type == DLLM_KV_E4M3;
-  if (pages->dh == 64) return fp8 ? launch_n<64, true>(pages, a, g, s) : launch_n<64, false>(pages, a, g, s);
-  return fp8 ? launch_n<128, true>(pages, a, g, s) : launch_n<128, false>(pages, a, g, s);
+  if (pages->dh == 64) return fp8 ? launch_attn<64, true>(pages, a, g, s) : launch_attn<64, false>(pages, a, g, s);
+  return fp8 ? launch_attn<128, true>(pages, a, g, s) : launch_attn<128, false>(pages, a, g, s);
 }

@@ -1,0 +1,624 @@
+// Attention over the paged cache where a request has many query rows per
+// cached head (blocks of a denoising step, pieces of prompts): the rows are
+// the M = 128 of the tensor-core tile, one per thread of the softmax, so
+// row maxima and sums need no exchange, and P goes back to TMEM as the A
+// operand of P V.
+//
+// Two streams share a CTA's tensor core: while one stream's softmax works on
+// its scores, the other's MMAs run. With more than 128 rows (tiles of 256)
+// each stream has 128 of them and both read every K and V tile; with up to
+// 128 the streams take every other key tile of the same rows and their
+// results are merged at the end.
+//
+// Warp roles:
+//   warp 0      TMA (load_tiles)
+//   warp 1      MMAs, alternating streams: P V of a tile, then the scores of
+//               the stream's next tile over the same TMEM (MMAs of one thread
+//               run in order)
+//   warp 3      walks the CTA's pieces one ahead of the others
+//   warps 4..11 two softmax warpgroups, one per stream, one row per thread;
+//               they also stage the query rows
+//   last four   (e4m3 pages) V codes -> bf16 with the scale folded in (a
+//               power of two: exact), and the K scales of the scores' columns
+// TMEM (512 columns): S / P of stream s at 128 s, O at 256 + 128 s.
+// A row's reference maximum moves only when its maximum passes it by more
+// than 2^8; the row's O is then rescaled in TMEM.
+// e4m3 pages: K codes and the query rows as in paged_attn.cu (two e4m3 parts
+// of the rows); the scores' columns are multiplied by scale * K scale.
+#include "paged.cuh"
+
+namespace dllm {
+
+namespace {
+
+constexpr uint32_t kColO = 256;
+
+template <int DH, bool FP8, bool TWO>
+struct RowsCfg {
+  static constexpr int kRows = TWO ? 256 : 128;               // rows of an item
+  static constexpr int kConvWarp0 = 12;
+  static constexpr int kThreads = 32 * (kConvWarp0 + (FP8 ? 4 : 0));
+  // registers a thread: what the TMA and MMA warps and the converters do not
+  // need goes to the softmax groups (the sum is the launch's)
+  static constexpr int kRegsIssue = FP8 ? 64 : 72, kRegsSoft = FP8 ? 184 : 216, kRegsConv = 80;
+  static_assert(FP8 ? kRegsIssue + 2 * kRegsSoft + kRegsConv <= 4 * 128 : kRegsIssue + 2 * kRegsSoft <= 3 * 168, "registers");
+  static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);
+  static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);
+  static constexpr int kVGroup8 = 8 * DH * 2;
+  static constexpr int kQ = 128 * DH * 2;                     // 128 rows: bf16, or two e4m3 parts
+  static constexpr int kCBuf = FP8 ? 4 : 0;                   // converted V pieces: two tiles
+  static constexpr int kConv = kCBuf * kConvKeys * DH * 2;
+  static constexpr int kScaleBytes = FP8 ? 8192 : 0;          // scale bytes, column factors, row factors
+  static constexpr int kMisc = 1984 + kScaleBytes;            // + 1024 of alignment
+  static constexpr int kMax = (232448 - 1024 - 2 * kQ - kConv - kMisc) / kRaw;
+  static constexpr int kCap = 196608 / kRaw;                  // 192 KB in flight are enough
+  static constexpr int kStages = (kMax < kCap ? kMax : kCap) & (FP8 ? ~1 : ~0);
+  static constexpr int kScaleSlots = FP8 ? kStages / 2 + 3 : 0;
+  static constexpr int kOffConv = kStages * kRaw;
+  static constexpr int kOffQ = kOffConv + kConv;
+  static constexpr int kOffMisc = kOffQ + 2 * kQ;
+  static constexpr int kBytes = kOffMisc + kMisc + 1024;
+  static_assert(kStages >= 4 && kBytes <= 232448, "shared memory");
+};
+
+struct alignas(16) RowsPiece {
+  Extent x;
+  TileList t;
+  int h, r0;               // head, first flat row
+  int two;                 // each stream has rows of its own
+  int j0, tiles, more, whole, slot;
+};
+
+// Query rows [n0, n0 + CNT) of the 128 in `sq`, flat rows r0 + n, as the A
+// operand of the scores (rows of 128 bytes under the 128-byte swizzle, column
+// pieces 16 KB apart; e4m3 parts: DH-byte rows, parts 128 DH apart), by 128
+// threads. The rows' powers of two go to qs.
+template <int DH, bool FP8, int CNT>
+__device__ __forceinline__ void stage_rows(const PagedArgs &a, const RowsPiece &pc, int r0, int n0, uint8_t *sq, float *qs,
+                                           int tid) {
+  const int rows = pc.x.W * a.group;
+  constexpr int kChunks = DH / 8;
+#pragma unroll 4
+  for (int idx = tid; idx < CNT * kChunks; idx += 128) {
+    const int n = n0 + idx / kChunks, c = idx % kChunks;
+    const int r = r0 + n, t = r / a.group, g = r - t * a.group;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (r < rows)
+      u = *reinterpret_cast<const uint4 *>(a.q + (pc.x.q0 + t) * a.q_stride + (pc.h * a.group + g) * DH + c * 8);
+    if constexpr (!FP8) {
+      *reinterpret_cast<uint4 *>(sq + (c / 8) * 16384 + (n / 8) * 1024 + (n % 8) * 128 + ((c % 8) ^ (n % 8)) * 16) = u;
+    } else {
+      const uint32_t m2 = max_mag(u, 0);
+      uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+      for (int o = kChunks / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      uint2 hi, lo;
+      const int byte = split_e4m3(u, m, hi, lo);
+      const int sc = DH == 128 ? (c / 2) ^ (n % 8) : (c / 2) ^ ((n / 2) % 4);
+      uint8_t *d = sq + n * DH + sc * 16 + (c % 2) * 8;
+      *reinterpret_cast<uint2 *>(d) = hi;
+      *reinterpret_cast<uint2 *>(d + 128 * DH) = lo;
+      if (c == 0) qs[n] = scale_of(m < 0x7f80u ? byte : 255);   // a row with an infinity or NaN scores NaN
+    }
+  }
+}
+
+template <int DH, bool FP8, bool TWO>
+__global__ void __launch_bounds__(RowsCfg<DH, FP8, TWO>::kThreads, 1)
+paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a,
+                  const int min_tiles) {
+  using C = RowsCfg<DH, FP8, TWO>;
+  constexpr int kSt = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *misc = smem + C::kOffMisc;
+  RowsPiece *pieces = reinterpret_cast<RowsPiece *>(misc);                // [2]: this one and the next one
+  float2 *ml_s = reinterpret_cast<float2 *>(pieces + 2);                  // [128] maxima and sums to merge
+  uint64_t *full = reinterpret_cast<uint64_t *>(ml_s + 128);              // [kSt] stage loaded
+  uint64_t *empty = full + kSt;             // [kSt] stage read by its MMAs (or converted)
+  uint64_t *s_full = empty + kSt;           // [stream]
+  uint64_t *p_full = s_full + 2;            // [stream]
+  uint64_t *piece_full = p_full + 2;        // [2]
+  uint64_t *piece_free = piece_full + 2;    // [2]
+  uint64_t *q_full = piece_free + 2;        // [2] query rows staged
+  uint64_t *o_full = q_full + 2;
+  uint64_t *o_free = o_full + 1;
+  long long *s_scan = reinterpret_cast<long long *>(o_free + 1);          // [16]
+  Start *start = reinterpret_cast<Start *>(s_scan + 16);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  static_assert(2 * sizeof(RowsPiece) + 1024 + (2 * kSt + 12) * 8 + 128 + sizeof(Start) + 8 <= 1984, "piece and barriers");
+  // e4m3 pages
+  uint8_t *scales = misc + 1984;                                          // [kScaleSlots][K, V][kTile]
+  float *col_s = reinterpret_cast<float *>(scales + C::kScaleSlots * 2 * kTile);   // [4][kTile] score factors of a tile's keys
+  float *qs_s = col_s + (FP8 ? 4 * kTile : 0);                            // [piece parity][256] powers of two of the rows
+  uint64_t *c_full = reinterpret_cast<uint64_t *>(qs_s + (FP8 ? 512 : 0));   // [kCBuf] V piece converted
+  uint64_t *c_free = c_full + C::kCBuf;     // [kCBuf] its MMAs done
+  uint64_t *sc_full = c_free + C::kCBuf;    // [kScaleSlots] scale bytes loaded
+  uint64_t *col_full = sc_full + C::kScaleSlots;   // [4] factors written
+  uint32_t *pages_of = reinterpret_cast<uint32_t *>(col_full + 4);        // [kScaleSlots]
+  static_assert(!FP8 || C::kScaleSlots * (2 * kTile + 12) + 4 * kTile * 4 + 2048 + (2 * C::kCBuf + 4) * 8 <= C::kScaleBytes,
+                "scales");
+  static_assert(1984 % 16 == 0 && sizeof(RowsPiece) % 16 == 0, "scales, 16-byte aligned for the bulk loads");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSt; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], FP8 && (s & 1) ? 4 : 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&p_full[b], 4);
+      mbar_init(&piece_full[b], 1);
+      mbar_init(&piece_free[b], 8 + 1 + (FP8 ? 4 : 0));   // the warps that read it
+      mbar_init(&q_full[b], 8);
+    }
+    mbar_init(o_full, 1);
+    mbar_init(o_free, 8);
+    if constexpr (FP8) {
+      for (int b = 0; b < C::kCBuf; ++b) { mbar_init(&c_full[b], 4); mbar_init(&c_free[b], 1); }
+      for (int b = 0; b < C::kScaleSlots; ++b) mbar_init(&sc_full[b], 1);
+      for (int b = 0; b < 4; ++b) mbar_init(&col_full[b], 4);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  pdl_wait();   // the batch's metadata, the pages and the queries may come from the previous kernel
+  find_start(a, C::kRows, min_tiles, s_scan, start);
+
+  if (warp < 4) {
+    reg_dealloc<C::kRegsIssue>();
+    if (warp == 0) {
+      load_tiles<DH, FP8 ? 1 : 2, kSt, C::kScaleSlots>(a, *start, C::kRows, &tm_k, &tm_v, smem, full, empty, scales, pages_of,
+                                                       sc_full, abort_flag, lane);
+    } else if (warp == 1) {
+      // ----------------------------------------------------------- MMAs
+      uint32_t n0 = 0, o_seg = 0, cnt[2] = {0, 0};   // tiles and streams' tiles before this piece
+      bool ok = true;
+      for (uint32_t seg = 0; ok; ++seg) {
+        const uint32_t pi = seg & 1;
+        ok = warp_wait(&piece_full[pi], (seg >> 1) & 1, abort_flag);
+        if (!ok || !pieces[pi].more) break;
+        const int nT = pieces[pi].tiles;
+        const bool two = TWO && pieces[pi].two;
+        const int n_s[2] = {two ? nT : (nT + 1) / 2, two ? nT : nT / 2};
+        ok = warp_wait(&q_full[pi], (seg >> 1) & 1, abort_flag);
+        // scores of stream s's k-th tile
+        auto scores = [&](int s, int k) {
+          const uint32_t n = n0 + (two ? k : 2 * k + s), pos = 2 * n, st = pos % kSt;
+          ok = ok && warp_wait(&full[st], (pos / kSt) & 1, abort_flag);
+          tc_fence_after();
+          if (ok && elect_one()) {
+            const uint32_t sk = smem_u32(smem + st * C::kRaw), t_s = tmem + s * 128;
+            const uint32_t sq = smem_u32(smem + C::kOffQ + (TWO ? (two ? s : 0) : pi) * C::kQ);
+            if constexpr (!FP8) {
+              const uint64_t dq = sw128_desc(sq, 16, 1024), dk = sw128_desc(sk, 16, C::kGroup8);
+#pragma unroll
+              for (int kk = 0; kk < DH / 16; ++kk)
+                umma_bf16(t_s, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                          idesc_bf16(128, 128, 0, 0), kk > 0);
+            } else {
+              const uint64_t dk = DH == 128 ? sw128_desc(sk, 16, C::kGroup8) : sw64_desc(sk, 16, C::kGroup8);
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                const uint32_t sp = sq + part * 128 * DH;
+                const uint64_t dq = DH == 128 ? sw128_desc(sp, 16, 8 * DH) : sw64_desc(sp, 16, 8 * DH);
+#pragma unroll
+                for (int kk = 0; kk < DH / 32; ++kk)
+                  umma_f8(t_s, dq + ((kk * 32) >> 4), dk + ((kk * 32) >> 4), idesc_e4m3(128, 128), part + kk > 0);
+              }
+            }
+            umma_commit(&s_full[s]);
+            if (!two || s == 1) umma_commit(&empty[st]);
+          }
+          __syncwarp();
+        };
+        // O of stream s += P V of its k-th tile
+        auto values = [&](int s, int k) {
+          const uint32_t n = n0 + (two ? k : 2 * k + s), pos = 2 * n + 1, st = pos % kSt;
+          const uint32_t ns = cnt[s] + k;
+          ok = ok && warp_wait(&p_full[s], ns & 1, abort_flag);
+          if (k == 0 && s == 0 && o_seg > 0) ok = ok && warp_wait(o_free, (o_seg - 1) & 1, abort_flag);
+          if constexpr (!FP8) ok = ok && warp_wait(&full[st], (pos / kSt) & 1, abort_flag);
+          constexpr int kPieces = FP8 ? kTile / kConvKeys : 1, kSteps = 8 / kPieces;
+#pragma unroll
+          for (int piece = 0; piece < kPieces; ++piece) {
+            const uint32_t cn = n * kPieces + piece, cb = FP8 ? cn % (C::kCBuf + !FP8) : 0;
+            if constexpr (FP8) ok = ok && warp_wait(&c_full[cb], (cn / C::kCBuf) & 1, abort_flag);
+            tc_fence_after();
+            if (ok && elect_one()) {
+              const uint32_t sv = smem_u32(FP8 ? smem + C::kOffConv + cb * (kConvKeys * DH * 2) : smem + st * C::kRaw);
+              const uint64_t dv = sw128_desc(sv, 1024, C::kVGroup8);
+#pragma unroll
+              for (int kk = 0; kk < kSteps; ++kk)
+                umma_bf16_tmem_a(tmem + kColO + s * 128, tmem + s * 128 + (piece * kSteps + kk) * 8,
+                                 dv + ((kk * 2 * C::kVGroup8) >> 4), idesc_bf16(128, DH, 0, 1), k > 0 || piece + kk > 0);
+              if (!two || s == 1) umma_commit(FP8 ? &c_free[cb] : &empty[st]);
+            }
+            __syncwarp();
+          }
+        };
+        if (nT > 0) {
+          scores(0, 0);
+          if (n_s[1] > 0) scores(1, 0);
+          for (int k = 0; ok && k < n_s[0]; ++k) {
+            values(0, k);
+            if (k + 1 < n_s[0]) scores(0, k + 1);
+            if (k < n_s[1]) values(1, k);
+            if (k + 1 < n_s[1]) scores(1, k + 1);
+          }
+          if (ok && elect_one()) umma_commit(o_full);
+          __syncwarp();
+          ++o_seg;
+        }
+        n0 += nT;
+        cnt[0] += n_s[0];
+        cnt[1] += n_s[1];
+        if (lane == 0) mbar_arrive(&piece_free[pi]);
+      }
+    } else if (warp == 3) {
+      // ----------------------------------------------------------- pieces
+      Walk w(a, C::kRows, *start);
+      bool more = true, began = false;
+      for (uint32_t seg = 0; more; ++seg) {
+        const uint32_t pi = seg & 1;
+        if (seg >= 2 && !warp_wait(&piece_free[pi], ((seg >> 1) - 1) & 1, abort_flag)) break;
+        more = w.next();
+        if (lane == 0) {
+          RowsPiece &pc = pieces[pi];
+          pc.more = more;
+          if (more) {
+            pc.x = w.x;
+            pc.t = w.t;
+            pc.h = w.h;
+            pc.r0 = w.rt * C::kRows;
+            pc.two = w.x.W * a.group - pc.r0 > 128;
+            pc.j0 = w.j0;
+            pc.tiles = w.tiles();
+            pc.whole = w.whole();
+            // a CTA's first piece has its first slot, its last one the second
+            pc.slot = 2 * blockIdx.x + (seg > 0);
+            began |= begin_join(a, w, *start, pc.slot);
+          }
+          mbar_arrive(&piece_full[pi]);
+        }
+        __syncwarp();
+      }
+      if (a.join && lane == 0 && !began) a.join[blockIdx.x].parts = 0;
+    }
+  } else if (FP8 && warp >= C::kConvWarp0) {
+    // ------------------------------------------------------------- V codes -> bf16, K scales
+    if constexpr (FP8) {
+      reg_dealloc<C::kRegsConv>();
+      const int t = (warp - C::kConvWarp0) * 32 + lane;
+      uint32_t n = 0;
+      for (uint32_t seg = 0;; ++seg) {
+        const uint32_t pi = seg & 1;
+        if (!warp_wait(&piece_full[pi], (seg >> 1) & 1, abort_flag) || !pieces[pi].more) break;
+        const TileList tl = pieces[pi].t;
+        const int j0 = pieces[pi].j0, nT = pieces[pi].tiles;
+        for (int j = 0; j < nT; ++j, ++n) {
+          const uint32_t pos = 2 * n + 1, st = pos % kSt, slot = n % C::kScaleSlots;
+          const int key0 = tl.tile(j0 + j) * kTile;
+          auto seen = [&](int key) { return key0 + key < tl.hi && (key0 + key >= tl.lo || key0 + key < a.sinks); };
+          // a key without a page is a row of zeros, one that no row sees may have any scale
+          auto byte_of = [&](int key, int kv) {
+            const bool has = (pages_of[slot] >> (key >> a.c.page_shift) & 1) && seen(key);
+            return has ? static_cast<uint32_t>(scales[slot * (2 * kTile) + kv * kTile + key]) : 127u;
+          };
+          mbar_wait(&sc_full[slot], (n / C::kScaleSlots) & 1, abort_flag);
+          col_s[(n % 4) * kTile + t] = a.scale_log2 * scale_of(byte_of(t, 0));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&col_full[n % 4]);
+          mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+#pragma unroll 1
+          for (int half = 0; half < kTile / kConvKeys; ++half) {
+            const uint32_t cn = n * (kTile / kConvKeys) + half, cb = cn % C::kCBuf;
+            const int key = half * kConvKeys + t % kConvKeys;
+            const uint32_t f = bf16x2_of(scale_of(byte_of(key, 1)));
+            convert_v<DH>(smem + st * C::kRaw, smem + C::kOffConv + cb * (kConvKeys * DH * 2), half, t, seen(key),
+                          [&] { if (cn >= C::kCBuf) mbar_wait(&c_free[cb], (cn / C::kCBuf - 1) & 1, abort_flag); },
+                          [&](uint2 v) { return make_uint2(mul_bf16x2(v.x, f), mul_bf16x2(v.y, f)); });
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c_full[cb]);
+          }
+          if (lane == 0) mbar_arrive(&empty[st]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&piece_free[pi]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    reg_alloc<C::kRegsSoft>();
+    const int s = (warp - 4) >> 2, quarter = warp & 3, tid = threadIdx.x & 127;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + s * 128, t_o = tmem + lane_base + kColO + s * 128;
+    uint32_t n0 = 0, ns = 0, o_seg = 0;
+    // this group's part of piece `seg`'s query rows
+    auto stage = [&](uint32_t seg) {
+      const uint32_t pi = seg & 1;
+      const RowsPiece &pc = pieces[pi];
+      if (!pc.more) return;
+      if (TWO && pc.two)
+        stage_rows<DH, FP8, 128>(a, pc, pc.r0 + s * 128, 0, smem + C::kOffQ + s * C::kQ, qs_s + pi * 256 + s * 128, tid);
+      else
+        stage_rows<DH, FP8, 64>(a, pc, pc.r0, s * 64, smem + C::kOffQ + (TWO ? 0 : pi) * C::kQ, qs_s + pi * 256, tid);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[pi]);
+    };
+    for (uint32_t seg = 0;; ++seg) {
+      const uint32_t pi = seg & 1;
+      // all of both groups go on or none does
+      if (bar_any(3, 256, !mbar_wait(&piece_full[pi], (seg >> 1) & 1, abort_flag))) break;
+      const RowsPiece &pc = pieces[pi];
+      if (!pc.more) break;
+      if (seg == 0) {
+        stage(0);
+        if constexpr (FP8) named_bar_sync(3, 256);   // the rows' powers of two
+      }
+      const TileList tl = pc.t;
+      const int nT = pc.tiles, j0 = pc.j0, rows = pc.x.W * a.group;
+      const bool two = TWO && pc.two;
+      const int r = pc.r0 + (two ? s * 128 : 0) + tid, t = r / a.group;
+      const bool live = r < rows;
+      int lo = 0, hi = 0x7fffffff;   // a row that is none masks nothing; its results go nowhere
+      if (live) visible(a, pc.x.pos + t, pc.x.L, lo, hi);
+      const float qs = FP8 ? qs_s[pi * 256 + (two ? s * 128 : 0) + tid] : 1.f;
+      const int cnt = two ? nT : s == 0 ? (nT + 1) / 2 : nT / 2;
+      float m = kNone, l = 0.f;
+      for (int k = 0; k < cnt; ++k, ++ns) {
+        const uint32_t n = n0 + (two ? k : 2 * k + s);
+        const int key0 = tl.tile(j0 + (two ? k : 2 * k + s)) * kTile;
+        const bool all_seen = key0 + kTile <= tl.hi_first && (key0 >= tl.lo_last || key0 + kTile <= a.sinks);
+        float c = a.scale_log2;
+        if constexpr (FP8) {
+          c = qs;
+          mbar_wait(&col_full[n % 4], (n / 4) & 1, abort_flag);
+        }
+        mbar_wait(&s_full[s], ns & 1, abort_flag);
+        tc_fence_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tmem_ld32(t_s + e * 32, *reinterpret_cast<uint32_t(*)[32]>(x + e * 32));
+        tmem_ld_wait();
+        if constexpr (FP8) {
+          const float4 *col = reinterpret_cast<const float4 *>(col_s + (n % 4) * kTile);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float4 f = col[e];
+            const float2 y0 = __fmul2_rn(make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), make_float2(f.x, f.y));
+            const float2 y1 = __fmul2_rn(make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), make_float2(f.z, f.w));
+            x[4 * e] = __float_as_uint(y0.x); x[4 * e + 1] = __float_as_uint(y0.y);
+            x[4 * e + 2] = __float_as_uint(y1.x); x[4 * e + 3] = __float_as_uint(y1.y);
+          }
+        }
+        if (!all_seen || c < 0.f) {
+          // a negative scale turns maxima into minima: scaled here, then as usual
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t mask = below(hi - key0 - w * 32) & (~below(lo - key0 - w * 32) | below(a.sinks - key0 - w * 32));
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float y = __uint_as_float(x[w * 32 + e]) * c;
+              x[w * 32 + e] = mask >> e & 1 ? __float_as_uint(y) : 0xff800000u;
+            }
+          }
+          c = 1.f;
+        }
+        // three-input maxima: two new scores per step and chain
+        float a0 = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), a1 = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
+#pragma unroll
+        for (int e = 4; e < 128; e += 4) {
+          a0 = fmaxf(a0, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+          a1 = fmaxf(a1, fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
+        }
+        const float mx = fmaxf(a0, a1) * c;
+        const bool move = mx > m + kLazy;
+        const float m_new = move ? mx : m;
+        if (__any_sync(0xffffffffu, move)) {
+          const float corr = move ? ex2_approx(m - m_new) : 1.f;
+          l *= corr;
+          if (k > 0) {
+            // O holds exactly the stream's tiles before this one: their MMAs
+            // were issued before this tile's scores, which are done. The
+            // whole warp rescales (1 for rows that keep their reference).
+#pragma unroll 1
+            for (int c0 = 0; c0 < DH; c0 += 32) {
+              uint32_t o[32];
+              tmem_ld32(t_o + c0, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              tmem_st32(t_o + c0, o);
+            }
+          }
+          m = m_new;
+        }
+        // P = 2^(score - reference) as bf16 pairs over the scores' first 64 columns
+        float2 acc = make_float2(0.f, 0.f);
+        const float2 cv = make_float2(c, c), mv = make_float2(-m, -m);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            const int i = h * 64 + e;
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), cv, mv);
+            const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            acc = __fadd2_rn(acc, p);
+            pk[e / 2] = pack_bf16x2(p.x, p.y);
+          }
+          tmem_st32(t_s + h * 32, pk);
+        }
+        if constexpr (!FP8) {
+          // rows of V that no query row sees may hold anything, and 0 * NaN is not 0
+          const int u = key0 + tid;
+          if ((!two || s == 0) && !(u < tl.hi && (u >= tl.lo || u < a.sinks))) {
+            const uint32_t pos = 2 * n + 1, st = pos % kSt;
+            mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+            uint8_t *sv = smem + st * C::kRaw + (tid / 8) * C::kGroup8 + (tid % 8) * 128;
+#pragma unroll
+            for (int e = 0; e < DH / 8; ++e)
+              *reinterpret_cast<uint4 *>(sv + (e / 8) * 1024 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+        }
+        tmem_st_wait();
+        l += acc.x + acc.y;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[s]);
+        if (!TWO && k == 0) {
+          // the next piece's rows, into the buffer of the last one's
+          mbar_wait(&piece_full[pi ^ 1], ((seg + 1) >> 1) & 1, abort_flag);
+          stage(seg + 1);
+        }
+      }
+      n0 += nT;
+      if (TWO || cnt == 0) {
+        // (TWO: both streams' scores are done, their rows' space is free)
+        mbar_wait(&piece_full[pi ^ 1], ((seg + 1) >> 1) & 1, abort_flag);
+        if (TWO) named_bar_sync(3, 256);
+        stage(seg + 1);
+      }
+      if (nT > 0) {
+        mbar_wait(o_full, o_seg & 1, abort_flag);
+        ++o_seg;
+        tc_fence_after();
+      }
+      // What the streams' O count for: f[0] this one's, f[1] the other's
+      // (streams with rows of their own: 1 and 0). Each group writes half of
+      // the columns of the shared rows, all columns of its own.
+      float f0 = 1.f, f1 = 0.f;
+      if (!two) {
+        if (s == 1) ml_s[tid] = make_float2(m, l);
+        named_bar_sync(3, 256);
+        if (s == 0) {
+          const float2 other = ml_s[tid];
+          const float mm = fmaxf(m, other.x);
+          f0 = cnt > 0 ? ex2_approx(m - mm) : 0.f;
+          f1 = nT > 1 ? ex2_approx(other.x - mm) : 0.f;
+          l = l * f0 + other.y * f1;
+          m = mm;
+        }
+        named_bar_sync(3, 256);
+        if (s == 0) ml_s[tid] = make_float2(f0, f1);
+        named_bar_sync(3, 256);
+        if (s == 1) {
+          const float2 f = ml_s[tid];
+          f0 = f.y;
+          f1 = f.x;
+        }
+      }
+      // final results are divided by the row's sum, which the first group has
+      const bool whole = pc.whole;
+      if (whole) {
+        float inv = l != 0.f ? 1.f / l : 0.f;
+        if (!two) {
+          named_bar_sync(3, 256);
+          if (s == 0) ml_s[tid] = make_float2(inv, 0.f);
+          named_bar_sync(3, 256);
+          inv = ml_s[tid].x;
+        }
+        f0 *= inv;
+        f1 *= inv;
+      }
+      const uint32_t t_other = tmem + lane_base + kColO + (s ^ 1) * 128;
+      const int c_begin = two ? 0 : s * (DH / 2), c_end = two ? DH : c_begin + DH / 2;
+      const size_t row = static_cast<size_t>(pc.x.q0 + t) * a.Hq + pc.h * a.group + (r - t * a.group);
+      const size_t part = static_cast<size_t>(pc.slot) * C::kRows + (two ? s * 128 : 0) + tid;
+#pragma unroll 1
+      for (int c0 = c_begin; c0 < c_end; c0 += 32) {
+        uint32_t o[32], o1[32];
+        if (nT > 0) {
+          tmem_ld32(t_o + c0, o);
+          if (!two) tmem_ld32(t_other + c0, o1);
+          tmem_ld_wait();
+        }
+        float y[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {   // an O that no tile was added to holds anything
+          y[e] = f0 != 0.f && nT > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
+          if (!two && f1 != 0.f && nT > 0) y[e] += __uint_as_float(o1[e]) * f1;
+        }
+        if constexpr (FP8) {   // converted V rows hold every four elements in the order 0, 2, 1, 3
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) { const float z = y[e + 1]; y[e + 1] = y[e + 2]; y[e + 2] = z; }
+        }
+        if (!whole) {
+          float4 *d = reinterpret_cast<float4 *>(a.part_o + part * DH + c0);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) d[e / 4] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+        } else if (live) {
+          if (a.out_fp32) {
+            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * DH + c0);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) d[e / 4] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          } else {
+            uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + row * DH + c0);
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) d[e / 8] = pack8(y + e);
+          }
+        }
+      }
+      if (two || s == 0) {
+        if (!whole) a.part_ml[part] = make_float2(m, l);
+        else if (live && a.lse) a.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (nT > 0) mbar_arrive(o_free);
+        mbar_arrive(&piece_free[pi]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(a.status, DLLM_DEV_WAIT_TIMEOUT);
+}
+
+template <int DH, bool FP8, bool TWO>
+dllm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int min_tiles, int ctas, cudaStream_t s) {
+  using C = RowsCfg<DH, FP8, TWO>;
+  auto kern = paged_rows_kernel<DH, FP8, TWO>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kBytes, s, tk, tv, a, min_tiles);
+  return e == cudaSuccess ? DLLM_OK : cuda_error(e);
+}
+
+}  // namespace
+
+dllm_status launch_paged_rows(int dh, bool fp8, int n_rows, const CUtensorMap &tk, const CUtensorMap &tv,
+                              const PagedArgs &a, int min_tiles, int ctas, cudaStream_t s) {
+  const bool two = n_rows == 256;
+  if (dh == 64) {
+    if (fp8) return two ? launch<64, true, true>(tk, tv, a, min_tiles, ctas, s) : launch<64, true, false>(tk, tv, a, min_tiles, ctas, s);
+    return two ? launch<64, false, true>(tk, tv, a, min_tiles, ctas, s) : launch<64, false, false>(tk, tv, a, min_tiles, ctas, s);
+  }
+  if (fp8) return two ? launch<128, true, true>(tk, tv, a, min_tiles, ctas, s) : launch<128, true, false>(tk, tv, a, min_tiles, ctas, s);
+  return two ? launch<128, false, true>(tk, tv, a, min_tiles, ctas, s) : launch<128, false, false>(tk, tv, a, min_tiles, ctas, s);
+}
+
+}  // namespace dllm

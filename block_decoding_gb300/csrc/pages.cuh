@@ -110,4 +110,39 @@ __device__ __forceinline__ uint32_t max_mag(const uint4 &u, uint32_t m) {
   return __vmaxu2(m, u.w & 0x7fff7fffu);
 }
 
+// Eight bf16 of a row whose largest magnitude has the bits m, scaled by a
+// power of two into (224, 448], as two e4m3 parts: hi = rn(x), lo = rn(x - hi).
+// Returns the byte of the power of two that undoes the scaling.
+__device__ __forceinline__ int split_e4m3(const uint4 &u, uint32_t m, uint2 &hi, uint2 &lo) {
+  const int byte = scale_byte(m);
+  const float f = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
+  float x[8];
+  unpack8(u, x);
+  uint32_t h[4], r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float p = x[2 * e] * f, q = x[2 * e + 1] * f;
+    const uint16_t hh = f32_to_e4m3x2(p, q);
+    const float2 b = e4m3x2_to_f32(hh);
+    h[e] = hh;
+    r[e] = f32_to_e4m3x2(p - b.x, q - b.y);
+  }
+  hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  lo = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+  return byte;
+}
+
+// Packed bf16 product, and a value that bf16 holds in both halves.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  return a;
+}
+__device__ __forceinline__ uint32_t bf16x2_of(float f) {
+  const uint32_t b = __float_as_uint(f) >> 16;
+  return b | (b << 16);
+}
+
+// The lowest n bits (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
 }  // namespace dllm

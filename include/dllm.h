@@ -527,7 +527,7 @@ dllm_status dllm_kv_read(const dllm_kv_pages *pages /* host */, dllm_bf16 *k,
  *   that multiply V are rounded to bf16 (e4m3 pages: to 9 bits or more).
  *   The same call on the same GPU gives the same bits.
  *   Supported: Hq a multiple of heads, Hq / heads <= 64; B <= 4096;
- *   left, right, sinks < 2^30.
+ *   q_rows * Hq, max_q * Hq, max_kv, left, right and sinks < 2^30.
  * dllm_paged_attn_workspace: bytes that serve this call and every call with
  * the same pages and Hq and no larger B, max_q or max_kv; 0 for an
  * unsupported shape. The contents need not be kept between calls. Calls

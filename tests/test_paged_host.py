@@ -71,6 +71,7 @@ def test_attention_refuses_bad_arguments():
     assert _attn(q_stride=248) == 1 and _attn(q_stride=260) == 1
     for name in ("left", "right", "sinks", "max_kv"):
         assert _attn(**{name: 1 << 30}) == 2
+    assert _attn(q_rows=1 << 28) == 2 and _attn(max_q=1 << 28) == 2
     assert _attn(B=0, q=None) == 0 and _attn(max_q=0, q=None) == 0 and _attn(q_rows=0, q=None) == 0
     assert bd.LIB.dllm_paged_attn(ctypes.byref(_pages()), None, None, 0, None) == 1
 
