@@ -40,7 +40,7 @@ struct RowsCfg {
   static constexpr int kThreads = 32 * (kConvWarp0 + (FP8 ? 4 : 0));
   // registers a thread: what the TMA and MMA warps and the converters do not
   // need goes to the softmax groups (the sum is the launch's)
-  static constexpr int kRegsIssue = FP8 ? 64 : 72, kRegsSoft = FP8 ? 184 : 216, kRegsConv = 80;
+  static constexpr int kRegsIssue = FP8 ? 96 : 120, kRegsSoft = FP8 ? 160 : 192, kRegsConv = 96;
   static_assert(FP8 ? kRegsIssue + 2 * kRegsSoft + kRegsConv <= 4 * 128 : kRegsIssue + 2 * kRegsSoft <= 3 * 168, "registers");
   static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);
   static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);
@@ -386,49 +386,53 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const uint32_t n = n0 + (two ? k : 2 * k + s);
         const int key0 = tl.tile(j0 + (two ? k : 2 * k + s)) * kTile;
         const bool all_seen = key0 + kTile <= tl.hi_first && (key0 >= tl.lo_last || key0 + kTile <= a.sinks);
-        float c = a.scale_log2;
+        const float c = FP8 ? qs : a.scale_log2;
         if constexpr (FP8) {
-          c = qs;
           mbar_wait(&col_full[n % 4], (n / 4) & 1, abort_flag);
         }
         mbar_wait(&s_full[s], ns & 1, abort_flag);
         tc_fence_after();
-        uint32_t x[128];
+        // The scores are read twice, 32 at a time, the next ones on their way
+        // meanwhile: for the maximum, then for P. Holding all 128 took more
+        // registers than there are, and spills share the path that feeds the MMAs.
+        const bool scaled = !all_seen || c < 0.f;   // (a negative scale turns maxima into minima)
+        const float4 *col = FP8 ? reinterpret_cast<const float4 *>(col_s + (n % 4) * kTile) : nullptr;
+        auto finish = [&](uint32_t (&x)[32], int w) {
+          if constexpr (FP8) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) tmem_ld32(t_s + e * 32, *reinterpret_cast<uint32_t(*)[32]>(x + e * 32));
-        tmem_ld_wait();
-        if constexpr (FP8) {
-          const float4 *col = reinterpret_cast<const float4 *>(col_s + (n % 4) * kTile);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float4 f = col[e];
-            const float2 y0 = __fmul2_rn(make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), make_float2(f.x, f.y));
-            const float2 y1 = __fmul2_rn(make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), make_float2(f.z, f.w));
-            x[4 * e] = __float_as_uint(y0.x); x[4 * e + 1] = __float_as_uint(y0.y);
-            x[4 * e + 2] = __float_as_uint(y1.x); x[4 * e + 3] = __float_as_uint(y1.y);
-          }
-        }
-        if (!all_seen || c < 0.f) {
-          // a negative scale turns maxima into minima: scaled here, then as usual
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t mask = below(hi - key0 - w * 32) & (~below(lo - key0 - w * 32) | below(a.sinks - key0 - w * 32));
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float y = __uint_as_float(x[w * 32 + e]) * c;
-              x[w * 32 + e] = mask >> e & 1 ? __float_as_uint(y) : 0xff800000u;
+            for (int e = 0; e < 8; ++e) {
+              const float4 f = col[w * 8 + e];
+              const float2 y0 = __fmul2_rn(make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), make_float2(f.x, f.y));
+              const float2 y1 = __fmul2_rn(make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), make_float2(f.z, f.w));
+              x[4 * e] = __float_as_uint(y0.x); x[4 * e + 1] = __float_as_uint(y0.y);
+              x[4 * e + 2] = __float_as_uint(y1.x); x[4 * e + 3] = __float_as_uint(y1.y);
             }
           }
-          c = 1.f;
-        }
-        // three-input maxima: two new scores per step and chain
-        float a0 = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), a1 = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
+          if (scaled) {
+            const uint32_t mask = below(hi - key0 - w * 32) & (~below(lo - key0 - w * 32) | below(a.sinks - key0 - w * 32));
 #pragma unroll
-        for (int e = 4; e < 128; e += 4) {
-          a0 = fmaxf(a0, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-          a1 = fmaxf(a1, fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
+            for (int e = 0; e < 32; ++e)
+              x[e] = mask >> e & 1 ? __float_as_uint(__uint_as_float(x[e]) * c) : 0xff800000u;
+          }
+        };
+        uint32_t xs[2][32];
+        tmem_ld32(t_s, xs[0]);
+        tmem_ld_wait();
+        float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          tmem_ld32(t_s + (w + 1) % 4 * 32, xs[(w + 1) & 1]);   // at the end: the first ones again
+          uint32_t(&x)[32] = xs[w & 1];
+          finish(x, w);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {   // three-input maxima
+            a0 = fmaxf(a0, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+            a1 = fmaxf(a1, fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
+          }
+          tmem_ld_wait();
         }
-        const float mx = fmaxf(a0, a1) * c;
+        const float c1 = scaled ? 1.f : c;   // what is still to be multiplied
+        const float mx = fmaxf(a0, a1) * c1;
         const bool move = mx > m + kLazy;
         const float m_new = move ? mx : m;
         if (__any_sync(0xffffffffu, move)) {
@@ -452,19 +456,22 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         // P = 2^(score - reference) as bf16 pairs over the scores' first 64 columns
         float2 acc = make_float2(0.f, 0.f);
-        const float2 cv = make_float2(c, c), mv = make_float2(-m, -m);
+        const float2 cv = make_float2(c1, c1), mv = make_float2(-m, -m);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
+        for (int w = 0; w < 4; ++w) {
+          if (w < 3) tmem_ld32(t_s + (w + 1) * 32, xs[(w + 1) & 1]);
+          uint32_t(&x)[32] = xs[w & 1];
+          finish(x, w);
+          uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            const int i = h * 64 + e;
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), cv, mv);
+          for (int e = 0; e < 32; e += 2) {
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cv, mv);
             const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
             acc = __fadd2_rn(acc, p);
             pk[e / 2] = pack_bf16x2(p.x, p.y);
           }
-          tmem_st32(t_s + h * 32, pk);
+          if (w < 3) tmem_ld_wait();
+          tmem_st16(t_s + w * 16, pk);   // over scores that both passes have read
         }
         if constexpr (!FP8) {
           // rows of V that no query row sees may hold anything, and 0 * NaN is not 0
