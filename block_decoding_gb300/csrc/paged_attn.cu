@@ -666,6 +666,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
   const JoinJob job = a.join[blockIdx.x];
   const int n = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (job.parts == 0 || n >= n_rows || job.r0 + n >= job.rows) return;
+  const int c = lane * kVec;
   float m = -INFINITY, l = 0.f, o[kVec] = {};
   for (int p0 = 0; p0 < job.parts; p0 += kAhead) {
     float2 ml[kAhead];
@@ -673,10 +674,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int p = p0 + k;
-      const size_t at = static_cast<size_t>(p == 0 ? job.slot : 2 * (blockIdx.x + p)) * n_rows + n;
+      const size_t slot = static_cast<size_t>(p == 0 ? job.slot : 2 * (blockIdx.x + p)) * n_rows;
       if (p < job.parts) {
-        ml[k] = a.part_ml[at];
-        y[k] = reinterpret_cast<const Vec *>(a.part_o + at * DH)[lane];
+        ml[k] = a.part_ml[slot + n];
+        // [slot][row][DH], and of many rows [slot][DH / 4][row][4]
+        y[k] = *reinterpret_cast<const Vec *>(a.part_o + slot * DH + (n_rows <= 32 ? n * DH + c : (c / 4 * n_rows + n) * 4 + c % 4));
       }
     }
 #pragma unroll

@@ -21,8 +21,12 @@
 //   last four   (e4m3 pages) V codes -> bf16 with the scale folded in (a
 //               power of two: exact), and the K scales of the scores' columns
 // TMEM (512 columns): S / P of stream s at 128 s, O at 256 + 128 s.
-// A row's reference maximum moves only when its maximum passes it by more
-// than 2^8; the row's O is then rescaled in TMEM.
+// P is taken against a reference maximum of the row in one pass over the
+// scores. P is bf16 and has the range of fp32, so the reference need not be
+// the maximum: it follows, from the next tile on, when scores passed it by
+// more than 2^8 (the row's O is then rescaled in TMEM), and at once when they
+// did by more than 2^32, as on a row's first keys. P V of a tile's first 64
+// keys starts while the exponentials of the other 64 run.
 // e4m3 pages: K codes and the query rows as in paged_attn.cu (two e4m3 parts
 // of the rows); the scores' columns are multiplied by scale * K scale.
 #include "paged.cuh"
@@ -31,7 +35,23 @@ namespace dllm {
 
 namespace {
 
+// Largest of 64 values, as four chains of three-input maxima.
+__device__ __forceinline__ float greatest(const uint32_t (&a)[32], const uint32_t (&b)[32]) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      m[i] = fmaxf(m[i], fmaxf(__uint_as_float(a[e + 2 * i]), __uint_as_float(a[e + 2 * i + 1])));
+      m[2 + i] = fmaxf(m[2 + i], fmaxf(__uint_as_float(b[e + 2 * i]), __uint_as_float(b[e + 2 * i + 1])));
+    }
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
 constexpr uint32_t kColO = 256;
+constexpr int kAhead = 4;        // pieces prepared, this one included
+constexpr float kJump = 32.f;    // a reference moves at once when a score passes it by more than 2^32
 
 template <int DH, bool FP8, bool TWO>
 struct RowsCfg {
@@ -46,19 +66,20 @@ struct RowsCfg {
   static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);
   static constexpr int kVGroup8 = 8 * DH * 2;
   static constexpr int kQ = 128 * DH * 2;                     // 128 rows: bf16, or two e4m3 parts
+  static constexpr int kQs = TWO ? 2 : 1;
   static constexpr int kCBuf = FP8 ? 4 : 0;                   // converted V pieces: two tiles
   static constexpr int kConv = kCBuf * kConvKeys * DH * 2;
   static constexpr int kScaleBytes = FP8 ? 8192 : 0;          // scale bytes, column factors, row factors
   static constexpr int kMisc = 1984 + kScaleBytes;            // + 1024 of alignment
-  static constexpr int kMax = (232448 - 1024 - 2 * kQ - kConv - kMisc) / kRaw;
-  static constexpr int kCap = 196608 / kRaw;                  // 192 KB in flight are enough
+  static constexpr int kMax = (232448 - 1024 - kQs * kQ - kConv - kMisc) / kRaw;
+  static constexpr int kCap = 196608 / kRaw < 12 ? 196608 / kRaw : 12;   // 192 KB in flight are enough
   static constexpr int kStages = (kMax < kCap ? kMax : kCap) & (FP8 ? ~1 : ~0);
   static constexpr int kScaleSlots = FP8 ? kStages / 2 + 3 : 0;
   static constexpr int kOffConv = kStages * kRaw;
   static constexpr int kOffQ = kOffConv + kConv;
-  static constexpr int kOffMisc = kOffQ + 2 * kQ;
+  static constexpr int kOffMisc = kOffQ + kQs * kQ;
   static constexpr int kBytes = kOffMisc + kMisc + 1024;
-  static_assert(kStages >= 4 && kBytes <= 232448, "shared memory");
+  static_assert(kConvKeys * 2 == kTile && kStages >= 4 && kBytes <= 232448, "shared memory");
 };
 
 struct alignas(16) RowsPiece {
@@ -78,7 +99,7 @@ __device__ __forceinline__ void stage_rows(const PagedArgs &a, const RowsPiece &
                                            int tid) {
   const int rows = pc.x.W * a.group;
   constexpr int kChunks = DH / 8;
-#pragma unroll 4
+#pragma unroll 8
   for (int idx = tid; idx < CNT * kChunks; idx += 128) {
     const int n = n0 + idx / kChunks, c = idx % kChunks;
     const int r = r0 + n, t = r / a.group, g = r - t * a.group;
@@ -112,22 +133,23 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *misc = smem + C::kOffMisc;
-  RowsPiece *pieces = reinterpret_cast<RowsPiece *>(misc);                // [2]: this one and the next one
-  float2 *ml_s = reinterpret_cast<float2 *>(pieces + 2);                  // [128] maxima and sums to merge
+  RowsPiece *pieces = reinterpret_cast<RowsPiece *>(misc);                // [kAhead]
+  float2 *ml_s = reinterpret_cast<float2 *>(pieces + kAhead);                  // [128] maxima and sums to merge
   uint64_t *full = reinterpret_cast<uint64_t *>(ml_s + 128);              // [kSt] stage loaded
   uint64_t *empty = full + kSt;             // [kSt] stage read by its MMAs (or converted)
   uint64_t *s_full = empty + kSt;           // [stream]
-  uint64_t *p_full = s_full + 2;            // [stream]
-  uint64_t *piece_full = p_full + 2;        // [2]
-  uint64_t *piece_free = piece_full + 2;    // [2]
-  uint64_t *q_full = piece_free + 2;        // [2] query rows staged
-  uint64_t *o_full = q_full + 2;
+  uint64_t *p_full = s_full + 2;            // [stream][half]
+  uint64_t *h_done = p_full + 4;            // [stream] P V of the first half done
+  uint64_t *piece_full = h_done + 2;        // [kAhead]
+  uint64_t *piece_free = piece_full + kAhead;   // [kAhead]
+  uint64_t *q_full = piece_free + kAhead;   // [kAhead] query rows staged
+  uint64_t *o_full = q_full + kAhead;
   uint64_t *o_free = o_full + 1;
   long long *s_scan = reinterpret_cast<long long *>(o_free + 1);          // [16]
   Start *start = reinterpret_cast<Start *>(s_scan + 16);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert(2 * sizeof(RowsPiece) + 1024 + (2 * kSt + 12) * 8 + 128 + sizeof(Start) + 8 <= 1984, "piece and barriers");
+  static_assert(kAhead * sizeof(RowsPiece) + 1024 + (2 * kSt + 10 + 3 * kAhead) * 8 + 128 + sizeof(Start) + 8 <= 1984, "piece and barriers");
   // e4m3 pages
   uint8_t *scales = misc + 1984;                                          // [kScaleSlots][K, V][kTile]
   float *col_s = reinterpret_cast<float *>(scales + C::kScaleSlots * 2 * kTile);   // [4][kTile] score factors of a tile's keys
@@ -148,9 +170,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], FP8 && (s & 1) ? 4 : 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], 4);
+    for (int b = 0; b < 2; ++b) { mbar_init(&s_full[b], 1); mbar_init(&h_done[b], 1); }
+    for (int b = 0; b < 4; ++b) mbar_init(&p_full[b], 4);
+    for (int b = 0; b < kAhead; ++b) {
       mbar_init(&piece_full[b], 1);
       mbar_init(&piece_free[b], 8 + 1 + (FP8 ? 4 : 0));   // the warps that read it
       mbar_init(&q_full[b], 8);
@@ -189,13 +211,13 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       uint32_t n0 = 0, o_seg = 0, cnt[2] = {0, 0};   // tiles and streams' tiles before this piece
       bool ok = true;
       for (uint32_t seg = 0; ok; ++seg) {
-        const uint32_t pi = seg & 1;
-        ok = warp_wait(&piece_full[pi], (seg >> 1) & 1, abort_flag);
+        const uint32_t pi = seg % kAhead;
+        ok = warp_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
         if (!ok || !pieces[pi].more) break;
         const int nT = pieces[pi].tiles;
         const bool two = TWO && pieces[pi].two;
         const int n_s[2] = {two ? nT : (nT + 1) / 2, two ? nT : nT / 2};
-        ok = warp_wait(&q_full[pi], (seg >> 1) & 1, abort_flag);
+        ok = warp_wait(&q_full[pi], (seg / kAhead) & 1, abort_flag);
         // scores of stream s's k-th tile
         auto scores = [&](int s, int k) {
           const uint32_t n = n0 + (two ? k : 2 * k + s), pos = 2 * n, st = pos % kSt;
@@ -203,7 +225,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           tc_fence_after();
           if (ok && elect_one()) {
             const uint32_t sk = smem_u32(smem + st * C::kRaw), t_s = tmem + s * 128;
-            const uint32_t sq = smem_u32(smem + C::kOffQ + (TWO ? (two ? s : 0) : pi) * C::kQ);
+            const uint32_t sq = smem_u32(smem + C::kOffQ + (two ? s : 0) * C::kQ);
             if constexpr (!FP8) {
               const uint64_t dq = sw128_desc(sq, 16, 1024), dk = sw128_desc(sk, 16, C::kGroup8);
 #pragma unroll
@@ -230,23 +252,25 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         auto values = [&](int s, int k) {
           const uint32_t n = n0 + (two ? k : 2 * k + s), pos = 2 * n + 1, st = pos % kSt;
           const uint32_t ns = cnt[s] + k;
-          ok = ok && warp_wait(&p_full[s], ns & 1, abort_flag);
           if (k == 0 && s == 0 && o_seg > 0) ok = ok && warp_wait(o_free, (o_seg - 1) & 1, abort_flag);
           if constexpr (!FP8) ok = ok && warp_wait(&full[st], (pos / kSt) & 1, abort_flag);
-          constexpr int kPieces = FP8 ? kTile / kConvKeys : 1, kSteps = 8 / kPieces;
 #pragma unroll
-          for (int piece = 0; piece < kPieces; ++piece) {
-            const uint32_t cn = n * kPieces + piece, cb = FP8 ? cn % (C::kCBuf + !FP8) : 0;
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && warp_wait(&p_full[s * 2 + half], ns & 1, abort_flag);
+            const uint32_t cn = 2 * n + half, cb = FP8 ? cn % (C::kCBuf + !FP8) : 0;
             if constexpr (FP8) ok = ok && warp_wait(&c_full[cb], (cn / C::kCBuf) & 1, abort_flag);
             tc_fence_after();
             if (ok && elect_one()) {
-              const uint32_t sv = smem_u32(FP8 ? smem + C::kOffConv + cb * (kConvKeys * DH * 2) : smem + st * C::kRaw);
+              const uint32_t sv = smem_u32(FP8 ? smem + C::kOffConv + cb * (kConvKeys * DH * 2)
+                                               : smem + st * C::kRaw + half * 8 * C::kVGroup8);
               const uint64_t dv = sw128_desc(sv, 1024, C::kVGroup8);
 #pragma unroll
-              for (int kk = 0; kk < kSteps; ++kk)
-                umma_bf16_tmem_a(tmem + kColO + s * 128, tmem + s * 128 + (piece * kSteps + kk) * 8,
-                                 dv + ((kk * 2 * C::kVGroup8) >> 4), idesc_bf16(128, DH, 0, 1), k > 0 || piece + kk > 0);
-              if (!two || s == 1) umma_commit(FP8 ? &c_free[cb] : &empty[st]);
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16_tmem_a(tmem + kColO + s * 128, tmem + s * 128 + (half * 4 + kk) * 8,
+                                 dv + ((kk * 2 * C::kVGroup8) >> 4), idesc_bf16(128, DH, 0, 1), k > 0 || half + kk > 0);
+              if (half == 0) umma_commit(&h_done[s]);
+              if (FP8 && (!two || s == 1)) umma_commit(&c_free[cb]);
+              if (!FP8 && half == 1 && (!two || s == 1)) umma_commit(&empty[st]);
             }
             __syncwarp();
           }
@@ -274,8 +298,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       Walk w(a, C::kRows, *start);
       bool more = true, began = false;
       for (uint32_t seg = 0; more; ++seg) {
-        const uint32_t pi = seg & 1;
-        if (seg >= 2 && !warp_wait(&piece_free[pi], ((seg >> 1) - 1) & 1, abort_flag)) break;
+        const uint32_t pi = seg % kAhead;
+        if (seg >= kAhead && !warp_wait(&piece_free[pi], (seg / kAhead - 1) & 1, abort_flag)) break;
         more = w.next();
         if (lane == 0) {
           RowsPiece &pc = pieces[pi];
@@ -296,6 +320,14 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           mbar_arrive(&piece_full[pi]);
         }
         __syncwarp();
+        if (more) {   // its rows on their way to L2
+          const int rows = w.x.W * a.group;
+          for (int idx = lane; idx < C::kRows * (DH / 64); idx += 32) {
+            const int r = w.rt * C::kRows + idx / (DH / 64), t = r / a.group;
+            if (r >= rows) break;
+            l2_prefetch_line(a.q + (w.x.q0 + t) * a.q_stride + (w.h * a.group + r - t * a.group) * DH + idx % (DH / 64) * 64);
+          }
+        }
       }
       if (a.join && lane == 0 && !began) a.join[blockIdx.x].parts = 0;
     }
@@ -306,8 +338,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const int t = (warp - C::kConvWarp0) * 32 + lane;
       uint32_t n = 0;
       for (uint32_t seg = 0;; ++seg) {
-        const uint32_t pi = seg & 1;
-        if (!warp_wait(&piece_full[pi], (seg >> 1) & 1, abort_flag) || !pieces[pi].more) break;
+        const uint32_t pi = seg % kAhead;
+        if (!warp_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag) || !pieces[pi].more) break;
         const TileList tl = pieces[pi].t;
         const int j0 = pieces[pi].j0, nT = pieces[pi].tiles;
         for (int j = 0; j < nT; ++j, ++n) {
@@ -351,21 +383,23 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     uint32_t n0 = 0, ns = 0, o_seg = 0;
     // this group's part of piece `seg`'s query rows
     auto stage = [&](uint32_t seg) {
-      const uint32_t pi = seg & 1;
+      const uint32_t pi = seg % kAhead;
+      mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
       const RowsPiece &pc = pieces[pi];
       if (!pc.more) return;
+      float *qs = qs_s + (seg & 1) * 256;
       if (TWO && pc.two)
-        stage_rows<DH, FP8, 128>(a, pc, pc.r0 + s * 128, 0, smem + C::kOffQ + s * C::kQ, qs_s + pi * 256 + s * 128, tid);
+        stage_rows<DH, FP8, 128>(a, pc, pc.r0 + s * 128, 0, smem + C::kOffQ + s * C::kQ, qs + s * 128, tid);
       else
-        stage_rows<DH, FP8, 64>(a, pc, pc.r0, s * 64, smem + C::kOffQ + (TWO ? 0 : pi) * C::kQ, qs_s + pi * 256, tid);
+        stage_rows<DH, FP8, 64>(a, pc, pc.r0, s * 64, smem + C::kOffQ, qs, tid);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[pi]);
     };
     for (uint32_t seg = 0;; ++seg) {
-      const uint32_t pi = seg & 1;
+      const uint32_t pi = seg % kAhead;
       // all of both groups go on or none does
-      if (bar_any(3, 256, !mbar_wait(&piece_full[pi], (seg >> 1) & 1, abort_flag))) break;
+      if (bar_any(3, 256, !mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag))) break;
       const RowsPiece &pc = pieces[pi];
       if (!pc.more) break;
       if (seg == 0) {
@@ -376,103 +410,31 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const int nT = pc.tiles, j0 = pc.j0, rows = pc.x.W * a.group;
       const bool two = TWO && pc.two;
       const int r = pc.r0 + (two ? s * 128 : 0) + tid, t = r / a.group;
-      const bool live = r < rows;
       int lo = 0, hi = 0x7fffffff;   // a row that is none masks nothing; its results go nowhere
-      if (live) visible(a, pc.x.pos + t, pc.x.L, lo, hi);
-      const float qs = FP8 ? qs_s[pi * 256 + (two ? s * 128 : 0) + tid] : 1.f;
+      if (r < rows) visible(a, pc.x.pos + t, pc.x.L, lo, hi);
+      const float qs = FP8 ? qs_s[(seg & 1) * 256 + (two ? s * 128 : 0) + tid] : 1.f;
       const int cnt = two ? nT : s == 0 ? (nT + 1) / 2 : nT / 2;
-      float m = kNone, l = 0.f;
+      // every row's O times its factor, by the whole warp (tcgen05.ld / st)
+      auto rescale = [&](float corr) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < DH; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(t_o + c0, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+          tmem_st32(t_o + c0, o);
+        }
+        tmem_st_wait();
+      };
+      // m: the row's reference, l: its sum, top: how far scores have passed the reference
+      float m = kNone, l = 0.f, top = -INFINITY;
       for (int k = 0; k < cnt; ++k, ++ns) {
         const uint32_t n = n0 + (two ? k : 2 * k + s);
         const int key0 = tl.tile(j0 + (two ? k : 2 * k + s)) * kTile;
-        const bool all_seen = key0 + kTile <= tl.hi_first && (key0 >= tl.lo_last || key0 + kTile <= a.sinks);
+        const bool masked = !(key0 + kTile <= tl.hi_first && (key0 >= tl.lo_last || key0 + kTile <= a.sinks));
         const float c = FP8 ? qs : a.scale_log2;
-        if constexpr (FP8) {
-          mbar_wait(&col_full[n % 4], (n / 4) & 1, abort_flag);
-        }
-        mbar_wait(&s_full[s], ns & 1, abort_flag);
-        tc_fence_after();
-        // The scores are read twice, 32 at a time, the next ones on their way
-        // meanwhile: for the maximum, then for P. Holding all 128 took more
-        // registers than there are, and spills share the path that feeds the MMAs.
-        const bool scaled = !all_seen || c < 0.f;   // (a negative scale turns maxima into minima)
-        const float4 *col = FP8 ? reinterpret_cast<const float4 *>(col_s + (n % 4) * kTile) : nullptr;
-        auto finish = [&](uint32_t (&x)[32], int w) {
-          if constexpr (FP8) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 f = col[w * 8 + e];
-              const float2 y0 = __fmul2_rn(make_float2(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), make_float2(f.x, f.y));
-              const float2 y1 = __fmul2_rn(make_float2(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), make_float2(f.z, f.w));
-              x[4 * e] = __float_as_uint(y0.x); x[4 * e + 1] = __float_as_uint(y0.y);
-              x[4 * e + 2] = __float_as_uint(y1.x); x[4 * e + 3] = __float_as_uint(y1.y);
-            }
-          }
-          if (scaled) {
-            const uint32_t mask = below(hi - key0 - w * 32) & (~below(lo - key0 - w * 32) | below(a.sinks - key0 - w * 32));
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              x[e] = mask >> e & 1 ? __float_as_uint(__uint_as_float(x[e]) * c) : 0xff800000u;
-          }
-        };
-        uint32_t xs[2][32];
-        tmem_ld32(t_s, xs[0]);
-        tmem_ld_wait();
-        float a0 = -INFINITY, a1 = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          tmem_ld32(t_s + (w + 1) % 4 * 32, xs[(w + 1) & 1]);   // at the end: the first ones again
-          uint32_t(&x)[32] = xs[w & 1];
-          finish(x, w);
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {   // three-input maxima
-            a0 = fmaxf(a0, fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
-            a1 = fmaxf(a1, fmaxf(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])));
-          }
-          tmem_ld_wait();
-        }
-        const float c1 = scaled ? 1.f : c;   // what is still to be multiplied
-        const float mx = fmaxf(a0, a1) * c1;
-        const bool move = mx > m + kLazy;
-        const float m_new = move ? mx : m;
-        if (__any_sync(0xffffffffu, move)) {
-          const float corr = move ? ex2_approx(m - m_new) : 1.f;
-          l *= corr;
-          if (k > 0) {
-            // O holds exactly the stream's tiles before this one: their MMAs
-            // were issued before this tile's scores, which are done. The
-            // whole warp rescales (1 for rows that keep their reference).
-#pragma unroll 1
-            for (int c0 = 0; c0 < DH; c0 += 32) {
-              uint32_t o[32];
-              tmem_ld32(t_o + c0, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-              tmem_st32(t_o + c0, o);
-            }
-          }
-          m = m_new;
-        }
-        // P = 2^(score - reference) as bf16 pairs over the scores' first 64 columns
-        float2 acc = make_float2(0.f, 0.f);
-        const float2 cv = make_float2(c1, c1), mv = make_float2(-m, -m);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          if (w < 3) tmem_ld32(t_s + (w + 1) * 32, xs[(w + 1) & 1]);
-          uint32_t(&x)[32] = xs[w & 1];
-          finish(x, w);
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cv, mv);
-            const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            acc = __fadd2_rn(acc, p);
-            pk[e / 2] = pack_bf16x2(p.x, p.y);
-          }
-          if (w < 3) tmem_ld_wait();
-          tmem_st16(t_s + w * 16, pk);   // over scores that both passes have read
-        }
+        if constexpr (FP8) mbar_wait(&col_full[n % 4], (n / 4) & 1, abort_flag);
         if constexpr (!FP8) {
           // rows of V that no query row sees may hold anything, and 0 * NaN is not 0
           const int u = key0 + tid;
@@ -485,25 +447,105 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               *reinterpret_cast<uint4 *>(sv + (e / 8) * 1024 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
           }
+          __syncwarp();
         }
-        tmem_st_wait();
-        l += acc.x + acc.y;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[s]);
-        if (!TWO && k == 0) {
-          // the next piece's rows, into the buffer of the last one's
-          mbar_wait(&piece_full[pi ^ 1], ((seg + 1) >> 1) & 1, abort_flag);
-          stage(seg + 1);
+        mbar_wait(&s_full[s], ns & 1, abort_flag);
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, top > kLazy)) {
+          // O holds exactly the stream's tiles before this one: their MMAs
+          // were issued before this tile's scores, which are done
+          const float corr = top > kLazy ? ex2_approx(-top) : 1.f;
+          if (top > kLazy) m += top;
+          l *= corr;
+          rescale(corr);
+        }
+        top = -INFINITY;
+        const float4 *col = FP8 ? reinterpret_cast<const float4 *>(col_s + (n % 4) * kTile) : nullptr;
+        // scores of keys 32 w .. to score * factor - ref in log2 units, -inf
+        // where the row does not see the key
+        auto relative = [&](uint32_t (&x)[32], int w, float ref) {
+          const float2 cv = make_float2(c, c), rv = make_float2(-ref, -ref);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float2 y0 = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            float2 y1 = make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+            if constexpr (FP8) {   // the keys' K scales
+              const float4 f = col[w * 8 + e / 4];
+              y0 = __fmul2_rn(y0, make_float2(f.x, f.y));
+              y1 = __fmul2_rn(y1, make_float2(f.z, f.w));
+            }
+            y0 = __ffma2_rn(y0, cv, rv);
+            y1 = __ffma2_rn(y1, cv, rv);
+            x[e] = __float_as_uint(y0.x); x[e + 1] = __float_as_uint(y0.y);
+            x[e + 2] = __float_as_uint(y1.x); x[e + 3] = __float_as_uint(y1.y);
+          }
+          if (masked) {
+            const uint32_t mask = below(hi - key0 - w * 32) & (~below(lo - key0 - w * 32) | below(a.sinks - key0 - w * 32));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(mask >> e & 1)) x[e] = 0xff800000u;
+          }
+        };
+        // 64 keys at a time: enough independent work to fill the pipes
+        // between the steps that depend on each other
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t t_h = t_s + half * 64;
+          uint32_t xa[32], xb[32];
+          tmem_ld32(t_h, xa);
+          tmem_ld32(t_h + 32, xb);
+          tmem_ld_wait();
+          relative(xa, half * 2, m);
+          relative(xb, half * 2 + 1, m);
+          float past = greatest(xa, xb);
+          if (__any_sync(0xffffffffu, past > kJump)) {
+            // new references for the rows that are far off, from these scores
+            // (they are still in TMEM); O is rescaled once it is final for
+            // what came before: P V of the first half is done
+            tmem_ld32(t_h, xa);
+            tmem_ld32(t_h + 32, xb);
+            tmem_ld_wait();
+            relative(xa, half * 2, 0.f);
+            relative(xb, half * 2 + 1, 0.f);
+            const float now = past > kJump ? greatest(xa, xb) : m;
+            const float corr = now == m ? 1.f : ex2_approx(m - now);
+            l *= corr;
+            top -= now - m;
+            m = now;
+            if (half == 1) {
+              mbar_wait(&h_done[s], ns & 1, abort_flag);
+              tc_fence_after();
+            }
+            if (half == 1 || k > 0) rescale(corr);
+            tmem_ld32(t_h, xa);
+            tmem_ld32(t_h + 32, xb);
+            tmem_ld_wait();
+            relative(xa, half * 2, m);
+            relative(xb, half * 2 + 1, m);
+            past = greatest(xa, xb);
+          }
+          top = fmaxf(top, past);
+          // P as bf16 pairs, over scores that have been read
+          float2 acc = make_float2(0.f, 0.f);
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t *x = e < 16 ? xa + 2 * e : xb + 2 * e - 32;
+            const float2 p = make_float2(ex2_approx(__uint_as_float(x[0])), ex2_approx(__uint_as_float(x[1])));
+            acc = __fadd2_rn(acc, p);
+            pk[e] = pack_bf16x2(p.x, p.y);
+          }
+          l += acc.x + acc.y;
+          tmem_st32(t_s + half * 32, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[s * 2 + half]);
         }
       }
       n0 += nT;
-      if (TWO || cnt == 0) {
-        // (TWO: both streams' scores are done, their rows' space is free)
-        mbar_wait(&piece_full[pi ^ 1], ((seg + 1) >> 1) & 1, abort_flag);
-        if (TWO) named_bar_sync(3, 256);
-        stage(seg + 1);
-      }
+      named_bar_sync(3, 256);   // both streams' scores are done, the query rows' space is free
+      stage(seg + 1);
       if (nT > 0) {
         mbar_wait(o_full, o_seg & 1, abort_flag);
         ++o_seg;
@@ -549,44 +591,45 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const uint32_t t_other = tmem + lane_base + kColO + (s ^ 1) * 128;
       const int c_begin = two ? 0 : s * (DH / 2), c_end = two ? DH : c_begin + DH / 2;
       const size_t row = static_cast<size_t>(pc.x.q0 + t) * a.Hq + pc.h * a.group + (r - t * a.group);
-      const size_t part = static_cast<size_t>(pc.slot) * C::kRows + (two ? s * 128 : 0) + tid;
+      const int rs = (two ? s * 128 : 0) + tid;   // row of the slot
 #pragma unroll 1
-      for (int c0 = c_begin; c0 < c_end; c0 += 32) {
-        uint32_t o[32], o1[32];
-        if (nT > 0) {
-          tmem_ld32(t_o + c0, o);
-          if (!two) tmem_ld32(t_other + c0, o1);
+      for (int c0 = c_begin; c0 < c_end; c0 += 16) {
+        uint32_t o[16], o1[16];
+        float y[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = o1[e] = 0;
+        if (nT > 0) {   // an O that no tile was added to holds anything
+          tmem_ld16(t_o + c0, o);
+          if (!two) tmem_ld16(t_other + c0, o1);
           tmem_ld_wait();
         }
-        float y[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {   // an O that no tile was added to holds anything
-          y[e] = f0 != 0.f && nT > 0 ? __uint_as_float(o[e]) * f0 : 0.f;
-          if (!two && f1 != 0.f && nT > 0) y[e] += __uint_as_float(o1[e]) * f1;
-        }
-        if constexpr (FP8) {   // converted V rows hold every four elements in the order 0, 2, 1, 3
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) { const float z = y[e + 1]; y[e + 1] = y[e + 2]; y[e + 2] = z; }
+        for (int e = 0; e < 16; ++e) {
+          // converted V rows hold every four elements in the order 0, 2, 1, 3
+          const int i = FP8 ? (e & ~3) | ((e & 1) << 1) | ((e >> 1) & 1) : e;
+          y[i] = f0 != 0.f ? __uint_as_float(o[e]) * f0 : 0.f;
+          if (f1 != 0.f) y[i] += __uint_as_float(o1[e]) * f1;
         }
         if (!whole) {
-          float4 *d = reinterpret_cast<float4 *>(a.part_o + part * DH + c0);
+          // [slot][DH / 4][row][4]: a warp's rows side by side
+          float4 *d = reinterpret_cast<float4 *>(a.part_o) + (static_cast<size_t>(pc.slot) * (DH / 4) + c0 / 4) * C::kRows + rs;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) d[e / 4] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-        } else if (live) {
+          for (int e = 0; e < 16; e += 4) d[e / 4 * C::kRows] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+        } else if (r < rows) {
           if (a.out_fp32) {
             float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * DH + c0);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) d[e / 4] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+            for (int e = 0; e < 16; e += 4) d[e / 4] = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
           } else {
             uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + row * DH + c0);
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) d[e / 8] = pack8(y + e);
+            d[0] = pack8(y);
+            d[1] = pack8(y + 8);
           }
         }
       }
       if (two || s == 0) {
-        if (!whole) a.part_ml[part] = make_float2(m, l);
-        else if (live && a.lse) a.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (!whole) a.part_ml[static_cast<size_t>(pc.slot) * C::kRows + rs] = make_float2(m, l);
+        else if (r < rows && a.lse) a.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       }
       tc_fence_before();
       __syncwarp();

@@ -157,6 +157,11 @@ __device__ __forceinline__ void l2_prefetch_bulk(const void *p, uint32_t bytes) 
                : "memory");
 }
 
+// The 128-byte line at p into L2.
+__device__ __forceinline__ void l2_prefetch_line(const void *p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(p)));
+}
+
 // This CTA's share of an L2 prefetch of [base, base + bytes) split evenly
 // over the grid, issued in chunks of up to 64 KB.
 __device__ __forceinline__ void l2_prefetch_share(const void *base, unsigned long long bytes) {
