@@ -57,7 +57,7 @@ struct Cfg {
   static constexpr int kThreads = 32 * (kConvWarp0 + (FP8 ? 4 : 0));
   // registers a thread: what the TMA and MMA warps and the converters do not
   // need goes to the softmax groups (the sum is the launch's)
-  static constexpr int kRegsIssue = FP8 ? 64 : 72, kRegsSoft = FP8 ? 176 : 216, kRegsConv = 96;
+  static constexpr int kRegsIssue = FP8 ? 96 : 104, kRegsSoft = FP8 ? 160 : 200, kRegsConv = 96;
   static_assert(FP8 ? kRegsIssue + 2 * kRegsSoft + kRegsConv <= 4 * 128 : kRegsIssue + 2 * kRegsSoft <= 3 * 168, "registers");
   static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);       // one K or V tile as it is cached
   static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);        // eight cached rows
@@ -157,26 +157,35 @@ __device__ __forceinline__ void stage_queries(const PagedArgs &a, const Walk &w,
   }
   constexpr int kChunks = DH / 8;                  // 16-byte chunks of a bf16 row
   constexpr int kRows = 32 / kChunks;              // rows of one round of the warp
+  constexpr int kRounds = N / kRows, kAtOnce = kRounds < 8 ? kRounds : 8;   // loads on their way before the first store
   const int c = lane % kChunks;
-#pragma unroll 8
-  for (int n = lane / kChunks; n < N; n += kRows) {
-    const int r = r0 + n, t = r / a.group, g = r - t * a.group;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (r < rows)
-      u = *reinterpret_cast<const uint4 *>(a.q + (w.x.q0 + t) * a.q_stride + (w.h * a.group + g) * DH + c * 8);
-    if constexpr (!FP8) {
-      *reinterpret_cast<uint4 *>(sq + (n / 8) * (kChunks * 128) + c * 128 + (n % 8) * 16) = u;
-    } else {
-      const uint32_t m2 = max_mag(u, 0);
-      uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll 1
+  for (int n0 = lane / kChunks; n0 < N; n0 += kRows * kAtOnce) {
+    uint4 u[kAtOnce];
 #pragma unroll
-      for (int o = kChunks / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      uint2 hi, lo;
-      const int byte = split_e4m3(u, m, hi, lo);
-      uint8_t *d = sq + (n / 8) * (DH / 16 * 128) + (c / 2) * 128 + (n % 8) * 16 + (c & 1) * 8;
-      *reinterpret_cast<uint2 *>(d) = hi;
-      *reinterpret_cast<uint2 *>(d + N * DH) = lo;
-      if (c == 0) info.scale[n] = scale_of(m < 0x7f80u ? byte : 255);   // a row with an infinity or NaN scores NaN
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int r = r0 + n0 + i * kRows, t = r / a.group, g = r - t * a.group;
+      u[i] = make_uint4(0, 0, 0, 0);
+      if (r < rows)
+        u[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + (w.x.q0 + t) * a.q_stride + (w.h * a.group + g) * DH + c * 8));
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int n = n0 + i * kRows;
+      if constexpr (!FP8) {
+        *reinterpret_cast<uint4 *>(sq + (n / 8) * (kChunks * 128) + c * 128 + (n % 8) * 16) = u[i];
+      } else {
+        const uint32_t m2 = max_mag(u[i], 0);
+        uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+        for (int o = kChunks / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        uint2 hi, lo;
+        const int byte = split_e4m3(u[i], m, hi, lo);
+        uint8_t *d = sq + (n / 8) * (DH / 16 * 128) + (c / 2) * 128 + (n % 8) * 16 + (c & 1) * 8;
+        *reinterpret_cast<uint2 *>(d) = hi;
+        *reinterpret_cast<uint2 *>(d + N * DH) = lo;
+        if (c == 0) info.scale[n] = scale_of(m < 0x7f80u ? byte : 255);   // a row with an infinity or NaN scores NaN
+      }
     }
   }
 }
@@ -263,22 +272,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                                                      abort_flag, lane);
   } else if (warp == 1) {
     // ------------------------------------------------------------- S^T MMAs
+    if (elect_one()) {
     uint32_t n = 0;
     bool ok = true;
     for (uint32_t seg = 0; ok; ++seg) {
       const uint32_t pi = seg & 1;
-      ok = warp_wait(&q_full[pi], (seg >> 1) & 1, abort_flag);
+      ok = mbar_wait(&q_full[pi], (seg >> 1) & 1, abort_flag);
       if (!ok || !pieces[pi].more) break;
       const int nT = pieces[pi].tiles;
       const uint32_t sq = smem_u32(smem + C::kOffQ + pi * C::kQ);
       for (int j = 0; j < nT; ++j, ++n) {
         const uint32_t pos = 2 * n, st = pos % kSt, b = n % kSBuf;
-        ok = warp_wait(&full[st], (pos / kSt) & 1, abort_flag);
-        if (ok && n >= kSBuf) ok = warp_wait(&s_free[b], (n / kSBuf - 1) & 1, abort_flag);
+        ok = mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+        if (ok && n >= kSBuf) ok = mbar_wait(&s_free[b], (n / kSBuf - 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         const uint32_t sk = smem_u32(smem + st * C::kRaw);
-        if (elect_one()) {
+        {
           if constexpr (!FP8) {
             const uint64_t dk = sw128_desc(sk, 16, C::kGroup8), dq = plain_desc(sq, 128, DH / 8 * 128);
 #pragma unroll
@@ -298,24 +308,26 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           umma_commit(&s_full[b]);
           umma_commit(&empty[st]);
         }
-        __syncwarp();
       }
-      if (lane == 0) mbar_arrive(&q_free[pi]);
+      mbar_arrive(&q_free[pi]);
     }
+    }
+    __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------------------- O^T MMAs
+    if (elect_one()) {
     uint32_t n = 0, o_seg = 0;
     bool ok = true;
     for (uint32_t seg = 0; ok; ++seg) {
       const uint32_t pi = seg & 1;
-      ok = warp_wait(&q_full[pi], (seg >> 1) & 1, abort_flag);
+      ok = mbar_wait(&q_full[pi], (seg >> 1) & 1, abort_flag);
       if (!ok || !pieces[pi].more) break;
       const int nT = pieces[pi].tiles;
       for (int j = 0; ok && j < nT; ++j, ++n) {
         const uint32_t pos = 2 * n + 1, st = pos % kSt, b = n % kPBuf;
-        ok = warp_wait(&p_full[b], (n / kPBuf) & 1, abort_flag);
-        if (ok && j == 0 && o_seg > 0) ok = warp_wait(o_free, (o_seg - 1) & 1, abort_flag);
-        if (ok && !FP8) ok = warp_wait(&full[st], (pos / kSt) & 1, abort_flag);
+        ok = mbar_wait(&p_full[b], (n / kPBuf) & 1, abort_flag);
+        if (ok && j == 0 && o_seg > 0) ok = mbar_wait(o_free, (o_seg - 1) & 1, abort_flag);
+        if (ok && !FP8) ok = mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
         const uint32_t t_d = kByTile ? t_o + (n & 1) * N : t_o;
         const bool first = j == 0 || (kByTile && j == 1);   // of its accumulator
         const uint64_t dp = plain_desc(smem_u32(smem + C::kOffP + b * C::kP), 128, 2048);
@@ -324,11 +336,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
         for (int piece = 0; piece < kPieces; ++piece) {
           const uint32_t cn = n * kPieces + piece, cb = cn % kCBuf;
-          if (FP8 && ok) ok = warp_wait(&c_full[cb], (cn / kCBuf) & 1, abort_flag);
+          if (FP8 && ok) ok = mbar_wait(&c_full[cb], (cn / kCBuf) & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sv = smem_u32(FP8 ? smem + C::kOffConv + cb * (kConvKeys * DH * 2) : smem + st * C::kRaw);
-          if (elect_one()) {
+          {
             const uint64_t dv = sw128_desc(sv, 1024, C::kVGroup8);
 #pragma unroll
             for (int kk = 0; kk < kSteps; ++kk)
@@ -340,12 +352,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               if (j + 1 == nT) umma_commit(o_full);
             }
           }
-          __syncwarp();
         }
       }
       o_seg += nT > 0;
-      if (lane == 0) mbar_arrive(&q_free[pi]);
+      mbar_arrive(&q_free[pi]);
     }
+    }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------- pieces and their query rows
     // One piece ahead of the others, so that its metadata and its rows are

@@ -99,27 +99,36 @@ __device__ __forceinline__ void stage_rows(const PagedArgs &a, const RowsPiece &
                                            int tid) {
   const int rows = pc.x.W * a.group;
   constexpr int kChunks = DH / 8;
-#pragma unroll 8
-  for (int idx = tid; idx < CNT * kChunks; idx += 128) {
-    const int n = n0 + idx / kChunks, c = idx % kChunks;
-    const int r = r0 + n, t = r / a.group, g = r - t * a.group;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (r < rows)
-      u = *reinterpret_cast<const uint4 *>(a.q + (pc.x.q0 + t) * a.q_stride + (pc.h * a.group + g) * DH + c * 8);
-    if constexpr (!FP8) {
-      *reinterpret_cast<uint4 *>(sq + (c / 8) * 16384 + (n / 8) * 1024 + (n % 8) * 128 + ((c % 8) ^ (n % 8)) * 16) = u;
-    } else {
-      const uint32_t m2 = max_mag(u, 0);
-      uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+  constexpr int kAtOnce = 8;   // loads on their way before the first store
+#pragma unroll 1
+  for (int i0 = tid; i0 < CNT * kChunks; i0 += 128 * kAtOnce) {
+    uint4 u[kAtOnce];
 #pragma unroll
-      for (int o = kChunks / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      uint2 hi, lo;
-      const int byte = split_e4m3(u, m, hi, lo);
-      const int sc = DH == 128 ? (c / 2) ^ (n % 8) : (c / 2) ^ ((n / 2) % 4);
-      uint8_t *d = sq + n * DH + sc * 16 + (c % 2) * 8;
-      *reinterpret_cast<uint2 *>(d) = hi;
-      *reinterpret_cast<uint2 *>(d + 128 * DH) = lo;
-      if (c == 0) qs[n] = scale_of(m < 0x7f80u ? byte : 255);   // a row with an infinity or NaN scores NaN
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int idx = i0 + i * 128, r = r0 + n0 + idx / kChunks, t = r / a.group, g = r - t * a.group;
+      u[i] = make_uint4(0, 0, 0, 0);
+      if (idx < CNT * kChunks && r < rows)
+        u[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + (pc.x.q0 + t) * a.q_stride + (pc.h * a.group + g) * DH + idx % kChunks * 8));
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int idx = i0 + i * 128, n = n0 + idx / kChunks, c = idx % kChunks;
+      if (idx >= CNT * kChunks) break;   // whole groups of 128
+      if constexpr (!FP8) {
+        *reinterpret_cast<uint4 *>(sq + (c / 8) * 16384 + (n / 8) * 1024 + (n % 8) * 128 + ((c % 8) ^ (n % 8)) * 16) = u[i];
+      } else {
+        const uint32_t m2 = max_mag(u[i], 0);
+        uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+        for (int o = kChunks / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        uint2 hi, lo;
+        const int byte = split_e4m3(u[i], m, hi, lo);
+        const int sc = DH == 128 ? (c / 2) ^ (n % 8) : (c / 2) ^ ((n / 2) % 4);
+        uint8_t *d = sq + n * DH + sc * 16 + (c % 2) * 8;
+        *reinterpret_cast<uint2 *>(d) = hi;
+        *reinterpret_cast<uint2 *>(d + 128 * DH) = lo;
+        if (c == 0) qs[n] = scale_of(m < 0x7f80u ? byte : 255);   // a row with an infinity or NaN scores NaN
+      }
     }
   }
 }
@@ -208,22 +217,25 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                                                        sc_full, abort_flag, lane);
     } else if (warp == 1) {
       // ----------------------------------------------------------- MMAs
+      // (one elected thread through the whole loop: a warp that stays
+      // together and elects around each group of MMAs took 12 % longer)
+      if (elect_one()) {
       uint32_t n0 = 0, o_seg = 0, cnt[2] = {0, 0};   // tiles and streams' tiles before this piece
       bool ok = true;
       for (uint32_t seg = 0; ok; ++seg) {
         const uint32_t pi = seg % kAhead;
-        ok = warp_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
+        ok = mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
         if (!ok || !pieces[pi].more) break;
         const int nT = pieces[pi].tiles;
         const bool two = TWO && pieces[pi].two;
         const int n_s[2] = {two ? nT : (nT + 1) / 2, two ? nT : nT / 2};
-        ok = warp_wait(&q_full[pi], (seg / kAhead) & 1, abort_flag);
+        ok = mbar_wait(&q_full[pi], (seg / kAhead) & 1, abort_flag);
         // scores of stream s's k-th tile
         auto scores = [&](int s, int k) {
           const uint32_t n = n0 + (two ? k : 2 * k + s), pos = 2 * n, st = pos % kSt;
-          ok = ok && warp_wait(&full[st], (pos / kSt) & 1, abort_flag);
+          ok = ok && mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
           tc_fence_after();
-          if (ok && elect_one()) {
+          if (ok) {
             const uint32_t sk = smem_u32(smem + st * C::kRaw), t_s = tmem + s * 128;
             const uint32_t sq = smem_u32(smem + C::kOffQ + (two ? s : 0) * C::kQ);
             if constexpr (!FP8) {
@@ -246,21 +258,20 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             umma_commit(&s_full[s]);
             if (!two || s == 1) umma_commit(&empty[st]);
           }
-          __syncwarp();
         };
         // O of stream s += P V of its k-th tile
         auto values = [&](int s, int k) {
           const uint32_t n = n0 + (two ? k : 2 * k + s), pos = 2 * n + 1, st = pos % kSt;
           const uint32_t ns = cnt[s] + k;
-          if (k == 0 && s == 0 && o_seg > 0) ok = ok && warp_wait(o_free, (o_seg - 1) & 1, abort_flag);
-          if constexpr (!FP8) ok = ok && warp_wait(&full[st], (pos / kSt) & 1, abort_flag);
+          if (k == 0 && s == 0 && o_seg > 0) ok = ok && mbar_wait(o_free, (o_seg - 1) & 1, abort_flag);
+          if constexpr (!FP8) ok = ok && mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            ok = ok && warp_wait(&p_full[s * 2 + half], ns & 1, abort_flag);
+            ok = ok && mbar_wait(&p_full[s * 2 + half], ns & 1, abort_flag);
             const uint32_t cn = 2 * n + half, cb = FP8 ? cn % (C::kCBuf + !FP8) : 0;
-            if constexpr (FP8) ok = ok && warp_wait(&c_full[cb], (cn / C::kCBuf) & 1, abort_flag);
+            if constexpr (FP8) ok = ok && mbar_wait(&c_full[cb], (cn / C::kCBuf) & 1, abort_flag);
             tc_fence_after();
-            if (ok && elect_one()) {
+            if (ok) {
               const uint32_t sv = smem_u32(FP8 ? smem + C::kOffConv + cb * (kConvKeys * DH * 2)
                                                : smem + st * C::kRaw + half * 8 * C::kVGroup8);
               const uint64_t dv = sw128_desc(sv, 1024, C::kVGroup8);
@@ -272,7 +283,6 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               if (FP8 && (!two || s == 1)) umma_commit(&c_free[cb]);
               if (!FP8 && half == 1 && (!two || s == 1)) umma_commit(&empty[st]);
             }
-            __syncwarp();
           }
         };
         if (nT > 0) {
@@ -284,15 +294,16 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             if (k < n_s[1]) values(1, k);
             if (k + 1 < n_s[1]) scores(1, k + 1);
           }
-          if (ok && elect_one()) umma_commit(o_full);
-          __syncwarp();
+          if (ok) umma_commit(o_full);
           ++o_seg;
         }
         n0 += nT;
         cnt[0] += n_s[0];
         cnt[1] += n_s[1];
-        if (lane == 0) mbar_arrive(&piece_free[pi]);
+        mbar_arrive(&piece_free[pi]);
       }
+      }
+      __syncwarp();
     } else if (warp == 3) {
       // ----------------------------------------------------------- pieces
       Walk w(a, C::kRows, *start);
