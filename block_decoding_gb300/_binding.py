@@ -516,12 +516,18 @@ class KVPages:
         if fp8 and not (k_scale.shape == k.shape[:3] and v_scale.shape == k.shape[:3]):
             raise ValueError("scales must be [num_pages][heads][page_size]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device = k.device
+        self.index = dev = k.get_device()
         self.num_pages, self.heads, self.page_size, self.dh = k.shape
         self.desc = KvPagesDesc(
-            _ptr_on(k, self.device, k.dtype, "k"), _ptr_on(v, self.device, k.dtype, "v"),
-            _ptr_on(k_scale, self.device, torch.uint8, "k_scale"), _ptr_on(v_scale, self.device, torch.uint8, "v_scale"),
+            _ptr_on(k, dev, k.dtype, "k"), _ptr_on(v, dev, k.dtype, "v"),
+            _ptr_on(k_scale, dev, torch.uint8, "k_scale") if fp8 else None,
+            _ptr_on(v_scale, dev, torch.uint8, "v_scale") if fp8 else None,
             1 if fp8 else 0, self.num_pages, self.page_size, self.heads, self.dh)
+        self._need = {}     # workspace bytes by shape
+
+    @property
+    def device(self):
+        return self.k.device
 
     @classmethod
     def empty(cls, num_pages, page_size, heads, dh, dtype=torch.bfloat16, device="cuda"):
@@ -533,51 +539,54 @@ class KVPages:
         return cls(k, v, *(torch.empty(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)))
 
 
-def _ptr_on(t, device, dtype, name):
-    """_ptr of a tensor that has to be on `device` (None stays None)."""
-    p = _ptr(t, dtype, name)
-    if t is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the pages are on {device}")
-    return p
+def _ptr_on(t, index, dtype, name):
+    """Pointer of a contiguous `dtype` tensor on GPU `index`."""
+    # one test on the way that every call goes; _ptr says what is wrong
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index >= 0 and t.is_contiguous()):
+        _ptr(t, dtype, name)
+        raise ValueError(f"{name} is on {t.device}, the pages are on GPU {index}")
+    return t.data_ptr()
 
 
-def _rows_ptr(t, device, heads, dh, name):
+def _rows_ptr(t, index, heads, dh, name):
     """(pointer, row stride) of bf16 rows [rows][heads][dh], dense within a row."""
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the pages are on {device}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dh:
-        raise ValueError(f"{name} must be [rows][{heads}][{dh}], got {tuple(t.shape)}")
-    n, s = t.shape[0], t.stride()
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the pages are on cuda:{index}")
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dh:
+        raise ValueError(f"{name} must be [rows][{heads}][{dh}], got {tuple(shape)}")
+    n, s = shape[0], t.stride()
     if n and (s[2] != 1 or (heads > 1 and s[1] != dh)):
         raise ValueError(f"{name} must be dense within a row")
     return t.data_ptr(), s[0] if n > 1 else heads * dh
 
 
-def _ragged(device, off, page_table, **per_request):
-    """(B, max_pages) after checking the ragged batch's metadata."""
-    _ptr_on(off, device, torch.int32, "offsets")
-    _ptr_on(page_table, device, torch.int32, "page_table")
+def _batch(index, off, page_table, per_request, name):
+    """(B, max_pages, pointers of off, page_table and per_request) of a ragged batch."""
+    po, pt = _ptr_on(off, index, torch.int32, "offsets"), _ptr_on(page_table, index, torch.int32, "page_table")
+    pr = _ptr_on(per_request, index, torch.int32, name)
     B = off.numel() - 1
-    if B < 0 or page_table.dim() != 2 or page_table.shape[0] != B:
+    shape = page_table.shape
+    if B < 0 or len(shape) != 2 or shape[0] != B:
         raise ValueError("page_table must be [B][max_pages] with B = offsets - 1")
-    for name, t in per_request.items():
-        if t is not None:
-            _ptr_on(t, device, torch.int32, name)
-            if t.numel() != B:
-                raise ValueError(f"{name} must have one entry per request")
-    return B, page_table.shape[1]
+    if per_request.numel() != B:
+        raise ValueError(f"{name} must have one entry per request")
+    return B, shape[1], po, pt, pr
 
 
-def _launch(device, stream, fn, *args):
-    """fn(*args, stream) with `device` current (its current stream by default)."""
-    if torch.cuda.current_device() == device.index:
-        return fn(*args, (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
-    with torch.cuda.device(device):
-        return fn(*args, (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
+def _launch(what, index, stream, *args):
+    """Call `what` with GPU `index` current, on `stream` or that GPU's current stream."""
+    fn = getattr(LIB, what)
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index))
+    _ck(rc, what)
 
 
 def _alloc(shape, dtype, device, stream):
@@ -592,36 +601,41 @@ def kv_write(pages: KVPages, k, v, off, pos0, page_table, stream=None):
     """Store rows k, v [rows][heads][dh] bf16 (any row stride) in the pages:
     row off[i] + t at position pos0[i] + t of request i. off int32 [B+1], pos0
     int32 [B], page_table int32 [B][max_pages]."""
-    dev = pages.device
+    dev = pages.index
     kp, ks = _rows_ptr(k, dev, pages.heads, pages.dh, "k")
     vp, vs = _rows_ptr(v, dev, pages.heads, pages.dh, "v")
-    if k.shape[0] != v.shape[0]:
+    rows = k.shape[0]
+    if rows != v.shape[0]:
         raise ValueError("k and v must have the same rows")
-    B, n = _ragged(dev, off, page_table, pos0=pos0)
-    _ck(_launch(dev, stream, LIB.dllm_kv_write, ctypes.byref(pages.desc), kp, vp, ks, vs, k.shape[0], off.data_ptr(),
-                pos0.data_ptr(), page_table.data_ptr(), n, B), "dllm_kv_write")
+    B, n, po, pt, pp = _batch(dev, off, page_table, pos0, "pos0")
+    _launch("dllm_kv_write", dev, stream, pages.desc, kp, vp, ks, vs, rows, po, pp, pt, n, B)
 
 
 def kv_read(pages: KVPages, off, pos0, page_table, rows, k=None, v=None, stream=None):
     """The cached rows of positions pos0[i] + t as bf16 rows off[i] + t of (k, v)
     [rows][heads][dh] (allocated unless given)."""
-    dev = pages.device
+    dev = pages.index
     shape = (int(rows), pages.heads, pages.dh)
-    k = k if k is not None else _alloc(shape, torch.bfloat16, dev, stream)
-    v = v if v is not None else _alloc(shape, torch.bfloat16, dev, stream)
-    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+    k = k if k is not None else _alloc(shape, torch.bfloat16, pages.k.device, stream)
+    v = v if v is not None else _alloc(shape, torch.bfloat16, pages.k.device, stream)
+    if k.shape != shape or v.shape != shape:
         raise ValueError(f"k and v must be {list(shape)}")
-    B, n = _ragged(dev, off, page_table, pos0=pos0)
-    _ck(_launch(dev, stream, LIB.dllm_kv_read, ctypes.byref(pages.desc), _ptr_on(k, dev, torch.bfloat16, "k"),
-                _ptr_on(v, dev, torch.bfloat16, "v"), shape[0], off.data_ptr(), pos0.data_ptr(), page_table.data_ptr(),
-                n, B), "dllm_kv_read")
+    B, n, po, pt, pp = _batch(dev, off, page_table, pos0, "pos0")
+    _launch("dllm_kv_read", dev, stream, pages.desc, _ptr_on(k, dev, torch.bfloat16, "k"),
+            _ptr_on(v, dev, torch.bfloat16, "v"), shape[0], po, pp, pt, n, B)
     return k, v
 
 
 def paged_attn_workspace(pages: KVPages, B, Hq, max_q, max_kv) -> int:
     """Workspace bytes of paged_attn for no larger B, max_q and max_kv."""
-    a = PagedAttnArgs(B=int(B), Hq=int(Hq), max_q=int(max_q), max_kv=int(max_kv))
-    return int(LIB.dllm_paged_attn_workspace(ctypes.byref(pages.desc), ctypes.byref(a)))
+    key = (int(B), int(Hq), int(max_q), int(max_kv))
+    need = pages._need.get(key)
+    if need is None:
+        a = PagedAttnArgs(B=key[0], Hq=key[1], max_q=key[2], max_kv=key[3])
+        need = int(LIB.dllm_paged_attn_workspace(ctypes.byref(pages.desc), ctypes.byref(a)))
+        if len(pages._need) < 4096:
+            pages._need[key] = need
+    return need
 
 
 def paged_attn(q, pages: KVPages, q_off, kv_len, page_table, max_q, max_kv, q_pos=None, scale=None, left=-1, right=-1,
@@ -633,29 +647,31 @@ def paged_attn(q, pages: KVPages, q_off, kv_len, page_table, max_q, max_kv, q_po
     (u >= position - left or u < sinks); negative left / right: no limit.
     Returns out [rows][Hq][dh], or (out, lse [rows][Hq]) with return_lse.
     """
-    dev = pages.device
-    Hq = q.shape[1] if q.dim() == 3 else -1
-    qp, qs = _rows_ptr(q, dev, Hq, pages.dh, "q")
-    B, n = _ragged(dev, q_off, page_table, kv_len=kv_len, q_pos=q_pos)
-    rows = q.shape[0]
+    dev, dh = pages.index, pages.dh
+    rows, Hq = (q.shape[0], q.shape[1]) if isinstance(q, torch.Tensor) and q.dim() == 3 else (0, 0)
+    qp, qs = _rows_ptr(q, dev, Hq, dh, "q")
+    B, n, po, pt, pn = _batch(dev, q_off, page_table, kv_len, "kv_len")
+    pp = None
+    if q_pos is not None:
+        pp = _ptr_on(q_pos, dev, torch.int32, "q_pos")
+        if q_pos.numel() != B:
+            raise ValueError("q_pos must have one entry per request")
     if out is None:
-        out = _alloc((rows, Hq, pages.dh), torch.float32 if out_fp32 else torch.bfloat16, dev, stream)
-    elif tuple(out.shape) != (rows, Hq, pages.dh) or out.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"out must be bf16 or fp32 [{rows}][{Hq}][{pages.dh}]")
-    if lse is None and return_lse:
-        lse = _alloc((rows, Hq), torch.float32, dev, stream)
-    elif lse is not None and tuple(lse.shape) != (rows, Hq):
+        out = _alloc((rows, Hq, dh), torch.float32 if out_fp32 else torch.bfloat16, q.device, stream)
+    elif out.shape != (rows, Hq, dh) or out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out must be bf16 or fp32 [{rows}][{Hq}][{dh}]")
+    if lse is None:
+        lse = _alloc((rows, Hq), torch.float32, q.device, stream) if return_lse else None
+    elif lse.shape != (rows, Hq):
         raise ValueError(f"lse must be [{rows}][{Hq}]")
-    a = PagedAttnArgs(qp, qs, _ptr_on(out, dev, out.dtype, "out"), 1 if out.dtype == torch.float32 else 0,
-                      _ptr_on(lse, dev, torch.float32, "lse"), q_off.data_ptr(), kv_len.data_ptr(),
-                      q_pos.data_ptr() if q_pos is not None else None, page_table.data_ptr(), n, B, Hq, int(max_q),
-                      int(max_kv), rows, float(scale if scale is not None else 1.0 / math.sqrt(pages.dh)), int(left),
+    a = PagedAttnArgs(qp, qs, _ptr_on(out, dev, out.dtype, "out"), 1 if out.dtype is torch.float32 else 0,
+                      None if lse is None else _ptr_on(lse, dev, torch.float32, "lse"), po, pn, pp, pt, n, B, Hq,
+                      int(max_q), int(max_kv), rows, 1.0 / math.sqrt(dh) if scale is None else float(scale), int(left),
                       int(right), int(sinks))
     if ws is None:
-        need = int(LIB.dllm_paged_attn_workspace(ctypes.byref(pages.desc), ctypes.byref(a)))
+        need = paged_attn_workspace(pages, B, Hq, max_q, max_kv)
         if need:
-            ws = _alloc(need, torch.uint8, dev, stream)
-    _ck(_launch(dev, stream, LIB.dllm_paged_attn, ctypes.byref(pages.desc), ctypes.byref(a),
-                _ptr_on(ws, dev, None, "ws"), ws.numel() * ws.element_size() if ws is not None else 0),
-        "dllm_paged_attn")
+            ws = _alloc(need, torch.uint8, q.device, stream)
+    _launch("dllm_paged_attn", dev, stream, pages.desc, a, None if ws is None else _ptr_on(ws, dev, ws.dtype, "ws"),
+            0 if ws is None else ws.numel() * ws.element_size())
     return (out, lse) if return_lse else out

@@ -223,6 +223,16 @@ __device__ __forceinline__ bool begin_join(const PagedArgs &a, const Walk &w, co
   return true;
 }
 
+// The query rows of the piece `w` on their way to L2, by one warp.
+__device__ __forceinline__ void prefetch_rows(const PagedArgs &a, const Walk &w, int n_rows, int dh, int lane) {
+  const int rows = w.x.W * a.group, lines = dh / 64;   // 128-byte lines of a row
+  for (int idx = lane; idx < n_rows * lines; idx += 32) {
+    const int r = w.rt * n_rows + idx / lines, t = r / a.group;
+    if (r >= rows) break;
+    l2_prefetch_line(a.q + (w.x.q0 + t) * a.q_stride + (w.h * a.group + r - t * a.group) * dh + idx % lines * 64);
+  }
+}
+
 // The warp that loads the K and V tiles of a CTA's pieces into one ring of
 // SLOTS stages, K tiles in the even ones: one box per page and tile. With
 // e4m3 pages (SCALES > 0) a tile's scale bytes, K's then V's, go to a ring of
@@ -323,7 +333,8 @@ __device__ __forceinline__ void convert_v(const uint8_t *raw, uint8_t *dst, int 
   }
 }
 
-constexpr int kMinTiles = 2;     // fewest tiles a CTA is given: each piece costs a prologue and a join
+constexpr int kMinTiles = 4;     // fewest tiles a CTA is given: each piece costs a prologue and a join
+constexpr int kWholeTiles = 4;   // items of no more tiles are not divided
 constexpr int kMaxCtas = 192;    // bound of the workspace, above any GB300's SM count
 constexpr int kConvKeys = 64;    // keys of one converted V piece
 constexpr float kLazy = 8.f;     // a reference maximum moves when a score passes it by more than 2^8

@@ -1,14 +1,15 @@
 // Attention of new tokens over the paged K/V cache (bf16 or e4m3 pages):
 // grouped query heads, causal or bidirectional, sliding window with the
-// first tokens visible.
+// first tokens visible. This kernel takes up to 32 query rows per request and
+// cached head (paged_rows.cu takes more), and joins divided items of both.
 //
 // The work of one (request, cached head) is S^T = K Q^T over the head's
 // cached rows, with the query rows that share the head (W rows x group heads)
 // as N. Keys are the M = 128 rows of the tensor-core tile, so N is as small
-// as the rows are (16, 32 or 64): a single token costs a tile of 16, not of
-// 128, the exponentials of one key tile spread over 128 threads (one key
-// each, whatever N is), and a key's scales and visibility are one thread's
-// scalars. O^T = V^T P^T accumulates in TMEM.
+// as the rows are (16 or 32): a single token costs a tile of 16, not of 128,
+// the exponentials of one key tile spread over 128 threads (one key each,
+// whatever N is), and a key's scales and visibility are one thread's scalars.
+// O^T = V^T P^T accumulates in TMEM.
 //
 // The key tiles of all (request, head, row tile) items form one line that is
 // cut into equal pieces, one per CTA: long and short requests balance, and a
@@ -20,18 +21,25 @@
 //   warp 0      TMA: one box per page and tile; K and V tiles alternate in one ring
 //   warp 1      S^T MMAs: K tile (A) x query rows (B) into an S buffer
 //   warp 2      O^T MMAs: V tile (A, transposed by its descriptor) x P (B)
-//   warps 4..11 two softmax warpgroups, one key per thread
-//   last four   (e4m3 pages) V codes -> bf16, 64 keys at a time
+//   warp 3      walks the CTA's pieces ahead of the others
+//   warps 4..11 two softmax warpgroups, one key per thread, on alternate key
+//               tiles, each with references, sums and an O of its own that are
+//               merged at the end: the steps of one tile depend on each other,
+//               and two tiles under way hide that. They also stage the rows.
 // A reference maximum per row moves only when a score passes it by more than
-// 2^8 (P is bf16: no precision is lost), so most tiles need no maximum at
-// all, only the vote that nobody passed it.
+// 2^kLazy, so most tiles need no maximum at all, only the vote that nobody
+// passed it.
 //
-// e4m3 pages: K codes go to the tensor cores as they are, against the query
-// rows split into two e4m3 parts (high + low: exact for elements within 2^-10
-// of the row's largest, else 2^-19 of that off), and the key's scale is a
-// factor of its thread's scores. V codes become bf16, which holds them
-// exactly, and the scale enters P before its one rounding to bf16, so tail
-// weights keep their relative precision however small they are.
+// e4m3 pages: K and V codes go to the tensor cores as they are.
+//   Scores: the query rows are split into two e4m3 parts (high + low: exact
+//   for elements within 2^-10 of the row's largest, else 2^-19 of that off),
+//   and the key's scale is a factor of its thread's scores.
+//   Weights: P times the V scale, relative to the largest V scale so far, is
+//   split into three e5m2 parts (9 bits together). e5m2 spans 2^32; weights
+//   below 2^-10 go, 2^12 times larger, to accumulator columns of their own,
+//   so that weights keep 9 bits down to 2^-30 of the largest and err by 2^-42
+//   of it below. (Codes converted to bf16 by four more warps, with P in bf16:
+//   the conversion took 1.9 k cycles a tile, the loads of a tile 1.4 k.)
 #include <type_traits>
 
 #include "paged.cuh"
@@ -42,60 +50,53 @@ DLLM_DEFINE_STATUS(paged)
 
 namespace {
 
-constexpr int kPBuf = 2, kCBuf = 2;
+constexpr int kPBuf = 2;         // one per softmax group
+constexpr int kSBuf = 4;
+constexpr int kAhead = 4;        // pieces prepared, the current one included
 
 template <int DH, bool FP8, int N>
 struct Cfg {
-  // Two softmax warpgroups. With up to 32 columns they take every other key
-  // tile (each with its own references, sums and O, merged at the end): the
-  // steps of one tile depend on each other, and two tiles under way hide
-  // that. With 64 columns each takes 32 of them, of every tile.
-  static constexpr bool kByTile = N <= 32;
-  static constexpr int kCols = kByTile ? N : N / 2;             // columns of one group
-  static constexpr int kSBuf = kByTile ? 4 : 3;
-  static constexpr int kConvWarp0 = 12;
-  static constexpr int kThreads = 32 * (kConvWarp0 + (FP8 ? 4 : 0));
-  // registers a thread: what the TMA and MMA warps and the converters do not
-  // need goes to the softmax groups (the sum is the launch's)
-  static constexpr int kRegsIssue = FP8 ? 96 : 104, kRegsSoft = FP8 ? 160 : 200, kRegsConv = 96;
-  static_assert(FP8 ? kRegsIssue + 2 * kRegsSoft + kRegsConv <= 4 * 128 : kRegsIssue + 2 * kRegsSoft <= 3 * 168, "registers");
-  static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);       // one K or V tile as it is cached
+  static constexpr int kThreads = 32 * 12;
+  // registers a thread: what the TMA and MMA warps do not need goes to the
+  // softmax groups (the sum is the launch's)
+  static constexpr int kRegsIssue = 104, kRegsSoft = 200;
+  static_assert(kRegsIssue + 2 * kRegsSoft <= 3 * 168, "registers");
+  static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);       // one K or V tile
   static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);        // eight cached rows
-  static constexpr int kVGroup8 = 8 * DH * 2;                   // eight bf16 rows of V
-  static constexpr int kP = kTile * N * 2;
+  static constexpr int kO = FP8 ? 2 * N : N;                    // columns of a group's O, and of a part of P
+  static constexpr int kPart = kTile * kO * (FP8 ? 1 : 2);
+  static constexpr int kP = kPart * (FP8 ? 3 : 1);
   static constexpr int kQ = N * DH * 2;                         // bf16, or two e4m3 parts
-  static constexpr int kConv = FP8 ? kCBuf * kConvKeys * DH * 2 : 0;
   static constexpr int kMisc = FP8 ? 12288 : 8192;              // row tables, scales, barriers, alignment
-  static constexpr int kFixed = kConv + kPBuf * kP + 2 * kQ + kMisc;
+  static constexpr int kFixed = kPBuf * kP + kQ + kMisc;
   static constexpr int kMaxStages = (232448 - kFixed) / kRaw;
   // even, so that K tiles have the even stages; 192 KB in flight are enough
   static constexpr int kStages = (kMaxStages * kRaw > 196608 ? 196608 / kRaw : kMaxStages) & ~1;
-  static constexpr int kOffConv = kStages * kRaw;
-  static constexpr int kOffP = kOffConv + kConv;
+  static constexpr int kOffP = kStages * kRaw;
   static constexpr int kOffQ = kOffP + kPBuf * kP;
-  static constexpr int kOffMisc = kOffQ + 2 * kQ;               // this piece's query rows and the next one's
+  static constexpr int kOffMisc = kOffQ + kQ;
   static constexpr int kBytes = kOffMisc + kMisc;
   // Scales of a tile's keys. A slot is written again once the K stage of the
   // tile kStages / 2 before it is free: that tile's S^T is done, so the
   // scores and scales of every tile up to kSBuf before that one are read.
   static constexpr int kScaleSlots = FP8 ? kStages / 2 + kSBuf + 1 : 0;
-  static constexpr uint32_t kTmemCols = N * (kByTile ? 8 : 4);  // S buffers and O (kSBuf + 1 or 2, a power of two)
+  static constexpr uint32_t kTmemCols = N * (FP8 ? 8 : 8);      // four S buffers of N, two O of kO
   static_assert(kStages >= 4 && kBytes <= 232448, "shared memory");
 };
 
 // What the softmax needs to know of the row tile's rows.
 template <int N>
-struct RowInfo {
+struct alignas(16) RowInfo {
   int lo[N], hi[N];   // the keys the row sees, apart from the sinks
   int out[N];         // row of out [q_rows * Hq], or -1: not a query row
   float scale[N];     // e4m3 parts: what the query row was divided by
 };
 
 // A piece of an item as the warps that work on it need it.
-template <int N>
 struct alignas(16) Piece {
-  RowInfo<N> rows;
+  Extent x;
   TileList t;
+  int h, r0;               // head, first flat row
   int j0, tiles;           // first tile of the piece, tiles of it that hold visible keys
   int more;                // 0: there is no such piece, the CTA is done
   int whole;               // the whole item: its results are final
@@ -121,14 +122,6 @@ __device__ __forceinline__ float reduce_columns(float (&v)[CNT], int lane, Op op
   return r;
 }
 
-// Scores of a key at position u in the columns whose rows do not see it.
-template <int CNT>
-__device__ __forceinline__ void mask_columns(float (&x)[CNT], const int *lo, const int *hi, int u, int sinks) {
-#pragma unroll
-  for (int e = 0; e < CNT; ++e)
-    if (!(u < hi[e] && (u >= lo[e] || u < sinks))) x[e] = -INFINITY;
-}
-
 template <int CNT>
 __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[CNT]) {
   if constexpr (CNT == 32) tmem_ld32(addr, r);
@@ -140,53 +133,85 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[CN
   if constexpr (CNT == 32) tmem_st32(addr, r); else tmem_st16(addr, r);
 }
 
-// The query rows of a row tile into shared memory as the B operand of S^T
-// (core matrices along K, row groups of 8), by one warp, with what the
+// The N query rows of a piece into shared memory as the B operand of S^T
+// (core matrices along K, row groups of 8), by 256 threads, with what the
 // softmax needs to know of each row.
 template <int DH, bool FP8, int N>
-__device__ __forceinline__ void stage_queries(const PagedArgs &a, const Walk &w, uint8_t *sq, RowInfo<N> &info, int lane) {
-  const int rows = w.x.W * a.group, r0 = w.rt * N;
-#pragma unroll
-  for (int n = lane; n < N; n += 32) {
-    const int r = r0 + n, t = r / a.group;
-    int lo = 0, hi = 0x7fffffff;   // a column that is no row masks nothing; its results go nowhere
-    if (r < rows) visible(a, w.x.pos + t, w.x.L, lo, hi);
-    info.lo[n] = lo;
-    info.hi[n] = hi;
-    info.out[n] = r < rows ? (w.x.q0 + t) * a.Hq + w.h * a.group + (r - t * a.group) : -1;
-  }
+__device__ __forceinline__ void stage_queries(const PagedArgs &a, const Piece &pc, uint8_t *sq, RowInfo<N> &info, int tid) {
+  const int rows = pc.x.W * a.group;
   constexpr int kChunks = DH / 8;                  // 16-byte chunks of a bf16 row
-  constexpr int kRows = 32 / kChunks;              // rows of one round of the warp
-  constexpr int kRounds = N / kRows, kAtOnce = kRounds < 8 ? kRounds : 8;   // loads on their way before the first store
-  const int c = lane % kChunks;
-#pragma unroll 1
-  for (int n0 = lane / kChunks; n0 < N; n0 += kRows * kAtOnce) {
-    uint4 u[kAtOnce];
+  constexpr int kEach = (N * kChunks + 255) / 256;
+  uint4 u[kEach];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int r = r0 + n0 + i * kRows, t = r / a.group, g = r - t * a.group;
-      u[i] = make_uint4(0, 0, 0, 0);
-      if (r < rows)
-        u[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + (w.x.q0 + t) * a.q_stride + (w.h * a.group + g) * DH + c * 8));
+  for (int i = 0; i < kEach; ++i) {                // every load on its way before the first store
+    const int idx = tid + i * 256, r = pc.r0 + idx / kChunks, t = r / a.group, g = r - t * a.group;
+    u[i] = make_uint4(0, 0, 0, 0);
+    if (idx < N * kChunks && r < rows)
+      u[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + (pc.x.q0 + t) * a.q_stride + (pc.h * a.group + g) * DH + idx % kChunks * 8));
+  }
+  if (tid < N) {
+    const int r = pc.r0 + tid, t = r / a.group;
+    int lo = 0, hi = 0x7fffffff;   // a column that is no row masks nothing; its results go nowhere
+    if (r < rows) visible(a, pc.x.pos + t, pc.x.L, lo, hi);
+    info.lo[tid] = lo;
+    info.hi[tid] = hi;
+    info.out[tid] = r < rows ? (pc.x.q0 + t) * a.Hq + pc.h * a.group + (r - t * a.group) : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int idx = tid + i * 256, n = idx / kChunks, c = idx % kChunks;
+    if (idx >= N * kChunks) break;                 // whole warps
+    if constexpr (!FP8) {
+      *reinterpret_cast<uint4 *>(sq + (n / 8) * (kChunks * 128) + c * 128 + (n % 8) * 16) = u[i];
+    } else {
+      const uint32_t m2 = max_mag(u[i], 0);
+      uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+      for (int o = kChunks / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      uint2 hi, lo;
+      const int byte = split_e4m3(u[i], m, hi, lo);
+      uint8_t *d = sq + (n / 8) * (DH / 16 * 128) + (c / 2) * 128 + (n % 8) * 16 + (c & 1) * 8;
+      *reinterpret_cast<uint2 *>(d) = hi;
+      *reinterpret_cast<uint2 *>(d + N * DH) = lo;
+      if (c == 0) info.scale[n] = scale_of(m < 0x7f80u ? byte : 255);   // a row with an infinity or NaN scores NaN
     }
+  }
+}
+
+// Weights of four rows (w >= 0) into three e5m2 parts, [part][0: as they are
+// times 2^13, 1: the small ones times 2^25, zero in the other].
+__device__ __forceinline__ void split_e5m2(const float (&w)[4], uint32_t (&out)[3][2]) {
+  constexpr float kSmall = 1.f / 1024.f;
+  float t[4], y[4];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int n = n0 + i * kRows;
-      if constexpr (!FP8) {
-        *reinterpret_cast<uint4 *>(sq + (n / 8) * (kChunks * 128) + c * 128 + (n % 8) * 16) = u[i];
-      } else {
-        const uint32_t m2 = max_mag(u[i], 0);
-        uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+  for (int i = 0; i < 4; ++i) {
+    t[i] = w[i] - kSmall;                                 // its sign: small
+    y[i] = w[i] * (t[i] < 0.f ? 33554432.f : 8192.f);
+  }
+  uint32_t h[2], part[3];
+  uint16_t lo[2];
+  uint32_t r[2];
 #pragma unroll
-        for (int o = kChunks / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        uint2 hi, lo;
-        const int byte = split_e4m3(u[i], m, hi, lo);
-        uint8_t *d = sq + (n / 8) * (DH / 16 * 128) + (c / 2) * 128 + (n % 8) * 16 + (c & 1) * 8;
-        *reinterpret_cast<uint2 *>(d) = hi;
-        *reinterpret_cast<uint2 *>(d + N * DH) = lo;
-        if (c == 0) info.scale[n] = scale_of(m < 0x7f80u ? byte : 255);   // a row with an infinity or NaN scores NaN
-      }
-    }
+  for (int i = 0; i < 2; ++i) {
+    // e5m2 is the upper byte of f16: two parts are cut off, the third rounds the rest
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(y[2 * i + 1]), "f"(y[2 * i]));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(h[i]), "r"(h[i] & 0xff00ff00u));
+    uint32_t r2;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r2) : "r"(r[i]), "r"(r[i] & 0xff00ff00u));
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo[i]) : "r"(r2));
+  }
+  part[0] = __byte_perm(h[0], h[1], 0x7531);
+  part[1] = __byte_perm(r[0], r[1], 0x7531);
+  part[2] = lo[0] | (static_cast<uint32_t>(lo[1]) << 16);
+  // 0xff in the bytes of the small ones: sign bytes replicated
+  uint32_t s01, s23;
+  asm("prmt.b32 %0, %1, %2, 0xfbfb;" : "=r"(s01) : "r"(__float_as_uint(t[0])), "r"(__float_as_uint(t[1])));
+  asm("prmt.b32 %0, %1, %2, 0xfbfb;" : "=r"(s23) : "r"(__float_as_uint(t[2])), "r"(__float_as_uint(t[3])));
+  const uint32_t small = __byte_perm(s01, s23, 0x5410);
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    out[p][0] = part[p] & ~small;
+    out[p][1] = part[p] & small;
   }
 }
 
@@ -195,55 +220,53 @@ __global__ void __launch_bounds__(Cfg<DH, FP8, N>::kThreads, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a,
                   const int min_tiles) {
   using C = Cfg<DH, FP8, N>;
-  constexpr int kSt = C::kStages, kCols = C::kCols, kSBuf = C::kSBuf;
-  constexpr bool kByTile = C::kByTile;
+  constexpr int kSt = C::kStages, kO = C::kO;
+  // FP8: the V scale enters the weights, so they must not pass 2^2
+  constexpr float kPass = FP8 ? 2.f : kLazy;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *misc = smem + C::kOffMisc;
-  Piece<N> *pieces = reinterpret_cast<Piece<N> *>(misc);                  // [2]: this one and the next one
-  float *m_s = reinterpret_cast<float *>(pieces + 2);                       // [group][kCols] reference maxima
-  float *corr_s = m_s + 2 * kCols;                                        // [group][kCols]
-  float *red_s = corr_s + 2 * kCols;                                      // [quarter][group][kCols]
-  uint8_t *scales = reinterpret_cast<uint8_t *>(red_s + 8 * kCols);           // [kScaleSlots][K, V][kTile]
+  RowInfo<N> *info = reinterpret_cast<RowInfo<N> *>(misc);                // [piece parity]
+  Piece *pieces = reinterpret_cast<Piece *>(info + 2);                    // [kAhead]
+  float *m_s = reinterpret_cast<float *>(pieces + kAhead);                // [group][N] reference maxima
+  float *corr_s = m_s + 2 * N;                                            // [group][N]
+  float *red_s = corr_s + 2 * N;                                          // [quarter][group][N]
+  int *eref_s = reinterpret_cast<int *>(red_s + 8 * N);                   // [group], [quarter][group] exponents of V scales
+  uint8_t *scales = reinterpret_cast<uint8_t *>(eref_s + 12);             // [kScaleSlots][K, V][kTile]
   uint32_t *pages_of = reinterpret_cast<uint32_t *>(scales + C::kScaleSlots * 2 * kTile);   // [kScaleSlots]: pages the tile has
-  uint64_t *bars = reinterpret_cast<uint64_t *>(pages_of + ((C::kScaleSlots + 1) & ~1));
-  uint64_t *full = bars;                    // [kSt] stage loaded
-  uint64_t *empty = full + kSt;             // [kSt] stage read by its MMAs (or converted)
+  uint64_t *full = reinterpret_cast<uint64_t *>(pages_of + ((C::kScaleSlots + 1) & ~1));    // [kSt] stage loaded
+  uint64_t *empty = full + kSt;             // [kSt] stage read by its MMAs
   uint64_t *s_full = empty + kSt;           // [kSBuf]
   uint64_t *s_free = s_full + kSBuf;        // [kSBuf]
   uint64_t *p_full = s_free + kSBuf;        // [kPBuf]
   uint64_t *p_free = p_full + kPBuf;        // [kPBuf] O^T MMAs of the tile done
-  uint64_t *c_full = p_free + kPBuf;        // [kCBuf] V piece converted
-  uint64_t *c_free = c_full + kCBuf;        // [kCBuf] its O^T MMAs done
-  uint64_t *sc_full = c_free + kCBuf;       // [kScaleSlots]
-  uint64_t *q_full = sc_full + C::kScaleSlots;   // [2] piece prepared
-  uint64_t *q_free = q_full + 2;            // [2] its last use over
-  uint64_t *o_full = q_free + 2;
+  uint64_t *sc_full = p_free + kPBuf;       // [kScaleSlots]
+  uint64_t *piece_full = sc_full + C::kScaleSlots;   // [kAhead]
+  uint64_t *piece_free = piece_full + kAhead;        // [kAhead] its last use over
+  uint64_t *q_full = piece_free + kAhead;   // [kAhead] its rows staged
+  uint64_t *o_full = q_full + kAhead;
   uint64_t *o_free = o_full + 1;
-  long long *s_scan = reinterpret_cast<long long *>(o_free + 1);          // [32]
-  Start *start = reinterpret_cast<Start *>(s_scan + 32);
+  long long *s_scan = reinterpret_cast<long long *>(o_free + 1);          // [16]
+  Start *start = reinterpret_cast<Start *>(s_scan + 16);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert(2 * sizeof(Piece<N>) + 12 * kCols * 4 + (2 * kSt + 2 * kSBuf + 2 * kPBuf + 2 * kCBuf + 6) * 8 + 256 + 64 +
-                        C::kScaleSlots * (2 * kTile + 8 + 4) + 4 <= C::kMisc - 1024,
+  static_assert(2 * sizeof(RowInfo<N>) + kAhead * sizeof(Piece) + 12 * N * 4 + 48 + C::kScaleSlots * (2 * kTile + 12) + 4 +
+                        (2 * kSt + 2 * kSBuf + 2 * kPBuf + 3 * kAhead + 2) * 8 + 128 + sizeof(Start) + 8 <=
+                    C::kMisc - 1024,
                 "row tables and barriers");
-  static_assert(sizeof(Piece<N>) % 16 == 0 && kCols % 16 == 0, "scales, 16-byte aligned for the bulk loads");
+  static_assert(sizeof(Piece) % 16 == 0 && (12 * N * 4 + 48) % 16 == 0, "scales, 16-byte aligned for the bulk loads");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   if (threadIdx.x == 0) {
-    constexpr int kTileWarps = C::kByTile ? 4 : 8;   // softmax warps of one tile
-    for (int s = 0; s < kSt; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], FP8 && (s & 1) ? 4 : 1);
-    }
-    for (int b = 0; b < kSBuf; ++b) { mbar_init(&s_full[b], 1); mbar_init(&s_free[b], kTileWarps); }
-    for (int b = 0; b < kPBuf; ++b) { mbar_init(&p_full[b], kTileWarps); mbar_init(&p_free[b], 1); }
-    for (int b = 0; b < kCBuf; ++b) { mbar_init(&c_full[b], 4); mbar_init(&c_free[b], 1); }
+    for (int s = 0; s < kSt; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int b = 0; b < kSBuf; ++b) { mbar_init(&s_full[b], 1); mbar_init(&s_free[b], 4); }
+    for (int b = 0; b < kPBuf; ++b) { mbar_init(&p_full[b], 4); mbar_init(&p_free[b], 1); }
     for (int b = 0; b < C::kScaleSlots; ++b) mbar_init(&sc_full[b], 1);
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&q_full[b], 1);
-      mbar_init(&q_free[b], 8 + 2 + (FP8 ? 4 : 0));   // the warps that read the piece
+    for (int b = 0; b < kAhead; ++b) {
+      mbar_init(&piece_full[b], 1);
+      mbar_init(&piece_free[b], 8 + 2);   // the warps that read the piece
+      mbar_init(&q_full[b], 8);
     }
     mbar_init(o_full, 1);
     mbar_init(o_free, 8);
@@ -260,203 +283,185 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t t_o = tmem + kSBuf * N;
+  const uint32_t t_o = tmem + kSBuf * N;    // O of group g at kO g
 
   pdl_wait();   // the batch's metadata, the pages and the queries may come from the previous kernel
   find_start(a, N, min_tiles, s_scan, start);
+
   if (warp < 4) {
-  reg_dealloc<C::kRegsIssue>();
-  if (warp == 0) {
-    // ------------------------------------------------------------- producer
-    load_tiles<DH, FP8 ? 1 : 2, kSt, C::kScaleSlots>(a, *start, N, &tm_k, &tm_v, smem, full, empty, scales, pages_of, sc_full,
-                                                     abort_flag, lane);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------- S^T MMAs
-    if (elect_one()) {
-    uint32_t n = 0;
-    bool ok = true;
-    for (uint32_t seg = 0; ok; ++seg) {
-      const uint32_t pi = seg & 1;
-      ok = mbar_wait(&q_full[pi], (seg >> 1) & 1, abort_flag);
-      if (!ok || !pieces[pi].more) break;
-      const int nT = pieces[pi].tiles;
-      const uint32_t sq = smem_u32(smem + C::kOffQ + pi * C::kQ);
-      for (int j = 0; j < nT; ++j, ++n) {
-        const uint32_t pos = 2 * n, st = pos % kSt, b = n % kSBuf;
-        ok = mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
-        if (ok && n >= kSBuf) ok = mbar_wait(&s_free[b], (n / kSBuf - 1) & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t sk = smem_u32(smem + st * C::kRaw);
-        {
-          if constexpr (!FP8) {
-            const uint64_t dk = sw128_desc(sk, 16, C::kGroup8), dq = plain_desc(sq, 128, DH / 8 * 128);
+    reg_dealloc<C::kRegsIssue>();
+    if (warp == 0) {
+      load_tiles<DH, FP8 ? 1 : 2, kSt, C::kScaleSlots>(a, *start, N, &tm_k, &tm_v, smem, full, empty, scales, pages_of, sc_full,
+                                                       abort_flag, lane);
+    } else if (warp == 1) {
+      // ----------------------------------------------------------- S^T MMAs
+      // (one elected thread through the whole loop: see paged_rows.cu)
+      if (elect_one()) {
+        uint32_t n = 0;
+        bool ok = true;
+        for (uint32_t seg = 0; ok; ++seg) {
+          const uint32_t pi = seg % kAhead;
+          ok = mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
+          if (!ok || !pieces[pi].more) break;
+          ok = mbar_wait(&q_full[pi], (seg / kAhead) & 1, abort_flag);
+          const int nT = pieces[pi].tiles;
+          const uint32_t sq = smem_u32(smem + C::kOffQ);
+          for (int j = 0; ok && j < nT; ++j, ++n) {
+            const uint32_t pos = 2 * n, st = pos % kSt, b = n % kSBuf;
+            ok = mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+            if (ok && n >= kSBuf) ok = mbar_wait(&s_free[b], (n / kSBuf - 1) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sk = smem_u32(smem + st * C::kRaw);
+            if constexpr (!FP8) {
+              const uint64_t dk = sw128_desc(sk, 16, C::kGroup8), dq = plain_desc(sq, 128, DH / 8 * 128);
 #pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk)
-              umma_bf16(tmem + b * N, dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), dq + ((kk * 256) >> 4),
-                        idesc_bf16(128, N, 0, 0), kk > 0);
-          } else {
-            const uint64_t dk = DH == 128 ? sw128_desc(sk, 16, C::kGroup8) : sw64_desc(sk, 16, C::kGroup8);
+              for (int kk = 0; kk < DH / 16; ++kk)
+                umma_bf16(tmem + b * N, dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), dq + ((kk * 256) >> 4),
+                          idesc_bf16(128, N, 0, 0), kk > 0);
+            } else {
+              const uint64_t dk = DH == 128 ? sw128_desc(sk, 16, C::kGroup8) : sw64_desc(sk, 16, C::kGroup8);
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              const uint64_t dq = plain_desc(sq + part * N * DH, 128, DH / 16 * 128);
+              for (int part = 0; part < 2; ++part) {
+                const uint64_t dq = plain_desc(sq + part * N * DH, 128, DH / 16 * 128);
 #pragma unroll
-              for (int kk = 0; kk < DH / 32; ++kk)
-                umma_f8(tmem + b * N, dk + ((kk * 32) >> 4), dq + ((kk * 256) >> 4), idesc_e4m3(128, N), part + kk > 0);
+                for (int kk = 0; kk < DH / 32; ++kk)
+                  umma_f8(tmem + b * N, dk + ((kk * 32) >> 4), dq + ((kk * 256) >> 4), idesc_f8(128, N, kE4M3, kE4M3, 0, 0),
+                          part + kk > 0);
+              }
             }
+            umma_commit(&s_full[b]);
+            umma_commit(&empty[st]);
           }
-          umma_commit(&s_full[b]);
-          umma_commit(&empty[st]);
+          mbar_arrive(&piece_free[pi]);
         }
       }
-      mbar_arrive(&q_free[pi]);
-    }
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    // ------------------------------------------------------------- O^T MMAs
-    if (elect_one()) {
-    uint32_t n = 0, o_seg = 0;
-    bool ok = true;
-    for (uint32_t seg = 0; ok; ++seg) {
-      const uint32_t pi = seg & 1;
-      ok = mbar_wait(&q_full[pi], (seg >> 1) & 1, abort_flag);
-      if (!ok || !pieces[pi].more) break;
-      const int nT = pieces[pi].tiles;
-      for (int j = 0; ok && j < nT; ++j, ++n) {
-        const uint32_t pos = 2 * n + 1, st = pos % kSt, b = n % kPBuf;
-        ok = mbar_wait(&p_full[b], (n / kPBuf) & 1, abort_flag);
-        if (ok && j == 0 && o_seg > 0) ok = mbar_wait(o_free, (o_seg - 1) & 1, abort_flag);
-        if (ok && !FP8) ok = mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
-        const uint32_t t_d = kByTile ? t_o + (n & 1) * N : t_o;
-        const bool first = j == 0 || (kByTile && j == 1);   // of its accumulator
-        const uint64_t dp = plain_desc(smem_u32(smem + C::kOffP + b * C::kP), 128, 2048);
-        // bf16: the tile as one piece; e4m3: its converted pieces
-        constexpr int kPieces = FP8 ? kTile / kConvKeys : 1, kSteps = 8 / kPieces;
-#pragma unroll
-        for (int piece = 0; piece < kPieces; ++piece) {
-          const uint32_t cn = n * kPieces + piece, cb = cn % kCBuf;
-          if (FP8 && ok) ok = mbar_wait(&c_full[cb], (cn / kCBuf) & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sv = smem_u32(FP8 ? smem + C::kOffConv + cb * (kConvKeys * DH * 2) : smem + st * C::kRaw);
-          {
-            const uint64_t dv = sw128_desc(sv, 1024, C::kVGroup8);
-#pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk)
-              umma_bf16(t_d, dv + ((kk * 2 * C::kVGroup8) >> 4), dp + (((piece * kSteps + kk) * 256) >> 4),
-                        idesc_bf16(DH, N, 1, 1), !first || piece + kk > 0);
-            umma_commit(FP8 ? &c_free[cb] : &empty[st]);
-            if (piece + 1 == kPieces) {
-              umma_commit(&p_free[b]);
-              if (j + 1 == nT) umma_commit(o_full);
-            }
-          }
-        }
-      }
-      o_seg += nT > 0;
-      mbar_arrive(&q_free[pi]);
-    }
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------- pieces and their query rows
-    // One piece ahead of the others, so that its metadata and its rows are
-    // there when the scores of the last one are.
-    Walk w(a, N, *start);
-    bool more = true, began = false;
-    for (uint32_t seg = 0; more; ++seg) {
-      const uint32_t pi = seg & 1;
-      if (seg >= 2 && !warp_wait(&q_free[pi], ((seg >> 1) - 1) & 1, abort_flag)) break;
-      Piece<N> &pc = pieces[pi];
-      more = w.next();
-      if (lane == 0) {
-        pc.more = more;
-        if (more) {
-          pc.t = w.t;
-          pc.j0 = w.j0;
-          pc.tiles = w.tiles();
-          pc.whole = w.whole();
-          // a CTA's first piece has its first slot, its last one the second
-          pc.slot = 2 * blockIdx.x + (seg > 0);
-          began |= begin_join(a, w, *start, pc.slot);
-        }
-      }
-      if (more) stage_queries<DH, FP8, N>(a, w, smem + C::kOffQ + pi * C::kQ, pc.rows, lane);
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[pi]);
-    }
-    if (a.join && lane == 0 && !began) a.join[blockIdx.x].parts = 0;
-  }
-  } else if (FP8 && warp >= C::kConvWarp0) {
-    // ------------------------------------------------------------- V codes -> bf16
-    if constexpr (FP8) {
-      reg_dealloc<C::kRegsConv>();
-      const int t = (warp - C::kConvWarp0) * 32 + lane;
-      uint32_t n = 0;
-      for (uint32_t seg = 0;; ++seg) {
-        const uint32_t pi = seg & 1;
-        if (!warp_wait(&q_full[pi], (seg >> 1) & 1, abort_flag) || !pieces[pi].more) break;
-        const TileList tl = pieces[pi].t;
-        const int j0 = pieces[pi].j0, nT = pieces[pi].tiles;
-        for (int j = 0; j < nT; ++j, ++n) {
-          const uint32_t pos = 2 * n + 1, st = pos % kSt;
-          mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
-#pragma unroll 1
-          for (int half = 0; half < kTile / kConvKeys; ++half) {
-            const uint32_t cn = n * (kTile / kConvKeys) + half, cb = cn % kCBuf;
-            const int u = tl.tile(j0 + j) * kTile + half * kConvKeys + t % kConvKeys;
-            convert_v<DH>(smem + st * C::kRaw, smem + C::kOffConv + cb * (kConvKeys * DH * 2), half, t,
-                          u < tl.hi && (u >= tl.lo || u < a.sinks),
-                          [&] { if (cn >= kCBuf) mbar_wait(&c_free[cb], (cn / kCBuf - 1) & 1, abort_flag); },
-                          [](uint2 v) { return v; });
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c_full[cb]);
+    } else if (warp == 2) {
+      // ----------------------------------------------------------- O^T MMAs
+      if (elect_one()) {
+        uint32_t n = 0, o_seg = 0;
+        bool ok = true;
+        for (uint32_t seg = 0; ok; ++seg) {
+          const uint32_t pi = seg % kAhead;
+          ok = mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
+          if (!ok || !pieces[pi].more) break;
+          const int nT = pieces[pi].tiles;
+          for (int j = 0; ok && j < nT; ++j, ++n) {
+            const uint32_t pos = 2 * n + 1, st = pos % kSt, b = n % kPBuf;
+            if (j == 0 && o_seg > 0) ok = mbar_wait(o_free, (o_seg - 1) & 1, abort_flag);
+            ok = ok && mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+            ok = ok && mbar_wait(&p_full[b], (n / kPBuf) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t t_d = t_o + (n & 1) * kO;
+            const uint32_t add = j > 1;   // the first tile of each group's accumulator
+            const uint32_t sv = smem_u32(smem + st * C::kRaw), sp = smem_u32(smem + C::kOffP + b * C::kP);
+            if constexpr (!FP8) {
+              const uint64_t dv = sw128_desc(sv, 1024, C::kGroup8), dp = plain_desc(sp, 128, 2048);
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                umma_bf16(t_d, dv + ((kk * 2 * C::kGroup8) >> 4), dp + ((kk * 256) >> 4), idesc_bf16(DH, N, 1, 1),
+                          kk > 0 ? 1u : add);
+            } else {
+              const uint64_t dv = DH == 128 ? sw128_desc(sv, 1024, C::kGroup8) : sw64_desc(sv, 1024, C::kGroup8);
+#pragma unroll
+              for (int part = 0; part < 3; ++part) {
+                const uint64_t dp = plain_desc(sp + part * C::kPart, 128, 2048);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_f8(t_d, dv + ((kk * 4 * C::kGroup8) >> 4), dp + ((kk * 512) >> 4), idesc_f8(DH, kO, kE4M3, kE5M2, 1, 1),
+                          part + kk > 0 ? 1u : add);
+              }
+            }
+            umma_commit(&empty[st]);
+            umma_commit(&p_free[b]);
+            if (j + 1 == nT) umma_commit(o_full);
           }
-          if (lane == 0) mbar_arrive(&empty[st]);
+          o_seg += nT > 0;
+          mbar_arrive(&piece_free[pi]);
+        }
+      }
+      __syncwarp();
+    } else {
+      // ----------------------------------------------------------- pieces
+      Walk w(a, N, *start);
+      bool more = true, began = false;
+      for (uint32_t seg = 0; more; ++seg) {
+        const uint32_t pi = seg % kAhead;
+        if (seg >= kAhead && !warp_wait(&piece_free[pi], (seg / kAhead - 1) & 1, abort_flag)) break;
+        more = w.next();
+        if (lane == 0) {
+          Piece &pc = pieces[pi];
+          pc.more = more;
+          if (more) {
+            pc.x = w.x;
+            pc.t = w.t;
+            pc.h = w.h;
+            pc.r0 = w.rt * N;
+            pc.j0 = w.j0;
+            pc.tiles = w.tiles();
+            pc.whole = w.whole();
+            // a CTA's first piece has its first slot, its last one the second
+            pc.slot = 2 * blockIdx.x + (seg > 0);
+            began |= begin_join(a, w, *start, pc.slot);
+          }
+          mbar_arrive(&piece_full[pi]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_free[pi]);
+        if (more) prefetch_rows(a, w, N, DH, lane);
       }
+      if (a.join && lane == 0 && !began) a.join[blockIdx.x].parts = 0;
     }
   } else {
     // ------------------------------------------------------------- softmax
     reg_alloc<C::kRegsSoft>();
     const int wg = (warp - 4) >> 2, quarter = warp & 3, tid = threadIdx.x & 127;
     const int key = quarter * 32 + lane;
-    const int c0 = kByTile ? 0 : wg * kCols;   // first column of the group's tiles
-    const int g0 = wg * kCols;                 // its part of the groups' arrays
-    constexpr int kOut = N / 2;                // rows that a group stages and writes
+    const int g0 = wg * N;                     // the group's part of the groups' arrays
+    constexpr int kOut = N / 2;                // rows that a group writes
     const int out0 = wg * kOut;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_d = t_o + lane_base + wg * kO;
     const auto maxop = [](float p, float q) { return fmaxf(p, q); };
     const auto addop = [](float p, float q) { return p + q; };
     uint32_t n = 0, o_seg = 0;
+    auto stage = [&](uint32_t seg) {           // piece seg's query rows
+      const uint32_t pi = seg % kAhead;
+      mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
+      if (!pieces[pi].more) return;
+      stage_queries<DH, FP8, N>(a, pieces[pi], smem + C::kOffQ, info[seg & 1], threadIdx.x - 128);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[pi]);
+    };
+    stage(0);
     for (uint32_t seg = 0;; ++seg) {
-      const uint32_t pi = seg & 1;
-      // all of both groups go on or none does (the last piece's maxima are read, too)
-      if (bar_any(3, 256, !mbar_wait(&q_full[pi], (seg >> 1) & 1, abort_flag))) break;
-      const Piece<N> &pc = pieces[pi];
+      const uint32_t pi = seg % kAhead;
+      // all of both groups go on or none does; the rows' info is written, the last piece's maxima are read
+      if (bar_any(3, 256, !mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag))) break;
+      const Piece &pc = pieces[pi];
       if (!pc.more) break;
-      const RowInfo<N> &ri = pc.rows;
+      const RowInfo<N> &ri = info[seg & 1];
       const TileList tl = pc.t;
       const int nT = pc.tiles, j0 = pc.j0;
-      float l[kCols];
+      float l[N];
 #pragma unroll
-      for (int e = 0; e < kCols; ++e) l[e] = 0.f;
-      if (tid < kCols) m_s[g0 + tid] = kNone;
+      for (int e = 0; e < N; ++e) l[e] = 0.f;
+      if (tid < N) m_s[g0 + tid] = kNone;
+      int eref = -128;                      // V scales are relative to 2^eref
       named_bar_sync(1 + wg, 128);
       bool first = true;                    // of the group's tiles
       for (int j = 0; j < nT; ++j, ++n) {
-        if (kByTile && (n & 1) != wg) continue;
+        if ((n & 1) != wg) continue;
         const uint32_t b = n % kSBuf, pb = n % kPBuf;
         const int key0 = tl.tile(j0 + j) * kTile, u = key0 + key;
         // every row of the tile sees every key of it?
         const bool all_seen = key0 + kTile <= tl.hi_first && (key0 >= tl.lo_last || key0 + kTile <= a.sinks);
         const bool seen = u < tl.hi && (u >= tl.lo || u < a.sinks);   // this key, by any row
-        float c = a.scale_log2, vs = 1.f;
+        float c = a.scale_log2;
+        int vexp = -128;                    // exponent of the key's V scale
+        bool vnan = false;
         if constexpr (FP8) {
           const uint32_t slot = n % C::kScaleSlots;
           mbar_wait(&sc_full[slot], (n / C::kScaleSlots) & 1, abort_flag);
@@ -464,102 +469,145 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           if ((pages_of[slot] >> (key >> a.c.page_shift) & 1) && seen) {
             const uint8_t *sc = scales + slot * (2 * kTile) + key;
             c *= scale_of(sc[0]);
-            vs = scale_of(sc[kTile]);
+            vnan = sc[kTile] == 255;
+            vexp = vnan ? -128 : static_cast<int>(sc[kTile]) - 127;
           }
         }
         mbar_wait(&s_full[b], (n / kSBuf) & 1, abort_flag);
         tc_fence_after();
-        uint32_t s[kCols];
-        const uint32_t t_s = tmem + lane_base + b * N + c0;
-        tmem_load<kCols>(t_s, s);
+        uint32_t s[N];
+        tmem_load<N>(tmem + lane_base + b * N, s);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[b]);
-        // x = score - reference in log2 units, two columns at a time; nobody
-        // past the reference by more than 2^8 is the common case
-        float x[kCols];
-        auto score2 = [&](int e) {
-          float2 f = make_float2(c, c);
-          if constexpr (FP8) f = __fmul2_rn(f, *reinterpret_cast<const float2 *>(&ri.scale[c0 + e]));
-          return f;
-        };
+        // x = score - reference in log2 units, two columns at a time, -inf
+        // where the column's row does not see the key
+        float x[N];
+        auto relative = [&](const float *ref) {
 #pragma unroll
-        for (int e = 0; e < kCols; e += 2) {
-          const float2 m2 = *reinterpret_cast<const float2 *>(&m_s[g0 + e]);
-          const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), score2(e),
-                                      make_float2(-m2.x, -m2.y));
-          x[e] = y.x;
-          x[e + 1] = y.y;
-        }
-        if (!all_seen) mask_columns<kCols>(x, ri.lo + c0, ri.hi + c0, u, a.sinks);
+          for (int e = 0; e < N; e += 2) {
+            float2 f = make_float2(c, c), r = make_float2(0.f, 0.f);
+            if constexpr (FP8) f = __fmul2_rn(f, *reinterpret_cast<const float2 *>(&ri.scale[e]));
+            if (ref) r = *reinterpret_cast<const float2 *>(ref + e);
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f, make_float2(-r.x, -r.y));
+            x[e] = y.x;
+            x[e + 1] = y.y;
+          }
+          if (!all_seen) {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+              if (!(u < ri.hi[e] && (u >= ri.lo[e] || u < a.sinks))) x[e] = -INFINITY;
+          }
+        };
+        relative(m_s + g0);
         float top = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < kCols; e += 2) top = fmaxf(top, fmaxf(x[e], x[e + 1]));
-        if (bar_any(1 + wg, 128, top > kLazy)) {
-          // new references: the columns' maxima over the tile
-          float v[kCols];
+        for (int e = 0; e < N; e += 2) top = fmaxf(top, fmaxf(x[e], x[e + 1]));
+        // nobody past its reference is the common case
+        if (bar_any(1 + wg, 128, top > kPass || (FP8 && vexp > eref))) {
+          // new references: the columns' maxima over the tile, the largest V scale
+          relative(nullptr);
+          float v[N];
 #pragma unroll
-          for (int e = 0; e < kCols; e += 2) {
-            const float2 y = __fmul2_rn(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), score2(e));
-            v[e] = y.x;
-            v[e + 1] = y.y;
+          for (int e = 0; e < N; ++e) v[e] = x[e];
+          const float most = reduce_columns<N>(v, lane, maxop);
+          if (lane < N) red_s[quarter * (2 * N) + g0 + lane] = most;
+          if constexpr (FP8) {
+            const int e = __reduce_max_sync(0xffffffffu, vexp);
+            if (lane == 0) eref_s[2 + quarter * 2 + wg] = e;
           }
-          if (!all_seen) mask_columns<kCols>(v, ri.lo + c0, ri.hi + c0, u, a.sinks);
-#pragma unroll
-          for (int e = 0; e < kCols; ++e) x[e] = v[e];
-          const float most = reduce_columns<kCols>(v, lane, maxop);
-          if (lane < kCols) red_s[quarter * (2 * kCols) + g0 + lane] = most;
           named_bar_sync(1 + wg, 128);
-          if (tid < kCols) {
+          int e_new = eref;
+          if constexpr (FP8)
+            e_new = max(max(max(eref_s[2 + wg], eref_s[4 + wg]), max(eref_s[6 + wg], eref_s[8 + wg])), eref);
+          if (tid < N) {
             const int e = g0 + tid;
-            const float mx = fmaxf(fmaxf(red_s[e], red_s[2 * kCols + e]), fmaxf(red_s[4 * kCols + e], red_s[6 * kCols + e]));
-            const float old = m_s[e], now = mx > old + kLazy ? mx : old;
+            const float mx = fmaxf(fmaxf(red_s[e], red_s[2 * N + e]), fmaxf(red_s[4 * N + e], red_s[6 * N + e]));
+            const float old = m_s[e], now = mx > old + kPass ? mx : old;
             corr_s[e] = now == old ? 1.f : ex2_approx(old - now);
             m_s[e] = now;
           }
           named_bar_sync(1 + wg, 128);
 #pragma unroll
-          for (int e = 0; e < kCols; ++e) {
+          for (int e = 0; e < N; ++e) {
             l[e] *= corr_s[g0 + e];
             x[e] -= m_s[g0 + e];
           }
           if (!first) {
             // O holds exactly the group's tiles before this one once the MMAs of the last are done
-            const uint32_t last = n - (kByTile ? 2 : 1), t_d = t_o + lane_base + (kByTile ? wg * N : c0);
-            mbar_wait(&p_free[last % kPBuf], (last / kPBuf) & 1, abort_flag);
+            mbar_wait(&p_free[pb], ((n - 2) / kPBuf) & 1, abort_flag);
             tc_fence_after();
-            uint32_t o[kCols];
-            tmem_load<kCols>(t_d, o);
-            tmem_ld_wait();
+            const float ev = FP8 ? ex2_approx(static_cast<float>(eref - e_new)) : 1.f;
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr_s[g0 + e]);
-            tmem_store<kCols>(t_d, o);
+            for (int q = 0; q < kO; q += N) {
+              uint32_t o[N];
+              tmem_load<N>(t_d + q, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < N; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (corr_s[g0 + e] * ev));
+              tmem_store<N>(t_d + q, o);
+            }
             tmem_st_wait();
             tc_fence_before();
           }
+          eref = e_new;
         }
-        // P = 2^x, its column sums per key, and P * v scale as bf16
-        uint32_t pk[kCols / 2];
-#pragma unroll
-        for (int e = 0; e < kCols; e += 2) {
-          float2 p = make_float2(ex2_approx(x[e]), ex2_approx(x[e + 1]));
-          const float2 sum = __fadd2_rn(make_float2(l[e], l[e + 1]), p);
-          l[e] = sum.x;
-          l[e + 1] = sum.y;
-          if constexpr (FP8) p = __fmul2_rn(p, make_float2(vs, vs));
-          pk[e / 2] = pack_bf16x2(p.x, p.y);
-        }
+        // P = 2^x and its column sums per key
         if (n >= kPBuf) mbar_wait(&p_free[pb], (n / kPBuf - 1) & 1, abort_flag);
-        uint8_t *sp = smem + C::kOffP + pb * C::kP + (c0 / 8) * 2048 + (key / 8) * 128 + (key % 8) * 16;
-#pragma unroll
-        for (int e = 0; e < kCols / 8; ++e)
-          *reinterpret_cast<uint4 *>(sp + e * 2048) = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+        uint8_t *sp = smem + C::kOffP + pb * C::kP + (key / 8) * 128 + (key % 8) * 16;
         if constexpr (!FP8) {
-          // rows of V that no query row sees may hold anything, and 0 * NaN is not 0
-          if ((kByTile || wg == 0) && !seen) {
-            const uint32_t pos = 2 * n + 1, st = pos % kSt;
-            mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+#pragma unroll
+          for (int e = 0; e < N; e += 8) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const float2 p = make_float2(ex2_approx(x[e + i]), ex2_approx(x[e + i + 1]));
+              const float2 sum = __fadd2_rn(make_float2(l[e + i], l[e + i + 1]), p);
+              l[e + i] = sum.x;
+              l[e + i + 1] = sum.y;
+              pk[i / 2] = pack_bf16x2(p.x, p.y);
+            }
+            *reinterpret_cast<uint4 *>(sp + e / 8 * 2048) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        } else {
+          // (no page: a weight of 0 for a row of zeros)
+          const float vs = vnan ? NAN : ex2_approx(static_cast<float>(vexp - eref));
+#pragma unroll
+          for (int e = 0; e < N; e += 16) {
+            uint32_t pk[3][2][4];
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              float w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float p = ex2_approx(x[e + i + k]);
+                l[e + i + k] += p;
+                w[k] = p * vs;
+              }
+              uint32_t q[3][2];
+              split_e5m2(w, q);
+#pragma unroll
+              for (int p = 0; p < 3; ++p) { pk[p][0][i / 4] = q[p][0]; pk[p][1][i / 4] = q[p][1]; }
+            }
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<uint4 *>(sp + p * C::kPart + (h * (N / 16) + e / 16) * 2048) =
+                    make_uint4(pk[p][h][0], pk[p][h][1], pk[p][h][2], pk[p][h][3]);
+          }
+        }
+        // rows of V that no query row sees may hold anything, and 0 * NaN is not 0
+        if (!seen) {
+          const uint32_t pos = 2 * n + 1, st = pos % kSt;
+          mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+          // (the swizzles permute 16-byte pieces within a row)
+          if constexpr (FP8) {
+            uint8_t *sv = smem + st * C::kRaw + key * DH;
+#pragma unroll
+            for (int e = 0; e < DH / 16; ++e) *reinterpret_cast<uint4 *>(sv + e * 16) = make_uint4(0, 0, 0, 0);
+          } else {
             uint8_t *sv = smem + st * C::kRaw + (key / 8) * C::kGroup8 + (key % 8) * 128;
 #pragma unroll
             for (int e = 0; e < DH / 8; ++e)
@@ -572,12 +620,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (lane == 0) mbar_arrive(&p_full[pb]);
         first = false;
       }
-      const float part = reduce_columns<kCols>(l, lane, addop);
-      if (lane < kCols) red_s[quarter * (2 * kCols) + g0 + lane] = part;
+      // the next piece's rows are staged before this one's results are
+      // written, so that its scores run meanwhile: every S^T of this piece
+      // is done
+      named_bar_sync(3, 256);
+      stage(seg + 1);
+      const float part = reduce_columns<N>(l, lane, addop);
+      if (lane < N) red_s[quarter * (2 * N) + g0 + lane] = part;
+      if (FP8 && tid == 0) eref_s[wg] = eref;
       named_bar_sync(1 + wg, 128);
-      if (tid < kCols) {
+      if (tid < N) {
         const int e = g0 + tid;
-        corr_s[e] = (red_s[e] + red_s[2 * kCols + e]) + (red_s[4 * kCols + e] + red_s[6 * kCols + e]);
+        corr_s[e] = (red_s[e] + red_s[2 * N + e]) + (red_s[4 * N + e] + red_s[6 * N + e]);
       }
       if (nT > 0) {
         mbar_wait(o_full, o_seg & 1, abort_flag);
@@ -587,29 +641,23 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       named_bar_sync(3, 256);
       // rows [out0, out0 + kOut): maximum, sum, and what the groups' O count for
       uint32_t o[kOut];
-      if constexpr (kByTile) {
-        uint32_t o1[kOut];
+#pragma unroll
+      for (int e = 0; e < kOut; ++e) o[e] = 0;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
         // a single tile leaves the other group without an O
-        const bool has0 = nT > 1 || (nT == 1 && ((n - 1) & 1) == 0), has1 = nT > 1 || (nT == 1 && ((n - 1) & 1) == 1);
-        if (nT > 0) {
-          tmem_load<kOut>(t_o + lane_base + out0, o);
-          tmem_load<kOut>(t_o + lane_base + N + out0, o1);
-          tmem_ld_wait();
-        }
+        if (!(nT > 1 || (nT == 1 && ((n - 1) & 1) == g))) continue;
+        uint32_t y[kOut], z[kOut];
+        tmem_load<kOut>(t_o + lane_base + g * kO + out0, y);
+        if constexpr (FP8) tmem_load<kOut>(t_o + lane_base + g * kO + N + out0, z);
+        tmem_ld_wait();
+        const float ev = FP8 ? scale_of(max(eref_s[g] + 127, 0)) : 1.f;
 #pragma unroll
         for (int e = 0; e < kOut; ++e) {
-          const float m0 = m_s[out0 + e], m1 = m_s[kCols + out0 + e], m = fmaxf(m0, m1);
-          const float y0 = has0 ? __uint_as_float(o[e]) * ex2_approx(m0 - m) : 0.f;
-          const float y1 = has1 ? __uint_as_float(o1[e]) * ex2_approx(m1 - m) : 0.f;
-          o[e] = __float_as_uint(y0 + y1);
-        }
-      } else {
-        if (nT > 0) {
-          tmem_load<kOut>(t_o + lane_base + out0, o);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int e = 0; e < kOut; ++e) o[e] = 0;
+          const float f = ex2_approx(m_s[g * N + out0 + e] - fmaxf(m_s[out0 + e], m_s[N + out0 + e]));
+          float w = __uint_as_float(y[e]);
+          if constexpr (FP8) w = (w * 0x1p-13f + __uint_as_float(z[e]) * 0x1p-25f) * ev;
+          o[e] = __float_as_uint(__uint_as_float(o[e]) + w * f);
         }
       }
       if (nT > 0) {
@@ -618,14 +666,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (lane == 0) mbar_arrive(o_free);
       }
       auto merged = [&](int e) {   // {maximum, sum} of row e
-        if constexpr (!kByTile) return make_float2(m_s[e], corr_s[e]);
-        const float m = fmaxf(m_s[e], m_s[kCols + e]);
-        return make_float2(m, corr_s[e] * ex2_approx(m_s[e] - m) + corr_s[kCols + e] * ex2_approx(m_s[kCols + e] - m));
+        const float m = fmaxf(m_s[e], m_s[N + e]);
+        return make_float2(m, corr_s[e] * ex2_approx(m_s[e] - m) + corr_s[N + e] * ex2_approx(m_s[N + e] - m));
       };
       // M = 64: rows 16 q .. 16 q + 15 lie in the first 16 lanes of quarter q
-      // converted V rows hold every four elements in the order 0, 2, 1, 3
-      const int dm = DH == 128 ? key : quarter * 16 + lane;
-      const int dc = FP8 ? (dm & ~3) | ((dm & 1) << 1) | ((dm >> 1) & 1) : dm;
+      const int dc = DH == 128 ? key : quarter * 16 + lane;
       const bool dlive = DH == 128 || lane < 16;
       if (pc.whole) {
 #pragma unroll
@@ -633,7 +678,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           const int row = ri.out[out0 + e];
           if (row < 0) break;
           const float sum = merged(out0 + e).y;
-          const float y = sum != 0.f ? __uint_as_float(o[e]) / sum : 0.f;
+          const float y = sum != 0.f ? __fdividef(__uint_as_float(o[e]), sum) : 0.f;
           if (dlive) {
             if (a.out_fp32) static_cast<float *>(a.out)[static_cast<size_t>(row) * DH + dc] = y;
             else static_cast<uint16_t *>(a.out)[static_cast<size_t>(row) * DH + dc] = f32_to_bf16(y);
@@ -652,7 +697,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (tid < kOut) a.part_ml[slot * N + out0 + tid] = merged(out0 + tid);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_free[pi]);
+      if (lane == 0) mbar_arrive(&piece_free[pi]);
     }
   }
 
@@ -745,8 +790,7 @@ int row_tile(const dllm_kv_pages *pages, const dllm_paged_attn_args *a) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
 }
 
-// A CTA's piece is at least kMinTiles tiles: items of no more are never cut.
-bool may_split(const dllm_paged_attn_args *a) { return a->max_kv > kMinTiles * kTile; }
+bool may_split(const dllm_paged_attn_args *a) { return a->max_kv > kWholeTiles * kTile; }
 
 struct Ws {
   size_t part_ml, join, total;   // part_o at 0

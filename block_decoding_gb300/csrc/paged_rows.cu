@@ -252,7 +252,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 const uint64_t dq = DH == 128 ? sw128_desc(sp, 16, 8 * DH) : sw64_desc(sp, 16, 8 * DH);
 #pragma unroll
                 for (int kk = 0; kk < DH / 32; ++kk)
-                  umma_f8(t_s, dq + ((kk * 32) >> 4), dk + ((kk * 32) >> 4), idesc_e4m3(128, 128), part + kk > 0);
+                  umma_f8(t_s, dq + ((kk * 32) >> 4), dk + ((kk * 32) >> 4), idesc_f8(128, 128, kE4M3, kE4M3, 0, 0), part + kk > 0);
               }
             }
             umma_commit(&s_full[s]);
@@ -331,14 +331,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           mbar_arrive(&piece_full[pi]);
         }
         __syncwarp();
-        if (more) {   // its rows on their way to L2
-          const int rows = w.x.W * a.group;
-          for (int idx = lane; idx < C::kRows * (DH / 64); idx += 32) {
-            const int r = w.rt * C::kRows + idx / (DH / 64), t = r / a.group;
-            if (r >= rows) break;
-            l2_prefetch_line(a.q + (w.x.q0 + t) * a.q_stride + (w.h * a.group + r - t * a.group) * DH + idx % (DH / 64) * 64);
-          }
-        }
+        if (more) prefetch_rows(a, w, C::kRows, DH, lane);
       }
       if (a.join && lane == 0 && !began) a.join[blockIdx.x].parts = 0;
     }

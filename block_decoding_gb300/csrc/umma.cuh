@@ -472,10 +472,12 @@ __device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr, uint32_t lbo_bytes
   return plain_desc(saddr, lbo_bytes, sbo_bytes) | (4ull << 61);
 }
 
-// Instruction descriptor of tcgen05.mma kind::f8f6f4 with e4m3 A and B, both
-// K-major, and fp32 D.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+// Instruction descriptor of tcgen05.mma kind::f8f6f4: 8-bit A and B of the
+// given formats, fp32 D, operand majorness (0 = K-major, 1 = MN-major).
+constexpr uint32_t kE4M3 = 0, kE5M2 = 1;
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, uint32_t a_type, uint32_t b_type, int a_mn, int b_mn) {
+  return (1u << 4) | (a_type << 7) | (b_type << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+         (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // Instruction descriptor of tcgen05.mma kind::f16: bf16 A and B, fp32 D,
