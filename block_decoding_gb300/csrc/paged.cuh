@@ -111,19 +111,25 @@ __device__ __forceinline__ int tiles_per_item(const PagedArgs &a, const Extent &
   return max(most, 1);
 }
 
-// Where this CTA starts: the total of all items' tiles, cut into gridDim.x
-// equal pieces (whole items with `uniform`).
+// The work is a line of all items, each as long as its tiles and kItemCost
+// more for what every item costs however short it is (rows staged, results
+// written: about as much as so many tiles; without it a CTA with many short
+// items took 40 % longer than the others). It is cut into gridDim.x equal
+// stretches (of whole items with `uniform`).
+constexpr int kItemCost = 6;
+
+// Where this CTA's stretch starts.
 struct Start {
-  long long residual;   // tiles of request i before this CTA's first
-  long long left;       // tiles of this CTA
-  long long per;        // tiles of every CTA
+  long long residual;   // length of request i before it
+  long long left;       // its length
+  long long per;        // the length of every stretch
   int i;
 };
 
-__device__ __forceinline__ long long request_tiles(const PagedArgs &a, int i, int n_rows, bool report) {
+__device__ __forceinline__ long long request_length(const PagedArgs &a, int i, int n_rows, bool report) {
   const Extent x = paged_extent(a, i, report);
   const long long items = static_cast<long long>((x.W * a.group + n_rows - 1) / n_rows) * a.c.heads;
-  return items ? items * tiles_per_item(a, x, n_rows) : 0;
+  return items ? items * (tiles_per_item(a, x, n_rows) + kItemCost) : 0;
 }
 
 // Every thread of the CTA takes part; s_scan holds 32 values.
@@ -133,7 +139,7 @@ __device__ __forceinline__ void find_start(const PagedArgs &a, int n_rows, int m
   const int chunk = (a.B + nt - 1) / nt;
   const int i0 = tid * chunk, i1 = min(a.B, i0 + chunk);
   long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += request_tiles(a, i, n_rows, blockIdx.x == 0);
+  for (int i = i0; i < i1; ++i) mine += request_length(a, i, n_rows, blockIdx.x == 0);
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -149,13 +155,13 @@ __device__ __forceinline__ void find_start(const PagedArgs &a, int n_rows, int m
     total += s_scan[w];
   }
   long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(min_tiles));
-  if (a.uniform) per = (per + a.uniform - 1) / a.uniform * a.uniform;
+  if (a.uniform) per = (per + a.uniform + kItemCost - 1) / (a.uniform + kItemCost) * (a.uniform + kItemCost);
   const long long begin = per * blockIdx.x;
   const long long excl = before + incl - mine;
   if (begin >= excl && begin < excl + mine) {
     long long at = excl;
     for (int i = i0; i < i1; ++i) {
-      const long long m = request_tiles(a, i, n_rows, false);
+      const long long m = request_length(a, i, n_rows, false);
       if (begin < at + m) {
         s_start->i = i;
         s_start->residual = begin - at;
@@ -173,10 +179,10 @@ __device__ __forceinline__ void find_start(const PagedArgs &a, int n_rows, int m
 struct Walk {
   const PagedArgs &a;
   int n_rows;
-  int i, item, j;          // request, item of the request, tile of the item
-  long long left;          // tiles of this CTA still to come
+  int i, item, at;         // request, item of the request, place in the item
+  long long left;          // length still to come
   Extent x;
-  int n, items, row_tiles;
+  int n, items, row_tiles; // tiles of an item, items of the request
   // the current piece
   int h, rt, j0, j1;       // head, row tile, tiles [j0, j1) of it
   TileList t;
@@ -184,8 +190,8 @@ struct Walk {
     if (left <= 0) return;
     i = s.i;
     load();
-    item = static_cast<int>(s.residual / n);
-    j = static_cast<int>(s.residual - static_cast<long long>(item) * n);
+    item = static_cast<int>(s.residual / (n + kItemCost));
+    at = static_cast<int>(s.residual - static_cast<long long>(item) * (n + kItemCost));
   }
   __device__ __forceinline__ void load() {
     x = paged_extent(a, i, false);
@@ -193,19 +199,24 @@ struct Walk {
     items = row_tiles * a.c.heads;
     n = items ? tiles_per_item(a, x, n_rows) : 0;
   }
+  // The next piece that has tiles: a cut within an item's fixed cost leaves
+  // the whole item to the CTA behind it.
   __device__ __forceinline__ bool next() {
-    if (left <= 0) return false;
-    while (item >= items) {
-      if (++i >= a.B) return false;
-      item = 0;
-      load();
-    }
-    h = item / row_tiles;
-    rt = item - h * row_tiles;
-    j0 = j;
-    j1 = static_cast<int>(min(static_cast<long long>(n), j + left));
-    left -= j1 - j0;
-    if (j1 == n) { j = 0; ++item; } else { j = j1; }
+    do {
+      if (left <= 0) return false;
+      while (item >= items) {
+        if (++i >= a.B) return false;
+        item = at = 0;
+        load();
+      }
+      h = item / row_tiles;
+      rt = item - h * row_tiles;
+      const int end = static_cast<int>(min(static_cast<long long>(n + kItemCost), at + left));
+      j0 = max(at - kItemCost, 0);
+      j1 = max(end - kItemCost, 0);
+      left -= end - at;
+      if (end == n + kItemCost) { at = 0; ++item; } else { at = end; }
+    } while (j1 <= j0);
     t = tile_list(a, x, rt, n_rows);
     return true;
   }
@@ -218,7 +229,7 @@ struct Walk {
 // CTAs. Returns whether the item is divided there.
 __device__ __forceinline__ bool begin_join(const PagedArgs &a, const Walk &w, const Start &s, int slot) {
   if (w.j0 != 0 || w.whole()) return false;
-  const int parts = 1 + static_cast<int>((w.n - w.j1 + s.per - 1) / s.per);
+  const int parts = 1 + static_cast<int>((w.n - w.j1 + s.per - 1) / s.per);   // (the fixed cost lies before tile 0)
   a.join[blockIdx.x] = JoinJob{slot, parts, w.rt * w.n_rows, w.x.W * a.group, w.x.q0, w.h, 0, 0};
   return true;
 }
@@ -233,11 +244,13 @@ __device__ __forceinline__ void prefetch_rows(const PagedArgs &a, const Walk &w,
   }
 }
 
-// The warp that loads the K and V tiles of a CTA's pieces into one ring of
-// SLOTS stages, K tiles in the even ones: one box per page and tile. With
-// e4m3 pages (SCALES > 0) a tile's scale bytes, K's then V's, go to a ring of
+// The warp that loads the K and V tiles of a CTA's pieces: one box per page
+// and tile, K tile n to stage n % KS, V tile n to stage KS + n % VS. A tile's
+// V is asked for LEAD tiles after its K: it is read that much later, and
+// until then its space would hold nothing back but other loads. With e4m3
+// pages (SCALES > 0) a tile's scale bytes, K's then V's, go to a ring of
 // SCALES slots with the truth of which pages the tile has.
-template <int DH, int ELEM, int SLOTS, int SCALES>
+template <int DH, int ELEM, int KS, int VS, int LEAD, int SCALES>
 __device__ __forceinline__ void load_tiles(const PagedArgs &a, const Start &start, int n_rows, const CUtensorMap *tm_k,
                                            const CUtensorMap *tm_v, uint8_t *ring, uint64_t *full, uint64_t *empty,
                                            uint8_t *scales, uint32_t *pages_of, uint64_t *sc_full, volatile int *abort,
@@ -247,7 +260,20 @@ __device__ __forceinline__ void load_tiles(const PagedArgs &a, const Start &star
   const int none = static_cast<int>((static_cast<long long>(a.c.num_pages) * a.c.heads << a.c.page_shift) / 8);
   Walk w(a, n_rows, start);
   bool bad = false, ok = true;
-  uint32_t n = 0, issued = 0;
+  uint32_t nk = 0, nv = 0;     // K and V tiles asked for
+  int lag[LEAD + 1];           // pages of the tiles whose V is not
+  // tile n's box of this lane's page (8-row group g)
+  auto load = [&](const CUtensorMap *tm, uint32_t st, uint32_t round, int g) {
+    if (round > 0) ok = ok && warp_wait(&empty[st], (round - 1) & 1, abort);
+    if (!ok) return;
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], kRaw);
+    __syncwarp();
+    if (lane < per_tile) tma_load_4d(ring + st * kRaw + lane * page_rows * kRow, tm, &full[st], g);
+  };
+  auto load_v = [&](int g) {
+    load(tm_v, KS + nv % VS, nv / VS, g);
+    if (ok) ++nv;
+  };
   while (ok && w.next()) {
     const int nT = w.tiles();
     const int32_t *row = a.c.table + static_cast<size_t>(w.i) * a.c.max_pages;
@@ -261,43 +287,42 @@ __device__ __forceinline__ void load_tiles(const PagedArgs &a, const Start &star
       return ((page * a.c.heads + w.h) << a.c.page_shift) / 8;
     };
     int g = group_of(w.j0);
-    for (int j = w.j0; ok && j < w.j0 + nT; ++j, ++n) {
+    for (int j = w.j0; ok && j < w.j0 + nT; ++j) {
       const int g_next = group_of(j + 1);     // its latency passes behind this tile's waits
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t pos = 2 * n + kv, st = pos % SLOTS, round = pos / SLOTS;
-        if (round > 0) ok = warp_wait(&empty[st], (round - 1) & 1, abort);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], kRaw);
+      load(tm_k, nk % KS, nk / KS, g);
+      if (!ok) break;
+      if constexpr (SCALES > 0) {
+        const bool live = g < none;
+        const uint32_t slot = nk % SCALES, pages = __ballot_sync(0xffffffffu, live);
+        if (lane == 0) {
+          pages_of[slot] = pages;
+          mbar_arrive_expect_tx(&sc_full[slot], __popc(pages) * page_rows * 2);
+        }
         __syncwarp();
-        if (lane < per_tile) tma_load_4d(ring + st * kRaw + lane * page_rows * kRow, kv ? tm_v : tm_k, &full[st], g);
-        issued = pos + 1;
-        if constexpr (SCALES > 0) {
-          if (kv == 0) {
-            const bool live = g < none;
-            const uint32_t slot = n % SCALES, pages = __ballot_sync(0xffffffffu, live);
-            if (lane == 0) {
-              pages_of[slot] = pages;
-              mbar_arrive_expect_tx(&sc_full[slot], __popc(pages) * page_rows * 2);
-            }
-            __syncwarp();
-            if (live) {
-              uint8_t *dst = scales + slot * (2 * kTile) + lane * page_rows;
-              bulk_load(dst, a.c.k_scale + static_cast<size_t>(g) * 8, page_rows, &sc_full[slot]);
-              bulk_load(dst + kTile, a.c.v_scale + static_cast<size_t>(g) * 8, page_rows, &sc_full[slot]);
-            }
-          }
+        if (live) {
+          uint8_t *dst = scales + slot * (2 * kTile) + lane * page_rows;
+          bulk_load(dst, a.c.k_scale + static_cast<size_t>(g) * 8, page_rows, &sc_full[slot]);
+          bulk_load(dst + kTile, a.c.v_scale + static_cast<size_t>(g) * 8, page_rows, &sc_full[slot]);
         }
       }
+      ++nk;
+#pragma unroll
+      for (int i = LEAD; i > 0; --i) lag[i] = lag[i - 1];
+      lag[0] = g;
+      if (nk > LEAD) load_v(lag[LEAD]);
       g = g_next;
     }
   }
+#pragma unroll
+  for (int i = LEAD - 1; i >= 0; --i)
+    if (ok && nk - nv == static_cast<uint32_t>(i) + 1) load_v(lag[i]);
   if (bad) atomicOr(a.status, DLLM_DEV_PAGE);
   // after an abort: the loads in flight land before the CTA's memory is given up
-  if (!ok && lane < SLOTS && lane < issued) mbar_drain(&full[lane], ((issued - 1 - lane) / SLOTS) & 1);
-  if constexpr (SCALES > 0) {
-    const uint32_t tiles = (issued + 1) / 2;
-    if (!ok && lane < SCALES && lane < tiles) mbar_drain(&sc_full[lane], ((tiles - 1 - lane) / SCALES) & 1);
+  if (!ok) {
+    if (lane < KS && lane < nk) mbar_drain(&full[lane], ((nk - 1 - lane) / KS) & 1);
+    if (lane < VS && lane < nv) mbar_drain(&full[KS + lane], ((nv - 1 - lane) / VS) & 1);
+    if constexpr (SCALES > 0)
+      if (lane < SCALES && lane < nk) mbar_drain(&sc_full[lane], ((nk - 1 - lane) / SCALES) & 1);
   }
 }
 

@@ -18,14 +18,15 @@
 // kernel joins them.
 //
 // Warp roles:
-//   warp 0      TMA: one box per page and tile; K and V tiles alternate in one ring
+//   warp 0      TMA: one box per page and tile (load_tiles)
 //   warp 1      S^T MMAs: K tile (A) x query rows (B) into an S buffer
 //   warp 2      O^T MMAs: V tile (A, transposed by its descriptor) x P (B)
 //   warp 3      walks the CTA's pieces ahead of the others
-//   warps 4..11 two softmax warpgroups, one key per thread, on alternate key
-//               tiles, each with references, sums and an O of its own that are
-//               merged at the end: the steps of one tile depend on each other,
-//               and two tiles under way hide that. They also stage the rows.
+//   warps 4..   softmax warpgroups (three, two with 32 rows), one key per
+//               thread, taking the key tiles in turn, each with references,
+//               sums and an O of its own that are merged at the end: the steps
+//               of one tile depend on each other, and several tiles under way
+//               hide that. They also stage the rows.
 // A reference maximum per row moves only when a score passes it by more than
 // 2^kLazy, so most tiles need no maximum at all, only the vote that nobody
 // passed it.
@@ -50,17 +51,17 @@ DLLM_DEFINE_STATUS(paged)
 
 namespace {
 
-constexpr int kPBuf = 2;         // one per softmax group
-constexpr int kSBuf = 4;
 constexpr int kAhead = 4;        // pieces prepared, the current one included
 
 template <int DH, bool FP8, int N>
 struct Cfg {
-  static constexpr int kThreads = 32 * 12;
+  static constexpr int kGroups = 2;                             // softmax warpgroups
+  static constexpr int kSBuf = 2 * kGroups, kPBuf = kGroups;
+  static constexpr int kThreads = 128 * (1 + kGroups);
   // registers a thread: what the TMA and MMA warps do not need goes to the
   // softmax groups (the sum is the launch's)
-  static constexpr int kRegsIssue = 104, kRegsSoft = 200;
-  static_assert(kRegsIssue + 2 * kRegsSoft <= 3 * 168, "registers");
+  static constexpr int kRegsIssue = 104, kRegsSoft = kGroups == 3 ? 136 : 200;
+  static_assert(kRegsIssue + kGroups * kRegsSoft <= (kGroups == 3 ? 4 * 128 : 3 * 168), "registers");
   static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);       // one K or V tile
   static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);        // eight cached rows
   static constexpr int kO = FP8 ? 2 * N : N;                    // columns of a group's O, and of a part of P
@@ -70,18 +71,20 @@ struct Cfg {
   static constexpr int kMisc = FP8 ? 12288 : 8192;              // row tables, scales, barriers, alignment
   static constexpr int kFixed = kPBuf * kP + kQ + kMisc;
   static constexpr int kMaxStages = (232448 - kFixed) / kRaw;
-  // even, so that K tiles have the even stages; 192 KB in flight are enough
-  static constexpr int kStages = (kMaxStages * kRaw > 196608 ? 196608 / kRaw : kMaxStages) & ~1;
+  static constexpr int kStages = kMaxStages * kRaw > 196608 ? 196608 / kRaw : kMaxStages;   // 192 KB in flight are enough
+  static constexpr int kKSt = kStages / 2, kVSt = kStages - kKSt, kLead = 2;
   static constexpr int kOffP = kStages * kRaw;
   static constexpr int kOffQ = kOffP + kPBuf * kP;
   static constexpr int kOffMisc = kOffQ + kQ;
   static constexpr int kBytes = kOffMisc + kMisc;
   // Scales of a tile's keys. A slot is written again once the K stage of the
-  // tile kStages / 2 before it is free: that tile's S^T is done, so the
-  // scores and scales of every tile up to kSBuf before that one are read.
-  static constexpr int kScaleSlots = FP8 ? kStages / 2 + kSBuf + 1 : 0;
-  static constexpr uint32_t kTmemCols = N * (FP8 ? 8 : 8);      // four S buffers of N, two O of kO
+  // tile kKSt before it is free: that tile's S^T is done, so the scores and
+  // scales of every tile up to kSBuf before that one are read.
+  static constexpr int kScaleSlots = FP8 ? kKSt + kSBuf + 1 : 0;
+  static constexpr int kUsedCols = kSBuf * N + kGroups * kO;    // S buffers and O
+  static constexpr uint32_t kTmemCols = kUsedCols <= 128 ? 128 : 256;
   static_assert(kStages >= 4 && kBytes <= 232448, "shared memory");
+  static_assert(kUsedCols <= kTmemCols, "tensor memory");
 };
 
 // What the softmax needs to know of the row tile's rows.
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(Cfg<DH, FP8, N>::kThreads, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a,
                   const int min_tiles) {
   using C = Cfg<DH, FP8, N>;
-  constexpr int kSt = C::kStages, kO = C::kO;
+  constexpr int kSt = C::kStages, kO = C::kO, kG = C::kGroups, kSBuf = C::kSBuf, kPBuf = C::kPBuf;
   // FP8: the V scale enters the weights, so they must not pass 2^2
   constexpr float kPass = FP8 ? 2.f : kLazy;
   extern __shared__ uint8_t smem_raw[];
@@ -229,10 +232,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   RowInfo<N> *info = reinterpret_cast<RowInfo<N> *>(misc);                // [piece parity]
   Piece *pieces = reinterpret_cast<Piece *>(info + 2);                    // [kAhead]
   float *m_s = reinterpret_cast<float *>(pieces + kAhead);                // [group][N] reference maxima
-  float *corr_s = m_s + 2 * N;                                            // [group][N]
-  float *red_s = corr_s + 2 * N;                                          // [quarter][group][N]
-  int *eref_s = reinterpret_cast<int *>(red_s + 8 * N);                   // [group], [quarter][group] exponents of V scales
-  uint8_t *scales = reinterpret_cast<uint8_t *>(eref_s + 12);             // [kScaleSlots][K, V][kTile]
+  float *corr_s = m_s + kG * N;                                           // [group][N]
+  float *red_s = corr_s + kG * N;                                         // [quarter][group][N]
+  int *eref_s = reinterpret_cast<int *>(red_s + 4 * kG * N);              // [group], [quarter][group] exponents of V scales
+  uint8_t *scales = reinterpret_cast<uint8_t *>(eref_s + 16);             // [kScaleSlots][K, V][kTile]
   uint32_t *pages_of = reinterpret_cast<uint32_t *>(scales + C::kScaleSlots * 2 * kTile);   // [kScaleSlots]: pages the tile has
   uint64_t *full = reinterpret_cast<uint64_t *>(pages_of + ((C::kScaleSlots + 1) & ~1));    // [kSt] stage loaded
   uint64_t *empty = full + kSt;             // [kSt] stage read by its MMAs
@@ -250,11 +253,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   Start *start = reinterpret_cast<Start *>(s_scan + 16);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert(2 * sizeof(RowInfo<N>) + kAhead * sizeof(Piece) + 12 * N * 4 + 48 + C::kScaleSlots * (2 * kTile + 12) + 4 +
+  static_assert(2 * sizeof(RowInfo<N>) + kAhead * sizeof(Piece) + 6 * kG * N * 4 + 64 + C::kScaleSlots * (2 * kTile + 12) + 4 +
                         (2 * kSt + 2 * kSBuf + 2 * kPBuf + 3 * kAhead + 2) * 8 + 128 + sizeof(Start) + 8 <=
                     C::kMisc - 1024,
                 "row tables and barriers");
-  static_assert(sizeof(Piece) % 16 == 0 && (12 * N * 4 + 48) % 16 == 0, "scales, 16-byte aligned for the bulk loads");
+  static_assert(sizeof(Piece) % 16 == 0 && (6 * kG * N * 4 + 64) % 16 == 0 && 5 * kG <= 16, "scales, 16-byte aligned for the bulk loads");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
@@ -265,11 +268,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     for (int b = 0; b < C::kScaleSlots; ++b) mbar_init(&sc_full[b], 1);
     for (int b = 0; b < kAhead; ++b) {
       mbar_init(&piece_full[b], 1);
-      mbar_init(&piece_free[b], 8 + 2);   // the warps that read the piece
+      mbar_init(&piece_free[b], 4 * kG + 2);   // the warps that read the piece
       mbar_init(&q_full[b], 8);
     }
     mbar_init(o_full, 1);
-    mbar_init(o_free, 8);
+    mbar_init(o_free, 8);             // the groups that read O
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm_k);
@@ -291,8 +294,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   if (warp < 4) {
     reg_dealloc<C::kRegsIssue>();
     if (warp == 0) {
-      load_tiles<DH, FP8 ? 1 : 2, kSt, C::kScaleSlots>(a, *start, N, &tm_k, &tm_v, smem, full, empty, scales, pages_of, sc_full,
-                                                       abort_flag, lane);
+      load_tiles<DH, FP8 ? 1 : 2, C::kKSt, C::kVSt, C::kLead, C::kScaleSlots>(a, *start, N, &tm_k, &tm_v, smem, full, empty, scales,
+                                                                              pages_of, sc_full, abort_flag, lane);
     } else if (warp == 1) {
       // ----------------------------------------------------------- S^T MMAs
       // (one elected thread through the whole loop: see paged_rows.cu)
@@ -307,8 +310,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           const int nT = pieces[pi].tiles;
           const uint32_t sq = smem_u32(smem + C::kOffQ);
           for (int j = 0; ok && j < nT; ++j, ++n) {
-            const uint32_t pos = 2 * n, st = pos % kSt, b = n % kSBuf;
-            ok = mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+            const uint32_t st = n % C::kKSt, b = n % kSBuf;
+            ok = mbar_wait(&full[st], (n / C::kKSt) & 1, abort_flag);
             if (ok && n >= kSBuf) ok = mbar_wait(&s_free[b], (n / kSBuf - 1) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -348,14 +351,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           if (!ok || !pieces[pi].more) break;
           const int nT = pieces[pi].tiles;
           for (int j = 0; ok && j < nT; ++j, ++n) {
-            const uint32_t pos = 2 * n + 1, st = pos % kSt, b = n % kPBuf;
+            const uint32_t st = C::kKSt + n % C::kVSt, b = n % kPBuf;
             if (j == 0 && o_seg > 0) ok = mbar_wait(o_free, (o_seg - 1) & 1, abort_flag);
-            ok = ok && mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+            ok = ok && mbar_wait(&full[st], (n / C::kVSt) & 1, abort_flag);
             ok = ok && mbar_wait(&p_full[b], (n / kPBuf) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t t_d = t_o + (n & 1) * kO;
-            const uint32_t add = j > 1;   // the first tile of each group's accumulator
+            const uint32_t t_d = t_o + n % kG * kO;
+            const uint32_t add = j >= kG;   // the first tile of each group's accumulator
             const uint32_t sv = smem_u32(smem + st * C::kRaw), sp = smem_u32(smem + C::kOffP + b * C::kP);
             if constexpr (!FP8) {
               const uint64_t dv = sw128_desc(sv, 1024, C::kGroup8), dp = plain_desc(sp, 128, 2048);
@@ -429,7 +432,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     auto stage = [&](uint32_t seg) {           // piece seg's query rows
       const uint32_t pi = seg % kAhead;
       mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
-      if (!pieces[pi].more) return;
+      if (wg >= 2 || !pieces[pi].more) return;
       stage_queries<DH, FP8, N>(a, pieces[pi], smem + C::kOffQ, info[seg & 1], threadIdx.x - 128);
       fence_proxy_async_smem();
       __syncwarp();
@@ -439,7 +442,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     for (uint32_t seg = 0;; ++seg) {
       const uint32_t pi = seg % kAhead;
       // all of both groups go on or none does; the rows' info is written, the last piece's maxima are read
-      if (bar_any(3, 256, !mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag))) break;
+      if (bar_any(4, 128 * kG, !mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag))) break;
       const Piece &pc = pieces[pi];
       if (!pc.more) break;
       const RowInfo<N> &ri = info[seg & 1];
@@ -453,7 +456,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       named_bar_sync(1 + wg, 128);
       bool first = true;                    // of the group's tiles
       for (int j = 0; j < nT; ++j, ++n) {
-        if ((n & 1) != wg) continue;
+        if (n % kG != wg) continue;
         const uint32_t b = n % kSBuf, pb = n % kPBuf;
         const int key0 = tl.tile(j0 + j) * kTile, u = key0 + key;
         // every row of the tile sees every key of it?
@@ -512,18 +515,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
           for (int e = 0; e < N; ++e) v[e] = x[e];
           const float most = reduce_columns<N>(v, lane, maxop);
-          if (lane < N) red_s[quarter * (2 * N) + g0 + lane] = most;
+          if (lane < N) red_s[quarter * (kG * N) + g0 + lane] = most;
           if constexpr (FP8) {
             const int e = __reduce_max_sync(0xffffffffu, vexp);
-            if (lane == 0) eref_s[2 + quarter * 2 + wg] = e;
+            if (lane == 0) eref_s[kG + quarter * kG + wg] = e;
           }
           named_bar_sync(1 + wg, 128);
           int e_new = eref;
           if constexpr (FP8)
-            e_new = max(max(max(eref_s[2 + wg], eref_s[4 + wg]), max(eref_s[6 + wg], eref_s[8 + wg])), eref);
+            e_new = max(max(max(eref_s[kG + wg], eref_s[2 * kG + wg]), max(eref_s[3 * kG + wg], eref_s[4 * kG + wg])), eref);
           if (tid < N) {
             const int e = g0 + tid;
-            const float mx = fmaxf(fmaxf(red_s[e], red_s[2 * N + e]), fmaxf(red_s[4 * N + e], red_s[6 * N + e]));
+            const float mx = fmaxf(fmaxf(red_s[e], red_s[kG * N + e]), fmaxf(red_s[2 * kG * N + e], red_s[3 * kG * N + e]));
             const float old = m_s[e], now = mx > old + kPass ? mx : old;
             corr_s[e] = now == old ? 1.f : ex2_approx(old - now);
             m_s[e] = now;
@@ -536,7 +539,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           }
           if (!first) {
             // O holds exactly the group's tiles before this one once the MMAs of the last are done
-            mbar_wait(&p_free[pb], ((n - 2) / kPBuf) & 1, abort_flag);
+            mbar_wait(&p_free[pb], (n / kPBuf - 1) & 1, abort_flag);
             tc_fence_after();
             const float ev = FP8 ? ex2_approx(static_cast<float>(eref - e_new)) : 1.f;
 #pragma unroll
@@ -600,8 +603,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         // rows of V that no query row sees may hold anything, and 0 * NaN is not 0
         if (!seen) {
-          const uint32_t pos = 2 * n + 1, st = pos % kSt;
-          mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+          const uint32_t st = C::kKSt + n % C::kVSt;
+          mbar_wait(&full[st], (n / C::kVSt) & 1, abort_flag);
           // (the swizzles permute 16-byte pieces within a row)
           if constexpr (FP8) {
             uint8_t *sv = smem + st * C::kRaw + key * DH;
@@ -623,30 +626,37 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       // the next piece's rows are staged before this one's results are
       // written, so that its scores run meanwhile: every S^T of this piece
       // is done
-      named_bar_sync(3, 256);
+      named_bar_sync(4, 128 * kG);
       stage(seg + 1);
       const float part = reduce_columns<N>(l, lane, addop);
-      if (lane < N) red_s[quarter * (2 * N) + g0 + lane] = part;
+      if (lane < N) red_s[quarter * (kG * N) + g0 + lane] = part;
       if (FP8 && tid == 0) eref_s[wg] = eref;
       named_bar_sync(1 + wg, 128);
       if (tid < N) {
         const int e = g0 + tid;
-        corr_s[e] = (red_s[e] + red_s[2 * N + e]) + (red_s[4 * N + e] + red_s[6 * N + e]);
+        corr_s[e] = (red_s[e] + red_s[kG * N + e]) + (red_s[2 * kG * N + e] + red_s[3 * kG * N + e]);
       }
       if (nT > 0) {
         mbar_wait(o_full, o_seg & 1, abort_flag);
         ++o_seg;
         tc_fence_after();
       }
-      named_bar_sync(3, 256);
+      named_bar_sync(4, 128 * kG);
+      if (wg < 2) {
       // rows [out0, out0 + kOut): maximum, sum, and what the groups' O count for
+      auto highest = [&](int e) {
+        float m = m_s[e];
+#pragma unroll
+        for (int g = 1; g < kG; ++g) m = fmaxf(m, m_s[g * N + e]);
+        return m;
+      };
       uint32_t o[kOut];
 #pragma unroll
       for (int e = 0; e < kOut; ++e) o[e] = 0;
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        // a single tile leaves the other group without an O
-        if (!(nT > 1 || (nT == 1 && ((n - 1) & 1) == g))) continue;
+      for (int g = 0; g < kG; ++g) {
+        // few tiles leave groups without an O
+        if ((g + kG - (n - nT) % kG) % kG >= static_cast<uint32_t>(nT)) continue;
         uint32_t y[kOut], z[kOut];
         tmem_load<kOut>(t_o + lane_base + g * kO + out0, y);
         if constexpr (FP8) tmem_load<kOut>(t_o + lane_base + g * kO + N + out0, z);
@@ -654,7 +664,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const float ev = FP8 ? scale_of(max(eref_s[g] + 127, 0)) : 1.f;
 #pragma unroll
         for (int e = 0; e < kOut; ++e) {
-          const float f = ex2_approx(m_s[g * N + out0 + e] - fmaxf(m_s[out0 + e], m_s[N + out0 + e]));
+          const float f = ex2_approx(m_s[g * N + out0 + e] - highest(out0 + e));
           float w = __uint_as_float(y[e]);
           if constexpr (FP8) w = (w * 0x1p-13f + __uint_as_float(z[e]) * 0x1p-25f) * ev;
           o[e] = __float_as_uint(__uint_as_float(o[e]) + w * f);
@@ -666,8 +676,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (lane == 0) mbar_arrive(o_free);
       }
       auto merged = [&](int e) {   // {maximum, sum} of row e
-        const float m = fmaxf(m_s[e], m_s[N + e]);
-        return make_float2(m, corr_s[e] * ex2_approx(m_s[e] - m) + corr_s[N + e] * ex2_approx(m_s[N + e] - m));
+        const float m = highest(e);
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < kG; ++g) sum += corr_s[g * N + e] * ex2_approx(m_s[g * N + e] - m);
+        return make_float2(m, sum);
       };
       // M = 64: rows 16 q .. 16 q + 15 lie in the first 16 lanes of quarter q
       const int dc = DH == 128 ? key : quarter * 16 + lane;
@@ -695,6 +708,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
           for (int e = 0; e < kOut; ++e) po[e * DH] = __uint_as_float(o[e]);
         if (tid < kOut) a.part_ml[slot * N + out0 + tid] = merged(out0 + tid);
+      }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&piece_free[pi]);

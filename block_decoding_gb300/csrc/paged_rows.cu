@@ -73,8 +73,11 @@ struct RowsCfg {
   static constexpr int kMisc = 1984 + kScaleBytes;            // + 1024 of alignment
   static constexpr int kMax = (232448 - 1024 - kQs * kQ - kConv - kMisc) / kRaw;
   static constexpr int kCap = 196608 / kRaw < 12 ? 196608 / kRaw : 12;   // 192 KB in flight are enough
-  static constexpr int kStages = (kMax < kCap ? kMax : kCap) & (FP8 ? ~1 : ~0);
-  static constexpr int kScaleSlots = FP8 ? kStages / 2 + 3 : 0;
+  static constexpr int kStages = kMax < kCap ? kMax : kCap;
+  static constexpr int kKSt = kStages / 2, kVSt = kStages - kKSt, kLead = 0;
+  // a slot is written again once the scores of the tile kKSt before it are
+  // done: the factors of every tile up to two before that one are computed
+  static constexpr int kScaleSlots = FP8 ? kKSt + 3 : 0;
   static constexpr int kOffConv = kStages * kRaw;
   static constexpr int kOffQ = kOffConv + kConv;
   static constexpr int kOffMisc = kOffQ + kQs * kQ;
@@ -177,7 +180,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSt; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], FP8 && (s & 1) ? 4 : 1);
+      mbar_init(&empty[s], FP8 && s >= C::kKSt ? 4 : 1);
     }
     for (int b = 0; b < 2; ++b) { mbar_init(&s_full[b], 1); mbar_init(&h_done[b], 1); }
     for (int b = 0; b < 4; ++b) mbar_init(&p_full[b], 4);
@@ -213,8 +216,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   if (warp < 4) {
     reg_dealloc<C::kRegsIssue>();
     if (warp == 0) {
-      load_tiles<DH, FP8 ? 1 : 2, kSt, C::kScaleSlots>(a, *start, C::kRows, &tm_k, &tm_v, smem, full, empty, scales, pages_of,
-                                                       sc_full, abort_flag, lane);
+      load_tiles<DH, FP8 ? 1 : 2, C::kKSt, C::kVSt, C::kLead, C::kScaleSlots>(a, *start, C::kRows, &tm_k, &tm_v, smem, full, empty,
+                                                                              scales, pages_of, sc_full, abort_flag, lane);
     } else if (warp == 1) {
       // ----------------------------------------------------------- MMAs
       // (one elected thread through the whole loop: a warp that stays
@@ -232,8 +235,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         ok = mbar_wait(&q_full[pi], (seg / kAhead) & 1, abort_flag);
         // scores of stream s's k-th tile
         auto scores = [&](int s, int k) {
-          const uint32_t n = n0 + (two ? k : 2 * k + s), pos = 2 * n, st = pos % kSt;
-          ok = ok && mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+          const uint32_t n = n0 + (two ? k : 2 * k + s), st = n % C::kKSt;
+          ok = ok && mbar_wait(&full[st], (n / C::kKSt) & 1, abort_flag);
           tc_fence_after();
           if (ok) {
             const uint32_t sk = smem_u32(smem + st * C::kRaw), t_s = tmem + s * 128;
@@ -261,10 +264,10 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         };
         // O of stream s += P V of its k-th tile
         auto values = [&](int s, int k) {
-          const uint32_t n = n0 + (two ? k : 2 * k + s), pos = 2 * n + 1, st = pos % kSt;
+          const uint32_t n = n0 + (two ? k : 2 * k + s), st = C::kKSt + n % C::kVSt;
           const uint32_t ns = cnt[s] + k;
           if (k == 0 && s == 0 && o_seg > 0) ok = ok && mbar_wait(o_free, (o_seg - 1) & 1, abort_flag);
-          if constexpr (!FP8) ok = ok && mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+          if constexpr (!FP8) ok = ok && mbar_wait(&full[st], (n / C::kVSt) & 1, abort_flag);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             ok = ok && mbar_wait(&p_full[s * 2 + half], ns & 1, abort_flag);
@@ -347,7 +350,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const TileList tl = pieces[pi].t;
         const int j0 = pieces[pi].j0, nT = pieces[pi].tiles;
         for (int j = 0; j < nT; ++j, ++n) {
-          const uint32_t pos = 2 * n + 1, st = pos % kSt, slot = n % C::kScaleSlots;
+          const uint32_t st = C::kKSt + n % C::kVSt, slot = n % C::kScaleSlots;
           const int key0 = tl.tile(j0 + j) * kTile;
           auto seen = [&](int key) { return key0 + key < tl.hi && (key0 + key >= tl.lo || key0 + key < a.sinks); };
           // a key without a page is a row of zeros, one that no row sees may have any scale
@@ -359,7 +362,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           col_s[(n % 4) * kTile + t] = a.scale_log2 * scale_of(byte_of(t, 0));
           __syncwarp();
           if (lane == 0) mbar_arrive(&col_full[n % 4]);
-          mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+          mbar_wait(&full[st], (n / C::kVSt) & 1, abort_flag);
 #pragma unroll 1
           for (int half = 0; half < kTile / kConvKeys; ++half) {
             const uint32_t cn = n * (kTile / kConvKeys) + half, cb = cn % C::kCBuf;
@@ -443,8 +446,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           // rows of V that no query row sees may hold anything, and 0 * NaN is not 0
           const int u = key0 + tid;
           if ((!two || s == 0) && !(u < tl.hi && (u >= tl.lo || u < a.sinks))) {
-            const uint32_t pos = 2 * n + 1, st = pos % kSt;
-            mbar_wait(&full[st], (pos / kSt) & 1, abort_flag);
+            const uint32_t st = C::kKSt + n % C::kVSt;
+            mbar_wait(&full[st], (n / C::kVSt) & 1, abort_flag);
             uint8_t *sv = smem + st * C::kRaw + (tid / 8) * C::kGroup8 + (tid % 8) * 128;
 #pragma unroll
             for (int e = 0; e < DH / 8; ++e)

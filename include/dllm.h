@@ -473,8 +473,8 @@ typedef struct {
  *         to the next (>= heads*dh, a multiple of 8), 16-byte aligned: the
  *         K and V columns of one projection's output serve as they are
  *   off   int32 [B+1], as q_off of dllm_block_attn (rows it names beyond
- *         `rows` are skipped, DLLM_DEV_OFFSETS; rows it names in no request
- *         are not read); pos0 int32 [B]; page_table int32 [B][max_pages]
+ *         `rows` are skipped, DLLM_DEV_OFFSETS; rows in no request are
+ *         not stored); pos0 int32 [B]; page_table int32 [B][max_pages]
  * Slots that no row is stored in keep their bytes. Two rows for one slot
  * leave it unspecified. B <= 4096. No workspace. */
 dllm_status dllm_kv_write(const dllm_kv_pages *pages /* host */,
