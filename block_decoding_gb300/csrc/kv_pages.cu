@@ -6,10 +6,7 @@
 // of K and 16 of V each: two 16-byte chunks half a row apart, so that the
 // lanes of a row read and write contiguous runs. A block takes neighbouring
 // rows of up to four neighbouring heads: runs of several rows on the pages'
-// side, of several heads on the other. Writing asks for the rows before it
-// looks their places up; reading looks up several rows' places at once.
-#include <type_traits>
-
+// side, of several heads on the other.
 #include "pages.cuh"
 
 namespace dllm {
@@ -19,7 +16,7 @@ DLLM_DEFINE_STATUS(kv)
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWriteUnits = 2, kReadUnits = 2;   // rows of one thread
+constexpr int kHeads = 4;   // heads of one block, at most
 
 struct MoveArgs {
   KvPages c;
@@ -81,30 +78,24 @@ __device__ __forceinline__ int quantise_row(const uint4 &a, const uint4 &b, uint
   return m >= 0x7f80u ? 255 : byte;
 }
 
-// The rows and heads of a block: unit u (LPR lanes each) has head h0 + u % HB
-// of row r0 + u / HB and of U - 1 more rows, `per` rows apart.
-struct Place {
-  int r, h, per;
-};
-
-template <int LPR, int U>
-__device__ __forceinline__ Place place_of(const MoveArgs &g) {
-  const int hb = min(g.c.heads, 4), groups = (g.c.heads + hb - 1) / hb;
+// This thread's row and head: unit u (LPR lanes each) of a block has head
+// h0 + u % hb of row r0 + u / hb. No row: 2^30.
+template <int LPR>
+__device__ __forceinline__ void place_of(const MoveArgs &g, int &r, int &h) {
+  const int hb = min(g.c.heads, kHeads), groups = (g.c.heads + hb - 1) / hb;
   const int u = threadIdx.x / LPR, per = (kThreads / LPR) / hb;
   const int rg = blockIdx.x / groups, hg = blockIdx.x - rg * groups;
-  Place p{rg * (per * U) + u / hb, hg * hb + u % hb, per};
-  if (u >= per * hb || p.h >= g.c.heads) p.r = 0x40000000;   // none
-  return p;
+  r = rg * per + u / hb;
+  h = hg * hb + u % hb;
+  if (u >= per * hb || h >= g.c.heads) r = 1 << 30;
 }
 
-// Cache row of row r for head h: -1 when it is in no request or has no place
-// (reported). `i` is where the search starts and ends.
-__device__ __forceinline__ int find_row(const MoveArgs &g, int r, int h, int &i) {
+// Cache row of row r for head h: -1 when it is in no request, -2 when it has
+// no place (reported).
+__device__ __forceinline__ int find_row(const MoveArgs &g, int r, int h) {
   if (r >= g.rows) return -1;
-  if (i < 0) i = request_of(g.off, g.B, r);
+  const int i = request_of(g.off, g.B, r);
   if (i < 0) return -1;
-  while (i + 1 < g.B && g.off[i + 1] <= r) ++i;
-  if (r >= g.off[i + 1]) return -1;
   const long long u = static_cast<long long>(g.pos0[i]) + (r - g.off[i]);
   const int row = u < 0 || u > 0x7fffffffll ? -1 : page_row(g.c, i, static_cast<int>(u));
   if (row < 0) {
@@ -116,48 +107,43 @@ __device__ __forceinline__ int find_row(const MoveArgs &g, int r, int h, int &i)
 
 template <int DH, bool FP8>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const MoveArgs g) {
-  constexpr int LPR = DH / 16, U = kWriteUnits;
+  constexpr int LPR = DH / 16;
   pdl_trigger();
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0 && (g.off[0] < 0 || g.off[g.B] > g.rows)) atomicOr(g.status, DLLM_DEV_OFFSETS);
-  const Place p = place_of<LPR, U>(g);
   const int l = threadIdx.x % LPR;
-  uint4 ka[U], kb[U], va[U], vb[U];
-#pragma unroll
-  for (int j = 0; j < U; ++j) {
-    const int r = p.r + j * p.per;
-    ka[j] = kb[j] = va[j] = vb[j] = make_uint4(0, 0, 0, 0);
-    if (r < g.rows) {
-      const uint4 *ks = reinterpret_cast<const uint4 *>(g.k + r * g.k_stride + p.h * DH);
-      const uint4 *vs = reinterpret_cast<const uint4 *>(g.v + r * g.v_stride + p.h * DH);
-      ka[j] = __ldg(ks + l); kb[j] = __ldg(ks + l + LPR);
-      va[j] = __ldg(vs + l); vb[j] = __ldg(vs + l + LPR);
-    }
+  int r, h;
+  place_of<LPR>(g, r, h);
+  uint4 ka = make_uint4(0, 0, 0, 0), kb = ka, va = ka, vb = ka;
+  if (r < g.rows) {
+    const uint4 *ks = reinterpret_cast<const uint4 *>(g.k + r * g.k_stride + h * DH);
+    const uint4 *vs = reinterpret_cast<const uint4 *>(g.v + r * g.v_stride + h * DH);
+    ka = __ldg(ks + l); kb = __ldg(ks + l + LPR);
+    va = __ldg(vs + l); vb = __ldg(vs + l + LPR);
   }
-  int i = -1, row[U];
-#pragma unroll
-  for (int j = 0; j < U; ++j) row[j] = find_row(g, p.r + j * p.per, p.h, i);
-#pragma unroll
-  for (int j = 0; j < U; ++j) {
-    if constexpr (FP8) {
-      uint2 qa, qb, pa, pb;
-      const int kbyte = quantise_row<LPR>(ka[j], kb[j], qa, qb), vbyte = quantise_row<LPR>(va[j], vb[j], pa, pb);
-      if (row[j] >= 0) {
-        uint2 *d = reinterpret_cast<uint2 *>(g.c.k + static_cast<size_t>(row[j]) * DH);
-        d[l] = qa; d[l + LPR] = qb;
-        d = reinterpret_cast<uint2 *>(g.c.v + static_cast<size_t>(row[j]) * DH);
-        d[l] = pa; d[l + LPR] = pb;
-        if (l == 0) {
-          g.c.k_scale[row[j]] = static_cast<uint8_t>(kbyte);
-          g.c.v_scale[row[j]] = static_cast<uint8_t>(vbyte);
-        }
-      }
-    } else if (row[j] >= 0) {
-      uint4 *d = reinterpret_cast<uint4 *>(g.c.k + static_cast<size_t>(row[j]) * (DH * 2));
-      d[l] = ka[j]; d[l + LPR] = kb[j];
-      d = reinterpret_cast<uint4 *>(g.c.v + static_cast<size_t>(row[j]) * (DH * 2));
-      d[l] = va[j]; d[l + LPR] = vb[j];
+  const int row = find_row(g, r, h);
+  const size_t at = static_cast<size_t>(max(row, 0));
+  if constexpr (FP8) {
+    uint2 qa, qb;
+    const int kbyte = quantise_row<LPR>(ka, kb, qa, qb);
+    if (row >= 0) {
+      uint2 *d = reinterpret_cast<uint2 *>(g.c.k + at * DH);
+      d[l] = qa; d[l + LPR] = qb;
     }
+    const int vbyte = quantise_row<LPR>(va, vb, qa, qb);
+    if (row >= 0) {
+      uint2 *d = reinterpret_cast<uint2 *>(g.c.v + at * DH);
+      d[l] = qa; d[l + LPR] = qb;
+      if (l == 0) {
+        g.c.k_scale[at] = static_cast<uint8_t>(kbyte);
+        g.c.v_scale[at] = static_cast<uint8_t>(vbyte);
+      }
+    }
+  } else if (row >= 0) {
+    uint4 *d = reinterpret_cast<uint4 *>(g.c.k + at * (DH * 2));
+    d[l] = ka; d[l + LPR] = kb;
+    d = reinterpret_cast<uint4 *>(g.c.v + at * (DH * 2));
+    d[l] = va; d[l + LPR] = vb;
   }
 }
 
@@ -176,43 +162,36 @@ __device__ __forceinline__ uint4 restore8(uint2 q, float f) {
 
 template <int DH, bool FP8>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const MoveArgs g) {
-  constexpr int LPR = DH / 16, U = kReadUnits;
+  constexpr int LPR = DH / 16;
   pdl_trigger();
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0 && (g.off[0] < 0 || g.off[g.B] > g.rows)) atomicOr(g.status, DLLM_DEV_OFFSETS);
-  const Place p = place_of<LPR, U>(g);
   const int l = threadIdx.x % LPR;
-  int i = -1, row[U];
-#pragma unroll
-  for (int j = 0; j < U; ++j) row[j] = find_row(g, p.r + j * p.per, p.h, i);
-  using Vec = typename std::conditional<FP8, uint2, uint4>::type;
-  Vec ka[U], kb[U], va[U], vb[U];
-  uint32_t kf[U], vf[U];
-#pragma unroll
-  for (int j = 0; j < U; ++j) {
-    ka[j] = kb[j] = va[j] = vb[j] = Vec{};
-    kf[j] = vf[j] = 127;
-    if (row[j] >= 0) {
-      const Vec *ks = reinterpret_cast<const Vec *>(g.c.k + static_cast<size_t>(row[j]) * (DH * (FP8 ? 1 : 2)));
-      const Vec *vs = reinterpret_cast<const Vec *>(g.c.v + static_cast<size_t>(row[j]) * (DH * (FP8 ? 1 : 2)));
-      ka[j] = __ldg(ks + l); kb[j] = __ldg(ks + l + LPR);
-      va[j] = __ldg(vs + l); vb[j] = __ldg(vs + l + LPR);
-      if constexpr (FP8) { kf[j] = g.c.k_scale[row[j]]; vf[j] = g.c.v_scale[row[j]]; }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < U; ++j) {
-    if (row[j] == -1) continue;   // in no request; a row without a place (-2) reads as zeros
-    uint4 *kd = reinterpret_cast<uint4 *>(g.k + (p.r + j * p.per) * g.k_stride + p.h * DH);
-    uint4 *vd = reinterpret_cast<uint4 *>(g.v + (p.r + j * p.per) * g.v_stride + p.h * DH);
+  int r, h;
+  place_of<LPR>(g, r, h);
+  const int row = find_row(g, r, h);
+  if (row == -1) return;   // a row without a place (-2) reads as zeros
+  uint4 ka = make_uint4(0, 0, 0, 0), kb = ka, va = ka, vb = ka;
+  if (row >= 0) {
+    const size_t at = static_cast<size_t>(row);
     if constexpr (FP8) {
-      kd[l] = restore8(ka[j], scale_of(kf[j])); kd[l + LPR] = restore8(kb[j], scale_of(kf[j]));
-      vd[l] = restore8(va[j], scale_of(vf[j])); vd[l + LPR] = restore8(vb[j], scale_of(vf[j]));
+      const uint2 *ks = reinterpret_cast<const uint2 *>(g.c.k + at * DH);
+      const uint2 *vs = reinterpret_cast<const uint2 *>(g.c.v + at * DH);
+      const uint2 qa = __ldg(ks + l), qb = __ldg(ks + l + LPR), pa = __ldg(vs + l), pb = __ldg(vs + l + LPR);
+      const float kf = scale_of(g.c.k_scale[at]), vf = scale_of(g.c.v_scale[at]);
+      ka = restore8(qa, kf); kb = restore8(qb, kf);
+      va = restore8(pa, vf); vb = restore8(pb, vf);
     } else {
-      kd[l] = ka[j]; kd[l + LPR] = kb[j];
-      vd[l] = va[j]; vd[l + LPR] = vb[j];
+      const uint4 *ks = reinterpret_cast<const uint4 *>(g.c.k + at * (DH * 2));
+      const uint4 *vs = reinterpret_cast<const uint4 *>(g.c.v + at * (DH * 2));
+      ka = __ldg(ks + l); kb = __ldg(ks + l + LPR);
+      va = __ldg(vs + l); vb = __ldg(vs + l + LPR);
     }
   }
+  uint4 *d = reinterpret_cast<uint4 *>(g.k + r * g.k_stride + h * DH);
+  d[l] = ka; d[l + LPR] = kb;
+  d = reinterpret_cast<uint4 *>(g.v + r * g.v_stride + h * DH);
+  d[l] = va; d[l + LPR] = vb;
 }
 
 dllm_status move(bool write, const dllm_kv_pages *pages, uint16_t *k, uint16_t *v, long long k_stride,
@@ -235,8 +214,8 @@ dllm_status move(bool write, const dllm_kv_pages *pages, uint16_t *k, uint16_t *
   g.rows = rows; g.B = B; g.off = off; g.pos0 = pos0;
   cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&g.status), g_status_kv);
   if (e != cudaSuccess) return cuda_error(e);
-  const int hb = pages->heads < 4 ? pages->heads : 4, groups = (pages->heads + hb - 1) / hb;
-  const int per_block = kThreads / (pages->dh / 16) / hb * (write ? kWriteUnits : kReadUnits);   // rows
+  const int hb = pages->heads < kHeads ? pages->heads : kHeads, groups = (pages->heads + hb - 1) / hb;
+  const int per_block = kThreads / (pages->dh / 16) / hb;   // rows
   const long long blocks = (static_cast<long long>(rows) + per_block - 1) / per_block * groups;
   if (blocks > 0x7fffffffll) return DLLM_ERR_UNSUPPORTED;
   const bool fp8 = pages->type == DLLM_KV_E4M3;

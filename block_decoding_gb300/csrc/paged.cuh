@@ -18,7 +18,7 @@ struct PagedArgs {
   int B, Hq, group, max_q, max_kv, q_rows;
   float scale_log2;
   int left, right, sinks;
-  int uniform;      // > 0: no item is divided
+  int whole;        // no item may be divided (there is no workspace)
   unsigned int *status;
   // partial results of items whose keys several CTAs share
   float *part_o;
@@ -94,11 +94,8 @@ __device__ __forceinline__ TileList tile_list(const PagedArgs &a, const Extent &
 }
 
 // Tiles that every row tile of the request is given (at least one, so that
-// rows without keys are written too): no fewer than any of them needs. With
-// `uniform` every item of the call is given that many, so that equal pieces
-// of whole items divide none.
+// rows without keys are written too): no fewer than any of them needs.
 __device__ __forceinline__ int tiles_per_item(const PagedArgs &a, const Extent &x, int n) {
-  if (a.uniform) return a.uniform;
   int lo, hi;
   visible(a, x.pos + x.W - 1, x.L, lo, hi);
   int most = (hi + kTile - 1) / kTile;
@@ -115,8 +112,10 @@ __device__ __forceinline__ int tiles_per_item(const PagedArgs &a, const Extent &
 // more for what every item costs however short it is (rows staged, results
 // written: about as much as so many tiles; without it a CTA with many short
 // items took 40 % longer than the others). It is cut into gridDim.x equal
-// stretches (of whole items with `uniform`).
-constexpr int kItemCost = 6;
+// stretches. Where it takes no longer that way, items stay whole: then every
+// item is as long as the longest, and stretches are so many items. (Dividing
+// costs an item's fixed part twice, and the joining about kJoinCost tiles.)
+constexpr int kItemCost = 6, kJoinCost = 4;
 
 // Where this CTA's stretch starts.
 struct Start {
@@ -124,49 +123,76 @@ struct Start {
   long long left;       // its length
   long long per;        // the length of every stretch
   int i;
+  int whole;            // > 0: tiles of every item, none is divided
 };
 
-__device__ __forceinline__ long long request_length(const PagedArgs &a, int i, int n_rows, bool report) {
-  const Extent x = paged_extent(a, i, report);
-  const long long items = static_cast<long long>((x.W * a.group + n_rows - 1) / n_rows) * a.c.heads;
-  return items ? items * (tiles_per_item(a, x, n_rows) + kItemCost) : 0;
-}
+struct Scan {           // sums and maxima of the warps
+  long long length[16];
+  int items[16], most[16];
+};
 
-// Every thread of the CTA takes part; s_scan holds 32 values.
-__device__ __forceinline__ void find_start(const PagedArgs &a, int n_rows, int min_tiles, long long *s_scan,
-                                           Start *s_start) {
+// Every thread of the CTA takes part.
+__device__ __forceinline__ void find_start(const PagedArgs &a, int n_rows, int min_tiles, Scan *s_scan, Start *s_start) {
   const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunk = (a.B + nt - 1) / nt;
   const int i0 = tid * chunk, i1 = min(a.B, i0 + chunk);
-  long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += request_length(a, i, n_rows, blockIdx.x == 0);
-  long long incl = mine;
+  auto request = [&](int i, bool report, int &items, int &n) {
+    const Extent x = paged_extent(a, i, report);
+    items = (x.W * a.group + n_rows - 1) / n_rows * a.c.heads;
+    n = items ? tiles_per_item(a, x, n_rows) : 0;
+  };
+  long long length = 0;
+  int items = 0, most = 0;
+  for (int i = i0; i < i1; ++i) {
+    int k, n;
+    request(i, blockIdx.x == 0, k, n);
+    items += k;
+    length += static_cast<long long>(k) * (n + kItemCost);
+    most = max(most, n);
+  }
+  long long length_up = length;
+  int items_up = items;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const long long y = __shfl_up_sync(0xffffffffu, length_up, o);
+    const int z = __shfl_up_sync(0xffffffffu, items_up, o);
+    if (lane >= o) { length_up += y; items_up += z; }
   }
-  if (lane == 31) s_scan[warp] = incl;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    s_scan->length[warp] = length_up;
+    s_scan->items[warp] = items_up;
+    s_scan->most[warp] = most;
+  }
   if (tid == 0) s_start->left = 0;
   __syncthreads();
-  long long before = 0, total = 0;
+  long long total = 0;
+  int total_items = 0;
+  most = 0;
   for (int w = 0; w < nt / 32; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
+    if (w < warp) { length_up += s_scan->length[w]; items_up += s_scan->items[w]; }
+    total += s_scan->length[w];
+    total_items += s_scan->items[w];
+    most = max(most, s_scan->most[w]);
   }
-  long long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(min_tiles));
-  if (a.uniform) per = (per + a.uniform + kItemCost - 1) / (a.uniform + kItemCost) * (a.uniform + kItemCost);
-  const long long begin = per * blockIdx.x;
-  const long long excl = before + incl - mine;
-  if (begin >= excl && begin < excl + mine) {
-    long long at = excl;
+  const long long even = max((total + gridDim.x - 1) / gridDim.x, static_cast<long long>(min_tiles));
+  const int each = (total_items + gridDim.x - 1) / gridDim.x;      // whole items of a CTA
+  const bool whole = a.whole || static_cast<long long>(each) * (most + kItemCost) <= even + kItemCost + kJoinCost;
+  const long long before = whole ? items_up - items : length_up - length, mine = whole ? items : length;
+  const long long begin = (whole ? each : even) * blockIdx.x, end = whole ? total_items : total;
+  if (begin >= before && begin < before + mine) {
+    long long at = before;
     for (int i = i0; i < i1; ++i) {
-      const long long m = request_length(a, i, n_rows, false);
+      int k, n;
+      request(i, false, k, n);
+      const long long m = whole ? k : static_cast<long long>(k) * (n + kItemCost);
       if (begin < at + m) {
+        const int unit = whole ? most + kItemCost : 1;
         s_start->i = i;
-        s_start->residual = begin - at;
-        s_start->left = min(per, total - begin);
-        s_start->per = per;
+        s_start->residual = (begin - at) * unit;
+        s_start->left = min(whole ? static_cast<long long>(each) : even, end - begin) * unit;
+        s_start->per = even;
+        s_start->whole = whole ? most : 0;
         break;
       }
       at += m;
@@ -178,7 +204,7 @@ __device__ __forceinline__ void find_start(const PagedArgs &a, int n_rows, int m
 // The pieces of work of one CTA, walked by the warps that prepare them.
 struct Walk {
   const PagedArgs &a;
-  int n_rows;
+  int n_rows, whole_tiles;
   int i, item, at;         // request, item of the request, place in the item
   long long left;          // length still to come
   Extent x;
@@ -186,7 +212,8 @@ struct Walk {
   // the current piece
   int h, rt, j0, j1;       // head, row tile, tiles [j0, j1) of it
   TileList t;
-  __device__ __forceinline__ Walk(const PagedArgs &args, int rows, const Start &s) : a(args), n_rows(rows), left(s.left) {
+  __device__ __forceinline__ Walk(const PagedArgs &args, int rows, const Start &s) 
+      : a(args), n_rows(rows), whole_tiles(s.whole), left(s.left) {
     if (left <= 0) return;
     i = s.i;
     load();
@@ -197,7 +224,7 @@ struct Walk {
     x = paged_extent(a, i, false);
     row_tiles = (x.W * a.group + n_rows - 1) / n_rows;
     items = row_tiles * a.c.heads;
-    n = items ? tiles_per_item(a, x, n_rows) : 0;
+    n = whole_tiles ? whole_tiles : items ? tiles_per_item(a, x, n_rows) : 0;
   }
   // The next piece that has tiles: a cut within an item's fixed cost leaves
   // the whole item to the CTA behind it.

@@ -249,12 +249,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   uint64_t *q_full = piece_free + kAhead;   // [kAhead] its rows staged
   uint64_t *o_full = q_full + kAhead;
   uint64_t *o_free = o_full + 1;
-  long long *s_scan = reinterpret_cast<long long *>(o_free + 1);          // [16]
-  Start *start = reinterpret_cast<Start *>(s_scan + 16);
+  Scan *s_scan = reinterpret_cast<Scan *>(o_free + 1);
+  Start *start = reinterpret_cast<Start *>(s_scan + 1);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   static_assert(2 * sizeof(RowInfo<N>) + kAhead * sizeof(Piece) + 6 * kG * N * 4 + 64 + C::kScaleSlots * (2 * kTile + 12) + 4 +
-                        (2 * kSt + 2 * kSBuf + 2 * kPBuf + 3 * kAhead + 2) * 8 + 128 + sizeof(Start) + 8 <=
+                        (2 * kSt + 2 * kSBuf + 2 * kPBuf + 3 * kAhead + 2) * 8 + sizeof(Scan) + sizeof(Start) + 8 <=
                     C::kMisc - 1024,
                 "row tables and barriers");
   static_assert(sizeof(Piece) % 16 == 0 && (6 * kG * N * 4 + 64) % 16 == 0 && 5 * kG <= 16, "scales, 16-byte aligned for the bulk loads");
@@ -841,11 +841,13 @@ dllm_status launch_attn(const dllm_kv_pages *pages, const dllm_paged_attn_args *
   const long long row_tiles = (static_cast<long long>(a->max_q) * g.group + n - 1) / n;
   const long long per_item = g.max_kv > 0 ? (g.max_kv + kTile - 1) / kTile : 1;
   const bool split = may_split(a);
-  const int min_tiles = split ? kMinTiles : static_cast<int>(per_item);
-  g.uniform = split ? 0 : min_tiles;
+  const int min_tiles = kMinTiles;
+  g.whole = !split;
   const double most = static_cast<double>(a->B) * pages->heads * row_tiles * per_item;
   int ctas = sm_budget() < kMaxCtas ? sm_budget() : kMaxCtas;
-  if (most / min_tiles < ctas) ctas = static_cast<int>(most / min_tiles) + 1;
+  // (a whole item per CTA, or at least min_tiles tiles)
+  const double useful = split ? most / min_tiles : most / per_item;
+  if (useful < ctas) ctas = static_cast<int>(useful) + 1;
   const dllm_status st = n == 16   ? launch<DH, FP8, 16>(tk, tv, g, min_tiles, ctas, s)
                          : n == 32 ? launch<DH, FP8, 32>(tk, tv, g, min_tiles, ctas, s)
                                    : launch_paged_rows(DH, FP8, n, tk, tv, g, min_tiles, ctas, s);

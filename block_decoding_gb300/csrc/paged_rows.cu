@@ -66,7 +66,7 @@ struct RowsCfg {
   static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);
   static constexpr int kVGroup8 = 8 * DH * 2;
   static constexpr int kQ = 128 * DH * 2;                     // 128 rows: bf16, or two e4m3 parts
-  static constexpr int kQs = TWO ? 2 : 1;
+  static constexpr int kQs = 2;                               // one per stream, or this piece's and the next one's
   static constexpr int kCBuf = FP8 ? 4 : 0;                   // converted V pieces: two tiles
   static constexpr int kConv = kCBuf * kConvKeys * DH * 2;
   static constexpr int kScaleBytes = FP8 ? 8192 : 0;          // scale bytes, column factors, row factors
@@ -157,11 +157,11 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   uint64_t *q_full = piece_free + kAhead;   // [kAhead] query rows staged
   uint64_t *o_full = q_full + kAhead;
   uint64_t *o_free = o_full + 1;
-  long long *s_scan = reinterpret_cast<long long *>(o_free + 1);          // [16]
-  Start *start = reinterpret_cast<Start *>(s_scan + 16);
+  Scan *s_scan = reinterpret_cast<Scan *>(ml_s);                          // before there are any
+  Start *start = reinterpret_cast<Start *>(o_free + 1);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert(kAhead * sizeof(RowsPiece) + 1024 + (2 * kSt + 10 + 3 * kAhead) * 8 + 128 + sizeof(Start) + 8 <= 1984, "piece and barriers");
+  static_assert(kAhead * sizeof(RowsPiece) + 1024 + (2 * kSt + 10 + 3 * kAhead) * 8 + sizeof(Start) + 8 <= 1984, "piece and barriers");
   // e4m3 pages
   uint8_t *scales = misc + 1984;                                          // [kScaleSlots][K, V][kTile]
   float *col_s = reinterpret_cast<float *>(scales + C::kScaleSlots * 2 * kTile);   // [4][kTile] score factors of a tile's keys
@@ -173,7 +173,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   uint32_t *pages_of = reinterpret_cast<uint32_t *>(col_full + 4);        // [kScaleSlots]
   static_assert(!FP8 || C::kScaleSlots * (2 * kTile + 12) + 4 * kTile * 4 + 2048 + (2 * C::kCBuf + 4) * 8 <= C::kScaleBytes,
                 "scales");
-  static_assert(1984 % 16 == 0 && sizeof(RowsPiece) % 16 == 0, "scales, 16-byte aligned for the bulk loads");
+  static_assert(sizeof(Scan) <= 1024 && 1984 % 16 == 0 && sizeof(RowsPiece) % 16 == 0, "scales, 16-byte aligned for the bulk loads");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
@@ -240,7 +240,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           tc_fence_after();
           if (ok) {
             const uint32_t sk = smem_u32(smem + st * C::kRaw), t_s = tmem + s * 128;
-            const uint32_t sq = smem_u32(smem + C::kOffQ + (two ? s : 0) * C::kQ);
+            const uint32_t sq = smem_u32(smem + C::kOffQ + (TWO ? (two ? s : 0) : seg & 1) * C::kQ);
             if constexpr (!FP8) {
               const uint64_t dq = sw128_desc(sq, 16, 1024), dk = sw128_desc(sk, 16, C::kGroup8);
 #pragma unroll
@@ -398,7 +398,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       if (TWO && pc.two)
         stage_rows<DH, FP8, 128>(a, pc, pc.r0 + s * 128, 0, smem + C::kOffQ + s * C::kQ, qs + s * 128, tid);
       else
-        stage_rows<DH, FP8, 64>(a, pc, pc.r0, s * 64, smem + C::kOffQ, qs, tid);
+        stage_rows<DH, FP8, 64>(a, pc, pc.r0, s * 64, smem + C::kOffQ + (TWO ? 0 : seg & 1) * C::kQ, qs, tid);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[pi]);
@@ -549,10 +549,15 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[s * 2 + half]);
         }
+        if (!TWO && k == 0) stage(seg + 1);   // into the space of the last piece's rows
       }
       n0 += nT;
-      named_bar_sync(3, 256);   // both streams' scores are done, the query rows' space is free
-      stage(seg + 1);
+      if (TWO) {
+        named_bar_sync(3, 256);   // both streams' scores are done, the query rows' space is free
+        stage(seg + 1);
+      } else if (cnt == 0) {
+        stage(seg + 1);
+      }
       if (nT > 0) {
         mbar_wait(o_full, o_seg & 1, abort_flag);
         ++o_seg;
