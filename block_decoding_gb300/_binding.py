@@ -647,6 +647,8 @@ def paged_attn(q, pages: KVPages, q_off, kv_len, page_table, max_q, max_kv, q_po
     (u >= position - left or u < sinks); negative left / right: no limit.
     Returns out [rows][Hq][dh], or (out, lse [rows][Hq]) with return_lse.
     """
+    if max(max_q, max_kv, left, right, sinks) >= 1 << 31 or min(max_q, max_kv, left, right, sinks) < -(1 << 31):
+        raise ValueError("max_q, max_kv, left, right and sinks must fit 32 bits")
     dev, dh = pages.index, pages.dh
     rows, Hq = (q.shape[0], q.shape[1]) if isinstance(q, torch.Tensor) and q.dim() == 3 else (0, 0)
     qp, qs = _rows_ptr(q, dev, Hq, dh, "q")

@@ -274,7 +274,7 @@ __device__ __forceinline__ void prefetch_rows(const PagedArgs &a, const Walk &w,
 // The warp that loads the K and V tiles of a CTA's pieces: one box per page
 // and tile, K tile n to stage n % KS, V tile n to stage KS + n % VS. A tile's
 // V is asked for LEAD tiles after its K: it is read that much later, and
-// until then its space would hold nothing back but other loads. With e4m3
+// until then its space would hold nothing but other loads back. With e4m3
 // pages (SCALES > 0) a tile's scale bytes, K's then V's, go to a ring of
 // SCALES slots with the truth of which pages the tile has.
 template <int DH, int ELEM, int KS, int VS, int LEAD, int SCALES>
@@ -357,7 +357,7 @@ __device__ __forceinline__ void load_tiles(const PagedArgs &a, const Start &star
 // out, the first of them key 64 * piece of the tile) to bf16 rows in the
 // layout of a bf16 tile, every four elements in the order 0, 2, 1, 3, by 128
 // threads (t): half a row each, of key 64 * piece + t % 64. `ready` waits
-// until dst may be written; factor(key) is the rows' scale, or 1.
+// until dst may be written; `extra` multiplies four elements by the row's scale.
 template <int DH, typename Ready, typename Extra>
 __device__ __forceinline__ void convert_v(const uint8_t *raw, uint8_t *dst, int piece, int t, bool seen, Ready ready,
                                           Extra extra) {

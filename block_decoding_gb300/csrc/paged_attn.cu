@@ -22,11 +22,11 @@
 //   warp 1      S^T MMAs: K tile (A) x query rows (B) into an S buffer
 //   warp 2      O^T MMAs: V tile (A, transposed by its descriptor) x P (B)
 //   warp 3      walks the CTA's pieces ahead of the others
-//   warps 4..   softmax warpgroups (three, two with 32 rows), one key per
-//               thread, taking the key tiles in turn, each with references,
-//               sums and an O of its own that are merged at the end: the steps
-//               of one tile depend on each other, and several tiles under way
-//               hide that. They also stage the rows.
+//   warps 4..11 two softmax warpgroups, one key per thread, taking the key
+//               tiles in turn, each with references, sums and an O of its own
+//               that are merged at the end: the steps of one tile depend on
+//               each other, and two tiles under way hide that. They also
+//               stage the rows.
 // A reference maximum per row moves only when a score passes it by more than
 // 2^kLazy, so most tiles need no maximum at all, only the vote that nobody
 // passed it.
@@ -55,13 +55,13 @@ constexpr int kAhead = 4;        // pieces prepared, the current one included
 
 template <int DH, bool FP8, int N>
 struct Cfg {
-  static constexpr int kGroups = 2;                             // softmax warpgroups
+  static constexpr int kGroups = 2;                             // softmax warpgroups (three: no gain)
   static constexpr int kSBuf = 2 * kGroups, kPBuf = kGroups;
   static constexpr int kThreads = 128 * (1 + kGroups);
   // registers a thread: what the TMA and MMA warps do not need goes to the
   // softmax groups (the sum is the launch's)
-  static constexpr int kRegsIssue = 104, kRegsSoft = kGroups == 3 ? 136 : 200;
-  static_assert(kRegsIssue + kGroups * kRegsSoft <= (kGroups == 3 ? 4 * 128 : 3 * 168), "registers");
+  static constexpr int kRegsIssue = 104, kRegsSoft = 200;
+  static_assert(kRegsIssue + kGroups * kRegsSoft <= 3 * 168, "registers");
   static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);       // one K or V tile
   static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);        // eight cached rows
   static constexpr int kO = FP8 ? 2 * N : N;                    // columns of a group's O, and of a part of P
@@ -432,7 +432,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     auto stage = [&](uint32_t seg) {           // piece seg's query rows
       const uint32_t pi = seg % kAhead;
       mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
-      if (wg >= 2 || !pieces[pi].more) return;
+      if (!pieces[pi].more) return;
       stage_queries<DH, FP8, N>(a, pieces[pi], smem + C::kOffQ, info[seg & 1], threadIdx.x - 128);
       fence_proxy_async_smem();
       __syncwarp();
@@ -642,7 +642,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         tc_fence_after();
       }
       named_bar_sync(4, 128 * kG);
-      if (wg < 2) {
       // rows [out0, out0 + kOut): maximum, sum, and what the groups' O count for
       auto highest = [&](int e) {
         float m = m_s[e];
@@ -708,7 +707,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
           for (int e = 0; e < kOut; ++e) po[e * DH] = __uint_as_float(o[e]);
         if (tid < kOut) a.part_ml[slot * N + out0 + tid] = merged(out0 + tid);
-      }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&piece_free[pi]);

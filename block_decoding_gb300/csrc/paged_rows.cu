@@ -96,30 +96,44 @@ struct alignas(16) RowsPiece {
 // Query rows [n0, n0 + CNT) of the 128 in `sq`, flat rows r0 + n, as the A
 // operand of the scores (rows of 128 bytes under the 128-byte swizzle, column
 // pieces 16 KB apart; e4m3 parts: DH-byte rows, parts 128 DH apart), by 128
-// threads. The rows' powers of two go to qs.
+// threads. bf16 rows are copied asynchronously: they are there after
+// copies_wait. The powers of two of rows in e4m3 parts go to qs.
 template <int DH, bool FP8, int CNT>
 __device__ __forceinline__ void stage_rows(const PagedArgs &a, const RowsPiece &pc, int r0, int n0, uint8_t *sq, float *qs,
                                            int tid) {
-  const int rows = pc.x.W * a.group;
-  constexpr int kChunks = DH / 8;
-  constexpr int kAtOnce = 8;   // loads on their way before the first store
-#pragma unroll 1
-  for (int i0 = tid; i0 < CNT * kChunks; i0 += 128 * kAtOnce) {
-    uint4 u[kAtOnce];
+  constexpr int kChunks = DH / 8, kEach = CNT * kChunks / 128, kStep = 128 / kChunks;   // chunks of a thread, rows from one to the next
+  constexpr int kAtOnce = kEach < 8 ? kEach : 8;   // loads on their way before the first store
+  static_assert(kEach % kAtOnce == 0, "whole rounds");
+  // row r = t * group + g, and the step from a thread's row to its next one
+  const int rows = pc.x.W * a.group, c = tid % kChunks, step_t = kStep / a.group, step_g = kStep - step_t * a.group;
+  int n = n0 + tid / kChunks, r = r0 + n, t = r / a.group, g = r - t * a.group;
+  const uint16_t *q = a.q + pc.x.q0 * a.q_stride + pc.h * a.group * DH + c * 8;
+  auto source = [&] { return reinterpret_cast<const uint4 *>(r < rows ? q + t * a.q_stride + g * DH : q); };
+  auto advance = [&] {
+    r += kStep;
+    t += step_t;
+    g += step_g;
+    if (g >= a.group) { g -= a.group; ++t; }
+  };
+  if constexpr (!FP8) {
+    uint8_t *d = sq + (c / 8) * 16384 + (n / 8) * 1024 + (n % 8) * 128 + ((c % 8) ^ (n % 8)) * 16;   // (kStep: whole eights)
+    static_assert(kStep % 8 == 0, "the swizzle of a thread's rows");
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int idx = i0 + i * 128, r = r0 + n0 + idx / kChunks, t = r / a.group, g = r - t * a.group;
-      u[i] = make_uint4(0, 0, 0, 0);
-      if (idx < CNT * kChunks && r < rows)
-        u[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + (pc.x.q0 + t) * a.q_stride + (pc.h * a.group + g) * DH + idx % kChunks * 8));
+    for (int i = 0; i < kEach; ++i) {
+      copy16(d + i * (kStep / 8 * 1024), source(), r < rows);
+      advance();
     }
+  } else {
+#pragma unroll 1
+    for (int i0 = 0; i0 < kEach; i0 += kAtOnce) {
+      uint4 u[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int idx = i0 + i * 128, n = n0 + idx / kChunks, c = idx % kChunks;
-      if (idx >= CNT * kChunks) break;   // whole groups of 128
-      if constexpr (!FP8) {
-        *reinterpret_cast<uint4 *>(sq + (c / 8) * 16384 + (n / 8) * 1024 + (n % 8) * 128 + ((c % 8) ^ (n % 8)) * 16) = u[i];
-      } else {
+      for (int i = 0; i < kAtOnce; ++i) {
+        u[i] = r < rows ? __ldg(source()) : make_uint4(0, 0, 0, 0);
+        advance();
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i, n += kStep) {
         const uint32_t m2 = max_mag(u[i], 0);
         uint32_t m = max(m2 & 0xffffu, m2 >> 16);
 #pragma unroll
@@ -223,88 +237,88 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       // (one elected thread through the whole loop: a warp that stays
       // together and elects around each group of MMAs took 12 % longer)
       if (elect_one()) {
-      uint32_t n0 = 0, o_seg = 0, cnt[2] = {0, 0};   // tiles and streams' tiles before this piece
-      bool ok = true;
-      for (uint32_t seg = 0; ok; ++seg) {
-        const uint32_t pi = seg % kAhead;
-        ok = mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
-        if (!ok || !pieces[pi].more) break;
-        const int nT = pieces[pi].tiles;
-        const bool two = TWO && pieces[pi].two;
-        const int n_s[2] = {two ? nT : (nT + 1) / 2, two ? nT : nT / 2};
-        ok = mbar_wait(&q_full[pi], (seg / kAhead) & 1, abort_flag);
-        // scores of stream s's k-th tile
-        auto scores = [&](int s, int k) {
-          const uint32_t n = n0 + (two ? k : 2 * k + s), st = n % C::kKSt;
-          ok = ok && mbar_wait(&full[st], (n / C::kKSt) & 1, abort_flag);
-          tc_fence_after();
-          if (ok) {
-            const uint32_t sk = smem_u32(smem + st * C::kRaw), t_s = tmem + s * 128;
-            const uint32_t sq = smem_u32(smem + C::kOffQ + (TWO ? (two ? s : 0) : seg & 1) * C::kQ);
-            if constexpr (!FP8) {
-              const uint64_t dq = sw128_desc(sq, 16, 1024), dk = sw128_desc(sk, 16, C::kGroup8);
-#pragma unroll
-              for (int kk = 0; kk < DH / 16; ++kk)
-                umma_bf16(t_s, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                          idesc_bf16(128, 128, 0, 0), kk > 0);
-            } else {
-              const uint64_t dk = DH == 128 ? sw128_desc(sk, 16, C::kGroup8) : sw64_desc(sk, 16, C::kGroup8);
-#pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                const uint32_t sp = sq + part * 128 * DH;
-                const uint64_t dq = DH == 128 ? sw128_desc(sp, 16, 8 * DH) : sw64_desc(sp, 16, 8 * DH);
-#pragma unroll
-                for (int kk = 0; kk < DH / 32; ++kk)
-                  umma_f8(t_s, dq + ((kk * 32) >> 4), dk + ((kk * 32) >> 4), idesc_f8(128, 128, kE4M3, kE4M3, 0, 0), part + kk > 0);
-              }
-            }
-            umma_commit(&s_full[s]);
-            if (!two || s == 1) umma_commit(&empty[st]);
-          }
-        };
-        // O of stream s += P V of its k-th tile
-        auto values = [&](int s, int k) {
-          const uint32_t n = n0 + (two ? k : 2 * k + s), st = C::kKSt + n % C::kVSt;
-          const uint32_t ns = cnt[s] + k;
-          if (k == 0 && s == 0 && o_seg > 0) ok = ok && mbar_wait(o_free, (o_seg - 1) & 1, abort_flag);
-          if constexpr (!FP8) ok = ok && mbar_wait(&full[st], (n / C::kVSt) & 1, abort_flag);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = ok && mbar_wait(&p_full[s * 2 + half], ns & 1, abort_flag);
-            const uint32_t cn = 2 * n + half, cb = FP8 ? cn % (C::kCBuf + !FP8) : 0;
-            if constexpr (FP8) ok = ok && mbar_wait(&c_full[cb], (cn / C::kCBuf) & 1, abort_flag);
+        uint32_t n0 = 0, o_seg = 0, cnt[2] = {0, 0};   // tiles and streams' tiles before this piece
+        bool ok = true;
+        for (uint32_t seg = 0; ok; ++seg) {
+          const uint32_t pi = seg % kAhead;
+          ok = mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
+          if (!ok || !pieces[pi].more) break;
+          const int nT = pieces[pi].tiles;
+          const bool two = TWO && pieces[pi].two;
+          const int n_s[2] = {two ? nT : (nT + 1) / 2, two ? nT : nT / 2};
+          ok = mbar_wait(&q_full[pi], (seg / kAhead) & 1, abort_flag);
+          // scores of stream s's k-th tile
+          auto scores = [&](int s, int k) {
+            const uint32_t n = n0 + (two ? k : 2 * k + s), st = n % C::kKSt;
+            ok = ok && mbar_wait(&full[st], (n / C::kKSt) & 1, abort_flag);
             tc_fence_after();
             if (ok) {
-              const uint32_t sv = smem_u32(FP8 ? smem + C::kOffConv + cb * (kConvKeys * DH * 2)
-                                               : smem + st * C::kRaw + half * 8 * C::kVGroup8);
-              const uint64_t dv = sw128_desc(sv, 1024, C::kVGroup8);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_bf16_tmem_a(tmem + kColO + s * 128, tmem + s * 128 + (half * 4 + kk) * 8,
-                                 dv + ((kk * 2 * C::kVGroup8) >> 4), idesc_bf16(128, DH, 0, 1), k > 0 || half + kk > 0);
-              if (half == 0) umma_commit(&h_done[s]);
-              if (FP8 && (!two || s == 1)) umma_commit(&c_free[cb]);
-              if (!FP8 && half == 1 && (!two || s == 1)) umma_commit(&empty[st]);
+              const uint32_t sk = smem_u32(smem + st * C::kRaw), t_s = tmem + s * 128;
+              const uint32_t sq = smem_u32(smem + C::kOffQ + (TWO ? (two ? s : 0) : seg & 1) * C::kQ);
+              if constexpr (!FP8) {
+                const uint64_t dq = sw128_desc(sq, 16, 1024), dk = sw128_desc(sk, 16, C::kGroup8);
+  #pragma unroll
+                for (int kk = 0; kk < DH / 16; ++kk)
+                  umma_bf16(t_s, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                            idesc_bf16(128, 128, 0, 0), kk > 0);
+              } else {
+                const uint64_t dk = DH == 128 ? sw128_desc(sk, 16, C::kGroup8) : sw64_desc(sk, 16, C::kGroup8);
+  #pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                  const uint32_t sp = sq + part * 128 * DH;
+                  const uint64_t dq = DH == 128 ? sw128_desc(sp, 16, 8 * DH) : sw64_desc(sp, 16, 8 * DH);
+  #pragma unroll
+                  for (int kk = 0; kk < DH / 32; ++kk)
+                    umma_f8(t_s, dq + ((kk * 32) >> 4), dk + ((kk * 32) >> 4), idesc_f8(128, 128, kE4M3, kE4M3, 0, 0), part + kk > 0);
+                }
+              }
+              umma_commit(&s_full[s]);
+              if (!two || s == 1) umma_commit(&empty[st]);
             }
+          };
+          // O of stream s += P V of its k-th tile
+          auto values = [&](int s, int k) {
+            const uint32_t n = n0 + (two ? k : 2 * k + s), st = C::kKSt + n % C::kVSt;
+            const uint32_t ns = cnt[s] + k;
+            if (k == 0 && s == 0 && o_seg > 0) ok = ok && mbar_wait(o_free, (o_seg - 1) & 1, abort_flag);
+            if constexpr (!FP8) ok = ok && mbar_wait(&full[st], (n / C::kVSt) & 1, abort_flag);
+  #pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              ok = ok && mbar_wait(&p_full[s * 2 + half], ns & 1, abort_flag);
+              const uint32_t cn = 2 * n + half, cb = FP8 ? cn % (C::kCBuf + !FP8) : 0;
+              if constexpr (FP8) ok = ok && mbar_wait(&c_full[cb], (cn / C::kCBuf) & 1, abort_flag);
+              tc_fence_after();
+              if (ok) {
+                const uint32_t sv = smem_u32(FP8 ? smem + C::kOffConv + cb * (kConvKeys * DH * 2)
+                                                 : smem + st * C::kRaw + half * 8 * C::kVGroup8);
+                const uint64_t dv = sw128_desc(sv, 1024, C::kVGroup8);
+  #pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_bf16_tmem_a(tmem + kColO + s * 128, tmem + s * 128 + (half * 4 + kk) * 8,
+                                   dv + ((kk * 2 * C::kVGroup8) >> 4), idesc_bf16(128, DH, 0, 1), k > 0 || half + kk > 0);
+                if (half == 0) umma_commit(&h_done[s]);
+                if (FP8 && (!two || s == 1)) umma_commit(&c_free[cb]);
+                if (!FP8 && half == 1 && (!two || s == 1)) umma_commit(&empty[st]);
+              }
+            }
+          };
+          if (nT > 0) {
+            scores(0, 0);
+            if (n_s[1] > 0) scores(1, 0);
+            for (int k = 0; ok && k < n_s[0]; ++k) {
+              values(0, k);
+              if (k + 1 < n_s[0]) scores(0, k + 1);
+              if (k < n_s[1]) values(1, k);
+              if (k + 1 < n_s[1]) scores(1, k + 1);
+            }
+            if (ok) umma_commit(o_full);
+            ++o_seg;
           }
-        };
-        if (nT > 0) {
-          scores(0, 0);
-          if (n_s[1] > 0) scores(1, 0);
-          for (int k = 0; ok && k < n_s[0]; ++k) {
-            values(0, k);
-            if (k + 1 < n_s[0]) scores(0, k + 1);
-            if (k < n_s[1]) values(1, k);
-            if (k + 1 < n_s[1]) scores(1, k + 1);
-          }
-          if (ok) umma_commit(o_full);
-          ++o_seg;
+          n0 += nT;
+          cnt[0] += n_s[0];
+          cnt[1] += n_s[1];
+          mbar_arrive(&piece_free[pi]);
         }
-        n0 += nT;
-        cnt[0] += n_s[0];
-        cnt[1] += n_s[1];
-        mbar_arrive(&piece_free[pi]);
-      }
       }
       __syncwarp();
     } else if (warp == 3) {
@@ -388,7 +402,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lane_base + s * 128, t_o = tmem + lane_base + kColO + s * 128;
     uint32_t n0 = 0, ns = 0, o_seg = 0;
-    // this group's part of piece `seg`'s query rows
+    // this group's part of piece `seg`'s query rows: begun, and there
     auto stage = [&](uint32_t seg) {
       const uint32_t pi = seg % kAhead;
       mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
@@ -399,9 +413,12 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         stage_rows<DH, FP8, 128>(a, pc, pc.r0 + s * 128, 0, smem + C::kOffQ + s * C::kQ, qs + s * 128, tid);
       else
         stage_rows<DH, FP8, 64>(a, pc, pc.r0, s * 64, smem + C::kOffQ + (TWO ? 0 : seg & 1) * C::kQ, qs, tid);
+    };
+    auto staged = [&](uint32_t seg) {
+      if constexpr (!FP8) copies_wait();
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[pi]);
+      if (lane == 0) mbar_arrive(&q_full[seg % kAhead]);
     };
     for (uint32_t seg = 0;; ++seg) {
       const uint32_t pi = seg % kAhead;
@@ -411,6 +428,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       if (!pc.more) break;
       if (seg == 0) {
         stage(0);
+        staged(0);
         if constexpr (FP8) named_bar_sync(3, 256);   // the rows' powers of two
       }
       const TileList tl = pc.t;
@@ -421,6 +439,15 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       if (r < rows) visible(a, pc.x.pos + t, pc.x.L, lo, hi);
       const float qs = FP8 ? qs_s[(seg & 1) * 256 + (two ? s * 128 : 0) + tid] : 1.f;
       const int cnt = two ? nT : s == 0 ? (nT + 1) / 2 : nT / 2;
+      // Streams with rows of their own, in this piece and the next: a stream's
+      // space is free as soon as its last scores are done, and bf16 rows are
+      // copied while its last weights are computed.
+      bool early = false;
+      if constexpr (TWO && !FP8) {
+        const uint32_t next = (seg + 1) % kAhead;
+        if (bar_any(3, 256, !mbar_wait(&piece_full[next], ((seg + 1) / kAhead) & 1, abort_flag))) break;
+        early = two && nT > 0 && pieces[next].more && pieces[next].two;
+      }
       // every row's O times its factor, by the whole warp (tcgen05.ld / st)
       auto rescale = [&](float corr) {
 #pragma unroll 1
@@ -458,6 +485,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         mbar_wait(&s_full[s], ns & 1, abort_flag);
         tc_fence_after();
+        // (without TWO: into the space of the last piece's rows)
+        const bool ahead = TWO ? early && k == cnt - 1 : k == 0;
+        if (!FP8 && ahead) stage(seg + 1);
         if (__any_sync(0xffffffffu, top > kLazy)) {
           // O holds exactly the stream's tiles before this one: their MMAs
           // were issued before this tile's scores, which are done
@@ -549,14 +579,16 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[s * 2 + half]);
         }
-        if (!TWO && k == 0) stage(seg + 1);   // into the space of the last piece's rows
+        if (ahead) {
+          if (FP8) stage(seg + 1);
+          staged(seg + 1);
+        }
       }
       n0 += nT;
-      if (TWO) {
-        named_bar_sync(3, 256);   // both streams' scores are done, the query rows' space is free
+      if (TWO ? !early : cnt == 0) {
+        if (TWO) named_bar_sync(3, 256);   // both streams' scores are done, the query rows' space is free
         stage(seg + 1);
-      } else if (cnt == 0) {
-        stage(seg + 1);
+        staged(seg + 1);
       }
       if (nT > 0) {
         mbar_wait(o_full, o_seg & 1, abort_flag);

@@ -248,10 +248,17 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// True in one lane of the (converged) warp, the same one every time. A warp
-// that runs its loop as a whole and elects around the MMAs alone keeps their
-// descriptors in uniform registers; under `if (lane == 0)` every operand of
-// every MMA is moved there first.
+// 16 bytes from global to shared memory without registers (zeros if !there);
+// copies_wait: the thread's copies have landed.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :: "r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// True in one lane of the (converged) warp, the same one every time. The
+// compiler keeps the descriptors of MMAs under it in uniform registers; under
+// `if (lane == 0)` every operand of every MMA is moved there first.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(

@@ -500,6 +500,138 @@ def test_binding_refusals():
         bd.paged_attn(b.q.cpu(), b.pages, off, n, b.table, 3, 20)
 
 
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_page_sizes_with_every_row_tile(dh, fp8, page):
+    b = Batch(30, [650, 31, 129], 2, dh, page, fp8)
+    for w, group in (([1, 1, 1], 3), ([9, 2, 8], 3), ([11, 40, 33], 3), ([140, 50, 129], 2)):
+        b.queries(w, group)
+        b.check(*b.run(left=150, right=0, sinks=20), left=150, right=0, sinks=20)
+        b.check(*b.run())
+
+
+@pytest.mark.parametrize("w", [1, 12, 40, 300])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_leaps_of_the_scores(w, fp8):
+    """Single keys whose scores lie 2^40 and more above all before them, in
+    either half of a tile, first and last ones among them; some rows have them
+    the other way round and see weights that vanish."""
+    at = [0, 1, 31, 32, 63, 64, 100, 127, 128, 190, 200, 255, 256, 300, 383, 400, 511, 512, 600, 690]
+    b = Batch(31, [700, 460], 1, 64, 64, fp8)
+    b.queries([w, w], 2)
+    b.q[:] = torch.where(torch.arange(2 * w, device=DEV) % 3 == 1, -0.5, 1.0)[:, None, None].to(torch.bfloat16)
+    k = torch.zeros((1160, 1, 64))
+    for n, u in enumerate(at):
+        k[u] = 4.0 * n                                   # scores 32 n apart at scale 1/8: 2^46
+        if u < 460:
+            k[700 + 459 - u] = 4.0 * n
+    k = k.to(torch.bfloat16)
+    bd.kv_write(b.pages, k.to(DEV), b.v_in, b.off, i32([0, 0]), b.table)
+    k = paged.restore(*paged.quantise(f64(k))) if fp8 else f64(k)
+    b.k = [k[:700], k[700:]]
+    for left in (-1, 130):
+        b.check(*b.run(left=left, right=0), left=left, right=0)
+    b.check(*b.run())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("w", [1, 12, 40, 200])
+def test_large_values_do_not_overflow(w, fp8):
+    # weights of up to 2^32 relative to a lagging reference, values of 2^60
+    b = Batch(32, [500], 1, 128, 32, fp8)
+    b.queries([w], 1, q_size=0.0)
+    b.q[:] = 2.0
+    k = torch.linspace(-1, 1, 500)[:, None, None].expand(-1, 1, 128).to(torch.bfloat16).contiguous()
+    v = (b.v_in.float() * 2.0 ** 60).to(torch.bfloat16)
+    bd.kv_write(b.pages, k.to(DEV), v, b.off, i32([0]), b.table)
+    k, v = f64(k), f64(v)
+    b.k, b.v = ([paged.restore(*paged.quantise(x))] if fp8 else [x] for x in (k, v))
+    b.check(*b.run(right=0), right=0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,most", [(4096, 1), (700, 7), (300, 60)])
+def test_many_requests(B, most, fp8):
+    # more than threads of a block, requests without rows or keys among them
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 180, B) * (rng.random(B) < 0.8)
+    b = Batch(33, [int(n) for n in lens], 1, 64, 16, fp8)
+    b.queries([int(x) for x in rng.integers(0, most + 1, B)], 2)
+    b.check(*b.run(right=0), right=0)
+    lens[B // 2] = 0
+    b.check(*b.run(left=50, right=0, sinks=2), left=50, right=0, sinks=2)
+
+
+@pytest.mark.parametrize("left,right,sinks", MASKS)
+@pytest.mark.parametrize("fp8", [False, True])
+def test_single_tokens_beside_pieces_of_prompts(fp8, left, right, sinks):
+    b = Batch(34, [900, 333, 1, 50, 2100, 128, 600], 2, 128, 64, fp8)
+    b.queries([290, 1, 1, 0, 1, 64, 1], 2)
+    b.check(*b.run(left=left, right=right, sinks=sinks), left=left, right=right, sinks=sinks)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("w", [1, 40])
+def test_bounds_far_above_the_batch(w, fp8):
+    # max_q and max_kv as a server that serves every batch with one graph gives them
+    b = Batch(35, [300, 5, 40], 2, 64, 16, fp8)
+    b.queries([w, 1, 3], 2)
+    table = torch.full((3, 1 << 12), -1, dtype=torch.int32, device=DEV)
+    table[:, :b.width] = b.table
+    got = bd.paged_attn(b.q, b.pages, i32(b.q_off), i32(b.lens), table, 5000, 1 << 16, right=0, return_lse=True)
+    b.check(*got, right=0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_two_graphs_with_a_workspace_each(fp8):
+    bs = [Batch(36 + i, [3500, 700], 2, 64, 32, fp8) for i in range(2)]
+    runs = []
+    for b, w in zip(bs, (1, 70)):
+        b.queries([w, w], 2)
+        args = (b.q, b.pages, i32(b.q_off), i32(b.lens), b.table, w, 4000)
+        want = bd.paged_attn(*args, right=0, return_lse=True)
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            got = bd.paged_attn(*args, right=0, return_lse=True)      # its workspace lives in the graph's pool
+        runs.append((s, g, want, got, args))
+    for _ in range(20):
+        for s, g, _, _, _ in runs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, _, want, got, _ in runs:
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+@pytest.mark.parametrize("w", [1, 12, 40, 200])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_nan_in_one_head_of_one_request_stays_there(w, fp8):
+    b = Batch(38, [400, 300, 350], 2, 64, 16, fp8)
+    b.queries([w, w, w], 2)
+    k, v = b.k_in.clone(), b.v_in.clone()
+    k[410, 0, 7], v[420, 0, 9] = float("nan"), float("-inf")              # request 1, head 0
+    bd.kv_write(b.pages, k, v, b.off, i32([0, 0, 0]), b.table)
+    out, lse = b.run()
+    assert not torch.isfinite(out[w:2 * w, :2]).all(-1).any()
+    out[w:2 * w, :2], lse[w:2 * w, :2] = 0, 0
+    b2 = Batch(38, [400, 300, 350], 2, 64, 16, fp8)
+    b2.queries([w, w, w], 2)
+    want, z = b2.run()
+    want[w:2 * w, :2], z[w:2 * w, :2] = 0, 0
+    assert torch.equal(out, want) and torch.equal(lse, z)                 # the rest has the same bits
+
+
+@pytest.mark.parametrize("name", ["max_q", "max_kv", "left", "right", "sinks"])
+def test_numbers_beyond_32_bits_are_refused(name):
+    b = Batch(39, [20], 1, 64, 16, False)
+    b.queries([3], 1)
+    kw = {"max_q": 3, "max_kv": 20, "left": -1, "right": -1, "sinks": 0, name: (1 << 32) + 3}
+    with pytest.raises(ValueError):
+        bd.paged_attn(b.q, b.pages, i32([0, 3]), i32([20]), b.table, **kw)
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_a_run_of_them_together(fp8):
     """Prompt pieces and single tokens as a server runs them: each piece's K/V
