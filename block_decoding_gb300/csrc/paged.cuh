@@ -110,11 +110,15 @@ __device__ __forceinline__ int tiles_per_item(const PagedArgs &a, const Extent &
 
 // The work is a line of all items, each as long as its tiles and kItemCost
 // more for what every item costs however short it is (rows staged, results
-// written: about as much as so many tiles; without it a CTA with many short
-// items took 40 % longer than the others). It is cut into gridDim.x equal
+// written: about as much as so many tiles). It is cut into gridDim.x equal
 // stretches. Where it takes no longer that way, items stay whole: then every
 // item is as long as the longest, and stretches are so many items. (Dividing
 // costs an item's fixed part twice, and the joining about kJoinCost tiles.)
+// Measured: 64 single tokens over 1 to 8192 keys (e4m3, 8 x 4 heads, dh 128)
+// take 161 us with a cost of 0, 132 with 3, 124 with 6, 131 with 12; 16 blocks
+// of 64 to 96 rows over 352 to 1120 keys (32 heads, bf16) 60, 54, 54, 55;
+// longer items hardly differ. A join cost of 0 or 12 for 4 changes nothing
+// but those blocks, by 1 %.
 constexpr int kItemCost = 6, kJoinCost = 4;
 
 // Where this CTA's stretch starts.
@@ -385,7 +389,8 @@ __device__ __forceinline__ void convert_v(const uint8_t *raw, uint8_t *dst, int 
   }
 }
 
-constexpr int kMinTiles = 4;     // fewest tiles a CTA is given: each piece costs a prologue and a join
+constexpr int kMinTiles = 4;     // fewest tiles a CTA is given: each piece costs a prologue and a join (1 or 8: the same time
+                                 // for single tokens over 257 keys and 20000 to 40000)
 constexpr int kWholeTiles = 4;   // items of no more tiles are not divided
 constexpr int kMaxCtas = 192;    // bound of the workspace, above any GB300's SM count
 constexpr int kConvKeys = 64;    // keys of one converted V piece

@@ -794,14 +794,34 @@ dllm_status check_shape(const dllm_kv_pages *pages, const dllm_paged_attn_args *
   return DLLM_OK;
 }
 
-// Rows of a row tile: the least of 16, 32 and 128 that holds a request's rows
-// of one cached head, 256 where none does. Up to 32 they are the N of the
-// MMAs here, from there on the M of those in paged_rows.cu.
+// Rows of a row tile. Up to 32 rows of a request and cached head are the N of
+// the MMAs here, more are the M of those in paged_rows.cu. Measured (us; cached
+// heads x group, dh 128, keys of a request):
+//   4 rows, 32 requests, 8 x 4, 4000 keys:  tiles of 16: 87 (e4m3: 62), 32: 89 (74), 128: 93 (106)
+//   32 rows, else the same:                 32: 91 (86), 128: 96 (108)
+//   128 rows, 16 requests, else the same:   128: 52 (62), 256: 55 (64); 64 as N: half as long again as 128
+// Tiles of 256 read each K and V tile once for twice the rows, but leave
+// partial results of twice the size where items are divided, which weighs more
+// in small calls. Measured by key tiles of all 256-row items together:
+//   512 rows, 4000 keys, 4 requests x 8 heads (2048):  128: 40 (59), 256: 51 (64)
+//   1200 rows, 4000 keys, 2 x 8 (2560):                128: 50 (74), 256: 56 (74)
+//   2048 rows, 1000 keys, 4 x 8 (2048):                128: 55 (82), 256: 52 (68)
+//   512 rows, 4000 keys, 8 x 8 (4096):                 128: 85 (113), 256: 70 (95)
+//   512 rows, 4000 keys, 24 x 8 (12288):               128: 257 (289), 256: 181 (246)
+// (never more with a larger B, max_q or max_kv: the workspace grows with it)
+constexpr double kFewTiles = 3000, kFewTilesE4m3 = 1500;
+
 int row_tile(const dllm_kv_pages *pages, const dllm_paged_attn_args *a) {
   const long long rows = static_cast<long long>(a->max_q) * (a->Hq / pages->heads);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+  if (rows <= 128) return rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+  const double tiles = static_cast<double>(a->B) * pages->heads * ((rows + 255) / 256) * ((a->max_kv + kTile - 1) / kTile);
+  return tiles <= (pages->type == DLLM_KV_E4M3 ? kFewTilesE4m3 : kFewTiles) ? 128 : 256;
 }
 
+// Whether items may be divided: those of up to kWholeTiles tiles are not, and
+// the call has one launch and no workspace. Measured (one request, one token,
+// 8 x 4 heads, dh 128, bf16): 500 keys whole 10.0 us, divided 11.3; 1000 keys
+// whole 12.8, divided 11.5.
 bool may_split(const dllm_paged_attn_args *a) { return a->max_kv > kWholeTiles * kTile; }
 
 struct Ws {

@@ -92,9 +92,9 @@ class Batch:
         self.q = (bf16_rows(self.rng, (int(self.q_off[-1]) + behind, self.heads * group, self.dh), 0.2) * q_size).to(DEV)
         return self.q
 
-    def run(self, pos=None, **kw):
+    def run(self, pos=None, max_kv=None, **kw):
         return bd.paged_attn(self.q, self.pages, i32(self.q_off), i32(self.lens), self.table, max(self.w + [1]),
-                             max(self.lens + [1]), q_pos=i32(pos) if pos is not None else None, return_lse=True, **kw)
+                             max_kv or max(self.lens + [1]), q_pos=i32(pos) if pos is not None else None, return_lse=True, **kw)
 
     def check(self, out, lse, pos=None, left=-1, right=-1, sinks=0, scale=None):
         scale = self.dh ** -0.5 if scale is None else scale
@@ -233,6 +233,7 @@ def test_bad_pages_and_positions_are_reported():
 # attention
 # ---------------------------------------------------------------------------
 
+LARGE = 1 << 20     # a bound of the keys that makes the call a large one: row tiles of 256
 MASKS = [(-1, -1, 0), (-1, 0, 0), (40, 0, 3), (200, 16, 0), (0, 0, 130), (5, -1, 1)]
 
 
@@ -531,9 +532,10 @@ def test_leaps_of_the_scores(w, fp8):
     bd.kv_write(b.pages, k.to(DEV), b.v_in, b.off, i32([0, 0]), b.table)
     k = paged.restore(*paged.quantise(f64(k))) if fp8 else f64(k)
     b.k = [k[:700], k[700:]]
-    for left in (-1, 130):
-        b.check(*b.run(left=left, right=0), left=left, right=0)
-    b.check(*b.run())
+    for max_kv in (None, LARGE) if w == 300 else (None,):
+        for left in (-1, 130):
+            b.check(*b.run(left=left, right=0, max_kv=max_kv), left=left, right=0)
+        b.check(*b.run(max_kv=max_kv))
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -549,6 +551,7 @@ def test_large_values_do_not_overflow(w, fp8):
     k, v = f64(k), f64(v)
     b.k, b.v = ([paged.restore(*paged.quantise(x))] if fp8 else [x] for x in (k, v))
     b.check(*b.run(right=0), right=0)
+    b.check(*b.run(right=0, max_kv=LARGE), right=0)
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -622,6 +625,28 @@ def test_nan_in_one_head_of_one_request_stays_there(w, fp8):
     want, z = b2.run()
     want[w:2 * w, :2], z[w:2 * w, :2] = 0, 0
     assert torch.equal(out, want) and torch.equal(lse, z)                 # the rest has the same bits
+
+
+@pytest.mark.parametrize("left,right,sinks", MASKS)
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dh,page,heads,group", [(64, 64, 1, 2), (128, 16, 1, 1), (128, 128, 2, 3)])
+def test_chunks_of_large_calls(dh, page, heads, group, fp8, left, right, sinks):
+    b = Batch(40, [257, 90, 700, 0, 1500, 60], heads, dh, page, fp8)
+    b.queries([130, 200, 257, 150, 129, 20], group)
+    b.check(*b.run(left=left, right=right, sinks=sinks, max_kv=LARGE), left=left, right=right, sinks=sinks)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_large_calls_with_many_pieces_each(dh, fp8):
+    # CTAs go from item to item, between those with up to 128 rows and those with more
+    rng = np.random.default_rng(41)
+    lens, w = [int(n) for n in rng.integers(0, 800, 90)], [int(n) for n in rng.choice([1, 40, 64, 65, 100, 128, 129, 300], 90)]
+    b = Batch(41, lens, 2, dh, 32, fp8)
+    b.queries(w, 2)
+    for max_kv in (LARGE, None):
+        b.check(*b.run(right=0, max_kv=max_kv), right=0)
+        b.check(*b.run(left=100, right=30, sinks=140, max_kv=max_kv), left=100, right=30, sinks=140)
 
 
 @pytest.mark.parametrize("name", ["max_q", "max_kv", "left", "right", "sinks"])
