@@ -7,6 +7,12 @@
 // lanes of a row read and write contiguous runs. A block takes neighbouring
 // rows of up to four neighbouring heads: runs of several rows on the pages'
 // side, of several heads on the other.
+// Measured (dh 128, 32 heads, e4m3): 10 k rows written in 57 us (4.5 TB/s, 66 %
+// of a copy's rate), 19 k rows read in 81 us (5.9 TB/s, 88 %); 64 single
+// tokens (8 heads) written in 3.2 us, of which nearly all is the launch and the
+// chain request -> page -> store. Writing loads its rows before it looks their
+// places up (60 us the other way round). Several rows per thread: 58 us, and 4.4
+// for the 64 tokens; a persistent grid that loads its next rows ahead: slower.
 #include "pages.cuh"
 
 namespace dllm {

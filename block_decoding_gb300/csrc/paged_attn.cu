@@ -41,6 +41,14 @@
 //   so that weights keep 9 bits down to 2^-30 of the largest and err by 2^-42
 //   of it below. (Codes converted to bf16 by four more warps, with P in bf16:
 //   the conversion took 1.9 k cycles a tile, the loads of a tile 1.4 k.)
+//
+// Bound by memory where the keys are long: 4 requests of 20 to 40 thousand
+// keys (bf16, 8 x 4 heads, dh 128) take 95 us, 5.7 TB/s and 85 % of a copy's
+// rate; 64 requests of 1 to 8192 keys (e4m3) 125 us, 4.7 TB/s and 69 %; 32
+// requests that see 4096 keys each (e4m3, 4 x 8 heads) 42 us, 47 %: there some
+// 5 us until the first scores, 3 us of joining and the steps of one tile, of
+// which an e4m3 tile's load hides less, remain. One token over 257 keys
+// (16 heads of 64): 9 us, all of it such latencies.
 #include <type_traits>
 
 #include "paged.cuh"
@@ -72,7 +80,7 @@ struct Cfg {
   static constexpr int kFixed = kPBuf * kP + kQ + kMisc;
   static constexpr int kMaxStages = (232448 - kFixed) / kRaw;
   static constexpr int kStages = kMaxStages * kRaw > 196608 ? 196608 / kRaw : kMaxStages;   // 192 KB in flight are enough
-  static constexpr int kKSt = kStages / 2, kVSt = kStages - kKSt, kLead = 2;
+  static constexpr int kKSt = kStages / 2, kVSt = kStages - kKSt, kLead = 2;   // (1 or 3: the same time)
   static constexpr int kOffP = kStages * kRaw;
   static constexpr int kOffQ = kOffP + kPBuf * kP;
   static constexpr int kOffMisc = kOffQ + kQ;
@@ -723,8 +731,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 }
 
 // Joins the partial results of the item that CTA blockIdx.x began and others
-// finished: one warp per row, the pieces in their order with a running
-// maximum, four of them on the way at a time.
+// finished, of up to 32 rows: one warp per row, the pieces in their order with a running
+// maximum, four of them on the way at a time. About 3 us after single tokens:
+// the partial results are still in L2, so it is latency.
 constexpr int kJoinThreads = 256;
 
 template <int DH>
@@ -747,8 +756,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
       const size_t slot = static_cast<size_t>(p == 0 ? job.slot : 2 * (blockIdx.x + p)) * n_rows;
       if (p < job.parts) {
         ml[k] = a.part_ml[slot + n];
-        // [slot][row][DH], and of many rows [slot][DH / 4][row][4]
-        y[k] = *reinterpret_cast<const Vec *>(a.part_o + slot * DH + (n_rows <= 32 ? n * DH + c : (c / 4 * n_rows + n) * 4 + c % 4));
+        y[k] = *reinterpret_cast<const Vec *>(a.part_o + slot * DH + n * DH + c);   // [slot][row][DH]
       }
     }
 #pragma unroll
@@ -776,6 +784,62 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
     for (int e = 0; e < kVec; e += 2) d[e / 2] = pack_bf16x2(o[e], o[e + 1]);
   }
   if (a.lse && lane == 0) a.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// The same for row tiles of paged_rows.cu, whose partial results lie as
+// [slot][DH / 4][row][4]: a block joins 32 rows, one per lane, each warp DH / 8
+// of their columns, so that a load has a warp's rows side by side (a warp per
+// row read half of each 32-byte sector: 5 to 8 us longer after prompts' pieces).
+template <int DH>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_rows_kernel(const PagedArgs a, const int n_rows) {
+  constexpr int kQuads = DH / 4 / (kJoinThreads / 32), kCols = 4 * kQuads;   // of a warp
+  pdl_trigger();
+  pdl_wait();
+  const JoinJob job = a.join[blockIdx.x];
+  const int n = blockIdx.y * 32 + (threadIdx.x & 31), quad0 = (threadIdx.x >> 5) * kQuads;
+  if (job.parts == 0 || job.r0 + n >= job.rows) return;   // (n < n_rows: whole blocks)
+  float m = -INFINITY, l = 0.f, o[kCols] = {};
+  auto load = [&](int p, float2 &ml, float4 (&y)[kQuads]) {
+    const size_t slot = static_cast<size_t>(p == 0 ? job.slot : 2 * (blockIdx.x + p)) * n_rows;
+    ml = a.part_ml[slot + n];
+    const float4 *src = reinterpret_cast<const float4 *>(a.part_o + slot * DH) + n;
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) y[i] = src[(quad0 + i) * n_rows];
+  };
+  float2 ml;
+  float4 y[kQuads];
+  load(0, ml, y);
+  for (int p = 0; p < job.parts; ++p) {
+    float2 ml_next = ml;
+    float4 next[kQuads];
+    if (p + 1 < job.parts) load(p + 1, ml_next, next);   // on its way meanwhile
+    const float mn = fmaxf(m, ml.x), f = ex2_approx(m - mn), g = ex2_approx(ml.x - mn);
+    l = l * f + ml.y * g;
+    m = mn;
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+      o[4 * i] = o[4 * i] * f + y[i].x * g;
+      o[4 * i + 1] = o[4 * i + 1] * f + y[i].y * g;
+      o[4 * i + 2] = o[4 * i + 2] * f + y[i].z * g;
+      o[4 * i + 3] = o[4 * i + 3] * f + y[i].w * g;
+      y[i] = next[i];
+    }
+    ml = ml_next;
+  }
+  const int r = job.r0 + n, t = r / a.group;
+  const size_t row = static_cast<size_t>(job.q0 + t) * a.Hq + job.h * a.group + (r - t * a.group);
+#pragma unroll
+  for (int e = 0; e < kCols; ++e) o[e] = l != 0.f ? o[e] / l : 0.f;
+  if (a.out_fp32) {
+    float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * DH) + quad0;
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  } else {
+    uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + row * DH + quad0 * 4);
+#pragma unroll
+    for (int i = 0; i < kCols / 8; ++i) d[i] = pack8(o + 8 * i);
+  }
+  if (a.lse && quad0 == 0) a.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -872,8 +936,9 @@ dllm_status launch_attn(const dllm_kv_pages *pages, const dllm_paged_attn_args *
   if (st != DLLM_OK) return st;
   unsigned launches = 1;
   if (split) {
-    const cudaError_t e = launch_pdl(paged_join_kernel<DH>, dim3(ctas, (n * 32 + kJoinThreads - 1) / kJoinThreads),
-                                     dim3(kJoinThreads), 0, s, g, n);
+    const cudaError_t e =
+        n <= 32 ? launch_pdl(paged_join_kernel<DH>, dim3(ctas, (n * 32 + kJoinThreads - 1) / kJoinThreads), dim3(kJoinThreads), 0, s, g, n)
+                : launch_pdl(paged_join_rows_kernel<DH>, dim3(ctas, n / 32), dim3(kJoinThreads), 0, s, g, n);
     if (e != cudaSuccess) return cuda_error(e);
     launches = 2;
   }

@@ -522,10 +522,19 @@ dllm_status dllm_kv_read(const dllm_kv_pages *pages /* host */, dllm_bf16 *k,
  *            them, q_rows or the table is not processed (DLLM_DEV_OFFSETS)
  * The cache must hold the rows' own K/V already (dllm_kv_write before, on
  * the same stream). Cached rows that no query row of the request sees may
- * hold anything, infinities and NaN included.
- *   Scores, maxima, sums and outputs are accumulated in fp32; the weights
- *   that multiply V are rounded to bf16 (e4m3 pages: to 9 bits or more).
- *   The same call on the same GPU gives the same bits.
+ * hold anything, infinities and NaN included; a V row with an infinity or
+ * NaN that some rows of a request see may also reach the request's other
+ * rows of the same cached head (0 * inf), and nothing else.
+ *   Scores, maxima, sums and outputs are accumulated in fp32. The weights
+ *   that multiply V are rounded to bf16 or, for e4m3 pages and up to 32 query
+ *   rows per request and cached head, weight times V scale to 9 bits down to
+ *   2^-30 of the largest V scale among the keys that the request's rows see,
+ *   and to 2^-42 of it below. With e4m3 pages, elements of q below 2^-10 of
+ *   the largest of their row are off by up to 2^-19 of that. Sums are divided
+ *   at the end: |v| below 2^60 keeps them finite at any length.
+ *   The same call on the same GPU gives the same bits. One call serves any
+ *   mix of requests, but the largest max_q decides the tiles of all: many
+ *   single tokens beside a piece of a prompt are faster in a call of their own.
  *   Supported: Hq a multiple of heads, Hq / heads <= 64; B <= 4096;
  *   q_rows * Hq, max_q * Hq, max_kv, left, right and sinks < 2^30.
  * dllm_paged_attn_workspace: bytes that serve this call and every call with
