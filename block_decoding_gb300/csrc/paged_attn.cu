@@ -861,17 +861,18 @@ dllm_status check_shape(const dllm_kv_pages *pages, const dllm_paged_attn_args *
 // Rows of a row tile. Up to 32 rows of a request and cached head are the N of
 // the MMAs here, more are the M of those in paged_rows.cu. Measured (us; cached
 // heads x group, dh 128, keys of a request):
-//   4 rows, 32 requests, 8 x 4, 4000 keys:  tiles of 16: 87 (e4m3: 62), 32: 89 (74), 128: 93 (106)
-//   32 rows, else the same:                 32: 91 (86), 128: 96 (108)
-//   128 rows, 16 requests, else the same:   128: 52 (62), 256: 55 (64); 64 as N: half as long again as 128
+//   4 rows, 32 requests, 8 x 4, 4000 keys:  tiles of 16: 87 (e4m3: 61), 32: 89 (74), 128: 93 (107)
+//   32 rows, else the same:                 32: 90 (86), 128: 95 (108)
+//   128 rows, 16 requests, else the same:   128: 50 (61), 256: 52 (61); 64 as N: half as long again as 128
 // Tiles of 256 read each K and V tile once for twice the rows, but leave
 // partial results of twice the size where items are divided, which weighs more
 // in small calls. Measured by key tiles of all 256-row items together:
-//   512 rows, 4000 keys, 4 requests x 8 heads (2048):  128: 40 (59), 256: 51 (64)
-//   1200 rows, 4000 keys, 2 x 8 (2560):                128: 50 (74), 256: 56 (74)
-//   2048 rows, 1000 keys, 4 x 8 (2048):                128: 55 (82), 256: 52 (68)
-//   512 rows, 4000 keys, 8 x 8 (4096):                 128: 85 (113), 256: 70 (95)
-//   512 rows, 4000 keys, 24 x 8 (12288):               128: 257 (289), 256: 181 (246)
+//   400 rows, 2000 keys, 2 x 8, dh 64 (512):           128: 19 (26), 256: 22 (27)
+//   512 rows, 4000 keys, 4 requests x 8 heads (2048):  128: 38 (58), 256: 46 (59)
+//   1200 rows, 4000 keys, 2 x 8 (2560):                128: 48 (71), 256: 52 (68)
+//   2048 rows, 1000 keys, 4 x 8 (2048):                128: 53 (81), 256: 48 (64)
+//   512 rows, 4000 keys, 8 x 8 (4096):                 128: 82 (109), 256: 66 (91)
+//   512 rows, 4000 keys, 24 x 8 (12288):               128: 255 (279), 256: 176 (240)
 // (never more with a larger B, max_q or max_kv: the workspace grows with it)
 constexpr double kFewTiles = 3000, kFewTilesE4m3 = 1500;
 

@@ -31,11 +31,11 @@
 // of the rows); the scores' columns are multiplied by scale * K scale.
 //
 // Pieces of two prompts of 1200 to 1536 tokens over 9 to 12 thousand keys (bf16,
-// 8 x 4 heads, dh 128, causal) take 335 us: 1.32 PFLOP/s, 71 % of a plain
+// 8 x 4 heads, dh 128, causal) take 331 us with the join: 1.34 PFLOP/s, 72 % of a plain
 // matrix product's rate. Bound by the tensor cores: a tile of 256 x 128 costs
 // 3.1 k cycles where its MMAs alone take 2.75 k; some 10 us pass until the first
 // scores. Four prompts' pieces of 300 to 512 tokens over 1500 to 8000 keys
-// (e4m3) take 247 us, 0.80 PFLOP/s: the softmax warps and the converters share
+// (e4m3) take 239 us, 0.83 PFLOP/s: the softmax warps and the converters share
 // the issue slots (of 253 us at the time, 27 went without the K scales' products
 // and their loads, 18 without the conversion; a second group of converters
 // leaves the softmax too few registers: 28 longer). 16 denoising blocks of 64 to 96 rows over 352 to
