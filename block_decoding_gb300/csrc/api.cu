@@ -6,6 +6,7 @@
 #include <utility>
 
 #include "common.cuh"
+#include "pages.cuh"
 #include "umma.cuh"
 
 namespace dllm {

@@ -20,8 +20,6 @@ uint32_t status_head(bool clear);
 uint32_t status_commit(bool clear);
 uint32_t status_model(bool clear);
 uint32_t status_moe(bool clear);
-uint32_t status_kv(bool clear);
-uint32_t status_paged(bool clear);
 
 #define DLLM_DEFINE_STATUS(tag)                                              \
   static __device__ unsigned int g_status_##tag;                             \

@@ -3,7 +3,7 @@
 #pragma once
 
 #include "pages.cuh"
-#include "umma.cuh"
+#include "umma_pages.cuh"
 
 namespace dllm {
 

@@ -6,6 +6,9 @@
 
 namespace dllm {
 
+uint32_t status_kv(bool clear);
+uint32_t status_paged(bool clear);
+
 struct KvPages {
   uint8_t *k, *v;                  // [num_pages][heads][page_size][dh], bf16 or e4m3
   uint8_t *k_scale, *v_scale;      // [num_pages][heads][page_size], or null (bf16)

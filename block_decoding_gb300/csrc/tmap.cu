@@ -3,7 +3,7 @@
 // per-device SM count used to size persistent grids.
 #include <mutex>
 
-#include "umma.cuh"
+#include "umma_pages.cuh"
 
 namespace dllm {
 

@@ -449,8 +449,9 @@ dllm_status dllm_moe_ffn(const dllm_bf16 *h, const dllm_bf16 *w_router,
  * floating-point code no precision, so a code is within half an e4m3 step
  * of its element (2^-4 relative; below 2^-6 * 2^e, 2^-10 * 2^e absolute).
  * Magnitudes above 1.875 * 2^127 are stored as that value. A row that holds
- * an infinity or NaN has the byte 255: all of it stands for NaN. (No row has
- * NaN codes; pages filled by other means must not have any either.)
+ * an infinity or NaN has the byte 255: all of it stands for NaN. (Bytes are 10
+ * to 247 or 255, and no row has NaN codes: pages filled by other means must
+ * keep to that.)
  *
  *   Supported: dh in {64, 128}; page_size in {16, 32, 64, 128};
  *   1 <= heads <= 256; num_pages * heads * page_size < 2^31; k, v,

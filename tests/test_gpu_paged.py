@@ -649,6 +649,45 @@ def test_large_calls_with_many_pieces_each(dh, fp8):
         b.check(*b.run(left=100, right=30, sinks=140, max_kv=max_kv), left=100, right=30, sinks=140)
 
 
+@pytest.mark.parametrize("w", [3, 12, 40, 200])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_nan_and_infinite_queries_stay_in_their_rows(w, fp8):
+    b = Batch(42, [600, 250], 2, 64, 32, fp8)
+    b.queries([w, w], 2)
+    want, z = b.run(right=0)
+    q = b.q.clone()
+    b.q[1, 2, 5], b.q[w + 2, 0, 9] = float("nan"), float("inf")
+    out, lse = b.run(right=0)
+    assert torch.isnan(out[1, 2]).all() and torch.isnan(lse[1, 2]) and torch.isnan(out[w + 2, 0]).all()
+    b.q = q
+    for t, good in ((out, want), (lse, z)):
+        t[1, 2], t[w + 2, 0] = good[1, 2], good[w + 2, 0]
+    b.check(out, lse, right=0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_the_most_heads(fp8):
+    b = Batch(43, [3, 140], 256, 64, 16, fp8)
+    k, v = bd.kv_read(b.pages, b.off, i32([0, 0]), b.table, 143)
+    assert np.array_equal(f64(k), np.concatenate(b.k)) and np.array_equal(f64(v), np.concatenate(b.v))
+    for w in ([1, 2], [0, 20], [3, 129]):
+        b.queries(w, 1)
+        b.check(*b.run(right=0), right=0)
+
+
+@pytest.mark.parametrize("w", [1, 40])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_requests_that_share_pages(w, fp8):
+    # the first 256 keys of both are the first request's, one of whose pages is named twice
+    b = Batch(44, [700, 500], 2, 64, 64, fp8)
+    b.table[1, :4] = b.table[0, :4]
+    b.table[0, 5] = b.table[0, 2]
+    b.k[1][:256], b.v[1][:256] = b.k[0][:256], b.v[0][:256]
+    b.k[0][320:384], b.v[0][320:384] = b.k[0][128:192], b.v[0][128:192]
+    b.queries([w, w], 2)
+    b.check(*b.run(right=0), right=0)
+
+
 @pytest.mark.parametrize("name", ["max_q", "max_kv", "left", "right", "sinks"])
 def test_numbers_beyond_32_bits_are_refused(name):
     b = Batch(39, [20], 1, 64, 16, False)
