@@ -631,6 +631,8 @@ def paged_attn_workspace(pages: KVPages, B, Hq, max_q, max_kv) -> int:
     key = (int(B), int(Hq), int(max_q), int(max_kv))
     need = pages._need.get(key)
     if need is None:
+        if max(key) >= 1 << 31 or min(key) < 0:
+            raise ValueError("B, Hq, max_q and max_kv must be 0 to 2^31 - 1")
         a = PagedAttnArgs(B=key[0], Hq=key[1], max_q=key[2], max_kv=key[3])
         need = int(LIB.dllm_paged_attn_workspace(ctypes.byref(pages.desc), ctypes.byref(a)))
         if len(pages._need) < 4096:

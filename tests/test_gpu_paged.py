@@ -695,6 +695,9 @@ def test_numbers_beyond_32_bits_are_refused(name):
     kw = {"max_q": 3, "max_kv": 20, "left": -1, "right": -1, "sinks": 0, name: (1 << 32) + 3}
     with pytest.raises(ValueError):
         bd.paged_attn(b.q, b.pages, i32([0, 3]), i32([20]), b.table, **kw)
+    if name in ("max_q", "max_kv"):
+        with pytest.raises(ValueError):
+            bd.paged_attn_workspace(b.pages, 1, 1, kw["max_q"], kw["max_kv"])
 
 @pytest.mark.parametrize("fp8", [False, True])
 def test_a_run_of_them_together(fp8):
