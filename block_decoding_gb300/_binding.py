@@ -523,11 +523,8 @@ class KVPages:
             _ptr_on(k_scale, dev, torch.uint8, "k_scale") if fp8 else None,
             _ptr_on(v_scale, dev, torch.uint8, "v_scale") if fp8 else None,
             1 if fp8 else 0, self.num_pages, self.page_size, self.heads, self.dh)
+        self.device = k.device
         self._need = {}     # workspace bytes by shape
-
-    @property
-    def device(self):
-        return self.k.device
 
     @classmethod
     def empty(cls, num_pages, page_size, heads, dh, dtype=torch.bfloat16, device="cuda"):
@@ -611,18 +608,25 @@ def kv_write(pages: KVPages, k, v, off, pos0, page_table, stream=None):
     _launch("dllm_kv_write", dev, stream, pages.desc, kp, vp, ks, vs, rows, po, pp, pt, n, B)
 
 
+def _rows_out(t, shape, pages, name, stream):
+    """The bf16 rows `t`, allocated unless given, and their pointer."""
+    if t is None:
+        t = _alloc(shape, torch.bfloat16, pages.device, stream)
+        return t, t.data_ptr()
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return t, _ptr_on(t, pages.index, torch.bfloat16, name)
+
+
 def kv_read(pages: KVPages, off, pos0, page_table, rows, k=None, v=None, stream=None):
     """The cached rows of positions pos0[i] + t as bf16 rows off[i] + t of (k, v)
     [rows][heads][dh] (allocated unless given)."""
     dev = pages.index
     shape = (int(rows), pages.heads, pages.dh)
-    k = k if k is not None else _alloc(shape, torch.bfloat16, pages.k.device, stream)
-    v = v if v is not None else _alloc(shape, torch.bfloat16, pages.k.device, stream)
-    if k.shape != shape or v.shape != shape:
-        raise ValueError(f"k and v must be {list(shape)}")
     B, n, po, pt, pp = _batch(dev, off, page_table, pos0, "pos0")
-    _launch("dllm_kv_read", dev, stream, pages.desc, _ptr_on(k, dev, torch.bfloat16, "k"),
-            _ptr_on(v, dev, torch.bfloat16, "v"), shape[0], po, pp, pt, n, B)
+    k, kp = _rows_out(k, shape, pages, "k", stream)
+    v, vp = _rows_out(v, shape, pages, "v", stream)
+    _launch("dllm_kv_read", dev, stream, pages.desc, kp, vp, shape[0], po, pp, pt, n, B)
     return k, v
 
 
@@ -640,6 +644,9 @@ def paged_attn_workspace(pages: KVPages, B, Hq, max_q, max_kv) -> int:
     return need
 
 
+_I31 = 1 << 31
+
+
 def paged_attn(q, pages: KVPages, q_off, kv_len, page_table, max_q, max_kv, q_pos=None, scale=None, left=-1, right=-1,
                sinks=0, out=None, out_fp32=False, return_lse=False, lse=None, ws=None, stream=None):
     """Attention of q [rows][Hq][dh] bf16 (any row stride) over the pages.
@@ -649,8 +656,9 @@ def paged_attn(q, pages: KVPages, q_off, kv_len, page_table, max_q, max_kv, q_po
     (u >= position - left or u < sinks); negative left / right: no limit.
     Returns out [rows][Hq][dh], or (out, lse [rows][Hq]) with return_lse.
     """
-    if max(max_q, max_kv, left, right, sinks) >= 1 << 31 or min(max_q, max_kv, left, right, sinks) < -(1 << 31):
-        raise ValueError("max_q, max_kv, left, right and sinks must fit 32 bits")
+    # (ctypes would cut longer numbers off)
+    if not (0 <= max_q < _I31 and 0 <= max_kv < _I31 and 0 <= sinks < _I31 and -_I31 <= left < _I31 and -_I31 <= right < _I31):
+        raise ValueError("max_q, max_kv, left, right and sinks must fit 32 bits, and only left and right may be negative")
     dev, dh = pages.index, pages.dh
     rows, Hq = (q.shape[0], q.shape[1]) if isinstance(q, torch.Tensor) and q.dim() == 3 else (0, 0)
     qp, qs = _rows_ptr(q, dev, Hq, dh, "q")
@@ -661,21 +669,30 @@ def paged_attn(q, pages: KVPages, q_off, kv_len, page_table, max_q, max_kv, q_po
         if q_pos.numel() != B:
             raise ValueError("q_pos must have one entry per request")
     if out is None:
-        out = _alloc((rows, Hq, dh), torch.float32 if out_fp32 else torch.bfloat16, q.device, stream)
+        out = _alloc((rows, Hq, dh), torch.float32 if out_fp32 else torch.bfloat16, pages.device, stream)
+        op = out.data_ptr()
     elif out.shape != (rows, Hq, dh) or out.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"out must be bf16 or fp32 [{rows}][{Hq}][{dh}]")
-    if lse is None:
-        lse = _alloc((rows, Hq), torch.float32, q.device, stream) if return_lse else None
-    elif lse.shape != (rows, Hq):
-        raise ValueError(f"lse must be [{rows}][{Hq}]")
-    a = PagedAttnArgs(qp, qs, _ptr_on(out, dev, out.dtype, "out"), 1 if out.dtype is torch.float32 else 0,
-                      None if lse is None else _ptr_on(lse, dev, torch.float32, "lse"), po, pn, pp, pt, n, B, Hq,
-                      int(max_q), int(max_kv), rows, 1.0 / math.sqrt(dh) if scale is None else float(scale), int(left),
-                      int(right), int(sinks))
-    if ws is None:
+    else:
+        op = _ptr_on(out, dev, out.dtype, "out")
+        out_fp32 = out.dtype is torch.float32
+    lp = None
+    if lse is not None:
+        if lse.shape != (rows, Hq):
+            raise ValueError(f"lse must be [{rows}][{Hq}]")
+        lp = _ptr_on(lse, dev, torch.float32, "lse")
+    elif return_lse:
+        lse = _alloc((rows, Hq), torch.float32, pages.device, stream)
+        lp = lse.data_ptr()
+    a = PagedAttnArgs(qp, qs, op, 1 if out_fp32 else 0, lp, po, pn, pp, pt, n, B, Hq, int(max_q), int(max_kv), rows,
+                      1.0 / math.sqrt(dh) if scale is None else float(scale), int(left), int(right), int(sinks))
+    wp, need = None, 0
+    if ws is not None:
+        wp, need = _ptr_on(ws, dev, ws.dtype, "ws"), ws.numel() * ws.element_size()
+    else:
         need = paged_attn_workspace(pages, B, Hq, max_q, max_kv)
         if need:
-            ws = _alloc(need, torch.uint8, q.device, stream)
-    _launch("dllm_paged_attn", dev, stream, pages.desc, a, None if ws is None else _ptr_on(ws, dev, ws.dtype, "ws"),
-            0 if ws is None else ws.numel() * ws.element_size())
+            ws = _alloc(need, torch.uint8, pages.device, stream)
+            wp = ws.data_ptr()
+    _launch("dllm_paged_attn", dev, stream, pages.desc, a, wp, need)
     return (out, lse) if return_lse else out

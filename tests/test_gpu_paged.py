@@ -688,6 +688,20 @@ def test_requests_that_share_pages(w, fp8):
     b.check(*b.run(right=0), right=0)
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn_shapes(seed):
+    rng = np.random.default_rng(100 + seed)
+    pick = lambda *x: x[rng.integers(len(x))]  # noqa: E731
+    B, top = int(pick(1, 2, 5, 40, 150)), int(pick(3, 130, 700, 2500))
+    lens = [int(n) for n in rng.integers(0, max(2, top // max(1, B // 20)), B)]
+    b = Batch(200 + seed, lens, int(pick(1, 2, 3)), int(pick(64, 128)), int(pick(16, 32, 64, 128)), bool(pick(0, 1)))
+    for _ in range(2):
+        b.queries([int(x) for x in rng.integers(0, pick(2, 2, 10, 40, 140, 330) if B < 40 else pick(2, 10, 70), B)], int(pick(1, 2, 4, 5, 7)))
+        mask = dict(left=int(pick(-1, 0, 9, 127, 128, 600)), right=int(pick(-1, 0, 0, 5, 200)), sinks=int(pick(0, 1, 4, 129, 1000)))
+        pos = [int(x) for x in rng.integers(-50, top + 50, B)] if pick(0, 0, 1) else None
+        b.check(*b.run(pos=pos, max_kv=pick(None, LARGE), out_fp32=bool(pick(0, 1)), **mask), pos=pos, **mask)
+
+
 @pytest.mark.parametrize("name", ["max_q", "max_kv", "left", "right", "sinks"])
 def test_numbers_beyond_32_bits_are_refused(name):
     b = Batch(39, [20], 1, 64, 16, False)
