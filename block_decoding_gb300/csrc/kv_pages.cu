@@ -7,12 +7,14 @@
 // lanes of a row read and write contiguous runs. A block takes neighbouring
 // rows of up to four neighbouring heads: runs of several rows on the pages'
 // side, of several heads on the other.
-// Measured (dh 128, 32 heads, e4m3): 10 k rows written in 57 us (4.5 TB/s, 66 %
-// of a copy's rate), 19 k rows read in 81 us (5.9 TB/s, 88 %); 64 single
-// tokens (8 heads) written in 3.2 us, of which nearly all is the launch and the
-// chain request -> page -> store. Writing loads its rows before it looks their
-// places up (60 us the other way round). Several rows per thread: 58 us, and 4.4
-// for the 64 tokens; a persistent grid that loads its next rows ahead: slower.
+// Measured (dh 128, 32 heads, e4m3): 10 k rows written in 54.6 us (4.7 TB/s, 69 %
+// of a copy's rate; short of issue slots: 57.3 us when every thread looked its
+// row's place up and multiplied in fp32), 19 k rows read in 79.8 us (6.0 TB/s,
+// 89 %); 64 single tokens (8 heads) written in 3.1 us, of which nearly all is the
+// launch and the chain request -> page -> store. Writing loads its rows before it
+// looks their places up (3 us less). Blocks of 64 or 256 threads and of 2 or 8
+// heads: within 3 %. Several rows per thread: 4.4 us for the 64 tokens; a
+// persistent grid that loads its next rows ahead: slower.
 #include "pages.cuh"
 
 namespace dllm {
@@ -21,7 +23,7 @@ DLLM_DEFINE_STATUS(kv)
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kHeads = 4;   // heads of one block, at most
 
 struct MoveArgs {
@@ -29,6 +31,9 @@ struct MoveArgs {
   uint16_t *k, *v;             // the contiguous side
   long long k_stride, v_stride;
   int rows, B;
+  int hb, per;                 // heads and rows of a block
+  int run;                     // blocks until the slower of row and head moves
+  uint32_t inv;                // n / hb = n * inv >> 16 for n < 256
   const int32_t *off, *pos0;
   unsigned int *status;
 };
@@ -46,11 +51,15 @@ __device__ __forceinline__ int request_of(const int32_t *off, int B, int r) {
 
 // Eight bf16 -> eight e4m3 codes of x * f.
 __device__ __forceinline__ uint2 quantise8(const uint4 &u, float f) {
-  float x[8];
-  unpack8(u, x);
+  // (a product with a power of two is exact in bf16 too, but for what is far
+  // below the least code)
+  const uint32_t f2 = bf16x2_of(f), x[4] = {u.x, u.y, u.z, u.w};
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = f32_to_e4m3x2(x[2 * i] * f, x[2 * i + 1] * f);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t y = mul_bf16x2(x[i], f2);
+    w[i] = f32_to_e4m3x2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u));
+  }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
@@ -84,31 +93,33 @@ __device__ __forceinline__ int quantise_row(const uint4 &a, const uint4 &b, uint
   return m >= 0x7f80u ? 255 : byte;
 }
 
-// This thread's row and head: unit u (LPR lanes each) of a block has head
-// h0 + u % hb of row r0 + u / hb. No row: 2^30.
-template <int LPR>
-__device__ __forceinline__ void place_of(const MoveArgs &g, int &r, int &h) {
-  const int hb = min(g.c.heads, kHeads), groups = (g.c.heads + hb - 1) / hb;
-  const int u = threadIdx.x / LPR, per = (kThreads / LPR) / hb;
-  const int rg = blockIdx.x / groups, hg = blockIdx.x - rg * groups;
-  r = rg * per + u / hb;
-  h = hg * hb + u % hb;
-  if (u >= per * hb || h >= g.c.heads) r = 1 << 30;
+// The block's first row, and this thread's row in the block and head: unit u
+// (LPR lanes each) of a block has head h0 + u % hb of row r0 + u / hb. Returns
+// whether there is such a unit. Neighbouring blocks have neighbouring rows of
+// the same heads where rows are written (54.6 us; heads first: 55.5), and the
+// heads of the same rows where they are read (79.8; rows first: 82.6).
+template <int LPR, bool ROWS_FIRST>
+__device__ __forceinline__ bool place_of(const MoveArgs &g, int &r0, int &n, int &h) {
+  const int u = threadIdx.x / LPR, slow = blockIdx.x / g.run, fast = blockIdx.x - slow * g.run;
+  r0 = (ROWS_FIRST ? fast : slow) * g.per;
+  n = static_cast<int>(u * g.inv >> 16);
+  h = (ROWS_FIRST ? slow : fast) * g.hb + u - n * g.hb;
+  return n < g.per && h < g.c.heads;
 }
 
-// Cache row of row r for head h: -1 when it is in no request, -2 when it has
+// Cache row of row r for head 0: -1 when it is in no request, -2 when it has
 // no place (reported).
-__device__ __forceinline__ int find_row(const MoveArgs &g, int r, int h) {
+__device__ __forceinline__ int find_row(const MoveArgs &g, int r) {
   if (r >= g.rows) return -1;
   const int i = request_of(g.off, g.B, r);
   if (i < 0) return -1;
   const long long u = static_cast<long long>(g.pos0[i]) + (r - g.off[i]);
   const int row = u < 0 || u > 0x7fffffffll ? -1 : page_row(g.c, i, static_cast<int>(u));
   if (row < 0) {
-    if (h == 0) atomicOr(g.status, DLLM_DEV_PAGE);
+    atomicOr(g.status, DLLM_DEV_PAGE);
     return -2;
   }
-  return row + (h << g.c.page_shift);
+  return row;
 }
 
 template <int DH, bool FP8>
@@ -116,19 +127,26 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const MoveArgs g) {
   constexpr int LPR = DH / 16;
   pdl_trigger();
   pdl_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0 && (g.off[0] < 0 || g.off[g.B] > g.rows)) atomicOr(g.status, DLLM_DEV_OFFSETS);
+  if (blockIdx.x + threadIdx.x == 0 && (g.off[0] < 0 || g.off[g.B] > g.rows)) atomicOr(g.status, DLLM_DEV_OFFSETS);
+  __shared__ int s_row[kThreads / LPR];
   const int l = threadIdx.x % LPR;
-  int r, h;
-  place_of<LPR>(g, r, h);
+  int r0, n, h;
+  const bool live = place_of<LPR, true>(g, r0, n, h);
+  const int r = r0 + n;
   uint4 ka = make_uint4(0, 0, 0, 0), kb = ka, va = ka, vb = ka;
-  if (r < g.rows) {
+  if (live && r < g.rows) {
     const uint4 *ks = reinterpret_cast<const uint4 *>(g.k + r * g.k_stride + h * DH);
     const uint4 *vs = reinterpret_cast<const uint4 *>(g.v + r * g.v_stride + h * DH);
     ka = __ldg(ks + l); kb = __ldg(ks + l + LPR);
     va = __ldg(vs + l); vb = __ldg(vs + l + LPR);
   }
-  const int row = find_row(g, r, h);
-  const size_t at = static_cast<size_t>(max(row, 0));
+  // the places of the block's rows, found once while the rows are on their way
+  // (the kernel is short of issue slots; reading, which has to wait for them
+  // before its loads, every thread finds its own: 81 us, this way 84)
+  if (threadIdx.x < g.per) s_row[threadIdx.x] = find_row(g, r0 + threadIdx.x);
+  __syncthreads();
+  const int row = live ? s_row[n] : -1;
+  const size_t at = static_cast<size_t>(max(row, 0)) + (static_cast<size_t>(h) << g.c.page_shift);
   if constexpr (FP8) {
     uint2 qa, qb;
     const int kbyte = quantise_row<LPR>(ka, kb, qa, qb);
@@ -171,15 +189,15 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const MoveArgs g) {
   constexpr int LPR = DH / 16;
   pdl_trigger();
   pdl_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0 && (g.off[0] < 0 || g.off[g.B] > g.rows)) atomicOr(g.status, DLLM_DEV_OFFSETS);
+  if (blockIdx.x + threadIdx.x == 0 && (g.off[0] < 0 || g.off[g.B] > g.rows)) atomicOr(g.status, DLLM_DEV_OFFSETS);
   const int l = threadIdx.x % LPR;
-  int r, h;
-  place_of<LPR>(g, r, h);
-  const int row = find_row(g, r, h);
+  int r0, n, h;
+  if (!place_of<LPR, false>(g, r0, n, h)) return;
+  const int r = r0 + n, row = find_row(g, r);
   if (row == -1) return;   // a row without a place (-2) reads as zeros
   uint4 ka = make_uint4(0, 0, 0, 0), kb = ka, va = ka, vb = ka;
   if (row >= 0) {
-    const size_t at = static_cast<size_t>(row);
+    const size_t at = static_cast<size_t>(row) + (static_cast<size_t>(h) << g.c.page_shift);
     if constexpr (FP8) {
       const uint2 *ks = reinterpret_cast<const uint2 *>(g.c.k + at * DH);
       const uint2 *vs = reinterpret_cast<const uint2 *>(g.c.v + at * DH);
@@ -220,9 +238,12 @@ dllm_status move(bool write, const dllm_kv_pages *pages, uint16_t *k, uint16_t *
   g.rows = rows; g.B = B; g.off = off; g.pos0 = pos0;
   cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&g.status), g_status_kv);
   if (e != cudaSuccess) return cuda_error(e);
-  const int hb = pages->heads < kHeads ? pages->heads : kHeads, groups = (pages->heads + hb - 1) / hb;
-  const int per_block = kThreads / (pages->dh / 16) / hb;   // rows
-  const long long blocks = (static_cast<long long>(rows) + per_block - 1) / per_block * groups;
+  g.hb = pages->heads < kHeads ? pages->heads : kHeads;
+  g.per = kThreads / (pages->dh / 16) / g.hb;
+  g.inv = 65536u / g.hb + 1;
+  const int groups = (pages->heads + g.hb - 1) / g.hb, row_blocks = (rows - 1) / g.per + 1;
+  const long long blocks = static_cast<long long>(row_blocks) * groups;
+  g.run = write ? row_blocks : groups;
   if (blocks > 0x7fffffffll) return DLLM_ERR_UNSUPPORTED;
   const bool fp8 = pages->type == DLLM_KV_E4M3;
   void (*kern)(MoveArgs);
