@@ -586,11 +586,25 @@ def _launch(what, index, stream, *args):
     _ck(rc, what)
 
 
+def _scratch(nbytes, device, stream):
+    """Workspace bytes of a call on `stream` (None: the current stream). The
+    memory is that stream's own: a block that the current stream's calls have
+    given back, but that their kernels still use, is not handed out, and this
+    one goes to no other stream's call when it is given back."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _alloc(shape, dtype, device, stream):
-    """torch.empty that stays allocated until `stream`'s work on it is done."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    """torch.empty, as _scratch, for what the caller gets back: kept, once the
+    caller gives it up, until what the current stream then does with it is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 
@@ -620,7 +634,8 @@ def _rows_out(t, shape, pages, name, stream):
 
 def kv_read(pages: KVPages, off, pos0, page_table, rows, k=None, v=None, stream=None):
     """The cached rows of positions pos0[i] + t as bf16 rows off[i] + t of (k, v)
-    [rows][heads][dh] (allocated unless given)."""
+    [rows][heads][dh] (allocated unless given; with `stream`, order other
+    streams' use of them after it)."""
     dev = pages.index
     shape = (int(rows), pages.heads, pages.dh)
     B, n, po, pt, pp = _batch(dev, off, page_table, pos0, "pos0")
@@ -654,7 +669,8 @@ def paged_attn(q, pages: KVPages, q_off, kv_len, page_table, max_q, max_kv, q_po
     Row t of request i has position q_pos[i] + t (default: the last rows of
     the cache) and sees keys u < kv_len[i] with u <= position + right and
     (u >= position - left or u < sinks); negative left / right: no limit.
-    Returns out [rows][Hq][dh], or (out, lse [rows][Hq]) with return_lse.
+    Returns out [rows][Hq][dh], or (out, lse [rows][Hq]) with return_lse; with
+    `stream`, order other streams' use of them after it.
     """
     # (ctypes would cut longer numbers off)
     if not (0 <= max_q < _I31 and 0 <= max_kv < _I31 and 0 <= sinks < _I31 and -_I31 <= left < _I31 and -_I31 <= right < _I31):
@@ -692,7 +708,7 @@ def paged_attn(q, pages: KVPages, q_off, kv_len, page_table, max_q, max_kv, q_po
     else:
         need = paged_attn_workspace(pages, B, Hq, max_q, max_kv)
         if need:
-            ws = _alloc(need, torch.uint8, pages.device, stream)
+            ws = _scratch(need, pages.device, stream)
             wp = ws.data_ptr()
     _launch("dllm_paged_attn", dev, stream, pages.desc, a, wp, need)
     return (out, lse) if return_lse else out

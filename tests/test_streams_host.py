@@ -1,0 +1,86 @@
+"""Calls on a given stream take their memory from that stream (CPU only: the
+library and the allocator are fakes that record what is asked of them)."""
+
+import contextlib
+import types
+
+import pytest
+import torch
+
+import block_decoding_gb300 as bd
+
+B = bd._binding
+
+
+class Stream:
+    cuda_stream = 77
+    device = torch.device("cpu")
+
+
+class World:
+    """Which stream was current at every allocation, and what was launched where."""
+
+    def __init__(self, mp):
+        self.caller, self.side = Stream(), Stream()
+        self.now = self.caller
+        self.blocks, self.recorded, self.launched = {}, [], []
+        empty = torch.empty
+
+        @contextlib.contextmanager
+        def stream(s):
+            before, self.now = self.now, s
+            yield
+            self.now = before
+
+        def record(t, s):
+            self.recorded.append((t.data_ptr(), s))
+
+        def new(*a, **kw):
+            t = empty(*a, **kw)
+            self.blocks[t.data_ptr()] = self.now
+            self.keep.append(t)
+            return t
+
+        self.keep = []
+        mp.setattr(torch, "empty", new)
+        mp.setattr(torch.cuda, "stream", stream)
+        mp.setattr(torch.cuda, "current_stream", lambda *a: self.now)
+        mp.setattr(torch.Tensor, "record_stream", record)
+        mp.setattr(B, "_ptr", lambda t, *a: None if t is None else t.data_ptr())
+        mp.setattr(B, "_ptr_on", lambda t, *a: t.data_ptr())
+        mp.setattr(B, "_rows_ptr", lambda t, *a: (t.data_ptr(), t.stride(0)))
+        mp.setattr(B, "_launch", lambda what, index, stream, *a: self.launched.append((what, stream)))
+        mp.setattr(B, "LIB", types.SimpleNamespace(dllm_paged_attn_workspace=lambda *a: 4096))
+
+    def check(self, returned, stream, scratch):
+        """Everything allocated belongs to `stream`; what is returned, and nothing else, is kept for the caller's."""
+        assert self.blocks and set(self.blocks.values()) == {stream or self.caller}
+        out = {t.data_ptr() for t in returned}
+        assert len(self.blocks) == len(out) + scratch
+        kept = {p for p, s in self.recorded if s is self.caller}
+        assert len(self.recorded) == len(kept) == (len(out) if stream else 0)
+        assert not stream or kept == out
+
+
+@pytest.fixture
+def world(monkeypatch):
+    w = types.SimpleNamespace()
+    zeros = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t)  # noqa: E731
+    w.i32 = lambda *v: torch.tensor(v, dtype=torch.int32)
+    w.zeros = zeros
+    w.pages = types.SimpleNamespace(index=0, device=torch.device("cpu"), heads=2, dh=64, desc=B.KvPagesDesc(), _need={})
+    w.w = World(monkeypatch)
+    return w
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_paged_calls_allocate_on_their_stream(world, side):
+    w = world.w
+    stream = w.side if side else None
+    table = torch.zeros((1, 2), dtype=torch.int32)
+    out = bd.paged_attn(world.zeros(3, 4, 64), world.pages, world.i32(0, 3), world.i32(20), table, 3, 20, return_lse=True,
+                        stream=stream)
+    w.check(out, stream, 1)
+    w.blocks.clear(), w.recorded.clear()
+    w.check(bd.kv_read(world.pages, world.i32(0, 3), world.i32(0), table, 3, stream=stream), stream, 0)
+    assert w.launched == [("dllm_paged_attn", stream), ("dllm_kv_read", stream)]
