@@ -145,6 +145,28 @@ def workspace(nbytes: int, device=None) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device or "cuda")
 
 
+def _scratch(nbytes, device, stream):
+    """Workspace bytes of a call on `stream` (None: the current stream). The
+    memory is that stream's own: a block that the current stream's calls have
+    given back, but that their kernels still use, is not handed out, and this
+    one goes to no other stream's call when it is given back."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _alloc(shape, dtype, device, stream):
+    """torch.empty, as _scratch, for what the caller gets back: kept, once the
+    caller gives it up, until what the current stream then does with it is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 # ---------------------------------------------------------------------------
 # entry points
 # ---------------------------------------------------------------------------
@@ -161,10 +183,10 @@ def block_attn(q, k, v, q_off, kv_off, max_q, max_kv, scale=None, out=None,
     if scale is None:
         scale = 1.0 / math.sqrt(dh)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32 if out_fp32 else torch.bfloat16, device=q.device)
+        out = _alloc(q.shape, torch.float32 if out_fp32 else torch.bfloat16, q.device, stream)
     need = block_attn_workspace(B, H, dh, max_q, max_kv)
     if ws is None and need:
-        ws = workspace(need, q.device)
+        ws = _scratch(need, q.device, stream)
     rc = LIB.dllm_block_attn(_ptr(q, torch.bfloat16, "q"), _ptr(k, torch.bfloat16, "k"),
                              _ptr(v, torch.bfloat16, "v"), _ptr(out, None, "out"),
                              1 if out.dtype == torch.float32 else 0,
@@ -187,15 +209,15 @@ def head_confidence(hidden, w_head, emb=None, with_pe=True, argmax=None, conf=No
     V = w_head.shape[0]
     dev = hidden.device
     with_pe = with_pe and emb is not None
-    argmax = argmax if argmax is not None else torch.empty(R, dtype=torch.int32, device=dev)
-    conf = conf if conf is not None else torch.empty(R, dtype=torch.float32, device=dev)
+    argmax = argmax if argmax is not None else _alloc(R, torch.int32, dev, stream)
+    conf = conf if conf is not None else _alloc(R, torch.float32, dev, stream)
     if with_pe and pe is None:
-        pe = torch.empty((R, d), dtype=torch.float32, device=dev)
+        pe = _alloc((R, d), torch.float32, dev, stream)
     if not with_pe:
         pe = None
     need = head_workspace(R, d, V, with_pe)
     if ws is None:
-        ws = workspace(need, dev)
+        ws = _scratch(max(need, 1), dev, stream)
     rc = LIB.dllm_head_confidence(_ptr(hidden, torch.bfloat16, "hidden"),
                                   _ptr(w_head, torch.bfloat16, "w_head"),
                                   _ptr(emb, torch.bfloat16, "emb") if emb is not None else None,
@@ -214,8 +236,8 @@ def commit(argmax, conf, pe, row_req, row_pos, mask, tokens, credit, prev, emb,
     V, d = emb.shape
     R = row_req.numel()
     dev = mask.device
-    next_emb = next_emb if next_emb is not None else torch.empty((B, blk, d), dtype=torch.bfloat16, device=dev)
-    n_commit = n_commit if n_commit is not None else torch.empty(B, dtype=torch.int32, device=dev)
+    next_emb = next_emb if next_emb is not None else _alloc((B, blk, d), torch.bfloat16, dev, stream)
+    n_commit = n_commit if n_commit is not None else _alloc(B, torch.int32, dev, stream)
     prm = params_struct(params)
     rc = LIB.dllm_commit(_ptr(argmax, torch.int32, "argmax"), _ptr(conf, torch.float32, "conf"),
                          _ptr(pe, torch.float32, "pe") if pe is not None else None,
@@ -318,7 +340,7 @@ def gemm_bf16(A, W, epilogue=0, aux=None, out=None, stream=None):
     """C = A W^T (+aux) or SwiGLU; A [M][K], W [N][K] (or [2N][K] for SwiGLU)."""
     M, K = A.shape
     N = W.shape[0] // 2 if epilogue == 2 else W.shape[0]
-    out = out if out is not None else torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+    out = out if out is not None else _alloc((M, N), torch.bfloat16, A.device, stream)
     rc = LIB.dllm_gemm_bf16(_ptr(A, torch.bfloat16, "A"), _ptr(W, torch.bfloat16, "W"),
                             _ptr(out, torch.bfloat16, "C"), M, N, K, int(epilogue),
                             _ptr(aux, torch.bfloat16, "aux") if aux is not None else None, _stream(stream))
@@ -351,8 +373,8 @@ def model_desc(weights: dict, max_seq: int):
 def model_forward(desc, x_in, pos0, k_cache, v_cache, ws=None, stream=None):
     n = x_in.shape[0]
     need = int(LIB.dllm_model_forward_workspace(ctypes.byref(desc), n))
-    ws = ws if ws is not None else workspace(need, x_in.device)
-    out = torch.empty_like(x_in)
+    ws = ws if ws is not None else _scratch(max(need, 1), x_in.device, stream)
+    out = _alloc(x_in.shape, x_in.dtype, x_in.device, stream)
     kc, vc = _ptr_array(k_cache), _ptr_array(v_cache)
     rc = LIB.dllm_model_forward(ctypes.byref(desc), _ptr(x_in, torch.bfloat16, "x_in"), n, int(pos0),
                                 ctypes.cast(kc, ctypes.POINTER(c_void_p)), ctypes.cast(vc, ctypes.POINTER(c_void_p)),
@@ -452,16 +474,16 @@ def moe_ffn(h, w_router, w13, w2, topk, out_fp32=True, out=None, ids=None, weigh
         raise ValueError("moe_ffn: inconsistent shapes")
     dev = h.device
     if out is None:
-        out = torch.empty((n, d), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=dev)
+        out = _alloc((n, d), torch.float32 if out_fp32 else torch.bfloat16, dev, stream)
     if ids is None:
-        ids = torch.empty((n, topk), dtype=torch.int32, device=dev)
+        ids = _alloc((n, topk), torch.int32, dev, stream)
     if weights is None:
-        weights = torch.empty((n, topk), dtype=torch.float32, device=dev)
+        weights = _alloc((n, topk), torch.float32, dev, stream)
     need = int(LIB.dllm_moe_ffn_workspace(n, d, E, F, topk))
     if need == 0 and n > 0:
         raise DllmError(2, "dllm_moe_ffn_workspace")
     if ws is None or ws.numel() < need:
-        ws = workspace(max(need, 256), dev)
+        ws = _scratch(max(need, 256), dev, stream)
     rc = LIB.dllm_moe_ffn(_ptr(h, torch.bfloat16, "h"), _ptr(w_router, torch.bfloat16, "w_router"),
                           _ptr(w13, torch.bfloat16, "w13"), _ptr(w2, torch.bfloat16, "w2"), n, d, E, F, topk,
                           _ptr(out, None, "out"), 1 if out.dtype == torch.float32 else 0,
@@ -584,28 +606,6 @@ def _launch(what, index, stream, *args):
         with torch.cuda.device(index):
             rc = fn(*args, stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index))
     _ck(rc, what)
-
-
-def _scratch(nbytes, device, stream):
-    """Workspace bytes of a call on `stream` (None: the current stream). The
-    memory is that stream's own: a block that the current stream's calls have
-    given back, but that their kernels still use, is not handed out, and this
-    one goes to no other stream's call when it is given back."""
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-
-
-def _alloc(shape, dtype, device, stream):
-    """torch.empty, as _scratch, for what the caller gets back: kept, once the
-    caller gives it up, until what the current stream then does with it is done."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(t.device))
-    return t
 
 
 def kv_write(pages: KVPages, k, v, off, pos0, page_table, stream=None):

@@ -120,3 +120,30 @@ def test_a_cache_filled_and_read_on_a_stream():
     torch.cuda.current_stream().wait_stream(side)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_product_and_head_beside_work_whose_memory_was_given_back():
+    gen = torch.Generator(device=DEV).manual_seed(11)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=DEV).to(torch.bfloat16)  # noqa: E731
+    a, w, x = rnd(1024, 512), rnd(768, 512), rnd(1024, 768)
+    hidden, head, emb = rnd(32, 512), rnd(1000, 512), rnd(1000, 512)
+    want = bd.gemm_bf16(a, w)
+    stats = bd.head_confidence(hidden, head, emb)
+    side = torch.cuda.Stream()
+
+    def chain():
+        y = x
+        for _ in range(100):
+            y = y * 0.99 + x
+        return y
+
+    ref = chain()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        mine = chain()
+        got = bd.gemm_bf16(a, w, stream=side)
+        both = [bd.head_confidence(hidden, head, emb), bd.head_confidence(hidden, head, emb, stream=side)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(mine, ref)
+        for s in both:
+            assert all(torch.equal(p, q) for p, q in zip(s, stats))

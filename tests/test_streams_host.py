@@ -50,7 +50,10 @@ class World:
         mp.setattr(B, "_ptr_on", lambda t, *a: t.data_ptr())
         mp.setattr(B, "_rows_ptr", lambda t, *a: (t.data_ptr(), t.stride(0)))
         mp.setattr(B, "_launch", lambda what, index, stream, *a: self.launched.append((what, stream)))
-        mp.setattr(B, "LIB", types.SimpleNamespace(dllm_paged_attn_workspace=lambda *a: 4096))
+        mp.setattr(B, "_stream", lambda s: self.launched.append(s))
+        # workspaces of 4096 bytes, every call succeeds
+        mp.setattr(B, "LIB", types.SimpleNamespace(**{
+            name: lambda *a, n=4096 if name.endswith("_workspace") else 0: n for name in B.SIGNATURES}))
 
     def check(self, returned, stream, scratch):
         """Everything allocated belongs to `stream`; what is returned, and nothing else, is kept for the caller's."""
@@ -84,3 +87,26 @@ def test_paged_calls_allocate_on_their_stream(world, side):
     w.blocks.clear(), w.recorded.clear()
     w.check(bd.kv_read(world.pages, world.i32(0, 3), world.i32(0), table, 3, stream=stream), stream, 0)
     assert w.launched == [("dllm_paged_attn", stream), ("dllm_kv_read", stream)]
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_other_calls_allocate_on_their_stream(world, side):
+    w, z, i32 = world.w, world.zeros, world.i32
+    stream = w.side if side else None
+    params = dict(tau=0.9, lam=0.5, kappa=0.1, hierarchical=1, hier_levels=2, smoothing=1, alpha=0.5, mask_id=0)
+    f32 = lambda *s: z(*s, t=torch.float32)  # noqa: E731
+    byte = lambda *s: z(*s, t=torch.uint8)  # noqa: E731
+    desc, keep = B.ModelDesc(), [z(4, 64)]
+    calls = [
+        (lambda: [bd.block_attn(z(3, 2, 64), z(5, 2, 64), z(5, 2, 64), i32(0, 3), i32(0, 5), 3, 5, stream=stream)], 1),
+        (lambda: bd.head_confidence(z(3, 64), z(32, 64), z(32, 64), stream=stream), 1),
+        (lambda: bd.commit(i32(0, 1), f32(2), None, i32(0, 0), i32(0, 1), byte(1, 2), i32(0, 0), f32(2), i32(0, 0),
+                           z(32, 64), params, stream=stream), 0),
+        (lambda: [bd.gemm_bf16(z(3, 64), z(8, 64), stream=stream)], 0),
+        (lambda: [bd.model_forward(desc, z(4, 64), 0, keep, keep, stream=stream)], 1),
+        (lambda: bd.moe_ffn(z(3, 64), z(4, 64), z(4, 32, 64), z(4, 64, 16), 2, stream=stream), 1),
+    ]
+    for call, scratch in calls:
+        w.blocks.clear(), w.recorded.clear()
+        w.check(call(), stream, scratch)
+    assert w.launched == [stream] * len(calls)
