@@ -437,9 +437,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const auto maxop = [](float p, float q) { return fmaxf(p, q); };
     const auto addop = [](float p, float q) { return p + q; };
     uint32_t n = 0, o_seg = 0;
-    auto stage = [&](uint32_t seg) {           // piece seg's query rows
+    // Piece seg's query rows. When its wait gave up the piece is not read:
+    // what lies there may be anything. (Then the abort flag is up for good,
+    // and both groups leave before the rows would be used.)
+    auto stage = [&](uint32_t seg) {
       const uint32_t pi = seg % kAhead;
-      mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
+      if (!warp_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag)) return;
       if (!pieces[pi].more) return;
       stage_queries<DH, FP8, N>(a, pieces[pi], smem + C::kOffQ, info[seg & 1], threadIdx.x - 128);
       fence_proxy_async_smem();
@@ -450,7 +453,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     for (uint32_t seg = 0;; ++seg) {
       const uint32_t pi = seg % kAhead;
       // all of both groups go on or none does; the rows' info is written, the last piece's maxima are read
-      if (bar_any(4, 128 * kG, !mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag))) break;
+      if (bar_any(4, 128 * kG, *abort_flag || !mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag))) break;
       const Piece &pc = pieces[pi];
       if (!pc.more) break;
       const RowInfo<N> &ri = info[seg & 1];

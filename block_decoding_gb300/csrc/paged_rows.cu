@@ -416,10 +416,13 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lane_base + s * 128, t_o = tmem + lane_base + kColO + s * 128;
     uint32_t n0 = 0, ns = 0, o_seg = 0;
-    // this group's part of piece `seg`'s query rows: begun, and there
+    // This group's part of piece `seg`'s query rows: begun, and there. When
+    // its wait gave up the piece is not read: what lies there may be anything.
+    // (Then the abort flag is up for good, and both groups leave before the
+    // next piece.)
     auto stage = [&](uint32_t seg) {
       const uint32_t pi = seg % kAhead;
-      mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
+      if (!warp_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag)) return;
       const RowsPiece &pc = pieces[pi];
       if (!pc.more) return;
       float *qs = qs_s + (seg & 1) * 256;
@@ -437,7 +440,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     for (uint32_t seg = 0;; ++seg) {
       const uint32_t pi = seg % kAhead;
       // all of both groups go on or none does
-      if (bar_any(3, 256, !mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag))) break;
+      if (bar_any(3, 256, *abort_flag || !mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag))) break;
       const RowsPiece &pc = pieces[pi];
       if (!pc.more) break;
       if (seg == 0) {

@@ -2,6 +2,7 @@
 anything is launched (CPU only)."""
 
 import ctypes
+import os
 
 import pytest
 import torch
@@ -107,3 +108,17 @@ def test_binding_refuses_what_is_not_a_cache():
     f = k.to(torch.float8_e4m3fn)
     with pytest.raises(ValueError):
         bd.KVPages(f, f)                                    # 8-bit pages without scales
+
+
+def test_no_piece_is_read_after_a_wait_that_gave_up():
+    """A piece's slot holds anything until the piece is published, and its
+    numbers become addresses: every wait for one decides what happens next."""
+    here = os.path.join(os.path.dirname(bd.__file__), "csrc")
+    for name in ("paged_attn.cu", "paged_rows.cu"):
+        with open(os.path.join(here, name)) as f:
+            lines = [x.strip() for x in f if "_wait(&piece_full[" in x]
+        assert len(lines) >= 4
+        for x in lines:
+            assert x.startswith(("ok = ", "if (")), f"{name}: result dropped: {x}"
+        # what a stage found is voted on before its rows are used
+        assert any(x.startswith("if (bar_any(") and "||" in x for x in lines), name
