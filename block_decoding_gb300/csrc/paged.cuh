@@ -33,7 +33,7 @@ struct JoinJob {
 };
 
 // Request i clipped to the buffers and host bounds: query rows [q0, q0 + W),
-// L keys, position of the first row.
+// L keys. The position of the first row is that of the request as it is given.
 struct Extent {
   int q0, W, L, pos;
 };
@@ -44,13 +44,14 @@ __device__ __forceinline__ Extent paged_extent(const PagedArgs &a, int i, bool r
   x.q0 = a.q_off[i];
   x.W = a.q_off[i + 1] - x.q0;
   x.L = a.kv_len[i];
+  const long long last = static_cast<long long>(x.L) - x.W;   // (of W < 0 no row is left)
   if (x.q0 < 0 || x.W < 0 || x.q0 > a.q_rows) { bad = true; x.q0 = 0; x.W = 0; }
   if (x.W > a.q_rows - x.q0) { bad = true; x.W = a.q_rows - x.q0; }
   if (x.W > a.max_q) { bad = true; x.W = a.max_q; }
   if (x.L < 0) { bad = true; x.L = 0; }
   if (x.L > a.max_kv) { bad = true; x.L = a.max_kv; }
   // positions beyond +-2^30 see what the nearest one there sees
-  x.pos = a.q_pos ? min(max(a.q_pos[i], -(1 << 30)), 1 << 30) : x.L - x.W;
+  x.pos = static_cast<int>(min(max(a.q_pos ? static_cast<long long>(a.q_pos[i]) : last, -(1ll << 30)), 1ll << 30));
   if (bad && report) atomicOr(a.status, DLLM_DEV_OFFSETS);
   return x;
 }

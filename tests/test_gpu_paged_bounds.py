@@ -1,0 +1,57 @@
+"""GPU: attention over the paged cache where the batch passes the host bounds,
+and at the ends of the ranges of its arguments, against the float64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+import block_decoding_gb300 as bd
+from test_gpu_paged import DEV_OFFSETS, Batch, i32
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+
+@pytest.fixture(autouse=True)
+def _status_clear():
+    bd.device_status()
+    yield
+    torch.cuda.synchronize()
+    assert bd.device_status() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("w", [9, 40, 150])
+def test_rows_of_clipped_requests_keep_their_positions(w, fp8):
+    """Rows beyond max_q or q, and keys beyond max_kv, are left out; the others
+    are where q_off and kv_len say."""
+    b = Batch(50, [500, 300], 2, 64, 16, fp8)
+    b.queries([w, w], 2)
+    off = i32(b.q_off)
+    cut = w - 5
+    mark = torch.full_like(b.q, 3.0)
+    out, lse = bd.paged_attn(b.q, b.pages, off, i32(b.lens), b.table, cut, 500, right=0, out=mark, return_lse=True)
+    torch.cuda.synchronize()
+    assert bd.device_status() == DEV_OFFSETS
+    pos = [n - w for n in b.lens]
+    kept = [np.arange(cut) + i * w for i in range(2)]
+    assert (out[cut:w] == 3).all() and (out[w + cut:] == 3).all()
+    c = Batch.__new__(Batch)
+    c.__dict__.update(b.__dict__)
+    c.w, c.q_off, c.q = [cut, cut], np.array([0, cut, 2 * cut]), torch.cat([b.q[k] for k in kept])
+    c.check(torch.cat([out[k] for k in kept]), torch.cat([lse[k] for k in kept]), pos=pos, right=0)
+    # q ends before the last request's rows do
+    out, lse = bd.paged_attn(b.q[:2 * w - 5], b.pages, off, i32(b.lens), b.table, w, 500, left=60, right=0, return_lse=True)
+    torch.cuda.synchronize()
+    assert bd.device_status() == DEV_OFFSETS
+    c.w, c.q_off, c.q = [w, cut], np.array([0, w, w + cut]), b.q[:w + cut]
+    c.check(out, lse, pos=pos, left=60, right=0)
+    # keys beyond max_kv are not there for any row
+    out, lse = bd.paged_attn(b.q, b.pages, off, i32(b.lens), b.table, w, 400, left=110, right=0, return_lse=True)
+    torch.cuda.synchronize()
+    assert bd.device_status() == DEV_OFFSETS
+    c.w, c.q_off, c.q, c.lens = b.w, b.q_off, b.q, [400, 300]
+    c.k, c.v = [x[:400] for x in b.k], [x[:400] for x in b.v]
+    c.check(out, lse, pos=pos, left=110, right=0)
