@@ -50,17 +50,18 @@ __device__ __forceinline__ Extent paged_extent(const PagedArgs &a, int i, bool r
   if (x.W > a.max_q) { bad = true; x.W = a.max_q; }
   if (x.L < 0) { bad = true; x.L = 0; }
   if (x.L > a.max_kv) { bad = true; x.L = a.max_kv; }
-  // positions beyond +-2^30 see what the nearest one there sees
-  x.pos = static_cast<int>(min(max(a.q_pos ? static_cast<long long>(a.q_pos[i]) : last, -(1ll << 30)), 1ll << 30));
+  // (what kv_len and q_off give is within 32 bits but for lengths that are out of bounds by as much)
+  x.pos = a.q_pos ? a.q_pos[i] : static_cast<int>(min(max(last, -0x80000000ll), 0x7fffffffll));
   if (bad && report) atomicOr(a.status, DLLM_DEV_OFFSETS);
   return x;
 }
 
-// Keys [lo, hi) that a row at position p (|p| < 2^31) sees apart from the
-// sinks. Sums that pass 2^31 are clamped: right and left are below 2^30.
-__device__ __forceinline__ void visible(const PagedArgs &a, int p, int L, int &lo, int &hi) {
-  hi = a.right < 0 ? L : min(L, max(min(p, (1 << 30) - 1) + a.right + 1, 0));
-  lo = a.left < 0 ? 0 : max(max(p, -(1 << 30)) - a.left, 0);
+// Keys [lo, hi) that row t of a request whose first row is at position pos sees
+// apart from the sinks. (64 bits: positions are any 32-bit numbers.)
+__device__ __forceinline__ void visible(const PagedArgs &a, int pos, int t, int L, int &lo, int &hi) {
+  const long long p = static_cast<long long>(pos) + t;
+  hi = a.right < 0 ? L : static_cast<int>(min(static_cast<long long>(L), max(p + a.right + 1, 0ll)));
+  lo = a.left < 0 ? 0 : static_cast<int>(min(max(p - a.left, 0ll), 0x7fffffffll));
 }
 
 constexpr int kTile = 128;   // keys per tile
@@ -79,8 +80,8 @@ struct TileList {
 __device__ __forceinline__ TileList tile_list(const PagedArgs &a, const Extent &x, int rt, int n) {
   TileList t;
   const int t0 = rt * n / a.group, t1 = min(((rt + 1) * n - 1) / a.group, x.W - 1);   // W * group <= 2^30
-  visible(a, x.pos + t0, x.L, t.lo, t.hi_first);
-  visible(a, x.pos + t1, x.L, t.lo_last, t.hi);
+  visible(a, x.pos, t0, x.L, t.lo, t.hi_first);
+  visible(a, x.pos, t1, x.L, t.lo_last, t.hi);
   const int s = min(a.sinks, t.hi);
   t.first = t.lo / kTile;
   int n_win = 0;
@@ -98,7 +99,7 @@ __device__ __forceinline__ TileList tile_list(const PagedArgs &a, const Extent &
 // rows without keys are written too): no fewer than any of them needs.
 __device__ __forceinline__ int tiles_per_item(const PagedArgs &a, const Extent &x, int n) {
   int lo, hi;
-  visible(a, x.pos + x.W - 1, x.L, lo, hi);
+  visible(a, x.pos, x.W - 1, x.L, lo, hi);
   int most = (hi + kTile - 1) / kTile;
   if (a.left >= 0 && a.right >= 0) {
     // window keys of one row tile: left + right + 1 of a row, and the rows' spread

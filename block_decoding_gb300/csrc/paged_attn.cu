@@ -163,7 +163,7 @@ __device__ __forceinline__ void stage_queries(const PagedArgs &a, const Piece &p
   if (tid < N) {
     const int r = pc.r0 + tid, t = r / a.group;
     int lo = 0, hi = 0x7fffffff;   // a column that is no row masks nothing; its results go nowhere
-    if (r < rows) visible(a, pc.x.pos + t, pc.x.L, lo, hi);
+    if (r < rows) visible(a, pc.x.pos, t, pc.x.L, lo, hi);
     info.lo[tid] = lo;
     info.hi[tid] = hi;
     info.out[tid] = r < rows ? (pc.x.q0 + t) * a.Hq + pc.h * a.group + (r - t * a.group) : -1;

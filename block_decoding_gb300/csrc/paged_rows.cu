@@ -453,7 +453,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const bool two = TWO && pc.two;
       const int r = pc.r0 + (two ? s * 128 : 0) + tid, t = r / a.group;
       int lo = 0, hi = 0x7fffffff;   // a row that is none masks nothing; its results go nowhere
-      if (r < rows) visible(a, pc.x.pos + t, pc.x.L, lo, hi);
+      if (r < rows) visible(a, pc.x.pos, t, pc.x.L, lo, hi);
       const float qs = FP8 ? qs_s[(seg & 1) * 256 + (two ? s * 128 : 0) + tid] : 1.f;
       const int cnt = two ? nT : s == 0 ? (nT + 1) / 2 : nT / 2;
       // Streams with rows of their own, in this piece and the next: a stream's

@@ -55,3 +55,16 @@ def test_rows_of_clipped_requests_keep_their_positions(w, fp8):
     c.w, c.q_off, c.q, c.lens = b.w, b.q_off, b.q, [400, 300]
     c.k, c.v = [x[:400] for x in b.k], [x[:400] for x in b.v]
     c.check(out, lse, pos=pos, left=110, right=0)
+
+
+FAR = (1 << 30) - 1
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("w", [1, 40, 150])
+@pytest.mark.parametrize("left,right", [(FAR, 0), (FAR - 20, 5), (-1, FAR), (FAR, FAR), (3, FAR)])
+def test_far_positions_under_the_widest_masks(w, fp8, left, right):
+    b = Batch(51, [200, 200, 200, 64], 1, 64, 32, fp8)
+    b.queries([w] * 4, 2)
+    for pos in ([FAR + 51, FAR + 130, -FAR - 60, -FAR + 30], [FAR - 20, (1 << 31) - 1, -(1 << 31), -FAR - 1 - w]):
+        b.check(*b.run(pos=pos, left=left, right=right, sinks=7), pos=pos, left=left, right=right, sinks=7)
