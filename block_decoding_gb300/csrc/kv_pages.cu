@@ -229,7 +229,7 @@ dllm_status move(bool write, const dllm_kv_pages *pages, uint16_t *k, uint16_t *
   const dllm_status sp = check_page_pointers(pages);
   if (sp != DLLM_OK) return sp;
   const long long d = static_cast<long long>(pages->heads) * pages->dh;
-  if (!k || !v || !off || !pos0 || !page_table) return DLLM_ERR_INVALID_ARG;
+  if (!k || !v || !off || !pos0 || (!page_table && max_pages > 0)) return DLLM_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v) || k_stride < d || v_stride < d || k_stride % 8 || v_stride % 8)
     return DLLM_ERR_INVALID_ARG;
   MoveArgs g{};

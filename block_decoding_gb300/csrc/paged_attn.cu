@@ -966,7 +966,7 @@ extern "C" dllm_status dllm_paged_attn(const dllm_kv_pages *pages, const dllm_pa
   if (a->B == 0 || a->max_q == 0 || a->q_rows == 0) return DLLM_OK;
   const dllm_status sp = check_page_pointers(pages);
   if (sp != DLLM_OK) return sp;
-  if (!a->q || !a->out || !a->q_off || !a->kv_len || !a->page_table) return DLLM_ERR_INVALID_ARG;
+  if (!a->q || !a->out || !a->q_off || !a->kv_len || (!a->page_table && a->max_pages > 0)) return DLLM_ERR_INVALID_ARG;
   if (!aligned16(a->q) || !aligned16(a->out) || a->q_stride < static_cast<long long>(a->Hq) * pages->dh ||
       a->q_stride % 8)
     return DLLM_ERR_INVALID_ARG;

@@ -457,7 +457,8 @@ dllm_status dllm_moe_ffn(const dllm_bf16 *h, const dllm_bf16 *w_router,
  *   1 <= heads <= 256; num_pages * heads * page_size < 2^31; k, v,
  *   k_scale and v_scale 16-byte aligned.
  *   A page id outside [0, num_pages) and a position outside the table set
- *   DLLM_DEV_PAGE: such a row is not written, and reads as zeros.
+ *   DLLM_DEV_PAGE: such a row is not written, and reads as zeros. A table
+ *   without pages (max_pages = 0) may be NULL.
  * ------------------------------------------------------------------- */
 enum { DLLM_KV_BF16 = 0, DLLM_KV_E4M3 = 1 };
 typedef struct {

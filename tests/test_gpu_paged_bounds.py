@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import block_decoding_gb300 as bd
-from test_gpu_paged import DEV_OFFSETS, Batch, i32
+from test_gpu_paged import DEV_OFFSETS, DEV_PAGE, Batch, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,26 @@ def test_far_positions_under_the_widest_masks(w, fp8, left, right):
     b.queries([w] * 4, 2)
     for pos in ([FAR + 51, FAR + 130, -FAR - 60, -FAR + 30], [FAR - 20, (1 << 31) - 1, -(1 << 31), -FAR - 1 - w]):
         b.check(*b.run(pos=pos, left=left, right=right, sinks=7), pos=pos, left=left, right=right, sinks=7)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("w", [1, 40, 150])
+def test_requests_without_a_cache_at_all(w, fp8):
+    b = Batch(52, [20, 30], 2, 64, 16, fp8)
+    b.queries([w, w], 2)
+    none = torch.empty((2, 0), dtype=torch.int32, device=b.table.device)
+    for max_kv in (0, 5000):
+        out, lse = bd.paged_attn(b.q, b.pages, i32(b.q_off), i32([0, 0]), none, w, max_kv, right=0, return_lse=True)
+        assert not out.any() and torch.isneginf(lse).all()
+    rows = torch.ones((2, 2, 64), dtype=torch.bfloat16, device=b.table.device)
+    before = b.pages.k.view(torch.uint8).clone()
+    bd.kv_write(b.pages, rows, rows, i32([0, 0, 0]), i32([0, 0]), none)          # no row belongs to a request
+    k, v = bd.kv_read(b.pages, i32([0, 0, 0]), i32([0, 0]), none, 2, k=rows.clone(), v=rows.clone())
+    assert torch.equal(k, rows) and torch.equal(v, rows)
+    torch.cuda.synchronize()
+    assert bd.device_status() == 0
+    bd.kv_write(b.pages, rows, rows, i32([0, 1, 2]), i32([0, 0]), none)          # rows without a place
+    k, v = bd.kv_read(b.pages, i32([0, 1, 2]), i32([0, 0]), none, 2)
+    torch.cuda.synchronize()
+    assert bd.device_status() == DEV_PAGE
+    assert not k.any() and not v.any() and torch.equal(before, b.pages.k.view(torch.uint8))

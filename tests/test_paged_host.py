@@ -122,3 +122,10 @@ def test_no_piece_is_read_after_a_wait_that_gave_up():
             assert x.startswith(("ok = ", "if (")), f"{name}: result dropped: {x}"
         # what a stage found is voted on before its rows are used
         assert any(x.startswith("if (bar_any(") and "||" in x for x in lines), name
+
+
+def test_a_table_without_pages_is_no_null_argument():
+    # what an empty tensor's address is: requests without any cached row
+    assert _attn(page_table=None, max_pages=0) != 1
+    assert _write(table=None, n=0) != 1 and _read(table=None, n=0) != 1
+    assert _attn(page_table=None, max_pages=1) == 1 and _write(table=None, n=1) == 1 and _read(table=None, n=1) == 1
