@@ -224,7 +224,8 @@ dllm_status move(bool write, const dllm_kv_pages *pages, uint16_t *k, uint16_t *
   const dllm_status st = check_pages(pages);
   if (st != DLLM_OK) return st;
   if (rows < 0 || B < 0 || max_pages < 0) return DLLM_ERR_INVALID_ARG;
-  if (B > 4096) return DLLM_ERR_UNSUPPORTED;
+  // (a block numbers its rows beyond the last one, by less than its threads)
+  if (B > 4096 || rows > 0x7fffffff - kThreads) return DLLM_ERR_UNSUPPORTED;
   if (rows == 0 || B == 0) return DLLM_OK;
   const dllm_status sp = check_page_pointers(pages);
   if (sp != DLLM_OK) return sp;

@@ -478,7 +478,7 @@ typedef struct {
  *         `rows` are skipped, DLLM_DEV_OFFSETS; rows in no request are
  *         not stored); pos0 int32 [B]; page_table int32 [B][max_pages]
  * Slots that no row is stored in keep their bytes. Two rows for one slot
- * leave it unspecified. B <= 4096. No workspace. */
+ * leave it unspecified. B <= 4096, rows < 2^31 - 128. No workspace. */
 dllm_status dllm_kv_write(const dllm_kv_pages *pages /* host */,
                           const dllm_bf16 *k, const dllm_bf16 *v,
                           long long k_stride, long long v_stride, int rows,

@@ -129,3 +129,11 @@ def test_a_table_without_pages_is_no_null_argument():
     assert _attn(page_table=None, max_pages=0) != 1
     assert _write(table=None, n=0) != 1 and _read(table=None, n=0) != 1
     assert _attn(page_table=None, max_pages=1) == 1 and _write(table=None, n=1) == 1 and _read(table=None, n=1) == 1
+
+
+@pytest.mark.parametrize("heads,dh", [(1, 64), (2, 128), (3, 64)])
+def test_moves_refuse_rows_whose_numbers_pass_32_bits(heads, dh):
+    # the last block's rows are numbered beyond `rows`, by less than a block of threads
+    p, stride = _pages(heads=heads, dh=dh), heads * dh
+    for rows in ((1 << 31) - 1, (1 << 31) - 127):
+        assert _write(p, ks=stride, vs=stride, rows=rows) == 2 and _read(p, rows=rows) == 2
