@@ -523,13 +523,14 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           for (int e = 0; e < 32; e += 4) {
             float2 y0 = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
             float2 y1 = make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-            if constexpr (FP8) {   // the keys' K scales
-              const float4 f = col[w * 8 + e / 4];
-              y0 = __fmul2_rn(y0, make_float2(f.x, f.y));
-              y1 = __fmul2_rn(y1, make_float2(f.z, f.w));
+            float2 c0 = cv, c1 = cv;
+            if constexpr (FP8) {   // the keys' K scales, times the row's before the score: exact, and no product
+              const float4 f = col[w * 8 + e / 4];   // on the way overflows unless the score does
+              c0 = __fmul2_rn(cv, make_float2(f.x, f.y));
+              c1 = __fmul2_rn(cv, make_float2(f.z, f.w));
             }
-            y0 = __ffma2_rn(y0, cv, rv);
-            y1 = __ffma2_rn(y1, cv, rv);
+            y0 = __ffma2_rn(y0, c0, rv);
+            y1 = __ffma2_rn(y1, c1, rv);
             x[e] = __float_as_uint(y0.x); x[e + 1] = __float_as_uint(y0.y);
             x[e + 2] = __float_as_uint(y1.x); x[e + 3] = __float_as_uint(y1.y);
           }

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import block_decoding_gb300 as bd
-from test_gpu_paged import DEV_OFFSETS, DEV_PAGE, Batch, i32
+from oracle import paged
+from test_gpu_paged import DEV_OFFSETS, DEV_PAGE, LARGE, Batch, f64, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +92,29 @@ def test_requests_without_a_cache_at_all(w, fp8):
     torch.cuda.synchronize()
     assert bd.device_status() == DEV_PAGE
     assert not k.any() and not v.any() and torch.equal(before, b.pages.k.view(torch.uint8))
+
+
+@pytest.mark.parametrize("w", [1, 30, 40, 150, 300])
+def test_small_queries_over_very_large_keys(w):
+    """e4m3: keys of 2^121 and queries of 2^-108. Scores are some 2^13, so that
+    products on the way to them pass fp32 unless the small factor comes first;
+    nearly every row has one key that takes all the weight."""
+    b = Batch(53, [700, 260], 2, 128, 32, True, spread=0.1, k_size=2.0 ** 121)
+    assert all(np.isfinite(k).all() for k in b.k)
+    b.queries([w, w], 2, q_size=2.0 ** -108)
+    for max_kv in (None, LARGE):
+        out, lse = b.run(right=0, max_kv=max_kv)
+        b.check(out, lse, right=0)
+        alone = 0
+        for i, n in enumerate(b.lens):
+            q, got = f64(b.q[i * w:(i + 1) * w]), f64(out[i * w:(i + 1) * w])
+            see = paged.visible(np.arange(n - w, n), n, -1, 0, 0)
+            for h in range(4):
+                s = np.where(see, q[:, h] @ b.k[i][:, h // 2].T / np.sqrt(128), -np.inf)
+                top = np.sort(s, axis=1)
+                clear = top[:, -1] - top[:, -2] > 60       # scores are off by less than 1
+                alone += clear.sum()
+                want = b.v[i][s.argmax(axis=1)[clear], h // 2]
+                # the weight's rounding and the output's, half a step of bf16 each
+                assert (np.abs(got[clear, h] - want) <= 2.01 * 2.0 ** -8 * np.abs(want)).all()
+        assert alone > 4 * w
