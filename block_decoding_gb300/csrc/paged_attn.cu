@@ -32,9 +32,12 @@
 // passed it.
 //
 // e4m3 pages: K and V codes go to the tensor cores as they are.
-//   Scores: the query rows are split into two e4m3 parts (high + low: exact
-//   for elements within 2^-10 of the row's largest, else 2^-19 of that off),
-//   and the key's scale is a factor of its thread's scores.
+//   Scores: the query rows are split into two e4m3 parts and the key's scale
+//   is a factor of its thread's scores. The rows are scaled so that their
+//   largest lies in (224, 448]. High + low is exact for elements from 1/4 on
+//   (eight significant bits, the last of them no less than the least e4m3 step
+//   2^-9), and 2^-10 off below: exact within 2^-9 of the row's largest, else up
+//   to 2^-10 / 224 = 2^-17.8 of that off.
 //   Weights: P times the V scale, relative to the largest V scale so far, is
 //   split into three e5m2 parts (9 bits together). e5m2 spans 2^32; weights
 //   below 2^-10 go, 2^12 times larger, to accumulator columns of their own,
