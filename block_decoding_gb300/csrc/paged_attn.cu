@@ -39,10 +39,10 @@
 //   2^-9), and 2^-10 off below: exact within 2^-9 of the row's largest, else up
 //   to 2^-10 / 224 = 2^-17.8 of that off.
 //   Weights: P times the V scale, relative to the largest V scale so far, is
-//   split into three e5m2 parts (9 bits together). e5m2 spans 2^32; weights
-//   below 2^-10 go, 2^12 times larger, to accumulator columns of their own,
-//   so that weights keep 9 bits down to 2^-30 of the largest and err by 2^-42
-//   of it below. (Codes converted to bf16 by four more warps, with P in bf16:
+//   split into three e5m2 parts (three bits each: half a step of the ninth, and
+//   half of fp16's before: 2^-8.8 off). e5m2 spans 2^32; weights below 2^-10
+//   go, 2^12 times larger, to accumulator columns of their own, so that this
+//   holds down to 2^-32 of the largest; weights err by 2^-41.8 of it below. (Codes converted to bf16 by four more warps, with P in bf16:
 //   the conversion took 1.9 k cycles a tile, the loads of a tile 1.4 k.)
 //
 // Bound by memory where the keys are long: 4 requests of 20 to 40 thousand

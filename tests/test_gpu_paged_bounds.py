@@ -118,3 +118,38 @@ def test_small_queries_over_very_large_keys(w):
                 # the weight's rounding and the output's, half a step of bf16 each
                 assert (np.abs(got[clear, h] - want) <= 2.01 * 2.0 ** -8 * np.abs(want)).all()
         assert alone > 4 * w
+
+
+@pytest.mark.parametrize("w", [1, 13, 30, 40, 200])
+def test_small_weights_beside_a_dominant_scale(w):
+    """e4m3: one key has by far the largest V scale and nothing in the columns
+    that are looked at; weight times V scale of the others, 2^-4 to 2^-35 of
+    it, a size to a column, keeps the bits that are promised."""
+    L, dh = 640, 64
+    b = Batch(54, [L], 1, dh, 32, True, spread=0.0, k_size=0.3)
+    b.queries([w], 1)
+    v = torch.zeros((L, 1, dh))
+    size = torch.exp2(-4.0 - torch.arange(L) % 32) * (1 + torch.from_numpy(b.rng.random(L)).float())
+    v[torch.arange(L), 0, 32 + torch.arange(L) % 32] = size
+    v[17] = 0
+    v[17, 0, 0] = 1.0
+    v = v.to(torch.bfloat16)
+    bd.kv_write(b.pages, b.k_in, v.to(b.table.device), b.off, i32([0]), b.table)
+    codes, scale = paged.quantise(f64(v))
+    b.v = [paged.restore(codes, scale)]
+    out, _ = b.run(out_fp32=True)
+    want, lse, absv, mag = paged.attention(f64(b.q), b.k[0], b.v[0], np.arange(w), dh ** -0.5)
+    s = f64(b.q)[:, 0] @ b.k[0][:, 0].T * dh ** -0.5
+    p = np.exp(s - lse)                                                     # [w][L]
+    value = np.abs(paged.restore(codes, np.full(scale.shape, 127)))[:, 0]   # the codes' own values
+    vs = 2.0 ** (scale[:, 0].astype(float) - 127)
+    if w <= 32:
+        # (l, the sum of exp(score - reference), is at least this: the reference is no score's superior)
+        floor = 2.0 ** -41.8 * vs.max() * np.exp(s.max(axis=1, keepdims=True) - lse)
+        tol = np.maximum(2.0 ** -8.8 * p * vs, floor) @ value
+    else:
+        tol = 2.0 ** -8 * (p * vs) @ value
+    d = (dh + 8) * 2.0 ** -23 * mag[..., None]
+    tol = tol + absv[:, 0] * (2 * d[:, 0] + 2.0 ** -20 + (L + 8) * 2.0 ** -23) + 1e-38
+    err = np.abs(f64(out) - want)[:, 0]
+    assert (err <= tol).all(), f"{(err / tol)[:, 32:].max(axis=0)} of the tolerance"

@@ -5,6 +5,7 @@ import os
 import re
 
 import numpy as np
+import torch
 
 from oracle.paged import E4M3, nearest_code
 
@@ -40,3 +41,37 @@ def test_query_parts_are_as_exact_as_stated():
         worst = max(worst, e.max())
     assert worst <= 2.0 ** -off_by
     assert worst > 2.0 ** -(off_by + 0.25)                            # and the statement is no looser than it has to be
+
+
+def _weights_statement():
+    """(a, b): weight times V scale is off by up to 2^-a of itself, or 2^-b of the largest V scale where that is more."""
+    with open(os.path.join(HERE, "..", "include", "dllm.h")) as f:
+        text = " ".join(f.read().replace("\n *", " ").split())
+    m = re.search(r"weight times V scale is off by up to 2\^-([\d.]+) of itself, or 2\^-([\d.]+) of the largest V scale", text)
+    return float(m.group(1)), float(m.group(2))
+
+
+def _three_parts(w):
+    """w (fp32, 0 <= w <= 4) as the sum of three e5m2 parts of w 2^13, or of w 2^25 below 2^-10."""
+    w = w.astype(np.float32)
+    small = w < np.float32(2.0 ** -10)
+    h = (w * np.where(small, np.float32(2.0 ** 25), np.float32(2.0 ** 13))).astype(np.float16)
+    total, rest = np.zeros(w.shape), h
+    for _ in range(2):                                               # e5m2 is the upper byte of fp16
+        part = (rest.view(np.uint16) & 0xFF00).view(np.float16)
+        total, rest = total + part, rest - part
+    total = total + torch.from_numpy(rest).to(torch.float8_e5m2).double().numpy()
+    return total * np.where(small, 2.0 ** -25, 2.0 ** -13)
+
+
+def test_weight_parts_are_as_exact_as_stated():
+    of_itself, of_largest = _weights_statement()
+    rng = np.random.default_rng(0)
+    worst = []
+    for e in range(-60, 2):
+        w = np.float32(2.0 ** e) * np.concatenate([1 + rng.random(20000), 1 + np.arange(4096) / 4096, [2 - 2.0 ** -23]]).astype(np.float32)
+        err = np.abs(_three_parts(w) - w)
+        assert (err <= np.maximum(2.0 ** -of_itself * w, 2.0 ** -of_largest)).all(), e
+        worst.append((np.log2((err / w).max()), np.log2(err.max())))
+    rel, absolute = np.array(worst).T
+    assert rel[-30:].max() > -of_itself - 0.25 and absolute[:20].max() > -of_largest - 0.25     # no looser than it has to be
