@@ -42,8 +42,10 @@
 //   split into three e5m2 parts (three bits each: half a step of the ninth, and
 //   half of fp16's before: 2^-8.8 off). e5m2 spans 2^32; weights below 2^-10
 //   go, 2^12 times larger, to accumulator columns of their own, so that this
-//   holds down to 2^-32 of the largest; weights err by 2^-41.8 of it below. (Codes converted to bf16 by four more warps, with P in bf16:
-//   the conversion took 1.9 k cycles a tile, the loads of a tile 1.4 k.)
+//   holds down to 2^-32 of the largest; below, half of e5m2's least step and of
+//   fp16's step there remain, (2^-17 + 2^-19) / 2^25 = 2^-41.6 of it. (Codes
+//   converted to bf16 by four more warps, with P in bf16: the conversion took
+//   1.9 k cycles a tile, the loads of a tile 1.4 k.)
 //
 // Bound by memory where the keys are long: 4 requests of 20 to 40 thousand
 // keys (bf16, 8 x 4 heads, dh 128) take 95 us, 5.7 TB/s and 85 % of a copy's

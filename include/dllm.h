@@ -530,7 +530,7 @@ dllm_status dllm_kv_read(const dllm_kv_pages *pages /* host */, dllm_bf16 *k,
  *   Scores, maxima, sums and outputs are accumulated in fp32. The weights
  *   that multiply V are rounded to bf16; for e4m3 pages and up to 32 query
  *   rows per request and cached head, weight times V scale is off by up to
- *   2^-8.8 of itself, or 2^-41.8 of the largest V scale among the keys that the
+ *   2^-8.8 of itself, or 2^-41.6 of the largest V scale among the keys that the
  *   request's rows see, where that is more. With e4m3 pages, elements of q below 2^-9 of
  *   the largest of their row are off by up to 2^-17.8 of that (2^-127, where
  *   that is more: rows all below 2^-108); the others are exact. Sums are divided

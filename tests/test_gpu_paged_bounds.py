@@ -145,7 +145,7 @@ def test_small_weights_beside_a_dominant_scale(w):
     vs = 2.0 ** (scale[:, 0].astype(float) - 127)
     if w <= 32:
         # (l, the sum of exp(score - reference), is at least this: the reference is no score's superior)
-        floor = 2.0 ** -41.8 * vs.max() * np.exp(s.max(axis=1, keepdims=True) - lse)
+        floor = 2.0 ** -41.6 * vs.max() * np.exp(s.max(axis=1, keepdims=True) - lse)
         tol = np.maximum(2.0 ** -8.8 * p * vs, floor) @ value
     else:
         tol = 2.0 ** -8 * (p * vs) @ value

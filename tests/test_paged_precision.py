@@ -71,7 +71,9 @@ def test_weight_parts_are_as_exact_as_stated():
     for e in range(-60, 2):
         w = np.float32(2.0 ** e) * np.concatenate([1 + rng.random(20000), 1 + np.arange(4096) / 4096, [2 - 2.0 ** -23]]).astype(np.float32)
         err = np.abs(_three_parts(w) - w)
+        # relative: half a step of nine bits and of fp16's eleven, 2^-9 + 2^-12 < 2^-8.8; else half of e5m2's least
+        # step 2^-16, and of fp16's step where w is near 2^-33: (2^-17 + 2^-19) / 2^25 = 1.25 * 2^-42 < 2^-41.6
         assert (err <= np.maximum(2.0 ** -of_itself * w, 2.0 ** -of_largest)).all(), e
         worst.append((np.log2((err / w).max()), np.log2(err.max())))
     rel, absolute = np.array(worst).T
-    assert rel[-30:].max() > -of_itself - 0.25 and absolute[:20].max() > -of_largest - 0.25     # no looser than it has to be
+    assert rel[-30:].max() > -of_itself - 0.25 and absolute[:28].max() > -of_largest - 0.25     # no looser than it has to be
