@@ -71,8 +71,16 @@ class StepServer:
         return self.sched.submit(rid, prompt_len, resp_len)
 
     def step(self, stream=None):
-        """Plan, run and complete one step. Returns the planned entries
-        (list of dicts) or None when nothing is runnable."""
+        """Plan, run and complete one step, all of it on `stream` (default: the
+        current stream). Returns the planned entries (list of dicts) or None
+        when nothing is runnable."""
+        if stream is None:
+            return self._step()
+        stream.wait_stream(torch.cuda.current_stream(self.dev))   # the buffers may have been filled there
+        with torch.cuda.stream(stream):
+            return self._step()
+
+    def _step(self):
         raw, n = self.sched.plan_raw()
         if n == 0:
             self.sched.complete(self.remaining)
@@ -112,7 +120,7 @@ class StepServer:
         if self.ws is None or self.ws.numel() < need:
             self.ws = B.workspace(need, self.dev)
         self.last = dict(entries=ents, q_off=q_off, kv_off=kv_off, row_req=rr, row_pos=rp, R=R, args=a)
-        B.denoise_step(a, self.ws, stream)
+        B.denoise_step(a, self.ws)
         self.commit_host.copy_(self.n_commit, non_blocking=True)
         if self.eos_id >= 0:
             self.tok_host.copy_(self.tokens, non_blocking=True)

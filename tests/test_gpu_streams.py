@@ -146,3 +146,28 @@ def test_product_and_head_beside_work_whose_memory_was_given_back():
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(mine, ref)
         assert all(torch.equal(p, q) for p, q in zip(s, stats))
+
+
+def test_served_steps_on_a_busy_stream():
+    from test_gpu_serve import _server
+    side = torch.cuda.Stream()
+    x = torch.randn((4096, 4096), device=DEV)
+    results = []
+    for stream in (None, side):
+        _, srv = _server()
+        for rid, (prompt, resp) in enumerate([(20, 16), (60, 8), (5, 16)]):
+            assert srv.submit(rid, prompt, resp)
+        steps = []
+        for _ in range(200):
+            if stream is not None:
+                with torch.cuda.stream(stream):
+                    for _ in range(20):        # the step waits behind this
+                        x.mul_(1.0)
+            ents = srv.step(stream)
+            if ents is None:
+                break
+            steps.append([(e["req"], e["block"], e["kind"], e["n_commit"]) for e in ents])
+        torch.cuda.synchronize()
+        results.append((steps, srv.tokens.cpu(), srv.mask.cpu()))
+    (a, tok_a, mask_a), (b, tok_b, mask_b) = results
+    assert a == b and torch.equal(tok_a, tok_b) and torch.equal(mask_a, mask_b) and not mask_a.any()

@@ -110,3 +110,48 @@ def test_other_calls_allocate_on_their_stream(world, side):
         w.blocks.clear(), w.recorded.clear()
         w.check(call(), stream, scratch)
     assert w.launched == [stream] * len(calls)
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_a_served_step_stays_on_its_stream(monkeypatch, side):
+    """The plan's upload, the step and the read of its commit counts."""
+    from block_decoding_gb300 import serve
+
+    class Ordered(Stream):
+        def __init__(self, log):
+            self.log = log
+
+        def wait_stream(self, other):
+            self.log.append(("wait", self, other))
+
+        def synchronize(self):
+            self.log.append(("sync", self))
+
+    log = []
+    caller, given = Ordered(log), Ordered(log)
+    now = [caller]
+
+    @contextlib.contextmanager
+    def stream(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    copy = torch.Tensor.copy_
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: now[-1])
+    monkeypatch.setattr(torch.Tensor, "pin_memory", lambda t: t)
+    monkeypatch.setattr(torch.Tensor, "copy_", lambda t, *a, **kw: (log.append(("copy", now[-1])), copy(t, *a, **kw))[1])
+    monkeypatch.setattr(serve.B, "step_args", lambda **kw: None)
+    monkeypatch.setattr(serve.B, "denoise_step_workspace", lambda a: 256)
+    monkeypatch.setattr(serve.B, "denoise_step", lambda a, ws, s=None: log.append(("step", s or now[-1])))
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    bufs = dict(q=z(200, 1, 64), k=z(200, 1, 64), v=z(200, 1, 64), w_head=z(32, 64), emb=z(32, 64), hidden=z(16, 64))
+    srv = serve.StepServer(bufs, slots=2, blk=8, vic=0, params=dict(mask_id=0, smoothing=0), quantum=100, budget_cap=200,
+                           max_step_rows=100, max_seq=64, device="cpu")
+    assert srv.submit(0, 16, 8)
+    del log[:]
+    assert srv.step(given if side else None)
+    on = given if side else caller
+    assert [x for x in log if x[0] != "wait"] == [("copy", on), ("step", on), ("copy", on), ("sync", on)]
+    assert [x for x in log if x[0] == "wait"] == ([("wait", given, caller)] if side else [])
