@@ -122,6 +122,8 @@ __device__ __forceinline__ int tiles_per_item(const PagedArgs &a, const Extent &
 // longer items hardly differ. A join cost of 0 or 12 for 4 changes nothing
 // but those blocks, by 1 %.
 constexpr int kItemCost = 6, kJoinCost = 4;
+constexpr int kMinTiles = 4;     // fewest tiles a CTA is given: each piece costs a prologue and a join (1 or 8: the same time
+                                 // for single tokens over 257 keys and 20000 to 40000)
 
 // Where this CTA's stretch starts.
 struct Start {
@@ -147,7 +149,7 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
 // Every thread of the CTA takes part. (A single token over 257 keys takes 8.8 us
 // this way, 9.1 with the warps' sums added up one after the other and 64-bit
 // divisions.)
-__device__ __forceinline__ void find_start(const PagedArgs &a, int n_rows, int min_tiles, Scan *s_scan, Start *s_start) {
+__device__ __forceinline__ void find_start(const PagedArgs &a, int n_rows, Scan *s_scan, Start *s_start) {
   const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunk = (a.B + nt - 1) / nt;
   const int i0 = tid * chunk, i1 = min(a.B, i0 + chunk);
@@ -193,7 +195,7 @@ __device__ __forceinline__ void find_start(const PagedArgs &a, int n_rows, int m
     earlier += __shfl_xor_sync(0xffffffffu, earlier, o);
   }
   length_up += earlier;
-  const long long even = max(quotient(total + gridDim.x - 1, gridDim.x), static_cast<long long>(min_tiles));
+  const long long even = max(quotient(total + gridDim.x - 1, gridDim.x), static_cast<long long>(kMinTiles));
   const int each = (total_items + gridDim.x - 1) / gridDim.x;      // whole items of a CTA
   const bool whole = a.whole || static_cast<long long>(each) * (most + kItemCost) <= even + kItemCost + kJoinCost;
   const long long before = whole ? items_up - items : length_up - length, mine = whole ? items : length;
@@ -402,8 +404,6 @@ __device__ __forceinline__ void convert_v(const uint8_t *raw, uint8_t *dst, int 
   }
 }
 
-constexpr int kMinTiles = 4;     // fewest tiles a CTA is given: each piece costs a prologue and a join (1 or 8: the same time
-                                 // for single tokens over 257 keys and 20000 to 40000)
 constexpr int kWholeTiles = 4;   // items of no more tiles are not divided
 constexpr int kMaxCtas = 192;    // bound of the workspace, above any GB300's SM count
 constexpr int kConvKeys = 64;    // keys of one converted V piece
@@ -414,6 +414,6 @@ constexpr float kLn2 = 0.69314718055994531f;
 // Launches the kernel for many rows per cached head (paged_rows.cu) with row
 // tiles of n_rows = 128 or 256 on `ctas` CTAs.
 dllm_status launch_paged_rows(int dh, bool fp8, int n_rows, const CUtensorMap &tk, const CUtensorMap &tv,
-                              const PagedArgs &a, int min_tiles, int ctas, cudaStream_t s);
+                              const PagedArgs &a, int ctas, cudaStream_t s);
 
 }  // namespace dllm

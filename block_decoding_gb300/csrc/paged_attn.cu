@@ -233,8 +233,7 @@ __device__ __forceinline__ void split_e5m2(const float (&w)[4], uint32_t (&out)[
 
 template <int DH, bool FP8, int N>
 __global__ void __launch_bounds__(Cfg<DH, FP8, N>::kThreads, 1)
-paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a,
-                  const int min_tiles) {
+paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a) {
   using C = Cfg<DH, FP8, N>;
   constexpr int kSt = C::kStages, kO = C::kO, kG = C::kGroups, kSBuf = C::kSBuf, kPBuf = C::kPBuf;
   // FP8: the V scale enters the weights, so they must not pass 2^2
@@ -302,7 +301,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   const uint32_t t_o = tmem + kSBuf * N;    // O of group g at kO g
 
   pdl_wait();   // the batch's metadata, the pages and the queries may come from the previous kernel
-  find_start(a, N, min_tiles, s_scan, start);
+  find_start(a, N, s_scan, start);
 
   if (warp < 4) {
     reg_dealloc<C::kRegsIssue>();
@@ -912,11 +911,11 @@ Ws ws_layout(const dllm_kv_pages *pages, const dllm_paged_attn_args *a) {
 }
 
 template <int DH, bool FP8, int N>
-dllm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &g, int min_tiles, int ctas, cudaStream_t s) {
+dllm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &g, int ctas, cudaStream_t s) {
   using C = Cfg<DH, FP8, N>;
   auto kern = paged_attn_kernel<DH, FP8, N>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
-  if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kBytes, s, tk, tv, g, min_tiles);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kBytes, s, tk, tv, g);
   return e == cudaSuccess ? DLLM_OK : cuda_error(e);
 }
 
@@ -932,16 +931,15 @@ dllm_status launch_attn(const dllm_kv_pages *pages, const dllm_paged_attn_args *
   const long long row_tiles = (static_cast<long long>(a->max_q) * g.group + n - 1) / n;
   const long long per_item = g.max_kv > 0 ? (g.max_kv + kTile - 1) / kTile : 1;
   const bool split = may_split(a);
-  const int min_tiles = kMinTiles;
   g.whole = !split;
   const double most = static_cast<double>(a->B) * pages->heads * row_tiles * per_item;
   int ctas = sm_budget() < kMaxCtas ? sm_budget() : kMaxCtas;
-  // (a whole item per CTA, or at least min_tiles tiles)
-  const double useful = split ? most / min_tiles : most / per_item;
+  // (a whole item per CTA, or at least kMinTiles tiles)
+  const double useful = split ? most / kMinTiles : most / per_item;
   if (useful < ctas) ctas = static_cast<int>(useful) + 1;
-  const dllm_status st = n == 16   ? launch<DH, FP8, 16>(tk, tv, g, min_tiles, ctas, s)
-                         : n == 32 ? launch<DH, FP8, 32>(tk, tv, g, min_tiles, ctas, s)
-                                   : launch_paged_rows(DH, FP8, n, tk, tv, g, min_tiles, ctas, s);
+  const dllm_status st = n == 16   ? launch<DH, FP8, 16>(tk, tv, g, ctas, s)
+                         : n == 32 ? launch<DH, FP8, 32>(tk, tv, g, ctas, s)
+                                   : launch_paged_rows(DH, FP8, n, tk, tv, g, ctas, s);
   if (st != DLLM_OK) return st;
   unsigned launches = 1;
   if (split) {

@@ -166,8 +166,7 @@ __device__ __forceinline__ void stage_rows(const PagedArgs &a, const RowsPiece &
 
 template <int DH, bool FP8, bool TWO>
 __global__ void __launch_bounds__(RowsCfg<DH, FP8, TWO>::kThreads, 1)
-paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a,
-                  const int min_tiles) {
+paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a) {
   using C = RowsCfg<DH, FP8, TWO>;
   constexpr int kSt = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -239,7 +238,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   const uint32_t tmem = *tmem_slot;
 
   pdl_wait();   // the batch's metadata, the pages and the queries may come from the previous kernel
-  find_start(a, C::kRows, min_tiles, s_scan, start);
+  find_start(a, C::kRows, s_scan, start);
 
   if (warp < 4) {
     reg_dealloc<C::kRegsIssue>();
@@ -712,25 +711,25 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 }
 
 template <int DH, bool FP8, bool TWO>
-dllm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int min_tiles, int ctas, cudaStream_t s) {
+dllm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int ctas, cudaStream_t s) {
   using C = RowsCfg<DH, FP8, TWO>;
   auto kern = paged_rows_kernel<DH, FP8, TWO>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
-  if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kBytes, s, tk, tv, a, min_tiles);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kBytes, s, tk, tv, a);
   return e == cudaSuccess ? DLLM_OK : cuda_error(e);
 }
 
 }  // namespace
 
 dllm_status launch_paged_rows(int dh, bool fp8, int n_rows, const CUtensorMap &tk, const CUtensorMap &tv,
-                              const PagedArgs &a, int min_tiles, int ctas, cudaStream_t s) {
+                              const PagedArgs &a, int ctas, cudaStream_t s) {
   const bool two = n_rows == 256;
   if (dh == 64) {
-    if (fp8) return two ? launch<64, true, true>(tk, tv, a, min_tiles, ctas, s) : launch<64, true, false>(tk, tv, a, min_tiles, ctas, s);
-    return two ? launch<64, false, true>(tk, tv, a, min_tiles, ctas, s) : launch<64, false, false>(tk, tv, a, min_tiles, ctas, s);
+    if (fp8) return two ? launch<64, true, true>(tk, tv, a, ctas, s) : launch<64, true, false>(tk, tv, a, ctas, s);
+    return two ? launch<64, false, true>(tk, tv, a, ctas, s) : launch<64, false, false>(tk, tv, a, ctas, s);
   }
-  if (fp8) return two ? launch<128, true, true>(tk, tv, a, min_tiles, ctas, s) : launch<128, true, false>(tk, tv, a, min_tiles, ctas, s);
-  return two ? launch<128, false, true>(tk, tv, a, min_tiles, ctas, s) : launch<128, false, false>(tk, tv, a, min_tiles, ctas, s);
+  if (fp8) return two ? launch<128, true, true>(tk, tv, a, ctas, s) : launch<128, true, false>(tk, tv, a, ctas, s);
+  return two ? launch<128, false, true>(tk, tv, a, ctas, s) : launch<128, false, false>(tk, tv, a, ctas, s);
 }
 
 }  // namespace dllm

@@ -12,7 +12,7 @@ uint32_t status_paged(bool clear);
 struct KvPages {
   uint8_t *k, *v;                  // [num_pages][heads][page_size][dh], bf16 or e4m3
   uint8_t *k_scale, *v_scale;      // [num_pages][heads][page_size], or null (bf16)
-  int num_pages, heads, dh, page_shift;
+  int num_pages, heads, page_shift;
   const int32_t *table;            // [B][max_pages]
   int max_pages;
 };
@@ -55,7 +55,6 @@ inline KvPages device_pages(const dllm_kv_pages *p, const int32_t *table, int ma
   c.v_scale = p->type == DLLM_KV_E4M3 ? p->v_scale : nullptr;
   c.num_pages = p->num_pages;
   c.heads = p->heads;
-  c.dh = p->dh;
   c.page_shift = p->page_size == 16 ? 4 : p->page_size == 32 ? 5 : p->page_size == 64 ? 6 : 7;
   c.table = table;
   c.max_pages = max_pages;
