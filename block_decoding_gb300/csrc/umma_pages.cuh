@@ -56,6 +56,16 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                : "memory");
 }
 
+// 16 bytes of shared memory, loaded where this stands among other such
+// statements (the compiler does not bring it forward).
+__device__ __forceinline__ float4 load_shared4(const float4 *p) {
+  float4 f;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+               : "r"(smem_u32(p)));
+  return f;
+}
+
 // 4-D tiled load of the box at (0, 0, 0, w).
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int w) {
   asm volatile(
