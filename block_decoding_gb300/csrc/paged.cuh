@@ -119,8 +119,12 @@ __device__ __forceinline__ int tiles_per_item(const PagedArgs &a, const Extent &
 // Measured: 64 single tokens over 1 to 8192 keys (e4m3, 8 x 4 heads, dh 128)
 // take 161 us with a cost of 0, 132 with 3, 124 with 6, 131 with 12; 16 blocks
 // of 64 to 96 rows over 352 to 1120 keys (32 heads, bf16) 60, 54, 54, 55;
-// longer items hardly differ. A join cost of 0 or 12 for 4 changes nothing
-// but those blocks, by 1 %.
+// longer items hardly differ. A join cost of 0 or 12 for 4 changes those blocks
+// by 1 %; the other calls divide their items, or leave them whole, with each.
+// Items that are left whole, against all of them divided: 32 tokens that see
+// 4096 keys (128 items of 35 tiles) 41.8 and 42.5 us (e4m3), 50.7 and 53.0
+// (bf16), that see 1024 (11 tiles) 23.5 and 24.8, 23.1 and 25.4; 2000 rows under
+// windows of 256 to 4096 (128 items) 5 to 22 % longer divided.
 constexpr int kItemCost = 6, kJoinCost = 4;
 constexpr int kMinTiles = 4;     // fewest tiles a CTA is given: each piece costs a prologue and a join (1 or 8: the same time
                                  // for single tokens over 257 keys and 20000 to 40000)

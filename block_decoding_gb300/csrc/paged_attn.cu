@@ -880,6 +880,13 @@ dllm_status check_shape(const dllm_kv_pages *pages, const dllm_paged_attn_args *
 //   2048 rows, 1000 keys, 4 x 8 (2048):                128: 53 (81), 256: 48 (64)
 //   512 rows, 4000 keys, 8 x 8 (4096):                 128: 82 (109), 256: 66 (91)
 //   512 rows, 4000 keys, 24 x 8 (12288):               128: 255 (279), 256: 176 (240)
+// (the fourth line's call stays with 128 in bf16, 10 % longer). max_kv tiles are
+// counted under a window too, which sees fewer: 2000 rows and 16 x 1 heads over
+// 16000 keys have 128 items of 256 rows then, one per CTA, and 256 of 128 rows.
+//   dh 64, window 256:                                 128: 26 (34), 256: 23 (28)
+//   dh 64, window 1024:                                128: 35 (46), 256: 33 (40)
+//   dh 64, window 4096:                                128: 68 (103), 256: 70 (86)
+//   dh 128, window 1024:                               128: 44 (60), 256: 40 (47)
 // (never more with a larger B, max_q or max_kv: the workspace grows with it)
 constexpr double kFewTiles = 3000, kFewTilesE4m3 = 1500;
 

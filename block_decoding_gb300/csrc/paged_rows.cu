@@ -35,8 +35,8 @@
 // matrix product's rate. Bound by the tensor cores: a tile of 256 x 128 costs
 // 3.1 k cycles where its MMAs alone take 2.75 k; some 10 us pass until the first
 // scores. Four prompts' pieces of 300 to 512 tokens over 1500 to 8000 keys
-// (e4m3) take 239 us, 0.83 PFLOP/s: the softmax warps and the converters share
-// the issue slots (of 253 us at the time, 27 went without the K scales' products
+// (e4m3) take 230 us, 0.86 PFLOP/s: the softmax warps and the converters share
+// the issue slots (of 253 us at an earlier stage, 27 went without the K scales' products
 // and their loads, 18 without the conversion; a second group of converters
 // leaves the softmax too few registers: 28 longer). 16 denoising blocks of 64 to 96 rows over 352 to
 // 1120 keys (32 heads, bf16): 54 us, 57 % of the bytes' time; an item has five

@@ -83,9 +83,7 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {
 }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// True in one lane of the (converged) warp, the same one every time. The
-// compiler keeps the descriptors of MMAs under it in uniform registers; under
-// `if (lane == 0)` every operand of every MMA is moved there first.
+// True in one lane of the (converged) warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
