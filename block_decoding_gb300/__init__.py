@@ -35,5 +35,12 @@ from ._binding import (  # noqa: F401
     kv_write,
     paged_attn,
     paged_attn_workspace,
+    Rope,
+    rope_kv_write,
+    tree_mask,
+    tree_attn,
+    attn_mass,
+    kv_move,
+    kv_evict,
 )
 from .decoder import BlockDecoder  # noqa: F401

@@ -672,6 +672,13 @@ def paged_attn(q, pages: KVPages, q_off, kv_len, page_table, max_q, max_kv, q_po
     Returns out [rows][Hq][dh], or (out, lse [rows][Hq]) with return_lse; with
     `stream`, order other streams' use of them after it.
     """
+    return _attend("dllm_paged_attn", (), q, pages, q_off, kv_len, page_table, max_q, max_kv, q_pos, scale, left, right, sinks,
+                   out, out_fp32, return_lse, lse, ws, stream)
+
+
+def _attend(what, more, q, pages, q_off, kv_len, page_table, max_q, max_kv, q_pos, scale, left, right, sinks, out, out_fp32,
+            return_lse, lse, ws, stream):
+    """Entry point `what` with the arguments of paged_attn and `more` behind the struct."""
     # (ctypes would cut longer numbers off)
     if not (0 <= max_q < _I31 and 0 <= max_kv < _I31 and 0 <= sinks < _I31 and -_I31 <= left < _I31 and -_I31 <= right < _I31):
         raise ValueError("max_q, max_kv, left, right and sinks must fit 32 bits, and only left and right may be negative")
@@ -710,5 +717,267 @@ def paged_attn(q, pages: KVPages, q_off, kv_len, page_table, max_q, max_kv, q_po
         if need:
             ws = _scratch(need, pages.device, stream)
             wp = ws.data_ptr()
-    _launch("dllm_paged_attn", dev, stream, pages.desc, a, wp, need)
+    _launch(what, dev, stream, pages.desc, a, *more, wp, need)
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------------------
+# around the paged cache: rotary positions, draft trees, eviction
+# (dllm_rope_kv_write, dllm_tree_mask, dllm_tree_attn, dllm_attn_mass,
+# dllm_kv_move, dllm_kv_evict)
+# ---------------------------------------------------------------------------
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rot", c_int), ("axes", c_int), ("axis", ctypes.c_uint8 * 64), ("freq", ctypes.c_double * 64)]
+
+
+class RopeWriteArgs(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("pos", "q", "k", "v", "q_out")] + \
+               [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride")] + \
+               [(n, c_void_p) for n in ("off", "pos0", "page_table")] + \
+               [(n, c_int) for n in ("max_pages", "B", "Hq", "rows")]
+
+
+class AttnMassArgs(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("q_stride", ctypes.c_longlong)] + \
+               [(n, c_void_p) for n in ("lse", "mass", "q_off", "kv_len", "q_pos", "fresh", "page_table")] + \
+               [(n, c_int) for n in ("max_pages", "B", "Hq", "max_q", "max_kv", "q_rows")] + \
+               [("scale", c_float), ("right", c_int), ("decay", c_float)]
+
+
+class KvMoveArgs(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("src", "count", "first", "page_table", "dst_table")] + \
+               [(n, c_int) for n in ("src_heads", "max_n", "max_pages", "dst_pages", "B")] + [("mass", c_void_p)]
+
+
+class KvEvictArgs(ctypes.Structure):
+    _fields_ = [(n, c_void_p) for n in ("mass", "kv_len", "page_table", "dst_table")] + \
+               [(n, c_int) for n in ("max_pages", "dst_pages", "B", "budget", "max_kv", "sinks", "recent", "move_mass")] + \
+               [("new_len", c_void_p), ("keep", c_void_p)]
+
+
+_CACHE_CALLS = {
+    "dllm_rope_kv_write": (c_int, [_PAGES_P, ctypes.POINTER(RopeDesc), ctypes.POINTER(RopeWriteArgs), c_void_p]),
+    "dllm_tree_mask": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_int, c_void_p, c_void_p]),
+    "dllm_tree_attn": (c_int, [_PAGES_P, ctypes.POINTER(PagedAttnArgs), c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "dllm_attn_mass": (c_int, [_PAGES_P, ctypes.POINTER(AttnMassArgs), c_void_p]),
+    "dllm_kv_move": (c_int, [_PAGES_P, ctypes.POINTER(KvMoveArgs), c_void_p]),
+    "dllm_kv_evict": (c_int, [_PAGES_P, ctypes.POINTER(KvEvictArgs), c_void_p]),
+}
+SIGNATURES.update(_CACHE_CALLS)
+for _name, (_res, _args) in _CACHE_CALLS.items():
+    _fn = getattr(LIB, _name)
+    _fn.restype, _fn.argtypes = _res, _args
+
+
+class Rope:
+    """Rotary frequencies of heads of `dh` elements: pair j (elements j and
+    j + len(freq)) turns by position[axis[j]] * freq[j] radians; what is left of
+    the head stays as it is."""
+
+    def __init__(self, dh, axis, freq):
+        n = len(freq)
+        if len(axis) != n:
+            raise ValueError("axis and freq must have one entry per pair")
+        if n % 8 or 2 * n > dh or dh > 128:
+            raise ValueError("pairs must be a multiple of 8, at most dh / 2")
+        self.dh, self.axes = int(dh), max(axis, default=0) + 1
+        if min(axis, default=0) < 0 or self.axes > 4:
+            raise ValueError("axes are numbered 0 to 3")
+        self.desc = RopeDesc(2 * n, self.axes, (ctypes.c_uint8 * 64)(*axis), (ctypes.c_double * 64)(*freq))
+
+    @classmethod
+    def standard(cls, dh, base=10000.0, rot=None, sections=None, interleaved=False):
+        """freq[j] = base^(-2j / rot), rot = dh unless given. `sections`: the pairs
+        of every axis (they add up to rot / 2), one run after the other or, with
+        `interleaved`, in turn (0, 1, 2, 0, 1, 2, ..) as long as an axis has pairs."""
+        rot = dh if rot is None else rot
+        sections = [rot // 2] if sections is None else list(sections)
+        if sum(sections) != rot // 2 or min(sections) < 0:
+            raise ValueError("sections must add up to rot / 2 pairs")
+        if interleaved:
+            left, axis = list(sections), []
+            while len(axis) < rot // 2:
+                for a, n in enumerate(left):
+                    if n > 0:
+                        axis.append(a)
+                        left[a] -= 1
+        else:
+            axis = [a for a, n in enumerate(sections) for _ in range(n)]
+        return cls(dh, axis, [float(base) ** (-2.0 * j / rot) for j in range(rot // 2)])
+
+
+def rope_kv_write(pages: KVPages, rope: Rope, pos, q, k, v, off, pos0, page_table, q_out=None, stream=None):
+    """Turn q [rows][Hq][dh] and k [rows][heads][dh] (bf16, any row stride) by
+    their positions pos int32 [axes][rows] ([rows] with one axis), store k and v
+    in the pages as kv_write does, and return the turned q (q_out, which may be q
+    itself; allocated unless given; with `stream`, order other streams' use of it
+    after it). q None: no q, returns None."""
+    dev, dh = pages.index, pages.dh
+    if rope.dh != dh:
+        raise ValueError(f"rope is for heads of {rope.dh}, the pages have heads of {dh}")
+    kp, ks = _rows_ptr(k, dev, pages.heads, dh, "k")
+    vp, vs = _rows_ptr(v, dev, pages.heads, dh, "v")
+    rows = k.shape[0]
+    if rows != v.shape[0]:
+        raise ValueError("k and v must have the same rows")
+    pp = _ptr_on(pos, dev, torch.int32, "pos")
+    if pos.shape != (rope.axes, rows) and not (rope.axes == 1 and pos.shape == (rows,)):
+        raise ValueError(f"pos must be [{rope.axes}][{rows}]")
+    B, n, po, pt, p0 = _batch(dev, off, page_table, pos0, "pos0")
+    Hq = qp = qs = op = os_ = 0
+    if q is not None:
+        Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+        qp, qs = _rows_ptr(q, dev, Hq, dh, "q")
+        if q.shape[0] != rows:
+            raise ValueError("q and k must have the same rows")
+        if q_out is None:
+            q_out = _alloc((rows, Hq, dh), torch.bfloat16, pages.device, stream)
+            op, os_ = q_out.data_ptr(), Hq * dh
+        else:
+            op, os_ = _rows_ptr(q_out, dev, Hq, dh, "q_out")
+            if q_out.shape[0] != rows:
+                raise ValueError("q_out and q must have the same rows")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    a = RopeWriteArgs(pp, qp, kp, vp, op, qs, ks, vs, os_, po, p0, pt, n, B, Hq, rows)
+    _launch("dllm_rope_kv_write", dev, stream, pages.desc, rope.desc, a)
+    return q_out
+
+
+def _host_sizes(**kw):
+    """(ctypes would cut longer numbers off)"""
+    for name, v in kw.items():
+        if not 0 <= v < _I31:
+            raise ValueError(f"{name} must be 0 to 2^31 - 1")
+
+
+def tree_mask(parent, off, max_q, mask=None, depth=None, stream=None):
+    """(mask int32 [rows][ceil(max_q / 32)], depth int32 [rows]) of the trees of
+    drafted tokens parent int32 [rows] (row off[i] + t: the parent's number, less
+    than t, or -1): which of its request's tokens each token descends from, itself
+    included, as bits, and how many they are without itself. Rows in no request
+    are left as they are. With `stream`, order other streams' use of them after it."""
+    _host_sizes(max_q=max_q)
+    dev = parent.get_device() if isinstance(parent, torch.Tensor) else -1
+    pp, po = _ptr_on(parent, dev, torch.int32, "parent"), _ptr_on(off, dev, torch.int32, "offsets")
+    rows, B, words = parent.numel(), off.numel() - 1, (int(max_q) + 31) // 32
+    if B < 0:
+        raise ValueError("offsets must have an entry")
+    if mask is None:
+        mask = _alloc((rows, words), torch.int32, parent.device, stream)
+    elif mask.dim() != 2 or mask.shape[0] != rows or mask.shape[1] < words:
+        raise ValueError(f"mask must be [{rows}][{words} or more]")
+    if depth is None:
+        depth = _alloc((rows,), torch.int32, parent.device, stream)
+    elif depth.shape != (rows,):
+        raise ValueError(f"depth must be [{rows}]")
+    _launch("dllm_tree_mask", dev, stream, pp, po, rows, int(max_q), B, _ptr_on(mask, dev, torch.int32, "mask"), mask.shape[1],
+            _ptr_on(depth, dev, torch.int32, "depth"))
+    return mask, depth
+
+
+def tree_attn(q, pages: KVPages, q_off, kv_len, page_table, mask, max_q, max_kv, scale=None, out=None, out_fp32=False,
+              return_lse=False, lse=None, ws=None, stream=None):
+    """paged_attn of drafted tokens: the rows of request i are its last cached
+    positions, and each sees all positions before them, itself, and the tokens
+    whose bits are set in its row of mask int32 [rows][ceil(max_q / 32) or more]
+    (tree_mask). Workspace: paged_attn_workspace of the same sizes."""
+    dev = pages.index
+    mp = _ptr_on(mask, dev, torch.int32, "mask")
+    rows = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+    if mask.dim() != 2 or mask.shape[0] != rows or 32 * mask.shape[1] < max_q:
+        raise ValueError(f"mask must be [{rows}][{-(-max_q // 32)} or more]")
+    return _attend("dllm_tree_attn", (mp, mask.shape[1]), q, pages, q_off, kv_len, page_table, max_q, max_kv, None, scale, -1,
+                   -1, 0, out, out_fp32, return_lse, lse, ws, stream)
+
+
+def _mass_ptr(mass, pages):
+    """Pointer of the weights beside the pages, or None."""
+    if mass is None:
+        return None
+    if mass.shape != pages.k.shape[:3]:
+        raise ValueError("mass must be [num_pages][heads][page_size]")
+    return _ptr_on(mass, pages.index, torch.float32, "mass")
+
+
+def _per_request(t, B, dev, name):
+    if t is None:
+        return None
+    if t.numel() != B:
+        raise ValueError(f"{name} must have one entry per request")
+    return _ptr_on(t, dev, torch.int32, name)
+
+
+def attn_mass(q, lse, pages: KVPages, mass, q_off, kv_len, page_table, max_q, max_kv, q_pos=None, fresh=None, scale=None,
+              right=-1, decay=1.0, stream=None):
+    """Add to mass float32 [num_pages][heads][page_size] (times `decay`; times 0
+    from position fresh[i] int32 [B] on) the weight that the query rows q
+    [rows][Hq][dh], with lse [rows][Hq] from paged_attn, gave to every cached row
+    of their requests. The rows see keys up to `right` behind their position
+    (negative: all). Returns mass."""
+    _host_sizes(max_q=max_q, max_kv=max_kv)
+    if not -_I31 <= right < _I31:
+        raise ValueError("right must fit 32 bits")
+    dev, dh = pages.index, pages.dh
+    rows, Hq = (q.shape[0], q.shape[1]) if isinstance(q, torch.Tensor) and q.dim() == 3 else (0, 0)
+    qp, qs = _rows_ptr(q, dev, Hq, dh, "q")
+    lp = _ptr_on(lse, dev, torch.float32, "lse")
+    if lse.shape != (rows, Hq):
+        raise ValueError(f"lse must be [{rows}][{Hq}]")
+    B, n, po, pt, pn = _batch(dev, q_off, page_table, kv_len, "kv_len")
+    a = AttnMassArgs(qp, qs, lp, _mass_ptr(mass, pages), po, pn, _per_request(q_pos, B, dev, "q_pos"),
+                     _per_request(fresh, B, dev, "fresh"), pt, n, B, Hq, int(max_q), int(max_kv), rows,
+                     1.0 / math.sqrt(dh) if scale is None else float(scale), int(right), float(decay))
+    _launch("dllm_attn_mass", dev, stream, pages.desc, a)
+    return mass
+
+
+def _tables(page_table, dst_table, dev, B):
+    """(pointer and pages of page_table, of dst_table): None stands for in place."""
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B][max_pages]")
+    pt, n = _ptr_on(page_table, dev, torch.int32, "page_table"), page_table.shape[1]
+    if dst_table is None or dst_table is page_table:
+        return pt, n, None, 0
+    if dst_table.dim() != 2 or dst_table.shape[0] != B:
+        raise ValueError("dst_table must be [B][pages]")
+    return pt, n, _ptr_on(dst_table, dev, torch.int32, "dst_table"), dst_table.shape[1]
+
+
+def kv_move(pages: KVPages, src, count, first, page_table, dst_table=None, mass=None, stream=None):
+    """Move the cached rows at positions src int32 [B][heads or 1][n] (the first
+    count[i] of them) to positions first[i] + 0, 1, .. (first None: from 0) of
+    dst_table's pages, which page_table does not name, or in place: then each list
+    ascends and no row moves to a later position. mass float32
+    [num_pages][heads][page_size] moves with the rows."""
+    dev, B = pages.index, count.numel()
+    if src.dim() != 3 or src.shape[0] != B or src.shape[1] not in (1, pages.heads):
+        raise ValueError(f"src must be [{B}][{pages.heads} or 1][n]")
+    sp, cp, fp = _ptr_on(src, dev, torch.int32, "src"), _per_request(count, B, dev, "count"), _per_request(first, B, dev, "first")
+    pt, n, dt, dn = _tables(page_table, dst_table, dev, B)
+    a = KvMoveArgs(sp, cp, fp, pt, dt, src.shape[1], src.shape[2], n, dn, B, _mass_ptr(mass, pages))
+    _launch("dllm_kv_move", dev, stream, pages.desc, a)
+
+
+def kv_evict(pages: KVPages, mass, kv_len, page_table, budget, max_kv, sinks=0, recent=0, dst_table=None, move_mass=True,
+             new_len=None, keep=None, stream=None):
+    """Cut every request down to `budget` rows a cached head: the first `sinks`,
+    the last `recent` and those of greatest mass float32
+    [num_pages][heads][page_size] stay, in their order, at positions 0, 1, .. of
+    dst_table's pages (default: in place, see kv_move). Returns (new_len int32 [B],
+    keep int32 [B][heads][budget], the positions that stayed, then -1); with
+    `stream`, order other streams' use of them after it."""
+    _host_sizes(budget=budget, max_kv=max_kv, sinks=sinks, recent=recent)
+    dev, B = pages.index, kv_len.numel()
+    kp = _ptr_on(kv_len, dev, torch.int32, "kv_len")
+    pt, n, dt, dn = _tables(page_table, dst_table, dev, B)
+    if new_len is None:
+        new_len = _alloc((B,), torch.int32, pages.device, stream)
+    if keep is None:
+        keep = _alloc((B, pages.heads, int(budget)), torch.int32, pages.device, stream)
+    elif keep.shape != (B, pages.heads, budget):
+        raise ValueError(f"keep must be [{B}][{pages.heads}][{budget}]")
+    a = KvEvictArgs(_mass_ptr(mass, pages), kp, pt, dt, n, dn, B, int(budget), int(max_kv), int(sinks), int(recent),
+                    1 if move_mass else 0, _per_request(new_len, B, dev, "new_len"), _ptr_on(keep, dev, torch.int32, "keep"))
+    _launch("dllm_kv_evict", dev, stream, pages.desc, a)
+    return new_len, keep

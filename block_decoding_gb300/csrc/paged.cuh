@@ -24,6 +24,9 @@ struct PagedArgs {
   float *part_o;
   float2 *part_ml;
   struct JoinJob *join;
+  // trees of drafted tokens: the bits of the new tokens that each row sees
+  const uint32_t *mask;
+  int mask_stride, mask_words;
 };
 
 // An item that several CTAs shared: its first piece, the number of pieces,
@@ -63,6 +66,9 @@ __device__ __forceinline__ void visible(const PagedArgs &a, int pos, int t, int 
   hi = a.right < 0 ? L : static_cast<int>(min(static_cast<long long>(L), max(p + a.right + 1, 0ll)));
   lo = a.left < 0 ? 0 : static_cast<int>(min(max(p - a.left, 0ll), 0x7fffffffll));
 }
+
+// Keys that every row of a request of drafted tokens sees: those before its first.
+__device__ __forceinline__ int tree_prefix(const Extent &x) { return min(max(x.pos, 0), x.L); }
 
 constexpr int kTile = 128;   // keys per tile
 
@@ -417,6 +423,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 // Launches the kernel for many rows per cached head (paged_rows.cu) with row
 // tiles of n_rows = 128 or 256 on `ctas` CTAs.
+// With a.mask the rows are drafted tokens.
 dllm_status launch_paged_rows(int dh, bool fp8, int n_rows, const CUtensorMap &tk, const CUtensorMap &tv,
                               const PagedArgs &a, int ctas, cudaStream_t s);
 

@@ -103,10 +103,20 @@ struct Cfg {
 // What the softmax needs to know of the row tile's rows.
 template <int N>
 struct alignas(16) RowInfo {
-  int lo[N], hi[N];   // the keys the row sees, apart from the sinks
+  int lo[N], hi[N];   // the keys the row sees, apart from the sinks (trees: lo[c], c < 32, the rows that see new token c)
   int out[N];         // row of out [q_rows * Hq], or -1: not a query row
   float scale[N];     // e4m3 parts: what the query row was divided by
 };
+
+// Trees: the rows (bits of flat rows) that see the new token `lane`, from the
+// bits of the tokens that each new token sees. By one warp; W * group <= 32.
+__device__ __forceinline__ uint32_t rows_that_see(const PagedArgs &a, const Extent &x, int lane) {
+  uint32_t sees = 0, rows = 0;
+  if (lane < x.W) sees = (a.mask[static_cast<size_t>(x.q0 + lane) * a.mask_stride] & below(a.max_q)) | (1u << lane);
+  for (int t = 0; t < x.W; ++t)
+    if (__shfl_sync(0xffffffffu, sees, t) >> lane & 1) rows |= below(a.group) << (t * a.group);
+  return rows;
+}
 
 // A piece of an item as the warps that work on it need it.
 struct alignas(16) Piece {
@@ -152,7 +162,7 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[CN
 // The N query rows of a piece into shared memory as the B operand of S^T
 // (core matrices along K, row groups of 8), by 256 threads, with what the
 // softmax needs to know of each row.
-template <int DH, bool FP8, int N>
+template <int DH, bool FP8, int N, bool TREE>
 __device__ __forceinline__ void stage_queries(const PagedArgs &a, const Piece &pc, uint8_t *sq, RowInfo<N> &info, int tid) {
   const int rows = pc.x.W * a.group;
   constexpr int kChunks = DH / 8;                  // 16-byte chunks of a bf16 row
@@ -165,11 +175,13 @@ __device__ __forceinline__ void stage_queries(const PagedArgs &a, const Piece &p
     if (idx < N * kChunks && r < rows)
       u[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + (pc.x.q0 + t) * a.q_stride + (pc.h * a.group + g) * DH + idx % kChunks * 8));
   }
+  uint32_t see_token = 0;
+  if (TREE && tid < 32) see_token = rows_that_see(a, pc.x, tid);
   if (tid < N) {
     const int r = pc.r0 + tid, t = r / a.group;
     int lo = 0, hi = 0x7fffffff;   // a column that is no row masks nothing; its results go nowhere
     if (r < rows) visible(a, pc.x.pos, t, pc.x.L, lo, hi);
-    info.lo[tid] = lo;
+    info.lo[tid] = TREE ? static_cast<int>(see_token) : lo;
     info.hi[tid] = hi;
     info.out[tid] = r < rows ? (pc.x.q0 + t) * a.Hq + pc.h * a.group + (r - t * a.group) : -1;
   }
@@ -231,7 +243,7 @@ __device__ __forceinline__ void split_e5m2(const float (&w)[4], uint32_t (&out)[
   }
 }
 
-template <int DH, bool FP8, int N>
+template <int DH, bool FP8, int N, bool TREE>
 __global__ void __launch_bounds__(Cfg<DH, FP8, N>::kThreads, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a) {
   using C = Cfg<DH, FP8, N>;
@@ -448,7 +460,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const uint32_t pi = seg % kAhead;
       if (!warp_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag)) return;
       if (!pieces[pi].more) return;
-      stage_queries<DH, FP8, N>(a, pieces[pi], smem + C::kOffQ, info[seg & 1], threadIdx.x - 128);
+      stage_queries<DH, FP8, N, TREE>(a, pieces[pi], smem + C::kOffQ, info[seg & 1], threadIdx.x - 128);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[pi]);
@@ -463,6 +475,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const RowInfo<N> &ri = info[seg & 1];
       const TileList tl = pc.t;
       const int nT = pc.tiles, j0 = pc.j0;
+      const int every = TREE ? tree_prefix(pc.x) : tl.hi_first;   // keys before it are behind no row
       float l[N];
 #pragma unroll
       for (int e = 0; e < N; ++e) l[e] = 0.f;
@@ -475,8 +488,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const uint32_t b = n % kSBuf, pb = n % kPBuf;
         const int key0 = tl.tile(j0 + j) * kTile, u = key0 + key;
         // every row of the tile sees every key of it?
-        const bool all_seen = key0 + kTile <= tl.hi_first && (key0 >= tl.lo_last || key0 + kTile <= a.sinks);
+        const bool all_seen = key0 + kTile <= every && (key0 >= tl.lo_last || key0 + kTile <= a.sinks);
         const bool seen = u < tl.hi && (u >= tl.lo || u < a.sinks);   // this key, by any row
+        uint32_t rows_see = 0xffffffffu;    // trees: the rows that see this key
+        if (TREE && !all_seen) {
+          if (u >= pc.x.L) {
+            rows_see = 0;
+          } else if (u >= pc.x.pos) {
+            const uint32_t token = static_cast<uint32_t>(u) - static_cast<uint32_t>(pc.x.pos);
+            rows_see = token < N ? static_cast<uint32_t>(ri.lo[token]) : 0u;
+          }
+        }
         float c = a.scale_log2;
         int vexp = -128;                    // exponent of the key's V scale
         bool vnan = false;
@@ -515,7 +537,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           if (!all_seen) {
 #pragma unroll
             for (int e = 0; e < N; ++e)
-              if (!(u < ri.hi[e] && (u >= ri.lo[e] || u < a.sinks))) x[e] = -INFINITY;
+              if (TREE ? !(rows_see >> e & 1) : !(u < ri.hi[e] && (u >= ri.lo[e] || u < a.sinks))) x[e] = -INFINITY;
           }
         };
         relative(m_s + g0);
@@ -920,7 +942,7 @@ Ws ws_layout(const dllm_kv_pages *pages, const dllm_paged_attn_args *a) {
 template <int DH, bool FP8, int N>
 dllm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &g, int ctas, cudaStream_t s) {
   using C = Cfg<DH, FP8, N>;
-  auto kern = paged_attn_kernel<DH, FP8, N>;
+  auto kern = g.mask ? paged_attn_kernel<DH, FP8, N, true> : paged_attn_kernel<DH, FP8, N, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kBytes, s, tk, tv, g);
   return e == cudaSuccess ? DLLM_OK : cuda_error(e);
@@ -969,10 +991,11 @@ extern "C" size_t dllm_paged_attn_workspace(const dllm_kv_pages *pages, const dl
   return ws_layout(pages, a).total;
 }
 
-extern "C" dllm_status dllm_paged_attn(const dllm_kv_pages *pages, const dllm_paged_attn_args *a, void *ws,
-                                       size_t ws_bytes, dllm_stream stream) {
-  const dllm_status st = check_shape(pages, a);
-  if (st != DLLM_OK) return st;
+namespace {
+
+// Either attention: of drafted tokens with the mask of a tree.
+dllm_status attend(const dllm_kv_pages *pages, const dllm_paged_attn_args *a, const uint32_t *mask, int mask_stride, void *ws,
+                   size_t ws_bytes, dllm_stream stream) {
   if (a->B == 0 || a->max_q == 0 || a->q_rows == 0) return DLLM_OK;
   const dllm_status sp = check_page_pointers(pages);
   if (sp != DLLM_OK) return sp;
@@ -993,6 +1016,7 @@ extern "C" dllm_status dllm_paged_attn(const dllm_kv_pages *pages, const dllm_pa
   g.max_kv = static_cast<int>(table < a->max_kv ? table : a->max_kv);
   g.scale_log2 = a->scale * 1.4426950408889634f;
   g.left = a->left; g.right = a->right; g.sinks = a->left >= 0 ? a->sinks : 0;
+  g.mask = mask; g.mask_stride = mask_stride; g.mask_words = (a->max_q + 31) / 32;
   cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&g.status), g_status_paged);
   if (e != cudaSuccess) return cuda_error(e);
   if (layout.total > 0) {
@@ -1005,4 +1029,23 @@ extern "C" dllm_status dllm_paged_attn(const dllm_kv_pages *pages, const dllm_pa
   const bool fp8 = pages->type == DLLM_KV_E4M3;
   if (pages->dh == 64) return fp8 ? launch_attn<64, true>(pages, a, g, s) : launch_attn<64, false>(pages, a, g, s);
   return fp8 ? launch_attn<128, true>(pages, a, g, s) : launch_attn<128, false>(pages, a, g, s);
+}
+
+}  // namespace
+
+extern "C" dllm_status dllm_paged_attn(const dllm_kv_pages *pages, const dllm_paged_attn_args *a, void *ws,
+                                       size_t ws_bytes, dllm_stream stream) {
+  const dllm_status st = check_shape(pages, a);
+  if (st != DLLM_OK) return st;
+  return attend(pages, a, nullptr, 0, ws, ws_bytes, stream);
+}
+
+extern "C" dllm_status dllm_tree_attn(const dllm_kv_pages *pages, const dllm_paged_attn_args *a, const uint32_t *mask,
+                                      int mask_stride, void *ws, size_t ws_bytes, dllm_stream stream) {
+  const dllm_status st = check_shape(pages, a);
+  if (st != DLLM_OK) return st;
+  if (a->q_pos || a->left >= 0 || a->right >= 0 || mask_stride < (a->max_q + 31) / 32) return DLLM_ERR_INVALID_ARG;
+  if (a->max_q > DLLM_TREE_TOKENS) return DLLM_ERR_UNSUPPORTED;
+  if (!mask && a->B > 0 && a->max_q > 0 && a->q_rows > 0) return DLLM_ERR_INVALID_ARG;
+  return attend(pages, a, mask, mask_stride, ws, ws_bytes, stream);
 }

@@ -164,7 +164,7 @@ __device__ __forceinline__ void stage_rows(const PagedArgs &a, const RowsPiece &
   }
 }
 
-template <int DH, bool FP8, bool TWO>
+template <int DH, bool FP8, bool TWO, bool TREE>
 __global__ void __launch_bounds__(RowsCfg<DH, FP8, TWO>::kThreads, 1)
 paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a) {
   using C = RowsCfg<DH, FP8, TWO>;
@@ -453,6 +453,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const int r = pc.r0 + (two ? s * 128 : 0) + tid, t = r / a.group;
       int lo = 0, hi = 0x7fffffff;   // a row that is none masks nothing; its results go nowhere
       if (r < rows) visible(a, pc.x.pos, t, pc.x.L, lo, hi);
+      const int every = TREE ? tree_prefix(pc.x) : tl.hi_first;   // keys before it are behind no row
       const float qs = FP8 ? qs_s[(seg & 1) * 256 + (two ? s * 128 : 0) + tid] : 1.f;
       const int cnt = two ? nT : s == 0 ? (nT + 1) / 2 : nT / 2;
       // Streams with rows of their own, in this piece and the next: a stream's
@@ -482,7 +483,26 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       for (int k = 0; k < cnt; ++k, ++ns) {
         const uint32_t n = n0 + (two ? k : 2 * k + s);
         const int key0 = tl.tile(j0 + (two ? k : 2 * k + s)) * kTile;
-        const bool masked = !(key0 + kTile <= tl.hi_first && (key0 >= tl.lo_last || key0 + kTile <= a.sinks));
+        const bool masked = !(key0 + kTile <= every && (key0 >= tl.lo_last || key0 + kTile <= a.sinks));
+        // trees: the keys of a masked tile that this row sees, fetched before the wait for the scores
+        uint32_t tree[4] = {0, 0, 0, 0};
+        if (TREE && masked) {
+          const uint32_t *bits = a.mask + static_cast<size_t>(pc.x.q0 + t) * a.mask_stride;
+          auto word = [&](long long i) {
+            return r < rows && i >= 0 && i < a.mask_words ? __ldg(bits + i) & below(a.max_q - static_cast<int>(i) * 32) : 0u;
+          };
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            // the first of these 32 keys is new token c: words floor(c / 32) and the next one, moved into place;
+            // every row sees the tokens before the first, and itself
+            const long long c = static_cast<long long>(key0) + w * 32 - pc.x.pos, own = t - c;
+            const long long i = c >> 5;
+            tree[w] = __funnelshift_r(word(i), word(i + 1), static_cast<uint32_t>(c) & 31);
+            if (c < 0) tree[w] |= below(c <= -32 ? 32 : static_cast<int>(-c));
+            if (own >= 0 && own < 32) tree[w] |= 1u << own;
+            tree[w] &= below(pc.x.L - key0 - w * 32);
+          }
+        }
         const float c = FP8 ? qs : a.scale_log2;
         if constexpr (FP8) mbar_wait(&col_full[n % 4], (n / 4) & 1, abort_flag);
         if constexpr (!FP8) {
@@ -539,7 +559,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             x[e + 2] = __float_as_uint(y1.x); x[e + 3] = __float_as_uint(y1.y);
           }
           if (masked) {
-            const uint32_t mask = below(hi - key0 - w * 32) & (~below(lo - key0 - w * 32) | below(a.sinks - key0 - w * 32));
+            const uint32_t mask = TREE ? (w < 2 ? (w == 0 ? tree[0] : tree[1]) : w == 2 ? tree[2] : tree[3])
+                                       : below(hi - key0 - w * 32) & (~below(lo - key0 - w * 32) | below(a.sinks - key0 - w * 32));
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!(mask >> e & 1)) x[e] = 0xff800000u;
@@ -718,7 +739,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 template <int DH, bool FP8, bool TWO>
 dllm_status launch(const CUtensorMap &tk, const CUtensorMap &tv, const PagedArgs &a, int ctas, cudaStream_t s) {
   using C = RowsCfg<DH, FP8, TWO>;
-  auto kern = paged_rows_kernel<DH, FP8, TWO>;
+  auto kern = a.mask ? paged_rows_kernel<DH, FP8, TWO, true> : paged_rows_kernel<DH, FP8, TWO, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
   if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kBytes, s, tk, tv, a);
   return e == cudaSuccess ? DLLM_OK : cuda_error(e);

@@ -8,6 +8,10 @@ namespace dllm {
 
 uint32_t status_kv(bool clear);
 uint32_t status_paged(bool clear);
+uint32_t status_rope(bool clear);
+uint32_t status_tree(bool clear);
+uint32_t status_mass(bool clear);
+uint32_t status_evict(bool clear);
 
 struct KvPages {
   uint8_t *k, *v;                  // [num_pages][heads][page_size][dh], bf16 or e4m3

@@ -1,0 +1,231 @@
+// Rotary positions on the way into the paged cache: q and k rows are turned by
+// their positions on one or several axes, q goes to its own rows and k, v to
+// the pages (bf16, or 8 bits with a scale per row and head), in one pass.
+//
+// Pair j of a head (elements j and j + rot / 2) turns by pos[axis(j)] * freq(j).
+// The angle is needed modulo a turn only: freq(j) / 2 pi is kept as a 64-bit
+// fraction of a turn, its product with the position wraps around by itself, and
+// what is left is within 2^-64 turns per position of the exact angle, however
+// far the position (a product in fp32 is off by 0.06 at position 10^6).
+//
+// Bound by memory: each row is read and written once. The sines and cosines of
+// a row are computed once per block and serve all of its heads. One row of one
+// head is handled by dh / 16 neighbouring lanes, two 16-byte chunks each: a pair's
+// two halves lie in the same lane.
+#include <math.h>
+
+#include "page_rows.cuh"
+#include "umma.cuh"
+
+namespace dllm {
+
+DLLM_DEFINE_STATUS(rope)
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxRows = 4;      // rows of a block
+constexpr int kMaxHalf = 64;     // pairs of a head
+
+struct RopeArgs {
+  KvPages c;
+  const uint16_t *q, *k, *v;
+  uint16_t *q_out;
+  long long q_stride, k_stride, v_stride, q_out_stride;
+  const int32_t *pos;          // [axes][rows]
+  int rows, B, Hq, half, per;
+  const int32_t *off, *pos0;
+  unsigned int *status;
+  unsigned long long turns[kMaxHalf];   // of a position, in 2^-64
+  uint8_t axis[kMaxHalf];
+};
+
+// Scale byte of a row whose largest magnitude has the bits `a` (finite fp32).
+__device__ __forceinline__ int scale_byte_f32(uint32_t a) {
+  const int b = static_cast<int>(a >> 23) - 8 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return min(max(b, 10), 247);
+}
+
+__device__ __forceinline__ uint2 quantise8_f32(const float *x, float f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = f32_to_e4m3x2(x[2 * i] * f, x[2 * i + 1] * f);
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// As quantise_row, of 16 fp32 elements a lane.
+template <int LPR>
+__device__ __forceinline__ int quantise_row_f32(const float (&a)[8], const float (&b)[8], uint2 &qa, uint2 &qb) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    m = max(m, max(__float_as_uint(a[e]) & 0x7fffffffu, __float_as_uint(b[e]) & 0x7fffffffu));
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int byte = scale_byte_f32(m);
+  const float f = __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
+  qa = quantise8_f32(a, f);
+  qb = quantise8_f32(b, f);
+  if (byte == 247) {
+    qa = make_uint2(cap240(qa.x), cap240(qa.y));
+    qb = make_uint2(cap240(qb.x), cap240(qb.y));
+  }
+  return m >= 0x7f800000u ? 255 : byte;
+}
+
+// (cos, sin) of `pos` times a 64-bit fraction of a turn.
+__device__ __forceinline__ float2 turn_of(int pos, unsigned long long turns) {
+  const long long t = static_cast<long long>(turns * static_cast<unsigned long long>(static_cast<long long>(pos)));
+  float2 r;
+  sincospif(__ll2float_rn(t) * 0x1p-63f, &r.y, &r.x);
+  return r;
+}
+
+template <int DH, bool FP8>
+__global__ void __launch_bounds__(kThreads) rope_write_kernel(const __grid_constant__ RopeArgs g) {
+  constexpr int LPR = DH / 16, kUnits = kThreads / LPR;
+  __shared__ float2 s_cs[kMaxRows * kMaxHalf];
+  __shared__ int s_row[kMaxRows];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, l = tid % LPR;
+  if (blockIdx.x + tid == 0 && (g.off[0] < 0 || g.off[g.B] > g.rows)) atomicOr(g.status, DLLM_DEV_OFFSETS);
+  const int r0 = blockIdx.x * g.per, rows = min(g.per, g.rows - r0);
+  const int heads = g.c.heads, T = g.Hq + 2 * heads, half = g.half, rc = half / 8;
+  // this lane's chunks of a head: the halves of eight pairs, or two that are not turned
+  const bool turns = l < rc;
+  const int ca = turns ? l : rc + l, cb = turns ? l + rc : ca + LPR - rc;
+  if (tid < rows) {
+    const int r = r0 + tid, i = request_of(g.off, g.B, r);
+    int row = -1;                                   // in no request
+    if (i >= 0) {
+      const long long u = static_cast<long long>(g.pos0[i]) + (r - g.off[i]);
+      row = u < 0 || u > 0x7fffffffll ? -1 : page_row(g.c, i, static_cast<int>(u));
+      if (row < 0) {
+        atomicOr(g.status, DLLM_DEV_PAGE);
+        row = -2;                                   // no place
+      }
+    }
+    s_row[tid] = row;
+  }
+  for (int idx = tid; idx < rows * half; idx += kThreads) {
+    const int n = idx / half, j = idx - n * half;
+    s_cs[n * kMaxHalf + j] = turn_of(g.pos[static_cast<size_t>(g.axis[j]) * g.rows + r0 + n], g.turns[j]);
+  }
+  __syncthreads();
+  // Every lane of a warp goes through the same number of rounds: the lanes of
+  // a row exchange maxima.
+  const int total = rows * T;
+  int n = 0, t = tid / LPR;
+  while (t >= T) { t -= T; ++n; }
+  for (int u0 = 0; u0 < total; u0 += kUnits) {
+    const bool live = n < rows;
+    const int row = live ? s_row[n] : -1;
+    const bool is_q = t < g.Hq, is_k = !is_q && t < g.Hq + heads;
+    const int h = is_q ? t : is_k ? t - g.Hq : t - g.Hq - heads;
+    const long long r = r0 + n;
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (row != -1) {
+      const uint16_t *src = is_q ? g.q + r * g.q_stride : is_k ? g.k + r * g.k_stride : g.v + r * g.v_stride;
+      const uint4 *s4 = reinterpret_cast<const uint4 *>(src + h * DH);
+      a = s4[ca];
+      b = s4[cb];
+    }
+    float x[8], y[8];
+    unpack8(a, x);
+    unpack8(b, y);
+    if (turns && (is_q || is_k) && live) {
+      const float2 *cs = s_cs + n * kMaxHalf + l * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 w = cs[e];
+        const float p = x[e] * w.x - y[e] * w.y;
+        y[e] = y[e] * w.x + x[e] * w.y;
+        x[e] = p;
+      }
+    }
+    if (is_q) {
+      if (row != -1) {
+        uint4 *d = reinterpret_cast<uint4 *>(g.q_out + r * g.q_out_stride + h * DH);
+        d[ca] = pack8(x);
+        d[cb] = pack8(y);
+      }
+    }
+    const size_t at = static_cast<size_t>(max(row, 0)) + (static_cast<size_t>(h) << g.c.page_shift);
+    if constexpr (FP8) {
+      uint2 qa, qb;
+      const int byte = quantise_row_f32<LPR>(x, y, qa, qb);
+      if (!is_q && row >= 0) {
+        uint2 *d = reinterpret_cast<uint2 *>((is_k ? g.c.k : g.c.v) + at * DH);
+        d[ca] = qa;
+        d[cb] = qb;
+        if (l == 0) (is_k ? g.c.k_scale : g.c.v_scale)[at] = static_cast<uint8_t>(byte);
+      }
+    } else if (!is_q && row >= 0) {
+      uint4 *d = reinterpret_cast<uint4 *>((is_k ? g.c.k : g.c.v) + at * (DH * 2));
+      d[ca] = is_k ? pack8(x) : a;
+      d[cb] = is_k ? pack8(y) : b;
+    }
+    t += kUnits;
+    while (t >= T) { t -= T; ++n; }
+  }
+}
+
+// freq / 2 pi modulo 1 as a 64-bit fraction: the product with 1 / 2 pi in two
+// parts, so that its error is that of the last bit kept.
+unsigned long long fraction_of_turn(double freq) {
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;   // 1 / 2 pi = kHi + kLo
+  const double hi = freq * kHi, lo = fma(freq, kHi, -hi) + freq * kLo;
+  const double whole = hi - floor(hi);                                        // exact, in [0, 1)
+  // (1 - 2^-53 is the most it can be; the sum wraps around a turn)
+  return static_cast<unsigned long long>(whole * 0x1p64) + static_cast<unsigned long long>(llrint(lo * 0x1p64));
+}
+
+}  // namespace
+}  // namespace dllm
+
+using namespace dllm;
+
+extern "C" dllm_status dllm_rope_kv_write(const dllm_kv_pages *pages, const dllm_rope *rope,
+                                          const dllm_rope_write_args *a, dllm_stream stream) {
+  const dllm_status st = check_pages(pages);
+  if (st != DLLM_OK) return st;
+  if (!rope || !a || a->rows < 0 || a->B < 0 || a->max_pages < 0 || a->Hq < 0) return DLLM_ERR_INVALID_ARG;
+  if (a->B > 4096 || a->rows > 0x7fffffff - kThreads || a->Hq > 16384) return DLLM_ERR_UNSUPPORTED;
+  if (rope->rot < 0 || rope->rot > pages->dh || rope->axes < 1) return DLLM_ERR_INVALID_ARG;
+  if (rope->rot % 16 || rope->axes > DLLM_ROPE_AXES) return DLLM_ERR_UNSUPPORTED;
+  for (int j = 0; j < rope->rot / 2; ++j) {
+    if (rope->axis[j] >= rope->axes) return DLLM_ERR_INVALID_ARG;
+    if (!(fabs(rope->freq[j]) <= 1024.0)) return DLLM_ERR_INVALID_ARG;      // NaN too
+  }
+  if (a->rows == 0 || a->B == 0) return DLLM_OK;
+  const dllm_status sp = check_page_pointers(pages);
+  if (sp != DLLM_OK) return sp;
+  const long long d = static_cast<long long>(pages->heads) * pages->dh, dq = static_cast<long long>(a->Hq) * pages->dh;
+  if (!a->k || !a->v || !a->pos || !a->off || !a->pos0 || (!a->page_table && a->max_pages > 0)) return DLLM_ERR_INVALID_ARG;
+  if (!aligned16(a->k) || !aligned16(a->v) || a->k_stride < d || a->v_stride < d || a->k_stride % 8 || a->v_stride % 8)
+    return DLLM_ERR_INVALID_ARG;
+  if (a->Hq > 0 && (!a->q || !a->q_out || !aligned16(a->q) || !aligned16(a->q_out) || a->q_stride < dq ||
+                    a->q_out_stride < dq || a->q_stride % 8 || a->q_out_stride % 8))
+    return DLLM_ERR_INVALID_ARG;
+  RopeArgs g{};
+  g.c = device_pages(pages, a->page_table, a->max_pages);
+  g.q = a->q; g.k = a->k; g.v = a->v; g.q_out = a->q_out;
+  g.q_stride = a->q_stride; g.k_stride = a->k_stride; g.v_stride = a->v_stride; g.q_out_stride = a->q_out_stride;
+  g.pos = a->pos; g.rows = a->rows; g.B = a->B; g.Hq = a->Hq; g.half = rope->rot / 2;
+  g.off = a->off; g.pos0 = a->pos0;
+  for (int j = 0; j < g.half; ++j) {
+    g.turns[j] = fraction_of_turn(rope->freq[j]);
+    g.axis[j] = rope->axis[j];
+  }
+  cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&g.status), g_status_rope);
+  if (e != cudaSuccess) return cuda_error(e);
+  g.per = a->rows >= 8 * num_sms() ? kMaxRows : 1;
+  const bool fp8 = pages->type == DLLM_KV_E4M3;
+  void (*kern)(RopeArgs) = pages->dh == 64 ? (fp8 ? rope_write_kernel<64, true> : rope_write_kernel<64, false>)
+                                           : (fp8 ? rope_write_kernel<128, true> : rope_write_kernel<128, false>);
+  e = launch_pdl(kern, dim3(static_cast<unsigned>((a->rows - 1) / g.per + 1)), dim3(kThreads), 0,
+                 static_cast<cudaStream_t>(stream), g);
+  if (e != cudaSuccess) return cuda_error(e);
+  return launch_status();
+}

@@ -63,6 +63,8 @@ typedef enum {
 #define DLLM_DEV_ROW_RANGE     0x10  /* a row map entry outside [0,B) x [0,blk) */
 #define DLLM_DEV_OFFSETS       0x20  /* q_off / kv_off beyond the given buffers  */
 #define DLLM_DEV_PAGE          0x40  /* a page id or position outside the pages  */
+#define DLLM_DEV_TREE          0x80  /* a drafted token's parent is none of its
+                                        request's earlier tokens               */
 
 /* Decoding-strategy parameters (host struct, passed by pointer).
  *  tau          confidence threshold: commit when p >= tau
@@ -562,6 +564,182 @@ size_t dllm_paged_attn_workspace(const dllm_kv_pages *pages /* host */,
 dllm_status dllm_paged_attn(const dllm_kv_pages *pages /* host */,
                             const dllm_paged_attn_args *args /* host */,
                             void *ws, size_t ws_bytes, dllm_stream stream);
+
+/* ---------------------------------------------------------------------
+ * dllm_rope_kv_write -- rotary positions on the way into the cache: q and k
+ * rows are turned by their positions on one or several axes, q goes to rows of
+ * its own, k and v to the pages, as dllm_kv_write stores rows.
+ *
+ *   Elements j and j + rot/2 of every q and k head, j < rot/2, turn by
+ *   a = pos[axis[j]][row] * freq[j] radians:
+ *     y_j        = x_j cos a - x_{j+rot/2} sin a
+ *     y_{j+rot/2} = x_{j+rot/2} cos a + x_j sin a
+ *   and elements from rot on stay as they are. Text has one axis; images and
+ *   video have one each for time, height and width, and axis[] says which
+ *   pairs turn by which: runs of pairs, or in turn.
+ *   The angle is the exact product modulo a turn, within 2^-64 turns per
+ *   position and 2^-24 of itself: far positions are as exact as near ones.
+ *   Products and sums are fp32 and a result is rounded once, to bf16 or, for
+ *   8-bit pages, to the row's codes (k's scale is that of the turned row).
+ *
+ *   rope     host: rot (a multiple of 16, at most dh; 0: nothing turns), axes
+ *            (1 to DLLM_ROPE_AXES), axis[j] < axes, |freq[j]| <= 1024
+ *   pos      int32 [axes][rows] on the device, any values
+ *   q        bf16 [rows][Hq][dh], q_out the same; k, v bf16 [rows][heads][dh];
+ *            strides in elements from row to row (at least a row, multiples of
+ *            8), 16-byte aligned. q_out may be q with the same stride. Hq = 0:
+ *            no q.
+ *   off, pos0, page_table, max_pages, B, rows: as dllm_kv_write: row off[i] + t
+ *            is stored at position pos0[i] + t of request i, whatever its
+ *            positions on the axes are (a drafted token's slot is not its depth,
+ *            an evicted cache's rows have moved up). A row in no request leaves
+ *            q_out as it is; one without a place (DLLM_DEV_PAGE) is not stored.
+ * Hq <= 16384. No workspace.
+ * ------------------------------------------------------------------- */
+#define DLLM_ROPE_AXES 4
+typedef struct {
+  int rot, axes;
+  uint8_t axis[64];
+  double freq[64];
+} dllm_rope;
+typedef struct {
+  const int32_t *pos;
+  const dllm_bf16 *q, *k, *v;
+  dllm_bf16 *q_out;
+  long long q_stride, k_stride, v_stride, q_out_stride;
+  const int32_t *off, *pos0, *page_table;
+  int max_pages, B, Hq, rows;
+} dllm_rope_write_args;
+dllm_status dllm_rope_kv_write(const dllm_kv_pages *pages /* host */,
+                               const dllm_rope *rope /* host */,
+                               const dllm_rope_write_args *args /* host */,
+                               dllm_stream stream);
+
+/* ---------------------------------------------------------------------
+ * dllm_tree_mask, dllm_tree_attn -- drafted tokens that form a tree per
+ * request, verified in one pass over the cache: a token sees the request's
+ * cached tokens, its ancestors and itself.
+ *
+ * dllm_tree_mask: from every token's parent the tokens on its path.
+ *   parent   int32 [rows]: row off[i] + t is token t of request i and holds its
+ *            parent's number, less than t, or -1 for a child of the last
+ *            cached token (anything else counts as -1, DLLM_DEV_TREE)
+ *   mask     uint32 [rows][mask_stride]: bit c % 32 of word c / 32 of row
+ *            off[i] + t is set where c = t or c is an ancestor of t; words
+ *            from ceil(max_q / 32) on keep their values
+ *   depth    int32 [rows] or NULL: ancestors of the token (0: no parent); the
+ *            token's rotary position is that of the first drafted one + depth
+ *   max_q    host upper bound of a request's tokens, at most DLLM_TREE_TOKENS;
+ *            tokens beyond it are not processed (DLLM_DEV_OFFSETS). B <= 4096.
+ *
+ * dllm_tree_attn: as dllm_paged_attn, with other visible keys. The W_i tokens
+ *   of request i have the last W_i cached positions, P = kv_len[i] - W_i on:
+ *   row t sees every position below P, position P + t (its own), and P + c
+ *   where bit c of its mask is set (c < max_q). One mask serves all layers of
+ *   a step; any other mask of the new tokens among each other does too.
+ *   args     as dllm_paged_attn with q_pos NULL, left and right negative;
+ *            max_q <= DLLM_TREE_TOKENS
+ *   mask     uint32 [q_rows][mask_stride], mask_stride >= ceil(max_q / 32)
+ *   A V row with an infinity or NaN may reach the request's other rows of the
+ *   same cached head, as it does in dllm_paged_attn. Workspace:
+ *   dllm_paged_attn_workspace of the same pages and args.
+ * ------------------------------------------------------------------- */
+#define DLLM_TREE_TOKENS 1024
+dllm_status dllm_tree_mask(const int32_t *parent, const int32_t *off, int rows,
+                           int max_q, int B, uint32_t *mask, int mask_stride,
+                           int32_t *depth, dllm_stream stream);
+dllm_status dllm_tree_attn(const dllm_kv_pages *pages /* host */,
+                           const dllm_paged_attn_args *args /* host */,
+                           const uint32_t *mask, int mask_stride, void *ws,
+                           size_t ws_bytes, dllm_stream stream);
+
+/* ---------------------------------------------------------------------
+ * dllm_attn_mass -- the weight that attention gave to every cached row,
+ * gathered in the row's own slot: for position u < kv_len[i] of every request
+ * that has query rows, and cached head h,
+ *     mass <- decay * mass + sum exp(scale * <q[t,g,:], k[u,h,:]> - lse[t,g])
+ *   over its query rows t and the query heads g of h that see u: those at
+ *   position p >= u - right (right < 0: all), p as in dllm_paged_attn. With the
+ *   lse that dllm_paged_attn returned for these rows the terms are the
+ *   attention's weights; a row with lse = -infinity (it saw no key) adds nothing.
+ *   mass     float [num_pages][heads][page_size], as the scales lie. Slots of
+ *            other positions keep their values.
+ *   fresh    int32 [B] or NULL: positions u >= fresh[i] start from 0, whatever
+ *            their slots hold (rows written since the last step); NULL: none
+ *   decay    finite; 1 sums up, 0 keeps the last step's weights only (a slot
+ *            that holds an infinity or NaN is not cleared by it: fresh is)
+ *   lse      float [q_rows][Hq]; the others as in dllm_paged_attn. What is
+ *            beyond max_q, max_kv, q_rows or the table is not processed
+ *            (DLLM_DEV_OFFSETS), nor a page id that is none (DLLM_DEV_PAGE).
+ * Sums are fp32, in an order that the shapes alone decide: the same call on the
+ * same GPU gives the same bits. A slot that two requests or two positions share
+ * ends with either's value. Sizes as dllm_paged_attn. No workspace.
+ * ------------------------------------------------------------------- */
+typedef struct {
+  const dllm_bf16 *q;
+  long long q_stride;
+  const float *lse;
+  float *mass;
+  const int32_t *q_off, *kv_len, *q_pos, *fresh, *page_table;
+  int max_pages, B, Hq, max_q, max_kv, q_rows;
+  float scale;
+  int right;
+  float decay;
+} dllm_attn_mass_args;
+dllm_status dllm_attn_mass(const dllm_kv_pages *pages /* host */,
+                           const dllm_attn_mass_args *args /* host */,
+                           dllm_stream stream);
+
+/* ---------------------------------------------------------------------
+ * dllm_kv_move -- rows to other positions of their request: the row of
+ * cached head h at position src[i][h][j] goes to position first[i] + j, for
+ * j < count[i].
+ *   src      int32 [B][src_heads][max_n], src_heads = heads (lists of their own)
+ *            or 1 (one list for all heads); count int32 [B] (at most max_n, what
+ *            is beyond is not moved, DLLM_DEV_OFFSETS); first int32 [B] or
+ *            NULL: 0
+ *   dst_table  int32 [B][dst_pages]: where the rows go. NULL or page_table: in
+ *            place; then every list ascends and src[i][h][j] >= first[i] + j
+ *            (a row that does not keep to that is not moved, DLLM_DEV_PAGE).
+ *            Else no page it names may be one that page_table names.
+ *   mass     float [num_pages][heads][page_size] that moves with the rows, or
+ *            NULL
+ * Rows, and with 8-bit pages their scales, are moved bit for bit. Slots that no
+ * row moves to keep theirs; a row without a place in either table is not moved
+ * (DLLM_DEV_PAGE). Two requests whose pages are the same may not both move rows
+ * there. B <= 4096, max_n < 2^30. No workspace.
+ *
+ * dllm_kv_evict -- cut every request down to `budget` rows a cached head: the
+ * first `sinks` and the last `recent` positions stay, and of those between the
+ * ones of greatest mass (NaN counts as the greatest; of equal ones the lower
+ * position), `budget` in all; each head has its own. They move, in their
+ * order, to positions 0, 1, .. as by dllm_kv_move. A request of no more than
+ * `budget` rows keeps all of them.
+ *   mass     float [num_pages][heads][page_size]; move_mass != 0: moves too
+ *   new_len  int32 [B]: min(kv_len[i], budget), the request's length from now on
+ *   keep     int32 [B][heads][budget]: the positions that stayed, ascending,
+ *            then -1
+ *   max_kv   host upper bound of kv_len[i]; rows beyond it or the table are
+ *            not there (DLLM_DEV_OFFSETS)
+ *   sinks + recent <= budget, 1 <= budget < 2^30. No workspace.
+ * ------------------------------------------------------------------- */
+typedef struct {
+  const int32_t *src, *count, *first, *page_table, *dst_table;
+  int src_heads, max_n, max_pages, dst_pages, B;
+  float *mass;
+} dllm_kv_move_args;
+dllm_status dllm_kv_move(const dllm_kv_pages *pages /* host */,
+                         const dllm_kv_move_args *args /* host */,
+                         dllm_stream stream);
+typedef struct {
+  float *mass;
+  const int32_t *kv_len, *page_table, *dst_table;
+  int max_pages, dst_pages, B, budget, max_kv, sinks, recent, move_mass;
+  int32_t *new_len, *keep;
+} dllm_kv_evict_args;
+dllm_status dllm_kv_evict(const dllm_kv_pages *pages /* host */,
+                          const dllm_kv_evict_args *args /* host */,
+                          dllm_stream stream);
 
 /* ---------------------------------------------------------------------
  * Status helpers.

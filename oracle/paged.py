@@ -71,14 +71,14 @@ def visible(pos, kv_len, left, right, sinks):
     return see
 
 
-def attention(q, k, v, pos, scale, left=-1, right=-1, sinks=0):
+def attention(q, k, v, pos, scale, left=-1, right=-1, sinks=0, see=None):
     """One request: q [W][Hq][dh], its cached rows k, v [L][H][dh], the rows'
-    positions [W]. Returns (out, lse, weighted |v| sums, score magnitudes):
+    positions [W], or what they see as truth values `see` [W][L]. Returns (out, lse, weighted |v| sums, score magnitudes):
     the last two are what rounding of the weights and of the scores scales
     with. What no row sees is not read."""
     W, Hq, dh = q.shape
     L, H, _ = k.shape
-    see = visible(pos, L, left, right, sinks)
+    see = visible(pos, L, left, right, sinks) if see is None else see
     used = see.any(axis=0)
     out, lse = np.zeros((W, Hq, dh)), np.full((W, Hq), -np.inf)
     absv, mag = np.zeros((W, Hq, dh)), np.zeros((W, Hq))
