@@ -143,4 +143,11 @@ __host__ __device__ constexpr uint32_t idesc_f8(int M, int N, uint32_t a_type, u
 // coordinate counts 8-row groups; groups beyond the pool read as zeros.
 bool make_tmap_page_rows(CUtensorMap *map, const void *base, uint64_t rows, int dh, int elem_bytes, uint32_t box_rows);
 
+// Tensor map over query rows [rows][heads][dh] bf16, `stride` elements (a
+// multiple of 8) from row to row: one box is 64 elements of `box_heads` heads of
+// `box_rows` rows, laid out in shared memory as one 128-byte row (swizzled) per
+// head after the other. Rows beyond the last read as zeros.
+bool make_tmap_query_rows(CUtensorMap *map, const void *q, uint64_t rows, int heads, int dh, long long stride,
+                          uint32_t box_heads, uint32_t box_rows);
+
 }  // namespace dllm
