@@ -1,6 +1,7 @@
 // Moving rows within the paged cache, and choosing the rows that stay when a
 // cache is cut down to a budget.
 #include "pages.cuh"
+#include "umma.cuh"
 
 namespace dllm {
 
@@ -20,7 +21,9 @@ struct SelectArgs {
   unsigned int *status;
 };
 
-constexpr int kSelThreads = 512;
+constexpr int kMaxSelWarps = 32;
+constexpr int kBins = 2048;      // 11 bits at a time
+constexpr int kCached = 49152;   // weights that shared memory holds (192 KB)
 
 // Order of weights as unsigned numbers: -0 is 0, NaN is above everything.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -29,16 +32,23 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One CTA per cached head and request: radix selection of the least weight
-// that stays, 8 bits at a time, then the positions in order.
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
-  __shared__ int s_hist[256];
-  __shared__ int s_scan[kSelThreads / 32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_left;
+// One CTA per cached head and request. The weights that are chosen from are
+// read once into shared memory (CACHED; more than fit are read again by every
+// pass, from L2). Radix selection finds the least weight that stays, 11 bits at a
+// time: a histogram, and the bin in which the count from above passes the number
+// of rows that stay, by one scan over all bins. Then every warp counts its own
+// run of positions and, behind the sum over the warps before it, writes those
+// that stay in their order.
+template <bool CACHED>
+__global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ SelectArgs a) {
+  extern __shared__ uint32_t s_key[];            // CACHED: [max_kv]
+  __shared__ uint32_t s_hist[kBins];
+  __shared__ int s_sum[kMaxSelWarps], s_tie[kMaxSelWarps];
+  __shared__ uint32_t s_bin;
+  __shared__ int s_left, s_of_bin;
   pdl_trigger();
   pdl_wait();
-  const int h = blockIdx.x, i = blockIdx.y, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int h = blockIdx.x, i = blockIdx.y, tid = threadIdx.x, nt = blockDim.x, warp = tid / 32, lane = tid % 32, warps = nt / 32;
   int n = a.kv_len[i];
   if (n < 0 || n > a.max_kv) {
     if (tid + h == 0) atomicOr(a.status, DLLM_DEV_OFFSETS);
@@ -47,13 +57,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
   int32_t *keep = a.keep + (static_cast<size_t>(i) * a.c.heads + h) * a.budget;
   const int k = min(n, a.budget);
   if (h == 0 && tid == 0) a.new_len[i] = k;
-  for (int j = tid + k; j < a.budget; j += kSelThreads) keep[j] = -1;
+  for (int j = tid + k; j < a.budget; j += nt) keep[j] = -1;
   if (n <= a.budget) {
-    for (int j = tid; j < k; j += kSelThreads) keep[j] = j;
+    for (int j = tid; j < k; j += nt) keep[j] = j;
     return;
   }
-  const int s = a.sinks, e = n - a.recent;       // [s, e) is chosen from: at least n - budget + 1 rows
-  auto key = [&](int u) {
+  const int s = a.sinks, e = n - a.recent;       // [s, e) is chosen from: at least n - budget rows
+  auto fetch = [&](int u) {
     const int row = page_row(a.c, i, u);
     if (row < 0) {
       atomicOr(a.status, DLLM_DEV_PAGE);
@@ -61,61 +71,111 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
     }
     return order_of(a.mass[row + (static_cast<size_t>(h) << a.c.page_shift)]);
   };
+  auto key = [&](int u) { return CACHED ? s_key[u] : fetch(u); };
   int left = k - s - a.recent;                   // how many of them stay
-  uint32_t prefix = 0;
-  for (int shift = 24; shift >= 0 && left > 0; shift -= 8) {
-    for (int b = tid; b < 256; b += kSelThreads) s_hist[b] = 0;
+  uint32_t least = 0;                            // the bits of the least that stays, found so far
+  int shift = 32;                                // ... from this bit on
+  for (int bits = 0; left > 0 && shift > 0; ) {
+    const bool filled = shift < 32;              // the weights are in shared memory
+    bits = shift == 32 || shift == 21 ? 11 : 10;
+    for (int b = tid; b < kBins; b += nt) s_hist[b] = 0;
     __syncthreads();
-    for (int u = s + tid; u < e; u += kSelThreads) {
-      const uint32_t x = key(u);
-      if (shift == 24 || x >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&s_hist[x >> shift & 255], 1);
+    const int low = shift - bits;
+    const uint32_t mask = (1u << bits) - 1;
+#pragma unroll 4
+    for (int u = s + tid; u < e; u += nt) {
+      uint32_t x;
+      if (CACHED && filled) {
+        x = s_key[u];
+      } else {
+        x = fetch(u);
+        if (CACHED) s_key[u] = x;
+      }
+      if (!filled || x >> shift == least >> shift) atomicAdd(&s_hist[x >> low & mask], 1u);
     }
     __syncthreads();
-    if (tid == 0) {
-      int b = 255;
-      while (s_hist[b] < left) left -= s_hist[b--];
-      s_prefix = prefix | static_cast<uint32_t>(b) << shift;
-      s_left = left;
+    // counts from the highest bin down: thread t has kBins / nt bins, the highest first
+    const int per = kBins / nt, top = kBins - 1 - tid * per;
+    int mine = 0;
+    for (int b = 0; b < per; ++b) mine += s_hist[top - b];
+    int up = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += y;
+    }
+    if (lane == 31) s_sum[warp] = up;
+    __syncthreads();
+    int before = up - mine;
+    {
+      const int y = lane < warp ? s_sum[lane] : 0;
+      before += __reduce_add_sync(0xffffffffu, y);
+    }
+    if (before < left && left <= before + mine) {     // one thread
+      int b = 0;
+      while (before + static_cast<int>(s_hist[top - b]) < left) before += s_hist[top - b++];
+      s_bin = top - b;
+      s_left = left - before;
+      s_of_bin = s_hist[top - b];
     }
     __syncthreads();
-    prefix = s_prefix;
+    least |= s_bin << low;
     left = s_left;
+    shift = low;
+    if (s_of_bin == left) break;                 // all of the bin stay
   }
-  if (left <= 0) prefix = 0xffffffffu;           // none of them
-  // `left` rows of weight `prefix` stay, the first ones, and all above
-  int done = 0, ties = 0;                        // before this round
-  for (int u0 = 0; u0 < n; u0 += kSelThreads) {
-    const int u = u0 + tid;
-    bool in = false, tie = false;
-    if (u < n) {
-      if (u < s || u >= e) in = true;
-      else if (left > 0) {
-        const uint32_t x = key(u);
-        in = x > prefix;
-        tie = x == prefix;
-      }
+  // Rows whose bits from `shift` on are those of `least` are ties: the first
+  // `left` of them stay, and all above. (The shift by 32 does not occur: with
+  // left <= 0 no row of [s, e) stays.)
+  const int run = ((n + warps - 1) / warps + 31) / 32 * 32, u0 = warp * run, u1 = min(n, u0 + run);
+  const bool some = left > 0;
+  auto look = [&](int u, bool &in, bool &tie) {
+    in = tie = false;
+    if (u >= u1) return;
+    if (u < s || u >= e) {
+      in = true;
+    } else if (some) {
+      const uint32_t x = key(u);
+      in = x >> shift > least >> shift;
+      tie = x >> shift == least >> shift;
     }
-    auto rank = [&](bool p, int &total) {        // of this thread among those with p
-      const uint32_t m = __ballot_sync(0xffffffffu, p);
-      if (lane == 0) s_scan[warp] = __popc(m);
-      __syncthreads();
-      int before = __popc(m & ((1u << lane) - 1));
-      total = 0;
-      for (int w = 0; w < kSelThreads / 32; ++w) {
-        if (w < warp) before += s_scan[w];
-        total += s_scan[w];
-      }
-      __syncthreads();
-      return before;
-    };
-    int total;
-    const int tr = rank(tie, total);
-    in |= tie && ties + tr < left;
-    ties += total;
-    const int r = rank(in, total);
-    if (in) keep[done + r] = u;
-    done += total;
+  };
+  int count = 0, ties = 0;
+  for (int u = u0; u < u1; u += 32) {
+    bool in, tie;
+    look(u + lane, in, tie);
+    count += __popc(__ballot_sync(0xffffffffu, in));
+    ties += __popc(__ballot_sync(0xffffffffu, tie));
   }
+  __syncthreads();                               // s_sum is read by all
+  if (lane == 0) {
+    s_sum[warp] = count;
+    s_tie[warp] = ties;
+  }
+  __syncthreads();
+  // ties before this warp, and rows that stay before it
+  const int c = lane < warp ? s_sum[lane] : 0, t = lane < warp ? s_tie[lane] : 0;
+  int tie_at = __reduce_add_sync(0xffffffffu, t);
+  int at = __reduce_add_sync(0xffffffffu, c) + min(tie_at, max(left, 0));
+  for (int u = u0; u < u1; u += 32) {
+    bool in, tie;
+    look(u + lane, in, tie);
+    const uint32_t below_lane = (1u << lane) - 1, tm = __ballot_sync(0xffffffffu, tie);
+    in |= tie && tie_at + __popc(tm & below_lane) < left;
+    tie_at += __popc(tm);
+    const uint32_t im = __ballot_sync(0xffffffffu, in);
+    if (in) keep[at + __popc(im & below_lane)] = u + lane;
+    at += __popc(im);
+  }
+}
+
+cudaError_t launch_select(const SelectArgs &g, int B, cudaStream_t s) {
+  const int threads = g.max_kv <= 2048 ? 256 : 1024;
+  if (g.max_kv > kCached) return launch_pdl(select_kernel<false>, dim3(g.c.heads, B), dim3(threads), 0, s, g);
+  const int smem = g.max_kv * 4;
+  cudaError_t e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(select_kernel<true>, dim3(g.c.heads, B), dim3(threads), smem, s, g);
 }
 
 // ---------------------------------------------------------------------------
@@ -129,80 +189,111 @@ struct ShiftArgs {
   int src_heads, max_n;
   const int32_t *count, *first;   // [B]; first may be null: 0
   float *mass;
-  bool in_place;
   unsigned int *status;
 };
 
-constexpr int kMoveThreads = 256, kEach = 8;   // 16-byte pieces of a thread on the way
+constexpr int kMoveThreads = 512;
+constexpr int kEach = 4;         // rows of a thread in a round (16 bytes of K and of V each)
 
-// One CTA per cached head, request, and K or V. Rows move in ascending order,
-// a piece at a time, every row of a piece read before any is written: in place
-// a row's own place is written no earlier than it is read.
-template <int ROW>
-__global__ void __launch_bounds__(kMoveThreads) shift_kernel(const ShiftArgs a) {
-  constexpr int kChunks = ROW / 16, kRows = kMoveThreads * kEach / kChunks;
+// Rows of ROW bytes that a CTA moves in a round.
+constexpr int round_rows(int row_bytes) { return kMoveThreads * kEach * 16 / row_bytes; }
+
+// One request and cached head, K and V: a CTA of the grid's x takes
+// round_rows of the list. Elsewhere that is all. In place the CTAs of x are a
+// cluster that walks the list from its start, round by round: every row of a
+// round is read before any is written (a cluster barrier between the two), and
+// since lists ascend and no row moves to a later position, a place is written
+// in no earlier round than it is read: position first + j is row src[j'] of the
+// list with j' <= j if it is any. The next round's rows lie behind all places
+// written so far, so it needs no barrier before its loads.
+template <int ROW, bool IN_PLACE>
+__global__ void __launch_bounds__(kMoveThreads) shift_kernel(const __grid_constant__ ShiftArgs a) {
+  constexpr int kChunks = ROW / 16, kStep = kMoveThreads / kChunks, kRows = kStep * kEach;
+  static_assert(kRows == round_rows(ROW), "rows of a round");
   pdl_trigger();
   pdl_wait();
-  const int h = blockIdx.x, i = blockIdx.y, tid = threadIdx.x;
-  const bool v = blockIdx.z;
-  uint8_t *pool = v ? a.c.v : a.c.k, *scale = v ? a.c.v_scale : a.c.k_scale;
-  float *mass = v ? nullptr : a.mass;
+  const int h = blockIdx.y, i = blockIdx.z, tid = threadIdx.x, c = tid % kChunks;
   int n = a.count[i];
+  const int first = a.first ? a.first[i] : 0;
   if (n < 0 || n > a.max_n) {
     if (tid == 0) atomicOr(a.status, DLLM_DEV_OFFSETS);
     n = min(max(n, 0), a.max_n);
   }
-  const int first = a.first ? a.first[i] : 0;
   const int32_t *src = a.src + (static_cast<size_t>(i) * a.src_heads + (a.src_heads > 1 ? h : 0)) * a.max_n;
   KvPages to = a.c;
   to.table = a.dst_table;
   to.max_pages = a.dst_pages;
-  for (int j0 = 0; j0 < n; j0 += kRows) {
-    uint4 x[kEach];
-    uint8_t sc[kEach];
+  const size_t head = static_cast<size_t>(h) << a.c.page_shift;
+  for (int base = IN_PLACE ? 0 : blockIdx.x * kRows; base < n; base += gridDim.x * kRows) {   // (n < 2^30)
+    const int j0 = IN_PLACE ? base + blockIdx.x * kRows : base;
+    uint4 k[kEach], v[kEach];
+    uint8_t ks[kEach], vs[kEach];
     float m[kEach];
-    long long at[kEach];
+    int from[kEach], dest[kEach];
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
-      const int idx = tid + q * kMoveThreads, j = j0 + idx / kChunks, c = idx % kChunks;
-      at[q] = -1;
+      const int j = j0 + tid / kChunks + q * kStep;
+      from[q] = dest[q] = -1;
       if (j >= n) continue;
       const int u = src[j];
       const long long d = static_cast<long long>(first) + j;
       bool bad = d < 0 || d > 0x7fffffffll;
-      if (a.in_place) bad |= u < d || (j > 0 && src[j - 1] >= u);
-      const int from = bad ? -1 : page_row(a.c, i, u), dest = bad ? -1 : page_row(to, i, static_cast<int>(d));
-      if (from < 0 || dest < 0) {
-        atomicOr(a.status, DLLM_DEV_PAGE);
-        continue;
+      if constexpr (IN_PLACE) {
+        bad |= u < d || (j > 0 && src[j - 1] >= u);
+        if (u == d && !bad) continue;                 // stays
       }
-      const size_t s = from + (static_cast<size_t>(h) << a.c.page_shift);
-      at[q] = dest + (static_cast<long long>(h) << a.c.page_shift);
-      x[q] = *reinterpret_cast<const uint4 *>(pool + s * ROW + c * 16);
-      if (c == 0) {
-        if (scale) sc[q] = scale[s];
-        if (mass) m[q] = mass[s];
+      if (!bad) {
+        from[q] = page_row(a.c, i, u);
+        dest[q] = page_row(to, i, static_cast<int>(d));
+      }
+      if (from[q] < 0 || dest[q] < 0) {
+        atomicOr(a.status, DLLM_DEV_PAGE);
+        from[q] = -1;
       }
     }
-    __syncthreads();
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
-      const int c = (tid + q * kMoveThreads) % kChunks;
-      if (at[q] < 0) continue;
-      *reinterpret_cast<uint4 *>(pool + at[q] * ROW + c * 16) = x[q];
+      if (from[q] < 0) continue;
+      const size_t s = from[q] + head;
+      k[q] = *reinterpret_cast<const uint4 *>(a.c.k + s * ROW + c * 16);
+      v[q] = *reinterpret_cast<const uint4 *>(a.c.v + s * ROW + c * 16);
       if (c == 0) {
-        if (scale) scale[at[q]] = sc[q];
-        if (mass) mass[at[q]] = m[q];
+        if (a.c.k_scale) { ks[q] = a.c.k_scale[s]; vs[q] = a.c.v_scale[s]; }
+        if (a.mass) m[q] = a.mass[s];
       }
     }
-    __syncthreads();
+    if constexpr (IN_PLACE) {
+      __syncwarp();
+      cluster_barrier();
+    }
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) {
+      if (from[q] < 0) continue;
+      const size_t s = dest[q] + head;
+      *reinterpret_cast<uint4 *>(a.c.k + s * ROW + c * 16) = k[q];
+      *reinterpret_cast<uint4 *>(a.c.v + s * ROW + c * 16) = v[q];
+      if (c == 0) {
+        if (a.c.k_scale) { a.c.k_scale[s] = ks[q]; a.c.v_scale[s] = vs[q]; }
+        if (a.mass) a.mass[s] = m[q];
+      }
+    }
+    if (!IN_PLACE) break;
   }
 }
 
-dllm_status launch_shift(const dllm_kv_pages *pages, const ShiftArgs &g, int B, cudaStream_t s) {
+template <int ROW>
+cudaError_t launch_shift_rows(const ShiftArgs &g, bool in_place, int heads, int B, cudaStream_t s) {
+  const int blocks = (g.max_n - 1) / round_rows(ROW) + 1;
+  if (!in_place) return launch_pdl(shift_kernel<ROW, false>, dim3(blocks, heads, B), dim3(kMoveThreads), 0, s, g);
+  const unsigned cluster = blocks > 4 ? 8 : blocks > 2 ? 4 : blocks;
+  return launch_pdl_clusters(shift_kernel<ROW, true>, cluster, dim3(cluster, heads, B), dim3(kMoveThreads), 0, s, g);
+}
+
+dllm_status launch_shift(const dllm_kv_pages *pages, const ShiftArgs &g, bool in_place, int B, cudaStream_t s) {
   const int row = pages->dh * (pages->type == DLLM_KV_E4M3 ? 1 : 2);
-  void (*kern)(ShiftArgs) = row == 64 ? shift_kernel<64> : row == 128 ? shift_kernel<128> : shift_kernel<256>;
-  const cudaError_t e = launch_pdl(kern, dim3(pages->heads, B, 2), dim3(kMoveThreads), 0, s, g);
+  const cudaError_t e = row == 64    ? launch_shift_rows<64>(g, in_place, pages->heads, B, s)
+                        : row == 128 ? launch_shift_rows<128>(g, in_place, pages->heads, B, s)
+                                     : launch_shift_rows<256>(g, in_place, pages->heads, B, s);
   return e == cudaSuccess ? DLLM_OK : cuda_error(e);
 }
 
@@ -224,13 +315,13 @@ extern "C" dllm_status dllm_kv_move(const dllm_kv_pages *pages, const dllm_kv_mo
     return DLLM_ERR_INVALID_ARG;
   ShiftArgs g{};
   g.c = device_pages(pages, a->page_table, a->max_pages);
-  g.in_place = !a->dst_table || a->dst_table == a->page_table;
-  g.dst_table = g.in_place ? a->page_table : a->dst_table;
-  g.dst_pages = g.in_place ? a->max_pages : a->dst_pages;
+  const bool in_place = !a->dst_table || a->dst_table == a->page_table;
+  g.dst_table = in_place ? a->page_table : a->dst_table;
+  g.dst_pages = in_place ? a->max_pages : a->dst_pages;
   g.src = a->src; g.src_heads = a->src_heads; g.max_n = a->max_n; g.count = a->count; g.first = a->first; g.mass = a->mass;
   cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&g.status), g_status_evict);
   if (e != cudaSuccess) return cuda_error(e);
-  const dllm_status sl = launch_shift(pages, g, a->B, static_cast<cudaStream_t>(stream));
+  const dllm_status sl = launch_shift(pages, g, in_place, a->B, static_cast<cudaStream_t>(stream));
   return sl == DLLM_OK ? launch_status() : sl;
 }
 
@@ -257,15 +348,15 @@ extern "C" dllm_status dllm_kv_evict(const dllm_kv_pages *pages, const dllm_kv_e
   if (e != cudaSuccess) return cuda_error(e);
   ShiftArgs m{};
   m.c = g.c;
-  m.in_place = !a->dst_table || a->dst_table == a->page_table;
-  m.dst_table = m.in_place ? a->page_table : a->dst_table;
-  m.dst_pages = m.in_place ? a->max_pages : a->dst_pages;
+  const bool in_place = !a->dst_table || a->dst_table == a->page_table;
+  m.dst_table = in_place ? a->page_table : a->dst_table;
+  m.dst_pages = in_place ? a->max_pages : a->dst_pages;
   m.src = a->keep; m.src_heads = pages->heads; m.max_n = a->budget; m.count = a->new_len;
   m.mass = a->move_mass ? a->mass : nullptr;
   m.status = g.status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  e = launch_pdl(select_kernel, dim3(pages->heads, a->B), dim3(kSelThreads), 0, s, g);
+  e = launch_select(g, a->B, s);
   if (e != cudaSuccess) return cuda_error(e);
-  const dllm_status sl = launch_shift(pages, m, a->B, s);
+  const dllm_status sl = launch_shift(pages, m, in_place, a->B, s);
   return sl == DLLM_OK ? launch_status(2) : sl;
 }
