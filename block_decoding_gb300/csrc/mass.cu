@@ -18,11 +18,15 @@
 // Warp roles:
 //   warp 0      K tiles by TMA, one box per page
 //   warp 1      MMAs
-//   warp 2      query rows by TMA, lse and bounds of each chunk's rows
+//   warp 2      lse and bounds of each chunk's rows, and (bf16 pages) the rows
+//               by TMA
 //   warp 3      walks the CTA's items ahead of the others
 //   warps 4..11 two groups, one key per thread: exponentials and sums
-//   last four   (e4m3 pages) K codes to bf16, exactly; the scale is a factor of
-//               the scores
+//   last four   (e4m3 pages) query rows in two e4m3 parts, as paged_attn.cu has
+//               them: K codes go to the tensor cores as they are, and the scores
+//               are those whose sum lse is. (Codes converted to bf16 by these
+//               warps: 2.1 k cycles a tile, the loads of a tile 0.7 k.)
+// Neighbouring items of a head whose rows are one chunk share it.
 #include <math.h>
 
 #include "paged.cuh"
@@ -39,44 +43,61 @@ struct MassArgs : PagedArgs {
   float decay;
   int tokens;       // query tokens of a chunk: tokens * group rows
   int columns;      // ... rounded up to the N of the MMA
+  int k_stages;     // tiles and chunks in shared memory, and where the chunks lie
+  int off_q, q_bytes;
 };
 
 constexpr int kItemKeys = 2 * kTile;
 constexpr int kChunkRows = 128;
-constexpr int kAhead = 4;        // items prepared, the current one included
-constexpr int kInfo = 4;         // chunks whose rows' numbers are prepared
+constexpr int kAhead = 16;       // items prepared, the current one included: loads run ahead by whole items
+constexpr int kInfo = 3;         // chunks whose rows' numbers are prepared
 constexpr int kItemLength = 2;   // what an item costs beside its chunks, in chunks
 
 template <int DH, bool FP8>
 struct MassCfg {
   static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);      // a K tile as it is loaded
-  static constexpr int kTileBytes = kTile * DH * 2;            // ... as the MMAs read it
-  static constexpr int kGroup8 = 8 * DH * 2;
-  static constexpr int kQ = kChunkRows * DH * 2;
+  static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);
   static constexpr int kQSt = 2;
-  static constexpr int kCSt = FP8 ? 2 : 0;                     // converted tiles
-  static constexpr int kKSt = FP8 ? (DH == 128 ? 5 : 8) : (DH == 128 ? 4 : 8);
-  static constexpr int kOffConv = kKSt * kRaw;
-  static constexpr int kOffQ = kOffConv + kCSt * kTileBytes;
-  static constexpr int kOffMisc = kOffQ + kQSt * kQ;
-  static constexpr int kMisc = 8192;
-  static constexpr int kBytes = kOffMisc + kMisc + 1024;
+  static constexpr int kMaxKSt = 12;
+  static constexpr int kOffK = 9216;                           // tiles, then chunks of query rows; before them what follows
+  static constexpr int kMost = 232448 - 1024;
   static constexpr int kThreads = 32 * (12 + (FP8 ? 4 : 0));
-  static_assert(kBytes <= 232448 && kOffConv % 1024 == 0, "shared memory");
+  // Bytes of a chunk (bf16, or two e4m3 parts), and the tiles that fit beside kQSt chunks.
+  static int chunk_bytes(int columns) { return columns * DH * 2; }
+  static int stages(int columns) {
+    const int fit = (kMost - kOffK - kQSt * chunk_bytes(columns)) / kRaw;
+    return fit < kMaxKSt ? fit : kMaxKSt;
+  }
+  static_assert((kMost - kOffK - kQSt * 128 * DH * 2) / kRaw >= 2, "shared memory");
+};
+
+// A place in a ring of n and the parity of its round: `full` barriers complete
+// phase `round`, `empty` ones (waited for with the other parity) the one before.
+struct Ring {
+  uint32_t at = 0, round = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++at == n) {
+      at = 0;
+      round ^= 1;
+    }
+  }
 };
 
 struct MassPiece {
   Extent x;
   int i, h, key0;          // request, head, first key
+  int fresh;               // positions from here on start from 0
   int first, chunks;       // chunks [first, chunks) hold rows that see a key of the item
+  int again, keep;         // the chunk is the last item's, is the next one's too
   int tiles;               // key tiles (1 or 2)
   int more;
 };
 
 struct alignas(16) Numbers {   // of a chunk's query rows
   float neg_lse[kChunkRows];   // - lse in log2 units
+  float scale[kChunkRows];     // e4m3 parts: what the row was divided by
   int hi[kChunkRows];          // keys before it are seen; 0: not a row, or one that saw nothing
-  int every;                   // keys before it are seen by all of them
+  int every[kChunkRows / 16];  // keys before it are seen by all of 16
 };
 
 struct MassStart {
@@ -141,21 +162,57 @@ __device__ __forceinline__ void tma_load_rows(void *dst, const CUtensorMap *map,
       : "memory");
 }
 
+// Rows of chunk c, rounded up to the N of an MMA.
+__device__ __forceinline__ int chunk_columns(const MassArgs &a, int W, int c) {
+  return (min(a.tokens, W - c * a.tokens) * a.group + 15) & ~15;
+}
+
+// The query rows of chunk c in two e4m3 parts (DH-byte rows as K's are loaded,
+// the parts a.columns rows apart) and the powers of two that they were divided
+// by, by 128 threads.
+template <int DH>
+__device__ __forceinline__ void stage_chunk(const MassArgs &a, const Extent &x, int h, int c, uint8_t *rows, float *scale, int tid) {
+  constexpr int kChunks = DH / 8, kStep = 128 / kChunks, kAtOnce = 4;   // 16-byte pieces of a row, rows of a step
+  const int count = min(a.tokens, x.W - c * a.tokens) * a.group, piece = tid % kChunks;
+  const uint16_t *q = a.q + (x.q0 + static_cast<long long>(c) * a.tokens) * a.q_stride + h * a.group * DH + piece * 8;
+  for (int n0 = tid / kChunks; n0 - tid / kChunks < count; n0 += kAtOnce * kStep) {    // whole warps
+    uint4 u[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int n = n0 + i * kStep, t = n / a.group;
+      u[i] = n < count ? __ldg(reinterpret_cast<const uint4 *>(q + t * a.q_stride + (n - t * a.group) * DH)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int n = n0 + i * kStep;
+      const uint32_t m2 = max_mag(u[i], 0);
+      uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+      for (int o = kChunks / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (n >= count) continue;
+      uint2 hi, lo;
+      const int byte = split_e4m3(u[i], m, hi, lo);
+      const int at = DH == 128 ? (piece / 2) ^ (n % 8) : (piece / 2) ^ ((n / 2) % 4);
+      uint8_t *d = rows + n * DH + at * 16 + (piece % 2) * 8;
+      *reinterpret_cast<uint2 *>(d) = hi;
+      *reinterpret_cast<uint2 *>(d + a.columns * DH) = lo;
+      if (piece == 0) scale[n] = scale_of(m < 0x7f80u ? byte : 255);   // a row with an infinity or NaN scores NaN
+    }
+  }
+}
+
 template <int DH, bool FP8>
 __global__ void __launch_bounds__(MassCfg<DH, FP8>::kThreads, 1)
 mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ MassArgs a) {
   using C = MassCfg<DH, FP8>;
-  constexpr int kKSt = C::kKSt, kQSt = C::kQSt, kCSt = C::kCSt;
+  constexpr int kQSt = C::kQSt, kTables = 6144;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *misc = smem + C::kOffMisc;
-  Numbers *numbers = reinterpret_cast<Numbers *>(misc);                      // [kInfo]
+  Numbers *numbers = reinterpret_cast<Numbers *>(smem);                      // [kInfo]
   MassPiece *pieces = reinterpret_cast<MassPiece *>(numbers + kInfo);        // [kAhead]
-  uint64_t *k_full = reinterpret_cast<uint64_t *>(misc + 5120);              // [kKSt]
-  uint64_t *k_empty = k_full + kKSt;
-  uint64_t *c_full = k_empty + kKSt;       // [kCSt] converted
-  uint64_t *c_empty = c_full + kCSt;
-  uint64_t *q_full = c_empty + kCSt;       // [kQSt]
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + kTables);              // [k_stages]
+  uint64_t *k_empty = k_full + C::kMaxKSt;
+  uint64_t *q_full = k_empty + C::kMaxKSt;   // [kQSt]
   uint64_t *q_empty = q_full + kQSt;
   uint64_t *n_full = q_empty + kQSt;       // [kInfo]
   uint64_t *n_empty = n_full + kInfo;
@@ -167,17 +224,16 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   MassStart *start = reinterpret_cast<MassStart *>(s_sum + 16);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert(kInfo * sizeof(Numbers) + kAhead * sizeof(MassPiece) <= 5120, "tables");
-  static_assert(5120 + (2 * kKSt + 2 * kCSt + 2 * kQSt + 2 * kInfo + 8 + 2 * kAhead + 16) * 8 + sizeof(MassStart) + 8 <= C::kMisc,
-                "barriers");
+  static_assert(kInfo * sizeof(Numbers) + kAhead * sizeof(MassPiece) <= kTables, "tables");
+  static_assert(kTables + (2 * C::kMaxKSt + 2 * kQSt + 2 * kInfo + 8 + 2 * kAhead + 16) * 8 + sizeof(MassStart) + 8 <= C::kOffK, "barriers");
+  uint8_t *const tiles_at = smem + C::kOffK, *const rows_at = smem + a.off_q;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kKSt; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], FP8 ? 4 : 1); }
-    for (int s = 0; s < kCSt; ++s) { mbar_init(&c_full[s], 4); mbar_init(&c_empty[s], 1); }
-    for (int s = 0; s < kQSt; ++s) { mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1); }
-    for (int s = 0; s < kInfo; ++s) { mbar_init(&n_full[s], 1); mbar_init(&n_empty[s], 8); }
+    for (int s = 0; s < a.k_stages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
+    for (int s = 0; s < kQSt; ++s) { mbar_init(&q_full[s], FP8 ? 4 : 1); mbar_init(&q_empty[s], 1); }
+    for (int s = 0; s < kInfo; ++s) { mbar_init(&n_full[s], FP8 ? 5 : 1); mbar_init(&n_empty[s], 8); }
     for (int s = 0; s < 4; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], 4); }
     for (int s = 0; s < kAhead; ++s) {
       mbar_init(&piece_full[s], 1);
@@ -214,128 +270,165 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 
   if (warp == 0) {
     // --------------------------------------------------------------- K tiles
-    const int per_tile = kTile >> a.c.page_shift, page_rows = 1 << a.c.page_shift;
+    // (an item's pages, one per lane, are looked up while the item before it
+    // waits for room)
+    const int page_rows = 1 << a.c.page_shift, per_tile = kTile >> a.c.page_shift;
     const int none = static_cast<int>((static_cast<long long>(a.c.num_pages) * a.c.heads << a.c.page_shift) / 8);
+    // this lane's page of the item, -1: none (not looked at before the item's turn)
+    auto look_up = [&](const MassPiece *p) {
+      const int u = p->key0 + lane * page_rows;
+      if (lane >= 2 * per_tile || u >= p->x.L) return -1;
+      return __ldg(a.c.table + static_cast<size_t>(p->i) * a.c.max_pages + (u >> a.c.page_shift));
+    };
     bool ok = true;
+    Ring k;
     uint32_t n = 0;
-    for (uint32_t seg = 0; ok; ++seg) {
-      const MassPiece *p = piece(seg);
-      if (!p) break;
-      const int32_t *row = a.c.table + static_cast<size_t>(p->i) * a.c.max_pages;
+    const MassPiece *p = piece(0);
+    int page = p ? look_up(p) : -1;
+    for (uint32_t seg = 0; ok && p; ++seg) {
       const int tiles = p->first < p->chunks ? p->tiles : 0;
-      for (int j = 0; ok && j < tiles; ++j, ++n) {
-        const uint32_t st = n % kKSt;
-        int g = none;              // 8-row group of this lane's page; what there is none of reads as zeros
-        const int u = p->key0 + j * kTile + lane * page_rows;
-        if (lane < per_tile && u < p->x.L) {
-          const int page = __ldg(row + (u >> a.c.page_shift));
-          if (page >= 0 && page < a.c.num_pages) g = ((page * a.c.heads + p->h) << a.c.page_shift) / 8;
-        }
-        if (n >= kKSt) ok = warp_wait(&k_empty[st], (n / kKSt - 1) & 1, abort_flag);
+      const MassPiece *p_next = piece(seg + 1);
+      const int page_next = p_next ? look_up(p_next) : -1;
+      // 8-row group of the page; what there is none of reads as zeros
+      const int g = page >= 0 && page < a.c.num_pages ? ((page * a.c.heads + p->h) << a.c.page_shift) / 8 : none;
+      for (int j = 0; ok && j < tiles; ++j) {
+        ok = warp_wait(&k_empty[k.at], k.round ^ 1, abort_flag);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&k_full[st], C::kRaw);
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[k.at], C::kRaw);
         __syncwarp();
-        if (lane < per_tile) tma_load_4d(smem + st * C::kRaw + lane * page_rows * (C::kRaw / kTile), &tm_k, &k_full[st], g);
+        if (lane / per_tile == j)
+          tma_load_4d(tiles_at + k.at * C::kRaw + (lane - j * per_tile) * page_rows * (C::kRaw / kTile), &tm_k, &k_full[k.at], g);
+        k.next(a.k_stages);
+        ++n;
       }
       piece_done(seg);
+      p = p_next;
+      page = page_next;
     }
     // after an abort the loads in flight land before the CTA's memory is given up
     if (!ok || *abort_flag)
-      if (lane < kKSt && lane < n) mbar_drain(&k_full[lane], ((n - 1 - lane) / kKSt) & 1);
+      if (lane < a.k_stages && lane < n) mbar_drain(&k_full[lane], ((n - 1 - lane) / a.k_stages) & 1);
     __syncwarp();
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMAs
     if (elect_one()) {
-      const uint32_t idesc = idesc_bf16(128, a.columns, 0, 0);
       bool ok = true;
-      uint32_t n = 0, nq = 0, ns[2] = {0, 0};     // key tiles, chunks, units of the groups before this item
+      Ring t, q;                    // key tiles, chunks
+      uint32_t ns[2] = {0, 0};      // units of the groups
       for (uint32_t seg = 0; ok; ++seg) {
         const uint32_t pi = seg % kAhead;
         ok = mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
         if (!ok || !pieces[pi].more) break;
-        const int chunks = pieces[pi].chunks - pieces[pi].first, tiles = pieces[pi].tiles;
-        for (int c = 0; ok && c < chunks; ++c, ++nq) {
-          const uint32_t qs = nq % kQSt;
-          ok = mbar_wait(&q_full[qs], (nq / kQSt) & 1, abort_flag);
-          const uint64_t dq = sw128_desc(smem_u32(smem + C::kOffQ + qs * C::kQ), 16, 1024);
+        const MassPiece &p = pieces[pi];
+        const int first = p.first, chunks = p.chunks, tiles = p.tiles, W = p.x.W;
+        const bool again = p.again, keep = p.keep;
+        Ring behind = t;            // the tile behind the item's
+        if (first < chunks)
+          for (int j = 0; j < tiles; ++j) behind.next(a.k_stages);
+        for (int c = first; ok && c < chunks; ++c) {
+          if (!again) ok = mbar_wait(&q_full[q.at], q.round, abort_flag);
+          const int columns = chunk_columns(a, W, c);
+          const uint32_t sq = smem_u32(rows_at + q.at * a.q_bytes);
+          Ring tile = t;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             if (j >= tiles || !ok) break;
-            const uint32_t t = n + j, b = ns[j] & 1, st = FP8 ? t % (kCSt + !FP8) : t % kKSt;
-            if (c == 0) ok = FP8 ? mbar_wait(&c_full[st], (t / (kCSt + !FP8)) & 1, abort_flag)
-                                 : mbar_wait(&k_full[st], (t / kKSt) & 1, abort_flag);
-            if (ok && ns[j] >= 2) ok = mbar_wait(&s_empty[j * 2 + b], (ns[j] / 2 - 1) & 1, abort_flag);
+            const uint32_t b = ns[j] & 1, t_s = tmem + (j * 2 + b) * 128;
+            if (c == first) ok = mbar_wait(&k_full[tile.at], tile.round, abort_flag);
+            ok = ok && mbar_wait(&s_empty[j * 2 + b], (ns[j] / 2 & 1) ^ 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t dk = sw128_desc(smem_u32(FP8 ? smem + C::kOffConv + st * C::kTileBytes : smem + st * C::kRaw), 16, C::kGroup8);
+            const uint32_t sk = smem_u32(tiles_at + tile.at * C::kRaw);
+            if constexpr (!FP8) {
+              const uint64_t dk = sw128_desc(sk, 16, C::kGroup8), dq = sw128_desc(sq, 16, 1024);
 #pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk)
-              umma_bf16(tmem + (j * 2 + b) * 128, dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                        dq + (((kk >> 2) * (kChunkRows * 128) + (kk & 3) * 32) >> 4), idesc, kk > 0);
+              for (int kk = 0; kk < DH / 16; ++kk)
+                umma_bf16(t_s, dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                          dq + (((kk >> 2) * (a.columns * 128) + (kk & 3) * 32) >> 4), idesc_bf16(128, columns, 0, 0), kk > 0);
+            } else {
+              const uint64_t dk = DH == 128 ? sw128_desc(sk, 16, C::kGroup8) : sw64_desc(sk, 16, C::kGroup8);
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                const uint32_t sp = sq + part * a.columns * DH;
+                const uint64_t dq = DH == 128 ? sw128_desc(sp, 16, 8 * DH) : sw64_desc(sp, 16, 8 * DH);
+#pragma unroll
+                for (int kk = 0; kk < DH / 32; ++kk)
+                  umma_f8(t_s, dk + ((kk * 32) >> 4), dq + ((kk * 32) >> 4), idesc_f8(128, columns, kE4M3, kE4M3, 0, 0), part + kk > 0);
+              }
+            }
             umma_commit(&s_full[j * 2 + b]);
             ++ns[j];
-            if (c + 1 == chunks) umma_commit(FP8 ? &c_empty[st] : &k_empty[st]);
+            if (c + 1 == chunks) umma_commit(&k_empty[tile.at]);
+            tile.next(a.k_stages);
           }
-          if (ok) umma_commit(&q_empty[qs]);
+          if (!keep) {
+            if (ok) umma_commit(&q_empty[q.at]);
+            q.next(kQSt);
+          }
         }
-        if (chunks > 0) n += tiles;
+        t = behind;
         mbar_arrive(&piece_empty[pi]);
       }
     }
     __syncwarp();
   } else if (warp == 2) {
-    // --------------------------------------------------------------- query rows and their numbers
+    // --------------------------------------------------------------- query rows' numbers, bf16 rows
     const uint32_t bytes = static_cast<uint32_t>(a.tokens * a.group) * DH * 2;
     bool ok = true;
-    uint32_t nq = 0, asked = 0;
+    Ring q, in;
+    uint32_t asked = 0;
     for (uint32_t seg = 0; ok; ++seg) {
       const MassPiece *p = piece(seg);
       if (!p) break;
       const Extent x = p->x;
       const int chunks = p->chunks, h = p->h;
-      for (int c = p->first; ok && c < chunks; ++c, ++nq) {
-        const uint32_t qs = nq % kQSt, in = nq % kInfo;
-        if (nq >= kQSt) ok = warp_wait(&q_empty[qs], (nq / kQSt - 1) & 1, abort_flag);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[qs], bytes);
+      for (int c = p->again ? chunks : p->first; ok && c < chunks; ++c) {
+        if constexpr (!FP8) {
+          ok = warp_wait(&q_empty[q.at], q.round ^ 1, abort_flag);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&q_full[q.at], bytes);
 #pragma unroll
-          for (int d = 0; d < DH / 64; ++d)
-            tma_load_rows(smem + C::kOffQ + qs * C::kQ + d * (kChunkRows * 128), &tm_q, &q_full[qs], d * 64, h * a.group,
-                          x.q0 + c * a.tokens);
+            for (int d = 0; d < DH / 64; ++d)
+              tma_load_rows(rows_at + q.at * a.q_bytes + d * (a.columns * 128), &tm_q, &q_full[q.at], d * 64, h * a.group,
+                            x.q0 + c * a.tokens);
+          }
+          q.next(kQSt);
+          ++asked;
+          __syncwarp();
         }
-        ++asked;
-        __syncwarp();
         float lse[kChunkRows / 32];
-        int hi[kChunkRows / 32], every = 0x7fffffff;
+        int hi[kChunkRows / 32], every[kChunkRows / 32];
 #pragma unroll
         for (int e = 0; e < kChunkRows / 32; ++e) {
-          const int r = e * 32 + lane, t = c * a.tokens + r / a.group;
+          const int r = e * 32 + lane, n = r / a.group, t = c * a.tokens + n;
           hi[e] = 0;
           lse[e] = 0.f;
-          if (r < a.tokens * a.group && t < x.W) {
+          if (n < a.tokens && t < x.W) {
             int lo;
-            lse[e] = a.lse[static_cast<size_t>(x.q0 + t) * a.Hq + h * a.group + r % a.group];
+            lse[e] = __ldg(&a.lse[static_cast<size_t>(x.q0 + t) * a.Hq + h * a.group + (r - n * a.group)]);
             visible(a, x.pos, t, x.L, lo, hi[e]);
           }
         }
 #pragma unroll
         for (int e = 0; e < kChunkRows / 32; ++e) {
           if (lse[e] == -INFINITY) hi[e] = 0;
-          if (e * 32 + lane < a.columns) every = min(every, hi[e]);
+          every[e] = hi[e];
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) every[e] = min(every[e], __shfl_xor_sync(0xffffffffu, every[e], o));
         }
-        every = __reduce_min_sync(0xffffffffu, every);
-        if (nq >= kInfo) ok = warp_wait(&n_empty[in], (nq / kInfo - 1) & 1, abort_flag);
+        ok = warp_wait(&n_empty[in.at], in.round ^ 1, abort_flag);
         if (!ok) break;
-        Numbers &s = numbers[in];
+        Numbers &s = numbers[in.at];
 #pragma unroll
         for (int e = 0; e < kChunkRows / 32; ++e) {
           s.neg_lse[e * 32 + lane] = lse[e] * -1.4426950408889634f;
           s.hi[e * 32 + lane] = hi[e];
+          if (lane % 16 == 0) s.every[e * 2 + lane / 16] = every[e];
         }
-        if (lane == 0) s.every = every;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&n_full[in]);
+        if (lane == 0) mbar_arrive(&n_full[in.at]);
+        in.next(kInfo);
       }
       piece_done(seg);
     }
@@ -347,11 +440,14 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     long long left = start->left;
     int i = start->i, item = start->item, items = 0, length = 1;
     Extent x{};
+    auto fresh_of = [&] { return a.fresh ? a.fresh[i] : 0x7fffffff; };
+    int fresh = 0;
     if (left > 0) {
       x = paged_extent(a, i, false);
       mass_request(a, x, items, length);
+      fresh = fresh_of();
     }
-    bool more = true;
+    bool more = true, again = false;
     for (uint32_t seg = 0; more; ++seg) {
       const uint32_t pi = seg % kAhead;
       if (seg >= kAhead && !warp_wait(&piece_empty[pi], (seg / kAhead - 1) & 1, abort_flag)) break;
@@ -361,68 +457,60 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         if (++i >= a.B) { more = false; break; }
         x = paged_extent(a, i, false);
         mass_request(a, x, items, length);
+        fresh = fresh_of();
       }
+      const int per_head = more ? items / a.c.heads : 1, h = item / per_head, at = item - h * per_head;
+      const int key0 = at * kItemKeys, chunks = length - kItemLength;
+      // the chunk of the first row that sees a key
+      auto first_of = [&](int key) {
+        const long long t = a.right < 0 ? 0 : max(static_cast<long long>(key) - x.pos - a.right, 0ll);
+        return t < x.W ? static_cast<int>(t) / a.tokens : chunks;
+      };
+      const bool keep = more && chunks == 1 && at + 1 < per_head && left > length && first_of(key0 + kItemKeys) < 1;
       if (lane == 0) {
         MassPiece &p = pieces[pi];
         p.more = more;
         if (more) {
-          const int per_head = items / a.c.heads, h = item / per_head;
-          const int key0 = (item - h * per_head) * kItemKeys;
           p.x = x;
           p.i = i;
           p.h = h;
           p.key0 = key0;
+          p.fresh = fresh;
           p.tiles = x.L - key0 > kTile ? 2 : 1;
-          p.chunks = length - kItemLength;
-          // the first row that sees the item's first key
-          long long t = a.right < 0 ? 0 : static_cast<long long>(key0) - x.pos - a.right;
-          t = max(t, 0ll);
-          p.first = t < x.W ? static_cast<int>(t) / a.tokens : p.chunks;
+          p.chunks = chunks;
+          p.first = first_of(key0);
+          p.again = again;
+          p.keep = keep;
         }
         mbar_arrive(&piece_full[pi]);
       }
       __syncwarp();
+      again = keep;
       left -= length;
       ++item;
     }
   } else if (FP8 && warp >= 12) {
-    // --------------------------------------------------------------- K codes -> bf16
+    // --------------------------------------------------------------- query rows -> e4m3 parts
     if constexpr (FP8) {
-      const int key = (warp - 12) * 32 + lane;
       bool ok = true;
-      uint32_t n = 0;
+      Ring q, in;
       for (uint32_t seg = 0; ok; ++seg) {
         const MassPiece *p = piece(seg);
         if (!p) break;
-        const int tiles = p->first < p->chunks ? p->tiles : 0;
-        for (int j = 0; ok && j < tiles; ++j, ++n) {
-          const uint32_t st = n % kKSt, cs = n % kCSt;
-          ok = warp_wait(&k_full[st], (n / kKSt) & 1, abort_flag);
-          if (ok && n >= kCSt) ok = warp_wait(&c_empty[cs], (n / kCSt - 1) & 1, abort_flag);
+        const Extent x = p->x;
+        const int chunks = p->chunks, h = p->h;
+        for (int c = p->again ? chunks : p->first; ok && c < chunks; ++c) {
+          ok = warp_wait(&q_empty[q.at], q.round ^ 1, abort_flag) && warp_wait(&n_empty[in.at], in.round ^ 1, abort_flag);
           if (!ok) break;
-          const uint8_t *src = smem + st * C::kRaw + key * DH;
-          uint8_t *dst = smem + C::kOffConv + cs * C::kTileBytes + (key / 8) * C::kGroup8 + (key % 8) * 128;
-#pragma unroll
-          for (int c = 0; c < DH / 16; ++c) {   // under the load's swizzle (rows of 128 or 64 bytes)
-            const uint4 w = *reinterpret_cast<const uint4 *>(src + (DH == 128 ? c ^ (key & 7) : c ^ ((key >> 1) & 3)) * 16);
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-            uint32_t out[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint2 v = e4m3x4_to_bf16_0213(in[e]);
-              out[2 * e] = __byte_perm(v.x, v.y, 0x5410);
-              out[2 * e + 1] = __byte_perm(v.x, v.y, 0x7632);
-            }
-            uint8_t *d = dst + (c / 4) * 1024;   // 64 columns: eight 16-byte pieces
-            *reinterpret_cast<uint4 *>(d + (((2 * c) & 7) ^ (key & 7)) * 16) = make_uint4(out[0], out[1], out[2], out[3]);
-            *reinterpret_cast<uint4 *>(d + (((2 * c + 1) & 7) ^ (key & 7)) * 16) = make_uint4(out[4], out[5], out[6], out[7]);
-          }
+          stage_chunk<DH>(a, x, h, c, rows_at + q.at * a.q_bytes, numbers[in.at].scale, threadIdx.x - 384);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&c_full[cs]);
-            mbar_arrive(&k_empty[st]);
+            mbar_arrive(&q_full[q.at]);
+            mbar_arrive(&n_full[in.at]);
           }
+          q.next(kQSt);
+          in.next(kInfo);
         }
         piece_done(seg);
       }
@@ -433,46 +521,74 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     const int key = quarter * 32 + lane;
     const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * 256;
     bool ok = true;
-    uint32_t nq = 0, ns = 0;
-    for (uint32_t seg = 0; ok; ++seg) {
-      const MassPiece *p = piece(seg);
-      if (!p) break;
-      const int u = p->key0 + g * kTile + key, chunks = p->chunks - p->first;
-      const bool there = g < p->tiles;            // this group's tile
-      float c = a.scale_log2, old = 0.f;
-      int row = -1;
-      size_t at = 0;
-      if (u < p->x.L) {
-        row = page_row(a.c, p->i, u);
-        if (row < 0) {
-          atomicOr(a.status, DLLM_DEV_PAGE);
-        } else {
-          at = row + (static_cast<size_t>(p->h) << a.c.page_shift);
-          if (!(a.fresh && u >= a.fresh[p->i])) old = a.mass[at] * a.decay;
-          if constexpr (FP8) c *= scale_of(a.c.k_scale[at]);
-        }
+    Ring in;
+    uint32_t ns = 0;
+    // This thread's key of an item: its page is looked up two items ahead, what
+    // lies in its slot is loaded one item ahead, and both are first looked at an
+    // item later, so that their latency passes meanwhile.
+    auto look_up = [&](const MassPiece *p) {
+      const int u = p->key0 + g * kTile + key;
+      return u < p->x.L ? __ldg(a.c.table + static_cast<size_t>(p->i) * a.c.max_pages + (u >> a.c.page_shift)) : 0;
+    };
+    struct Slot {
+      size_t at;
+      bool there;
+      float old;
+      uint32_t scale;
+    };
+    auto load = [&](const MassPiece *p, int page) {
+      Slot s{0, false, 0.f, 0};
+      const int u = p->key0 + g * kTile + key;
+      if (u >= p->x.L) return s;
+      if (page < 0 || page >= a.c.num_pages) {
+        atomicOr(a.status, DLLM_DEV_PAGE);
+        return s;
       }
+      s.at = (static_cast<size_t>(page * a.c.heads + p->h) << a.c.page_shift) + (u & ((1 << a.c.page_shift) - 1));
+      s.there = true;
+      s.old = a.mass[s.at];
+      if constexpr (FP8) s.scale = a.c.k_scale[s.at];
+      return s;
+    };
+    const MassPiece *p = piece(0), *p1 = p ? piece(1) : nullptr;
+    int page1 = 0;
+    Slot slot{};
+    if (p) slot = load(p, look_up(p));
+    if (p1) page1 = look_up(p1);
+    for (uint32_t seg = 0; ok && p; ++seg) {
+      const MassPiece *p2 = p1 ? piece(seg + 2) : nullptr;
+      Slot slot1{};
+      int page2 = 0;
+      if (p1) slot1 = load(p1, page1);
+      if (p2) page2 = look_up(p2);
+      const int u = p->key0 + g * kTile + key, chunks = p->chunks, W = p->x.W;
+      const bool again = p->again, keep = p->keep;
+      const bool there = g < p->tiles;            // this group's tile
+      const float c = FP8 && slot.there ? a.scale_log2 * scale_of(slot.scale) : a.scale_log2;
       float sum = 0.f;
-      for (int k = 0; ok && k < chunks; ++k, ++nq) {
-        const uint32_t in = nq % kInfo;
-        ok = warp_wait(&n_full[in], (nq / kInfo) & 1, abort_flag);
+      for (int k = p->first; ok && k < chunks; ++k) {
+        if (!again) ok = warp_wait(&n_full[in.at], in.round, abort_flag);
         if (ok && there) {
           const uint32_t b = ns & 1;
           ok = warp_wait(&s_full[g * 2 + b], (ns / 2) & 1, abort_flag);
           if (ok) {
             tc_fence_after();
-            const Numbers &s = numbers[in];
-            const bool masked = p->key0 + (g + 1) * kTile > s.every;
-            float2 acc = make_float2(0.f, 0.f);
-            for (int c0 = 0; c0 < a.columns; c0 += 16) {
-              uint32_t x[16];
-              tmem_ld16(t_s + b * 128 + c0, x);
-              tmem_ld_wait();
+            const Numbers &s = numbers[in.at];
+            const int columns = chunk_columns(a, W, k), end = p->key0 + (g + 1) * kTile;
+            float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+            auto add = [&](const uint32_t (&x)[16], int c0) {
+              const bool masked = end > s.every[c0 / 16];
 #pragma unroll
               for (int e = 0; e < 16; e += 4) {
                 const float4 z = *reinterpret_cast<const float4 *>(&s.neg_lse[c0 + e]);
-                float2 y0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), make_float2(c, c), make_float2(z.x, z.y));
-                float2 y1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), make_float2(c, c), make_float2(z.z, z.w));
+                float2 f0 = make_float2(c, c), f1 = f0;
+                if constexpr (FP8) {     // the row's factor and the key's first: no product on the way overflows
+                  const float4 f = *reinterpret_cast<const float4 *>(&s.scale[c0 + e]);
+                  f0 = __fmul2_rn(f0, make_float2(f.x, f.y));
+                  f1 = __fmul2_rn(f1, make_float2(f.z, f.w));
+                }
+                float2 y0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f0, make_float2(z.x, z.y));
+                float2 y1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), f1, make_float2(z.z, z.w));
                 if (masked) {
                   const int4 hi = *reinterpret_cast<const int4 *>(&s.hi[c0 + e]);
                   if (u >= hi.x) y0.x = -INFINITY;
@@ -480,11 +596,25 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                   if (u >= hi.z) y1.x = -INFINITY;
                   if (u >= hi.w) y1.y = -INFINITY;
                 }
-                acc = __fadd2_rn(acc, make_float2(ex2_approx(y0.x), ex2_approx(y0.y)));
-                acc = __fadd2_rn(acc, make_float2(ex2_approx(y1.x), ex2_approx(y1.y)));
+                acc0 = __fadd2_rn(acc0, make_float2(ex2_approx(y0.x), ex2_approx(y0.y)));
+                acc1 = __fadd2_rn(acc1, make_float2(ex2_approx(y1.x), ex2_approx(y1.y)));
               }
+            };
+            // the next 16 columns are on their way while these are summed up
+            uint32_t x0[16], x1[16];
+            const uint32_t t = t_s + b * 128;
+            tmem_ld16(t, x0);
+            for (int c0 = 0; c0 < columns; c0 += 32) {
+              const bool second = c0 + 16 < columns;
+              tmem_ld_wait();
+              if (second) tmem_ld16(t + c0 + 16, x1);
+              add(x0, c0);
+              if (!second) break;
+              tmem_ld_wait();
+              if (c0 + 32 < columns) tmem_ld16(t + c0 + 32, x0);
+              add(x1, c0 + 16);
             }
-            sum += acc.x + acc.y;
+            sum += (acc0.x + acc0.y) + (acc1.x + acc1.y);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[g * 2 + b]);
@@ -492,10 +622,17 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&n_empty[in]);
+        if (!keep) {
+          if (lane == 0) mbar_arrive(&n_empty[in.at]);
+          in.next(kInfo);
+        }
       }
-      if (ok && row >= 0) a.mass[at] = old + sum;
+      if (ok && slot.there) a.mass[slot.at] = (u < p->fresh ? slot.old * a.decay : 0.f) + sum;
       piece_done(seg);
+      p = p1;
+      p1 = p2;
+      slot = slot1;
+      page1 = page2;
     }
   }
 
@@ -516,11 +653,15 @@ dllm_status launch_mass(const dllm_kv_pages *pages, MassArgs &g, cudaStream_t s)
   if (!make_tmap_page_rows(&tk, pages->k, rows, DH, FP8 ? 1 : 2, pages->page_size) ||
       !make_tmap_query_rows(&tq, g.q, g.q_rows, g.Hq, DH, g.q_stride, g.group, g.tokens))
     return DLLM_ERR_CUDA;
+  g.k_stages = C::stages(g.columns);
+  g.off_q = C::kOffK + g.k_stages * C::kRaw;
+  g.q_bytes = C::chunk_bytes(g.columns);
+  const int smem = g.off_q + C::kQSt * g.q_bytes + 1024;
   auto kern = mass_kernel<DH, FP8>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kMost + 1024);
   const long long items = static_cast<long long>(g.B) * pages->heads * ((g.max_kv + kItemKeys - 1) / kItemKeys);
   const int ctas = items < sm_budget() ? static_cast<int>(items) : sm_budget();
-  if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), C::kBytes, s, tk, tq, g);
+  if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), smem, s, tk, tq, g);
   return e == cudaSuccess ? launch_status() : cuda_error(e);
 }
 
