@@ -16,18 +16,22 @@
 // chunks and what every item costs, cut into equal stretches, one per CTA.
 //
 // Warp roles:
-//   warp 0      K tiles by TMA, one box per page
-//   warp 1      MMAs
-//   warp 2      lse and bounds of each chunk's rows, and (bf16 pages) the rows
-//               by TMA
+//   warp 0      K tiles by TMA, one box per page, and the slots' old values (and
+//               scales) by bulk copies, whole items ahead
+//   warps 1, 2  MMAs of the item's two tiles (one thread for both is short of
+//               time with few query rows: some 900 cycles a tile)
 //   warp 3      walks the CTA's items ahead of the others
 //   warps 4..11 two groups, one key per thread: exponentials and sums
-//   last four   (e4m3 pages) query rows in two e4m3 parts, as paged_attn.cu has
-//               them: K codes go to the tensor cores as they are, and the scores
-//               are those whose sum lse is. (Codes converted to bf16 by these
-//               warps: 2.1 k cycles a tile, the loads of a tile 0.7 k.)
+//   from 12 on  a chunk's query rows, their lse and bounds. bf16 pages: one warp,
+//               the rows by TMA. e4m3 pages: four warps, the rows in two e4m3
+//               parts as paged_attn.cu has them: K codes go to the tensor cores
+//               as they are, and the scores are those whose sum lse is. (Codes
+//               converted to bf16 instead: 2.1 k cycles a tile, the loads of a
+//               tile 0.7 k.)
 // Neighbouring items of a head whose rows are one chunk share it.
 #include <math.h>
+
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -49,8 +53,9 @@ struct MassArgs : PagedArgs {
 
 constexpr int kItemKeys = 2 * kTile;
 constexpr int kChunkRows = 128;
-constexpr int kAhead = 16;       // items prepared, the current one included: loads run ahead by whole items
+constexpr int kAhead = 16;       // items prepared, the current one included
 constexpr int kInfo = 3;         // chunks whose rows' numbers are prepared
+constexpr int kSlots = 6;        // items whose slots are loaded
 constexpr int kItemLength = 2;   // what an item costs beside its chunks, in chunks
 
 template <int DH, bool FP8>
@@ -59,9 +64,10 @@ struct MassCfg {
   static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);
   static constexpr int kQSt = 2;
   static constexpr int kMaxKSt = 12;
-  static constexpr int kOffK = 9216;                           // tiles, then chunks of query rows; before them what follows
+  static constexpr int kOffK = 15360;                          // tiles, then chunks of query rows; before them what follows
   static constexpr int kMost = 232448 - 1024;
-  static constexpr int kThreads = 32 * (12 + (FP8 ? 4 : 0));
+  static constexpr int kRowWarps = FP8 ? 4 : 1;
+  static constexpr int kThreads = 32 * (12 + kRowWarps);
   // Bytes of a chunk (bf16, or two e4m3 parts), and the tiles that fit beside kQSt chunks.
   static int chunk_bytes(int columns) { return columns * DH * 2; }
   static int stages(int columns) {
@@ -100,9 +106,16 @@ struct alignas(16) Numbers {   // of a chunk's query rows
   int every[kChunkRows / 16];  // keys before it are seen by all of 16
 };
 
+struct alignas(16) Slots { // of an item's keys
+  float old[kItemKeys];
+  uint8_t scale[kItemKeys];
+  int page[kItemKeys / 16];    // cache row of the head's first slot of each page, -1: no page
+};
+
 struct MassStart {
   long long left;          // length of the CTA's stretch from its first item on
   int i, item;
+  Extent x;
 };
 
 __device__ __forceinline__ void mass_request(const MassArgs &a, const Extent &x, int &items, int &length) {
@@ -138,12 +151,14 @@ __device__ __forceinline__ void mass_start(const MassArgs &a, long long *s_sum, 
   if (begin >= before && begin < before + mine) {
     long long at = before;
     for (int i = i0; i < i1; ++i) {
-      mass_request(a, paged_extent(a, i, false), items, length);
+      const Extent x = paged_extent(a, i, false);
+      mass_request(a, x, items, length);
       const long long m = static_cast<long long>(items) * length;
       if (begin < at + m) {
         const int item = static_cast<int>(quotient(begin - at + length - 1, length));
         s_start->i = i;
         s_start->item = item;
+        s_start->x = x;
         s_start->left = begin + per - (at + static_cast<long long>(item) * length);
         break;
       }
@@ -201,22 +216,43 @@ __device__ __forceinline__ void stage_chunk(const MassArgs &a, const Extent &x, 
   }
 }
 
+// -lse, bound and the share in `every` of row n of chunk c, by whole warps of
+// neighbouring rows.
+__device__ __forceinline__ void numbers_of(const MassArgs &a, const Extent &x, int h, int c, int n, float &neg_lse, int &hi, int &every) {
+  const int at = n / a.group, t = c * a.tokens + at;
+  hi = 0;
+  neg_lse = 0.f;
+  if (at < a.tokens && t < x.W) {
+    int lo;
+    const float lse = __ldg(&a.lse[static_cast<size_t>(x.q0 + t) * a.Hq + h * a.group + (n - at * a.group)]);
+    visible(a, x.pos, t, x.L, lo, hi);
+    if (lse == -INFINITY) hi = 0;
+    neg_lse = lse * -1.4426950408889634f;
+  }
+  every = hi;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) every = min(every, __shfl_xor_sync(0xffffffffu, every, o));
+}
+
 template <int DH, bool FP8>
 __global__ void __launch_bounds__(MassCfg<DH, FP8>::kThreads, 1)
 mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ MassArgs a) {
   using C = MassCfg<DH, FP8>;
-  constexpr int kQSt = C::kQSt, kTables = 6144;
+  constexpr int kQSt = C::kQSt, kTables = 13824;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Numbers *numbers = reinterpret_cast<Numbers *>(smem);                      // [kInfo]
-  MassPiece *pieces = reinterpret_cast<MassPiece *>(numbers + kInfo);        // [kAhead]
-  uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + kTables);              // [k_stages]
+  Slots *slots = reinterpret_cast<Slots *>(numbers + kInfo);                 // [kSlots]
+  MassPiece *pieces = reinterpret_cast<MassPiece *>(slots + kSlots);         // [kAhead]
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + kTables);           // [k_stages]
   uint64_t *k_empty = k_full + C::kMaxKSt;
-  uint64_t *q_full = k_empty + C::kMaxKSt;   // [kQSt]
+  uint64_t *q_full = k_empty + C::kMaxKSt; // [kQSt]
   uint64_t *q_empty = q_full + kQSt;
   uint64_t *n_full = q_empty + kQSt;       // [kInfo]
   uint64_t *n_empty = n_full + kInfo;
-  uint64_t *s_full = n_empty + kInfo;      // [group][2]
+  uint64_t *slot_full = n_empty + kInfo;   // [kSlots]
+  uint64_t *slot_empty = slot_full + kSlots;
+  uint64_t *s_full = slot_empty + kSlots;  // [group][2]
   uint64_t *s_empty = s_full + 4;
   uint64_t *piece_full = s_empty + 4;      // [kAhead]
   uint64_t *piece_empty = piece_full + kAhead;
@@ -224,25 +260,27 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   MassStart *start = reinterpret_cast<MassStart *>(s_sum + 16);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert(kInfo * sizeof(Numbers) + kAhead * sizeof(MassPiece) <= kTables, "tables");
-  static_assert(kTables + (2 * C::kMaxKSt + 2 * kQSt + 2 * kInfo + 8 + 2 * kAhead + 16) * 8 + sizeof(MassStart) + 8 <= C::kOffK, "barriers");
+  static_assert(kInfo * sizeof(Numbers) + kSlots * sizeof(Slots) + kAhead * sizeof(MassPiece) <= kTables && kTables % 16 == 0, "tables");
+  static_assert(kTables + (2 * C::kMaxKSt + 2 * kQSt + 2 * kInfo + 2 * kSlots + 8 + 2 * kAhead + 16) * 8 + sizeof(MassStart) + 8 <= C::kOffK,
+                "barriers");
   uint8_t *const tiles_at = smem + C::kOffK, *const rows_at = smem + a.off_q;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.k_stages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
-    for (int s = 0; s < kQSt; ++s) { mbar_init(&q_full[s], FP8 ? 4 : 1); mbar_init(&q_empty[s], 1); }
-    for (int s = 0; s < kInfo; ++s) { mbar_init(&n_full[s], FP8 ? 5 : 1); mbar_init(&n_empty[s], 8); }
+    for (int s = 0; s < kQSt; ++s) { mbar_init(&q_full[s], C::kRowWarps); mbar_init(&q_empty[s], 2); }
+    for (int s = 0; s < kInfo; ++s) { mbar_init(&n_full[s], C::kRowWarps); mbar_init(&n_empty[s], 8); }
+    for (int s = 0; s < kSlots; ++s) { mbar_init(&slot_full[s], 1); mbar_init(&slot_empty[s], 8); }
     for (int s = 0; s < 4; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], 4); }
     for (int s = 0; s < kAhead; ++s) {
       mbar_init(&piece_full[s], 1);
-      mbar_init(&piece_empty[s], 3 + 8 + (FP8 ? 4 : 0));   // the warps that read it
+      mbar_init(&piece_empty[s], 1 + 2 + 8 + C::kRowWarps);   // the warps that read it
     }
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_q);
+    if (!FP8) tma_prefetch_desc(&tm_q);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -269,35 +307,49 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   };
 
   if (warp == 0) {
-    // --------------------------------------------------------------- K tiles
-    // (an item's pages, one per lane, are looked up while the item before it
-    // waits for room)
+    // --------------------------------------------------------------- K tiles, slots
     const int page_rows = 1 << a.c.page_shift, per_tile = kTile >> a.c.page_shift;
     const int none = static_cast<int>((static_cast<long long>(a.c.num_pages) * a.c.heads << a.c.page_shift) / 8);
-    // this lane's page of the item, -1: none (not looked at before the item's turn)
+    // this lane's page of an item, looked up while the item before it waits for room
     auto look_up = [&](const MassPiece *p) {
       const int u = p->key0 + lane * page_rows;
-      if (lane >= 2 * per_tile || u >= p->x.L) return -1;
+      if (lane >= 2 * per_tile || u >= p->x.L) return 0;
       return __ldg(a.c.table + static_cast<size_t>(p->i) * a.c.max_pages + (u >> a.c.page_shift));
     };
     bool ok = true;
-    Ring k;
-    uint32_t n = 0;
+    Ring k, sl;
+    uint32_t n = 0, items = 0;
     const MassPiece *p = piece(0);
-    int page = p ? look_up(p) : -1;
+    int page = p ? look_up(p) : 0;
     for (uint32_t seg = 0; ok && p; ++seg) {
       const int tiles = p->first < p->chunks ? p->tiles : 0;
+      const bool mine = lane < 2 * per_tile, held = mine && p->key0 + lane * page_rows < p->x.L;
+      const bool bad = held && (page < 0 || page >= a.c.num_pages), live = held && !bad;
+      if (bad) atomicOr(a.status, DLLM_DEV_PAGE);
+      const int row = ((page * a.c.heads + p->h) << a.c.page_shift);
       const MassPiece *p_next = piece(seg + 1);
-      const int page_next = p_next ? look_up(p_next) : -1;
-      // 8-row group of the page; what there is none of reads as zeros
-      const int g = page >= 0 && page < a.c.num_pages ? ((page * a.c.heads + p->h) << a.c.page_shift) / 8 : none;
+      const int page_next = p_next ? look_up(p_next) : 0;
+      ok = warp_wait(&slot_empty[sl.at], sl.round ^ 1, abort_flag);
+      if (!ok) break;
+      Slots &s = slots[sl.at];
+      if (mine) s.page[lane] = live ? row : -1;
+      const int pages = __popc(__ballot_sync(0xffffffffu, live));
+      if (lane == 0) mbar_arrive_expect_tx(&slot_full[sl.at], pages * page_rows * (FP8 ? 5 : 4));
+      __syncwarp();
+      if (live) {
+        bulk_load(s.old + lane * page_rows, a.mass + row, page_rows * 4, &slot_full[sl.at]);
+        if constexpr (FP8) bulk_load(s.scale + lane * page_rows, a.c.k_scale + row, page_rows, &slot_full[sl.at]);
+      }
+      sl.next(kSlots);
+      ++items;
       for (int j = 0; ok && j < tiles; ++j) {
         ok = warp_wait(&k_empty[k.at], k.round ^ 1, abort_flag);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&k_full[k.at], C::kRaw);
         __syncwarp();
-        if (lane / per_tile == j)
-          tma_load_4d(tiles_at + k.at * C::kRaw + (lane - j * per_tile) * page_rows * (C::kRaw / kTile), &tm_k, &k_full[k.at], g);
+        if (lane / per_tile == j)      // (what there is none of reads as zeros)
+          tma_load_4d(tiles_at + k.at * C::kRaw + (lane - j * per_tile) * page_rows * (C::kRaw / kTile), &tm_k, &k_full[k.at],
+                      live ? row / 8 : none);
         k.next(a.k_stages);
         ++n;
       }
@@ -306,134 +358,72 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       page = page_next;
     }
     // after an abort the loads in flight land before the CTA's memory is given up
-    if (!ok || *abort_flag)
+    if (!ok || *abort_flag) {
       if (lane < a.k_stages && lane < n) mbar_drain(&k_full[lane], ((n - 1 - lane) / a.k_stages) & 1);
+      if (lane < kSlots && lane < items) mbar_drain(&slot_full[lane], ((items - 1 - lane) / kSlots) & 1);
+    }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp <= 2) {
     // --------------------------------------------------------------- MMAs
+    // (one elected thread through the whole loop: see paged_rows.cu)
+    const int j = warp - 1;         // the tile of the item, and the group that sums it up
     if (elect_one()) {
       bool ok = true;
       Ring t, q;                    // key tiles, chunks
-      uint32_t ns[2] = {0, 0};      // units of the groups
+      uint32_t ns = 0;              // units of the group
       for (uint32_t seg = 0; ok; ++seg) {
         const uint32_t pi = seg % kAhead;
         ok = mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
         if (!ok || !pieces[pi].more) break;
         const MassPiece &p = pieces[pi];
-        const int first = p.first, chunks = p.chunks, tiles = p.tiles, W = p.x.W;
-        const bool again = p.again, keep = p.keep;
-        Ring behind = t;            // the tile behind the item's
-        if (first < chunks)
-          for (int j = 0; j < tiles; ++j) behind.next(a.k_stages);
+        const int first = p.first, chunks = p.chunks, W = p.x.W;
+        const bool again = p.again, keep = p.keep, there = j < p.tiles;
+        Ring tile = t;
+        if (first < chunks) {
+          t.next(a.k_stages);
+          if (p.tiles > 1) t.next(a.k_stages);
+          if (j == 1) tile.next(a.k_stages);
+        }
+        const uint32_t sk = smem_u32(tiles_at + tile.at * C::kRaw);
         for (int c = first; ok && c < chunks; ++c) {
           if (!again) ok = mbar_wait(&q_full[q.at], q.round, abort_flag);
-          const int columns = chunk_columns(a, W, c);
-          const uint32_t sq = smem_u32(rows_at + q.at * a.q_bytes);
-          Ring tile = t;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (j >= tiles || !ok) break;
-            const uint32_t b = ns[j] & 1, t_s = tmem + (j * 2 + b) * 128;
+          if (ok && there) {
+            const uint32_t b = ns & 1, t_s = tmem + (j * 2 + b) * 128, sq = smem_u32(rows_at + q.at * a.q_bytes);
+            const int columns = chunk_columns(a, W, c);
             if (c == first) ok = mbar_wait(&k_full[tile.at], tile.round, abort_flag);
-            ok = ok && mbar_wait(&s_empty[j * 2 + b], (ns[j] / 2 & 1) ^ 1, abort_flag);
+            ok = ok && mbar_wait(&s_empty[j * 2 + b], (ns / 2 & 1) ^ 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sk = smem_u32(tiles_at + tile.at * C::kRaw);
             if constexpr (!FP8) {
+              const uint32_t idesc = idesc_bf16(128, columns, 0, 0);
               const uint64_t dk = sw128_desc(sk, 16, C::kGroup8), dq = sw128_desc(sq, 16, 1024);
 #pragma unroll
               for (int kk = 0; kk < DH / 16; ++kk)
                 umma_bf16(t_s, dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                          dq + (((kk >> 2) * (a.columns * 128) + (kk & 3) * 32) >> 4), idesc_bf16(128, columns, 0, 0), kk > 0);
+                          dq + (((kk >> 2) * (a.columns * 128) + (kk & 3) * 32) >> 4), idesc, kk > 0);
             } else {
+              const uint32_t idesc = idesc_f8(128, columns, kE4M3, kE4M3, 0, 0);
               const uint64_t dk = DH == 128 ? sw128_desc(sk, 16, C::kGroup8) : sw64_desc(sk, 16, C::kGroup8);
 #pragma unroll
               for (int part = 0; part < 2; ++part) {
                 const uint32_t sp = sq + part * a.columns * DH;
                 const uint64_t dq = DH == 128 ? sw128_desc(sp, 16, 8 * DH) : sw64_desc(sp, 16, 8 * DH);
 #pragma unroll
-                for (int kk = 0; kk < DH / 32; ++kk)
-                  umma_f8(t_s, dk + ((kk * 32) >> 4), dq + ((kk * 32) >> 4), idesc_f8(128, columns, kE4M3, kE4M3, 0, 0), part + kk > 0);
+                for (int kk = 0; kk < DH / 32; ++kk) umma_f8(t_s, dk + ((kk * 32) >> 4), dq + ((kk * 32) >> 4), idesc, part + kk > 0);
               }
             }
             umma_commit(&s_full[j * 2 + b]);
-            ++ns[j];
             if (c + 1 == chunks) umma_commit(&k_empty[tile.at]);
-            tile.next(a.k_stages);
+            ++ns;
           }
           if (!keep) {
             if (ok) umma_commit(&q_empty[q.at]);
             q.next(kQSt);
           }
         }
-        t = behind;
         mbar_arrive(&piece_empty[pi]);
       }
     }
-    __syncwarp();
-  } else if (warp == 2) {
-    // --------------------------------------------------------------- query rows' numbers, bf16 rows
-    const uint32_t bytes = static_cast<uint32_t>(a.tokens * a.group) * DH * 2;
-    bool ok = true;
-    Ring q, in;
-    uint32_t asked = 0;
-    for (uint32_t seg = 0; ok; ++seg) {
-      const MassPiece *p = piece(seg);
-      if (!p) break;
-      const Extent x = p->x;
-      const int chunks = p->chunks, h = p->h;
-      for (int c = p->again ? chunks : p->first; ok && c < chunks; ++c) {
-        if constexpr (!FP8) {
-          ok = warp_wait(&q_empty[q.at], q.round ^ 1, abort_flag);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&q_full[q.at], bytes);
-#pragma unroll
-            for (int d = 0; d < DH / 64; ++d)
-              tma_load_rows(rows_at + q.at * a.q_bytes + d * (a.columns * 128), &tm_q, &q_full[q.at], d * 64, h * a.group,
-                            x.q0 + c * a.tokens);
-          }
-          q.next(kQSt);
-          ++asked;
-          __syncwarp();
-        }
-        float lse[kChunkRows / 32];
-        int hi[kChunkRows / 32], every[kChunkRows / 32];
-#pragma unroll
-        for (int e = 0; e < kChunkRows / 32; ++e) {
-          const int r = e * 32 + lane, n = r / a.group, t = c * a.tokens + n;
-          hi[e] = 0;
-          lse[e] = 0.f;
-          if (n < a.tokens && t < x.W) {
-            int lo;
-            lse[e] = __ldg(&a.lse[static_cast<size_t>(x.q0 + t) * a.Hq + h * a.group + (r - n * a.group)]);
-            visible(a, x.pos, t, x.L, lo, hi[e]);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < kChunkRows / 32; ++e) {
-          if (lse[e] == -INFINITY) hi[e] = 0;
-          every[e] = hi[e];
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) every[e] = min(every[e], __shfl_xor_sync(0xffffffffu, every[e], o));
-        }
-        ok = warp_wait(&n_empty[in.at], in.round ^ 1, abort_flag);
-        if (!ok) break;
-        Numbers &s = numbers[in.at];
-#pragma unroll
-        for (int e = 0; e < kChunkRows / 32; ++e) {
-          s.neg_lse[e * 32 + lane] = lse[e] * -1.4426950408889634f;
-          s.hi[e * 32 + lane] = hi[e];
-          if (lane % 16 == 0) s.every[e * 2 + lane / 16] = every[e];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&n_full[in.at]);
-        in.next(kInfo);
-      }
-      piece_done(seg);
-    }
-    if (!ok || *abort_flag)
-      if (lane < kQSt && lane < asked) mbar_drain(&q_full[lane], ((asked - 1 - lane) / kQSt) & 1);
     __syncwarp();
   } else if (warp == 3) {
     // --------------------------------------------------------------- items
@@ -443,7 +433,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     auto fresh_of = [&] { return a.fresh ? a.fresh[i] : 0x7fffffff; };
     int fresh = 0;
     if (left > 0) {
-      x = paged_extent(a, i, false);
+      x = start->x;
       mass_request(a, x, items, length);
       fresh = fresh_of();
     }
@@ -489,82 +479,82 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       left -= length;
       ++item;
     }
-  } else if (FP8 && warp >= 12) {
-    // --------------------------------------------------------------- query rows -> e4m3 parts
-    if constexpr (FP8) {
-      bool ok = true;
-      Ring q, in;
-      for (uint32_t seg = 0; ok; ++seg) {
-        const MassPiece *p = piece(seg);
-        if (!p) break;
-        const Extent x = p->x;
-        const int chunks = p->chunks, h = p->h;
-        for (int c = p->again ? chunks : p->first; ok && c < chunks; ++c) {
-          ok = warp_wait(&q_empty[q.at], q.round ^ 1, abort_flag) && warp_wait(&n_empty[in.at], in.round ^ 1, abort_flag);
-          if (!ok) break;
-          stage_chunk<DH>(a, x, h, c, rows_at + q.at * a.q_bytes, numbers[in.at].scale, threadIdx.x - 384);
-          fence_proxy_async_smem();
-          __syncwarp();
+  } else if (warp >= 12) {
+    // --------------------------------------------------------------- query rows and their numbers
+    bool ok = true;
+    Ring q, in;
+    uint32_t asked = 0;
+    for (uint32_t seg = 0; ok; ++seg) {
+      const MassPiece *p = piece(seg);
+      if (!p) break;
+      const Extent x = p->x;
+      const int chunks = p->chunks, h = p->h;
+      for (int c = p->again ? chunks : p->first; ok && c < chunks; ++c) {
+        ok = warp_wait(&q_empty[q.at], q.round ^ 1, abort_flag);
+        if (!ok) break;
+        constexpr int kMine = kChunkRows / 32 / C::kRowWarps;   // rows of a lane
+        const int n0 = (warp - 12) * 32 + lane;
+        if constexpr (!FP8) {
           if (lane == 0) {
-            mbar_arrive(&q_full[q.at]);
-            mbar_arrive(&n_full[in.at]);
+            mbar_arrive_expect_tx(&q_full[q.at], a.tokens * a.group * (DH * 2));
+#pragma unroll
+            for (int d = 0; d < DH / 64; ++d)
+              tma_load_rows(rows_at + q.at * a.q_bytes + d * (a.columns * 128), &tm_q, &q_full[q.at], d * 64, h * a.group,
+                            x.q0 + c * a.tokens);
           }
-          q.next(kQSt);
-          in.next(kInfo);
+          ++asked;
+          __syncwarp();
         }
-        piece_done(seg);
+        float neg_lse[kMine];
+        int hi[kMine], every[kMine];
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) numbers_of(a, x, h, c, e * 32 + n0, neg_lse[e], hi[e], every[e]);
+        ok = warp_wait(&n_empty[in.at], in.round ^ 1, abort_flag);
+        if (!ok) break;
+        Numbers &s = numbers[in.at];
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) {
+          const int n = e * 32 + n0;
+          s.neg_lse[n] = neg_lse[e];
+          s.hi[n] = hi[e];
+          if (n % 16 == 0) s.every[n / 16] = every[e];
+        }
+        if constexpr (FP8) {
+          stage_chunk<DH>(a, x, h, c, rows_at + q.at * a.q_bytes, s.scale, n0);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&n_full[in.at]);
+          if (FP8) mbar_arrive(&q_full[q.at]);
+        }
+        q.next(kQSt);
+        in.next(kInfo);
       }
+      piece_done(seg);
     }
+    if (!FP8 && (!ok || *abort_flag))
+      if (lane < kQSt && lane < asked) mbar_drain(&q_full[lane], ((asked - 1 - lane) / kQSt) & 1);
+    __syncwarp();
   } else {
     // --------------------------------------------------------------- exponentials and sums
     const int g = (warp - 4) >> 2, quarter = warp & 3;
-    const int key = quarter * 32 + lane;
+    const int key = g * kTile + quarter * 32 + lane;      // of the item
     const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * 256;
     bool ok = true;
-    Ring in;
+    Ring in, sl;
     uint32_t ns = 0;
-    // This thread's key of an item: its page is looked up two items ahead, what
-    // lies in its slot is loaded one item ahead, and both are first looked at an
-    // item later, so that their latency passes meanwhile.
-    auto look_up = [&](const MassPiece *p) {
-      const int u = p->key0 + g * kTile + key;
-      return u < p->x.L ? __ldg(a.c.table + static_cast<size_t>(p->i) * a.c.max_pages + (u >> a.c.page_shift)) : 0;
-    };
-    struct Slot {
-      size_t at;
-      bool there;
-      float old;
-      uint32_t scale;
-    };
-    auto load = [&](const MassPiece *p, int page) {
-      Slot s{0, false, 0.f, 0};
-      const int u = p->key0 + g * kTile + key;
-      if (u >= p->x.L) return s;
-      if (page < 0 || page >= a.c.num_pages) {
-        atomicOr(a.status, DLLM_DEV_PAGE);
-        return s;
-      }
-      s.at = (static_cast<size_t>(page * a.c.heads + p->h) << a.c.page_shift) + (u & ((1 << a.c.page_shift) - 1));
-      s.there = true;
-      s.old = a.mass[s.at];
-      if constexpr (FP8) s.scale = a.c.k_scale[s.at];
-      return s;
-    };
-    const MassPiece *p = piece(0), *p1 = p ? piece(1) : nullptr;
-    int page1 = 0;
-    Slot slot{};
-    if (p) slot = load(p, look_up(p));
-    if (p1) page1 = look_up(p1);
-    for (uint32_t seg = 0; ok && p; ++seg) {
-      const MassPiece *p2 = p1 ? piece(seg + 2) : nullptr;
-      Slot slot1{};
-      int page2 = 0;
-      if (p1) slot1 = load(p1, page1);
-      if (p2) page2 = look_up(p2);
-      const int u = p->key0 + g * kTile + key, chunks = p->chunks, W = p->x.W;
-      const bool again = p->again, keep = p->keep;
-      const bool there = g < p->tiles;            // this group's tile
-      const float c = FP8 && slot.there ? a.scale_log2 * scale_of(slot.scale) : a.scale_log2;
+    for (uint32_t seg = 0; ok; ++seg) {
+      const MassPiece *p = piece(seg);
+      if (!p) break;
+      ok = warp_wait(&slot_full[sl.at], sl.round, abort_flag);
+      if (!ok) break;
+      const int u = p->key0 + key, chunks = p->chunks, W = p->x.W, end = p->key0 + (g + 1) * kTile;
+      const bool again = p->again, keep = p->keep, there = g < p->tiles;     // (this group's tile)
+      const Slots &slot = slots[sl.at];
+      const int page = slot.page[key >> a.c.page_shift];
+      const bool live = u < p->x.L && page >= 0;
+      const float c = FP8 && live ? a.scale_log2 * scale_of(slot.scale[key]) : a.scale_log2;
       float sum = 0.f;
       for (int k = p->first; ok && k < chunks; ++k) {
         if (!again) ok = warp_wait(&n_full[in.at], in.round, abort_flag);
@@ -574,10 +564,9 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           if (ok) {
             tc_fence_after();
             const Numbers &s = numbers[in.at];
-            const int columns = chunk_columns(a, W, k), end = p->key0 + (g + 1) * kTile;
+            const int columns = chunk_columns(a, W, k);
             float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
-            auto add = [&](const uint32_t (&x)[16], int c0) {
-              const bool masked = end > s.every[c0 / 16];
+            auto add_some = [&](const uint32_t (&x)[16], int c0, auto masked) {
 #pragma unroll
               for (int e = 0; e < 16; e += 4) {
                 const float4 z = *reinterpret_cast<const float4 *>(&s.neg_lse[c0 + e]);
@@ -589,7 +578,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 }
                 float2 y0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f0, make_float2(z.x, z.y));
                 float2 y1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), f1, make_float2(z.z, z.w));
-                if (masked) {
+                if constexpr (decltype(masked)::value) {
                   const int4 hi = *reinterpret_cast<const int4 *>(&s.hi[c0 + e]);
                   if (u >= hi.x) y0.x = -INFINITY;
                   if (u >= hi.y) y0.y = -INFINITY;
@@ -599,6 +588,11 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 acc0 = __fadd2_rn(acc0, make_float2(ex2_approx(y0.x), ex2_approx(y0.y)));
                 acc1 = __fadd2_rn(acc1, make_float2(ex2_approx(y1.x), ex2_approx(y1.y)));
               }
+            };
+            // (a branch: as selects under a condition the comparisons are all computed)
+            auto add = [&](const uint32_t (&x)[16], int c0) {
+              if (end > s.every[c0 / 16]) add_some(x, c0, std::true_type{});
+              else add_some(x, c0, std::false_type{});
             };
             // the next 16 columns are on their way while these are summed up
             uint32_t x0[16], x1[16];
@@ -627,12 +621,12 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           in.next(kInfo);
         }
       }
-      if (ok && slot.there) a.mass[slot.at] = (u < p->fresh ? slot.old * a.decay : 0.f) + sum;
+      if (ok && live)
+        a.mass[static_cast<size_t>(page) + (key & ((1 << a.c.page_shift) - 1))] = (u < p->fresh ? slot.old[key] * a.decay : 0.f) + sum;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&slot_empty[sl.at]);
+      sl.next(kSlots);
       piece_done(seg);
-      p = p1;
-      p1 = p2;
-      slot = slot1;
-      page1 = page2;
     }
   }
 
@@ -683,7 +677,7 @@ extern "C" dllm_status dllm_attn_mass(const dllm_kv_pages *pages, const dllm_att
   const dllm_status sp = check_page_pointers(pages);
   if (sp != DLLM_OK) return sp;
   if (!a->q || !a->lse || !a->mass || !a->q_off || !a->kv_len || !a->page_table) return DLLM_ERR_INVALID_ARG;
-  if (!aligned16(a->q) || a->q_stride < static_cast<long long>(a->Hq) * pages->dh || a->q_stride % 8) return DLLM_ERR_INVALID_ARG;
+  if (!aligned16(a->q) || !aligned16(a->mass) || a->q_stride < static_cast<long long>(a->Hq) * pages->dh || a->q_stride % 8) return DLLM_ERR_INVALID_ARG;
   MassArgs g{};
   g.c = device_pages(pages, a->page_table, a->max_pages);
   g.q = a->q; g.q_stride = a->q_stride; g.lse = const_cast<float *>(a->lse);

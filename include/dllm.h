@@ -662,8 +662,8 @@ dllm_status dllm_tree_attn(const dllm_kv_pages *pages /* host */,
  *   position p >= u - right (right < 0: all), p as in dllm_paged_attn. With the
  *   lse that dllm_paged_attn returned for these rows the terms are the
  *   attention's weights; a row with lse = -infinity (it saw no key) adds nothing.
- *   mass     float [num_pages][heads][page_size], as the scales lie. Slots of
- *            other positions keep their values.
+ *   mass     float [num_pages][heads][page_size], as the scales lie, 16-byte
+ *            aligned. Slots of other positions keep their values.
  *   fresh    int32 [B] or NULL: positions u >= fresh[i] start from 0, whatever
  *            their slots hold (rows written since the last step); NULL: none
  *   decay    finite; 1 sums up, 0 keeps the last step's weights only (a slot
@@ -671,7 +671,8 @@ dllm_status dllm_tree_attn(const dllm_kv_pages *pages /* host */,
  *   lse      float [q_rows][Hq]; the others as in dllm_paged_attn. What is
  *            beyond max_q, max_kv, q_rows or the table is not processed
  *            (DLLM_DEV_OFFSETS), nor a page id that is none (DLLM_DEV_PAGE).
- * Sums are fp32, in an order that the shapes alone decide: the same call on the
+ * Scores are as exact as dllm_paged_attn's, with e4m3 pages too. Sums are fp32,
+ * in an order that the shapes alone decide: the same call on the
  * same GPU gives the same bits. A slot that two requests or two positions share
  * ends with either's value. Sizes as dllm_paged_attn. No workspace.
  * ------------------------------------------------------------------- */

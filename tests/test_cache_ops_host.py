@@ -124,7 +124,7 @@ def test_mass_refuses_bad_arguments():
     for name in ("q", "lse", "mass", "q_off", "kv_len", "page_table"):
         assert _mass(**{name: None}) == 1
     assert _mass(Hq=0) == 1 and _mass(Hq=3) == 2 and _mass(Hq=130, q_stride=130 * 64) == 2 and _mass(B=4097) == 2
-    assert _mass(q=FAKE + 8) == 1 and _mass(q_stride=248) == 1 and _mass(q_stride=260) == 1
+    assert _mass(q=FAKE + 8) == 1 and _mass(mass=FAKE + 4) == 1 and _mass(q_stride=248) == 1 and _mass(q_stride=260) == 1
     for name in ("right", "max_kv"):
         assert _mass(**{name: 1 << 30}) == 2
     assert _mass(q_rows=1 << 28) == 2 and _mass(max_q=1 << 28) == 2
