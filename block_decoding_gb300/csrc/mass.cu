@@ -10,24 +10,23 @@
 // that the shapes decide. The key's scale, slot and visibility are scalars of
 // its thread; lse and the bound of every query row come from shared memory.
 //
-// An item is two key tiles (256 rows) of one request and cached head, one for
-// each of two epilogue warpgroups; query rows pass by in chunks of up to 128,
-// each read once for both tiles. The items form one line, each as long as its
+// An item is four key tiles (512 rows) of one request and cached head, one for
+// each of four epilogue warpgroups; query rows pass by in chunks of up to 128,
+// each read once for all tiles. The items form one line, each as long as its
 // chunks and what every item costs, cut into equal stretches, one per CTA.
 //
 // Warp roles:
-//   warp 0      K tiles by TMA, one box per page, and the slots' old values (and
-//               scales) by bulk copies, whole items ahead
-//   warps 1, 2  MMAs of the item's two tiles (one thread for both is short of
-//               time with few query rows: some 900 cycles a tile)
-//   warp 3      walks the CTA's items ahead of the others
-//   warps 4..11 two groups, one key per thread: exponentials and sums
-//   from 12 on  a chunk's query rows, their lse and bounds. bf16 pages: one warp,
-//               the rows by TMA. e4m3 pages: four warps, the rows in two e4m3
-//               parts as paged_attn.cu has them: K codes go to the tensor cores
-//               as they are, and the scores are those whose sum lse is. (Codes
-//               converted to bf16 instead: 2.1 k cycles a tile, the loads of a
-//               tile 0.7 k.)
+//   warp 0        K tiles by TMA, one box per page, two tiles to a stage, and the
+//                 slots' old values (and scales) by bulk copies, whole items ahead
+//   warps 1, 2    MMAs, of every other tile (one thread for all is short of time
+//                 with few query rows: some 900 cycles a tile)
+//   warp 3        walks the CTA's items ahead of the others
+//   warps 4..7    a chunk's query rows, their lse and bounds. bf16 pages: the rows
+//                 by TMA. e4m3 pages: in two e4m3 parts as paged_attn.cu has them:
+//                 K codes go to the tensor cores as they are, and the scores are
+//                 those whose sum lse is. (Codes converted to bf16 instead: 2.1 k
+//                 cycles a tile, the loads of a tile 0.7 k.)
+//   warps 8..23   four groups, one key per thread: exponentials and sums
 // Neighbouring items of a head whose rows are one chunk share it.
 #include <math.h>
 
@@ -51,30 +50,35 @@ struct MassArgs : PagedArgs {
   int off_q, q_bytes;
 };
 
-constexpr int kItemKeys = 2 * kTile;
+constexpr int kGroups = 4;       // epilogue warpgroups, and key tiles of an item
+constexpr int kItemKeys = kGroups * kTile;
 constexpr int kChunkRows = 128;
-constexpr int kAhead = 16;       // items prepared, the current one included
+constexpr int kAhead = 8;        // items prepared, the current one included
 constexpr int kInfo = 3;         // chunks whose rows' numbers are prepared
-constexpr int kSlots = 6;        // items whose slots are loaded
+constexpr int kSlots = 4;        // items whose slots are loaded
 constexpr int kItemLength = 2;   // what an item costs beside its chunks, in chunks
 
 template <int DH, bool FP8>
 struct MassCfg {
-  static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);      // a K tile as it is loaded
+  static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);      // a K tile
+  static constexpr int kStage = 2 * kRaw;
   static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);
   static constexpr int kQSt = 2;
-  static constexpr int kMaxKSt = 12;
-  static constexpr int kOffK = 15360;                          // tiles, then chunks of query rows; before them what follows
+  static constexpr int kMaxKSt = 6;
+  static constexpr int kOffK = 17408;                          // tiles, then chunks of query rows; before them what follows
   static constexpr int kMost = 232448 - 1024;
-  static constexpr int kRowWarps = FP8 ? 4 : 1;
-  static constexpr int kThreads = 32 * (12 + kRowWarps);
-  // Bytes of a chunk (bf16, or two e4m3 parts), and the tiles that fit beside kQSt chunks.
+  static constexpr int kThreads = 32 * (8 + 4 * kGroups);
+  // registers a thread: what the loading and MMA warps do not need goes to the
+  // groups (the sum is the launch's)
+  static constexpr int kRegsIssue = 56, kRegsRows = 72, kRegsSum = 88;
+  static_assert(kRegsIssue + kRegsRows + kGroups * kRegsSum <= (2 + kGroups) * 80, "registers");
+  // Bytes of a chunk (bf16, or two e4m3 parts), and the stages that fit beside kQSt chunks.
   static int chunk_bytes(int columns) { return columns * DH * 2; }
   static int stages(int columns) {
-    const int fit = (kMost - kOffK - kQSt * chunk_bytes(columns)) / kRaw;
+    const int fit = (kMost - kOffK - kQSt * chunk_bytes(columns)) / kStage;
     return fit < kMaxKSt ? fit : kMaxKSt;
   }
-  static_assert((kMost - kOffK - kQSt * 128 * DH * 2) / kRaw >= 2, "shared memory");
+  static_assert((kMost - kOffK - kQSt * 128 * DH * 2) / kStage >= 2, "shared memory");
 };
 
 // A place in a ring of n and the parity of its round: `full` barriers complete
@@ -95,7 +99,7 @@ struct MassPiece {
   int fresh;               // positions from here on start from 0
   int first, chunks;       // chunks [first, chunks) hold rows that see a key of the item
   int again, keep;         // the chunk is the last item's, is the next one's too
-  int tiles;               // key tiles (1 or 2)
+  int tiles;               // key tiles (1 to 4)
   int more;
 };
 
@@ -238,7 +242,7 @@ template <int DH, bool FP8>
 __global__ void __launch_bounds__(MassCfg<DH, FP8>::kThreads, 1)
 mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ MassArgs a) {
   using C = MassCfg<DH, FP8>;
-  constexpr int kQSt = C::kQSt, kTables = 13824;
+  constexpr int kQSt = C::kQSt, kTables = 16128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Numbers *numbers = reinterpret_cast<Numbers *>(smem);                      // [kInfo]
@@ -253,29 +257,29 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   uint64_t *slot_full = n_empty + kInfo;   // [kSlots]
   uint64_t *slot_empty = slot_full + kSlots;
   uint64_t *s_full = slot_empty + kSlots;  // [group][2]
-  uint64_t *s_empty = s_full + 4;
-  uint64_t *piece_full = s_empty + 4;      // [kAhead]
+  uint64_t *s_empty = s_full + 2 * kGroups;
+  uint64_t *piece_full = s_empty + 2 * kGroups;   // [kAhead]
   uint64_t *piece_empty = piece_full + kAhead;
-  long long *s_sum = reinterpret_cast<long long *>(piece_empty + kAhead);    // [16]
-  MassStart *start = reinterpret_cast<MassStart *>(s_sum + 16);
+  long long *s_sum = reinterpret_cast<long long *>(piece_empty + kAhead);    // [24]
+  MassStart *start = reinterpret_cast<MassStart *>(s_sum + 24);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   static_assert(kInfo * sizeof(Numbers) + kSlots * sizeof(Slots) + kAhead * sizeof(MassPiece) <= kTables && kTables % 16 == 0, "tables");
-  static_assert(kTables + (2 * C::kMaxKSt + 2 * kQSt + 2 * kInfo + 2 * kSlots + 8 + 2 * kAhead + 16) * 8 + sizeof(MassStart) + 8 <= C::kOffK,
+  static_assert(kTables + (2 * C::kMaxKSt + 2 * kQSt + 2 * kInfo + 2 * kSlots + 4 * kGroups + 2 * kAhead + 24) * 8 + sizeof(MassStart) + 8 <= C::kOffK,
                 "barriers");
   uint8_t *const tiles_at = smem + C::kOffK, *const rows_at = smem + a.off_q;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.k_stages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
-    for (int s = 0; s < kQSt; ++s) { mbar_init(&q_full[s], C::kRowWarps); mbar_init(&q_empty[s], 2); }
-    for (int s = 0; s < kInfo; ++s) { mbar_init(&n_full[s], C::kRowWarps); mbar_init(&n_empty[s], 8); }
-    for (int s = 0; s < kSlots; ++s) { mbar_init(&slot_full[s], 1); mbar_init(&slot_empty[s], 8); }
-    for (int s = 0; s < 4; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], 4); }
+    for (int s = 0; s < a.k_stages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 2); }
+    for (int s = 0; s < kQSt; ++s) { mbar_init(&q_full[s], FP8 ? 4 : 1); mbar_init(&q_empty[s], 2); }
+    for (int s = 0; s < kInfo; ++s) { mbar_init(&n_full[s], 4); mbar_init(&n_empty[s], 4 * kGroups); }
+    for (int s = 0; s < kSlots; ++s) { mbar_init(&slot_full[s], 1); mbar_init(&slot_empty[s], 4 * kGroups); }
+    for (int s = 0; s < 2 * kGroups; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], 4); }
     for (int s = 0; s < kAhead; ++s) {
       mbar_init(&piece_full[s], 1);
-      mbar_init(&piece_empty[s], 1 + 2 + 8 + C::kRowWarps);   // the warps that read it
+      mbar_init(&piece_empty[s], 1 + 2 + 4 + 4 * kGroups);   // the warps that read it
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -293,6 +297,9 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 
   pdl_wait();   // everything that is read may come from the previous kernel
   mass_start(a, s_sum, start);
+
+  // scores of a group: two buffers of up to 64 columns, or one
+  const bool two = a.columns <= 64;
 
   // The item of number `seg`, or null when there is none (or a wait gave up:
   // then the slot is not read). By a whole warp.
@@ -313,7 +320,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     // this lane's page of an item, looked up while the item before it waits for room
     auto look_up = [&](const MassPiece *p) {
       const int u = p->key0 + lane * page_rows;
-      if (lane >= 2 * per_tile || u >= p->x.L) return 0;
+      if (lane >= kGroups * per_tile || u >= p->x.L) return 0;
       return __ldg(a.c.table + static_cast<size_t>(p->i) * a.c.max_pages + (u >> a.c.page_shift));
     };
     bool ok = true;
@@ -323,7 +330,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     int page = p ? look_up(p) : 0;
     for (uint32_t seg = 0; ok && p; ++seg) {
       const int tiles = p->first < p->chunks ? p->tiles : 0;
-      const bool mine = lane < 2 * per_tile, held = mine && p->key0 + lane * page_rows < p->x.L;
+      const bool mine = lane < kGroups * per_tile, held = mine && p->key0 + lane * page_rows < p->x.L;
       const bool bad = held && (page < 0 || page >= a.c.num_pages), live = held && !bad;
       if (bad) atomicOr(a.status, DLLM_DEV_PAGE);
       const int row = ((page * a.c.heads + p->h) << a.c.page_shift);
@@ -342,14 +349,14 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       }
       sl.next(kSlots);
       ++items;
-      for (int j = 0; ok && j < tiles; ++j) {
+      for (int j = 0; ok && j < tiles; j += 2) {
         ok = warp_wait(&k_empty[k.at], k.round ^ 1, abort_flag);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&k_full[k.at], C::kRaw);
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[k.at], C::kStage);
         __syncwarp();
-        if (lane / per_tile == j)      // (what there is none of reads as zeros)
-          tma_load_4d(tiles_at + k.at * C::kRaw + (lane - j * per_tile) * page_rows * (C::kRaw / kTile), &tm_k, &k_full[k.at],
-                      live ? row / 8 : none);
+        const int at = lane - j * per_tile;
+        if (at >= 0 && at < 2 * per_tile)      // (what there is none of reads as zeros)
+          tma_load_4d(tiles_at + k.at * C::kStage + at * page_rows * (C::kRaw / kTile), &tm_k, &k_full[k.at], live ? row / 8 : none);
         k.next(a.k_stages);
         ++n;
       }
@@ -366,60 +373,66 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   } else if (warp <= 2) {
     // --------------------------------------------------------------- MMAs
     // (one elected thread through the whole loop: see paged_rows.cu)
-    const int j = warp - 1;         // the tile of the item, and the group that sums it up
+    const int j = warp - 1;         // tiles j and j + 2 of the item: those of a stage's two
     if (elect_one()) {
       bool ok = true;
-      Ring t, q;                    // key tiles, chunks
-      uint32_t ns = 0;              // units of the group
+      Ring t, q;                    // stages, chunks
+      uint32_t ns[2] = {0, 0};      // units of the two groups
       for (uint32_t seg = 0; ok; ++seg) {
         const uint32_t pi = seg % kAhead;
         ok = mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
         if (!ok || !pieces[pi].more) break;
         const MassPiece &p = pieces[pi];
-        const int first = p.first, chunks = p.chunks, W = p.x.W;
-        const bool again = p.again, keep = p.keep, there = j < p.tiles;
-        Ring tile = t;
-        if (first < chunks) {
-          t.next(a.k_stages);
-          if (p.tiles > 1) t.next(a.k_stages);
-          if (j == 1) tile.next(a.k_stages);
-        }
-        const uint32_t sk = smem_u32(tiles_at + tile.at * C::kRaw);
+        const int first = p.first, chunks = p.chunks, W = p.x.W, tiles = p.tiles;
+        const bool again = p.again, keep = p.keep;
         for (int c = first; ok && c < chunks; ++c) {
           if (!again) ok = mbar_wait(&q_full[q.at], q.round, abort_flag);
-          if (ok && there) {
-            const uint32_t b = ns & 1, t_s = tmem + (j * 2 + b) * 128, sq = smem_u32(rows_at + q.at * a.q_bytes);
-            const int columns = chunk_columns(a, W, c);
-            if (c == first) ok = mbar_wait(&k_full[tile.at], tile.round, abort_flag);
-            ok = ok && mbar_wait(&s_empty[j * 2 + b], (ns / 2 & 1) ^ 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            if constexpr (!FP8) {
-              const uint32_t idesc = idesc_bf16(128, columns, 0, 0);
-              const uint64_t dk = sw128_desc(sk, 16, C::kGroup8), dq = sw128_desc(sq, 16, 1024);
+          const uint32_t sq = smem_u32(rows_at + q.at * a.q_bytes);
+          const int columns = chunk_columns(a, W, c);
+          Ring stage = t;
 #pragma unroll
-              for (int kk = 0; kk < DH / 16; ++kk)
-                umma_bf16(t_s, dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                          dq + (((kk >> 2) * (a.columns * 128) + (kk & 3) * 32) >> 4), idesc, kk > 0);
-            } else {
-              const uint32_t idesc = idesc_f8(128, columns, kE4M3, kE4M3, 0, 0);
-              const uint64_t dk = DH == 128 ? sw128_desc(sk, 16, C::kGroup8) : sw64_desc(sk, 16, C::kGroup8);
+          for (int s = 0; s < 2; ++s) {
+            if (2 * s >= tiles || !ok) break;
+            const int tile = 2 * s + j;
+            if (c == first) ok = mbar_wait(&k_full[stage.at], stage.round, abort_flag);
+            if (ok && tile < tiles) {
+              const uint32_t b = two ? ns[s] & 1 : 0, t_s = tmem + tile * 128 + b * 64;
+              ok = mbar_wait(&s_empty[tile * 2 + b], ((two ? ns[s] / 2 : ns[s]) & 1) ^ 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t sk = smem_u32(tiles_at + stage.at * C::kStage + j * C::kRaw);
+              if constexpr (!FP8) {
+                const uint32_t idesc = idesc_bf16(128, columns, 0, 0);
+                const uint64_t dk = sw128_desc(sk, 16, C::kGroup8), dq = sw128_desc(sq, 16, 1024);
 #pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                const uint32_t sp = sq + part * a.columns * DH;
-                const uint64_t dq = DH == 128 ? sw128_desc(sp, 16, 8 * DH) : sw64_desc(sp, 16, 8 * DH);
+                for (int kk = 0; kk < DH / 16; ++kk)
+                  umma_bf16(t_s, dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                            dq + (((kk >> 2) * (a.columns * 128) + (kk & 3) * 32) >> 4), idesc, kk > 0);
+              } else {
+                const uint32_t idesc = idesc_f8(128, columns, kE4M3, kE4M3, 0, 0);
+                const uint64_t dk = DH == 128 ? sw128_desc(sk, 16, C::kGroup8) : sw64_desc(sk, 16, C::kGroup8);
 #pragma unroll
-                for (int kk = 0; kk < DH / 32; ++kk) umma_f8(t_s, dk + ((kk * 32) >> 4), dq + ((kk * 32) >> 4), idesc, part + kk > 0);
+                for (int part = 0; part < 2; ++part) {
+                  const uint32_t sp = sq + part * a.columns * DH;
+                  const uint64_t dq = DH == 128 ? sw128_desc(sp, 16, 8 * DH) : sw64_desc(sp, 16, 8 * DH);
+#pragma unroll
+                  for (int kk = 0; kk < DH / 32; ++kk) umma_f8(t_s, dk + ((kk * 32) >> 4), dq + ((kk * 32) >> 4), idesc, part + kk > 0);
+                }
               }
+              umma_commit(&s_full[tile * 2 + b]);
+              ++ns[s];
             }
-            umma_commit(&s_full[j * 2 + b]);
-            if (c + 1 == chunks) umma_commit(&k_empty[tile.at]);
-            ++ns;
+            if (ok && c + 1 == chunks) umma_commit(&k_empty[stage.at]);
+            stage.next(a.k_stages);
           }
           if (!keep) {
             if (ok) umma_commit(&q_empty[q.at]);
             q.next(kQSt);
           }
+        }
+        if (first < chunks) {
+          t.next(a.k_stages);
+          if (tiles > 2) t.next(a.k_stages);
         }
         mbar_arrive(&piece_empty[pi]);
       }
@@ -438,6 +451,14 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       fresh = fresh_of();
     }
     bool more = true, again = false;
+    int per_head = 1, h = 0, at = 0;       // items of a head, and where the item is
+    auto divide = [&] {
+      if (items == 0) return;
+      per_head = items / a.c.heads;
+      h = item / per_head;
+      at = item - h * per_head;
+    };
+    divide();
     for (uint32_t seg = 0; more; ++seg) {
       const uint32_t pi = seg % kAhead;
       if (seg >= kAhead && !warp_wait(&piece_empty[pi], (seg / kAhead - 1) & 1, abort_flag)) break;
@@ -448,13 +469,14 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         x = paged_extent(a, i, false);
         mass_request(a, x, items, length);
         fresh = fresh_of();
+        divide();
       }
-      const int per_head = more ? items / a.c.heads : 1, h = item / per_head, at = item - h * per_head;
       const int key0 = at * kItemKeys, chunks = length - kItemLength;
       // the chunk of the first row that sees a key
       auto first_of = [&](int key) {
-        const long long t = a.right < 0 ? 0 : max(static_cast<long long>(key) - x.pos - a.right, 0ll);
-        return t < x.W ? static_cast<int>(t) / a.tokens : chunks;
+        if (a.right < 0) return 0;
+        const long long t = max(static_cast<long long>(key) - x.pos - a.right, 0ll);
+        return t == 0 ? 0 : t < x.W ? static_cast<int>(t) / a.tokens : chunks;
       };
       const bool keep = more && chunks == 1 && at + 1 < per_head && left > length && first_of(key0 + kItemKeys) < 1;
       if (lane == 0) {
@@ -466,7 +488,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           p.h = h;
           p.key0 = key0;
           p.fresh = fresh;
-          p.tiles = x.L - key0 > kTile ? 2 : 1;
+          p.tiles = min((x.L - key0 + kTile - 1) / kTile, kGroups);
           p.chunks = chunks;
           p.first = first_of(key0);
           p.again = again;
@@ -478,9 +500,14 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       again = keep;
       left -= length;
       ++item;
+      if (++at == per_head) {
+        at = 0;
+        ++h;
+      }
     }
-  } else if (warp >= 12) {
+  } else if (warp < 8) {
     // --------------------------------------------------------------- query rows and their numbers
+    const int n = threadIdx.x - 128;       // row of a chunk
     bool ok = true;
     Ring q, in;
     uint32_t asked = 0;
@@ -490,11 +517,9 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       const Extent x = p->x;
       const int chunks = p->chunks, h = p->h;
       for (int c = p->again ? chunks : p->first; ok && c < chunks; ++c) {
-        ok = warp_wait(&q_empty[q.at], q.round ^ 1, abort_flag);
+        if (FP8 || warp == 4) ok = warp_wait(&q_empty[q.at], q.round ^ 1, abort_flag);
         if (!ok) break;
-        constexpr int kMine = kChunkRows / 32 / C::kRowWarps;   // rows of a lane
-        const int n0 = (warp - 12) * 32 + lane;
-        if constexpr (!FP8) {
+        if (!FP8 && warp == 4) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&q_full[q.at], a.tokens * a.group * (DH * 2));
 #pragma unroll
@@ -505,22 +530,17 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           ++asked;
           __syncwarp();
         }
-        float neg_lse[kMine];
-        int hi[kMine], every[kMine];
-#pragma unroll
-        for (int e = 0; e < kMine; ++e) numbers_of(a, x, h, c, e * 32 + n0, neg_lse[e], hi[e], every[e]);
+        float neg_lse;
+        int hi, every;
+        numbers_of(a, x, h, c, n, neg_lse, hi, every);
         ok = warp_wait(&n_empty[in.at], in.round ^ 1, abort_flag);
         if (!ok) break;
         Numbers &s = numbers[in.at];
-#pragma unroll
-        for (int e = 0; e < kMine; ++e) {
-          const int n = e * 32 + n0;
-          s.neg_lse[n] = neg_lse[e];
-          s.hi[n] = hi[e];
-          if (n % 16 == 0) s.every[n / 16] = every[e];
-        }
+        s.neg_lse[n] = neg_lse;
+        s.hi[n] = hi;
+        if (n % 16 == 0) s.every[n / 16] = every;
         if constexpr (FP8) {
-          stage_chunk<DH>(a, x, h, c, rows_at + q.at * a.q_bytes, s.scale, n0);
+          stage_chunk<DH>(a, x, h, c, rows_at + q.at * a.q_bytes, s.scale, n);
           fence_proxy_async_smem();
         }
         __syncwarp();
@@ -538,9 +558,9 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     __syncwarp();
   } else {
     // --------------------------------------------------------------- exponentials and sums
-    const int g = (warp - 4) >> 2, quarter = warp & 3;
+    const int g = (warp - 8) >> 2, quarter = warp & 3;
     const int key = g * kTile + quarter * 32 + lane;      // of the item
-    const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * 256;
+    const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * 128;
     bool ok = true;
     Ring in, sl;
     uint32_t ns = 0;
@@ -559,16 +579,16 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       for (int k = p->first; ok && k < chunks; ++k) {
         if (!again) ok = warp_wait(&n_full[in.at], in.round, abort_flag);
         if (ok && there) {
-          const uint32_t b = ns & 1;
-          ok = warp_wait(&s_full[g * 2 + b], (ns / 2) & 1, abort_flag);
+          const uint32_t b = two ? ns & 1 : 0;
+          ok = warp_wait(&s_full[g * 2 + b], (two ? ns / 2 : ns) & 1, abort_flag);
           if (ok) {
             tc_fence_after();
             const Numbers &s = numbers[in.at];
             const int columns = chunk_columns(a, W, k);
             float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
-            auto add_some = [&](const uint32_t (&x)[16], int c0, auto masked) {
+            auto add_some = [&](auto &x, int c0, auto masked) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) {
+              for (int e = 0; e < static_cast<int>(sizeof(x) / 4); e += 4) {
                 const float4 z = *reinterpret_cast<const float4 *>(&s.neg_lse[c0 + e]);
                 float2 f0 = make_float2(c, c), f1 = f0;
                 if constexpr (FP8) {     // the row's factor and the key's first: no product on the way overflows
@@ -590,23 +610,23 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
               }
             };
             // (a branch: as selects under a condition the comparisons are all computed)
-            auto add = [&](const uint32_t (&x)[16], int c0) {
-              if (end > s.every[c0 / 16]) add_some(x, c0, std::true_type{});
+            auto add = [&](auto &x, int c0, int every) {
+              if (end > every) add_some(x, c0, std::true_type{});
               else add_some(x, c0, std::false_type{});
             };
-            // the next 16 columns are on their way while these are summed up
-            uint32_t x0[16], x1[16];
-            const uint32_t t = t_s + b * 128;
-            tmem_ld16(t, x0);
-            for (int c0 = 0; c0 < columns; c0 += 32) {
-              const bool second = c0 + 16 < columns;
+            const uint32_t t = t_s + b * 64;
+            int c0 = 0;
+            for (; c0 + 32 <= columns; c0 += 32) {
+              uint32_t x[32];
+              tmem_ld32(t + c0, x);
               tmem_ld_wait();
-              if (second) tmem_ld16(t + c0 + 16, x1);
-              add(x0, c0);
-              if (!second) break;
+              add(x, c0, min(s.every[c0 / 16], s.every[c0 / 16 + 1]));
+            }
+            if (c0 < columns) {
+              uint32_t x[16];
+              tmem_ld16(t + c0, x);
               tmem_ld_wait();
-              if (c0 + 32 < columns) tmem_ld16(t + c0 + 32, x0);
-              add(x1, c0 + 16);
+              add(x, c0, s.every[c0 / 16]);
             }
             sum += (acc0.x + acc0.y) + (acc1.x + acc1.y);
             tc_fence_before();
@@ -648,7 +668,7 @@ dllm_status launch_mass(const dllm_kv_pages *pages, MassArgs &g, cudaStream_t s)
       !make_tmap_query_rows(&tq, g.q, g.q_rows, g.Hq, DH, g.q_stride, g.group, g.tokens))
     return DLLM_ERR_CUDA;
   g.k_stages = C::stages(g.columns);
-  g.off_q = C::kOffK + g.k_stages * C::kRaw;
+  g.off_q = C::kOffK + g.k_stages * C::kStage;
   g.q_bytes = C::chunk_bytes(g.columns);
   const int smem = g.off_q + C::kQSt * g.q_bytes + 1024;
   auto kern = mass_kernel<DH, FP8>;
