@@ -192,7 +192,7 @@ struct ShiftArgs {
   unsigned int *status;
 };
 
-constexpr int kMoveThreads = 512;
+constexpr int kMoveThreads = 256;
 constexpr int kEach = 4;         // rows of a thread in a round (16 bytes of K and of V each)
 
 // Rows of ROW bytes that a CTA moves in a round.

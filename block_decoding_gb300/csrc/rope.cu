@@ -24,8 +24,9 @@ DLLM_DEFINE_STATUS(rope)
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRows = 4;      // rows of a block
-constexpr int kMaxHalf = 64;     // pairs of a head
+constexpr int kMaxRows = kThreads / 32;   // rows of a block: a warp finds each one's place
+constexpr int kMaxHalf = 64;              // pairs of a head
+constexpr int kAhead = 3;                 // units of a thread whose loads are on their way
 
 struct RopeArgs {
   KvPages c;
@@ -81,6 +82,20 @@ __device__ __forceinline__ float2 turn_of(int pos, unsigned long long turns) {
   return r;
 }
 
+// Request that holds row r, or -1, by a whole warp: 32 offsets at a time (a
+// bisection's loads wait for each other).
+__device__ __forceinline__ int request_of_warp(const int32_t *off, int B, int r, int lane) {
+  int lo = 0, hi = B + 1;      // off[lo] <= r, and r < off[hi] if there is one
+  if (r < off[0]) return -1;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const uint32_t m = __ballot_sync(0xffffffffu, at < hi && off[at] <= r);
+    lo += (31 - __clz(m)) * step;       // (lane 0's holds)
+    hi = min(hi, lo + step);
+  }
+  return lo < B ? lo : -1;
+}
+
 template <int DH, bool FP8>
 __global__ void __launch_bounds__(kThreads) rope_write_kernel(const __grid_constant__ RopeArgs g) {
   constexpr int LPR = DH / 16, kUnits = kThreads / LPR;
@@ -91,83 +106,101 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const __grid_const
   const int tid = threadIdx.x, l = tid % LPR;
   if (blockIdx.x + tid == 0 && (g.off[0] < 0 || g.off[g.B] > g.rows)) atomicOr(g.status, DLLM_DEV_OFFSETS);
   const int r0 = blockIdx.x * g.per, rows = min(g.per, g.rows - r0);
-  const int heads = g.c.heads, T = g.Hq + 2 * heads, half = g.half, rc = half / 8;
+  const int heads = g.c.heads, T = g.Hq + 2 * heads, half = g.half, rc = half / 8, total = rows * T;
   // this lane's chunks of a head: the halves of eight pairs, or two that are not turned
   const bool turns = l < rc;
   const int ca = turns ? l : rc + l, cb = turns ? l + rc : ca + LPR - rc;
-  if (tid < rows) {
-    const int r = r0 + tid, i = request_of(g.off, g.B, r);
+  // Unit u of the block is head u % T of row u / T: q's heads, k's, v's. A
+  // thread's units are kUnits apart, and kAhead of them are loaded at a time.
+  int n = 0, t = tid / LPR;
+  while (t >= T) { t -= T; ++n; }
+  uint4 a[kAhead], b[kAhead];
+  int un[kAhead], ut[kAhead];
+  auto load = [&] {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      un[i] = n;
+      ut[i] = t;
+      a[i] = b[i] = make_uint4(0, 0, 0, 0);
+      if (n < rows) {
+        const long long r = r0 + n;
+        const uint16_t *src = t < g.Hq           ? g.q + r * g.q_stride + t * DH
+                              : t < g.Hq + heads ? g.k + r * g.k_stride + (t - g.Hq) * DH
+                                                 : g.v + r * g.v_stride + (t - g.Hq - heads) * DH;
+        a[i] = reinterpret_cast<const uint4 *>(src)[ca];
+        b[i] = reinterpret_cast<const uint4 *>(src)[cb];
+      }
+      t += kUnits;
+      while (t >= T) { t -= T; ++n; }
+    }
+  };
+  load();
+  // the rows' places, and their sines and cosines, while the first units are on their way
+  if (tid / 32 < rows) {
+    const int r = r0 + tid / 32, i = request_of_warp(g.off, g.B, r, tid % 32);
     int row = -1;                                   // in no request
     if (i >= 0) {
       const long long u = static_cast<long long>(g.pos0[i]) + (r - g.off[i]);
       row = u < 0 || u > 0x7fffffffll ? -1 : page_row(g.c, i, static_cast<int>(u));
       if (row < 0) {
-        atomicOr(g.status, DLLM_DEV_PAGE);
+        if (tid % 32 == 0) atomicOr(g.status, DLLM_DEV_PAGE);
         row = -2;                                   // no place
       }
     }
-    s_row[tid] = row;
+    if (tid % 32 == 0) s_row[tid / 32] = row;
   }
   for (int idx = tid; idx < rows * half; idx += kThreads) {
-    const int n = idx / half, j = idx - n * half;
-    s_cs[n * kMaxHalf + j] = turn_of(g.pos[static_cast<size_t>(g.axis[j]) * g.rows + r0 + n], g.turns[j]);
+    const int m = idx / half, j = idx - m * half;
+    s_cs[m * kMaxHalf + j] = turn_of(g.pos[static_cast<size_t>(g.axis[j]) * g.rows + r0 + m], g.turns[j]);
   }
   __syncthreads();
-  // Every lane of a warp goes through the same number of rounds: the lanes of
-  // a row exchange maxima.
-  const int total = rows * T;
-  int n = 0, t = tid / LPR;
-  while (t >= T) { t -= T; ++n; }
-  for (int u0 = 0; u0 < total; u0 += kUnits) {
-    const bool live = n < rows;
-    const int row = live ? s_row[n] : -1;
-    const bool is_q = t < g.Hq, is_k = !is_q && t < g.Hq + heads;
-    const int h = is_q ? t : is_k ? t - g.Hq : t - g.Hq - heads;
-    const long long r = r0 + n;
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (row != -1) {
-      const uint16_t *src = is_q ? g.q + r * g.q_stride : is_k ? g.k + r * g.k_stride : g.v + r * g.v_stride;
-      const uint4 *s4 = reinterpret_cast<const uint4 *>(src + h * DH);
-      a = s4[ca];
-      b = s4[cb];
-    }
-    float x[8], y[8];
-    unpack8(a, x);
-    unpack8(b, y);
-    if (turns && (is_q || is_k) && live) {
-      const float2 *cs = s_cs + n * kMaxHalf + l * 8;
+  // Every lane of a warp goes through the same rounds: the lanes of a row
+  // exchange maxima.
+  for (int u0 = 0; u0 < total; u0 += kAhead * kUnits) {
+    if (u0 > 0) load();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 w = cs[e];
-        const float p = x[e] * w.x - y[e] * w.y;
-        y[e] = y[e] * w.x + x[e] * w.y;
-        x[e] = p;
+    for (int i = 0; i < kAhead; ++i) {
+      const bool live = un[i] < rows, is_q = ut[i] < g.Hq, is_k = !is_q && ut[i] < g.Hq + heads;
+      const int row = live ? s_row[un[i]] : -1;
+      const int h = is_q ? ut[i] : is_k ? ut[i] - g.Hq : ut[i] - g.Hq - heads;
+      float x[8], y[8];
+      unpack8(a[i], x);
+      unpack8(b[i], y);
+      if (turns && (is_q || is_k) && live) {
+        const float4 *cs = reinterpret_cast<const float4 *>(s_cs + un[i] * kMaxHalf + l * 8);   // two pairs each
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float4 w = cs[e / 2];
+          const float p = x[e] * w.x - y[e] * w.y, q = x[e + 1] * w.z - y[e + 1] * w.w;
+          y[e] = y[e] * w.x + x[e] * w.y;
+          y[e + 1] = y[e + 1] * w.z + x[e + 1] * w.w;
+          x[e] = p;
+          x[e + 1] = q;
+        }
       }
-    }
-    if (is_q) {
-      if (row != -1) {
-        uint4 *d = reinterpret_cast<uint4 *>(g.q_out + r * g.q_out_stride + h * DH);
+      if (is_q && row != -1) {
+        uint4 *d = reinterpret_cast<uint4 *>(g.q_out + (r0 + un[i]) * g.q_out_stride + h * DH);
         d[ca] = pack8(x);
         d[cb] = pack8(y);
       }
-    }
-    const size_t at = static_cast<size_t>(max(row, 0)) + (static_cast<size_t>(h) << g.c.page_shift);
-    if constexpr (FP8) {
-      uint2 qa, qb;
-      const int byte = quantise_row_f32<LPR>(x, y, qa, qb);
-      if (!is_q && row >= 0) {
-        uint2 *d = reinterpret_cast<uint2 *>((is_k ? g.c.k : g.c.v) + at * DH);
-        d[ca] = qa;
-        d[cb] = qb;
-        if (l == 0) (is_k ? g.c.k_scale : g.c.v_scale)[at] = static_cast<uint8_t>(byte);
+      const size_t at = static_cast<size_t>(max(row, 0)) + (static_cast<size_t>(h) << g.c.page_shift);
+      if constexpr (FP8) {
+        // (a round without rows for the pages is one for whole warps)
+        if (!__any_sync(0xffffffffu, !is_q && row >= 0)) continue;
+        uint2 qa, qb;
+        const int byte = quantise_row_f32<LPR>(x, y, qa, qb);
+        if (!is_q && row >= 0) {
+          uint2 *d = reinterpret_cast<uint2 *>((is_k ? g.c.k : g.c.v) + at * DH);
+          d[ca] = qa;
+          d[cb] = qb;
+          if (l == 0) (is_k ? g.c.k_scale : g.c.v_scale)[at] = static_cast<uint8_t>(byte);
+        }
+      } else if (!is_q && row >= 0) {
+        uint4 *d = reinterpret_cast<uint4 *>((is_k ? g.c.k : g.c.v) + at * (DH * 2));
+        d[ca] = is_k ? pack8(x) : a[i];
+        d[cb] = is_k ? pack8(y) : b[i];
       }
-    } else if (!is_q && row >= 0) {
-      uint4 *d = reinterpret_cast<uint4 *>((is_k ? g.c.k : g.c.v) + at * (DH * 2));
-      d[ca] = is_k ? pack8(x) : a;
-      d[cb] = is_k ? pack8(y) : b;
     }
-    t += kUnits;
-    while (t >= T) { t -= T; ++n; }
   }
 }
 
