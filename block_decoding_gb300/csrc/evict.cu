@@ -23,6 +23,7 @@ struct SelectArgs {
 
 constexpr int kMaxSelWarps = 32;
 constexpr int kBins = 2048;      // 11 bits at a time
+constexpr int kBatch = 8;        // loads of a thread on their way
 constexpr int kCached = 49152;   // weights that shared memory holds (192 KB)
 
 // Order of weights as unsigned numbers: -0 is 0, NaN is above everything.
@@ -62,16 +63,34 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Se
     for (int j = tid; j < k; j += nt) keep[j] = j;
     return;
   }
+  const int32_t *table = a.c.table + static_cast<size_t>(i) * a.c.max_pages;
   const int s = a.sinks, e = n - a.recent;       // [s, e) is chosen from: at least n - budget rows
-  auto fetch = [&](int u) {
-    const int row = page_row(a.c, i, u);
-    if (row < 0) {
-      atomicOr(a.status, DLLM_DEV_PAGE);
-      return 0u;
+  // The weights of positions u, u + nt, .. below e: pages first, so that the
+  // loads of a batch wait together.
+  auto fetch = [&](int u, uint32_t (&x)[kBatch]) {
+    int page[kBatch];
+    float w[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) page[q] = u + q * nt < e ? __ldg(table + ((u + q * nt) >> a.c.page_shift)) : 0;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const bool held = u + q * nt < e, bad = page[q] < 0 || page[q] >= a.c.num_pages;
+      w[q] = 0.f;
+      if (held && !bad)
+        w[q] = a.mass[(static_cast<size_t>(page[q] * a.c.heads + h) << a.c.page_shift) + ((u + q * nt) & ((1 << a.c.page_shift) - 1))];
+      if (held && bad) {       // (without a weight: the least of all)
+        atomicOr(a.status, DLLM_DEV_PAGE);
+        w[q] = -INFINITY;
+      }
     }
-    return order_of(a.mass[row + (static_cast<size_t>(h) << a.c.page_shift)]);
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) x[q] = order_of(w[q]);
   };
-  auto key = [&](int u) { return CACHED ? s_key[u] : fetch(u); };
+  auto key = [&](int u) {                        // (of [s, e))
+    if (CACHED) return s_key[u];
+    const int row = page_row(a.c, i, u);
+    return order_of(row < 0 ? -INFINITY : a.mass[row + (static_cast<size_t>(h) << a.c.page_shift)]);
+  };
   int left = k - s - a.recent;                   // how many of them stay
   uint32_t least = 0;                            // the bits of the least that stays, found so far
   int shift = 32;                                // ... from this bit on
@@ -82,16 +101,23 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Se
     __syncthreads();
     const int low = shift - bits;
     const uint32_t mask = (1u << bits) - 1;
-#pragma unroll 4
-    for (int u = s + tid; u < e; u += nt) {
-      uint32_t x;
-      if (CACHED && filled) {
-        x = s_key[u];
-      } else {
-        x = fetch(u);
-        if (CACHED) s_key[u] = x;
+    if (CACHED && filled) {
+      for (int u = s + tid; u < e; u += nt) {
+        const uint32_t x = s_key[u];
+        if (x >> shift == least >> shift) atomicAdd(&s_hist[x >> low & mask], 1u);
       }
-      if (!filled || x >> shift == least >> shift) atomicAdd(&s_hist[x >> low & mask], 1u);
+    } else {
+      for (int u0 = s + tid; u0 < e; u0 += kBatch * nt) {
+        uint32_t x[kBatch];
+        fetch(u0, x);
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const int u = u0 + q * nt;
+          if (u >= e) break;
+          if (CACHED) s_key[u] = x[q];
+          if (!filled || x[q] >> shift == least >> shift) atomicAdd(&s_hist[x[q] >> low & mask], 1u);
+        }
+      }
     }
     __syncthreads();
     // counts from the highest bin down: thread t has kBins / nt bins, the highest first
@@ -125,28 +151,42 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Se
     if (s_of_bin == left) break;                 // all of the bin stay
   }
   // Rows whose bits from `shift` on are those of `least` are ties: the first
-  // `left` of them stay, and all above. (The shift by 32 does not occur: with
-  // left <= 0 no row of [s, e) stays.)
+  // `left` of them stay, and all above. (With left <= 0 no row of [s, e) stays,
+  // and `shift` may be 32.) A warp has a run of positions, 32 x 32 at a time:
+  // lane l keeps the votes of the l-th 32.
   const int run = ((n + warps - 1) / warps + 31) / 32 * 32, u0 = warp * run, u1 = min(n, u0 + run);
   const bool some = left > 0;
-  auto look = [&](int u, bool &in, bool &tie) {
-    in = tie = false;
-    if (u >= u1) return;
-    if (u < s || u >= e) {
-      in = true;
-    } else if (some) {
-      const uint32_t x = key(u);
-      in = x >> shift > least >> shift;
-      tie = x >> shift == least >> shift;
+  auto votes = [&](int from, uint32_t &in_votes, uint32_t &tie_votes) {
+    in_votes = tie_votes = 0;
+    const int rounds = min((u1 - from + 31) / 32, 32);
+    for (int l = 0; l < rounds; ++l) {
+      const int u = from + l * 32 + lane;
+      bool in = false, tie = false;
+      if (u < u1) {
+        if (u < s || u >= e) {
+          in = true;
+        } else if (some) {
+          const uint32_t x = key(u) >> shift, y = least >> shift;
+          in = x > y;
+          tie = x == y;
+        }
+      }
+      const uint32_t iv = __ballot_sync(0xffffffffu, in), tv = __ballot_sync(0xffffffffu, tie);
+      if (lane == l) {
+        in_votes = iv;
+        tie_votes = tv;
+      }
     }
   };
+  uint32_t in_votes = 0, tie_votes = 0;
   int count = 0, ties = 0;
-  for (int u = u0; u < u1; u += 32) {
-    bool in, tie;
-    look(u + lane, in, tie);
-    count += __popc(__ballot_sync(0xffffffffu, in));
-    ties += __popc(__ballot_sync(0xffffffffu, tie));
+  for (int from = u0; from < u1; from += 1024) {
+    votes(from, in_votes, tie_votes);
+    count += __popc(in_votes);
+    ties += __popc(tie_votes);
   }
+  count = __reduce_add_sync(0xffffffffu, count);
+  ties = __reduce_add_sync(0xffffffffu, ties);
   __syncthreads();                               // s_sum is read by all
   if (lane == 0) {
     s_sum[warp] = count;
@@ -157,15 +197,31 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Se
   const int c = lane < warp ? s_sum[lane] : 0, t = lane < warp ? s_tie[lane] : 0;
   int tie_at = __reduce_add_sync(0xffffffffu, t);
   int at = __reduce_add_sync(0xffffffffu, c) + min(tie_at, max(left, 0));
-  for (int u = u0; u < u1; u += 32) {
-    bool in, tie;
-    look(u + lane, in, tie);
-    const uint32_t below_lane = (1u << lane) - 1, tm = __ballot_sync(0xffffffffu, tie);
-    in |= tie && tie_at + __popc(tm & below_lane) < left;
-    tie_at += __popc(tm);
-    const uint32_t im = __ballot_sync(0xffffffffu, in);
-    if (in) keep[at + __popc(im & below_lane)] = u + lane;
-    at += __popc(im);
+  auto before = [&](int x) {                     // sum over the lanes before this one
+    int up = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += y;
+    }
+    return up - x;
+  };
+  for (int from = u0; from < u1; from += 1024) {
+    if (run > 1024) votes(from, in_votes, tie_votes);      // (else they are the first pass's)
+    // the lane's ties that stay: the lowest
+    const int room = left - tie_at - before(__popc(tie_votes));
+    uint32_t stay = tie_votes;
+    while (__popc(stay) > max(room, 0)) stay ^= 0x80000000u >> __clz(stay);
+    tie_at += __reduce_add_sync(0xffffffffu, __popc(tie_votes));
+    stay |= in_votes;
+    const int mine = at + before(__popc(stay));
+    at += __reduce_add_sync(0xffffffffu, __popc(stay));
+    const int rounds = min((u1 - from + 31) / 32, 32);
+    for (int l = 0; l < rounds; ++l) {
+      const uint32_t m = __shfl_sync(0xffffffffu, stay, l);
+      const int to = __shfl_sync(0xffffffffu, mine, l) + __popc(m & ((1u << lane) - 1));
+      if (m >> lane & 1) keep[to] = from + l * 32 + lane;
+    }
   }
 }
 
@@ -189,51 +245,50 @@ struct ShiftArgs {
   int src_heads, max_n;
   const int32_t *count, *first;   // [B]; first may be null: 0
   float *mass;
+  uint32_t zero;               // 0, which the compiler does not know
   unsigned int *status;
 };
 
 constexpr int kMoveThreads = 256;
-constexpr int kEach = 4;         // rows of a thread in a round (16 bytes of K and of V each)
 
-// Rows of ROW bytes that a CTA moves in a round.
-constexpr int round_rows(int row_bytes) { return kMoveThreads * kEach * 16 / row_bytes; }
+// Rows of a thread at a time, 16 bytes of K and of V each: elsewhere a block has
+// no more; in place one such set is written while the next is on its way.
+constexpr int kEachAway = 2, kEachInPlace = 2;
 
-// One request and cached head, K and V: a CTA of the grid's x takes
-// round_rows of the list. Elsewhere that is all. In place the CTAs of x are a
-// cluster that walks the list from its start, round by round: every row of a
-// round is read before any is written (a cluster barrier between the two), and
-// since lists ascend and no row moves to a later position, a place is written
-// in no earlier round than it is read: position first + j is row src[j'] of the
-// list with j' <= j if it is any. The next round's rows lie behind all places
-// written so far, so it needs no barrier before its loads.
+// Rows of ROW bytes that a CTA moves at a time.
+constexpr int round_rows(int row_bytes, bool in_place) {
+  return kMoveThreads * (in_place ? kEachInPlace : kEachAway) * 16 / row_bytes;
+}
+
+// What a thread moves at a time.
+template <int EACH>
+struct Moved {
+  uint4 k[EACH], v[EACH];
+  float mass[EACH];
+  uint8_t k_scale[EACH], v_scale[EACH];
+  int dest[EACH];                // cache row for head 0, -1: nothing
+};
+
 template <int ROW, bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads) shift_kernel(const __grid_constant__ ShiftArgs a) {
-  constexpr int kChunks = ROW / 16, kStep = kMoveThreads / kChunks, kRows = kStep * kEach;
-  static_assert(kRows == round_rows(ROW), "rows of a round");
-  pdl_trigger();
-  pdl_wait();
-  const int h = blockIdx.y, i = blockIdx.z, tid = threadIdx.x, c = tid % kChunks;
-  int n = a.count[i];
-  const int first = a.first ? a.first[i] : 0;
-  if (n < 0 || n > a.max_n) {
-    if (tid == 0) atomicOr(a.status, DLLM_DEV_OFFSETS);
-    n = min(max(n, 0), a.max_n);
-  }
-  const int32_t *src = a.src + (static_cast<size_t>(i) * a.src_heads + (a.src_heads > 1 ? h : 0)) * a.max_n;
-  KvPages to = a.c;
-  to.table = a.dst_table;
-  to.max_pages = a.dst_pages;
-  const size_t head = static_cast<size_t>(h) << a.c.page_shift;
-  for (int base = IN_PLACE ? 0 : blockIdx.x * kRows; base < n; base += gridDim.x * kRows) {   // (n < 2^30)
-    const int j0 = IN_PLACE ? base + blockIdx.x * kRows : base;
-    uint4 k[kEach], v[kEach];
-    uint8_t ks[kEach], vs[kEach];
-    float m[kEach];
-    int from[kEach], dest[kEach];
+struct Mover {
+  static constexpr int kEach = IN_PLACE ? kEachInPlace : kEachAway;
+  static constexpr int kChunks = ROW / 16, kStep = kMoveThreads / kChunks, kRows = kStep * kEach;
+  static_assert(kRows == round_rows(ROW, IN_PLACE), "rows of a round");
+  const ShiftArgs &a;
+  const int i, n, first, c;      // request, rows of its list, first position, the thread's 16 bytes of a row
+  const int32_t *src;
+  const size_t head;
+
+  // Rows j0 .. j0 + kRows - 1 of the list.
+  __device__ __forceinline__ void load(Moved<kEach> &m, int j0) const {
+    KvPages to = a.c;
+    to.table = a.dst_table;
+    to.max_pages = a.dst_pages;
+    int from[kEach];
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
-      const int j = j0 + tid / kChunks + q * kStep;
-      from[q] = dest[q] = -1;
+      const int j = j0 + threadIdx.x / kChunks + q * kStep;
+      from[q] = m.dest[q] = -1;
       if (j >= n) continue;
       const int u = src[j];
       const long long d = static_cast<long long>(first) + j;
@@ -244,46 +299,107 @@ __global__ void __launch_bounds__(kMoveThreads) shift_kernel(const __grid_consta
       }
       if (!bad) {
         from[q] = page_row(a.c, i, u);
-        dest[q] = page_row(to, i, static_cast<int>(d));
+        m.dest[q] = page_row(to, i, static_cast<int>(d));
       }
-      if (from[q] < 0 || dest[q] < 0) {
+      if (from[q] < 0 || m.dest[q] < 0) {
         atomicOr(a.status, DLLM_DEV_PAGE);
-        from[q] = -1;
+        m.dest[q] = -1;
       }
     }
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
-      if (from[q] < 0) continue;
+      if (m.dest[q] < 0) continue;
       const size_t s = from[q] + head;
-      k[q] = *reinterpret_cast<const uint4 *>(a.c.k + s * ROW + c * 16);
-      v[q] = *reinterpret_cast<const uint4 *>(a.c.v + s * ROW + c * 16);
+      m.k[q] = *reinterpret_cast<const uint4 *>(a.c.k + s * ROW + c * 16);
+      m.v[q] = *reinterpret_cast<const uint4 *>(a.c.v + s * ROW + c * 16);
       if (c == 0) {
-        if (a.c.k_scale) { ks[q] = a.c.k_scale[s]; vs[q] = a.c.v_scale[s]; }
-        if (a.mass) m[q] = a.mass[s];
+        if (a.c.k_scale) { m.k_scale[q] = a.c.k_scale[s]; m.v_scale[q] = a.c.v_scale[s]; }
+        if (a.mass) m.mass[q] = a.mass[s];
       }
     }
-    if constexpr (IN_PLACE) {
-      __syncwarp();
-      cluster_barrier();
-    }
+  }
+  // 0, once all of m is there.
+  __device__ __forceinline__ uint32_t loaded(const Moved<kEach> &m) const {
+    uint32_t x = 0;
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
-      if (from[q] < 0) continue;
-      const size_t s = dest[q] + head;
-      *reinterpret_cast<uint4 *>(a.c.k + s * ROW + c * 16) = k[q];
-      *reinterpret_cast<uint4 *>(a.c.v + s * ROW + c * 16) = v[q];
+      if (m.dest[q] < 0) continue;
+      x ^= m.k[q].x ^ m.k[q].y ^ m.k[q].z ^ m.k[q].w ^ m.v[q].x ^ m.v[q].y ^ m.v[q].z ^ m.v[q].w;
       if (c == 0) {
-        if (a.c.k_scale) { a.c.k_scale[s] = ks[q]; a.c.v_scale[s] = vs[q]; }
-        if (a.mass) a.mass[s] = m[q];
+        if (a.c.k_scale) x ^= m.k_scale[q] ^ m.v_scale[q];
+        if (a.mass) x ^= __float_as_uint(m.mass[q]);
       }
     }
-    if (!IN_PLACE) break;
+    return x & a.zero;
+  }
+  __device__ __forceinline__ void store(const Moved<kEach> &m) const {
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) {
+      if (m.dest[q] < 0) continue;
+      const size_t s = m.dest[q] + head;
+      *reinterpret_cast<uint4 *>(a.c.k + s * ROW + c * 16) = m.k[q];
+      *reinterpret_cast<uint4 *>(a.c.v + s * ROW + c * 16) = m.v[q];
+      if (c == 0) {
+        if (a.c.k_scale) { a.c.k_scale[s] = m.k_scale[q]; a.c.v_scale[s] = m.v_scale[q]; }
+        if (a.mass) a.mass[s] = m.mass[q];
+      }
+    }
+  }
+};
+
+// One request and cached head, K and V: a CTA of the grid's x takes
+// round_rows of the list. Elsewhere that is all. In place the CTAs of x are a
+// cluster that walks the list from its start, round by round: every row of a
+// round is read before any is written (a cluster barrier between the two), and
+// since lists ascend and no row moves to a later position, a place is written
+// in no earlier round than it is read: position first + j is row src[j'] of the
+// list with j' <= j if it is any. So rounds behind may be read at any time
+// before: the next one is on its way while the CTAs meet and this one is written.
+template <int ROW, bool IN_PLACE>
+__global__ void __launch_bounds__(kMoveThreads, 4) shift_kernel(const __grid_constant__ ShiftArgs a) {
+  using M = Mover<ROW, IN_PLACE>;
+  pdl_trigger();
+  pdl_wait();
+  const int h = blockIdx.y, i = blockIdx.z;
+  int n = a.count[i];
+  const int first = a.first ? a.first[i] : 0;
+  if (n < 0 || n > a.max_n) {
+    if (threadIdx.x == 0) atomicOr(a.status, DLLM_DEV_OFFSETS);
+    n = min(max(n, 0), a.max_n);
+  }
+  const M move{a, i, n, first, static_cast<int>(threadIdx.x) % M::kChunks,
+               a.src + (static_cast<size_t>(i) * a.src_heads + (a.src_heads > 1 ? h : 0)) * a.max_n,
+               static_cast<size_t>(h) << a.c.page_shift};
+  const int mine = blockIdx.x * M::kRows;       // (n < 2^30)
+  if constexpr (!IN_PLACE) {
+    if (mine >= n) return;
+    Moved<M::kEach> m;
+    move.load(m, mine);
+    move.store(m);
+  } else {
+    const int round = gridDim.x * M::kRows;
+    Moved<M::kEach> m[2];
+    if (n > 0) move.load(m[0], mine);
+    for (int base = 0; base < n; base += 2 * round) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int at = base + k * round;
+        if (at >= n) break;                     // (the whole cluster)
+        if (at + round < n) move.load(m[k ^ 1], mine + at + round);
+        // The barrier orders this round's loads before its stores, and needs
+        // nothing of the stores before: a release would wait for all of them.
+        // The loads are done when their values decide whether to arrive.
+        if (move.loaded(m[k]) == 0) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+        asm volatile("barrier.cluster.wait;" ::: "memory");
+        move.store(m[k]);
+      }
+    }
   }
 }
 
 template <int ROW>
 cudaError_t launch_shift_rows(const ShiftArgs &g, bool in_place, int heads, int B, cudaStream_t s) {
-  const int blocks = (g.max_n - 1) / round_rows(ROW) + 1;
+  const int blocks = (g.max_n - 1) / round_rows(ROW, in_place) + 1;
   if (!in_place) return launch_pdl(shift_kernel<ROW, false>, dim3(blocks, heads, B), dim3(kMoveThreads), 0, s, g);
   const unsigned cluster = blocks > 4 ? 8 : blocks > 2 ? 4 : blocks;
   return launch_pdl_clusters(shift_kernel<ROW, true>, cluster, dim3(cluster, heads, B), dim3(kMoveThreads), 0, s, g);

@@ -24,9 +24,9 @@ DLLM_DEFINE_STATUS(rope)
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRows = kThreads / 32;   // rows of a block: a warp finds each one's place
-constexpr int kMaxHalf = 64;              // pairs of a head
-constexpr int kAhead = 3;                 // units of a thread whose loads are on their way
+constexpr int kMaxRows = 4;      // rows of a block: a warp finds each one's place
+constexpr int kMaxHalf = 64;     // pairs of a head
+constexpr int kAhead = 2;        // units of a thread whose loads are on their way
 
 struct RopeArgs {
   KvPages c;
@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const __grid_const
   }
   for (int idx = tid; idx < rows * half; idx += kThreads) {
     const int m = idx / half, j = idx - m * half;
-    s_cs[m * kMaxHalf + j] = turn_of(g.pos[static_cast<size_t>(g.axis[j]) * g.rows + r0 + m], g.turns[j]);
+    // (lane l of a unit reads pairs 8 l .. 8 l + 7, two at a time: the l-th pairs of two of all lanes lie side by side)
+    s_cs[m * kMaxHalf + j % 8 / 2 * 16 + j / 8 * 2 + j % 2] = turn_of(g.pos[static_cast<size_t>(g.axis[j]) * g.rows + r0 + m], g.turns[j]);
   }
   __syncthreads();
   // Every lane of a warp goes through the same rounds: the lanes of a row
@@ -167,10 +168,10 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const __grid_const
       unpack8(a[i], x);
       unpack8(b[i], y);
       if (turns && (is_q || is_k) && live) {
-        const float4 *cs = reinterpret_cast<const float4 *>(s_cs + un[i] * kMaxHalf + l * 8);   // two pairs each
+        const float4 *cs = reinterpret_cast<const float4 *>(s_cs + un[i] * kMaxHalf) + l;
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-          const float4 w = cs[e / 2];
+          const float4 w = cs[e / 2 * 8];
           const float p = x[e] * w.x - y[e] * w.y, q = x[e + 1] * w.z - y[e + 1] * w.w;
           y[e] = y[e] * w.x + x[e] * w.y;
           y[e + 1] = y[e + 1] * w.z + x[e + 1] * w.w;
