@@ -8,26 +8,32 @@
 // its N puts all scores of one cached row into one thread's TMEM lane, and the
 // sum over query rows is that thread's alone. No exchange, no atomics, an order
 // that the shapes decide. The key's scale, slot and visibility are scalars of
-// its thread; lse and the bound of every query row come from shared memory.
+// its thread. What depends on the query row is read by every thread of the CTA,
+// 4 bytes a score: with bf16 pages lse is therefore part of the product, as three
+// more columns of the query rows (-lse / scale in bf16 parts) against ones. (As
+// factors and terms from shared memory, 16 warps' reads of 16 bytes for all
+// lanes took 2 k cycles of a unit's 3.3 k.)
 //
-// An item is four key tiles (512 rows) of one request and cached head, one for
-// each of four epilogue warpgroups; query rows pass by in chunks of up to 128,
-// each read once for all tiles. The items form one line, each as long as its
+// Query rows pass by in chunks of up to 128, each read once for all tiles of an
+// item. An item is a stretch of keys of one request and cached head, 128 of them
+// for each of four epilogue warpgroups at a time: chunks of up to 64 rows (decode
+// steps) take 1024 keys, two a thread, so that what an item costs by itself is
+// spread over more of them; wider ones 512. Neighbouring items of a head whose
+// rows are one chunk share it. The items form one line, each as long as its
 // chunks and what every item costs, cut into equal stretches, one per CTA.
 //
 // Warp roles:
 //   warp 0        K tiles by TMA, one box per page, two tiles to a stage, and the
 //                 slots' old values (and scales) by bulk copies, whole items ahead
 //   warps 1, 2    MMAs, of every other tile (one thread for all is short of time
-//                 with few query rows: some 900 cycles a tile)
+//                 with few query rows: some 900 cycles a tile; four: no gain)
 //   warp 3        walks the CTA's items ahead of the others
 //   warps 4..7    a chunk's query rows, their lse and bounds. bf16 pages: the rows
 //                 by TMA. e4m3 pages: in two e4m3 parts as paged_attn.cu has them:
 //                 K codes go to the tensor cores as they are, and the scores are
 //                 those whose sum lse is. (Codes converted to bf16 instead: 2.1 k
 //                 cycles a tile, the loads of a tile 0.7 k.)
-//   warps 8..23   four groups, one key per thread: exponentials and sums
-// Neighbouring items of a head whose rows are one chunk share it.
+//   warps 8..23   four groups: exponentials and sums
 #include <math.h>
 
 #include <type_traits>
@@ -46,39 +52,44 @@ struct MassArgs : PagedArgs {
   float decay;
   int tokens;       // query tokens of a chunk: tokens * group rows
   int columns;      // ... rounded up to the N of the MMA
-  int k_stages;     // tiles and chunks in shared memory, and where the chunks lie
+  int item_keys;    // keys of an item
+  int k_stages;     // stages of two tiles, and where the chunks lie
   int off_q, q_bytes;
+  float lse_scale;  // - 1 / scale
 };
 
-constexpr int kGroups = 4;       // epilogue warpgroups, and key tiles of an item
-constexpr int kItemKeys = kGroups * kTile;
+constexpr int kGroups = 4;       // epilogue warpgroups
+constexpr int kNarrow = 64;      // chunks of up to so many rows: two keys a thread (they are all of a request's rows: more
+                                 // would make chunks of 65 or more; so a stage is free again as soon as it is read)
 constexpr int kChunkRows = 128;
 constexpr int kAhead = 8;        // items prepared, the current one included
 constexpr int kInfo = 3;         // chunks whose rows' numbers are prepared
-constexpr int kSlots = 4;        // items whose slots are loaded
 constexpr int kItemLength = 2;   // what an item costs beside its chunks, in chunks
 
-template <int DH, bool FP8>
+template <int DH, bool FP8, bool NARROW, bool FOLD>
 struct MassCfg {
+  static constexpr int kPer = NARROW ? 2 : 1;                  // keys of a thread
+  static constexpr int kTiles = kGroups * kPer, kItemKeys = kTiles * kTile;
   static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);      // a K tile
   static constexpr int kStage = 2 * kRaw;
   static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);
   static constexpr int kQSt = 2;
   static constexpr int kMaxKSt = 6;
-  static constexpr int kOffK = 17408;                          // tiles, then chunks of query rows; before them what follows
+  static constexpr int kTables = 16128;                        // numbers, pieces and slots, before the barriers
+  static constexpr int kSlotBytes = kItemKeys * 5 + kItemKeys / 16 * 4;
+  static constexpr int kSlots = NARROW ? 2 : 4;                // items whose slots are loaded
+  static constexpr int kOffOnes = 17408;                       // FOLD: a key's ones, and lse's parts of kInfo chunks
+  static constexpr int kFold = FOLD ? kTile * 32 : 0;
+  static constexpr int kOffK = kOffOnes + (1 + kInfo) * kFold; // stages, then chunks of query rows
   static constexpr int kMost = 232448 - 1024;
   static constexpr int kThreads = 32 * (8 + 4 * kGroups);
-  // registers a thread: what the loading and MMA warps do not need goes to the
-  // groups (the sum is the launch's)
-  static constexpr int kRegsIssue = 56, kRegsRows = 72, kRegsSum = 88;
-  static_assert(kRegsIssue + kRegsRows + kGroups * kRegsSum <= (2 + kGroups) * 80, "registers");
   // Bytes of a chunk (bf16, or two e4m3 parts), and the stages that fit beside kQSt chunks.
   static int chunk_bytes(int columns) { return columns * DH * 2; }
   static int stages(int columns) {
     const int fit = (kMost - kOffK - kQSt * chunk_bytes(columns)) / kStage;
     return fit < kMaxKSt ? fit : kMaxKSt;
   }
-  static_assert((kMost - kOffK - kQSt * 128 * DH * 2) / kStage >= 2, "shared memory");
+  static_assert(kOffK % 1024 == 0 && (kMost - kOffK - kQSt * (NARROW ? kNarrow : kChunkRows) * DH * 2) / kStage >= 2, "shared memory");
 };
 
 // A place in a ring of n and the parity of its round: `full` barriers complete
@@ -110,10 +121,11 @@ struct alignas(16) Numbers {   // of a chunk's query rows
   int every[kChunkRows / 16];  // keys before it are seen by all of 16
 };
 
+template <int KEYS>
 struct alignas(16) Slots { // of an item's keys
-  float old[kItemKeys];
-  uint8_t scale[kItemKeys];
-  int page[kItemKeys / 16];    // cache row of the head's first slot of each page, -1: no page
+  float old[KEYS];
+  uint8_t scale[KEYS];
+  int page[KEYS / 16];     // cache row of the head's first slot of each page, -1: no page
 };
 
 struct MassStart {
@@ -123,7 +135,7 @@ struct MassStart {
 };
 
 __device__ __forceinline__ void mass_request(const MassArgs &a, const Extent &x, int &items, int &length) {
-  items = x.W > 0 ? (x.L + kItemKeys - 1) / kItemKeys * a.c.heads : 0;
+  items = x.W > 0 ? (x.L + a.item_keys - 1) / a.item_keys * a.c.heads : 0;
   length = (x.W + a.tokens - 1) / a.tokens + kItemLength;
 }
 
@@ -146,11 +158,14 @@ __device__ __forceinline__ void mass_start(const MassArgs &a, long long *s_sum, 
   if (lane == 31) s_sum[warp] = up;
   if (tid == 0) s_start->left = 0;
   __syncthreads();
-  long long total = 0, before = up - mine;
-  for (int w = 0; w < nt / 32; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
+  // the sums of all warps, and of those before this one
+  long long total = lane < nt / 32 ? s_sum[lane] : 0, before = lane < warp ? total : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
   }
+  before += up - mine;
   const long long per = quotient(total + gridDim.x - 1, gridDim.x), begin = per * blockIdx.x;
   if (begin >= before && begin < before + mine) {
     long long at = before;
@@ -220,33 +235,47 @@ __device__ __forceinline__ void stage_chunk(const MassArgs &a, const Extent &x, 
   }
 }
 
-// -lse, bound and the share in `every` of row n of chunk c, by whole warps of
+// lse, bound and the share in `every` of row n of chunk c, by whole warps of
 // neighbouring rows.
-__device__ __forceinline__ void numbers_of(const MassArgs &a, const Extent &x, int h, int c, int n, float &neg_lse, int &hi, int &every) {
+__device__ __forceinline__ void numbers_of(const MassArgs &a, const Extent &x, int h, int c, int n, float &lse, int &hi, int &every) {
   const int at = n / a.group, t = c * a.tokens + at;
   hi = 0;
-  neg_lse = 0.f;
+  lse = 0.f;
   if (at < a.tokens && t < x.W) {
     int lo;
-    const float lse = __ldg(&a.lse[static_cast<size_t>(x.q0 + t) * a.Hq + h * a.group + (n - at * a.group)]);
+    lse = __ldg(&a.lse[static_cast<size_t>(x.q0 + t) * a.Hq + h * a.group + (n - at * a.group)]);
     visible(a, x.pos, t, x.L, lo, hi);
-    if (lse == -INFINITY) hi = 0;
-    neg_lse = lse * -1.4426950408889634f;
+    if (lse == -INFINITY) {
+      hi = 0;
+      lse = 0.f;
+    }
   }
   every = hi;
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) every = min(every, __shfl_xor_sync(0xffffffffu, every, o));
 }
 
-template <int DH, bool FP8>
-__global__ void __launch_bounds__(MassCfg<DH, FP8>::kThreads, 1)
+// y as three bf16 parts that add up to it within 2^-24 (an infinity: itself and zeros).
+__device__ __forceinline__ uint4 three_parts(float y) {
+  const uint32_t hi = f32_to_bf16(y);
+  const bool whole = (hi & 0x7fffu) == 0x7f80u;
+  const float r = whole ? 0.f : y - bf16_to_f32(static_cast<uint16_t>(hi));
+  const uint32_t mid = f32_to_bf16(r), lo = f32_to_bf16(r - bf16_to_f32(static_cast<uint16_t>(mid)));
+  return make_uint4(hi | (mid << 16), lo, 0u, 0u);
+}
+
+template <int DH, bool FP8, bool NARROW, bool FOLD>
+__global__ void __launch_bounds__(MassCfg<DH, FP8, NARROW, FOLD>::kThreads, 1)
 mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ MassArgs a) {
-  using C = MassCfg<DH, FP8>;
-  constexpr int kQSt = C::kQSt, kTables = 16128;
+  using C = MassCfg<DH, FP8, NARROW, FOLD>;
+  using SlotsOf = Slots<C::kItemKeys>;
+  static_assert(sizeof(SlotsOf) == C::kSlotBytes && !(FP8 && FOLD), "slots");
+  constexpr int kQSt = C::kQSt, kTables = C::kTables, kSlots = C::kSlots;
+  constexpr int kWidth = NARROW ? kNarrow : kChunkRows;        // columns of a tile's scores
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Numbers *numbers = reinterpret_cast<Numbers *>(smem);                      // [kInfo]
-  Slots *slots = reinterpret_cast<Slots *>(numbers + kInfo);                 // [kSlots]
+  SlotsOf *slots = reinterpret_cast<SlotsOf *>(numbers + kInfo);             // [kSlots]
   MassPiece *pieces = reinterpret_cast<MassPiece *>(slots + kSlots);         // [kAhead]
   uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + kTables);           // [k_stages]
   uint64_t *k_empty = k_full + C::kMaxKSt;
@@ -256,27 +285,27 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   uint64_t *n_empty = n_full + kInfo;
   uint64_t *slot_full = n_empty + kInfo;   // [kSlots]
   uint64_t *slot_empty = slot_full + kSlots;
-  uint64_t *s_full = slot_empty + kSlots;  // [group][2]
-  uint64_t *s_empty = s_full + 2 * kGroups;
-  uint64_t *piece_full = s_empty + 2 * kGroups;   // [kAhead]
+  uint64_t *s_full = slot_empty + kSlots;  // [kTiles] scores of a tile
+  uint64_t *s_empty = s_full + C::kTiles;
+  uint64_t *piece_full = s_empty + C::kTiles;     // [kAhead]
   uint64_t *piece_empty = piece_full + kAhead;
   long long *s_sum = reinterpret_cast<long long *>(piece_empty + kAhead);    // [24]
   MassStart *start = reinterpret_cast<MassStart *>(s_sum + 24);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  static_assert(kInfo * sizeof(Numbers) + kSlots * sizeof(Slots) + kAhead * sizeof(MassPiece) <= kTables && kTables % 16 == 0, "tables");
-  static_assert(kTables + (2 * C::kMaxKSt + 2 * kQSt + 2 * kInfo + 2 * kSlots + 4 * kGroups + 2 * kAhead + 24) * 8 + sizeof(MassStart) + 8 <= C::kOffK,
-                "barriers");
+  static_assert(kInfo * sizeof(Numbers) + kSlots * sizeof(SlotsOf) + kAhead * sizeof(MassPiece) <= kTables && kTables % 16 == 0, "tables");
+  static_assert(kTables + (2 * C::kMaxKSt + 2 * kQSt + 2 * kInfo + 2 * kSlots + 2 * C::kTiles + 2 * kAhead + 24) * 8 + sizeof(MassStart) + 8 <=
+                    C::kOffOnes, "barriers");
   uint8_t *const tiles_at = smem + C::kOffK, *const rows_at = smem + a.off_q;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.k_stages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 2); }
-    for (int s = 0; s < kQSt; ++s) { mbar_init(&q_full[s], FP8 ? 4 : 1); mbar_init(&q_empty[s], 2); }
+    for (int s = 0; s < kQSt; ++s) { mbar_init(&q_full[s], FP8 ? 4 : 5); mbar_init(&q_empty[s], 2); }
     for (int s = 0; s < kInfo; ++s) { mbar_init(&n_full[s], 4); mbar_init(&n_empty[s], 4 * kGroups); }
     for (int s = 0; s < kSlots; ++s) { mbar_init(&slot_full[s], 1); mbar_init(&slot_empty[s], 4 * kGroups); }
-    for (int s = 0; s < 2 * kGroups; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], 4); }
+    for (int s = 0; s < C::kTiles; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], 4); }
     for (int s = 0; s < kAhead; ++s) {
       mbar_init(&piece_full[s], 1);
       mbar_init(&piece_empty[s], 1 + 2 + 4 + 4 * kGroups);   // the warps that read it
@@ -290,6 +319,14 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  if constexpr (FOLD) {
+    // ones, and the second half of each of lse's rows, which stays 0
+    for (int n = threadIdx.x; n < kTile * 2; n += C::kThreads)
+      *reinterpret_cast<uint4 *>(smem + C::kOffOnes + n * 16) = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    for (int n = threadIdx.x; n < kInfo * kChunkRows; n += C::kThreads)
+      *reinterpret_cast<uint4 *>(smem + C::kOffOnes + C::kFold + n / 8 * 256 + 128 + n % 8 * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -297,9 +334,6 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 
   pdl_wait();   // everything that is read may come from the previous kernel
   mass_start(a, s_sum, start);
-
-  // scores of a group: two buffers of up to 64 columns, or one
-  const bool two = a.columns <= 64;
 
   // The item of number `seg`, or null when there is none (or a wait gave up:
   // then the slot is not read). By a whole warp.
@@ -315,37 +349,53 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
 
   if (warp == 0) {
     // --------------------------------------------------------------- K tiles, slots
-    const int page_rows = 1 << a.c.page_shift, per_tile = kTile >> a.c.page_shift;
+    constexpr int kPages = C::kItemKeys / 16 / 32;      // pages of a lane, at most: lane + 32 q
+    const int page_rows = 1 << a.c.page_shift, per_tile = kTile >> a.c.page_shift, item_pages = C::kItemKeys >> a.c.page_shift;
     const int none = static_cast<int>((static_cast<long long>(a.c.num_pages) * a.c.heads << a.c.page_shift) / 8);
-    // this lane's page of an item, looked up while the item before it waits for room
-    auto look_up = [&](const MassPiece *p) {
-      const int u = p->key0 + lane * page_rows;
-      if (lane >= kGroups * per_tile || u >= p->x.L) return 0;
-      return __ldg(a.c.table + static_cast<size_t>(p->i) * a.c.max_pages + (u >> a.c.page_shift));
+    // this lane's pages of an item, looked up while the item before it waits for room
+    auto look_up = [&](const MassPiece *p, int (&page)[kPages]) {
+#pragma unroll
+      for (int q = 0; q < kPages; ++q) {
+        const int n = lane + 32 * q, u = p->key0 + n * page_rows;
+        page[q] = 0;
+        if (n < item_pages && u < p->x.L)
+          page[q] = __ldg(a.c.table + static_cast<size_t>(p->i) * a.c.max_pages + (u >> a.c.page_shift));
+      }
     };
     bool ok = true;
     Ring k, sl;
     uint32_t n = 0, items = 0;
+    int page[kPages], page_next[kPages] = {};
     const MassPiece *p = piece(0);
-    int page = p ? look_up(p) : 0;
+    if (p) look_up(p, page);
     for (uint32_t seg = 0; ok && p; ++seg) {
       const int tiles = p->first < p->chunks ? p->tiles : 0;
-      const bool mine = lane < kGroups * per_tile, held = mine && p->key0 + lane * page_rows < p->x.L;
-      const bool bad = held && (page < 0 || page >= a.c.num_pages), live = held && !bad;
-      if (bad) atomicOr(a.status, DLLM_DEV_PAGE);
-      const int row = ((page * a.c.heads + p->h) << a.c.page_shift);
+      int row[kPages];             // cache row of the head's first slot of the page, -1: none
+      int pages = 0;
+#pragma unroll
+      for (int q = 0; q < kPages; ++q) {
+        const int at = lane + 32 * q;
+        const bool held = at < item_pages && p->key0 + at * page_rows < p->x.L, bad = held && (page[q] < 0 || page[q] >= a.c.num_pages);
+        if (bad) atomicOr(a.status, DLLM_DEV_PAGE);
+        row[q] = held && !bad ? (page[q] * a.c.heads + p->h) << a.c.page_shift : -1;
+        pages += __popc(__ballot_sync(0xffffffffu, row[q] >= 0));
+      }
       const MassPiece *p_next = piece(seg + 1);
-      const int page_next = p_next ? look_up(p_next) : 0;
+      if (p_next) look_up(p_next, page_next);
       ok = warp_wait(&slot_empty[sl.at], sl.round ^ 1, abort_flag);
       if (!ok) break;
-      Slots &s = slots[sl.at];
-      if (mine) s.page[lane] = live ? row : -1;
-      const int pages = __popc(__ballot_sync(0xffffffffu, live));
+      SlotsOf &s = slots[sl.at];
+#pragma unroll
+      for (int q = 0; q < kPages; ++q)
+        if (lane + 32 * q < item_pages) s.page[lane + 32 * q] = row[q];
+      __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(&slot_full[sl.at], pages * page_rows * (FP8 ? 5 : 4));
       __syncwarp();
-      if (live) {
-        bulk_load(s.old + lane * page_rows, a.mass + row, page_rows * 4, &slot_full[sl.at]);
-        if constexpr (FP8) bulk_load(s.scale + lane * page_rows, a.c.k_scale + row, page_rows, &slot_full[sl.at]);
+#pragma unroll
+      for (int q = 0; q < kPages; ++q) {
+        if (row[q] < 0) continue;
+        bulk_load(s.old + (lane + 32 * q) * page_rows, a.mass + row[q], page_rows * 4, &slot_full[sl.at]);
+        if constexpr (FP8) bulk_load(s.scale + (lane + 32 * q) * page_rows, a.c.k_scale + row[q], page_rows, &slot_full[sl.at]);
       }
       sl.next(kSlots);
       ++items;
@@ -354,15 +404,20 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&k_full[k.at], C::kStage);
         __syncwarp();
-        const int at = lane - j * per_tile;
-        if (at >= 0 && at < 2 * per_tile)      // (what there is none of reads as zeros)
-          tma_load_4d(tiles_at + k.at * C::kStage + at * page_rows * (C::kRaw / kTile), &tm_k, &k_full[k.at], live ? row / 8 : none);
+#pragma unroll
+        for (int q = 0; q < kPages; ++q) {
+          const int at = lane + 32 * q - j * per_tile;
+          if (at >= 0 && at < 2 * per_tile)      // (what there is none of reads as zeros)
+            tma_load_4d(tiles_at + k.at * C::kStage + at * page_rows * (C::kRaw / kTile), &tm_k, &k_full[k.at],
+                        row[q] >= 0 ? row[q] / 8 : none);
+        }
         k.next(a.k_stages);
         ++n;
       }
       piece_done(seg);
       p = p_next;
-      page = page_next;
+#pragma unroll
+      for (int q = 0; q < kPages; ++q) page[q] = page_next[q];
     }
     // after an abort the loads in flight land before the CTA's memory is given up
     if (!ok || *abort_flag) {
@@ -373,11 +428,11 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   } else if (warp <= 2) {
     // --------------------------------------------------------------- MMAs
     // (one elected thread through the whole loop: see paged_rows.cu)
-    const int j = warp - 1;         // tiles j and j + 2 of the item: those of a stage's two
+    const int j = warp - 1;         // tiles j, j + 2, ..: one of a stage's two
     if (elect_one()) {
       bool ok = true;
-      Ring t, q;                    // stages, chunks
-      uint32_t ns[2] = {0, 0};      // units of the two groups
+      Ring t, q, in;                // stages, chunks, lse
+      uint32_t ns[C::kTiles / 2] = {};   // units of the tiles
       for (uint32_t seg = 0; ok; ++seg) {
         const uint32_t pi = seg % kAhead;
         ok = mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
@@ -385,29 +440,34 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         const MassPiece &p = pieces[pi];
         const int first = p.first, chunks = p.chunks, W = p.x.W, tiles = p.tiles;
         const bool again = p.again, keep = p.keep;
+        Ring stage = t;
         for (int c = first; ok && c < chunks; ++c) {
           if (!again) ok = mbar_wait(&q_full[q.at], q.round, abort_flag);
           const uint32_t sq = smem_u32(rows_at + q.at * a.q_bytes);
           const int columns = chunk_columns(a, W, c);
-          Ring stage = t;
+          stage = t;
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
+          for (int s = 0; s < C::kTiles / 2; ++s) {
             if (2 * s >= tiles || !ok) break;
             const int tile = 2 * s + j;
             if (c == first) ok = mbar_wait(&k_full[stage.at], stage.round, abort_flag);
             if (ok && tile < tiles) {
-              const uint32_t b = two ? ns[s] & 1 : 0, t_s = tmem + tile * 128 + b * 64;
-              ok = mbar_wait(&s_empty[tile * 2 + b], ((two ? ns[s] / 2 : ns[s]) & 1) ^ 1, abort_flag);
+              const uint32_t t_s = tmem + tile * kWidth;
+              ok = mbar_wait(&s_empty[tile], (ns[s] & 1) ^ 1, abort_flag);
               if (!ok) break;
               tc_fence_after();
               const uint32_t sk = smem_u32(tiles_at + stage.at * C::kStage + j * C::kRaw);
               if constexpr (!FP8) {
                 const uint32_t idesc = idesc_bf16(128, columns, 0, 0);
                 const uint64_t dk = sw128_desc(sk, 16, C::kGroup8), dq = sw128_desc(sq, 16, 1024);
+                if constexpr (FOLD) {
+                  const uint32_t ones = smem_u32(smem + C::kOffOnes);
+                  umma_bf16(t_s, plain_desc(ones, 128, 256), plain_desc(ones + (1 + in.at) * C::kFold, 128, 256), idesc, 0);
+                }
 #pragma unroll
                 for (int kk = 0; kk < DH / 16; ++kk)
                   umma_bf16(t_s, dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                            dq + (((kk >> 2) * (a.columns * 128) + (kk & 3) * 32) >> 4), idesc, kk > 0);
+                            dq + (((kk >> 2) * (a.columns * 128) + (kk & 3) * 32) >> 4), idesc, FOLD || kk > 0);
               } else {
                 const uint32_t idesc = idesc_f8(128, columns, kE4M3, kE4M3, 0, 0);
                 const uint64_t dk = DH == 128 ? sw128_desc(sk, 16, C::kGroup8) : sw64_desc(sk, 16, C::kGroup8);
@@ -419,7 +479,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                   for (int kk = 0; kk < DH / 32; ++kk) umma_f8(t_s, dk + ((kk * 32) >> 4), dq + ((kk * 32) >> 4), idesc, part + kk > 0);
                 }
               }
-              umma_commit(&s_full[tile * 2 + b]);
+              umma_commit(&s_full[tile]);
               ++ns[s];
             }
             if (ok && c + 1 == chunks) umma_commit(&k_empty[stage.at]);
@@ -428,12 +488,10 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           if (!keep) {
             if (ok) umma_commit(&q_empty[q.at]);
             q.next(kQSt);
+            in.next(kInfo);
           }
         }
-        if (first < chunks) {
-          t.next(a.k_stages);
-          if (tiles > 2) t.next(a.k_stages);
-        }
+        t = stage;                  // behind the item's stages
         mbar_arrive(&piece_empty[pi]);
       }
     }
@@ -471,14 +529,14 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         fresh = fresh_of();
         divide();
       }
-      const int key0 = at * kItemKeys, chunks = length - kItemLength;
+      const int key0 = at * C::kItemKeys, chunks = length - kItemLength;
       // the chunk of the first row that sees a key
       auto first_of = [&](int key) {
         if (a.right < 0) return 0;
         const long long t = max(static_cast<long long>(key) - x.pos - a.right, 0ll);
         return t == 0 ? 0 : t < x.W ? static_cast<int>(t) / a.tokens : chunks;
       };
-      const bool keep = more && chunks == 1 && at + 1 < per_head && left > length && first_of(key0 + kItemKeys) < 1;
+      const bool keep = more && chunks == 1 && at + 1 < per_head && left > length && first_of(key0 + C::kItemKeys) < 1;
       if (lane == 0) {
         MassPiece &p = pieces[pi];
         p.more = more;
@@ -488,7 +546,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           p.h = h;
           p.key0 = key0;
           p.fresh = fresh;
-          p.tiles = min((x.L - key0 + kTile - 1) / kTile, kGroups);
+          p.tiles = min((x.L - key0 + kTile - 1) / kTile, C::kTiles);
           p.chunks = chunks;
           p.first = first_of(key0);
           p.again = again;
@@ -517,7 +575,8 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       const Extent x = p->x;
       const int chunks = p->chunks, h = p->h;
       for (int c = p->again ? chunks : p->first; ok && c < chunks; ++c) {
-        if (FP8 || warp == 4) ok = warp_wait(&q_empty[q.at], q.round ^ 1, abort_flag);
+        // (every warp waits: one that arrived twice in a round of q_full would complete it for another)
+        ok = warp_wait(&q_empty[q.at], q.round ^ 1, abort_flag);
         if (!ok) break;
         if (!FP8 && warp == 4) {
           if (lane == 0) {
@@ -530,13 +589,18 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           ++asked;
           __syncwarp();
         }
-        float neg_lse;
+        float lse;
         int hi, every;
-        numbers_of(a, x, h, c, n, neg_lse, hi, every);
+        numbers_of(a, x, h, c, n, lse, hi, every);
         ok = warp_wait(&n_empty[in.at], in.round ^ 1, abort_flag);
         if (!ok) break;
         Numbers &s = numbers[in.at];
-        s.neg_lse[n] = neg_lse;
+        if constexpr (FOLD) {
+          *reinterpret_cast<uint4 *>(smem + C::kOffOnes + (1 + in.at) * C::kFold + n / 8 * 256 + n % 8 * 16) = three_parts(lse * a.lse_scale);
+          fence_proxy_async_smem();
+        } else {
+          s.neg_lse[n] = lse * -1.4426950408889634f;
+        }
         s.hi[n] = hi;
         if (n % 16 == 0) s.every[n / 16] = every;
         if constexpr (FP8) {
@@ -544,9 +608,10 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           fence_proxy_async_smem();
         }
         __syncwarp();
+        // (groups with a tile read the numbers when its scores are there, MMAs wait for q_full)
         if (lane == 0) {
           mbar_arrive(&n_full[in.at]);
-          if (FP8) mbar_arrive(&q_full[q.at]);
+          mbar_arrive(&q_full[q.at]);
         }
         q.next(kQSt);
         in.next(kInfo);
@@ -558,55 +623,76 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     __syncwarp();
   } else {
     // --------------------------------------------------------------- exponentials and sums
+    constexpr int kPer = C::kPer;
     const int g = (warp - 8) >> 2, quarter = warp & 3;
-    const int key = g * kTile + quarter * 32 + lane;      // of the item
-    const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * 128;
+    const int key = g * kTile + quarter * 32 + lane;      // of the item, and key + kGroups * kTile
+    const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * kWidth;
     bool ok = true;
     Ring in, sl;
-    uint32_t ns = 0;
+    uint32_t ns[kPer] = {};
     for (uint32_t seg = 0; ok; ++seg) {
       const MassPiece *p = piece(seg);
       if (!p) break;
       ok = warp_wait(&slot_full[sl.at], sl.round, abort_flag);
       if (!ok) break;
-      const int u = p->key0 + key, chunks = p->chunks, W = p->x.W, end = p->key0 + (g + 1) * kTile;
-      const bool again = p->again, keep = p->keep, there = g < p->tiles;     // (this group's tile)
-      const Slots &slot = slots[sl.at];
-      const int page = slot.page[key >> a.c.page_shift];
-      const bool live = u < p->x.L && page >= 0;
-      const float c = FP8 && live ? a.scale_log2 * scale_of(slot.scale[key]) : a.scale_log2;
-      float sum = 0.f;
+      const int key0 = p->key0, L = p->x.L, W = p->x.W, chunks = p->chunks, tiles = p->tiles;
+      const bool again = p->again, keep = p->keep;
+      const SlotsOf &slot = slots[sl.at];
+      float c[kPer], sum[kPer] = {};
+      int page[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int k = key + i * kGroups * kTile;
+        page[i] = key0 + k < L ? slot.page[k >> a.c.page_shift] : -1;
+        c[i] = FP8 && page[i] >= 0 ? a.scale_log2 * scale_of(slot.scale[k]) : a.scale_log2;
+      }
+      const int end = key0 + (g + 1 + (kPer - 1) * kGroups) * kTile;   // behind the last of its keys
       for (int k = p->first; ok && k < chunks; ++k) {
-        if (!again) ok = warp_wait(&n_full[in.at], in.round, abort_flag);
-        if (ok && there) {
-          const uint32_t b = two ? ns & 1 : 0;
-          ok = warp_wait(&s_full[g * 2 + b], (two ? ns / 2 : ns) & 1, abort_flag);
+        if (g >= tiles) {
+          // no tile, no scores to wait for: but not ahead of the chunk
+          if (!again) ok = warp_wait(&n_full[in.at], in.round, abort_flag);
+        } else {
+          bool there[kPer];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            there[i] = g + i * kGroups < tiles;
+            if (there[i]) ok = ok && warp_wait(&s_full[g + i * kGroups], ns[i]++ & 1, abort_flag);
+          }
           if (ok) {
             tc_fence_after();
             const Numbers &s = numbers[in.at];
             const int columns = chunk_columns(a, W, k);
-            float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+            float2 acc[kPer][2] = {};
             auto add_some = [&](auto &x, int c0, auto masked) {
 #pragma unroll
-              for (int e = 0; e < static_cast<int>(sizeof(x) / 4); e += 4) {
-                const float4 z = *reinterpret_cast<const float4 *>(&s.neg_lse[c0 + e]);
-                float2 f0 = make_float2(c, c), f1 = f0;
-                if constexpr (FP8) {     // the row's factor and the key's first: no product on the way overflows
-                  const float4 f = *reinterpret_cast<const float4 *>(&s.scale[c0 + e]);
-                  f0 = __fmul2_rn(f0, make_float2(f.x, f.y));
-                  f1 = __fmul2_rn(f1, make_float2(f.z, f.w));
+              for (int e = 0; e < static_cast<int>(sizeof(x[0]) / 4); e += 4) {
+                float4 z{};
+                [[maybe_unused]] float4 f{};
+                int4 hi{};
+                if constexpr (!FOLD) z = *reinterpret_cast<const float4 *>(&s.neg_lse[c0 + e]);
+                if constexpr (FP8) f = *reinterpret_cast<const float4 *>(&s.scale[c0 + e]);
+                if constexpr (decltype(masked)::value) hi = *reinterpret_cast<const int4 *>(&s.hi[c0 + e]);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                  float2 f0 = make_float2(c[i], c[i]), f1 = f0;
+                  if constexpr (FP8) {     // the row's factor and the key's first: no product on the way overflows
+                    f0 = __fmul2_rn(f0, make_float2(f.x, f.y));
+                    f1 = __fmul2_rn(f1, make_float2(f.z, f.w));
+                  }
+                  float2 y0 = make_float2(__uint_as_float(x[i][e]), __uint_as_float(x[i][e + 1]));
+                  float2 y1 = make_float2(__uint_as_float(x[i][e + 2]), __uint_as_float(x[i][e + 3]));
+                  y0 = FOLD ? __fmul2_rn(y0, f0) : __ffma2_rn(y0, f0, make_float2(z.x, z.y));
+                  y1 = FOLD ? __fmul2_rn(y1, f1) : __ffma2_rn(y1, f1, make_float2(z.z, z.w));
+                  if constexpr (decltype(masked)::value) {
+                    const int u = key0 + key + i * kGroups * kTile;
+                    if (u >= hi.x) y0.x = -INFINITY;
+                    if (u >= hi.y) y0.y = -INFINITY;
+                    if (u >= hi.z) y1.x = -INFINITY;
+                    if (u >= hi.w) y1.y = -INFINITY;
+                  }
+                  acc[i][0] = __fadd2_rn(acc[i][0], make_float2(ex2_approx(y0.x), ex2_approx(y0.y)));
+                  acc[i][1] = __fadd2_rn(acc[i][1], make_float2(ex2_approx(y1.x), ex2_approx(y1.y)));
                 }
-                float2 y0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f0, make_float2(z.x, z.y));
-                float2 y1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), f1, make_float2(z.z, z.w));
-                if constexpr (decltype(masked)::value) {
-                  const int4 hi = *reinterpret_cast<const int4 *>(&s.hi[c0 + e]);
-                  if (u >= hi.x) y0.x = -INFINITY;
-                  if (u >= hi.y) y0.y = -INFINITY;
-                  if (u >= hi.z) y1.x = -INFINITY;
-                  if (u >= hi.w) y1.y = -INFINITY;
-                }
-                acc0 = __fadd2_rn(acc0, make_float2(ex2_approx(y0.x), ex2_approx(y0.y)));
-                acc1 = __fadd2_rn(acc1, make_float2(ex2_approx(y1.x), ex2_approx(y1.y)));
               }
             };
             // (a branch: as selects under a condition the comparisons are all computed)
@@ -614,35 +700,46 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
               if (end > every) add_some(x, c0, std::true_type{});
               else add_some(x, c0, std::false_type{});
             };
-            const uint32_t t = t_s + b * 64;
             int c0 = 0;
-            for (; c0 + 32 <= columns; c0 += 32) {
-              uint32_t x[32];
-              tmem_ld32(t + c0, x);
-              tmem_ld_wait();
-              add(x, c0, min(s.every[c0 / 16], s.every[c0 / 16 + 1]));
+            if constexpr (!NARROW) {
+              for (; c0 + 32 <= columns; c0 += 32) {
+                uint32_t x[1][32];
+                tmem_ld32(t_s + c0, x[0]);
+                tmem_ld_wait();
+                add(x, c0, min(s.every[c0 / 16], s.every[c0 / 16 + 1]));
+              }
             }
-            if (c0 < columns) {
-              uint32_t x[16];
-              tmem_ld16(t + c0, x);
+            for (; c0 < columns; c0 += 16) {
+              uint32_t x[kPer][16];
+              tmem_ld16(t_s + c0, x[0]);
+              if constexpr (kPer > 1) tmem_ld16(t_s + kGroups * kWidth + c0, x[kPer - 1]);   // (anything where there is no tile)
               tmem_ld_wait();
               add(x, c0, s.every[c0 / 16]);
             }
-            sum += (acc0.x + acc0.y) + (acc1.x + acc1.y);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[g * 2 + b]);
-            ++ns;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+              if (there[i] && lane == 0) mbar_arrive(&s_empty[g + i * kGroups]);
+              sum[i] += (acc[i][0].x + acc[i][0].y) + (acc[i][1].x + acc[i][1].y);
+            }
           }
         }
-        __syncwarp();
         if (!keep) {
+          __syncwarp();
           if (lane == 0) mbar_arrive(&n_empty[in.at]);
           in.next(kInfo);
         }
       }
-      if (ok && live)
-        a.mass[static_cast<size_t>(page) + (key & ((1 << a.c.page_shift) - 1))] = (u < p->fresh ? slot.old[key] * a.decay : 0.f) + sum;
+      if (ok) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int k = key + i * kGroups * kTile;
+          if (page[i] >= 0)
+            a.mass[static_cast<size_t>(page[i]) + (k & ((1 << a.c.page_shift) - 1))] =
+                (key0 + k < p->fresh ? slot.old[k] * a.decay : 0.f) + sum[i];
+        }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&slot_empty[sl.at]);
       sl.next(kSlots);
@@ -659,24 +756,39 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   if (threadIdx.x == 0 && *abort_flag) atomicOr(a.status, DLLM_DEV_WAIT_TIMEOUT);
 }
 
-template <int DH, bool FP8>
+template <int DH, bool FP8, bool NARROW, bool FOLD>
 dllm_status launch_mass(const dllm_kv_pages *pages, MassArgs &g, cudaStream_t s) {
-  using C = MassCfg<DH, FP8>;
+  using C = MassCfg<DH, FP8, NARROW, FOLD>;
   CUtensorMap tk, tq;
   const uint64_t rows = static_cast<uint64_t>(pages->num_pages) * pages->heads * pages->page_size;
   if (!make_tmap_page_rows(&tk, pages->k, rows, DH, FP8 ? 1 : 2, pages->page_size) ||
       !make_tmap_query_rows(&tq, g.q, g.q_rows, g.Hq, DH, g.q_stride, g.group, g.tokens))
     return DLLM_ERR_CUDA;
+  g.item_keys = C::kItemKeys;
   g.k_stages = C::stages(g.columns);
   g.off_q = C::kOffK + g.k_stages * C::kStage;
   g.q_bytes = C::chunk_bytes(g.columns);
   const int smem = g.off_q + C::kQSt * g.q_bytes + 1024;
-  auto kern = mass_kernel<DH, FP8>;
+  auto kern = mass_kernel<DH, FP8, NARROW, FOLD>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kMost + 1024);
-  const long long items = static_cast<long long>(g.B) * pages->heads * ((g.max_kv + kItemKeys - 1) / kItemKeys);
+  const long long items = static_cast<long long>(g.B) * pages->heads * ((g.max_kv + C::kItemKeys - 1) / C::kItemKeys);
   const int ctas = items < sm_budget() ? static_cast<int>(items) : sm_budget();
   if (e == cudaSuccess) e = launch_pdl(kern, dim3(ctas), dim3(C::kThreads), smem, s, tk, tq, g);
   return e == cudaSuccess ? launch_status() : cuda_error(e);
+}
+
+template <int DH>
+dllm_status launch_mass(const dllm_kv_pages *pages, float scale, MassArgs &g, cudaStream_t s) {
+  const bool narrow = g.columns <= kNarrow;
+  if (pages->type == DLLM_KV_E4M3)
+    return narrow ? launch_mass<DH, true, true, false>(pages, g, s) : launch_mass<DH, true, false, false>(pages, g, s);
+  // lse / scale has to be a number
+  const float size = fabsf(scale);
+  if (size >= 0x1p-40f && size <= 0x1p40f) {
+    g.lse_scale = -1.f / scale;
+    return narrow ? launch_mass<DH, false, true, true>(pages, g, s) : launch_mass<DH, false, false, true>(pages, g, s);
+  }
+  return narrow ? launch_mass<DH, false, true, false>(pages, g, s) : launch_mass<DH, false, false, false>(pages, g, s);
 }
 
 }  // namespace
@@ -713,7 +825,5 @@ extern "C" dllm_status dllm_attn_mass(const dllm_kv_pages *pages, const dllm_att
   cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&g.status), g_status_mass);
   if (e != cudaSuccess) return cuda_error(e);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool fp8 = pages->type == DLLM_KV_E4M3;
-  if (pages->dh == 64) return fp8 ? launch_mass<64, true>(pages, g, s) : launch_mass<64, false>(pages, g, s);
-  return fp8 ? launch_mass<128, true>(pages, g, s) : launch_mass<128, false>(pages, g, s);
+  return pages->dh == 64 ? launch_mass<64>(pages, a->scale, g, s) : launch_mass<128>(pages, a->scale, g, s);
 }
