@@ -24,7 +24,7 @@
 //
 // Warp roles:
 //   warp 0        K tiles by TMA, one box per page, two tiles to a stage, and the
-//                 slots' old values (and scales) by bulk copies, whole items ahead
+//                 slots' old values (and scales), whole items ahead
 //   warps 1, 2    MMAs, of every other tile (one thread for all is short of time
 //                 with few query rows: some 900 cycles a tile; four: no gain)
 //   warp 3        walks the CTA's items ahead of the others
@@ -304,7 +304,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     for (int s = 0; s < a.k_stages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 2); }
     for (int s = 0; s < kQSt; ++s) { mbar_init(&q_full[s], FP8 ? 4 : 5); mbar_init(&q_empty[s], 2); }
     for (int s = 0; s < kInfo; ++s) { mbar_init(&n_full[s], 4); mbar_init(&n_empty[s], 4 * kGroups); }
-    for (int s = 0; s < kSlots; ++s) { mbar_init(&slot_full[s], 1); mbar_init(&slot_empty[s], 4 * kGroups); }
+    for (int s = 0; s < kSlots; ++s) { mbar_init(&slot_full[s], 33); mbar_init(&slot_empty[s], 4 * kGroups); }
     for (int s = 0; s < C::kTiles; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], 4); }
     for (int s = 0; s < kAhead; ++s) {
       mbar_init(&piece_full[s], 1);
@@ -364,21 +364,19 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     };
     bool ok = true;
     Ring k, sl;
-    uint32_t n = 0, items = 0;
+    uint32_t n = 0;
     int page[kPages], page_next[kPages] = {};
     const MassPiece *p = piece(0);
     if (p) look_up(p, page);
     for (uint32_t seg = 0; ok && p; ++seg) {
       const int tiles = p->first < p->chunks ? p->tiles : 0;
       int row[kPages];             // cache row of the head's first slot of the page, -1: none
-      int pages = 0;
 #pragma unroll
       for (int q = 0; q < kPages; ++q) {
         const int at = lane + 32 * q;
         const bool held = at < item_pages && p->key0 + at * page_rows < p->x.L, bad = held && (page[q] < 0 || page[q] >= a.c.num_pages);
         if (bad) atomicOr(a.status, DLLM_DEV_PAGE);
         row[q] = held && !bad ? (page[q] * a.c.heads + p->h) << a.c.page_shift : -1;
-        pages += __popc(__ballot_sync(0xffffffffu, row[q] >= 0));
       }
       const MassPiece *p_next = piece(seg + 1);
       if (p_next) look_up(p_next, page_next);
@@ -389,16 +387,22 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       for (int q = 0; q < kPages; ++q)
         if (lane + 32 * q < item_pages) s.page[lane + 32 * q] = row[q];
       __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(&slot_full[sl.at], pages * page_rows * (FP8 ? 5 : 4));
-      __syncwarp();
-#pragma unroll
-      for (int q = 0; q < kPages; ++q) {
-        if (row[q] < 0) continue;
-        bulk_load(s.old + (lane + 32 * q) * page_rows, a.mass + row[q], page_rows * 4, &slot_full[sl.at]);
-        if constexpr (FP8) bulk_load(s.scale + (lane + 32 * q) * page_rows, a.c.k_scale + row[q], page_rows, &slot_full[sl.at]);
+      // the slots 16 bytes a lane (bulk copies, one per page: some 100 cycles each)
+#pragma unroll 4
+      for (int at = lane * 4; at < C::kItemKeys; at += 128) {
+        const int page = s.page[at >> a.c.page_shift];
+        if (page >= 0) copy16(s.old + at, a.mass + page + (at & (page_rows - 1)), true);
       }
+      if constexpr (FP8) {
+#pragma unroll
+        for (int at = lane * 16; at < C::kItemKeys; at += 512) {
+          const int page = s.page[at >> a.c.page_shift];
+          if (page >= 0) copy16(s.scale + at, a.c.k_scale + page + (at & (page_rows - 1)), true);
+        }
+      }
+      copies_arrive(&slot_full[sl.at]);
+      if (lane == 0) mbar_arrive(&slot_full[sl.at]);      // (the pages' rows are written)
       sl.next(kSlots);
-      ++items;
       for (int j = 0; ok && j < tiles; j += 2) {
         ok = warp_wait(&k_empty[k.at], k.round ^ 1, abort_flag);
         if (!ok) break;
@@ -422,7 +426,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     // after an abort the loads in flight land before the CTA's memory is given up
     if (!ok || *abort_flag) {
       if (lane < a.k_stages && lane < n) mbar_drain(&k_full[lane], ((n - 1 - lane) / a.k_stages) & 1);
-      if (lane < kSlots && lane < items) mbar_drain(&slot_full[lane], ((items - 1 - lane) / kSlots) & 1);
+      copies_wait();
     }
     __syncwarp();
   } else if (warp <= 2) {

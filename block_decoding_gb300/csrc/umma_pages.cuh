@@ -81,6 +81,11 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                :: "r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+// copies_arrive: one arrival on `bar` when they have (the barrier's count
+// includes it).
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // True in one lane of the (converged) warp, the same one every time.
