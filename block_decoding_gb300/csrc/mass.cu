@@ -29,11 +29,13 @@
 //                 with few query rows: some 900 cycles a tile; four: no gain)
 //   warp 3        walks the CTA's items ahead of the others
 //   warps 4..7    a chunk's query rows, their lse and bounds. bf16 pages: the rows
-//                 by TMA. e4m3 pages: in two e4m3 parts as paged_attn.cu has them:
-//                 K codes go to the tensor cores as they are, and the scores are
-//                 those whose sum lse is. (Codes converted to bf16 instead: 2.1 k
-//                 cycles a tile, the loads of a tile 0.7 k.)
-//   warps 8..23   four groups: exponentials and sums
+//                 by TMA. e4m3 pages and few rows: in two e4m3 parts as
+//                 paged_attn.cu has them, for K codes go to the tensor cores as
+//                 they are (converted to bf16 by four warps: 2.1 k cycles a tile,
+//                 the loads of a tile 0.7 k). With more rows the rows cost more
+//                 than the codes, and are needed once a chunk and item.
+//   warps 8..23   four groups: (e4m3 pages and many rows) codes to bf16,
+//                 exponentials and sums
 #include <math.h>
 
 #include <type_traits>
@@ -70,9 +72,12 @@ template <int DH, bool FP8, bool NARROW, bool FOLD>
 struct MassCfg {
   static constexpr int kPer = NARROW ? 2 : 1;                  // keys of a thread
   static constexpr int kTiles = kGroups * kPer, kItemKeys = kTiles * kTile;
-  static constexpr int kRaw = kTile * DH * (FP8 ? 1 : 2);      // a K tile
+  // e4m3 pages and few rows: the codes are the MMA's operand; else converted
+  static constexpr bool kCodes = FP8 && NARROW;
+  static constexpr int kLoad = kTile * DH * (FP8 ? 1 : 2);     // a K tile as it is loaded, to the end of its space
+  static constexpr int kRaw = kTile * DH * (kCodes ? 1 : 2);   // ... as the MMAs read it
   static constexpr int kStage = 2 * kRaw;
-  static constexpr int kGroup8 = 8 * DH * (FP8 ? 1 : 2);
+  static constexpr int kGroup8 = 8 * DH * (kCodes ? 1 : 2);
   static constexpr int kQSt = 2;
   static constexpr int kMaxKSt = 6;
   static constexpr int kTables = 16128;                        // numbers, pieces and slots, before the barriers
@@ -255,6 +260,42 @@ __device__ __forceinline__ void numbers_of(const MassArgs &a, const Extent &x, i
   for (int o = 8; o > 0; o >>= 1) every = min(every, __shfl_xor_sync(0xffffffffu, every, o));
 }
 
+// A tile of e4m3 codes, which the loads put into the upper half of its space
+// (DH-byte rows under their swizzle), to the bf16 rows that the codes and scales
+// stand for, exactly, in the layout of a bf16 tile. By 128 threads, of row `key`
+// each; all of them have read their codes before any writes (c_read). Returns
+// whether the wait for that went well.
+template <int DH>
+__device__ __forceinline__ bool convert_codes(uint8_t *tile, int key, uint32_t scale2, uint64_t *c_read, uint32_t parity,
+                                              volatile int *abort) {
+  constexpr int kChunks = DH / 16;
+  const uint8_t *src = tile + kTile * DH + key * DH;
+  uint4 w[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c)
+    w[c] = *reinterpret_cast<const uint4 *>(src + (DH == 128 ? c ^ (key & 7) : c ^ ((key >> 1) & 3)) * 16);
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) mbar_arrive(c_read);
+  if (!warp_wait(c_read, parity, abort)) return false;
+  uint8_t *dst = tile + (key / 8) * (8 * DH * 2) + (key % 8) * 128;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const uint32_t in[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+    uint32_t out[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint2 v = e4m3x4_to_bf16_0213(in[e]);
+      const uint32_t even = mul_bf16x2(v.x, scale2), odd = mul_bf16x2(v.y, scale2);
+      out[2 * e] = __byte_perm(even, odd, 0x5410);
+      out[2 * e + 1] = __byte_perm(even, odd, 0x7632);
+    }
+    uint8_t *d = dst + (c / 4) * 1024;   // 64 columns: eight 16-byte pieces
+    *reinterpret_cast<uint4 *>(d + (((2 * c) & 7) ^ (key & 7)) * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+    *reinterpret_cast<uint4 *>(d + (((2 * c + 1) & 7) ^ (key & 7)) * 16) = make_uint4(out[4], out[5], out[6], out[7]);
+  }
+  return true;
+}
+
 // y as three bf16 parts that add up to it within 2^-24 (an infinity: itself and zeros).
 __device__ __forceinline__ uint4 three_parts(float y) {
   const uint32_t hi = f32_to_bf16(y);
@@ -269,8 +310,9 @@ __global__ void __launch_bounds__(MassCfg<DH, FP8, NARROW, FOLD>::kThreads, 1)
 mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ MassArgs a) {
   using C = MassCfg<DH, FP8, NARROW, FOLD>;
   using SlotsOf = Slots<C::kItemKeys>;
-  static_assert(sizeof(SlotsOf) == C::kSlotBytes && !(FP8 && FOLD), "slots");
+  static_assert(sizeof(SlotsOf) == C::kSlotBytes && !(C::kCodes && FOLD), "slots");
   constexpr int kQSt = C::kQSt, kTables = C::kTables, kSlots = C::kSlots;
+  constexpr bool kCodes = C::kCodes, kConvert = FP8 && !kCodes;
   constexpr int kWidth = NARROW ? kNarrow : kChunkRows;        // columns of a tile's scores
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -287,14 +329,16 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   uint64_t *slot_empty = slot_full + kSlots;
   uint64_t *s_full = slot_empty + kSlots;  // [kTiles] scores of a tile
   uint64_t *s_empty = s_full + C::kTiles;
-  uint64_t *piece_full = s_empty + C::kTiles;     // [kAhead]
+  uint64_t *c_full = s_empty + C::kTiles;         // [kGroups] codes of a group's tile are bf16
+  uint64_t *c_read = c_full + kGroups;            // [kGroups] ... are read
+  uint64_t *piece_full = c_read + kGroups;        // [kAhead]
   uint64_t *piece_empty = piece_full + kAhead;
   long long *s_sum = reinterpret_cast<long long *>(piece_empty + kAhead);    // [24]
   MassStart *start = reinterpret_cast<MassStart *>(s_sum + 24);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   static_assert(kInfo * sizeof(Numbers) + kSlots * sizeof(SlotsOf) + kAhead * sizeof(MassPiece) <= kTables && kTables % 16 == 0, "tables");
-  static_assert(kTables + (2 * C::kMaxKSt + 2 * kQSt + 2 * kInfo + 2 * kSlots + 2 * C::kTiles + 2 * kAhead + 24) * 8 + sizeof(MassStart) + 8 <=
+  static_assert(kTables + (2 * C::kMaxKSt + 2 * kQSt + 2 * kInfo + 2 * kSlots + 2 * C::kTiles + 2 * kGroups + 2 * kAhead + 24) * 8 + sizeof(MassStart) + 8 <=
                     C::kOffOnes, "barriers");
   uint8_t *const tiles_at = smem + C::kOffK, *const rows_at = smem + a.off_q;
 
@@ -302,9 +346,10 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.k_stages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 2); }
-    for (int s = 0; s < kQSt; ++s) { mbar_init(&q_full[s], FP8 ? 4 : 5); mbar_init(&q_empty[s], 2); }
+    for (int s = 0; s < kQSt; ++s) { mbar_init(&q_full[s], kCodes ? 4 : 5); mbar_init(&q_empty[s], 2); }
     for (int s = 0; s < kInfo; ++s) { mbar_init(&n_full[s], 4); mbar_init(&n_empty[s], 4 * kGroups); }
     for (int s = 0; s < kSlots; ++s) { mbar_init(&slot_full[s], 33); mbar_init(&slot_empty[s], 4 * kGroups); }
+    for (int s = 0; s < kGroups; ++s) { mbar_init(&c_full[s], 4); mbar_init(&c_read[s], 4); }
     for (int s = 0; s < C::kTiles; ++s) { mbar_init(&s_full[s], 1); mbar_init(&s_empty[s], 4); }
     for (int s = 0; s < kAhead; ++s) {
       mbar_init(&piece_full[s], 1);
@@ -313,7 +358,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm_k);
-    if (!FP8) tma_prefetch_desc(&tm_q);
+    if (!kCodes) tma_prefetch_desc(&tm_q);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -350,7 +395,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   if (warp == 0) {
     // --------------------------------------------------------------- K tiles, slots
     constexpr int kPages = C::kItemKeys / 16 / 32;      // pages of a lane, at most: lane + 32 q
-    const int page_rows = 1 << a.c.page_shift, per_tile = kTile >> a.c.page_shift, item_pages = C::kItemKeys >> a.c.page_shift;
+    const int page_rows = 1 << a.c.page_shift, item_pages = C::kItemKeys >> a.c.page_shift;
     const int none = static_cast<int>((static_cast<long long>(a.c.num_pages) * a.c.heads << a.c.page_shift) / 8);
     // this lane's pages of an item, looked up while the item before it waits for room
     auto look_up = [&](const MassPiece *p, int (&page)[kPages]) {
@@ -406,14 +451,14 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       for (int j = 0; ok && j < tiles; j += 2) {
         ok = warp_wait(&k_empty[k.at], k.round ^ 1, abort_flag);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&k_full[k.at], C::kStage);
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[k.at], 2 * C::kLoad);
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < kPages; ++q) {
-          const int at = lane + 32 * q - j * per_tile;
-          if (at >= 0 && at < 2 * per_tile)      // (what there is none of reads as zeros)
-            tma_load_4d(tiles_at + k.at * C::kStage + at * page_rows * (C::kRaw / kTile), &tm_k, &k_full[k.at],
-                        row[q] >= 0 ? row[q] / 8 : none);
+          const int at = (lane + 32 * q) * page_rows - j * kTile;   // row of the stage
+          if (at >= 0 && at < 2 * kTile)      // (what there is none of reads as zeros)
+            tma_load_4d(tiles_at + k.at * C::kStage + (at / kTile + 1) * C::kRaw - C::kLoad + at % kTile * (C::kLoad / kTile), &tm_k,
+                        &k_full[k.at], row[q] >= 0 ? row[q] / 8 : none);
         }
         k.next(a.k_stages);
         ++n;
@@ -437,6 +482,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       bool ok = true;
       Ring t, q, in;                // stages, chunks, lse
       uint32_t ns[C::kTiles / 2] = {};   // units of the tiles
+      uint32_t nc[C::kTiles / 2] = {};   // tiles converted
       for (uint32_t seg = 0; ok; ++seg) {
         const uint32_t pi = seg % kAhead;
         ok = mbar_wait(&piece_full[pi], (seg / kAhead) & 1, abort_flag);
@@ -457,11 +503,12 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
             if (c == first) ok = mbar_wait(&k_full[stage.at], stage.round, abort_flag);
             if (ok && tile < tiles) {
               const uint32_t t_s = tmem + tile * kWidth;
-              ok = mbar_wait(&s_empty[tile], (ns[s] & 1) ^ 1, abort_flag);
+              if (kConvert && c == first) ok = mbar_wait(&c_full[tile], nc[s]++ & 1, abort_flag);
+              ok = ok && mbar_wait(&s_empty[tile], (ns[s] & 1) ^ 1, abort_flag);
               if (!ok) break;
               tc_fence_after();
               const uint32_t sk = smem_u32(tiles_at + stage.at * C::kStage + j * C::kRaw);
-              if constexpr (!FP8) {
+              if constexpr (!kCodes) {
                 const uint32_t idesc = idesc_bf16(128, columns, 0, 0);
                 const uint64_t dk = sw128_desc(sk, 16, C::kGroup8), dq = sw128_desc(sq, 16, 1024);
                 if constexpr (FOLD) {
@@ -582,7 +629,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         // (every warp waits: one that arrived twice in a round of q_full would complete it for another)
         ok = warp_wait(&q_empty[q.at], q.round ^ 1, abort_flag);
         if (!ok) break;
-        if (!FP8 && warp == 4) {
+        if (!kCodes && warp == 4) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&q_full[q.at], a.tokens * a.group * (DH * 2));
 #pragma unroll
@@ -607,7 +654,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
         }
         s.hi[n] = hi;
         if (n % 16 == 0) s.every[n / 16] = every;
-        if constexpr (FP8) {
+        if constexpr (kCodes) {
           stage_chunk<DH>(a, x, h, c, rows_at + q.at * a.q_bytes, s.scale, n);
           fence_proxy_async_smem();
         }
@@ -622,7 +669,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       }
       piece_done(seg);
     }
-    if (!FP8 && (!ok || *abort_flag))
+    if (!kCodes && (!ok || *abort_flag))
       if (lane < kQSt && lane < asked) mbar_drain(&q_full[lane], ((asked - 1 - lane) / kQSt) & 1);
     __syncwarp();
   } else {
@@ -633,7 +680,9 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
     const uint32_t t_s = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + g * kWidth;
     bool ok = true;
     Ring in, sl;
+    [[maybe_unused]] Ring t;
     uint32_t ns[kPer] = {};
+    [[maybe_unused]] uint32_t nc = 0;
     for (uint32_t seg = 0; ok; ++seg) {
       const MassPiece *p = piece(seg);
       if (!p) break;
@@ -648,9 +697,29 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       for (int i = 0; i < kPer; ++i) {
         const int k = key + i * kGroups * kTile;
         page[i] = key0 + k < L ? slot.page[k >> a.c.page_shift] : -1;
-        c[i] = FP8 && page[i] >= 0 ? a.scale_log2 * scale_of(slot.scale[k]) : a.scale_log2;
+        c[i] = kCodes && page[i] >= 0 ? a.scale_log2 * scale_of(slot.scale[k]) : a.scale_log2;
       }
       const int end = key0 + (g + 1 + (kPer - 1) * kGroups) * kTile;   // behind the last of its keys
+      if constexpr (kConvert) {
+        if (p->first < chunks) {
+          Ring stage = t;
+          t.next(a.k_stages);
+          if (tiles > 2) t.next(a.k_stages);
+          if (g >= 2) stage.next(a.k_stages);
+          if (g < tiles) {
+            ok = warp_wait(&k_full[stage.at], stage.round, abort_flag);
+            if (ok) {
+              const uint32_t byte = page[0] >= 0 ? slot.scale[key] : 127u;      // (codes of no page are 0)
+              ok = convert_codes<DH>(tiles_at + stage.at * C::kStage + (g & 1) * C::kRaw, key % kTile, bf16x2_of(scale_of(byte)),
+                                     &c_read[g], nc & 1, abort_flag);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c_full[g]);
+            ++nc;
+          }
+        }
+      }
       for (int k = p->first; ok && k < chunks; ++k) {
         if (g >= tiles) {
           // no tile, no scores to wait for: but not ahead of the chunk
@@ -674,12 +743,12 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
                 [[maybe_unused]] float4 f{};
                 int4 hi{};
                 if constexpr (!FOLD) z = *reinterpret_cast<const float4 *>(&s.neg_lse[c0 + e]);
-                if constexpr (FP8) f = *reinterpret_cast<const float4 *>(&s.scale[c0 + e]);
+                if constexpr (kCodes) f = *reinterpret_cast<const float4 *>(&s.scale[c0 + e]);
                 if constexpr (decltype(masked)::value) hi = *reinterpret_cast<const int4 *>(&s.hi[c0 + e]);
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
                   float2 f0 = make_float2(c[i], c[i]), f1 = f0;
-                  if constexpr (FP8) {     // the row's factor and the key's first: no product on the way overflows
+                  if constexpr (kCodes) {  // the row's factor and the key's first: no product on the way overflows
                     f0 = __fmul2_rn(f0, make_float2(f.x, f.y));
                     f1 = __fmul2_rn(f1, make_float2(f.z, f.w));
                   }
@@ -783,16 +852,19 @@ dllm_status launch_mass(const dllm_kv_pages *pages, MassArgs &g, cudaStream_t s)
 
 template <int DH>
 dllm_status launch_mass(const dllm_kv_pages *pages, float scale, MassArgs &g, cudaStream_t s) {
-  const bool narrow = g.columns <= kNarrow;
-  if (pages->type == DLLM_KV_E4M3)
-    return narrow ? launch_mass<DH, true, true, false>(pages, g, s) : launch_mass<DH, true, false, false>(pages, g, s);
+  const bool narrow = g.columns <= kNarrow, fp8 = pages->type == DLLM_KV_E4M3;
+  if (fp8 && narrow) return launch_mass<DH, true, true, false>(pages, g, s);
   // lse / scale has to be a number
   const float size = fabsf(scale);
   if (size >= 0x1p-40f && size <= 0x1p40f) {
     g.lse_scale = -1.f / scale;
-    return narrow ? launch_mass<DH, false, true, true>(pages, g, s) : launch_mass<DH, false, false, true>(pages, g, s);
+    return fp8      ? launch_mass<DH, true, false, true>(pages, g, s)
+           : narrow ? launch_mass<DH, false, true, true>(pages, g, s)
+                    : launch_mass<DH, false, false, true>(pages, g, s);
   }
-  return narrow ? launch_mass<DH, false, true, false>(pages, g, s) : launch_mass<DH, false, false, false>(pages, g, s);
+  return fp8      ? launch_mass<DH, true, false, false>(pages, g, s)
+         : narrow ? launch_mass<DH, false, true, false>(pages, g, s)
+                  : launch_mass<DH, false, false, false>(pages, g, s);
 }
 
 }  // namespace

@@ -448,6 +448,41 @@ def test_mass_of_scores_that_are_large():
     check_mass(b, mass, torch.zeros_like(mass), lse)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -45, -0.125, 3.0])
+@pytest.mark.parametrize("w", [3, 80])
+def test_mass_at_any_scale(w, scale, fp8):
+    b = Batch(56, [130, 700, 20], 2, 64, 16, fp8, spread=0.1)
+    b.queries([w, w, 7], 1, 0.3)
+    _, lse = b.run(right=0, scale=scale)
+    mass = mass_of(b)
+    old = mass.clone()
+    bd.attn_mass(b.q, lse, b.pages, mass, i32(b.q_off), i32(b.lens), b.table, max(w, 7), 700, right=0, scale=scale)
+    check_mass(b, mass, old, lse, right=0, scale=scale)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("dh,page", [(64, 16), (128, 128)])
+def test_mass_of_long_requests_and_many_rows(dh, page, fp8):
+    # more items than CTAs, chunks that come by several times, rows of several requests behind each other
+    b = Batch(57, [6000, 5000, 1, 4100], 8, dh, page, fp8, spread=0.1)
+    b.queries([130, 300, 1, 65], 2, behind=3)
+    pos = [6000 - 130, 100, 0, 4000]
+    _, lse = b.run(pos=pos, right=0)
+    mass = torch.zeros(tuple(b.pages.k.shape[:3]), device=DEV)
+    bd.attn_mass(b.q, lse, b.pages, mass, i32(b.q_off), i32(b.lens), b.table, 300, 6000, q_pos=i32(pos), right=0)
+    check_mass(b, mass, torch.zeros_like(mass), lse, pos=pos, right=0)
+    # single tokens of many requests
+    lens = [int(n) for n in np.random.default_rng(58).integers(1, 2500, 40)]
+    b = Batch(59, lens, 4, dh, page, fp8, spread=0.1)
+    b.queries([1] * 40, 3)
+    _, lse = b.run(right=0)
+    mass = mass_of(b)
+    old = mass.clone()
+    bd.attn_mass(b.q, lse, b.pages, mass, i32(b.q_off), i32(b.lens), b.table, 1, 2500, right=0, decay=0.5)
+    check_mass(b, mass, old, lse, right=0, decay=0.5)
+
+
 def test_mass_reports_what_it_does_not_reach():
     b = Batch(54, [200, 100], 1, 64, 16, False)
     b.queries([6, 4], 1)
@@ -648,6 +683,103 @@ def test_eviction_reports_lengths_beyond_their_bounds():
     assert new.tolist() == [8, 0] and (keep[1] == -1).all()
     for h in range(2):
         assert np.array_equal(keep.cpu().numpy()[0, h], cache_ops.keep(m[pg, h, sl], 8, 0, 0))
+
+
+@pytest.mark.parametrize("n", [49152, 49153, 70001])
+def test_eviction_from_long_requests(n):
+    # more weights than shared memory holds, and just as many
+    p = Pool(92, [n, 300], 1, 64, 128, True)
+    m = f64(p.mass)
+    pg, sl = slots(p.table, 128, 0, n)
+    lists = [[cache_ops.keep(m[pg, 0, sl], 5000, 4, 100)], [list(range(300))]]
+    want = p.moved(lists, [0, 0], True, True)
+    new, keep = bd.kv_evict(p.pages, p.mass, i32([n, 300]), i32(p.table), 5000, n, sinks=4, recent=100)
+    assert new.tolist() == [5000, 300] and keep[0, 0].tolist() == lists[0][0]
+    p.check(want)
+
+
+# ---------------------------------------------------------------------------
+# many requests
+# ---------------------------------------------------------------------------
+
+def test_thousands_of_requests():
+    rng = np.random.default_rng(120)
+    B, heads, dh, page = 3000, 1, 64, 16
+    w = rng.integers(0, 3, B)
+    lens = w + rng.integers(0, 40, B)
+    b = Batch(121, lens.tolist(), heads, dh, page, False, spread=0.1)
+    off = np.cumsum(np.concatenate([[0], w]))
+    rows = int(off[-1])
+    q, k, v = rope_case(rng, rows, heads, 2, dh, 0.1)
+    pos = rng.integers(0, 5000, rows)
+    freq = [10000.0 ** (-j / 32) for j in range(32)]
+    args = (i32(off), i32(lens - w), b.table)
+    q2 = bd.rope_kv_write(b.pages, bd.Rope(dh, [0] * 32, freq), i32(pos), q, k, v, *args)
+    check_turned(f64(q2), cache_ops.rotate(f64(q), [pos], [0] * 32, freq), pair_sizes(f64(q), 32))
+    kk, vv = bd.kv_read(b.pages, *args, rows)
+    check_turned(f64(kk), cache_ops.rotate(f64(k), [pos], [0] * 32, freq), pair_sizes(f64(k), 32))
+    assert torch.equal(vv, v.contiguous())
+    # the cache as it is now
+    kr, vr = f64(kk), f64(vv)
+    for i in range(B):
+        if w[i]:
+            b.k[i], b.v[i] = b.k[i].copy(), b.v[i].copy()
+            b.k[i][lens[i] - w[i]:], b.v[i][lens[i] - w[i]:] = kr[off[i]:off[i + 1]], vr[off[i]:off[i + 1]]
+    b.w, b.group, b.q_off, b.q = w.tolist(), 2, off, q2
+    parent = i32(np.concatenate([np.arange(-1, n - 1) for n in w]).astype(np.int64))
+    mask, depth = bd.tree_mask(parent, i32(off), 2)
+    assert depth.tolist() == [t for n in w for t in range(n)]
+    out, lse = bd.tree_attn(q2, b.pages, i32(off), i32(lens), b.table, mask, 2, 64, return_lse=True)
+    b.check(out, lse, right=0)
+    mass = mass_of(b)
+    old = mass.clone()
+    bd.attn_mass(q2, lse, b.pages, mass, i32(off), i32(lens), b.table, 2, 64, right=0)
+    check_mass(b, mass, old, lse, right=0)
+    new, keep = bd.kv_evict(b.pages, mass, i32(lens), b.table, 7, 64, recent=2)
+    m, table = f64(mass), b.table.cpu().numpy()
+    assert new.tolist() == np.minimum(lens, 7).tolist()
+    # (the rows have moved in place: mass too)
+    kept = keep.cpu().numpy()[:, 0]
+    assert all((np.diff(kept[i, :n]) > 0).all() and (kept[i, n:] == -1).all() for i, n in enumerate(np.minimum(lens, 7)))
+    for i in (5, 1500, 2999):
+        n = int(min(lens[i], 7))
+        pg, sl = slots(table, page, i, n)
+        pages = b.pages.k.float()[pg, 0, sl].cpu().numpy()
+        assert np.array_equal(pages, b.k[i][kept[i, :n], 0].astype(np.float32))
+
+
+def test_two_calls_at_once():
+    # two streams, a cache each: the calls share no memory of the library's
+    cases = []
+    for seed in (130, 131):
+        b = Drafts(seed, [900, 3000, 17], 4, 128, 32, seed == 131)
+        b.drafts([40, 64, 5], 2, seed)
+        cases.append((b, mass_of(b), torch.empty(max(1, bd.paged_attn_workspace(b.pages, 3, 8, 64, 3000)), dtype=torch.uint8, device=DEV)))
+
+    def work(b, mass, ws):
+        out, lse = bd.tree_attn(b.q, b.pages, i32_cached(b.q_off), i32_cached(b.lens), b.table, b.mask, 64, 3000, return_lse=True, ws=ws)
+        bd.attn_mass(b.q, lse, b.pages, mass, i32_cached(b.q_off), i32_cached(b.lens), b.table, 64, 3000, right=0)
+        new, keep = bd.kv_evict(b.pages, mass, i32_cached(b.lens), b.table, 500, 3000, sinks=1, recent=70)
+        return [out, lse, mass, new, keep, b.pages.k.view(torch.uint8), b.pages.v.view(torch.uint8)]
+
+    start = [[t.clone() for t in (b.pages.k.view(torch.uint8), b.pages.v.view(torch.uint8), m)] for b, m, _ in cases]
+    want = [[t.clone() for t in work(*c)] for c in cases]
+    for (b, m, _), s in zip(cases, start):
+        for t, x in zip((b.pages.k.view(torch.uint8), b.pages.v.view(torch.uint8), m), s):
+            t.copy_(x)
+        if b.pages.k_scale is not None:                        # the scales moved as well: write the rows again
+            bd.kv_write(b.pages, b.k_in, b.v_in, b.off, i32([0, 0, 0]), b.table)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for c, s in zip(cases, streams):
+        with torch.cuda.stream(s):
+            got.append(work(*c))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for x, y in zip(g, w):
+            x, y = (t.view(torch.uint8) if t.dtype == torch.bfloat16 else t for t in (x, y))
+            assert torch.equal(x, y)
 
 
 # ---------------------------------------------------------------------------
