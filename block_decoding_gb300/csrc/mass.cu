@@ -511,14 +511,14 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
               if constexpr (!kCodes) {
                 const uint32_t idesc = idesc_bf16(128, columns, 0, 0);
                 const uint64_t dk = sw128_desc(sk, 16, C::kGroup8), dq = sw128_desc(sq, 16, 1024);
-                if constexpr (FOLD) {
-                  const uint32_t ones = smem_u32(smem + C::kOffOnes);
-                  umma_bf16(t_s, plain_desc(ones, 128, 256), plain_desc(ones + (1 + in.at) * C::kFold, 128, 256), idesc, 0);
-                }
 #pragma unroll
                 for (int kk = 0; kk < DH / 16; ++kk)
                   umma_bf16(t_s, dk + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
-                            dq + (((kk >> 2) * (a.columns * 128) + (kk & 3) * 32) >> 4), idesc, FOLD || kk > 0);
+                            dq + (((kk >> 2) * (a.columns * 128) + (kk & 3) * 32) >> 4), idesc, kk > 0);
+                if constexpr (FOLD) {     // (last: sums are cut off at their size, and now they get small; first, 3 times the error)
+                  const uint32_t ones = smem_u32(smem + C::kOffOnes);
+                  umma_bf16(t_s, plain_desc(ones, 128, 256), plain_desc(ones + (1 + in.at) * C::kFold, 128, 256), idesc, 1);
+                }
               } else {
                 const uint32_t idesc = idesc_f8(128, columns, kE4M3, kE4M3, 0, 0);
                 const uint64_t dk = DH == 128 ? sw128_desc(sk, 16, C::kGroup8) : sw64_desc(sk, 16, C::kGroup8);
