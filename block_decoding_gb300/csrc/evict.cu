@@ -1,5 +1,14 @@
 // Moving rows within the paged cache, and choosing the rows that stay when a
 // cache is cut down to a budget.
+//
+// Choosing is bound by latency (a head's weights are some 40 KB): 9.4 us for
+// 8242 weights, of which 3 until they are in shared memory, 4 for three passes
+// with their scans, 2.5 for the positions in their order. Moving is bound by
+// memory: 262 k rows of 128 bytes, a third of those read past, to other pages in
+// 30 us, 4.5 TB/s, beside as many sectors for scales and weights of single rows
+// (two rows of a thread on their way: with four 33); 192 k rows in place in 34
+// us, the longest of 64 lists being a third longer than the mean. One request's
+// 701 rows cut down to 512 in place: 9.6 us, both launches.
 #include "pages.cuh"
 #include "umma.cuh"
 
@@ -226,7 +235,7 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Se
 }
 
 cudaError_t launch_select(const SelectArgs &g, int B, cudaStream_t s) {
-  const int threads = g.max_kv <= 2048 ? 256 : 1024;
+  const int threads = 1024;      // (256: 3 to 9 % longer from 500 rows on)
   if (g.max_kv > kCached) return launch_pdl(select_kernel<false>, dim3(g.c.heads, B), dim3(threads), 0, s, g);
   const int smem = g.max_kv * 4;
   cudaError_t e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4);
@@ -249,7 +258,7 @@ struct ShiftArgs {
   unsigned int *status;
 };
 
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 256;      // (in place, with 128: 34 us become 56; 4 CTAs an SM, or half of the clusters wait for the others)
 
 // Rows of a thread at a time, 16 bytes of K and of V each: elsewhere a block has
 // no more; in place one such set is written while the next is on its way.
@@ -401,6 +410,9 @@ template <int ROW>
 cudaError_t launch_shift_rows(const ShiftArgs &g, bool in_place, int heads, int B, cudaStream_t s) {
   const int blocks = (g.max_n - 1) / round_rows(ROW, in_place) + 1;
   if (!in_place) return launch_pdl(shift_kernel<ROW, false>, dim3(blocks, heads, B), dim3(kMoveThreads), 0, s, g);
+  // As many CTAs as have rows, up to the most that every cluster may have. (One
+  // request, 200 rows that move: 4 CTAs 9.1 us with the choice, 8 9.2, one 15.0;
+  // 800 rows: 8 CTAs 12.8, one 39.7.)
   const unsigned cluster = blocks > 4 ? 8 : blocks > 2 ? 4 : blocks;
   return launch_pdl_clusters(shift_kernel<ROW, true>, cluster, dim3(cluster, heads, B), dim3(kMoveThreads), 0, s, g);
 }

@@ -15,12 +15,12 @@
 // lanes took 2 k cycles of a unit's 3.3 k.)
 //
 // Query rows pass by in chunks of up to 128, each read once for all tiles of an
-// item. An item is a stretch of keys of one request and cached head, 128 of them
-// for each of four epilogue warpgroups at a time: chunks of up to 64 rows (decode
-// steps) take 1024 keys, two a thread, so that what an item costs by itself is
-// spread over more of them; wider ones 512. Neighbouring items of a head whose
-// rows are one chunk share it. The items form one line, each as long as its
-// chunks and what every item costs, cut into equal stretches, one per CTA.
+// item. An item is 512 keys of one request and cached head, 128 of them for each
+// of four epilogue warpgroups. Over e4m3 pages, chunks of up to 64 rows (decode
+// steps) take 1024 keys, two a thread: a tile is half as long on its way, and
+// what an item costs by itself is spread over more of them. Neighbouring items of
+// a head whose rows are one chunk share it. The items form one line, each as long
+// as its chunks and what every item costs, cut into equal stretches, one per CTA.
 //
 // Warp roles:
 //   warp 0        K tiles by TMA, one box per page, two tiles to a stage, and the
@@ -36,6 +36,14 @@
 //                 than the codes, and are needed once a chunk and item.
 //   warps 8..23   four groups: (e4m3 pages and many rows) codes to bf16,
 //                 exponentials and sums
+//
+// 64 single tokens over 1 to 8192 keys (8 x 4 heads, dh 128): e4m3 55 us, 4.9
+// TB/s and 73 % of a copy's rate; bf16 90 us, 86 %. e4m3 is bound by the roles'
+// steps for an item, one after the other (without any loads and sums 39 us). The
+// last 50 to 64 tokens of four prompts over 9 to 12 thousand keys, bf16: 30.5 us,
+// of which 5 pass until the first scores; the last 1000 to 1200: 343 us, 1.02
+// PFLOP/s, 53 % of a plain matrix product's rate (e4m3 362 us): a chunk's MMAs on
+// four tiles take some 2.3 k cycles, their exponentials 2 k, the unit 3.8 k.
 #include <math.h>
 
 #include <type_traits>
@@ -61,19 +69,20 @@ struct MassArgs : PagedArgs {
 };
 
 constexpr int kGroups = 4;       // epilogue warpgroups
-constexpr int kNarrow = 64;      // chunks of up to so many rows: two keys a thread (they are all of a request's rows: more
-                                 // would make chunks of 65 or more; so a stage is free again as soon as it is read)
+constexpr int kNarrow = 64;      // rows of a chunk that two keys a thread go with (they are all of a request's: had it more,
+                                 // its chunks would have 65 or more; so a stage is free again as soon as it is read)
 constexpr int kChunkRows = 128;
 constexpr int kAhead = 8;        // items prepared, the current one included
 constexpr int kInfo = 3;         // chunks whose rows' numbers are prepared
-constexpr int kItemLength = 2;   // what an item costs beside its chunks, in chunks
+constexpr int kItemLength = 2;   // what an item costs beside its chunks, in chunks (0 to 4: the same time where requests are alike)
 
 template <int DH, bool FP8, bool NARROW, bool FOLD>
 struct MassCfg {
   static constexpr int kPer = NARROW ? 2 : 1;                  // keys of a thread
   static constexpr int kTiles = kGroups * kPer, kItemKeys = kTiles * kTile;
   // e4m3 pages and few rows: the codes are the MMA's operand; else converted
-  static constexpr bool kCodes = FP8 && NARROW;
+  static_assert(FP8 || !NARROW, "two keys a thread: codes");
+  static constexpr bool kCodes = NARROW;
   static constexpr int kLoad = kTile * DH * (FP8 ? 1 : 2);     // a K tile as it is loaded, to the end of its space
   static constexpr int kRaw = kTile * DH * (kCodes ? 1 : 2);   // ... as the MMAs read it
   static constexpr int kStage = 2 * kRaw;
@@ -852,19 +861,19 @@ dllm_status launch_mass(const dllm_kv_pages *pages, MassArgs &g, cudaStream_t s)
 
 template <int DH>
 dllm_status launch_mass(const dllm_kv_pages *pages, float scale, MassArgs &g, cudaStream_t s) {
-  const bool narrow = g.columns <= kNarrow, fp8 = pages->type == DLLM_KV_E4M3;
-  if (fp8 && narrow) return launch_mass<DH, true, true, false>(pages, g, s);
+  const bool fp8 = pages->type == DLLM_KV_E4M3;
+  // e4m3 pages and few rows: codes as they are. 16 requests, 9 to 12 thousand
+  // keys, 8 x 4 heads: 4 rows a head 39 us, converted 68; 64 rows 47 and 73. (The
+  // most rows that eight tiles' scores leave room for. Two keys a thread over bf16
+  // pages: 61 to 63 us, one 60 to 61.)
+  if (fp8 && g.columns <= kNarrow) return launch_mass<DH, true, true, false>(pages, g, s);
   // lse / scale has to be a number
   const float size = fabsf(scale);
   if (size >= 0x1p-40f && size <= 0x1p40f) {
     g.lse_scale = -1.f / scale;
-    return fp8      ? launch_mass<DH, true, false, true>(pages, g, s)
-           : narrow ? launch_mass<DH, false, true, true>(pages, g, s)
-                    : launch_mass<DH, false, false, true>(pages, g, s);
+    return fp8 ? launch_mass<DH, true, false, true>(pages, g, s) : launch_mass<DH, false, false, true>(pages, g, s);
   }
-  return fp8      ? launch_mass<DH, true, false, false>(pages, g, s)
-         : narrow ? launch_mass<DH, false, true, false>(pages, g, s)
-                  : launch_mass<DH, false, false, false>(pages, g, s);
+  return fp8 ? launch_mass<DH, true, false, false>(pages, g, s) : launch_mass<DH, false, false, false>(pages, g, s);
 }
 
 }  // namespace

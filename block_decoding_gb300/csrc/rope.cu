@@ -11,7 +11,12 @@
 // Bound by memory: each row is read and written once. The sines and cosines of
 // a row are computed once per block and serve all of its heads. One row of one
 // head is handled by dh / 16 neighbouring lanes, two 16-byte chunks each: a pair's
-// two halves lie in the same lane.
+// two halves lie in the same lane. Measured (dh 128): 7.1 k rows of 32 + 2 x 8
+// heads, bf16 pages, 36 us, 4.9 TB/s and 72 % of a copy's rate; 11 k rows of 32 +
+// 2 x 32 heads, e4m3 pages, 92 us, the same rate. (Blocks of 2 rows 42, of 8 40 to
+// 43 us; one unit of a thread on the way 45, three or four 38 to 40: registers.
+// Sines and cosines read with bank conflicts: 2 us more.) 64 single tokens: 4.6
+// us, the chain offsets -> position -> page -> store.
 #include <math.h>
 
 #include "page_rows.cuh"
@@ -254,6 +259,8 @@ extern "C" dllm_status dllm_rope_kv_write(const dllm_kv_pages *pages, const dllm
   }
   cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&g.status), g_status_rope);
   if (e != cudaSuccess) return cuda_error(e);
+  // Blocks of four rows, or of one where there are few. (32 + 2 x 8 heads: 300
+  // rows 6.3 and 4.6 us, 600 6.7 and 5.2, 1200 8.9 and 8.9, 2400 12.3 and 15.7.)
   g.per = a->rows >= 8 * num_sms() ? kMaxRows : 1;
   const bool fp8 = pages->type == DLLM_KV_E4M3;
   void (*kern)(RopeArgs) = pages->dh == 64 ? (fp8 ? rope_write_kernel<64, true> : rope_write_kernel<64, false>)
