@@ -5,12 +5,11 @@
 // 8242 weights, of which 3 until they are in shared memory, 4 for three passes
 // with their scans, 2.5 for the positions in their order. Moving is bound by
 // memory: 262 k rows of 128 bytes, a third of those read past, to other pages in
-// 30 us, 4.5 TB/s, beside as many sectors for scales and weights of single rows
-// (two rows of a thread on their way: with four 33); 192 k rows in place in 34
-// us, the longest of 64 lists being a third longer than the mean. One request's
-// 701 rows cut down to 512 in place: 9.6 us, both launches.
+// 30 us, 4.5 TB/s, beside as many sectors for scales and weights of single rows;
+// 192 k rows in place, 64 lists of 2 to 4 thousand, in 27 us. One request's 701
+// rows cut down to 512 in place: 9.7 us, both launches.
 #include "pages.cuh"
-#include "umma.cuh"
+#include "umma_pages.cuh"
 
 namespace dllm {
 
@@ -235,7 +234,8 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Se
 }
 
 cudaError_t launch_select(const SelectArgs &g, int B, cudaStream_t s) {
-  const int threads = 1024;      // (256: 3 to 9 % longer from 500 rows on)
+  // (16 x 8 heads of 1000 rows and half of them kept: 256 threads 15.4 us, 1024 14.5; one request's 16 of 701: 9.6 and 10.2)
+  const int threads = g.max_kv <= 768 ? 256 : 1024;
   if (g.max_kv > kCached) return launch_pdl(select_kernel<false>, dim3(g.c.heads, B), dim3(threads), 0, s, g);
   const int smem = g.max_kv * 4;
   cudaError_t e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4);
@@ -254,50 +254,42 @@ struct ShiftArgs {
   int src_heads, max_n;
   const int32_t *count, *first;   // [B]; first may be null: 0
   float *mass;
-  uint32_t zero;               // 0, which the compiler does not know
   unsigned int *status;
 };
 
-constexpr int kMoveThreads = 256;      // (in place, with 128: 34 us become 56; 4 CTAs an SM, or half of the clusters wait for the others)
+constexpr int kMoveThreads = 256;
 
-// Rows of a thread at a time, 16 bytes of K and of V each: elsewhere a block has
-// no more; in place one such set is written while the next is on its way.
-constexpr int kEachAway = 2, kEachInPlace = 2;
+// Rows of a thread, 16 bytes of K and of V each: elsewhere all that a block
+// has (four instead of two: 33 us for 30), in place what it has at a time. (192 k
+// rows of 128 and of 256 bytes in place: two rows 29 and 64 us, four 27 and 56, six
+// 33 and 67, eight 38 and 68; 262 k rows of 16 requests, with the choice: 40, 44,
+// 57, 58. In registers, two at a time, the next two on their way: 35 and 75, 55.)
+constexpr int kEachAway = 2, kEachInPlace = 4;
+constexpr int kAtOnce = 4;       // ... whose places are looked up together
 
 // Rows of ROW bytes that a CTA moves at a time.
 constexpr int round_rows(int row_bytes, bool in_place) {
   return kMoveThreads * (in_place ? kEachInPlace : kEachAway) * 16 / row_bytes;
 }
 
-// What a thread moves at a time.
-template <int EACH>
-struct Moved {
-  uint4 k[EACH], v[EACH];
-  float mass[EACH];
-  uint8_t k_scale[EACH], v_scale[EACH];
-  int dest[EACH];                // cache row for head 0, -1: nothing
-};
-
 template <int ROW, bool IN_PLACE>
 struct Mover {
-  static constexpr int kEach = IN_PLACE ? kEachInPlace : kEachAway;
-  static constexpr int kChunks = ROW / 16, kStep = kMoveThreads / kChunks, kRows = kStep * kEach;
-  static_assert(kRows == round_rows(ROW, IN_PLACE), "rows of a round");
+  static constexpr int kChunks = ROW / 16, kStep = kMoveThreads / kChunks;   // rows of a CTA that lie side by side
   const ShiftArgs &a;
   const int i, n, first, c;      // request, rows of its list, first position, the thread's 16 bytes of a row
   const int32_t *src;
   const size_t head;
 
-  // Rows j0 .. j0 + kRows - 1 of the list.
-  __device__ __forceinline__ void load(Moved<kEach> &m, int j0) const {
+  // The cache rows, for head 0, that COUNT of the thread's entries from entry j
+  // on, `step` apart, come from and go to: -1 where nothing moves.
+  template <int COUNT>
+  __device__ __forceinline__ void find(int j, int step, int (&from)[COUNT], int (&dest)[COUNT]) const {
     KvPages to = a.c;
     to.table = a.dst_table;
     to.max_pages = a.dst_pages;
-    int from[kEach];
 #pragma unroll
-    for (int q = 0; q < kEach; ++q) {
-      const int j = j0 + threadIdx.x / kChunks + q * kStep;
-      from[q] = m.dest[q] = -1;
+    for (int q = 0; q < COUNT; ++q, j += step) {
+      from[q] = dest[q] = -1;
       if (j >= n) continue;
       const int u = src[j];
       const long long d = static_cast<long long>(first) + j;
@@ -308,67 +300,20 @@ struct Mover {
       }
       if (!bad) {
         from[q] = page_row(a.c, i, u);
-        m.dest[q] = page_row(to, i, static_cast<int>(d));
+        dest[q] = page_row(to, i, static_cast<int>(d));
       }
-      if (from[q] < 0 || m.dest[q] < 0) {
+      if (from[q] < 0 || dest[q] < 0) {
         atomicOr(a.status, DLLM_DEV_PAGE);
-        m.dest[q] = -1;
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < kEach; ++q) {
-      if (m.dest[q] < 0) continue;
-      const size_t s = from[q] + head;
-      m.k[q] = *reinterpret_cast<const uint4 *>(a.c.k + s * ROW + c * 16);
-      m.v[q] = *reinterpret_cast<const uint4 *>(a.c.v + s * ROW + c * 16);
-      if (c == 0) {
-        if (a.c.k_scale) { m.k_scale[q] = a.c.k_scale[s]; m.v_scale[q] = a.c.v_scale[s]; }
-        if (a.mass) m.mass[q] = a.mass[s];
+        from[q] = dest[q] = -1;
       }
     }
   }
-  // 0, once all of m is there.
-  __device__ __forceinline__ uint32_t loaded(const Moved<kEach> &m) const {
-    uint32_t x = 0;
-#pragma unroll
-    for (int q = 0; q < kEach; ++q) {
-      if (m.dest[q] < 0) continue;
-      x ^= m.k[q].x ^ m.k[q].y ^ m.k[q].z ^ m.k[q].w ^ m.v[q].x ^ m.v[q].y ^ m.v[q].z ^ m.v[q].w;
-      if (c == 0) {
-        if (a.c.k_scale) x ^= m.k_scale[q] ^ m.v_scale[q];
-        if (a.mass) x ^= __float_as_uint(m.mass[q]);
-      }
-    }
-    return x & a.zero;
-  }
-  __device__ __forceinline__ void store(const Moved<kEach> &m) const {
-#pragma unroll
-    for (int q = 0; q < kEach; ++q) {
-      if (m.dest[q] < 0) continue;
-      const size_t s = m.dest[q] + head;
-      *reinterpret_cast<uint4 *>(a.c.k + s * ROW + c * 16) = m.k[q];
-      *reinterpret_cast<uint4 *>(a.c.v + s * ROW + c * 16) = m.v[q];
-      if (c == 0) {
-        if (a.c.k_scale) { a.c.k_scale[s] = m.k_scale[q]; a.c.v_scale[s] = m.v_scale[q]; }
-        if (a.mass) a.mass[s] = m.mass[q];
-      }
-    }
-  }
+  __device__ __forceinline__ uint8_t *k_at(int row) const { return a.c.k + (row + head) * ROW + c * 16; }
+  __device__ __forceinline__ uint8_t *v_at(int row) const { return a.c.v + (row + head) * ROW + c * 16; }
 };
 
-// One request and cached head, K and V: a CTA of the grid's x takes
-// round_rows of the list. Elsewhere that is all. In place the CTAs of x are a
-// cluster that walks the list from its start, round by round: every row of a
-// round is read before any is written (a cluster barrier between the two), and
-// since lists ascend and no row moves to a later position, a place is written
-// in no earlier round than it is read: position first + j is row src[j'] of the
-// list with j' <= j if it is any. So rounds behind may be read at any time
-// before: the next one is on its way while the CTAs meet and this one is written.
 template <int ROW, bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads, 4) shift_kernel(const __grid_constant__ ShiftArgs a) {
-  using M = Mover<ROW, IN_PLACE>;
-  pdl_trigger();
-  pdl_wait();
+__device__ __forceinline__ Mover<ROW, IN_PLACE> mover(const ShiftArgs &a) {
   const int h = blockIdx.y, i = blockIdx.z;
   int n = a.count[i];
   const int first = a.first ? a.first[i] : 0;
@@ -376,31 +321,115 @@ __global__ void __launch_bounds__(kMoveThreads, 4) shift_kernel(const __grid_con
     if (threadIdx.x == 0) atomicOr(a.status, DLLM_DEV_OFFSETS);
     n = min(max(n, 0), a.max_n);
   }
-  const M move{a, i, n, first, static_cast<int>(threadIdx.x) % M::kChunks,
-               a.src + (static_cast<size_t>(i) * a.src_heads + (a.src_heads > 1 ? h : 0)) * a.max_n,
-               static_cast<size_t>(h) << a.c.page_shift};
-  const int mine = blockIdx.x * M::kRows;       // (n < 2^30)
-  if constexpr (!IN_PLACE) {
-    if (mine >= n) return;
-    Moved<M::kEach> m;
-    move.load(m, mine);
-    move.store(m);
-  } else {
-    const int round = gridDim.x * M::kRows;
-    Moved<M::kEach> m[2];
-    if (n > 0) move.load(m[0], mine);
-    for (int base = 0; base < n; base += 2 * round) {
+  return Mover<ROW, IN_PLACE>{a, i, n, first, static_cast<int>(threadIdx.x) % (ROW / 16),
+                              a.src + (static_cast<size_t>(i) * a.src_heads + (a.src_heads > 1 ? h : 0)) * a.max_n,
+                              static_cast<size_t>(h) << a.c.page_shift};
+}
+
+// One request and cached head, K and V, to other pages: a CTA of the grid's x
+// takes round_rows of the list.
+template <int ROW>
+__global__ void __launch_bounds__(kMoveThreads) shift_kernel(const __grid_constant__ ShiftArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const Mover<ROW, false> m = mover<ROW, false>(a);
+  const int j0 = blockIdx.x * round_rows(ROW, false);       // (n < 2^30)
+  if (j0 >= m.n) return;
+  int from[kEachAway], dest[kEachAway];
+  uint4 k[kEachAway], v[kEachAway];
+  float mass[kEachAway];
+  uint8_t k_scale[kEachAway], v_scale[kEachAway];
+  m.find(j0 + threadIdx.x / m.kChunks, m.kStep, from, dest);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int at = base + k * round;
-        if (at >= n) break;                     // (the whole cluster)
-        if (at + round < n) move.load(m[k ^ 1], mine + at + round);
-        // The barrier orders this round's loads before its stores, and needs
-        // nothing of the stores before: a release would wait for all of them.
-        // The loads are done when their values decide whether to arrive.
-        if (move.loaded(m[k]) == 0) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
-        asm volatile("barrier.cluster.wait;" ::: "memory");
-        move.store(m[k]);
+  for (int q = 0; q < kEachAway; ++q) {
+    if (from[q] < 0) continue;
+    const size_t s = from[q] + m.head;
+    k[q] = *reinterpret_cast<const uint4 *>(m.k_at(from[q]));
+    v[q] = *reinterpret_cast<const uint4 *>(m.v_at(from[q]));
+    if (m.c == 0) {
+      if (a.c.k_scale) { k_scale[q] = a.c.k_scale[s]; v_scale[q] = a.c.v_scale[s]; }
+      if (a.mass) mass[q] = a.mass[s];
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < kEachAway; ++q) {
+    if (from[q] < 0) continue;
+    const size_t s = dest[q] + m.head;
+    *reinterpret_cast<uint4 *>(m.k_at(dest[q])) = k[q];
+    *reinterpret_cast<uint4 *>(m.v_at(dest[q])) = v[q];
+    if (m.c == 0) {
+      if (a.c.k_scale) { a.c.k_scale[s] = k_scale[q]; a.c.v_scale[s] = v_scale[q]; }
+      if (a.mass) a.mass[s] = mass[q];
+    }
+  }
+}
+
+// What a thread of shift_in_place_kernel holds between reading and writing:
+// shared memory of its own, so that many rows fit and loads need no registers.
+struct Held {
+  uint4 k[kEachInPlace][kMoveThreads], v[kEachInPlace][kMoveThreads];
+  float mass[kEachInPlace][kMoveThreads];
+  int dest[kEachInPlace][kMoveThreads];
+  uint8_t k_scale[kEachInPlace][kMoveThreads], v_scale[kEachInPlace][kMoveThreads];
+};
+
+// In place the CTAs of x are a cluster that walks the list from its start, round
+// by round: every row of a round is read before any is written (a cluster barrier
+// between the two), and since lists ascend and no row moves to a later position,
+// a place is written in no earlier round than it is read: position first + j is
+// row src[j'] of the list with j' <= j if it is any. The next round's rows lie
+// behind all places written so far, so its loads wait for nobody.
+template <int ROW>
+__global__ void __launch_bounds__(kMoveThreads) shift_in_place_kernel(const __grid_constant__ ShiftArgs a) {
+  extern __shared__ uint4 smem_held[];
+  Held &held = *reinterpret_cast<Held *>(smem_held);
+  pdl_trigger();
+  pdl_wait();
+  const Mover<ROW, true> m = mover<ROW, true>(a);
+  const int tid = threadIdx.x, rows = round_rows(ROW, true);
+  for (int base = 0; base < m.n; base += gridDim.x * rows) {
+#pragma unroll 1
+    for (int q0 = 0; q0 < kEachInPlace; q0 += kAtOnce) {
+      int from[kAtOnce], dest[kAtOnce];
+      // (kStep rows to a CTA in turn: short lists have all of the cluster's loads)
+      m.find(base + (q0 * gridDim.x + blockIdx.x) * m.kStep + tid / m.kChunks, gridDim.x * m.kStep, from, dest);
+      float mass[kAtOnce];
+      uint8_t k_scale[kAtOnce], v_scale[kAtOnce];
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q) {
+        held.dest[q0 + q][tid] = dest[q];
+        if (from[q] < 0) continue;
+        copy16(&held.k[q0 + q][tid], m.k_at(from[q]), true);
+        copy16(&held.v[q0 + q][tid], m.v_at(from[q]), true);
+        const size_t s = from[q] + m.head;
+        if (m.c == 0) {
+          if (a.c.k_scale) { k_scale[q] = a.c.k_scale[s]; v_scale[q] = a.c.v_scale[s]; }
+          if (a.mass) mass[q] = a.mass[s];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q) {
+        if (from[q] < 0 || m.c != 0) continue;
+        if (a.c.k_scale) { held.k_scale[q0 + q][tid] = k_scale[q]; held.v_scale[q0 + q][tid] = v_scale[q]; }
+        if (a.mass) held.mass[q0 + q][tid] = mass[q];
+      }
+    }
+    copies_wait();
+    // The round's reads are over (each value is in shared memory); of writes
+    // before nothing has to be known. Every CTA reaches the barrier.
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+#pragma unroll
+    for (int q = 0; q < kEachInPlace; ++q) {
+      const int dest = held.dest[q][tid];
+      if (dest < 0) continue;
+      *reinterpret_cast<uint4 *>(m.k_at(dest)) = held.k[q][tid];
+      *reinterpret_cast<uint4 *>(m.v_at(dest)) = held.v[q][tid];
+      if (m.c == 0) {
+        const size_t s = dest + m.head;
+        if (a.c.k_scale) { a.c.k_scale[s] = held.k_scale[q][tid]; a.c.v_scale[s] = held.v_scale[q][tid]; }
+        if (a.mass) a.mass[s] = held.mass[q][tid];
       }
     }
   }
@@ -408,13 +437,16 @@ __global__ void __launch_bounds__(kMoveThreads, 4) shift_kernel(const __grid_con
 
 template <int ROW>
 cudaError_t launch_shift_rows(const ShiftArgs &g, bool in_place, int heads, int B, cudaStream_t s) {
-  const int blocks = (g.max_n - 1) / round_rows(ROW, in_place) + 1;
-  if (!in_place) return launch_pdl(shift_kernel<ROW, false>, dim3(blocks, heads, B), dim3(kMoveThreads), 0, s, g);
-  // As many CTAs as have rows, up to the most that every cluster may have. (One
-  // request, 200 rows that move: 4 CTAs 9.1 us with the choice, 8 9.2, one 15.0;
-  // 800 rows: 8 CTAs 12.8, one 39.7.)
-  const unsigned cluster = blocks > 4 ? 8 : blocks > 2 ? 4 : blocks;
-  return launch_pdl_clusters(shift_kernel<ROW, true>, cluster, dim3(cluster, heads, B), dim3(kMoveThreads), 0, s, g);
+  if (!in_place)
+    return launch_pdl(shift_kernel<ROW>, dim3((g.max_n - 1) / round_rows(ROW, false) + 1, heads, B), dim3(kMoveThreads), 0, s, g);
+  const int parts = (g.max_n - 1) / Mover<ROW, true>::kStep + 1;
+  // As many CTAs as there are parts, up to the most that every cluster may have.
+  // (One request, 800 rows that move: 8 CTAs 12 us with
+  // the choice, one 40.)
+  const unsigned cluster = parts > 4 ? 8 : parts > 2 ? 4 : parts;
+  const cudaError_t e = cudaFuncSetAttribute(shift_in_place_kernel<ROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Held));
+  if (e != cudaSuccess) return e;
+  return launch_pdl_clusters(shift_in_place_kernel<ROW>, cluster, dim3(cluster, heads, B), dim3(kMoveThreads), sizeof(Held), s, g);
 }
 
 dllm_status launch_shift(const dllm_kv_pages *pages, const ShiftArgs &g, bool in_place, int B, cudaStream_t s) {
