@@ -973,7 +973,7 @@ def kv_evict(pages: KVPages, mass, kv_len, page_table, budget, max_kv, sinks=0, 
     the last `recent` and those of greatest mass float32
     [num_pages][heads][page_size] stay, in their order, at positions 0, 1, .. of
     dst_table's pages (default: in place, see kv_move). Returns (new_len int32 [B],
-    keep int32 [B][heads][budget], the positions that stayed, then -1); with
+    which may be kv_len, keep int32 [B][heads][budget], the positions that stayed, then -1); with
     `stream`, order other streams' use of them after it."""
     _host_sizes(budget=budget, max_kv=max_kv, sinks=sinks, recent=recent)
     dev, B = pages.index, kv_len.numel()

@@ -24,7 +24,7 @@ struct SelectArgs {
   KvPages c;
   const float *mass;
   const int32_t *kv_len;
-  int32_t *new_len, *keep;     // [B], [B][heads][budget]
+  int32_t *keep;               // [B][heads][budget]
   int budget, max_kv, sinks, recent;
   unsigned int *status;
 };
@@ -65,7 +65,6 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Se
   }
   int32_t *keep = a.keep + (static_cast<size_t>(i) * a.c.heads + h) * a.budget;
   const int k = min(n, a.budget);
-  if (h == 0 && tid == 0) a.new_len[i] = k;
   for (int j = tid + k; j < a.budget; j += nt) keep[j] = -1;
   if (n <= a.budget) {
     for (int j = tid; j < k; j += nt) keep[j] = j;
@@ -253,6 +252,8 @@ struct ShiftArgs {
   const int32_t *src;          // [B][src_heads][max_n]
   int src_heads, max_n;
   const int32_t *count, *first;   // [B]; first may be null: 0
+  int most;                    // rows of a list, at most
+  int32_t *new_len;            // null, or where the rows of a list are written: then more than `most` is no mistake
   float *mass;
   unsigned int *status;
 };
@@ -317,10 +318,12 @@ __device__ __forceinline__ Mover<ROW, IN_PLACE> mover(const ShiftArgs &a) {
   const int h = blockIdx.y, i = blockIdx.z;
   int n = a.count[i];
   const int first = a.first ? a.first[i] : 0;
-  if (n < 0 || n > a.max_n) {
-    if (threadIdx.x == 0) atomicOr(a.status, DLLM_DEV_OFFSETS);
-    n = min(max(n, 0), a.max_n);
+  if (n < 0 || n > a.most) {
+    if (threadIdx.x == 0 && !a.new_len) atomicOr(a.status, DLLM_DEV_OFFSETS);
+    n = min(max(n, 0), a.most);
   }
+  // (new_len may be count: whoever reads the number after this finds the same n)
+  if (a.new_len && blockIdx.x + h + threadIdx.x == 0) a.new_len[i] = n;
   return Mover<ROW, IN_PLACE>{a, i, n, first, static_cast<int>(threadIdx.x) % (ROW / 16),
                               a.src + (static_cast<size_t>(i) * a.src_heads + (a.src_heads > 1 ? h : 0)) * a.max_n,
                               static_cast<size_t>(h) << a.c.page_shift};
@@ -479,6 +482,7 @@ extern "C" dllm_status dllm_kv_move(const dllm_kv_pages *pages, const dllm_kv_mo
   g.dst_table = in_place ? a->page_table : a->dst_table;
   g.dst_pages = in_place ? a->max_pages : a->dst_pages;
   g.src = a->src; g.src_heads = a->src_heads; g.max_n = a->max_n; g.count = a->count; g.first = a->first; g.mass = a->mass;
+  g.most = a->max_n;
   cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&g.status), g_status_evict);
   if (e != cudaSuccess) return cuda_error(e);
   const dllm_status sl = launch_shift(pages, g, in_place, a->B, static_cast<cudaStream_t>(stream));
@@ -501,7 +505,7 @@ extern "C" dllm_status dllm_kv_evict(const dllm_kv_pages *pages, const dllm_kv_e
   SelectArgs g{};
   g.c = device_pages(pages, a->page_table, a->max_pages);
   const long long table = static_cast<long long>(a->max_pages) * pages->page_size;   // rows beyond the table are not there
-  g.mass = a->mass; g.kv_len = a->kv_len; g.new_len = a->new_len; g.keep = a->keep;
+  g.mass = a->mass; g.kv_len = a->kv_len; g.keep = a->keep;
   g.budget = a->budget; g.max_kv = static_cast<int>(table < a->max_kv ? table : a->max_kv);
   g.sinks = a->sinks; g.recent = a->recent;
   cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&g.status), g_status_evict);
@@ -511,7 +515,9 @@ extern "C" dllm_status dllm_kv_evict(const dllm_kv_pages *pages, const dllm_kv_e
   const bool in_place = !a->dst_table || a->dst_table == a->page_table;
   m.dst_table = in_place ? a->page_table : a->dst_table;
   m.dst_pages = in_place ? a->max_pages : a->dst_pages;
-  m.src = a->keep; m.src_heads = pages->heads; m.max_n = a->budget; m.count = a->new_len;
+  m.src = a->keep; m.src_heads = pages->heads; m.max_n = a->budget; m.count = a->kv_len;
+  m.most = g.max_kv < a->budget ? g.max_kv : a->budget;
+  m.new_len = a->new_len;
   m.mass = a->move_mass ? a->mass : nullptr;
   m.status = g.status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

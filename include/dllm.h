@@ -717,7 +717,8 @@ dllm_status dllm_attn_mass(const dllm_kv_pages *pages /* host */,
  * order, to positions 0, 1, .. as by dllm_kv_move. A request of no more than
  * `budget` rows keeps all of them.
  *   mass     float [num_pages][heads][page_size]; move_mass != 0: moves too
- *   new_len  int32 [B]: min(kv_len[i], budget), the request's length from now on
+ *   new_len  int32 [B]: min(kv_len[i], budget), the request's length from now on;
+ *            may be kv_len
  *   keep     int32 [B][heads][budget]: the positions that stayed, ascending,
  *            then -1
  *   max_kv   host upper bound of kv_len[i]; rows beyond it or the table are

@@ -685,6 +685,30 @@ def test_eviction_reports_lengths_beyond_their_bounds():
         assert np.array_equal(keep.cpu().numpy()[0, h], cache_ops.keep(m[pg, h, sl], 8, 0, 0))
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+def test_lengths_that_are_cut_down_where_they_stand(in_place):
+    # so many heads, and room for such long requests, that not all CTAs run at a time
+    lens, heads, page = [70, 40, 8, 0, -3], 256, 16
+    p = Pool(94, [70, 40, 8, 0, 0], heads, 64, page, True, None if in_place else [24, 24, 8, 0, 0])
+    m = f64(p.mass)
+    lists = [[cache_ops.keep(m[pg, h, sl], 24, 2, 3) for h in range(heads)]
+             for pg, sl in (slots(p.table, page, i, max(n, 0)) for i, n in enumerate(lens))]
+    want = p.moved(lists, [0] * len(lens), in_place, True)
+    table = np.full((len(lens), 3000), -1)
+    table[:, :p.table.shape[1]] = p.table
+    kv_len = i32(lens)
+    new, keep = bd.kv_evict(p.pages, p.mass, kv_len, i32(table), 24, 48000, sinks=2, recent=3, dst_table=None if in_place else i32(p.dst),
+                            new_len=kv_len)
+    torch.cuda.synchronize()
+    assert bd.device_status() == DEV_OFFSETS               # the length below 0
+    assert new is kv_len and kv_len.tolist() == [24, 24, 8, 0, 0]
+    keep = keep.cpu().numpy()
+    for i, per in enumerate(lists):
+        for h, u in enumerate(per):
+            assert np.array_equal(keep[i, h], list(u) + [-1] * (24 - len(u))), (i, h)
+    p.check(want)
+
+
 @pytest.mark.parametrize("n", [49152, 49153, 70001])
 def test_eviction_from_long_requests(n):
     # more weights than shared memory holds, and just as many
