@@ -799,6 +799,8 @@ class Rope:
         of every axis (they add up to rot / 2), one run after the other or, with
         `interleaved`, in turn (0, 1, 2, 0, 1, 2, ..) as long as an axis has pairs."""
         rot = dh if rot is None else rot
+        if rot % 16:
+            raise ValueError("rot must be a multiple of 16")
         sections = [rot // 2] if sections is None else list(sections)
         if sum(sections) != rot // 2 or min(sections) < 0:
             raise ValueError("sections must add up to rot / 2 pairs")

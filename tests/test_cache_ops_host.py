@@ -167,6 +167,12 @@ def test_rope_tables():
             bad()
 
 
+@pytest.mark.parametrize("rot", [17, 24, 31, -16, 80])
+def test_rope_of_uncommon_sizes_is_refused(rot):
+    with pytest.raises(ValueError):
+        bd.Rope.standard(64, rot=rot)
+
+
 @pytest.fixture
 def world(monkeypatch):
     w = types.SimpleNamespace(i32=lambda *v: torch.tensor(v, dtype=torch.int32), zeros=lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t))
