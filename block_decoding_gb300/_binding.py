@@ -524,6 +524,9 @@ for _name in ("dllm_kv_write", "dllm_kv_read", "dllm_paged_attn_workspace", "dll
     _fn.restype, _fn.argtypes = SIGNATURES[_name]
 
 
+_NEED = {}      # workspace bytes by shape, of pages by type and shape
+
+
 class KVPages:
     """Page pools of a K/V cache: k, v [num_pages][heads][page_size][dh], bf16
     or float8_e4m3fn; the 8-bit rows with uint8 k_scale, v_scale
@@ -548,7 +551,9 @@ class KVPages:
             _ptr_on(v_scale, dev, torch.uint8, "v_scale") if fp8 else None,
             1 if fp8 else 0, self.num_pages, self.page_size, self.heads, self.dh)
         self.device = k.device
-        self._need = {}     # workspace bytes by shape
+        if len(_NEED) >= 256:
+            _NEED.clear()
+        self._need = _NEED.setdefault((fp8, *k.shape), {})
 
     @classmethod
     def empty(cls, num_pages, page_size, heads, dh, dtype=torch.bfloat16, device="cuda"):
@@ -854,20 +859,14 @@ def rope_kv_write(pages: KVPages, rope: Rope, pos, q, k, v, off, pos0, page_tabl
     return q_out
 
 
-def _host_sizes(**kw):
-    """(ctypes would cut longer numbers off)"""
-    for name, v in kw.items():
-        if not 0 <= v < _I31:
-            raise ValueError(f"{name} must be 0 to 2^31 - 1")
-
-
 def tree_mask(parent, off, max_q, mask=None, depth=None, stream=None):
     """(mask int32 [rows][ceil(max_q / 32)], depth int32 [rows]) of the trees of
     drafted tokens parent int32 [rows] (row off[i] + t: the parent's number, less
     than t, or -1): which of its request's tokens each token descends from, itself
     included, as bits, and how many they are without itself. Rows in no request
     are left as they are. With `stream`, order other streams' use of them after it."""
-    _host_sizes(max_q=max_q)
+    if not 0 <= max_q < _I31:       # (ctypes would cut longer numbers off)
+        raise ValueError("max_q must be 0 to 2^31 - 1")
     dev = parent.get_device() if isinstance(parent, torch.Tensor) else -1
     pp, po = _ptr_on(parent, dev, torch.int32, "parent"), _ptr_on(off, dev, torch.int32, "offsets")
     rows, B, words = parent.numel(), off.numel() - 1, (int(max_q) + 31) // 32
@@ -875,14 +874,19 @@ def tree_mask(parent, off, max_q, mask=None, depth=None, stream=None):
         raise ValueError("offsets must have an entry")
     if mask is None:
         mask = _alloc((rows, words), torch.int32, parent.device, stream)
+        mp = mask.data_ptr()
     elif mask.dim() != 2 or mask.shape[0] != rows or mask.shape[1] < words:
         raise ValueError(f"mask must be [{rows}][{words} or more]")
+    else:
+        mp, words = _ptr_on(mask, dev, torch.int32, "mask"), mask.shape[1]
     if depth is None:
         depth = _alloc((rows,), torch.int32, parent.device, stream)
+        dp = depth.data_ptr()
     elif depth.shape != (rows,):
         raise ValueError(f"depth must be [{rows}]")
-    _launch("dllm_tree_mask", dev, stream, pp, po, rows, int(max_q), B, _ptr_on(mask, dev, torch.int32, "mask"), mask.shape[1],
-            _ptr_on(depth, dev, torch.int32, "depth"))
+    else:
+        dp = _ptr_on(depth, dev, torch.int32, "depth")
+    _launch("dllm_tree_mask", dev, stream, pp, po, rows, int(max_q), B, mp, words, dp)
     return mask, depth
 
 
@@ -925,9 +929,8 @@ def attn_mass(q, lse, pages: KVPages, mass, q_off, kv_len, page_table, max_q, ma
     [rows][Hq][dh], with lse [rows][Hq] from paged_attn, gave to every cached row
     of their requests. The rows see keys up to `right` behind their position
     (negative: all). Returns mass."""
-    _host_sizes(max_q=max_q, max_kv=max_kv)
-    if not -_I31 <= right < _I31:
-        raise ValueError("right must fit 32 bits")
+    if not (0 <= max_q < _I31 and 0 <= max_kv < _I31 and -_I31 <= right < _I31):
+        raise ValueError("max_q, max_kv and right must fit 32 bits, and only right may be negative")
     dev, dh = pages.index, pages.dh
     rows, Hq = (q.shape[0], q.shape[1]) if isinstance(q, torch.Tensor) and q.dim() == 3 else (0, 0)
     qp, qs = _rows_ptr(q, dev, Hq, dh, "q")
@@ -977,17 +980,24 @@ def kv_evict(pages: KVPages, mass, kv_len, page_table, budget, max_kv, sinks=0, 
     dst_table's pages (default: in place, see kv_move). Returns (new_len int32 [B],
     which may be kv_len, keep int32 [B][heads][budget], the positions that stayed, then -1); with
     `stream`, order other streams' use of them after it."""
-    _host_sizes(budget=budget, max_kv=max_kv, sinks=sinks, recent=recent)
+    if not (0 <= budget < _I31 and 0 <= max_kv < _I31 and 0 <= sinks < _I31 and 0 <= recent < _I31):
+        raise ValueError("budget, max_kv, sinks and recent must be 0 to 2^31 - 1")
     dev, B = pages.index, kv_len.numel()
     kp = _ptr_on(kv_len, dev, torch.int32, "kv_len")
     pt, n, dt, dn = _tables(page_table, dst_table, dev, B)
     if new_len is None:
         new_len = _alloc((B,), torch.int32, pages.device, stream)
+        np_ = new_len.data_ptr()
+    else:
+        np_ = _per_request(new_len, B, dev, "new_len")
     if keep is None:
         keep = _alloc((B, pages.heads, int(budget)), torch.int32, pages.device, stream)
+        ep = keep.data_ptr()
     elif keep.shape != (B, pages.heads, budget):
         raise ValueError(f"keep must be [{B}][{pages.heads}][{budget}]")
+    else:
+        ep = _ptr_on(keep, dev, torch.int32, "keep")
     a = KvEvictArgs(_mass_ptr(mass, pages), kp, pt, dt, n, dn, B, int(budget), int(max_kv), int(sinks), int(recent),
-                    1 if move_mass else 0, _per_request(new_len, B, dev, "new_len"), _ptr_on(keep, dev, torch.int32, "keep"))
+                    1 if move_mass else 0, np_, ep)
     _launch("dllm_kv_evict", dev, stream, pages.desc, a)
     return new_len, keep
