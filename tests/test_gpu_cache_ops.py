@@ -772,6 +772,54 @@ def test_thousands_of_requests():
         assert np.array_equal(pages, b.k[i][kept[i, :n], 0].astype(np.float32))
 
 
+@pytest.mark.parametrize("w", [6, 70])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_far_into_a_large_pool(fp8, w):
+    # K and V pass 2^32 bytes: the same bits as in a small pool
+    page, heads, group, dh, lens = 128, 4, 2, 128, [700, 130, 2000]
+    need = [-(-n // page) for n in lens]
+    small = np.full((3, max(need)), -1)
+    for i, (a, n) in enumerate(zip(np.cumsum([0] + need), need)):
+        small[i, :n] = np.arange(a, a + n)
+    total = 2 * sum(need)                                      # the rows' pages, and those that they are moved to
+    row = dh * (1 if fp8 else 2)
+    pools = [total, (1 << 32) // (heads * page * row) + 2 * total]
+    results = []
+    rng = np.random.default_rng(140)
+    old_k, old_v = (torch.from_numpy(rng.standard_normal((sum(lens), heads, dh), dtype=np.float32)).to(DEV, torch.bfloat16) for _ in range(2))
+    q, k, v = rope_case(rng, 3 * w, heads, group, dh)
+    par = i32([tree(rng, w, "any") for _ in lens]).flatten()
+    start = torch.from_numpy(rng.random((total, heads, page), dtype=np.float32)).to(DEV)
+    off, zero, pos0, kv_len = i32([0, w, 2 * w, 3 * w]), i32([0, 0, 0]), i32([n - w for n in lens]), i32(lens)
+    for n in pools:
+        first = n - total
+        p = bd.KVPages.empty(n, page, heads, dh, torch.float8_e4m3fn if fp8 else torch.bfloat16, DEV)
+        mass = torch.empty((n, heads, page), device=DEV)
+        mass[first:] = start
+        tensors = [t for t in (p.k, p.v, p.k_scale, p.v_scale) if t is not None]
+        for t in tensors:
+            t[first:].view(torch.uint8).zero_()
+        table = np.where(small >= 0, small + first, -1)
+        away = i32(np.where(small >= 0, small + first + sum(need), -1))
+        table = i32(table)
+        bd.kv_write(p, old_k, old_v, i32(np.cumsum([0] + lens)), zero, table)
+        bd.kv_write(p, old_k, old_v, i32(np.cumsum([0] + lens)), zero, away)
+        mask, depth = bd.tree_mask(par, off, w)
+        q2 = bd.rope_kv_write(p, bd.Rope.standard(dh), depth + 1000, q, k, v, off, pos0, table)
+        out, lse = bd.tree_attn(q2, p, off, kv_len, table, mask, w, max(lens), return_lse=True)
+        bd.attn_mass(q2, lse, p, mass, off, kv_len, table, w, max(lens), right=0)
+        new, keep = bd.kv_evict(p, mass, kv_len, table, 500, max(lens), sinks=2, recent=w, dst_table=away)
+        new2, keep2 = bd.kv_evict(p, mass, kv_len, table, 400, max(lens), sinks=2, recent=w)
+        bd.kv_move(p, keep2[:, :, 10:20].contiguous(), i32([10, 10, 10]), i32([3, 0, 7]), table, away, mass=mass)
+        results.append([q2, out, lse, new, keep, new2, keep2, mass[first:].clone(), *(t[first:].view(torch.uint8).clone() for t in tensors)])
+        torch.cuda.synchronize()
+        assert bd.device_status() == 0
+        del p, mass, tensors, t
+    torch.cuda.empty_cache()
+    for x, y in zip(*results):
+        assert torch.equal(x.view(torch.uint8) if x.dtype == torch.bfloat16 else x, y.view(torch.uint8) if y.dtype == torch.bfloat16 else y)
+
+
 def test_two_calls_at_once():
     # two streams, a cache each: the calls share no memory of the library's
     cases = []
