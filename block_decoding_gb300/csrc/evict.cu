@@ -264,7 +264,8 @@ constexpr int kMoveThreads = 256;
 // has (four instead of two: 33 us for 30), in place what it has at a time. (192 k
 // rows of 128 and of 256 bytes in place: two rows 29 and 64 us, four 27 and 56, six
 // 33 and 67, eight 38 and 68; 262 k rows of 16 requests, with the choice: 40, 44,
-// 57, 58. In registers, two at a time, the next two on their way: 35 and 75, 55.)
+// 57, 58. In registers, two at a time, the next two on their way: 35 and 75, 55.
+// In shared memory, the next round on its way: one row 30 and 63, 41; two 29 and 63, 47.)
 constexpr int kEachAway = 2, kEachInPlace = 4;
 constexpr int kAtOnce = 4;       // ... whose places are looked up together
 
