@@ -7,7 +7,7 @@
 // memory: 262 k rows of 128 bytes, a third of those read past, to other pages in
 // 30 us, 4.5 TB/s, beside as many sectors for scales and weights of single rows;
 // 192 k rows in place, 64 lists of 2 to 4 thousand, in 27 us. One request's 701
-// rows cut down to 512 in place: 9.7 us, both launches.
+// rows cut down to 512 in place: 8.9 us, both in one launch.
 #include "pages.cuh"
 #include "umma_pages.cuh"
 
@@ -16,6 +16,13 @@ namespace dllm {
 DLLM_DEFINE_STATUS(evict)
 
 namespace {
+
+// All threads of the cluster are here; of what they have written nothing is known.
+__device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 
 // ---------------------------------------------------------------------------
 // selection
@@ -27,12 +34,17 @@ struct SelectArgs {
   int32_t *keep;               // [B][heads][budget]
   int budget, max_kv, sinks, recent;
   unsigned int *status;
+  // rows that the same kernel moves, in place
+  int ctas, share;             // CTAs of a list, rows of a CTA
+  int32_t *new_len;            // [B]
+  float *move_mass;            // null: stays
 };
 
 constexpr int kMaxSelWarps = 32;
 constexpr int kBins = 2048;      // 11 bits at a time
 constexpr int kBatch = 8;        // loads of a thread on their way
 constexpr int kCached = 49152;   // weights that shared memory holds (192 KB)
+constexpr int kSelectBytes = 4 * kCached + 16384;      // dynamic shared memory, at most (10 KB beside it)
 
 // Order of weights as unsigned numbers: -0 is 0, NaN is above everything.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -41,6 +53,74 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// Chosen rows of ROW bytes on their way to their places, through shared memory.
+__host__ __device__ constexpr long long few_bytes(int row, long long budget) {
+  return row > 0 ? (budget * (2 * row + 14) + 15) / 16 * 16 : 0;
+}
+
+template <int ROW>
+struct Few {
+  static constexpr int kChunks = ROW / 16;
+  uint4 *k, *v;                // [share][kChunks]
+  int *from, *dest;            // [share]: positions that stay, then cache rows for head 0; -1: nothing moves
+  float *mass;
+  uint8_t *k_scale, *v_scale;
+  __device__ Few(void *smem, int share) {
+    k = reinterpret_cast<uint4 *>(smem);
+    v = k + share * kChunks;
+    from = reinterpret_cast<int *>(v + share * kChunks);
+    dest = from + share;
+    mass = reinterpret_cast<float *>(dest + share);
+    k_scale = reinterpret_cast<uint8_t *>(mass + share);
+    v_scale = k_scale + share;
+  }
+
+  // The kept rows rank, rank + ctas, .. of k, in `from`.
+  __device__ __forceinline__ void move(const SelectArgs &a, int i, int h, int rank, int kept) const {
+    const int tid = threadIdx.x, nt = blockDim.x, count = (kept - rank + a.ctas - 1) / a.ctas;
+    const size_t head = static_cast<size_t>(h) << a.c.page_shift;
+    __syncthreads();
+    for (int j = tid; j < count; j += nt) {
+      const int u = from[j], at = j * a.ctas + rank;
+      int f = -1, d = -1;
+      if (u != at) {
+        f = page_row(a.c, i, u);
+        d = page_row(a.c, i, at);
+        if (f < 0 || d < 0) {
+          atomicOr(a.status, DLLM_DEV_PAGE);
+          f = d = -1;
+        }
+      }
+      from[j] = f;
+      dest[j] = d;
+      if (f < 0) continue;
+      if (a.c.k_scale) { k_scale[j] = a.c.k_scale[f + head]; v_scale[j] = a.c.v_scale[f + head]; }
+      if (a.move_mass) mass[j] = a.move_mass[f + head];
+    }
+    __syncthreads();
+    for (int p = tid; p < count * kChunks; p += nt) {
+      const int f = from[p / kChunks];
+      if (f < 0) continue;
+      copy16(k + p, a.c.k + (f + head) * ROW + p % kChunks * 16, true);
+      copy16(v + p, a.c.v + (f + head) * ROW + p % kChunks * 16, true);
+    }
+    copies_wait();
+    cluster_barrier();
+    for (int p = tid; p < count * kChunks; p += nt) {
+      const int d = dest[p / kChunks];
+      if (d < 0) continue;
+      *reinterpret_cast<uint4 *>(a.c.k + (d + head) * ROW + p % kChunks * 16) = k[p];
+      *reinterpret_cast<uint4 *>(a.c.v + (d + head) * ROW + p % kChunks * 16) = v[p];
+    }
+    for (int j = tid; j < count; j += nt) {
+      const int d = dest[j];
+      if (d < 0) continue;
+      if (a.c.k_scale) { a.c.k_scale[d + head] = k_scale[j]; a.c.v_scale[d + head] = v_scale[j]; }
+      if (a.move_mass) a.move_mass[d + head] = mass[j];
+    }
+  }
+};
+
 // One CTA per cached head and request. The weights that are chosen from are
 // read once into shared memory (CACHED; more than fit are read again by every
 // pass, from L2). Radix selection finds the least weight that stays, 11 bits at a
@@ -48,26 +128,39 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 // of rows that stay, by one scan over all bins. Then every warp counts its own
 // run of positions and, behind the sum over the warps before it, writes those
 // that stay in their order.
-template <bool CACHED>
+//
+// ROW > 0: a.ctas CTAs of a cluster, which all choose the same rows, then move
+// them, of ROW bytes, in place, in turn: all through shared memory, every one
+// read before any is written (a cluster barrier between the two).
+template <bool CACHED, int ROW>
 __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ SelectArgs a) {
-  extern __shared__ uint32_t s_key[];            // CACHED: [max_kv]
+  extern __shared__ uint4 smem_select[];         // ROW > 0: what moves; CACHED: keys [max_kv]
+  uint32_t *const s_key = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(smem_select) + few_bytes(ROW, a.share));
   __shared__ uint32_t s_hist[kBins];
   __shared__ int s_sum[kMaxSelWarps], s_tie[kMaxSelWarps];
   __shared__ uint32_t s_bin;
   __shared__ int s_left, s_of_bin;
   pdl_trigger();
   pdl_wait();
-  const int h = blockIdx.x, i = blockIdx.y, tid = threadIdx.x, nt = blockDim.x, warp = tid / 32, lane = tid % 32, warps = nt / 32;
+  const int rank = ROW > 0 ? static_cast<int>(blockIdx.x) % a.ctas : 0, h = ROW > 0 ? static_cast<int>(blockIdx.x) / a.ctas : blockIdx.x;
+  const int i = blockIdx.y, tid = threadIdx.x, nt = blockDim.x, warp = tid / 32, lane = tid % 32, warps = nt / 32;
   int n = a.kv_len[i];
   if (n < 0 || n > a.max_kv) {
-    if (tid + h == 0) atomicOr(a.status, DLLM_DEV_OFFSETS);
+    if (tid + blockIdx.x == 0) atomicOr(a.status, DLLM_DEV_OFFSETS);
     n = min(max(n, 0), a.max_kv);
   }
   int32_t *keep = a.keep + (static_cast<size_t>(i) * a.c.heads + h) * a.budget;
   const int k = min(n, a.budget);
-  for (int j = tid + k; j < a.budget; j += nt) keep[j] = -1;
+  if (rank == 0) {
+    for (int j = tid + k; j < a.budget; j += nt) keep[j] = -1;
+    if constexpr (ROW > 0) {
+      if (h == 0 && tid == 0) a.new_len[i] = k;
+    }
+  }
   if (n <= a.budget) {
-    for (int j = tid; j < k; j += nt) keep[j] = j;
+    if (rank == 0)
+      for (int j = tid; j < k; j += nt) keep[j] = j;
+    if constexpr (ROW > 0) cluster_barrier();    // (every CTA comes to one)
     return;
   }
   const int32_t *table = a.c.table + static_cast<size_t>(i) * a.c.max_pages;
@@ -227,19 +320,41 @@ __global__ void __launch_bounds__(1024) select_kernel(const __grid_constant__ Se
     for (int l = 0; l < rounds; ++l) {
       const uint32_t m = __shfl_sync(0xffffffffu, stay, l);
       const int to = __shfl_sync(0xffffffffu, mine, l) + __popc(m & ((1u << lane) - 1));
-      if (m >> lane & 1) keep[to] = from + l * 32 + lane;
+      if (m >> lane & 1) {
+        if (rank == 0) keep[to] = from + l * 32 + lane;
+        if constexpr (ROW > 0) {
+          if (to % a.ctas == rank) Few<ROW>(smem_select, a.share).from[to / a.ctas] = from + l * 32 + lane;
+        }
+      }
     }
   }
+  if constexpr (ROW > 0) Few<ROW>(smem_select, a.share).move(a, i, h, rank, k);
 }
 
+template <int ROW>
 cudaError_t launch_select(const SelectArgs &g, int B, cudaStream_t s) {
   // (16 x 8 heads of 1000 rows and half of them kept: 256 threads 15.4 us, 1024 14.5; one request's 16 of 701: 9.6 and 10.2)
   const int threads = g.max_kv <= 768 ? 256 : 1024;
-  if (g.max_kv > kCached) return launch_pdl(select_kernel<false>, dim3(g.c.heads, B), dim3(threads), 0, s, g);
-  const int smem = g.max_kv * 4;
-  cudaError_t e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4);
+  if (g.max_kv > kCached) return launch_pdl(select_kernel<false, 0>, dim3(g.c.heads, B), dim3(threads), 0, s, g);
+  const int smem = static_cast<int>(few_bytes(ROW, g.share)) + g.max_kv * 4;
+  cudaError_t e = cudaFuncSetAttribute(select_kernel<true, ROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(select_kernel<true>, dim3(g.c.heads, B), dim3(threads), smem, s, g);
+  if (ROW == 0) return launch_pdl(select_kernel<true, ROW>, dim3(g.c.heads, B), dim3(threads), smem, s, g);
+  return launch_pdl_clusters(select_kernel<true, ROW>, g.ctas, dim3(g.c.heads * g.ctas, B), dim3(threads), smem, s, g);
+}
+
+// CTAs of a list that move the rows that they chose, or 0: short requests in place,
+// where the rows fit into the CTAs' shared memory and there is an SM for each. (Both
+// in one launch, and in two: one request's 16 heads of 701 rows, 512 kept, 8.9 and 9.7
+// us, of 1400 10.8 and 12.0, of 4000 12.2 and 12.3, of 8000 13.3 and 13.0; eight
+// requests of 1000 13.8 and 16.1, of 4000 16.2 and 18.3. To other pages 10.4 and
+// 9.8, 14.3 and 14.5.)
+int moving_ctas(const SelectArgs &g, int row, int B) {
+  if (g.max_kv > 4096 || g.new_len == g.kv_len) return 0;      // (the other heads' CTAs read the length)
+  // (16 clusters of 8 CTAs, an SM each, do not run at a time: 17.5 us for the 1000 rows' 10.8)
+  const long long lists = static_cast<long long>(B) * g.c.heads;
+  const int n = 12 * lists <= num_sms() ? 8 : 4 * lists <= num_sms() ? 4 : 2 * lists <= num_sms() ? 2 : 1;
+  return n * lists <= num_sms() && few_bytes(row, (g.budget + n - 1) / n) + 4ll * g.max_kv <= kSelectBytes ? n : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -421,9 +536,7 @@ __global__ void __launch_bounds__(kMoveThreads) shift_in_place_kernel(const __gr
     copies_wait();
     // The round's reads are over (each value is in shared memory); of writes
     // before nothing has to be known. Every CTA reaches the barrier.
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    cluster_barrier();
 #pragma unroll
     for (int q = 0; q < kEachInPlace; ++q) {
       const int dest = held.dest[q][tid];
@@ -522,7 +635,15 @@ extern "C" dllm_status dllm_kv_evict(const dllm_kv_pages *pages, const dllm_kv_e
   m.mass = a->move_mass ? a->mass : nullptr;
   m.status = g.status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  e = launch_select(g, a->B, s);
+  const int row = pages->dh * (pages->type == DLLM_KV_E4M3 ? 1 : 2);
+  g.new_len = a->new_len; g.move_mass = m.mass;
+  g.ctas = in_place ? moving_ctas(g, row, a->B) : 0;
+  if (g.ctas > 0) {
+    g.share = (g.budget + g.ctas - 1) / g.ctas;
+    e = row == 64 ? launch_select<64>(g, a->B, s) : row == 128 ? launch_select<128>(g, a->B, s) : launch_select<256>(g, a->B, s);
+    return e == cudaSuccess ? launch_status() : cuda_error(e);
+  }
+  e = launch_select<0>(g, a->B, s);
   if (e != cudaSuccess) return cuda_error(e);
   const dllm_status sl = launch_shift(pages, m, in_place, a->B, s);
   return sl == DLLM_OK ? launch_status(2) : sl;

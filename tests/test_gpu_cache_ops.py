@@ -685,6 +685,52 @@ def test_eviction_reports_lengths_beyond_their_bounds():
         assert np.array_equal(keep.cpu().numpy()[0, h], cache_ops.keep(m[pg, h, sl], 8, 0, 0))
 
 
+@pytest.mark.parametrize("dh,page,fp8", [(64, 16, True), (64, 128, False), (128, 32, True), (128, 16, False)])
+@pytest.mark.parametrize("heads", [1, 6, 13, 28, 40])
+@pytest.mark.parametrize("budget,sinks,recent", [(1, 0, 0), (77, 3, 20), (300, 300, 0)])
+def test_short_requests_cut_down_in_place(dh, page, fp8, heads, budget, sinks, recent):
+    # 5 to 200 lists: eight CTAs a list, four, two, one, and two launches
+    lens = [0, 1, 78, 700, 301]
+    p = Pool(95 + heads + budget, lens, heads, dh, page, fp8)
+    m = f64(p.mass)
+    lists = [[cache_ops.keep(m[pg, h, sl], budget, sinks, recent) for h in range(heads)]
+             for pg, sl in (slots(p.table, page, i, n) for i, n in enumerate(lens))]
+    want = p.moved(lists, [0] * len(lens), True, True)
+    new, keep = bd.kv_evict(p.pages, p.mass, i32(lens), i32(p.table), budget, max(lens), sinks=sinks, recent=recent)
+    assert new.tolist() == [min(n, budget) for n in lens]
+    keep = keep.cpu().numpy()
+    for i, per in enumerate(lists):
+        for h, u in enumerate(per):
+            assert np.array_equal(keep[i, h], list(u) + [-1] * (budget - len(u))), (i, h)
+    p.check(want)
+
+
+def test_short_requests_with_bad_pages_in_place():
+    lens = [100, 90]
+    p = Pool(96, lens, 2, 64, 16, True)
+    m = f64(p.mass)
+    table = p.table.copy()
+    table[0, 1], table[1, 0] = -1, 999                         # rows from there and to there stay where they are
+    lists = []
+    for i, n in enumerate(lens):
+        pg, sl = slots(p.table, 16, i, n)
+        gone = table[i, np.arange(n) // 16] != p.table[i, np.arange(n) // 16]
+        lists.append([cache_ops.keep(np.where(gone, -np.inf, m[pg, h, sl]), 40, 0, 0) for h in range(2)])
+    before = p.state()
+    new, keep = bd.kv_evict(p.pages, p.mass, i32(lens), i32(table), 40, 100)
+    torch.cuda.synchronize()
+    assert bd.device_status() == DEV_PAGE and new.tolist() == [40, 40]
+    keep, after = keep.cpu().numpy(), p.state()
+    for i in range(2):
+        for h in range(2):
+            assert np.array_equal(keep[i, h], lists[i][h])
+            for j, u in enumerate(keep[i, h]):
+                to = (p.table[i, j // 16], h, j % 16)
+                there = table[i, j // 16] == p.table[i, j // 16] and table[i, u // 16] == p.table[i, u // 16]
+                for a, b in zip(after, before):
+                    assert np.array_equal(a[to], b[p.table[i, u // 16], h, u % 16] if there else b[to])
+
+
 @pytest.mark.parametrize("in_place", [True, False])
 def test_lengths_that_are_cut_down_where_they_stand(in_place):
     # so many heads, and room for such long requests, that not all CTAs run at a time
