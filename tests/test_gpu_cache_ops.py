@@ -1031,3 +1031,31 @@ def test_the_same_in_a_graph_and_on_another_stream(where):
         if a.dtype == torch.bfloat16:
             a, b = a.view(torch.int16), b.view(torch.int16)
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("lens,budget", [([700, 90, 400], 64), ([9000, 400, 65], 1000)])
+def test_in_place_in_a_graph_replayed(lens, budget):
+    # one launch and two; the replays go on from what the one before left
+    def setup():
+        p = Pool(150, lens, 2, 128, 32, True)
+        return p, i32(lens), i32(p.table), i32([[[30, 33, 40]]] * 3), i32([3, 2, 3]), i32([20, 30, 29])
+
+    def step(p, kv_len, table, src, count, first):
+        new, keep = bd.kv_evict(p.pages, p.mass, kv_len, table, budget, max(lens), sinks=2, recent=9)
+        bd.kv_move(p.pages, src, count, first, table, mass=p.mass)
+        return new, keep
+
+    a, b = setup(), setup()
+    got = []
+    for _ in range(3):
+        got.append([t.clone() for t in step(*a)])
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        out = step(*b)
+    for want in got:
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want))
+    assert bd.device_status() == 0
+    b[0].check(a[0].state())
