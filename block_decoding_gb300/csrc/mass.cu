@@ -42,7 +42,7 @@
 // steps for an item, one after the other (without any loads and sums 39 us). The
 // last 50 to 64 tokens of four prompts over 9 to 12 thousand keys, bf16: 30.5 us,
 // of which 5 pass until the first scores; the last 1000 to 1200: 343 us, 1.02
-// PFLOP/s, 53 % of a plain matrix product's rate (e4m3 362 us): a chunk's MMAs on
+// PFLOP/s, 53 % of a plain matrix product's rate (e4m3 369 us): a chunk's MMAs on
 // four tiles take some 2.3 k cycles, their exponentials 2 k, the unit 3.8 k.
 #include <math.h>
 
@@ -354,7 +354,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.k_stages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 2); }
+    for (int s = 0; s < a.k_stages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], kConvert ? 2 + 4 * kGroups : 2); }
     for (int s = 0; s < kQSt; ++s) { mbar_init(&q_full[s], kCodes ? 4 : 5); mbar_init(&q_empty[s], 2); }
     for (int s = 0; s < kInfo; ++s) { mbar_init(&n_full[s], 4); mbar_init(&n_empty[s], 4 * kGroups); }
     for (int s = 0; s < kSlots; ++s) { mbar_init(&slot_full[s], 33); mbar_init(&slot_empty[s], 4 * kGroups); }
@@ -710,23 +710,23 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
       }
       const int end = key0 + (g + 1 + (kPer - 1) * kGroups) * kTile;   // behind the last of its keys
       if constexpr (kConvert) {
-        if (p->first < chunks) {
-          Ring stage = t;
-          t.next(a.k_stages);
-          if (tiles > 2) t.next(a.k_stages);
-          if (g >= 2) stage.next(a.k_stages);
-          if (g < tiles) {
-            ok = warp_wait(&k_full[stage.at], stage.round, abort_flag);
-            if (ok) {
-              const uint32_t byte = page[0] >= 0 ? slot.scale[key] : 127u;      // (codes of no page are 0)
-              ok = convert_codes<DH>(tiles_at + stage.at * C::kStage + (g & 1) * C::kRaw, key % kTile, bf16x2_of(scale_of(byte)),
-                                     &c_read[g], nc & 1, abort_flag);
-            }
+        // Every warp waits for every stage of the item, with a tile in it or not, and a stage is not loaded again before all
+        // have: a wait tells a phase from the next one only, so none may go by unseen and nobody may be two behind.
+#pragma unroll 1
+        for (int s = 0; ok && p->first < chunks && 2 * s < tiles; ++s) {
+          ok = warp_wait(&k_full[t.at], t.round, abort_flag);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(&k_empty[t.at]);
+          if (s == g / 2 && g < tiles) {
+            const uint32_t byte = page[0] >= 0 ? slot.scale[key] : 127u;      // (codes of no page are 0)
+            ok = convert_codes<DH>(tiles_at + t.at * C::kStage + (g & 1) * C::kRaw, key % kTile, bf16x2_of(scale_of(byte)),
+                                   &c_read[g], nc & 1, abort_flag);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&c_full[g]);
             ++nc;
           }
+          t.next(a.k_stages);
         }
       }
       for (int k = p->first; ok && k < chunks; ++k) {
