@@ -17,9 +17,8 @@
 // 43 us; one unit of a thread on the way 45, three or four 38 to 40: registers.
 // Sines and cosines read with bank conflicts: 2 us more.) 64 single tokens: 4.6
 // us, the chain offsets -> position -> page -> store.
-#include <math.h>
-
 #include "page_rows.cuh"
+#include "turns.cuh"
 #include "umma.cuh"
 
 namespace dllm {
@@ -208,16 +207,6 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const __grid_const
       }
     }
   }
-}
-
-// freq / 2 pi modulo 1 as a 64-bit fraction: the product with 1 / 2 pi in two
-// parts, so that its error is that of the last bit kept.
-unsigned long long fraction_of_turn(double freq) {
-  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;   // 1 / 2 pi = kHi + kLo
-  const double hi = freq * kHi, lo = fma(freq, kHi, -hi) + freq * kLo;
-  const double whole = hi - floor(hi);                                        // exact, in [0, 1)
-  // (1 - 2^-53 is the most it can be; the sum wraps around a turn)
-  return static_cast<unsigned long long>(whole * 0x1p64) + static_cast<unsigned long long>(llrint(lo * 0x1p64));
 }
 
 }  // namespace
