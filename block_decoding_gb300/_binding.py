@@ -954,6 +954,8 @@ def _tables(page_table, dst_table, dev, B):
         return pt, n, None, 0
     if dst_table.dim() != 2 or dst_table.shape[0] != B:
         raise ValueError("dst_table must be [B][pages]")
+    if B and not dst_table.shape[1]:        # (a null pointer, which stands for in place)
+        raise ValueError("dst_table has no pages")
     return pt, n, _ptr_on(dst_table, dev, torch.int32, "dst_table"), dst_table.shape[1]
 
 

@@ -574,6 +574,11 @@ dllm_status launch_shift(const dllm_kv_pages *pages, const ShiftArgs &g, bool in
   return e == cudaSuccess ? DLLM_OK : cuda_error(e);
 }
 
+// Rows go to another table, or stay in theirs: no table at all has no pages.
+bool tables_agree(const int32_t *table, int pages, const int32_t *dst, int dst_pages) {
+  return dst ? dst != table || dst_pages == pages : dst_pages == 0;
+}
+
 }  // namespace
 }  // namespace dllm
 
@@ -588,7 +593,7 @@ extern "C" dllm_status dllm_kv_move(const dllm_kv_pages *pages, const dllm_kv_mo
   if (a->B == 0 || a->max_n == 0) return DLLM_OK;
   const dllm_status sp = check_page_pointers(pages);
   if (sp != DLLM_OK) return sp;
-  if (!a->src || !a->count || (!a->page_table && a->max_pages > 0) || (a->dst_table && a->dst_table == a->page_table && a->dst_pages != a->max_pages))
+  if (!a->src || !a->count || (!a->page_table && a->max_pages > 0) || !tables_agree(a->page_table, a->max_pages, a->dst_table, a->dst_pages))
     return DLLM_ERR_INVALID_ARG;
   ShiftArgs g{};
   g.c = device_pages(pages, a->page_table, a->max_pages);
@@ -614,7 +619,7 @@ extern "C" dllm_status dllm_kv_evict(const dllm_kv_pages *pages, const dllm_kv_e
   const dllm_status sp = check_page_pointers(pages);
   if (sp != DLLM_OK) return sp;
   if (!a->mass || !a->kv_len || (!a->page_table && a->max_pages > 0) || !a->new_len || !a->keep ||
-      (a->dst_table && a->dst_table == a->page_table && a->dst_pages != a->max_pages))
+      !tables_agree(a->page_table, a->max_pages, a->dst_table, a->dst_pages))
     return DLLM_ERR_INVALID_ARG;
   SelectArgs g{};
   g.c = device_pages(pages, a->page_table, a->max_pages);

@@ -699,10 +699,11 @@ dllm_status dllm_attn_mass(const dllm_kv_pages *pages /* host */,
  *            or 1 (one list for all heads); count int32 [B] (at most max_n, what
  *            is beyond is not moved, DLLM_DEV_OFFSETS); first int32 [B] or
  *            NULL: 0
- *   dst_table  int32 [B][dst_pages]: where the rows go. NULL or page_table: in
- *            place; then every list ascends and src[i][h][j] >= first[i] + j
- *            (a row that does not keep to that is not moved, DLLM_DEV_PAGE).
- *            Else no page it names may be one that page_table names.
+ *   dst_table  int32 [B][dst_pages]: where the rows go. NULL (with dst_pages = 0)
+ *            or page_table: in place; then every list ascends and
+ *            src[i][h][j] >= first[i] + j (a row that does not keep to that is
+ *            not moved, DLLM_DEV_PAGE). Else no page it names may be one that
+ *            page_table names.
  *   mass     float [num_pages][heads][page_size] that moves with the rows, or
  *            NULL
  * Rows, and with 8-bit pages their scales, are moved bit for bit. Slots that no
