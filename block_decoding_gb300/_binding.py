@@ -791,17 +791,19 @@ class Rope:
         if n % 8 or 2 * n > dh or dh > 128:
             raise ValueError("pairs must be a multiple of 8, at most dh / 2")
         axis = bytes(axis)      # (refuses what is negative or above 255)
-        self.dh, self.axes = int(dh), max(axis, default=0) + 1
+        # axes that pairs turn by, and those of the positions (standard: one per section)
+        self.dh, self.used = int(dh), max(axis, default=0) + 1
+        self.axes = self.used
         if self.axes > 4:
             raise ValueError("axes are numbered 0 to 3")
         # (packed at once: a tenth of the time of ctypes arrays, entry by entry)
-        self.desc = RopeDesc.from_buffer_copy(_ROPE_HEAD.pack(2 * n, self.axes, axis) + array.array("d", freq).tobytes() +
+        self.desc = RopeDesc.from_buffer_copy(_ROPE_HEAD.pack(2 * n, self.used, axis) + array.array("d", freq).tobytes() +
                                               bytes(8 * (64 - n)))
 
     @classmethod
     def standard(cls, dh, base=10000.0, rot=None, sections=None, interleaved=False):
         """freq[j] = base^(-2j / rot), rot = dh unless given. `sections`: the pairs
-        of every axis (they add up to rot / 2), one run after the other or, with
+        of every axis (they add up to rot / 2; one may have none), one run after the other or, with
         `interleaved`, in turn (0, 1, 2, 0, 1, 2, ..) as long as an axis has pairs."""
         rot = dh if rot is None else rot
         if rot % 16:
@@ -818,15 +820,17 @@ class Rope:
                         left[a] -= 1
         else:
             axis = [a for a, n in enumerate(sections) for _ in range(n)]
-        return cls(dh, axis, [float(base) ** (-2.0 * j / rot) for j in range(rot // 2)])
+        rope = cls(dh, axis, [float(base) ** (-2.0 * j / rot) for j in range(rot // 2)])
+        rope.axes = max(rope.axes, len(sections))
+        return rope
 
 
 def rope_kv_write(pages: KVPages, rope: Rope, pos, q, k, v, off, pos0, page_table, q_out=None, stream=None):
     """Turn q [rows][Hq][dh] and k [rows][heads][dh] (bf16, any row stride) by
-    their positions pos int32 [axes][rows] ([rows] with one axis), store k and v
-    in the pages as kv_write does, and return the turned q (q_out, which may be q
-    itself; allocated unless given; with `stream`, order other streams' use of it
-    after it). q None: no q, returns None."""
+    their positions pos int32 [axes][rows] ([rows] with one axis; last axes that no
+    pair turns by may be left out), store k and v in the pages as kv_write does, and
+    return the turned q (q_out, which may be q itself; allocated unless given; with
+    `stream`, order other streams' use of it after it). q None: no q, returns None."""
     dev, dh = pages.index, pages.dh
     if rope.dh != dh:
         raise ValueError(f"rope is for heads of {rope.dh}, the pages have heads of {dh}")
@@ -836,7 +840,8 @@ def rope_kv_write(pages: KVPages, rope: Rope, pos, q, k, v, off, pos0, page_tabl
     if rows != v.shape[0]:
         raise ValueError("k and v must have the same rows")
     pp = _ptr_on(pos, dev, torch.int32, "pos")
-    if pos.shape != (rope.axes, rows) and not (rope.axes == 1 and pos.shape == (rows,)):
+    if not (pos.dim() == 2 and rope.used <= pos.shape[0] <= rope.axes and pos.shape[1] == rows) and \
+            not (rope.used == 1 and pos.shape == (rows,)):
         raise ValueError(f"pos must be [{rope.axes}][{rows}]")
     B, n, po, pt, p0 = _batch(dev, off, page_table, pos0, "pos0")
     Hq = qp = qs = op = os_ = 0

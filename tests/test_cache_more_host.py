@@ -27,3 +27,18 @@ def test_pages_of_no_table_are_refused():
     assert _move(dst_table=None, dst_pages=2) == 1 and _evict(dst_table=None, dst_pages=2) == 1
     assert _move(dst_table=None, dst_pages=2, B=0) == 0 and _evict(dst_table=None, dst_pages=2, B=0) == 0
     assert _move(dst_table=FAKE + 64, dst_pages=2) != 1 and _evict(dst_table=FAKE + 64, dst_pages=2) != 1
+
+
+@pytest.mark.parametrize("sections,interleaved", [([32, 0], False), ([16, 16, 0], True), ([0, 32, 0, 0], False), ([0, 0, 32], False)])
+def test_sections_without_pairs_are_axes(world, sections, interleaved):  # noqa: F811
+    i32, zeros, p = world.i32, world.zeros, world.pages
+    r = bd.Rope.standard(64, sections=sections, interleaved=interleaved)
+    assert r.axes == len(sections)
+    off, table, n, k = i32(0, 5), i32(0, 1)[None], i32(17), zeros(5, 2, 64)
+    used = max(a for a, m in enumerate(sections) if m) + 1
+    for axes in range(used, len(sections) + 1):         # rows that no pair turns by may be left out
+        bd.rope_kv_write(p, r, torch.zeros((axes, 5), dtype=torch.int32), None, k, k, off, n, table)
+    assert len(world.w.launched) == len(sections) - used + 1
+    for axes in (used - 1, len(sections) + 1):
+        with pytest.raises(ValueError):
+            bd.rope_kv_write(p, r, torch.zeros((axes, 5), dtype=torch.int32), None, k, k, off, n, table)
