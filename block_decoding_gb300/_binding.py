@@ -790,7 +790,8 @@ class Rope:
             raise ValueError("axis and freq must have one entry per pair")
         if n % 8 or 2 * n > dh or dh > 128:
             raise ValueError("pairs must be a multiple of 8, at most dh / 2")
-        axis = bytes(axis)      # (refuses what is negative or above 255)
+        # (refuses what is negative or above 255; not an array's memory, whatever its type)
+        axis = bytes(axis if isinstance(axis, (list, tuple, bytes)) else [int(a) for a in axis])
         # axes that pairs turn by, and those of the positions (standard: one per section)
         self.dh, self.used = int(dh), max(axis, default=0) + 1
         self.axes = self.used

@@ -1,6 +1,9 @@
-"""More calls around the paged cache that the host answers: tables without
-pages (CPU only)."""
+"""More calls around the paged cache that the host answers: tables without pages,
+axes without pairs, frequencies from any sequence (CPU only)."""
 
+import array
+
+import numpy as np
 import pytest
 import torch
 
@@ -42,3 +45,13 @@ def test_sections_without_pairs_are_axes(world, sections, interleaved):  # noqa:
     for axes in (used - 1, len(sections) + 1):
         with pytest.raises(ValueError):
             bd.rope_kv_write(p, r, torch.zeros((axes, 5), dtype=torch.int32), None, k, k, off, n, table)
+
+
+@pytest.mark.parametrize("make", [list, tuple, bytes, lambda x: np.array(x), lambda x: np.array(x, np.int16), lambda x: torch.tensor(x),
+                                  lambda x: array.array("i", x)])
+def test_axes_and_frequencies_of_any_sequence(make):
+    axis, freq = [0, 1, 2, 0, 1, 2, 2, 1], [1.0, 0.5, 0.25, 2.0, 3.0, -1.0, 0.0, 8.0]
+    r = bd.Rope(64, make(axis), np.array(freq, np.float32))
+    assert r.axes == 3 and list(r.desc.axis)[:9] == axis + [0] and list(r.desc.freq)[:9] == freq + [0.0]
+    with pytest.raises(ValueError):
+        bd.Rope(64, make([0] * 7 + [4]), freq)
