@@ -934,7 +934,9 @@ def attn_mass(q, lse, pages: KVPages, mass, q_off, kv_len, page_table, max_q, ma
     from position fresh[i] int32 [B] on) the weight that the query rows q
     [rows][Hq][dh], with lse [rows][Hq] from paged_attn, gave to every cached row
     of their requests. The rows see keys up to `right` behind their position
-    (negative: all). Returns mass."""
+    (negative: all), and paged_attn has to have had the same `right` and no `left`:
+    with the lse of a window or of tree_attn the keys left out there are weighed
+    too. Returns mass."""
     if not (0 <= max_q < _I31 and 0 <= max_kv < _I31 and -_I31 <= right < _I31):
         raise ValueError("max_q, max_kv and right must fit 32 bits, and only right may be negative")
     dev, dh = pages.index, pages.dh

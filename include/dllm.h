@@ -660,8 +660,11 @@ dllm_status dllm_tree_attn(const dllm_kv_pages *pages /* host */,
  *     mass <- decay * mass + sum exp(scale * <q[t,g,:], k[u,h,:]> - lse[t,g])
  *   over its query rows t and the query heads g of h that see u: those at
  *   position p >= u - right (right < 0: all), p as in dllm_paged_attn. With the
- *   lse that dllm_paged_attn returned for these rows the terms are the
- *   attention's weights; a row with lse = -infinity (it saw no key) adds nothing.
+ *   lse that dllm_paged_attn returned for these rows, at the same right and with
+ *   left < 0, the terms are the attention's weights. They are not with the lse of
+ *   rows that saw less, under a window (left >= 0) or a tree (dllm_tree_attn): the
+ *   keys that such a row did not see are weighed too, some by more than 1. A row
+ *   with lse = -infinity (it saw no key) adds nothing.
  *   mass     float [num_pages][heads][page_size], as the scales lie, 16-byte
  *            aligned. Slots of other positions keep their values.
  *   fresh    int32 [B] or NULL: positions u >= fresh[i] start from 0, whatever
