@@ -18,6 +18,11 @@ DLLM_DEFINE_STATUS(evict)
 namespace {
 
 // All threads of the cluster are here; of what they have written nothing is known.
+// Reads before it and other CTAs' writes of the same rows behind it are in order all
+// the same: by then each value that was read, scales and weights by plain loads
+// too, is in the reader's shared memory or registers, so its load is over.
+// (As release and acquire: lists per head in place 28.9 us for 26.8, one request's 9.2
+// for 8.8.)
 __device__ __forceinline__ void cluster_barrier() {
   __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");

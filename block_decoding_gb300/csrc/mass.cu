@@ -38,7 +38,7 @@
 //                 exponentials and sums
 //
 // 64 single tokens over 1 to 8192 keys (8 x 4 heads, dh 128): e4m3 55 us, 4.9
-// TB/s and 73 % of a copy's rate; bf16 90 us, 86 %. e4m3 is bound by the roles'
+// TB/s and 73 % of a copy's rate; bf16 87 us, 89 %. e4m3 is bound by the roles'
 // steps for an item, one after the other (without any loads and sums 39 us). The
 // last 50 to 64 tokens of four prompts over 9 to 12 thousand keys, bf16: 30.5 us,
 // of which 5 pass until the first scores; the last 1000 to 1200: 343 us, 1.02
@@ -124,7 +124,7 @@ struct MassPiece {
   int fresh;               // positions from here on start from 0
   int first, chunks;       // chunks [first, chunks) hold rows that see a key of the item
   int again, keep;         // the chunk is the last item's, is the next one's too
-  int tiles;               // key tiles (1 to 4)
+  int tiles;               // key tiles, 1 to kTiles (4, or 8 with two keys a thread)
   int more;
 };
 
@@ -742,6 +742,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CU
           }
           if (ok) {
             tc_fence_after();
+            // (written before the arrival that the MMAs waited for, at q_full, and so before their scores)
             const Numbers &s = numbers[in.at];
             const int columns = chunk_columns(a, W, k);
             float2 acc[kPer][2] = {};

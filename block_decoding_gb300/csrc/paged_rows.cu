@@ -34,7 +34,7 @@
 // the wait for the scores, and only by tiles from the first token's key on.
 //
 // Drafts of 32 requests of 20 to 64 tokens over up to 8192 keys (8 x 4 heads, dh
-// 128): e4m3 168 us, bf16 124; two thirds of the 256 rows are tokens'.
+// 128): e4m3 170 us, bf16 128; two thirds of the 256 rows are tokens'.
 // Pieces of two prompts of 1200 to 1536 tokens over 9 to 12 thousand keys (bf16,
 // 8 x 4 heads, dh 128, causal) take 331 us with the join: 1.34 PFLOP/s, 72 % of a plain
 // matrix product's rate. Bound by the tensor cores: a tile of 256 x 128 costs
